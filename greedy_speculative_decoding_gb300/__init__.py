@@ -17,8 +17,10 @@ from . import _lib
 from ._lib import (SF_DRAFT_NEURAL, SF_DRAFT_NGRAM, SF_DRAFT_NONE, SF_DRAFT_TREE, SF_MAX_ROWS, SFError, load)
 from .engine import (SpecEngine, linear, linear_frag, model_cfg, nf4_quantize, nf4_scale_ld, quantize_model_nf4,
                      to_frag, weight_order)
+from .paged import PagePlan, kv_append, page_plan, paged_attention, paged_attention_workspace, rope_table
 
 __all__ = ["SpecEngine", "SFError", "linear", "linear_frag", "to_frag", "model_cfg", "weight_order",
            "nf4_quantize", "nf4_scale_ld",
-           "quantize_model_nf4", "SF_DRAFT_NEURAL",
+           "quantize_model_nf4", "PagePlan", "page_plan", "rope_table", "kv_append", "paged_attention",
+           "paged_attention_workspace", "SF_DRAFT_NEURAL",
            "SF_DRAFT_NGRAM", "SF_DRAFT_NONE", "SF_DRAFT_TREE", "SF_MAX_ROWS"]

@@ -16,6 +16,7 @@ SF_OK, SF_ERR_ARG, SF_ERR_CAPACITY, SF_ERR_CUDA, SF_ERR_NONFINITE, SF_ERR_STATE,
 SF_WDTYPE_BF16, SF_WDTYPE_NF4, SF_WDTYPE_F32 = 0, 1, 2
 SF_DRAFT_NEURAL, SF_DRAFT_NGRAM, SF_DRAFT_NONE, SF_DRAFT_TREE = 0, 1, 2, 3
 SF_MAX_ROWS = 80
+SF_DT_F32, SF_DT_BF16, SF_DT_F16 = 0, 1, 2
 
 EXPORTS = (
     "sf_weight_count", "sf_kv_bytes", "sf_workspace_bytes", "sf_create", "sf_prefill", "sf_draft",
@@ -24,6 +25,7 @@ EXPORTS = (
     "sf_destroy", "sf_nf4_quantize", "sf_linear_workspace_bytes", "sf_linear", "sf_linear_noalloc",
     "sf_trace", "sf_trace_label", "sf_frag_bytes", "sf_to_frag", "sf_linear_frag", "sf_round_launches",
     "sf_tree_draft", "sf_set_tree_candidates", "sf_tree_winner",
+    "sf_page_plan", "sf_rope_table", "sf_kv_append", "sf_paged_attention_workspace_bytes", "sf_paged_attention",
 )
 
 
@@ -35,6 +37,22 @@ class ModelCfg(ctypes.Structure):
         ("embed_ld", ctypes.c_int32), ("rope_theta", ctypes.c_float), ("rms_eps", ctypes.c_float),
         ("wdtype", ctypes.c_int32),
     ]
+
+
+class PagedCache(ctypes.Structure):
+    """sf_paged_cache"""
+    _fields_ = [
+        ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("dtype", ctypes.c_int32), ("n_pages", ctypes.c_int32),
+        ("n_kv_heads", ctypes.c_int32), ("page", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+        ("reserved", ctypes.c_int32), ("k_page", ctypes.c_int64), ("k_head", ctypes.c_int64),
+        ("k_slot", ctypes.c_int64), ("v_page", ctypes.c_int64), ("v_head", ctypes.c_int64), ("v_slot", ctypes.c_int64),
+    ]
+
+
+class Rows(ctypes.Structure):
+    """sf_rows"""
+    _fields_ = [("data", ctypes.c_void_p), ("dtype", ctypes.c_int32), ("n_heads", ctypes.c_int32),
+                ("row", ctypes.c_int64), ("head", ctypes.c_int64)]
 
 
 class SFError(RuntimeError):
@@ -89,6 +107,11 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "sf_tree_draft": (ST, [P, I32, I32, I32, P, P]),
         "sf_set_tree_candidates": (ST, [P, I32]),
         "sf_tree_winner": (ST, [P, PI32]),
+        "sf_page_plan": (ST, [P, P, I32, I32, P, I32, P, P, I32, P, I32, P, P, P, P, P, P]),
+        "sf_rope_table": (ST, [P, I32, I32, ctypes.c_float, P]),
+        "sf_kv_append": (ST, [P, I32, P, P, P, P, P, P, P, I32, P]),
+        "sf_paged_attention_workspace_bytes": (SZ, [I32, I32, I32, I32]),
+        "sf_paged_attention": (ST, [P, P, P, I32, P, I32, P, P, I32, I32, P, ctypes.c_float, P, P, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)

@@ -373,6 +373,127 @@ SF_API sf_status sf_linear_noalloc(const void* d_w, int32_t N, int32_t K, int32_
 SF_API sf_status sf_nf4_quantize(const void* d_w, int32_t rows, int32_t cols, int32_t ld,
                           void* d_packed, void* d_scales, void* cuda_stream);
 
+/* ------------------------------------------------------------------------
+ * A key-value cache in pages, for programs that serve sequences of different
+ * lengths from one pool (the engine's own caches are s_max slots per
+ * sequence). Three operators run one after the other in a pass:
+ * sf_page_plan (block tables, cache slots and positions from the requests'
+ * lengths), sf_kv_append (RoPE and the new rows' keys and values into their
+ * slots) and sf_paged_attention (the new rows over their requests' pages).
+ * Everything they need to know about a pass lies in device memory, so a pass
+ * is captured into a CUDA graph once and replayed with other lengths. No call
+ * synchronises or allocates; all work is enqueued on cuda_stream. A pass's
+ * token rows lie request after request: starts[b] .. starts[b + 1] - 1 are
+ * the newest rows of request b, the last of them at position lens[b] - 1.
+ */
+
+/* Element types of rows and caches. */
+enum { SF_DT_F32 = 0, SF_DT_BF16 = 1, SF_DT_F16 = 2 };
+
+/* One layer's cache: k and v are device tensors [n_pages][n_kv_heads][page]
+ * [head_dim] with any strides (in elements, the last dimension contiguous):
+ * pages whose keys and values alternate in one pool, or pages laid out
+ * [page][n_kv_heads][head_dim], are views of this form. dtype SF_DT_BF16 or
+ * SF_DT_F16; page 16, 32, 64, 128 or 256; head_dim 64 or 128. Pointers
+ * 16-byte aligned, strides positive multiples of 8, the page stride the
+ * largest, n_pages * page < 2^31. Slot s is slot s % page of page s / page. */
+typedef struct {
+  void* k;
+  void* v;
+  int32_t dtype, n_pages, n_kv_heads, page, head_dim, reserved;
+  int64_t k_page, k_head, k_slot;   /* strides of k */
+  int64_t v_page, v_head, v_slot;   /* strides of v */
+} sf_paged_cache;
+
+/* n token rows of n_heads heads each: element (i, h, d) at
+ * data[i * row + h * head + d] (row and head strides in elements). */
+typedef struct {
+  void* data;
+  int32_t dtype, n_heads;
+  int64_t row, head;
+} sf_rows;
+
+/*
+ * Block tables and slot maps from request lengths. Request b is to hold
+ * lens[b] tokens after the pass, its rows among them (0: it has finished), so
+ * ceil(lens[b] / page) pages: entries 0 .. held[b] - 1 of row b of tables
+ * [batch][table_width] are the pages it holds on entry; free[0 .. *n_free - 1]
+ * is a stack of the pages nobody holds (capacity: the size of free). First
+ * every page that a request no longer needs goes onto the stack, in request
+ * order and within a request in table order; then every page that a request
+ * lacks is taken from the top, in request order. A request whose pages would
+ * not all be there (counting those that the requests before it want) gets
+ * none and keeps what it holds, and so does every later request that wants
+ * pages. Outputs: tables and free in place; held_out and n_free_out (they may
+ * be held and n_free themselves); status [batch]: 0 served, 1 not enough
+ * pages, 2 refused (a negative length, more pages than table_width, more rows
+ * than tokens, or held[b] outside 0..table_width), the last two leaving the
+ * request's pages as they are; and for each of the n_rows rows its cache slot
+ * (page number * page + offset) and position. Rows of requests whose status
+ * is not 0 and rows behind the last request get slot -1, position 0.
+ * With held_out and n_free_out apart from held and n_free a call can be
+ * repeated: it reads nothing that it changes. All int32; starts [batch + 1].
+ * batch 1..8192; page a power of two 16..256; n_rows may be 0 (slots and
+ * positions may then be NULL).
+ */
+SF_API sf_status sf_page_plan(const int32_t* d_lens, const int32_t* d_starts, int32_t batch, int32_t page,
+                              int32_t* d_tables, int32_t table_width, const int32_t* d_held, int32_t* d_free,
+                              int32_t capacity, const int32_t* d_n_free, int32_t n_rows, int32_t* d_slots,
+                              int32_t* d_positions, int32_t* d_held_out, int32_t* d_n_free_out, int32_t* d_status,
+                              void* cuda_stream);
+
+/* The RoPE table of the engine's models: fp32 [n_pos][head_dim / 2][2] =
+ * (cos, sin) of pos * theta^(-2 i / head_dim), computed in double precision. */
+SF_API sf_status sf_rope_table(float* d_table, int32_t n_pos, int32_t head_dim, float theta, void* cuda_stream);
+
+/*
+ * RoPE and cache append of n rows: row i's keys and values go, rounded once,
+ * to slot slots[i] of every KV head; with d_rope (sf_rope_table's layout,
+ * n_pos positions) the keys and queries are first rotated by the row's
+ * position (element i is paired with i + head_dim / 2), in fp32. q may be
+ * NULL (keys and values only); otherwise its rows go to q_out (the same heads;
+ * q's or the cache's type; it may be q itself when the types are equal). Rows
+ * whose slot lies outside the cache, or whose position lies outside the table,
+ * are padding: nothing is written for them. The slots of a call are distinct
+ * (of two rows with one slot, it is open whose elements stay). positions is
+ * read only with d_rope. k and v have one type, F32, BF16 or F16, and q the
+ * same. Data 16-byte aligned, strides multiples of 8 (of 4 for F32).
+ */
+SF_API sf_status sf_kv_append(const sf_paged_cache* cache, int32_t n, const sf_rows* k, const sf_rows* v,
+                              const int32_t* d_slots, const sf_rows* q, const sf_rows* q_out,
+                              const int32_t* d_positions, const float* d_rope, int32_t n_pos, void* cuda_stream);
+
+/*
+ * Attention of the requests' newest rows over their pages: out = softmax(q k^T
+ * * scale) v over the slots that the row sees, query head h reading KV head
+ * h / (n_heads / n_kv_heads). Row j of the n_b rows of request b sees the
+ * lens[b] - n_b slots before the pass's rows, and of those rows: the first to
+ * its own (row i of the pass lies in slot lens[b] - n_b + i); with d_mask
+ * (uint64 [n], max_rows <= 64) instead those whose bit i is set, which is how
+ * several guesses are verified side by side. A row that sees nothing gives out
+ * 0 and lse -infinity; what masked slots and slots past lens[b] hold, NaN
+ * included, changes nothing. lse (fp32 [n][n_heads], may be NULL): the natural
+ * logarithm of the row's sum of exponentials. d_starts NULL: every request has
+ * n / batch rows (n a multiple of batch). A request may have 0 rows, and at
+ * most max_rows (1..SF_MAX_ROWS; further ones are not computed). Rows outside
+ * every request are left as they were. lens[b] is cut to table_width * page,
+ * and a table entry that is no page of the cache reads as zeros.
+ * q and out have one type: the cache's, or F32 over a BF16 cache (exact in the
+ * queries and probabilities: each is three bf16 terms). n_heads a multiple of
+ * n_kv_heads. workspace: sf_paged_attention_workspace_bytes(...) bytes of
+ * device scratch, 256-byte aligned, any contents; calls that may overlap on
+ * the GPU need one each. A result depends on the whole batch's lengths in its
+ * last bits (the split over the cache's length follows them) and is the same
+ * in every run.
+ */
+SF_API size_t sf_paged_attention_workspace_bytes(int32_t n_heads, int32_t n_kv_heads, int32_t head_dim,
+                                                 int32_t max_rows);
+SF_API sf_status sf_paged_attention(const sf_paged_cache* cache, const sf_rows* q, const sf_rows* out, int32_t n,
+                                    const int32_t* d_tables, int32_t table_width, const int32_t* d_lens,
+                                    const int32_t* d_starts, int32_t batch, int32_t max_rows,
+                                    const uint64_t* d_mask, float scale, float* d_lse, void* d_workspace,
+                                    void* cuda_stream);
+
 #ifdef __cplusplus
 }
 #endif

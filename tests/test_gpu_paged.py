@@ -1,0 +1,555 @@
+"""GPU parity of the paged-cache operators against the float64 oracle.
+
+page_plan is integers: equal. kv_append rounds fp32 arithmetic once to the
+cache's type, so an element is off by at most half a step of that type plus
+the fp32 rotation's three roundings.
+
+paged_attention: with x the scaled scores, p the probabilities and A = sum p|v|
+(the oracle's), an output is off by at most
+  * the probabilities' rounding to the cache's type, u * A (u = half a step,
+    2^-8 bf16, 2^-11 fp16; fp32 queries carry them exactly), and the output's
+    own, u_out * |out|;
+  * a relative error of every probability from its score: fp32 sums of hd
+    products (each step may truncate: 2^-23 of the sum of magnitudes, qk), two
+    roundings of the score and the exponential's 2^-22, which reach numerator
+    and denominator: eps = 2 (hd + 8) 2^-23 max(qk, 1) + 2^-18 (running sums
+    over at most 1000 pieces at 2^-23 each and rescalings) times A and |out|.
+The logarithm lse is off by eps. Sizes keep the sums under 1000 pieces per
+lane.
+"""
+
+import ctypes
+import math
+import random
+
+import pytest
+import torch
+
+from oracle import paged as op
+
+pytestmark = pytest.mark.gpu
+
+U = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11, torch.float32: 2.0 ** -24}
+TINY = {torch.bfloat16: 2.0 ** -134, torch.float16: 2.0 ** -25, torch.float32: 2.0 ** -150}
+BF, FH, F4 = torch.bfloat16, torch.float16, torch.float32
+
+
+@pytest.fixture(scope="module")
+def pkg():
+    import __graft_entry__ as g
+    g.build()
+    import greedy_speculative_decoding_gb300 as p
+    return p
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+# ------------------------------------------------------------------ page_plan
+def plan_case(seed, B, W, page, tight=False, prompts=False, bad=False):
+    r = random.Random(seed)
+    held = [0 if prompts else r.randint(0, W) for _ in range(B)]
+    lens = [r.choice([0, 1, r.randint(0, W * page), min(W * page, max(0, h * page + r.randint(-20, 20)))]) for h in held]
+    rows = [n if prompts else min(n, r.randint(0, 5)) for n in lens]
+    if bad:
+        for b in r.sample(range(B), max(1, B // 4)):
+            k = r.randint(0, 2)
+            if k == 0:
+                lens[b] = -r.randint(1, 2 ** 31 - 1)
+            elif k == 1:
+                lens[b] = W * page + r.randint(1, 2 ** 30)
+            else:
+                rows[b] = max(lens[b], 0) + 1
+    need = [max(0, -(-n // page)) for n in lens]
+    grow = sum(max(0, min(n, W) - h) for n, h in zip(need, held))
+    spare = grow // 2 if tight else grow + 3
+    cap = sum(held) + spare + 2
+    pages = list(range(cap))
+    r.shuffle(pages)
+    tables, at = [[-1] * W for _ in range(B)], 0
+    for b in range(B):
+        tables[b][:held[b]] = pages[at:at + held[b]]
+        at += held[b]
+    free = pages[at:at + spare] + [-1] * (cap - spare)
+    starts = [0]
+    for n in rows:
+        starts.append(starts[-1] + n)
+    return lens, starts, tables, held, free, spare, page, starts[-1] + 3
+
+
+def check_plan(pkg, case, in_place=False, repeat=1):
+    lens, starts, tables, held, free, n_free, page, n_rows = case
+    ref = op.page_plan(*case)
+    t, h, f, nf = i32(tables), i32(held), i32(free), i32([n_free])
+    for _ in range(repeat):
+        kw = {} if in_place else dict(held_out=torch.full_like(h, -7), n_free_out=torch.full_like(nf, -7))
+        res = pkg.page_plan(i32(lens), i32(starts), t, h, f, nf, page, n_rows=n_rows, **kw)
+        got = dict(tables=t, held=res.held, free=f, n_free=res.n_free, status=res.status, slots=res.slots,
+                   positions=res.positions)
+        for name, x in got.items():
+            want = [ref[name]] if name == "n_free" else ref[name]
+            assert x.tolist() == want, name
+    if in_place:
+        assert res.held is h and res.n_free is nf
+    else:
+        assert h.tolist() == held and nf.tolist() == [n_free]
+
+
+@pytest.mark.parametrize("B,W,page", [(1, 1, 16), (2, 9, 256), (8, 130, 64), (31, 5, 32), (32, 7, 16), (33, 64, 128),
+                                      (1023, 6, 16), (1025, 3, 64), (8192, 2, 16)])
+@pytest.mark.parametrize("tight", [False, True])
+def test_plan(pkg, B, W, page, tight):
+    check_plan(pkg, plan_case(B + W, B, W, page, tight))
+
+
+@pytest.mark.parametrize("seed", range(8))
+def test_plan_in_place_and_repeated(pkg, seed):
+    r = random.Random(seed)
+    case = plan_case(seed, r.randint(1, 60), r.randint(1, 40), r.choice([16, 32, 64, 128, 256]), seed % 2 == 1)
+    check_plan(pkg, case, in_place=True)
+    check_plan(pkg, case, repeat=3)
+
+
+@pytest.mark.parametrize("B,W,page,tight", [(1, 300, 16, False), (5, 700, 16, True), (200, 30, 64, True), (9, 1, 256, False)])
+def test_plan_of_whole_prompts(pkg, B, W, page, tight):
+    check_plan(pkg, plan_case(7 * B, B, W, page, tight, prompts=True))
+
+
+@pytest.mark.parametrize("seed", range(4))
+def test_plan_refuses_bad_requests_alone(pkg, seed):
+    check_plan(pkg, plan_case(seed, 40, 11, 32, seed % 2 == 1, bad=True))
+
+
+def test_plan_without_rows(pkg):
+    lens, starts, tables, held, free, n_free, page, _ = plan_case(3, 12, 8, 16)
+    check_plan(pkg, (lens, [0] * 13, tables, held, free, n_free, page, 0))
+    check_plan(pkg, (lens, [4] * 13, tables, held, free, n_free, page, 9))
+
+
+# ------------------------------------------------------------------ kv_append
+def make_cache(n_pages, nkv, page, hd, dtype, layout="pages", fill=0.25):
+    if layout == "pool":      # a page's keys and values side by side
+        pool = torch.full((n_pages, 2, nkv, page, hd), fill, dtype=dtype, device="cuda")
+        return pool[:, 0], pool[:, 1]
+    if layout == "nhd":       # [page][head][dim] within a page
+        k, v = (torch.full((n_pages, page, nkv, hd), fill, dtype=dtype, device="cuda") for _ in range(2))
+        return k.transpose(1, 2), v.transpose(1, 2)
+    if layout == "padded":    # rows of a slot, heads and pages apart
+        k, v = (torch.full((n_pages, nkv + 1, page + 3, hd + 16), fill, dtype=dtype, device="cuda") for _ in range(2))
+        return k[:, :nkv, :page, :hd], v[:, 1:, 3:, 16:]
+    return tuple(torch.full((n_pages, nkv, page, hd), fill, dtype=dtype, device="cuda") for _ in range(2))
+
+
+@pytest.mark.parametrize("din,dc", [(F4, BF), (F4, FH), (BF, BF), (FH, FH)])
+@pytest.mark.parametrize("hd,nq,nkv,page,layout", [(64, 14, 2, 64, "pages"), (128, 4, 1, 16, "nhd"), (128, 5, 5, 256, "pool"),
+                                                   (64, 3, 1, 32, "padded")])
+@pytest.mark.parametrize("rope,fused,with_q", [(True, True, True), (True, False, False), (False, True, True)])
+def test_append(pkg, din, dc, hd, nq, nkv, page, layout, rope, fused, with_q):
+    g = torch.Generator(device="cuda").manual_seed(hd + nq + page)
+    n, n_pages, n_pos = 37, 9, 50
+    if fused:
+        buf = torch.randn((n, (nq + 2 * nkv) * hd), dtype=din, device="cuda", generator=g)
+        q, k, v = (x.view(n, -1, hd) for x in buf.split([nq * hd, nkv * hd, nkv * hd], dim=1))
+    else:
+        q, k, v = (torch.randn((n, h, hd), dtype=din, device="cuda", generator=g) for h in (nq, nkv, nkv))
+    r = random.Random(5)
+    slots = r.sample(range(n_pages * page), n)
+    slots[3], slots[7], slots[11] = -1, n_pages * page, -2 ** 31
+    pos = [r.randrange(n_pos) for _ in range(n)]
+    pos[5], pos[6] = -1, n_pos
+    cs = pkg.rope_table(n_pos, hd, 1e4) if rope else None
+    k_cache, v_cache = make_cache(n_pages, nkv, page, hd, dc, layout)
+    for q_dt in ({dc, din} if with_q else {None}):
+        k_cache.fill_(0.25)
+        v_cache.fill_(0.25)
+        q_out = None if q_dt is None else torch.full((n, nq, hd), 0.5, dtype=q_dt, device="cuda")
+        res = pkg.kv_append(k, v, i32(slots), k_cache, v_cache, q=q if with_q else None, q_out=q_out,
+                            positions=i32(pos) if rope else None, rope=cs)
+        assert res is q_out
+        live = [i for i in range(n) if 0 <= slots[i] < n_pages * page and (not rope or 0 <= pos[i] < n_pos)]
+        want = {}
+        for name, src, turn in (("q", q, rope), ("k", k, rope), ("v", v, False)):
+            x = src.cpu().double()
+            y = x.clone()
+            if turn:
+                t = cs.cpu()
+                for i in live:
+                    for h in range(x.shape[1]):
+                        y[i, h] = op.rotate(x[i, h], t[pos[i]])
+            want[name] = (y, x.abs() + x.roll(hd // 2, -1).abs() if turn else torch.zeros_like(x))
+        for name, got, fill, dt in (("q", q_out, 0.5, q_dt), ("k", k_cache, 0.25, dc), ("v", v_cache, 0.25, dc)):
+            if got is None:
+                continue
+            y, mag = want[name]
+            if name == "q":
+                ref, m = torch.full_like(y, fill), torch.zeros_like(y)
+                ref[live], m[live] = y[live], mag[live]
+                out = got.cpu().double()
+            else:
+                ref = torch.full((n_pages * page, nkv, hd), fill, dtype=torch.float64)
+                m = torch.zeros_like(ref)
+                for i in live:
+                    ref[slots[i]], m[slots[i]] = y[i], mag[i]
+                out = got.transpose(1, 2).reshape(n_pages * page, nkv, hd).cpu().double()
+            assert bool(((out - ref).abs() <= U[dt] * ref.abs() + 4 * 2.0 ** -24 * m + TINY[dt]).all()), name
+
+
+def test_append_queries_in_place_and_one_row(pkg):
+    g = torch.Generator(device="cuda").manual_seed(1)
+    q, k, v = (torch.randn((1, h, 64), dtype=BF, device="cuda", generator=g) for h in (4, 2, 2))
+    cs = pkg.rope_table(1000, 64, 1e6)
+    a, b = make_cache(2, 2, 16, 64, BF), make_cache(2, 2, 16, 64, BF)
+    apart = pkg.kv_append(k, v, i32([17]), *a, q=q, positions=i32([999]), rope=cs)
+    kept = q.clone()
+    assert pkg.kv_append(k, v, i32([17]), *b, q=q, q_out=q, positions=i32([999]), rope=cs) is q
+    assert torch.equal(q, apart) and not torch.equal(q, kept)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_rope_table_is_the_engines_formula(pkg):
+    t = pkg.rope_table(5000, 128, 1e6).double().cpu()
+    i = torch.arange(64, dtype=torch.float64)
+    ang = torch.arange(5000, dtype=torch.float64)[:, None] * torch.tensor(1e6, dtype=torch.float64) ** (-2 * i / 128)
+    assert float((t - torch.stack([ang.cos(), ang.sin()], -1)).abs().max()) <= 2.0 ** -24 + 1e-11
+
+
+# ------------------------------------------------------------------ attention
+def attn_case(seed, lens, rows, nq, nkv, hd, page, dq=BF, dc=BF, layout="pages", tree=False, pad=2, q_scale=2.0,
+              stale=None, strided_q=False):
+    """Inputs of one call; cache slots that no request reaches hold `stale`."""
+    r = random.Random(seed)
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    B = len(lens)
+    held = [-(-n // page) for n in lens]
+    W = max(1, max(held))
+    n_pages = sum(held) + 2
+    pages = list(range(n_pages))
+    r.shuffle(pages)
+    k, v = make_cache(n_pages, nkv, page, hd, dc, layout, float("nan") if stale is None else stale)
+    tables, at = [[0] * W for _ in range(B)], 0
+    for b in range(B):
+        tables[b][:held[b]] = pages[at:at + held[b]]
+        at += held[b]
+        for i in range(held[b]):
+            m = min(page, lens[b] - i * page)
+            for c in (k, v):
+                c[tables[b][i], :, :m] = torch.randn((nkv, m, hd), dtype=dc, device="cuda", generator=g)
+    starts = [0]
+    for x in rows:
+        starts.append(starts[-1] + x)
+    n = starts[-1] + pad
+    if strided_q:
+        q = (torch.randn((n, nq + 3, hd + 16), dtype=dq, device="cuda", generator=g) * q_scale)[:, 2:2 + nq, 8:8 + hd]
+    else:
+        q = torch.randn((n, nq, hd), dtype=dq, device="cuda", generator=g) * q_scale
+    mask = None
+    if tree:
+        mask = [0] * n
+        for b in range(B):
+            for j in range(rows[b]):
+                m = 1 << j
+                if j:
+                    m |= mask[starts[b] + r.randrange(j)]
+                mask[starts[b] + j] = m if r.random() < 0.9 else 0
+        mask = [m - (1 << 64) if m >> 63 else m for m in mask]
+    return dict(q=q, k=k, v=v, tables=tables, lens=lens, starts=starts, mask=mask, max_rows=max(1, max(rows)))
+
+
+def call(pkg, c, **kw):
+    out = torch.full(c["q"].shape, 7.0, dtype=c["q"].dtype, device="cuda")
+    lse = torch.full(c["q"].shape[:2], 7.0, device="cuda")
+    mask = None if c["mask"] is None else torch.tensor(c["mask"], dtype=torch.int64, device="cuda")
+    a = dict(starts=i32(c["starts"]), max_rows=c["max_rows"], mask=mask, out=out, lse=lse)
+    a.update(kw)
+    res = pkg.paged_attention(c["q"], c["k"], c["v"], i32(c["tables"]), i32(c["lens"]), **a)
+    assert a["out"] is None or res is a["out"]
+    return res, a["lse"]
+
+
+def check_attn(c, out, lse, scale=None):
+    hd = c["q"].shape[2]
+    scale = 1 / math.sqrt(hd) if scale is None else scale
+    ref, rl, A, qk, live = op.paged_attention(c["q"].cpu(), c["k"].cpu(), c["v"].cpu(), c["tables"], c["lens"],
+                                              c["starts"], scale, c["mask"], c["max_rows"])
+    out, lse = out.double().cpu(), lse.double().cpu()
+    assert bool((out[~live] == 7).all() and (lse[~live] == 7).all())
+    up = 0.0 if c["q"].dtype == F4 else U[c["k"].dtype]
+    eps = 2 * (hd + 8) * 2.0 ** -23 * qk.clamp(min=1.0) + 2.0 ** -18
+    bound = (up + eps[..., None]) * A + (U[c["q"].dtype] + eps[..., None]) * ref.abs() + TINY[c["q"].dtype]
+    err = (out - ref).abs()
+    assert bool((err[live] <= bound[live]).all()), float((err / bound)[live].max())
+    empty = rl == float("-inf")
+    assert bool((lse[live] == rl[live])[empty[live]].all())
+    assert bool(((lse - rl).abs() <= eps)[live & ~empty.all(1)][~empty[live & ~empty.all(1)]].all())
+
+
+LENS = [[1], [0, 1, 15, 16, 17], [63, 64, 65, 0, 0], [128, 200, 1, 511], [1000]]
+
+
+@pytest.mark.parametrize("dq,dc", [(BF, BF), (FH, FH), (F4, BF)])
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("lens", LENS)
+def test_one_token(pkg, dq, dc, hd, lens):
+    """Single new tokens: group 7, page 16; empty requests among them."""
+    c = attn_case(hd + len(lens), lens, [min(1, n) for n in lens], 14, 2, hd, 16, dq, dc)
+    check_attn(c, *call(pkg, c))
+
+
+@pytest.mark.parametrize("nq,nkv", [(1, 1), (8, 1), (4, 4), (10, 2), (16, 1), (17, 1), (40, 8), (66, 2)])
+@pytest.mark.parametrize("rows", [1, 3, 9])
+def test_head_layouts(pkg, nq, nkv, rows):
+    c = attn_case(nq + rows, [77, 9, 130], [rows] * 3, nq, nkv, 64, 32)
+    check_attn(c, *call(pkg, c))
+
+
+@pytest.mark.parametrize("page", [16, 32, 64, 128, 256])
+@pytest.mark.parametrize("layout", ["pages", "pool", "nhd", "padded"])
+@pytest.mark.parametrize("hd", [64, 128])
+def test_pages_and_cache_layouts(pkg, page, layout, hd):
+    c = attn_case(page, [page - 1, page, page + 1, 3 * page + 5], [1, 2, 3, 4], 4, 2, hd, page, layout=layout,
+                  strided_q=True)
+    check_attn(c, *call(pkg, c))
+
+
+@pytest.mark.parametrize("dq,dc", [(BF, BF), (FH, FH), (F4, BF)])
+@pytest.mark.parametrize("rows", [2, 5, 9, 16, 17, 33, 64])
+def test_tree_masks(pkg, dq, dc, rows):
+    """Masked rows, some of which see nothing of the pass; requests that are
+    nothing but the pass's rows leave such rows empty."""
+    c = attn_case(rows, [rows, rows + 1, 100 + rows, rows], [rows, rows, rows, 1], 6, 2, 64, 16, dq, dc, tree=True)
+    check_attn(c, *call(pkg, c))
+
+
+@pytest.mark.parametrize("dq,dc", [(BF, BF), (F4, BF)])
+@pytest.mark.parametrize("rows", [1, 7, 40, 80])
+def test_many_rows(pkg, dq, dc, rows):
+    c = attn_case(rows, [rows, 300 + rows, rows + 63], [rows, rows, max(1, rows - 1)], 14, 2, 128, 64, dq, dc)
+    check_attn(c, *call(pkg, c))
+
+
+def test_ragged_rows_and_requests_without_rows(pkg):
+    c = attn_case(5, [70, 33, 0, 129, 5, 64], [3, 0, 0, 9, 5, 1], 4, 2, 128, 32, pad=4)
+    check_attn(c, *call(pkg, c))
+
+
+def test_rows_past_max_rows_and_past_n_are_left(pkg):
+    c = attn_case(6, [50, 60], [6, 6], 4, 2, 64, 16, pad=0)
+    c["max_rows"] = 4
+    check_attn(c, *call(pkg, c))
+    c = attn_case(6, [50, 60], [6, 6], 4, 2, 64, 16, pad=0)
+    out, lse = call(pkg, c)
+    # The same call told of fewer rows than starts promises writes those alone.
+    short = dict(c, q=c["q"][:9])
+    o9, l9 = call(pkg, short)
+    assert torch.equal(o9, out[:9]) and torch.equal(l9, lse[:9])
+
+
+def test_more_rows_than_tokens(pkg):
+    """Rows before position 0 see nothing."""
+    c = attn_case(8, [3, 40], [3, 2], 4, 2, 64, 16)
+    c["starts"] = [0, 5, 7]
+    c["q"] = torch.randn(9, 4, 64, device="cuda").to(BF)
+    c["max_rows"] = 5
+    check_attn(c, *call(pkg, c))
+
+
+def test_without_starts(pkg):
+    c = attn_case(9, [30, 70, 12], [2, 2, 2], 4, 2, 64, 16, pad=0)
+    a, la = call(pkg, c)
+    b, lb = call(pkg, c, starts=None, max_rows=None)
+    assert torch.equal(a, b) and torch.equal(la, lb)
+    check_attn(c, a, la)
+
+
+def test_scale_and_no_lse(pkg):
+    for scale in (1.0, -0.3, 0.0):
+        c = attn_case(10, [90, 33], [1, 4], 4, 2, 64, 16, q_scale=1.0)
+        out, lse = call(pkg, c, scale=scale)
+        check_attn(c, out, lse, scale)
+        o2, _ = call(pkg, c, scale=scale, lse=None)
+        assert torch.equal(out[:5], o2[:5])
+
+
+def test_lens_past_the_table_and_pages_outside_the_cache(pkg):
+    c = attn_case(11, [64, 100], [1, 2], 4, 2, 64, 16, stale=0.5)
+    c["lens"] = [10 ** 9, 100]      # cut to the table's width
+    c["tables"][0] = [c["tables"][0][i % 4] for i in range(len(c["tables"][0]))]
+    c["tables"][1][2], c["tables"][1][5] = -5, c["k"].shape[0]   # read as zeros
+    check_attn(c, *call(pkg, c))
+    c["lens"] = [-3, 100]           # nothing to see
+    check_attn(c, *call(pkg, c))
+
+
+@pytest.mark.parametrize("dq,dc", [(BF, BF), (FH, FH), (F4, BF)])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("tree", [False, True])
+def test_masked_nan_and_inf_change_nothing(pkg, dq, dc, bad, tree):
+    """Keys and values of later rows, other branches and slots past the
+    length: whatever they hold, rows that do not see them stay the same."""
+    rows = 9
+    c = attn_case(12, [100, rows, 64 + 3], [rows, rows, 6], 14, 2, 64, 16, dq, dc, tree=tree, stale=bad)
+    good, lgood = call(pkg, c)
+    check_attn(c, good, lgood)
+    # Spoil the last row's slot of every request: only rows that see it change.
+    spoiled = []
+    for b, n in enumerate(c["lens"]):
+        pg, off = c["tables"][b][(n - 1) // 16], (n - 1) % 16
+        c["k"][pg, 0, off] = bad
+        c["v"][pg, :, off] = bad
+        r = c["starts"][b + 1] - c["starts"][b]
+        for j in range(r):
+            m = c["mask"][c["starts"][b] + j] if tree else (1 << (j + 1)) - 1
+            if (m >> (r - 1)) & 1:
+                spoiled.append(c["starts"][b] + j)
+    out, lse = call(pkg, c)
+    keep = [i for i in range(good.shape[0]) if i not in spoiled]
+    assert torch.equal(out[keep], good[keep]) and torch.equal(lse[keep], lgood[keep])
+    assert spoiled and not bool(torch.isfinite(out[spoiled][:, 7:]).any())   # head 1: V alone is spoiled
+
+
+def test_large_scores(pkg):
+    """Scores far apart and far from zero: the running maximum is followed."""
+    c = attn_case(13, [500, 3], [2, 3], 4, 2, 64, 16, q_scale=60.0)
+    check_attn(c, *call(pkg, c))
+
+
+def test_same_result_in_every_run_and_on_another_stream(pkg):
+    c = attn_case(14, [700, 33, 64, 1300], [9, 2, 9, 1], 14, 2, 128, 32)
+    a, la = call(pkg, c)
+    s = torch.cuda.Stream()
+    for _ in range(3):
+        s.wait_stream(torch.cuda.current_stream())
+        b, lb = call(pkg, c, stream=s)
+        torch.cuda.current_stream().wait_stream(s)
+        assert torch.equal(a, b) and torch.equal(la, lb)
+
+
+def test_two_calls_at_once(pkg):
+    """Two streams, a workspace each (allocated by the calls)."""
+    cs = [attn_case(15 + i, [900 + i, 40], [3, 1], 14, 2, 128, 32) for i in range(2)]
+    want = [call(pkg, c) for c in cs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cs]
+    got = []
+    for _ in range(5):
+        for c, s in zip(cs, streams):
+            with torch.cuda.stream(s):
+                got.append(call(pkg, c))
+    torch.cuda.synchronize()
+    for i, (o, l) in enumerate(got):
+        assert torch.equal(o, want[i % 2][0]) and torch.equal(l, want[i % 2][1])
+
+
+def test_captured_pass_replayed_with_other_lengths(pkg):
+    """Plan, append and attention captured once; replays read new lengths."""
+    nq, nkv, hd, page, B, R, W = 4, 2, 64, 16, 3, 2, 8
+    g = torch.Generator(device="cuda").manual_seed(3)
+    kc, vc = make_cache(30, nkv, page, hd, BF, fill=0.0)
+    lens, starts = i32([0] * B), i32([0, R, 2 * R, 3 * R])
+    tables, held, free, n_free = i32([[0] * W] * B), i32([0] * B), i32(list(range(30))), i32([30])
+    q, k, v = (torch.zeros((B * R, h, hd), dtype=BF, device="cuda") for h in (nq, nkv, nkv))
+    cs = pkg.rope_table(W * page, hd, 1e4)
+    out, lse = torch.zeros_like(q), torch.zeros((B * R, nq), device="cuda")
+    ws = pkg.paged_attention_workspace(q, kc, tables, R)
+    plan = pkg.PagePlan(i32([0] * B * R), i32([0] * B * R), held, n_free, i32([0] * B))
+
+    def one_pass():
+        pkg.page_plan(lens, starts, tables, held, free, n_free, page, slots=plan.slots, positions=plan.positions,
+                      status=plan.status)
+        qr = pkg.kv_append(k, v, plan.slots, kc, vc, q=q, positions=plan.positions, rope=cs)
+        pkg.paged_attention(qr, kc, vc, tables, lens, starts=starts, max_rows=R, out=out, lse=lse, workspace=ws)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        lens.fill_(R)
+        one_pass()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        one_pass()
+    hist = [[] for _ in range(B)]      # (k, v) of every committed token, as the cache holds them
+    now = [0] * B
+    r = random.Random(4)
+    lens.fill_(0)
+    for step in range(40):
+        for x, h in ((q, nq), (k, nkv), (v, nkv)):
+            x.copy_(torch.randn((B * R, h, hd), device="cuda", generator=g))
+        now = [x + R if x + R <= W * page else R for x in now]
+        lens.copy_(i32(now))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert plan.status.tolist() == [0] * B
+        assert sorted(free.tolist()[:n_free.item()] + [p for b in range(B) for p in tables[b].tolist()[:held[b].item()]]) \
+            == list(range(30))
+        cq = torch.zeros_like(q)
+        for b in range(B):
+            hist[b] = hist[b][:now[b] - R]
+            for j in range(R):
+                i, pos = b * R + j, now[b] - R + j
+                rot = [op.rotate(k[i, h].cpu(), cs[pos].cpu()).to(BF) for h in range(nkv)]
+                hist[b].append((torch.stack(rot), v[i].cpu()))
+                for h in range(nq):
+                    cq[i, h] = op.rotate(q[i, h].cpu(), cs[pos].cpu()).to(BF)
+        for b in range(B):
+            kk = torch.stack([x[0] for x in hist[b]]).double()
+            vv = torch.stack([x[1] for x in hist[b]]).double()
+            for j in range(R):
+                seen = torch.zeros(now[b], dtype=torch.bool)
+                seen[:now[b] - R + j + 1] = True
+                for h in range(nq):
+                    ref, _, A, qk = op.attention(cq[b * R + j, h].cpu(), kk[:, h // 2], vv[:, h // 2], 0.125, seen)
+                    # Beside the operator's own bound: the oracle's rotated rows may round to
+                    # the other bf16 neighbour (an error of 2^-7 of a key or query), which
+                    # moves a score by at most 2 * 2^-7 * qk.
+                    eps = 2 * 2.0 ** -6 * max(qk, 1.0)
+                    err = (out[b * R + j, h].double().cpu() - ref).abs()
+                    assert bool((err <= (2.0 ** -8 + eps) * A + (2.0 ** -8 + eps) * ref.abs() + 1e-30).all())
+        # Some guesses are rejected: the next pass starts from fewer tokens.
+        now = [max(0, x - r.randint(0, R)) if r.random() < 0.9 else 0 for x in now]
+
+
+def test_offsets_past_32_bits(pkg):
+    """Pages whose keys lie more than 2^31 elements into the cache."""
+    nkv, page, hd = 8, 256, 128
+    per = nkv * page * hd
+    n_pages = (2 ** 31 + 2 ** 27) // per
+    k = torch.zeros((n_pages, nkv, page, hd), dtype=BF, device="cuda")
+    v = torch.zeros_like(k)
+    g = torch.Generator(device="cuda").manual_seed(2)
+    ids = [n_pages - 1, 0, n_pages - 3, n_pages - 2]
+    kr, vr = (torch.randn((700, nkv, hd), dtype=BF, device="cuda", generator=g) for _ in range(2))
+    slots = [ids[s // page] * page + s % page for s in range(700)]
+    pkg.kv_append(kr, vr, i32(slots), k, v)
+    small_k, small_v = k[torch.tensor(ids, device="cuda")], v[torch.tensor(ids, device="cuda")]
+    assert torch.equal(small_k.transpose(1, 2).reshape(-1, nkv, hd)[:700], kr)
+    q = torch.randn((2, 16, hd), dtype=BF, device="cuda", generator=g)
+    c = dict(q=q, k=k, v=v, tables=[ids], lens=[700], starts=[0, 2], mask=None, max_rows=2)
+    out, lse = call(pkg, c)
+    c.update(k=small_k, v=small_v, tables=[[0, 1, 2, 3]])
+    o2, l2 = call(pkg, c)
+    assert torch.equal(out, o2) and torch.equal(lse, l2)
+    check_attn(c, out, lse)
+
+
+def test_many_requests(pkg):
+    r = random.Random(1)
+    lens = [r.choice([0, 1, r.randint(1, 60)]) for _ in range(1500)]
+    c = attn_case(21, lens, [min(1, n) for n in lens], 2, 1, 64, 16)
+    check_attn(c, *call(pkg, c))
+
+
+def test_wrapper_refusals(pkg):
+    c = attn_case(22, [30], [1], 4, 2, 64, 16)
+    for kw in (dict(max_rows=None), dict(workspace=torch.empty(1, dtype=torch.uint8, device="cuda")),
+               dict(lse=torch.empty(2, 3, device="cuda")), dict(out=torch.empty(3, 4, 32, dtype=BF, device="cuda")),
+               dict(starts=i32([0, 1, 2])), dict(mask=i32([1, 2, 3])), dict(mask=torch.ones(3, dtype=torch.int64))):
+        with pytest.raises(ValueError):
+            call(pkg, c, **kw)
+    with pytest.raises(ValueError):
+        pkg.kv_append(c["k"][:, 0], c["v"][:, 0], i32([0]), c["k"], c["v"])
+    with pytest.raises(ValueError):
+        pkg.page_plan(i32([1]), i32([0, 1]), i32([[0]]), i32([0]), i32([0]), i32([1]), 16)
+    with pytest.raises(pkg.SFError):
+        pkg.page_plan(i32([1]), i32([0, 1]), i32([[0]]), i32([0]), i32([0]), i32([1]), 17, n_rows=1)
