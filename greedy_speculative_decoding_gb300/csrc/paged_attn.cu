@@ -1,112 +1,69 @@
-// Attention of the requests' newest rows over a paged key-value cache
-// (sf_paged_attention).
-//
-// One warp per (token row, query head): 32 slots at a time, a lane scores one
-// slot; the softmax runs online (running maximum, sum and output), in fp32.
+// Attention over a paged key-value cache: the C entry (the kernels are in
+// paged_attn.cuh).
+#include <algorithm>
 #include <cmath>
 
-#include "paged.h"
+#include "paged_attn_launch.cuh"
 
 namespace sf {
-namespace {
+namespace pa {
 
-struct PagedAttnArgs {
-  const void *q, *kc, *vc;
-  void* out;
-  long q_row, q_head, o_row, o_head;
-  long k_page, k_head, k_slot, v_page, v_head, v_slot;
-  float* lse;
-  const int *tables, *lens, *starts;
-  const unsigned long long* mask;
-  int B, N, W, nq, group, shift, n_pages, max_rows;
-  float scale;
+constexpr int kMaxCtas = 512;   // CTAs of a launch, at most
+constexpr int kMaxDesc = 1024;  // item descriptors
+
+struct Layout {
+  size_t ml, part, total;
 };
-
-__device__ __forceinline__ float to_f(float x) { return x; }
-__device__ __forceinline__ float to_f(bf16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
-__device__ __forceinline__ void from_f(float* p, float x) { *p = x; }
-__device__ __forceinline__ void from_f(bf16* p, float x) { *p = __float2bfloat16_rn(x); }
-__device__ __forceinline__ void from_f(__half* p, float x) { *p = __float2half_rn(x); }
-
-template <int HD, typename TQ, typename TC>
-__global__ void __launch_bounds__(128) k_paged_attn_rows(const __grid_constant__ PagedAttnArgs a) {
-  __shared__ float sq[4][HD];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long w = blockIdx.x * 4l + warp;
-  const int b = (int)(w / ((long)a.max_rows * a.nq)), rem = (int)(w - (long)b * a.max_rows * a.nq);
-  const int j = rem / a.nq, h = rem - j * a.nq;
-  if (b >= a.B) return;
-  int s0, rows;
-  if (a.starts) {
-    s0 = a.starts[b];
-    rows = a.starts[b + 1] - s0;
-  } else {
-    rows = a.N / a.B;
-    s0 = b * rows;
-  }
-  if (j >= rows || s0 < 0 || s0 + j >= a.N) return;
-  const int row = s0 + j, kvh = h / a.group;
-  const int len = (int)min((long)max(a.lens[b], 0), (long)a.W << a.shift);
-  const int p0 = len - rows;   // the pass's first slot
-  const unsigned long long bits = a.mask ? a.mask[row] : 0;
-  const TQ* q = static_cast<const TQ*>(a.q) + row * a.q_row + h * a.q_head;
-  for (int d = lane; d < HD; d += 32) sq[warp][d] = to_f(q[d]);
-  __syncwarp();
-  float m = -INFINITY, l = 0.f, o[HD / 32];
-#pragma unroll
-  for (int i = 0; i < HD / 32; ++i) o[i] = 0.f;
-  for (int t = 0; t < len; t += 32) {
-    const int s = t + lane, i = s - p0;
-    const bool see = s < len && (i < 0 || (a.mask ? i < 64 && ((bits >> i) & 1) : i <= j));
-    int page = -1;
-    float x = -INFINITY;
-    if (see) {
-      page = a.tables[(long)b * a.W + (s >> a.shift)];
-      float dot = 0.f;
-      if (page >= 0 && page < a.n_pages) {
-        const TC* k = static_cast<const TC*>(a.kc) + page * a.k_page + kvh * a.k_head +
-                      (s & ((1 << a.shift) - 1)) * a.k_slot;
-        for (int d = 0; d < HD; ++d) dot = fmaf(sq[warp][d], to_f(k[d]), dot);
-      } else {
-        page = -1;
-      }
-      x = dot * a.scale;
-    }
-    const float m_new = fmaxf(m, warp_max(x));
-    const float ref = m_new == -INFINITY ? 0.f : m_new;
-    const float alpha = expf(m - ref), p = see ? expf(x - ref) : 0.f;
-    l = l * alpha + warp_sum(p);
-#pragma unroll
-    for (int e = 0; e < HD / 32; ++e) o[e] *= alpha;
-    for (int c = 0; c < 32; ++c) {
-      const float pc = __shfl_sync(0xffffffffu, p, c);
-      const int pg = __shfl_sync(0xffffffffu, page, c);
-      if (pg < 0) continue;
-      const TC* v = static_cast<const TC*>(a.vc) + pg * a.v_page + kvh * a.v_head +
-                    ((t + c) & ((1 << a.shift) - 1)) * a.v_slot;
-#pragma unroll
-      for (int e = 0; e < HD / 32; ++e) o[e] = fmaf(pc, to_f(v[lane + 32 * e]), o[e]);
-    }
-    m = m_new;
-  }
-  TQ* out = static_cast<TQ*>(a.out) + row * a.o_row + h * a.o_head;
-#pragma unroll
-  for (int e = 0; e < HD / 32; ++e) from_f(out + lane + 32 * e, l == 0.f ? 0.f : o[e] / l);
-  if (a.lse && lane == 0) a.lse[(long)row * a.nq + h] = l == 0.f ? -INFINITY : m + logf(l);
+static Layout layout(int n_heads, int n_kv_heads, int head_dim, int max_rows) {
+  const int queries = max_rows * (n_heads / n_kv_heads);
+  const size_t mt = std::min(queries, tile_of(queries));
+  Layout l;
+  l.ml = kMaxDesc * sizeof(int4);
+  l.part = l.ml + 2 * kMaxCtas * mt * sizeof(float2);
+  l.total = l.part + 2 * kMaxCtas * mt * head_dim * sizeof(float);
+  return l;
 }
 
-template <int HD>
-cudaError_t launch_rows(const PagedAttnArgs& a, int qt, int ct, cudaStream_t st) {
-  const long warps = (long)a.B * a.max_rows * a.nq;
-  const int grid = (int)((warps + 3) / 4);
-  if (qt == SF_DT_BF16) k_paged_attn_rows<HD, bf16, bf16><<<grid, 128, 0, st>>>(a);
-  else if (qt == SF_DT_F16) k_paged_attn_rows<HD, __half, __half><<<grid, 128, 0, st>>>(a);
-  else k_paged_attn_rows<HD, float, bf16><<<grid, 128, 0, st>>>(a);
-  return cudaGetLastError();
+// Tensor map of the keys or values, {head_dim, slots, heads, pages}: the
+// two middle dimensions by ascending stride (*nhd: the heads come first).
+static cudaError_t cache_map(CUtensorMap* map, int* nhd, const sf_paged_cache& c, const void* base, int64_t s_page,
+                             int64_t s_head, int64_t s_slot) {
+  typedef CUresult (*encode_fn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+  static std::atomic<encode_fn> known{nullptr};
+  encode_fn encode = known.load(std::memory_order_relaxed);
+  if (!encode) {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q);
+    if (e != cudaSuccess) return e;
+    if (q != cudaDriverEntryPointSuccess || !fn) return cudaErrorSymbolNotFound;
+    encode = reinterpret_cast<encode_fn>(fn);
+    known.store(encode, std::memory_order_relaxed);
+  }
+  // Dimensions of one element never move: their strides only have to be legal.
+  if (c.n_kv_heads == 1) s_head = std::max<int64_t>(s_slot, c.head_dim) * c.page;
+  if (c.n_pages == 1) s_page = std::max(s_head * c.n_kv_heads, s_slot * c.page);
+  *nhd = c.n_kv_heads > 1 && s_head < s_slot;
+  const cuuint32_t bp = std::min(c.page, kTile);
+  cuuint64_t dims[4] = {(cuuint64_t)c.head_dim, (cuuint64_t)c.page, (cuuint64_t)c.n_kv_heads, (cuuint64_t)c.n_pages};
+  cuuint64_t strides[3] = {(cuuint64_t)s_slot * 2, (cuuint64_t)s_head * 2, (cuuint64_t)s_page * 2};
+  cuuint32_t box[4] = {64, bp, 1, 1};
+  if (*nhd) {
+    std::swap(dims[1], dims[2]);
+    std::swap(strides[0], strides[1]);
+    std::swap(box[1], box[2]);
+  }
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  const CUresult r = encode(map, c.dtype == SF_DT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                            4, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-}  // namespace
+}  // namespace pa
 }  // namespace sf
 
 using namespace sf;
@@ -116,7 +73,7 @@ extern "C" size_t sf_paged_attention_workspace_bytes(int32_t n_heads, int32_t n_
   if (n_heads < 1 || n_kv_heads < 1 || n_heads % n_kv_heads || n_heads > 65535 || (head_dim != 64 && head_dim != 128) ||
       max_rows < 1 || max_rows > SF_MAX_ROWS)
     return 0;
-  return 256;
+  return pa::layout(n_heads, n_kv_heads, head_dim, max_rows).total;
 }
 
 extern "C" sf_status sf_paged_attention(const sf_paged_cache* cache, const sf_rows* q, const sf_rows* out, int32_t n,
@@ -147,20 +104,37 @@ extern "C" sf_status sf_paged_attention(const sf_paged_cache* cache, const sf_ro
         (r->n_heads > 1 && r->head % al))
       return set_error(SF_ERR_ARG, "sf_paged_attention: q and out must be 16-byte aligned with strides of multiples of 16 bytes");
   if (!std::isfinite(scale)) return set_error(SF_ERR_ARG, "sf_paged_attention: scale must be finite");
-  PagedAttnArgs a{};
+  pa::Args a{};
+  cudaError_t e = pa::cache_map(&a.km, &a.k_nhd, *cache, cache->k, cache->k_page, cache->k_head, cache->k_slot);
+  if (e == cudaSuccess) e = pa::cache_map(&a.vm, &a.v_nhd, *cache, cache->v, cache->v_page, cache->v_head, cache->v_slot);
+  int dev = 0, sms = 0;
+  if (e == cudaSuccess) e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return set_error(SF_ERR_CUDA, "sf_paged_attention: %s", cudaGetErrorString(e));
   a.q = q->data, a.q_row = q->row, a.q_head = q->head;
   a.out = out->data, a.o_row = out->row, a.o_head = out->head;
-  a.kc = cache->k, a.k_page = cache->k_page, a.k_head = cache->k_head, a.k_slot = cache->k_slot;
-  a.vc = cache->v, a.v_page = cache->v_page, a.v_head = cache->v_head, a.v_slot = cache->v_slot;
   a.lse = d_lse;
   a.tables = d_tables, a.lens = d_lens, a.starts = d_starts;
   a.mask = reinterpret_cast<const unsigned long long*>(d_mask);
-  a.B = batch, a.N = n, a.W = table_width, a.nq = q->n_heads, a.group = q->n_heads / cache->n_kv_heads;
-  a.shift = log2_of(cache->page), a.n_pages = cache->n_pages, a.max_rows = max_rows;
-  a.scale = scale;
+  a.B = batch, a.N = n, a.W = table_width, a.nq = q->n_heads, a.nkv = cache->n_kv_heads;
+  a.group = q->n_heads / cache->n_kv_heads;
+  a.shift = log2_of(cache->page), a.max_rows = max_rows, a.rows_each = n / batch;
+  a.scale2 = scale * 1.44269504088896f;
+  const int queries = max_rows * a.group, mt = pa::tile_of(queries);
+  a.mt_max = std::min(queries, mt);
+  a.ntq_max = (queries + mt - 1) / mt;
+  const long items = (long)batch * a.nkv * a.ntq_max;
+  a.by_item = items <= pa::kMaxDesc;
+  const pa::Layout lay = pa::layout(q->n_heads, cache->n_kv_heads, cache->head_dim, max_rows);
+  unsigned char* ws = static_cast<unsigned char*>(d_workspace);
+  a.desc = reinterpret_cast<int4*>(ws);
+  a.part_ml = reinterpret_cast<float2*>(ws + lay.ml);
+  a.part = reinterpret_cast<float*>(ws + lay.part);
+  const long max_units = items * (((long)table_width * cache->page + pa::kTile - 1) / pa::kTile);
+  sms = std::min(sms, pa::kMaxCtas / 2);
   cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
-  const cudaError_t e = cache->head_dim == 128 ? launch_rows<128>(a, q->dtype, cache->dtype, st)
-                                               : launch_rows<64>(a, q->dtype, cache->dtype, st);
+  e = cache->head_dim == 128 ? pa::launch_hd128(a, q->dtype, sms, max_units, st)
+                             : pa::launch_hd64(a, q->dtype, sms, max_units, st);
   if (e != cudaSuccess) return set_error(SF_ERR_CUDA, "sf_paged_attention: %s", cudaGetErrorString(e));
   return SF_OK;
 }

@@ -1,0 +1,742 @@
+// Attention of the requests' newest rows over a paged key-value cache.
+//
+// For a token row and query head, out = sum_s p_s v_s / sum_s p_s with
+// p_s = 2^(x_s - max x), x_s = (q . k_s) * scale * log2(e), over the slots s
+// that the row sees. The cache is read once: the maximum, the sum and the
+// output run along with the slots (in fp32; a new maximum rescales them).
+//
+// Work. An item is (request, KV head, tile of MT queries): the queries are
+// the request's rows times the query heads that read this KV head. An item
+// has one unit per 64 slots of the request. The units of all items, in
+// order, are dealt out evenly to the CTAs, so lengths that differ by orders
+// of magnitude load the GPU evenly and a single long request is spread over
+// all of it. A CTA that holds an item from end to end writes the result; of
+// an item that several CTAs share each leaves its part (output, maximum, sum)
+// in the workspace, and the join kernel adds the parts in slot order.
+//
+// A CTA: one producer warp follows the block table and brings 64 slots of
+// keys and values at a time into a ring in shared memory (TMA boxes of 64
+// dimensions by min(page, 64) slots, 128-byte swizzle); WM x WK consumer
+// warps compute on them with mma.sync: warp (wm, wk) takes 16 queries and
+// 64 / WK of the slots, with a running maximum, sum and output of its own,
+// joined over wk at the end of the item. Few queries (one new token: the
+// query heads of one KV head) share the slots out between the warps, many
+// queries share out the queries.
+#pragma once
+
+#include "paged.h"
+
+namespace sf {
+namespace pa {
+
+constexpr int kTile = 64;                 // slots of a unit
+constexpr uint32_t kWaitIters = 1u << 24; // bound of every wait
+
+struct Args {
+  CUtensorMap km, vm;      // cache as {head_dim, slot or head, head or slot, page}
+  int k_nhd, v_nhd;        // 1: the tensor map's second dimension is the head
+  const void* q;
+  void* out;
+  long q_row, q_head, o_row, o_head;
+  float* lse;
+  const int *tables, *lens, *starts;
+  const unsigned long long* mask;
+  int B, N, W, nq, nkv, group, shift, max_rows, rows_each;
+  float scale2;            // scale * log2(e)
+  int stages;
+  int mt_max;              // queries of an item at most (min(MT, max_rows * group))
+  int ntq_max;             // items of a (request, KV head) at most
+  int by_item;             // descriptors by item (else by the CTA that starts it)
+  int4* desc;              // {first CTA, CTAs, request, KV head * ntq + query tile}
+  float* part;             // [CTA][2][mt_max][HD]: output parts (0: of an item begun before, 1: begun here)
+  float2* part_ml;         // [CTA][2][mt_max]: (maximum, sum)
+};
+
+// A request as the kernel sees it: whatever lens and starts hold, rows lie in
+// [0, N) and slots within the table.
+struct Request {
+  int s0, rows, len, p0, nt, ntq;   // first row, rows computed, slots, the pass's first slot, units, query tiles
+};
+
+template <int MT>
+__device__ __forceinline__ Request request(const Args& a, int b) {
+  Request r;
+  int rows;
+  if (a.starts) {
+    r.s0 = a.starts[b];
+    rows = a.starts[b + 1] - r.s0;
+  } else {
+    r.s0 = b * a.rows_each;
+    rows = a.rows_each;
+  }
+  r.len = (int)min((long)max(a.lens[b], 0), (long)a.W << a.shift);
+  r.p0 = r.len - rows;
+  r.rows = (r.s0 < 0 || r.s0 >= a.N) ? 0 : max(0, min(min(rows, a.max_rows), a.N - r.s0));
+  r.nt = r.rows > 0 ? max(1, (r.len + kTile - 1) / kTile) : 0;
+  r.ntq = (r.rows * a.group + MT - 1) / MT;
+  return r;
+}
+
+// CTA c of G takes units [c * T / G, (c + 1) * T / G) of T.
+__device__ __forceinline__ long first_unit(long c, long T, long G) { return c * T / G; }
+__device__ __forceinline__ int cta_of_unit(long u, long T, long G) { return (int)(((u + 1) * G - 1) / T); }
+
+template <typename T>
+struct Num;
+template <>
+struct Num<bf16> {
+  static constexpr uint32_t kExp = 0x7f80u;   // exponent bits: all set in infinities and NaN
+  static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+  static __device__ __forceinline__ float lo(uint32_t w) { return __uint_as_float(w << 16); }
+  static __device__ __forceinline__ float hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+  static __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    mma_bf16_16816(d, a[0], a[1], a[2], a[3], b0, b1);
+  }
+};
+template <>
+struct Num<__half> {
+  static constexpr uint32_t kExp = 0x7c00u;
+  static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+  static __device__ __forceinline__ float lo(uint32_t w) { return __low2float(*reinterpret_cast<const __half2*>(&w)); }
+  static __device__ __forceinline__ float hi(uint32_t w) { return __high2float(*reinterpret_cast<const __half2*>(&w)); }
+  static __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+        "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  }
+};
+
+__device__ __forceinline__ void ldsm_x4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+__device__ __forceinline__ void ldsm_x4_trans(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+__device__ __forceinline__ float exp2_approx(float x) {   // relative error 2^-22; 0 below the normal range
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w,
+                                            uint64_t* bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar)), "l"(policy)
+      : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+template <int HD, int WM, int WK, bool F32>
+struct Shape {
+  static constexpr int MT = 16 * WM;                 // queries of an item
+  static constexpr int kWarps = WM * WK;             // consumer warps
+  static constexpr int kThreads = (kWarps + 1) * 32;
+  static constexpr int kHalf = HD / 64;              // 64-dimension boxes of a key
+  static constexpr int kBox = kTile * 128;           // bytes of one box column: 64 slots x 64 dimensions
+  static constexpr int kStage = 2 * kHalf * kBox;    // keys and values of a unit
+  static constexpr int QP = HD + 8;                  // pitch of the fp32 queries' bf16 terms
+  static constexpr int OP = HD + 8;                  // pitch of the parts joined over wk
+  static constexpr int kQBytes = F32 ? 3 * MT * QP * 2 : 0;
+  static constexpr int kOBytes = WK > 1 ? WK * MT * (OP + 2) * 4 : 0;
+  static constexpr int kExtra = kQBytes > kOBytes ? kQBytes : kOBytes;   // one region: never both at once
+  static constexpr int kMaxStages = 4;
+  // Two CTAs on an SM when at least two stages fit in half its shared memory.
+  static constexpr int kFit2 = (kHalfSmBytes - 1024 - kExtra) / kStage;
+  static constexpr int kCtas = kFit2 >= 2 ? 2 : 1;
+  static constexpr int kFit1 = (220 * 1024 - 1024 - kExtra) / kStage;
+  static constexpr int kFit = kCtas == 2 ? kFit2 : kFit1;
+  static constexpr int kStages = kFit < kMaxStages ? kFit : kMaxStages;
+  static constexpr int kSmem = 1024 + kStages * kStage + kExtra;
+};
+
+// The CTA's first unit: (request, unit within it). Every thread calls it.
+struct Start {
+  long T;       // units in all
+  long base;    // units before request b
+  int b;
+};
+template <int MT, int NT>
+__device__ __forceinline__ Start locate(const Args& a, long G, long* sh) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  constexpr int NW = NT / 32;
+  const int per = (a.B + NT - 1) / NT;
+  const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
+  long mine = 0;
+  for (int b = b0; b < b1; ++b) {
+    const Request r = request<MT>(a, b);
+    mine += (long)a.nkv * r.ntq * r.nt;
+  }
+  long incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long x = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += x;
+  }
+  if (lane == 31) sh[warp] = incl;
+  __syncthreads();
+  long before = 0, T = 0;
+#pragma unroll
+  for (int w = 0; w < NW; ++w) {
+    if (w < warp) before += sh[w];
+    T += sh[w];
+  }
+  const long g = min(G, T);
+  const long u0 = (long)blockIdx.x < g ? first_unit(blockIdx.x, T, g) : -1;
+  const long lo = before + incl - mine;
+  if (u0 >= lo && u0 < lo + mine) {
+    long base = lo;
+    for (int b = b0; b < b1; ++b) {
+      const Request r = request<MT>(a, b);
+      const long n = (long)a.nkv * r.ntq * r.nt;
+      if (u0 < base + n) {
+        sh[NW] = base;
+        sh[NW + 1] = b;
+        break;
+      }
+      base += n;
+    }
+  }
+  __syncthreads();
+  return {T, sh[NW], (int)sh[NW + 1]};
+}
+
+// Walks the pieces of items that a CTA's units [u, u1) make up.
+template <int MT>
+struct Walk {
+  long u, u1, rem;
+  int b;
+  Request r;
+  int item, kvh, qt, t0, t1;   // the current piece: item within the request, units t0 .. t1 - 1
+  __device__ __forceinline__ Walk(const Args& a, const Start& s, long first, long last)
+      : u(first), u1(last), rem(first - s.base), b(s.b) {
+    r = request<MT>(a, b);
+  }
+  // The next piece; false at the end.
+  __device__ __forceinline__ bool next(const Args& a) {
+    if (u >= u1) return false;
+    while (rem >= (long)a.nkv * r.ntq * r.nt) {
+      rem = 0;
+      r = request<MT>(a, ++b);
+    }
+    item = (int)(rem / r.nt);
+    t0 = (int)(rem - (long)item * r.nt);
+    t1 = (int)min((long)r.nt, t0 + (u1 - u));
+    kvh = item / r.ntq;
+    qt = item - kvh * r.ntq;
+    u += t1 - t0;
+    rem += t1 - t0;
+    return true;
+  }
+};
+
+template <typename TQ>
+__device__ __forceinline__ void store2(TQ* p, float x, float y) {
+  *reinterpret_cast<uint32_t*>(p) = Num<TQ>::pack(x, y);
+}
+template <>
+__device__ __forceinline__ void store2<float>(float* p, float x, float y) {
+  *reinterpret_cast<float2*>(p) = make_float2(x, y);
+}
+
+// TC: the cache's type. F32: fp32 queries and output over a bf16 cache, the
+// queries and the probabilities as three bf16 terms each (24 bits: exact).
+template <int HD, typename TC, bool F32, int WM, int WK>
+__global__ void __launch_bounds__(Shape<HD, WM, WK, F32>::kThreads, Shape<HD, WM, WK, F32>::kCtas)
+    k_paged_attn(const __grid_constant__ Args a) {
+  using S = Shape<HD, WM, WK, F32>;
+  using TQ = typename std::conditional<F32, float, TC>::type;
+  constexpr int MT = S::MT, SW = kTile / WK, KS = HD / 16, ND = HD / 8, NS = SW / 8, NQ = F32 ? 3 : 1;
+  extern __shared__ unsigned char pa_smem_raw[];
+  unsigned char* ring = pa_smem_raw + ((1024 - (smem_u32(pa_smem_raw) & 1023)) & 1023);
+  unsigned char* extra = ring + S::kStages * S::kStage;
+  __shared__ long sh_loc[S::kWarps + 3];
+  __shared__ __align__(8) uint64_t full[S::kStages], empty[S::kStages];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) {
+    for (int s = 0; s < S::kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], S::kWarps);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  const Start st = locate<MT, S::kThreads>(a, gridDim.x, sh_loc);   // (its barriers publish the mbarriers too)
+  const long G = min((long)gridDim.x, st.T);
+  if ((long)blockIdx.x >= G) {
+    if (tid == 0 && !a.by_item) a.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
+    pdl_launch_next();
+    return;
+  }
+  const long u0 = first_unit(blockIdx.x, st.T, G), u1 = first_unit(blockIdx.x + 1, st.T, G);
+  Walk<MT> w(a, st, u0, u1);
+
+  if (warp == S::kWarps) {
+    // ---------------------------------------------------------- producer warp
+    const int bp = min(1 << a.shift, kTile);        // slots of a box
+    const int np = kTile / bp;                      // boxes of a column
+    const int boxes = np * S::kHalf * 2;
+    const int i = lane % np, h = (lane / np) % S::kHalf, is_v = lane / (np * S::kHalf);
+    const uint32_t dst0 = smem_u32(ring) + (is_v * S::kHalf + h) * S::kBox + i * bp * 128;
+    const CUtensorMap* map = is_v ? &a.vm : &a.km;
+    const int nhd = is_v ? a.v_nhd : a.k_nhd;
+    int win_b = -1, win = -1, entry = 0;            // the 32 table entries at hand, one per lane
+    int n = 0;
+    bool ok = true;
+    while (ok && w.next(a)) {
+      const uint64_t policy = w.r.ntq == 1 ? policy_evict_first() : policy_evict_normal();
+      for (int t = w.t0; t < w.t1; ++t, ++n) {
+        const int s = n % S::kStages;
+        const int first = (t * kTile) >> a.shift;
+        if (w.b != win_b || (first >> 5) != win) {
+          win_b = w.b;
+          win = first >> 5;
+          const int e = 32 * win + lane;
+          entry = e < a.W ? a.tables[(long)w.b * a.W + e] : -1;
+        }
+        if (n >= S::kStages) ok = mbar_wait(&empty[s], (n / S::kStages - 1) & 1, kWaitIters);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const int left = w.r.len - t * kTile;       // slots from here on
+        const int nb = max(0, min(np, (left + bp - 1) / bp));
+        const int page = __shfl_sync(0xffffffffu, entry, (first + i) & 31);
+        if (lane == 0) mbar_expect_tx(&full[s], nb * bp * 128 * S::kHalf * 2);
+        __syncwarp();
+        if (lane < boxes && i < nb) {
+          const int off = (t * kTile) & ((1 << a.shift) - 1) & ~(kTile - 1);
+          tma_load_4d(dst0 + s * S::kStage, map, 64 * h, nhd ? w.kvh : off, nhd ? off : w.kvh, page, &full[s], policy);
+        }
+      }
+    }
+    // An expired wait: the copies in flight land before the CTA may end.
+    if (!ok)
+      for (int k = max(0, n - S::kStages); k < n; ++k)
+        mbar_wait(&full[k % S::kStages], (k / S::kStages) & 1, kWaitIters);
+    return;
+  }
+
+  // ------------------------------------------------------------ consumer warps
+  const int wm = warp / WK, wk = warp % WK;
+  const int g = lane >> 2, c4 = lane & 3;
+  auto cta_sync = [] { asm volatile("bar.sync 1, %0;" ::"n"(S::kWarps * 32) : "memory"); };
+  // Shared-memory offsets of this lane's ldmatrix rows (keys: 16 slots x 16
+  // dimensions; values: 16 slots x 16 dimensions, transposed).
+  const int k_slot = wk * SW + (lane & 7) + 8 * (lane >> 4), k_piece = (lane >> 3) & 1;
+  const int v_slot = wk * SW + (lane & 7) + 8 * ((lane >> 3) & 1), v_piece = lane >> 4;
+  int n = 0;
+  bool ok = true;
+  while (w.next(a)) {
+    const Request r = w.r;
+    const int q0 = w.qt * MT + 16 * wm;            // this warp's first query
+    const int Mq = r.rows * a.group;
+    int qi[2], j[2];                               // this lane's queries (rows g and g + 8 of the tile)
+    const TQ* qp[2];
+    unsigned long long bits[2] = {0, 0};
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      qi[e] = q0 + g + 8 * e;
+      j[e] = qi[e] / a.group;
+      const int hh = w.kvh * a.group + qi[e] - j[e] * a.group;
+      qp[e] = qi[e] < Mq ? static_cast<const TQ*>(a.q) + (r.s0 + j[e]) * a.q_row + hh * a.q_head : nullptr;
+      if (a.mask && qi[e] < Mq) bits[e] = a.mask[r.s0 + j[e]];
+    }
+    uint32_t qf[F32 ? 1 : KS][4];
+    if constexpr (F32) {
+      // The tile's queries as three bf16 terms in shared memory.
+      bf16* sq = reinterpret_cast<bf16*>(extra);
+      cta_sync();   // the region's last readers are done
+      for (int e = tid; e < MT * (HD / 4); e += S::kWarps * 32) {
+        const int m = e / (HD / 4), d = 4 * (e - m * (HD / 4));
+        const int x = w.qt * MT + m, jj = x / a.group, hh = w.kvh * a.group + x - jj * a.group;
+        float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (x < Mq)
+          f = *reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + (r.s0 + jj) * a.q_row + hh * a.q_head + d);
+        float v[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+          uint32_t p[2];
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            p[y] = Num<bf16>::pack(v[2 * y], v[2 * y + 1]);
+            v[2 * y] -= Num<bf16>::lo(p[y]);
+            v[2 * y + 1] -= Num<bf16>::hi(p[y]);
+          }
+          *reinterpret_cast<uint2*>(sq + (k * MT + m) * S::QP + d) = make_uint2(p[0], p[1]);
+        }
+      }
+      cta_sync();
+    } else {
+#pragma unroll
+      for (int k = 0; k < KS; ++k)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          qf[k][e] = qp[e & 1] ? *reinterpret_cast<const uint32_t*>(qp[e & 1] + 16 * k + 2 * c4 + 8 * (e >> 1)) : 0u;
+    }
+    float o[ND][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+#pragma unroll
+    for (int d = 0; d < ND; ++d) o[d][0] = o[d][1] = o[d][2] = o[d][3] = 0.f;
+
+    for (int t = w.t0; t < w.t1; ++t, ++n) {
+      const int s = n % S::kStages;
+      if (ok && !mbar_wait(&full[s], (n / S::kStages) & 1, kWaitIters)) ok = false;
+      ok = __all_sync(0xffffffffu, ok);
+      const uint32_t ks = smem_u32(ring) + s * S::kStage, vs = ks + S::kHalf * S::kBox;
+      const int base = t * kTile + wk * SW;         // this warp's first slot
+      // ---- scores
+      float x[NS][4];
+#pragma unroll
+      for (int i = 0; i < NS; ++i) x[i][0] = x[i][1] = x[i][2] = x[i][3] = 0.f;
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        uint32_t qk[NQ][4];
+        if constexpr (F32) {
+          const bf16* sq = reinterpret_cast<const bf16*>(extra);
+#pragma unroll
+          for (int e = 0; e < 3; ++e)
+            ldsm_x4(qk[e], smem_u32(sq + (e * MT + 16 * wm + (lane & 7) + 8 * ((lane >> 3) & 1)) * S::QP + 16 * k +
+                                    8 * (lane >> 4)));
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) qk[0][e] = qf[k][e];
+        }
+#pragma unroll
+        for (int i = 0; i < NS / 2; ++i) {
+          const int slot = k_slot + 16 * i, piece = 2 * k + k_piece;
+          uint32_t kb[4];
+          ldsm_x4(kb, ks + (piece >> 3) * S::kBox + slot * 128 + (((piece & 7) ^ (slot & 7)) << 4));
+#pragma unroll
+          for (int e = NQ - 1; e >= 0; --e) {       // the small terms first
+            Num<TC>::mma(x[2 * i], qk[e], kb[0], kb[1]);
+            Num<TC>::mma(x[2 * i + 1], qk[e], kb[2], kb[3]);
+          }
+        }
+      }
+      // ---- what a row does not see is -infinity (never added to: what such
+      // slots hold, NaN included, does not matter)
+      const bool tail = t * kTile + kTile > r.p0 || t * kTile + kTile > r.len;   // holds slots of the pass, or past the end
+      auto sees = [&](int e, int slot) {
+        const int i = slot - r.p0;
+        return qi[e] < Mq && slot < r.len && (i < 0 || (a.mask ? i < 64 && ((bits[e] >> i) & 1) : i <= j[e]));
+      };
+#pragma unroll
+      for (int i = 0; i < NS; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          x[i][e] *= a.scale2;
+          if (tail && !sees(e >> 1, base + 8 * i + 2 * c4 + (e & 1))) x[i][e] = -INFINITY;
+        }
+      // ---- running maximum and sum
+      float ref[2];
+      bool raise = false;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float mx = fmaxf(x[0][2 * e], x[0][2 * e + 1]);
+#pragma unroll
+        for (int i = 1; i < NS; ++i) mx = fmaxf(mx, fmaxf(x[i][2 * e], x[i][2 * e + 1]));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        ref[e] = fmaxf(m[e], mx);
+        raise |= ref[e] != m[e];
+      }
+      if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float f = m[e] == -INFINITY ? 0.f : exp2_approx(m[e] - ref[e]);
+          m[e] = ref[e];
+          l[e] *= f;
+#pragma unroll
+          for (int d = 0; d < ND; ++d) {
+            o[d][2 * e] *= f;
+            o[d][2 * e + 1] *= f;
+          }
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) ref[e] = m[e] == -INFINITY ? 0.f : m[e];
+#pragma unroll
+      for (int i = 0; i < NS; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          x[i][e] = exp2_approx(x[i][e] - ref[e >> 1]);
+          l[e >> 1] += x[i][e];
+        }
+      // ---- output: probabilities (the cache's type, or three bf16 terms) x
+      // values. In a tail unit values past the end are cut off, and values of
+      // the pass that are no finite numbers are taken out of the product (a
+      // probability 0 times NaN is NaN) and added for the rows that see them.
+      bool odd = false;
+      const bool clean = tail && r.rows > 1;
+#pragma unroll
+      for (int i = 0; i < NS / 2; ++i) {
+        uint32_t p[NQ][4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int ti = 2 * i + (e >> 1), ei = 2 * (e & 1);
+          float y0 = x[ti][ei], y1 = x[ti][ei + 1];
+#pragma unroll
+          for (int k = 0; k < NQ; ++k) {
+            p[k][e] = Num<TC>::pack(y0, y1);
+            if (NQ > 1) {
+              y0 -= Num<TC>::lo(p[k][e]);
+              y1 -= Num<TC>::hi(p[k][e]);
+            }
+          }
+        }
+        const int slot = v_slot + 16 * i;
+        const int s0 = base + 16 * i + 2 * c4;       // slots of this lane's value pairs: s0, s0 + 1 and s0 + 8, s0 + 9
+        uint32_t keep[2] = {0xffffffffu, 0xffffffffu};
+        if (tail) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            keep[e] = (s0 + 8 * e < r.len ? 0xffffu : 0u) | (s0 + 8 * e + 1 < r.len ? 0xffff0000u : 0u);
+        }
+#pragma unroll
+        for (int d = 0; d < ND / 2; ++d) {
+          const int piece = 2 * d + v_piece;
+          uint32_t vb[4];
+          ldsm_x4_trans(vb, vs + (piece >> 3) * S::kBox + slot * 128 + (((piece & 7) ^ (slot & 7)) << 4));
+          if (tail) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              vb[e] &= keep[e & 1];
+              if (clean) {
+                constexpr uint32_t X = Num<TC>::kExp;
+                const int sl = s0 + 8 * (e & 1);
+                if ((vb[e] & X) == X && sl >= r.p0) vb[e] &= 0xffff0000u, odd = true;
+                if ((vb[e] >> 16 & X) == X && sl + 1 >= r.p0) vb[e] &= 0xffffu, odd = true;
+              }
+            }
+          }
+#pragma unroll
+          for (int k = NQ - 1; k >= 0; --k) {
+            Num<TC>::mma(o[2 * d], p[k], vb[0], vb[1]);
+            Num<TC>::mma(o[2 * d + 1], p[k], vb[2], vb[3]);
+          }
+        }
+      }
+      if (clean && __any_sync(0xffffffffu, odd)) {
+#pragma unroll
+        for (int i = 0; i < NS; ++i)
+#pragma unroll 1
+          for (int c = 0; c < 8; ++c) {
+            const int slot = base + 8 * i + c, src = (lane & ~3) + (c >> 1);
+            const float pa = __shfl_sync(0xffffffffu, c & 1 ? x[i][1] : x[i][0], src);
+            const float pb = __shfl_sync(0xffffffffu, c & 1 ? x[i][3] : x[i][2], src);
+            if (slot < r.p0 || slot >= r.len) continue;
+            const bool sa = sees(0, slot), sb = sees(1, slot);
+            const int sl = slot & (kTile - 1);
+#pragma unroll
+            for (int d = 0; d < ND; ++d) {
+              uint32_t v;
+              asm volatile("ld.shared.b32 %0, [%1];"
+                           : "=r"(v)
+                           : "r"(vs + (d >> 3) * S::kBox + sl * 128 + (((d & 7) ^ (sl & 7)) << 4) + 4 * c4));
+              constexpr uint32_t X = Num<TC>::kExp;
+              if ((v & X) == X) {
+                if (sa) o[d][0] = fmaf(pa, Num<TC>::lo(v), o[d][0]);
+                if (sb) o[d][2] = fmaf(pb, Num<TC>::lo(v), o[d][2]);
+              }
+              if ((v >> 16 & X) == X) {
+                if (sa) o[d][1] = fmaf(pa, Num<TC>::hi(v), o[d][1]);
+                if (sb) o[d][3] = fmaf(pb, Num<TC>::hi(v), o[d][3]);
+              }
+            }
+          }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[s]);
+    }
+
+    // ---- the end of the piece
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
+      l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
+      if (!ok) l[e] = __int_as_float(0x7fc00000);   // an expired wait: NaN
+    }
+    const bool begins = w.t0 == 0, whole = begins && w.t1 == r.nt;
+    if (begins && tid == 0) {
+      const long first = w.u - (w.t1 - w.t0);
+      const int c1 = cta_of_unit(first + r.nt - 1, st.T, G);
+      const int4 d = make_int4(blockIdx.x, c1 - (int)blockIdx.x + 1, w.b, w.item);
+      if (a.by_item) a.desc[((long)w.b * a.nkv + w.kvh) * a.ntq_max + w.qt] = d;
+      else if (!whole) a.desc[blockIdx.x] = d;
+    }
+    const long slot = 2l * blockIdx.x + (begins ? 1 : 0);
+    float* part = a.part + slot * a.mt_max * HD;
+    float2* part_ml = a.part_ml + slot * a.mt_max;
+    const float kLn2 = 0.693147180559945f;
+    if constexpr (WK == 1) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        if (qi[e] >= Mq) continue;
+        if (whole) {
+          const int hh = w.kvh * a.group + qi[e] - j[e] * a.group;
+          const float inv = l[e] == 0.f ? 0.f : 1.f / l[e];
+          TQ* dst = static_cast<TQ*>(a.out) + (r.s0 + j[e]) * a.o_row + hh * a.o_head + 2 * c4;
+#pragma unroll
+          for (int d = 0; d < ND; ++d) store2<TQ>(dst + 8 * d, o[d][2 * e] * inv, o[d][2 * e + 1] * inv);
+          if (a.lse && c4 == 0)
+            a.lse[(long)(r.s0 + j[e]) * a.nq + hh] = l[e] == 0.f ? -INFINITY : m[e] * kLn2 + logf(l[e]);
+        } else {
+          const int x = 16 * wm + g + 8 * e;
+#pragma unroll
+          for (int d = 0; d < ND; ++d)
+            *reinterpret_cast<float2*>(part + x * HD + 8 * d + 2 * c4) = make_float2(o[d][2 * e], o[d][2 * e + 1]);
+          if (c4 == 0) part_ml[x] = make_float2(m[e], l[e]);
+        }
+      }
+    } else {
+      // Joined over the warps that shared out the slots.
+      float* so = reinterpret_cast<float*>(extra);                 // [WK][MT][OP]
+      float2* sml = reinterpret_cast<float2*>(so + WK * MT * S::OP);   // [WK][MT]
+      if (F32) cta_sync();   // the queries' terms have been read
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int x = wk * MT + 16 * wm + g + 8 * e;
+#pragma unroll
+        for (int d = 0; d < ND; ++d)
+          *reinterpret_cast<float2*>(so + x * S::OP + 8 * d + 2 * c4) = make_float2(o[d][2 * e], o[d][2 * e + 1]);
+        if (c4 == 0) sml[x] = make_float2(m[e], l[e]);
+      }
+      cta_sync();
+      for (int e = tid; e < MT * (HD / 4); e += S::kWarps * 32) {
+        const int x = e / (HD / 4), d = 4 * (e - x * (HD / 4));
+        const int q = w.qt * MT + x;
+        if (q >= Mq) break;
+        float mm = -INFINITY, ll = 0.f, f[WK];
+        float2 ml[WK];
+#pragma unroll
+        for (int k = 0; k < WK; ++k) {
+          ml[k] = sml[k * MT + x];
+          mm = fmaxf(mm, ml[k].x);
+        }
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < WK; ++k) {
+          f[k] = ml[k].x == -INFINITY ? 0.f : exp2_approx(ml[k].x - mm);
+          // (a warp that saw nothing has l = 0; one whose wait expired, NaN)
+          ll += ml[k].x == -INFINITY ? ml[k].y : ml[k].y * f[k];
+          const float4 y = *reinterpret_cast<const float4*>(so + (k * MT + x) * S::OP + d);
+          v.x = fmaf(y.x, f[k], v.x);
+          v.y = fmaf(y.y, f[k], v.y);
+          v.z = fmaf(y.z, f[k], v.z);
+          v.w = fmaf(y.w, f[k], v.w);
+        }
+        if (whole) {
+          const int jj = q / a.group, hh = w.kvh * a.group + q - jj * a.group;
+          const float inv = ll == 0.f ? 0.f : 1.f / ll;
+          TQ* dst = static_cast<TQ*>(a.out) + (r.s0 + jj) * a.o_row + hh * a.o_head + d;
+          store2<TQ>(dst, v.x * inv, v.y * inv);
+          store2<TQ>(dst + 2, v.z * inv, v.w * inv);
+          if (a.lse && d == 0) a.lse[(long)(r.s0 + jj) * a.nq + hh] = ll == 0.f ? -INFINITY : mm * kLn2 + logf(ll);
+        } else {
+          *reinterpret_cast<float4*>(part + x * HD + d) = v;
+          if (d == 0) part_ml[x] = make_float2(mm, ll);
+        }
+      }
+      cta_sync();   // the region is free again
+    }
+  }
+  // No item begins here that others share (descriptors by CTA).
+  if (!a.by_item && tid == 0) {
+    const bool shared = u1 < st.T && [&] {
+      // The last unit's item begins in this CTA and goes on in the next one.
+      return w.t0 == 0 && w.t1 < w.r.nt;
+    }();
+    if (!shared) a.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
+  }
+  pdl_launch_next();
+}
+
+// The join: one CTA per (shared item, query). The parts lie with the CTAs
+// first .. first + count - 1; the warps take them in turn and their four
+// sums are added in order.
+constexpr int kJoinThreads = 128;
+
+template <int HD, typename TQ, int MT>
+__global__ void __launch_bounds__(kJoinThreads) k_paged_join(const __grid_constant__ Args a) {
+  constexpr int V = HD / 32;   // dimensions of a lane
+  __shared__ float so[4][HD];
+  __shared__ float2 sml[4];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int x = blockIdx.y;
+  pdl_wait();
+  if (a.by_item) {   // items of requests with fewer rows have no descriptor
+    const int b = blockIdx.x / (a.nkv * a.ntq_max), qt = blockIdx.x % a.ntq_max;
+    const Request r = request<MT>(a, b);
+    if (qt >= r.ntq) return;
+  }
+  const int4 d = a.desc[blockIdx.x];
+  if (d.y < 2) return;
+  const Request r = request<MT>(a, d.z);
+  const int kvh = d.w / r.ntq, q = (d.w - kvh * r.ntq) * MT + x;
+  if (q >= r.rows * a.group) return;
+  auto slot = [&](int k) { return (2l * (d.x + k) + (k == 0 ? 1 : 0)) * a.mt_max + x; };
+  float mm = -INFINITY;
+  for (int k = lane; k < d.y; k += 32) mm = fmaxf(mm, a.part_ml[slot(k)].x);
+  mm = warp_max(mm);
+  float l = 0.f, o[V];
+#pragma unroll
+  for (int e = 0; e < V; ++e) o[e] = 0.f;
+  for (int k0 = warp; k0 < d.y; k0 += 4 * 8) {
+    float v[8][V];
+    float2 ml[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int k = k0 + 4 * i;
+      if (k < d.y) {
+        ml[i] = a.part_ml[slot(k)];
+        const float* p = a.part + slot(k) * HD + V * lane;
+        if constexpr (V == 4) {
+          const float4 f = *reinterpret_cast<const float4*>(p);
+          v[i][0] = f.x, v[i][1] = f.y, v[i][2] = f.z, v[i][3] = f.w;
+        } else {
+          const float2 f = *reinterpret_cast<const float2*>(p);
+          v[i][0] = f.x, v[i][1] = f.y;
+        }
+      } else {
+        ml[i] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+        for (int e = 0; e < V; ++e) v[i][e] = 0.f;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float f = ml[i].x == -INFINITY ? 0.f : exp2_approx(ml[i].x - mm);
+      l += ml[i].x == -INFINITY ? ml[i].y : ml[i].y * f;
+#pragma unroll
+      for (int e = 0; e < V; ++e) o[e] = fmaf(v[i][e], f, o[e]);
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < V; ++e) so[warp][V * lane + e] = o[e];
+  if (lane == 0) sml[warp] = make_float2(mm, l);
+  __syncthreads();
+  if (threadIdx.x * 2 >= HD) return;
+  l = ((sml[0].y + sml[1].y) + sml[2].y) + sml[3].y;
+  const int d0 = 2 * threadIdx.x;
+  const float y0 = ((so[0][d0] + so[1][d0]) + so[2][d0]) + so[3][d0];
+  const float y1 = ((so[0][d0 + 1] + so[1][d0 + 1]) + so[2][d0 + 1]) + so[3][d0 + 1];
+  const int jj = q / a.group, hh = kvh * a.group + q - jj * a.group;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  store2<TQ>(static_cast<TQ*>(a.out) + (r.s0 + jj) * a.o_row + hh * a.o_head + d0, y0 * inv, y1 * inv);
+  if (a.lse && threadIdx.x == 0)
+    a.lse[(long)(r.s0 + jj) * a.nq + hh] = l == 0.f ? -INFINITY : mm * 0.693147180559945f + logf(l);
+}
+
+}  // namespace pa
+}  // namespace sf

@@ -1,0 +1,71 @@
+// Launches of the paged attention kernels for one head dimension (one
+// translation unit each).
+#pragma once
+
+#include <atomic>
+
+#include "paged_attn.cuh"
+
+namespace sf {
+namespace pa {
+
+// Query tile of a launch, from the queries that a KV head can have in one
+// request (max_rows * group): one m16 tile shared by four warps that split
+// the slots, two by two, or four tiles with a warp each.
+inline int tile_of(int queries) { return queries <= 16 ? 16 : queries <= 32 ? 32 : 64; }
+
+template <int HD, typename TC, bool F32, int WM, int WK>
+cudaError_t launch(Args& a, int sms, long max_units, cudaStream_t st) {
+  using S = Shape<HD, WM, WK, F32>;
+  using TQ = typename std::conditional<F32, float, TC>::type;
+  auto* fn = k_paged_attn<HD, TC, F32, WM, WK>;
+  static std::atomic<uint64_t> ready{0};   // devices whose shared-memory limit for this kernel is set
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !(ready.load(std::memory_order_relaxed) >> dev & 1)) {
+    e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(fn, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) ready.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
+  }
+  const long most = (long)sms * S::kCtas;
+  const int grid = (int)(max_units < most ? max_units : most);
+  fn<<<grid, S::kThreads, S::kSmem, st>>>(a);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(a.by_item ? a.B * a.nkv * a.ntq_max : grid, a.mt_max);
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k_paged_join<HD, TQ, S::MT>, a);
+}
+
+template <int HD, typename TC, bool F32>
+cudaError_t launch_tiles(Args& a, int sms, long max_units, cudaStream_t st) {
+  switch (tile_of(a.max_rows * a.group)) {
+    case 16: return launch<HD, TC, F32, 1, 4>(a, sms, max_units, st);
+    case 32: return launch<HD, TC, F32, 2, 2>(a, sms, max_units, st);
+    default: return launch<HD, TC, F32, 4, 1>(a, sms, max_units, st);
+  }
+}
+
+template <int HD>
+cudaError_t launch_types(Args& a, int q_dtype, int sms, long max_units, cudaStream_t st) {
+  switch (q_dtype) {
+    case SF_DT_BF16: return launch_tiles<HD, bf16, false>(a, sms, max_units, st);
+    case SF_DT_F16: return launch_tiles<HD, __half, false>(a, sms, max_units, st);
+    default: return launch_tiles<HD, bf16, true>(a, sms, max_units, st);
+  }
+}
+
+cudaError_t launch_hd64(Args& a, int q_dtype, int sms, long max_units, cudaStream_t st);
+cudaError_t launch_hd128(Args& a, int q_dtype, int sms, long max_units, cudaStream_t st);
+
+}  // namespace pa
+}  // namespace sf
