@@ -1,8 +1,9 @@
 // RoPE and cache append of a pass's token rows (sf_kv_append), the RoPE table.
 //
 // Bound by memory: every projected element is read once and written once. A
-// thread takes eight consecutive elements of the lower half of a head and the
-// eight they are paired with (16-byte accesses on both sides of a 16-bit type).
+// thread takes the same eight elements of the lower half, and the eight they
+// are paired with, of kHeads heads of a row: their rotation is loaded once,
+// and all the heads' loads are in flight together (16-byte accesses).
 #include <cmath>
 
 #include "paged.h"
@@ -11,6 +12,7 @@ namespace sf {
 namespace {
 
 constexpr int kAppendThreads = 256;
+constexpr int kHeads = 2;   // heads of a thread
 
 struct AppendArgs {
   const void *q, *k, *v;
@@ -72,58 +74,58 @@ __device__ __forceinline__ void store8(__half* p, const float (&x)[8]) {
 template <typename TI, typename TC, typename TO>
 __global__ void __launch_bounds__(kAppendThreads) k_append(const __grid_constant__ AppendArgs a) {
   const int half = a.hd >> 1;
-  const int per_head = half >> 3;                           // threads of a head
-  const int per_row = (a.nq + 2 * a.nkv) * per_head;        // threads of a row
-  for (long u = blockIdx.x * (long)kAppendThreads + threadIdx.x; u < (long)a.n * per_row;
-       u += (long)gridDim.x * kAppendThreads) {
-    const int i = (int)(u / per_row), r = (int)(u - (long)i * per_row);
-    int h = r / per_head;
-    const int d = (r - h * per_head) * 8;
-    const int slot = a.slots[i];
-    if (slot < 0 || slot >= a.n_slots) continue;
-    int pos = 0;
-    if (a.rope) {
-      pos = a.positions[i];
-      if (pos < 0 || pos >= a.n_pos) continue;
-    }
-    const long page = slot >> a.shift, off = slot & ((1 << a.shift) - 1);
-    const TI* src;
-    bool turn = a.rope != nullptr;
-    TO* qo = nullptr;
-    TC* co = nullptr;
-    if (h < a.nq) {
-      src = static_cast<const TI*>(a.q) + i * a.q_row + h * a.q_head;
-      qo = static_cast<TO*>(a.q_out) + i * a.o_row + h * a.o_head;
-    } else if ((h -= a.nq) < a.nkv) {
-      src = static_cast<const TI*>(a.k) + i * a.k_row + h * a.k_head;
-      co = static_cast<TC*>(a.kc) + page * a.kc_page + h * a.kc_head + off * a.kc_slot;
-    } else {
-      h -= a.nkv;
-      src = static_cast<const TI*>(a.v) + i * a.v_row + h * a.v_head;
-      co = static_cast<TC*>(a.vc) + page * a.vc_page + h * a.vc_head + off * a.vc_slot;
-      turn = false;
-    }
-    float x[8], y[8];
-    load8(x, src + d);
-    load8(y, src + d + half);
-    if (turn) {
-      const float4* cs = a.rope + ((size_t)pos * half + d) / 2;
+  const int per_head = half >> 3;                           // pieces of a head
+  const int heads = a.nq + 2 * a.nkv;
+  const int groups = (heads + kHeads - 1) / kHeads;
+  const int per_row = groups * per_head;                    // threads of a row
+  const long u = blockIdx.x * (long)kAppendThreads + threadIdx.x;
+  const int i = (int)(u / per_row), r = (int)(u - (long)i * per_row);
+  if (i >= a.n) return;
+  const int h0 = r / per_head * kHeads, d = (r - r / per_head * per_head) * 8;
+  const int slot = a.slots[i];
+  const int pos = a.rope ? a.positions[i] : 0;
+  float x[kHeads][8], y[kHeads][8];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float4 t = cs[e];
-        const float x0 = x[2 * e], y0 = y[2 * e], x1 = x[2 * e + 1], y1 = y[2 * e + 1];
-        x[2 * e] = x0 * t.x - y0 * t.y;
-        y[2 * e] = y0 * t.x + x0 * t.y;
-        x[2 * e + 1] = x1 * t.z - y1 * t.w;
-        y[2 * e + 1] = y1 * t.z + x1 * t.w;
+  for (int e = 0; e < kHeads; ++e) {
+    const int h = h0 + e;
+    if (h >= heads) break;
+    const TI* src = h < a.nq ? static_cast<const TI*>(a.q) + i * a.q_row + h * a.q_head
+                    : h < a.nq + a.nkv ? static_cast<const TI*>(a.k) + i * a.k_row + (h - a.nq) * a.k_head
+                                       : static_cast<const TI*>(a.v) + i * a.v_row + (h - a.nq - a.nkv) * a.v_head;
+    load8(x[e], src + d);
+    load8(y[e], src + d + half);
+  }
+  if (slot < 0 || slot >= a.n_slots || (a.rope && (pos < 0 || pos >= a.n_pos))) return;
+  float4 cs[4];
+  if (a.rope) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) cs[e] = a.rope[((size_t)pos * half + d) / 2 + e];
+  }
+  const long page = slot >> a.shift, off = slot & ((1 << a.shift) - 1);
+#pragma unroll
+  for (int e = 0; e < kHeads; ++e) {
+    const int h = h0 + e;
+    if (h >= heads) break;
+    if (a.rope && h < a.nq + a.nkv) {
+#pragma unroll
+      for (int p = 0; p < 4; ++p) {
+        const float x0 = x[e][2 * p], y0 = y[e][2 * p], x1 = x[e][2 * p + 1], y1 = y[e][2 * p + 1];
+        x[e][2 * p] = x0 * cs[p].x - y0 * cs[p].y;
+        y[e][2 * p] = y0 * cs[p].x + x0 * cs[p].y;
+        x[e][2 * p + 1] = x1 * cs[p].z - y1 * cs[p].w;
+        y[e][2 * p + 1] = y1 * cs[p].z + x1 * cs[p].w;
       }
     }
-    if (co) {
-      store8(co + d, x);
-      store8(co + d + half, y);
+    if (h < a.nq) {
+      TO* dst = static_cast<TO*>(a.q_out) + i * a.o_row + h * a.o_head + d;
+      store8(dst, x[e]);
+      store8(dst + half, y[e]);
     } else {
-      store8(qo + d, x);
-      store8(qo + d + half, y);
+      const bool k = h < a.nq + a.nkv;
+      TC* dst = k ? static_cast<TC*>(a.kc) + page * a.kc_page + (h - a.nq) * a.kc_head + off * a.kc_slot
+                  : static_cast<TC*>(a.vc) + page * a.vc_page + (h - a.nq - a.nkv) * a.vc_head + off * a.vc_slot;
+      store8(dst + d, x[e]);
+      store8(dst + d + half, y[e]);
     }
   }
 }
@@ -229,9 +231,10 @@ extern "C" sf_status sf_kv_append(const sf_paged_cache* cache, int32_t n, const 
   a.shift = log2_of(cache->page);
   a.n_slots = cache->n_pages * cache->page;
   a.n_pos = n_pos;
-  const long units = (long)n * (a.nq + 2 * a.nkv) * (a.hd / 16);
-  const long want = (units + kAppendThreads - 1) / kAppendThreads;
-  const int grid = (int)(want < (1 << 20) ? want : (1 << 20));
+  const long units = (long)n * ((a.nq + 2 * a.nkv + kHeads - 1) / kHeads) * (a.hd / 16);
+  const long grid_l = (units + kAppendThreads - 1) / kAppendThreads;
+  if (grid_l > INT32_MAX) return set_error(SF_ERR_UNSUPPORTED, "sf_kv_append: too many rows for one call");
+  const int grid = (int)grid_l;
   cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
   cudaError_t e;
   if (k->dtype == SF_DT_BF16) e = launch_append<bf16, bf16>(a, true, grid, st);

@@ -14,9 +14,9 @@ constexpr int kMaxDesc = 1024;  // item descriptors
 struct Layout {
   size_t ml, part, total;
 };
-static Layout layout(int n_heads, int n_kv_heads, int head_dim, int max_rows) {
+static Layout layout(int n_heads, int n_kv_heads, int head_dim, int max_rows) {   // (whatever the tile)
   const int queries = max_rows * (n_heads / n_kv_heads);
-  const size_t mt = std::min(queries, tile_of(queries));
+  const size_t mt = std::min(queries, tile_of(queries, false));
   Layout l;
   l.ml = kMaxDesc * sizeof(int4);
   l.part = l.ml + 2 * kMaxCtas * mt * sizeof(float2);
@@ -120,17 +120,25 @@ extern "C" sf_status sf_paged_attention(const sf_paged_cache* cache, const sf_ro
   a.group = q->n_heads / cache->n_kv_heads;
   a.shift = log2_of(cache->page), a.max_rows = max_rows, a.rows_each = n / batch;
   a.scale2 = scale * 1.44269504088896f;
-  const int queries = max_rows * a.group, mt = pa::tile_of(queries);
-  a.mt_max = std::min(queries, mt);
-  a.ntq_max = (queries + mt - 1) / mt;
-  const long items = (long)batch * a.nkv * a.ntq_max;
-  a.by_item = items <= pa::kMaxDesc;
+  // A smaller tile where the larger one's units could not occupy the GPU even
+  // if every request filled its table: the cache is then read once for each
+  // tile (from L2), by CTAs that would be idle.
+  const int queries = max_rows * a.group;
+  const long units = ((long)table_width * cache->page + pa::kTile - 1) / pa::kTile;   // of an item, at most
+  auto items = [&](int mt) { return (long)batch * a.nkv * ((queries + mt - 1) / mt); };
+  a.mt = pa::tile_of(queries, q->dtype == SF_DT_F32);
+  while (a.mt > 16 && items(a.mt) * units < 2 * sms) a.mt /= 2;
+  a.mt_max = std::min(queries, a.mt);
+  a.ntq_max = (queries + a.mt - 1) / a.mt;
+  a.by_item = items(a.mt) <= pa::kMaxDesc;
+  if (a.nkv * (long)a.ntq_max * units > INT32_MAX)
+    return set_error(SF_ERR_UNSUPPORTED, "sf_paged_attention: table_width * page too large for this many heads and rows");
   const pa::Layout lay = pa::layout(q->n_heads, cache->n_kv_heads, cache->head_dim, max_rows);
   unsigned char* ws = static_cast<unsigned char*>(d_workspace);
   a.desc = reinterpret_cast<int4*>(ws);
   a.part_ml = reinterpret_cast<float2*>(ws + lay.ml);
   a.part = reinterpret_cast<float*>(ws + lay.part);
-  const long max_units = items * (((long)table_width * cache->page + pa::kTile - 1) / pa::kTile);
+  const long max_units = items(a.mt) * units;
   sms = std::min(sms, pa::kMaxCtas / 2);
   cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
   e = cache->head_dim == 128 ? pa::launch_hd128(a, q->dtype, sms, max_units, st)

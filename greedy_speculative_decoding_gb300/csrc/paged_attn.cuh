@@ -24,6 +24,8 @@
 // queries share out the queries.
 #pragma once
 
+#include <type_traits>
+
 #include "paged.h"
 
 namespace sf {
@@ -43,7 +45,7 @@ struct Args {
   const unsigned long long* mask;
   int B, N, W, nq, nkv, group, shift, max_rows, rows_each;
   float scale2;            // scale * log2(e)
-  int stages;
+  int mt;                  // queries of a tile (MT)
   int mt_max;              // queries of an item at most (min(MT, max_rows * group))
   int ntq_max;             // items of a (request, KV head) at most
   int by_item;             // descriptors by item (else by the CTA that starts it)
@@ -93,7 +95,10 @@ struct Num<bf16> {
   static __device__ __forceinline__ float lo(uint32_t w) { return __uint_as_float(w << 16); }
   static __device__ __forceinline__ float hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
   static __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    mma_bf16_16816(d, a[0], a[1], a[2], a[3], b0, b1);
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
+        "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
   }
 };
 template <>
@@ -106,8 +111,7 @@ struct Num<__half> {
   static __device__ __forceinline__ float lo(uint32_t w) { return __low2float(*reinterpret_cast<const __half2*>(&w)); }
   static __device__ __forceinline__ float hi(uint32_t w) { return __high2float(*reinterpret_cast<const __half2*>(&w)); }
   static __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
         "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -149,9 +153,10 @@ struct Shape {
   static constexpr int kHalf = HD / 64;              // 64-dimension boxes of a key
   static constexpr int kBox = kTile * 128;           // bytes of one box column: 64 slots x 64 dimensions
   static constexpr int kStage = 2 * kHalf * kBox;    // keys and values of a unit
-  static constexpr int QP = HD + 8;                  // pitch of the fp32 queries' bf16 terms
+  static constexpr bool kQSmem = F32 || WK == 1;     // queries in shared memory (else in registers)
+  static constexpr int QP = HD + 8;                  // pitch of the queries there
   static constexpr int OP = HD + 8;                  // pitch of the parts joined over wk
-  static constexpr int kQBytes = F32 ? 3 * MT * QP * 2 : 0;
+  static constexpr int kQBytes = kQSmem ? (F32 ? 3 : 1) * MT * QP * 2 : 0;
   static constexpr int kOBytes = WK > 1 ? WK * MT * (OP + 2) * 4 : 0;
   static constexpr int kExtra = kQBytes > kOBytes ? kQBytes : kOBytes;   // one region: never both at once
   static constexpr int kMaxStages = 4;
@@ -218,28 +223,30 @@ __device__ __forceinline__ Start locate(const Args& a, long G, long* sh) {
 // Walks the pieces of items that a CTA's units [u, u1) make up.
 template <int MT>
 struct Walk {
-  long u, u1, rem;
+  long u;          // units before the next piece
+  int left, rem;   // units of the CTA from there on; units of request b before it
   int b;
   Request r;
   int item, kvh, qt, t0, t1;   // the current piece: item within the request, units t0 .. t1 - 1
   __device__ __forceinline__ Walk(const Args& a, const Start& s, long first, long last)
-      : u(first), u1(last), rem(first - s.base), b(s.b) {
+      : u(first), left((int)(last - first)), rem((int)(first - s.base)), b(s.b) {
     r = request<MT>(a, b);
   }
   // The next piece; false at the end.
   __device__ __forceinline__ bool next(const Args& a) {
-    if (u >= u1) return false;
-    while (rem >= (long)a.nkv * r.ntq * r.nt) {
+    if (left <= 0) return false;
+    while (rem >= a.nkv * r.ntq * r.nt) {
       rem = 0;
       r = request<MT>(a, ++b);
     }
-    item = (int)(rem / r.nt);
-    t0 = (int)(rem - (long)item * r.nt);
-    t1 = (int)min((long)r.nt, t0 + (u1 - u));
+    item = rem / r.nt;
+    t0 = rem - item * r.nt;
+    t1 = min(r.nt, t0 + left);
     kvh = item / r.ntq;
     qt = item - kvh * r.ntq;
     u += t1 - t0;
     rem += t1 - t0;
+    left -= t1 - t0;
     return true;
   }
 };
@@ -332,64 +339,68 @@ __global__ void __launch_bounds__(Shape<HD, WM, WK, F32>::kThreads, Shape<HD, WM
   const int wm = warp / WK, wk = warp % WK;
   const int g = lane >> 2, c4 = lane & 3;
   auto cta_sync = [] { asm volatile("bar.sync 1, %0;" ::"n"(S::kWarps * 32) : "memory"); };
-  // Shared-memory offsets of this lane's ldmatrix rows (keys: 16 slots x 16
-  // dimensions; values: 16 slots x 16 dimensions, transposed).
-  const int k_slot = wk * SW + (lane & 7) + 8 * (lane >> 4), k_piece = (lane >> 3) & 1;
-  const int v_slot = wk * SW + (lane & 7) + 8 * ((lane >> 3) & 1), v_piece = lane >> 4;
+  // This lane's ldmatrix rows (keys: 16 slots x 16 dimensions; values: 16
+  // slots x 16 dimensions, transposed): 16-byte piece p of slot s lies at
+  // (128 s + 16 (s % 8)) ^ 16 p of its box column.
+  const int k_slot = wk * SW + (lane & 7) + 8 * (lane >> 4), v_slot = wk * SW + (lane & 7) + 8 * ((lane >> 3) & 1);
+  const uint32_t k_off = (k_slot * 128 + ((k_slot & 7) << 4)) ^ (((lane >> 3) & 1) << 4);
+  const uint32_t v_off = (v_slot * 128 + ((v_slot & 7) << 4)) ^ ((lane >> 4) << 4);
   int n = 0;
   bool ok = true;
   while (w.next(a)) {
     const Request r = w.r;
-    const int q0 = w.qt * MT + 16 * wm;            // this warp's first query
+    const int q0 = w.qt * MT + 16 * wm + g;        // this lane's queries: q0 and q0 + 8
     const int Mq = r.rows * a.group;
-    int qi[2], j[2];                               // this lane's queries (rows g and g + 8 of the tile)
-    const TQ* qp[2];
-    unsigned long long bits[2] = {0, 0};
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      qi[e] = q0 + g + 8 * e;
-      j[e] = qi[e] / a.group;
-      const int hh = w.kvh * a.group + qi[e] - j[e] * a.group;
-      qp[e] = qi[e] < Mq ? static_cast<const TQ*>(a.q) + (r.s0 + j[e]) * a.q_row + hh * a.q_head : nullptr;
-      if (a.mask && qi[e] < Mq) bits[e] = a.mask[r.s0 + j[e]];
-    }
-    uint32_t qf[F32 ? 1 : KS][4];
-    if constexpr (F32) {
-      // The tile's queries as three bf16 terms in shared memory.
-      bf16* sq = reinterpret_cast<bf16*>(extra);
+    uint32_t qf[S::kQSmem ? 1 : KS][4];
+    if constexpr (S::kQSmem) {
+      // The tile's queries in shared memory (fp32 ones as three bf16 terms).
+      TC* sq = reinterpret_cast<TC*>(extra);
       cta_sync();   // the region's last readers are done
       for (int e = tid; e < MT * (HD / 4); e += S::kWarps * 32) {
         const int m = e / (HD / 4), d = 4 * (e - m * (HD / 4));
         const int x = w.qt * MT + m, jj = x / a.group, hh = w.kvh * a.group + x - jj * a.group;
-        float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (x < Mq)
-          f = *reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + (r.s0 + jj) * a.q_row + hh * a.q_head + d);
-        float v[4] = {f.x, f.y, f.z, f.w};
+        const TQ* src = static_cast<const TQ*>(a.q) + (r.s0 + jj) * a.q_row + hh * a.q_head + d;
+        if constexpr (F32) {
+          float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (x < Mq) f = *reinterpret_cast<const float4*>(src);
+          float v[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
-        for (int k = 0; k < 3; ++k) {
-          uint32_t p[2];
+          for (int k = 0; k < 3; ++k) {
+            uint32_t p[2];
 #pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            p[y] = Num<bf16>::pack(v[2 * y], v[2 * y + 1]);
-            v[2 * y] -= Num<bf16>::lo(p[y]);
-            v[2 * y + 1] -= Num<bf16>::hi(p[y]);
+            for (int y = 0; y < 2; ++y) {
+              p[y] = Num<bf16>::pack(v[2 * y], v[2 * y + 1]);
+              v[2 * y] -= Num<bf16>::lo(p[y]);
+              v[2 * y + 1] -= Num<bf16>::hi(p[y]);
+            }
+            *reinterpret_cast<uint2*>(sq + (k * MT + m) * S::QP + d) = make_uint2(p[0], p[1]);
           }
-          *reinterpret_cast<uint2*>(sq + (k * MT + m) * S::QP + d) = make_uint2(p[0], p[1]);
+        } else {
+          *reinterpret_cast<uint2*>(sq + m * S::QP + d) =
+              x < Mq ? *reinterpret_cast<const uint2*>(src) : make_uint2(0u, 0u);
         }
       }
       cta_sync();
     } else {
 #pragma unroll
-      for (int k = 0; k < KS; ++k)
+      for (int e = 0; e < 2; ++e) {
+        const int x = q0 + 8 * e, jj = x / a.group, hh = w.kvh * a.group + x - jj * a.group;
+        const TQ* src = static_cast<const TQ*>(a.q) + (r.s0 + jj) * a.q_row + hh * a.q_head + 2 * c4;
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          qf[k][e] = qp[e & 1] ? *reinterpret_cast<const uint32_t*>(qp[e & 1] + 16 * k + 2 * c4 + 8 * (e >> 1)) : 0u;
+        for (int k = 0; k < KS; ++k) {
+          qf[k][e] = x < Mq ? *reinterpret_cast<const uint32_t*>(src + 16 * k) : 0u;
+          qf[k][e + 2] = x < Mq ? *reinterpret_cast<const uint32_t*>(src + 16 * k + 8) : 0u;
+        }
+      }
     }
     float o[ND][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 #pragma unroll
     for (int d = 0; d < ND; ++d) o[d][0] = o[d][1] = o[d][2] = o[d][3] = 0.f;
 
-    for (int t = w.t0; t < w.t1; ++t, ++n) {
+    // One unit. Every row sees all slots of a plain one; a tail unit holds
+    // slots of the pass itself, or slots past the end.
+    auto unit = [&](auto tail_type, int t) {
+      constexpr bool TAIL = decltype(tail_type)::value;
       const int s = n % S::kStages;
       if (ok && !mbar_wait(&full[s], (n / S::kStages) & 1, kWaitIters)) ok = false;
       ok = __all_sync(0xffffffffu, ok);
@@ -402,10 +413,10 @@ __global__ void __launch_bounds__(Shape<HD, WM, WK, F32>::kThreads, Shape<HD, WM
 #pragma unroll
       for (int k = 0; k < KS; ++k) {
         uint32_t qk[NQ][4];
-        if constexpr (F32) {
-          const bf16* sq = reinterpret_cast<const bf16*>(extra);
+        if constexpr (S::kQSmem) {
+          const TC* sq = reinterpret_cast<const TC*>(extra);
 #pragma unroll
-          for (int e = 0; e < 3; ++e)
+          for (int e = 0; e < NQ; ++e)
             ldsm_x4(qk[e], smem_u32(sq + (e * MT + 16 * wm + (lane & 7) + 8 * ((lane >> 3) & 1)) * S::QP + 16 * k +
                                     8 * (lane >> 4)));
         } else {
@@ -414,9 +425,8 @@ __global__ void __launch_bounds__(Shape<HD, WM, WK, F32>::kThreads, Shape<HD, WM
         }
 #pragma unroll
         for (int i = 0; i < NS / 2; ++i) {
-          const int slot = k_slot + 16 * i, piece = 2 * k + k_piece;
           uint32_t kb[4];
-          ldsm_x4(kb, ks + (piece >> 3) * S::kBox + slot * 128 + (((piece & 7) ^ (slot & 7)) << 4));
+          ldsm_x4(kb, ((ks + k_off) ^ ((2 * k & 7) << 4)) + (k >> 2) * S::kBox + i * 2048);
 #pragma unroll
           for (int e = NQ - 1; e >= 0; --e) {       // the small terms first
             Num<TC>::mma(x[2 * i], qk[e], kb[0], kb[1]);
@@ -424,20 +434,30 @@ __global__ void __launch_bounds__(Shape<HD, WM, WK, F32>::kThreads, Shape<HD, WM
           }
         }
       }
-      // ---- what a row does not see is -infinity (never added to: what such
-      // slots hold, NaN included, does not matter)
-      const bool tail = t * kTile + kTile > r.p0 || t * kTile + kTile > r.len;   // holds slots of the pass, or past the end
-      auto sees = [&](int e, int slot) {
-        const int i = slot - r.p0;
-        return qi[e] < Mq && slot < r.len && (i < 0 || (a.mask ? i < 64 && ((bits[e] >> i) & 1) : i <= j[e]));
-      };
 #pragma unroll
       for (int i = 0; i < NS; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          x[i][e] *= a.scale2;
-          if (tail && !sees(e >> 1, base + 8 * i + 2 * c4 + (e & 1))) x[i][e] = -INFINITY;
+        for (int e = 0; e < 4; ++e) x[i][e] *= a.scale2;
+      // ---- what a row does not see is -infinity (set, not added: what such
+      // slots hold, NaN included, does not matter)
+      int j[2] = {0, 0};
+      unsigned long long bits[2] = {0, 0};
+      auto sees = [&](int e, int slot) {
+        const int i = slot - r.p0;
+        return q0 + 8 * e < Mq && slot < r.len && (i < 0 || (a.mask ? i < 64 && ((bits[e] >> i) & 1) : i <= j[e]));
+      };
+      if constexpr (TAIL) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          j[e] = (q0 + 8 * e) / a.group;
+          if (a.mask && q0 + 8 * e < Mq) bits[e] = a.mask[r.s0 + j[e]];
         }
+#pragma unroll
+        for (int i = 0; i < NS; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (!sees(e >> 1, base + 8 * i + 2 * c4 + (e & 1))) x[i][e] = -INFINITY;
+      }
       // ---- running maximum and sum
       float ref[2];
       bool raise = false;
@@ -478,7 +498,7 @@ __global__ void __launch_bounds__(Shape<HD, WM, WK, F32>::kThreads, Shape<HD, WM
       // the pass that are no finite numbers are taken out of the product (a
       // probability 0 times NaN is NaN) and added for the rows that see them.
       bool odd = false;
-      const bool clean = tail && r.rows > 1;
+      const bool clean = TAIL && (r.len - r.p0 > 1 || a.mask);
 #pragma unroll
       for (int i = 0; i < NS / 2; ++i) {
         uint32_t p[NQ][4];
@@ -495,20 +515,18 @@ __global__ void __launch_bounds__(Shape<HD, WM, WK, F32>::kThreads, Shape<HD, WM
             }
           }
         }
-        const int slot = v_slot + 16 * i;
         const int s0 = base + 16 * i + 2 * c4;       // slots of this lane's value pairs: s0, s0 + 1 and s0 + 8, s0 + 9
         uint32_t keep[2] = {0xffffffffu, 0xffffffffu};
-        if (tail) {
+        if constexpr (TAIL) {
 #pragma unroll
           for (int e = 0; e < 2; ++e)
             keep[e] = (s0 + 8 * e < r.len ? 0xffffu : 0u) | (s0 + 8 * e + 1 < r.len ? 0xffff0000u : 0u);
         }
 #pragma unroll
         for (int d = 0; d < ND / 2; ++d) {
-          const int piece = 2 * d + v_piece;
           uint32_t vb[4];
-          ldsm_x4_trans(vb, vs + (piece >> 3) * S::kBox + slot * 128 + (((piece & 7) ^ (slot & 7)) << 4));
-          if (tail) {
+          ldsm_x4_trans(vb, ((vs + v_off) ^ ((2 * d & 7) << 4)) + (d >> 2) * S::kBox + i * 2048);
+          if constexpr (TAIL) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               vb[e] &= keep[e & 1];
@@ -527,38 +545,45 @@ __global__ void __launch_bounds__(Shape<HD, WM, WK, F32>::kThreads, Shape<HD, WM
           }
         }
       }
-      if (clean && __any_sync(0xffffffffu, odd)) {
+      if constexpr (TAIL) {
+        if (clean && __any_sync(0xffffffffu, odd)) {
 #pragma unroll
-        for (int i = 0; i < NS; ++i)
+          for (int i = 0; i < NS; ++i)
 #pragma unroll 1
-          for (int c = 0; c < 8; ++c) {
-            const int slot = base + 8 * i + c, src = (lane & ~3) + (c >> 1);
-            const float pa = __shfl_sync(0xffffffffu, c & 1 ? x[i][1] : x[i][0], src);
-            const float pb = __shfl_sync(0xffffffffu, c & 1 ? x[i][3] : x[i][2], src);
-            if (slot < r.p0 || slot >= r.len) continue;
-            const bool sa = sees(0, slot), sb = sees(1, slot);
-            const int sl = slot & (kTile - 1);
+            for (int c = 0; c < 8; ++c) {
+              const int slot = base + 8 * i + c, src = (lane & ~3) + (c >> 1);
+              const float pa = __shfl_sync(0xffffffffu, c & 1 ? x[i][1] : x[i][0], src);
+              const float pb = __shfl_sync(0xffffffffu, c & 1 ? x[i][3] : x[i][2], src);
+              if (slot < r.p0 || slot >= r.len) continue;
+              const bool sa = sees(0, slot), sb = sees(1, slot);
+              const int sl = slot & (kTile - 1);
 #pragma unroll
-            for (int d = 0; d < ND; ++d) {
-              uint32_t v;
-              asm volatile("ld.shared.b32 %0, [%1];"
-                           : "=r"(v)
-                           : "r"(vs + (d >> 3) * S::kBox + sl * 128 + (((d & 7) ^ (sl & 7)) << 4) + 4 * c4));
-              constexpr uint32_t X = Num<TC>::kExp;
-              if ((v & X) == X) {
-                if (sa) o[d][0] = fmaf(pa, Num<TC>::lo(v), o[d][0]);
-                if (sb) o[d][2] = fmaf(pb, Num<TC>::lo(v), o[d][2]);
-              }
-              if ((v >> 16 & X) == X) {
-                if (sa) o[d][1] = fmaf(pa, Num<TC>::hi(v), o[d][1]);
-                if (sb) o[d][3] = fmaf(pb, Num<TC>::hi(v), o[d][3]);
+              for (int d = 0; d < ND; ++d) {
+                uint32_t v;
+                asm volatile("ld.shared.b32 %0, [%1];"
+                             : "=r"(v)
+                             : "r"(vs + (d >> 3) * S::kBox + sl * 128 + (((d & 7) ^ (sl & 7)) << 4) + 4 * c4));
+                constexpr uint32_t X = Num<TC>::kExp;
+                if ((v & X) == X) {
+                  if (sa) o[d][0] = fmaf(pa, Num<TC>::lo(v), o[d][0]);
+                  if (sb) o[d][2] = fmaf(pb, Num<TC>::lo(v), o[d][2]);
+                }
+                if ((v >> 16 & X) == X) {
+                  if (sa) o[d][1] = fmaf(pa, Num<TC>::hi(v), o[d][1]);
+                  if (sb) o[d][3] = fmaf(pb, Num<TC>::hi(v), o[d][3]);
+                }
               }
             }
-          }
+        }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[s]);
-    }
+      ++n;
+    };
+    const int plain = max(0, min(r.p0, r.len)) / kTile;   // units whose slots every row sees
+    int t = w.t0;
+    for (; t < min(w.t1, plain); ++t) unit(std::false_type{}, t);
+    for (; t < w.t1; ++t) unit(std::true_type{}, t);
 
     // ---- the end of the piece
 #pragma unroll
@@ -570,7 +595,7 @@ __global__ void __launch_bounds__(Shape<HD, WM, WK, F32>::kThreads, Shape<HD, WM
     const bool begins = w.t0 == 0, whole = begins && w.t1 == r.nt;
     if (begins && tid == 0) {
       const long first = w.u - (w.t1 - w.t0);
-      const int c1 = cta_of_unit(first + r.nt - 1, st.T, G);
+      const int c1 = whole ? (int)blockIdx.x : cta_of_unit(first + r.nt - 1, st.T, G);
       const int4 d = make_int4(blockIdx.x, c1 - (int)blockIdx.x + 1, w.b, w.item);
       if (a.by_item) a.desc[((long)w.b * a.nkv + w.kvh) * a.ntq_max + w.qt] = d;
       else if (!whole) a.desc[blockIdx.x] = d;
@@ -582,15 +607,16 @@ __global__ void __launch_bounds__(Shape<HD, WM, WK, F32>::kThreads, Shape<HD, WM
     if constexpr (WK == 1) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        if (qi[e] >= Mq) continue;
+        const int q = q0 + 8 * e;
+        if (q >= Mq) continue;
         if (whole) {
-          const int hh = w.kvh * a.group + qi[e] - j[e] * a.group;
+          const int jj = q / a.group, hh = w.kvh * a.group + q - jj * a.group;
           const float inv = l[e] == 0.f ? 0.f : 1.f / l[e];
-          TQ* dst = static_cast<TQ*>(a.out) + (r.s0 + j[e]) * a.o_row + hh * a.o_head + 2 * c4;
+          TQ* dst = static_cast<TQ*>(a.out) + (r.s0 + jj) * a.o_row + hh * a.o_head + 2 * c4;
 #pragma unroll
           for (int d = 0; d < ND; ++d) store2<TQ>(dst + 8 * d, o[d][2 * e] * inv, o[d][2 * e + 1] * inv);
           if (a.lse && c4 == 0)
-            a.lse[(long)(r.s0 + j[e]) * a.nq + hh] = l[e] == 0.f ? -INFINITY : m[e] * kLn2 + logf(l[e]);
+            a.lse[(long)(r.s0 + jj) * a.nq + hh] = l[e] == 0.f ? -INFINITY : m[e] * kLn2 + logf(l[e]);
         } else {
           const int x = 16 * wm + g + 8 * e;
 #pragma unroll

@@ -11,8 +11,9 @@ namespace pa {
 
 // Query tile of a launch, from the queries that a KV head can have in one
 // request (max_rows * group): one m16 tile shared by four warps that split
-// the slots, two by two, or four tiles with a warp each.
-inline int tile_of(int queries) { return queries <= 16 ? 16 : queries <= 32 ? 32 : 64; }
+// the slots, two by two, or four tiles with a warp each. fp32 queries take at
+// most 32 a tile: their three terms of 64 would leave room for one CTA an SM.
+inline int tile_of(int queries, bool f32) { return queries <= 16 ? 16 : queries <= 32 || f32 ? 32 : 64; }
 
 template <int HD, typename TC, bool F32, int WM, int WK>
 cudaError_t launch(Args& a, int sms, long max_units, cudaStream_t st) {
@@ -48,11 +49,9 @@ cudaError_t launch(Args& a, int sms, long max_units, cudaStream_t st) {
 
 template <int HD, typename TC, bool F32>
 cudaError_t launch_tiles(Args& a, int sms, long max_units, cudaStream_t st) {
-  switch (tile_of(a.max_rows * a.group)) {
-    case 16: return launch<HD, TC, F32, 1, 4>(a, sms, max_units, st);
-    case 32: return launch<HD, TC, F32, 2, 2>(a, sms, max_units, st);
-    default: return launch<HD, TC, F32, 4, 1>(a, sms, max_units, st);
-  }
+  if (a.mt == 16) return launch<HD, TC, F32, 1, 4>(a, sms, max_units, st);
+  if (F32 || a.mt == 32) return launch<HD, TC, F32, 2, 2>(a, sms, max_units, st);
+  return launch<HD, TC, F32, F32 ? 2 : 4, F32 ? 2 : 1>(a, sms, max_units, st);
 }
 
 template <int HD>
