@@ -13,9 +13,9 @@ Every call takes tensors of the current CUDA device and enqueues its work on
 belong to that stream.
 """
 
-import contextlib
 import ctypes
 import math
+import struct
 from typing import NamedTuple
 
 import torch
@@ -23,6 +23,9 @@ import torch
 from . import _lib as L
 
 _DT = {torch.float32: L.SF_DT_F32, torch.bfloat16: L.SF_DT_BF16, torch.float16: L.SF_DT_F16}
+# sf_paged_cache and sf_rows as bytes (their fields as in L.PagedCache and L.Rows).
+_CACHE, _ROWS = struct.Struct("=QQiiiiiiqqqqqq"), struct.Struct("=Qiiqq")
+assert _CACHE.size == ctypes.sizeof(L.PagedCache) and _ROWS.size == ctypes.sizeof(L.Rows)
 
 
 class PagePlan(NamedTuple):
@@ -36,44 +39,51 @@ class PagePlan(NamedTuple):
     status: torch.Tensor
 
 
-def _stream(stream):
-    """(stream handle, context to allocate in): tensors made for a call on
-    another stream than the current one must belong to it."""
-    cur = torch.cuda.current_stream()
-    if stream is None or stream.cuda_stream == cur.cuda_stream:
-        return ctypes.c_void_p(cur.cuda_stream), contextlib.nullcontext()
-    return ctypes.c_void_p(stream.cuda_stream), torch.cuda.stream(stream)
+def _device(stream):
+    """(current device, stream handle)."""
+    dev = torch.cuda.current_device()
+    return dev, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
-def _on_gpu(dev, **tensors):
-    """Refuse tensors that are not on the current CUDA device."""
-    for name, t in tensors.items():
-        if t is not None and (not t.is_cuda or t.device.index != dev):
-            raise ValueError(f"{name}: expected a tensor on cuda:{dev}, got {t.device}")
+def _empty(shape, dtype, dev, stream):
+    """A tensor that belongs to the stream the call runs on."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
 
 
-def _ints(name, t, shape, dtype=torch.int32):
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous {dtype} tensor {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+def _ptr(name, t, shape, dtype, dev):
+    """The address of a contiguous tensor, checked."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous {dtype} tensor {tuple(shape)} on cuda:{dev}, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
     return t.data_ptr()
 
 
-def _rows(name, t, n, hd):
-    if t.dtype not in _DT or t.dim() != 3 or t.shape[0] != n or t.shape[2] != hd or t.stride(2) != 1:
-        raise ValueError(f"{name}: expected rows [{n}, heads, {hd}] (fp32, bf16 or fp16, last dimension contiguous), "
-                         f"got {t.dtype} {tuple(t.shape)}")
-    return L.Rows(t.data_ptr(), _DT[t.dtype], t.shape[1], t.stride(0), t.stride(1))
+def _rows(name, t, n, hd, dev):
+    dt = _DT.get(t.dtype)
+    if dt is None or t.dim() != 3 or t.get_device() != dev:
+        raise ValueError(f"{name}: expected rows [{n}, heads, {hd}] (fp32, bf16 or fp16) on cuda:{dev}, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
+    (rows, heads, d), (s0, s1, s2) = t.shape, t.stride()
+    if rows != n or d != hd or s2 != 1:
+        raise ValueError(f"{name}: expected rows [{n}, heads, {hd}] with the last dimension contiguous, got "
+                         f"{tuple(t.shape)} with strides {t.stride()}")
+    return _ROWS.pack(t.data_ptr(), dt, heads, s0, s1)
 
 
-def _cache(k, v):
-    if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or k.dtype not in _DT:
+def _cache(k, v, dev):
+    """(sf_paged_cache, kv_heads, head_dim)."""
+    if k.dim() != 4 or k.shape != v.shape or k.dtype is not v.dtype or k.dtype not in _DT:
         raise ValueError(f"caches: expected k and v [pages, kv_heads, page, head_dim] of one type, got "
                          f"{k.dtype} {tuple(k.shape)} and {v.dtype} {tuple(v.shape)}")
-    ks, vs = k.stride(), v.stride()
-    if ks[3] != 1 or vs[3] != 1:
+    if k.get_device() != dev or v.get_device() != dev:
+        raise ValueError(f"caches: expected tensors on cuda:{dev}, got {k.device} and {v.device}")
+    (k0, k1, k2, k3), (v0, v1, v2, v3), (p, h, s, d) = k.stride(), v.stride(), k.shape
+    if k3 != 1 or v3 != 1:
         raise ValueError("caches: the last dimension must be contiguous")
-    p, h, s, d = k.shape
-    return L.PagedCache(k.data_ptr(), v.data_ptr(), _DT[k.dtype], p, h, s, d, 0, ks[0], ks[1], ks[2], vs[0], vs[1], vs[2])
+    return _CACHE.pack(k.data_ptr(), v.data_ptr(), _DT[k.dtype], p, h, s, d, 0, k0, k1, k2, v0, v1, v2), h, d
 
 
 def page_plan(lens, starts, tables, held, free, n_free, page, n_rows=None, slots=None, positions=None, held_out=None,
@@ -89,41 +99,41 @@ def page_plan(lens, starts, tables, held, free, n_free, page, n_rows=None, slots
     held_out and n_free_out are given; slots and positions int32 [n_rows] and
     status int32 [B] are allocated unless given."""
     lib = L.load()
-    dev = torch.cuda.current_device()
-    _on_gpu(dev, lens=lens, starts=starts, tables=tables, held=held, free=free, n_free=n_free, slots=slots,
-            positions=positions, held_out=held_out, n_free_out=n_free_out, status=status)
+    dev, st = _device(stream)
     if tables.dim() != 2 or free.dim() != 1:
         raise ValueError("tables must be [B, W], free [capacity]")
-    B, W = tables.shape
+    (B, W), (cap,), i32 = tables.shape, free.shape, torch.int32
     if n_rows is None:
         given = slots if slots is not None else positions
         if given is None:
             raise ValueError("n_rows is needed unless slots or positions are given")
         n_rows = given.shape[0]
-    st, own = _stream(stream)
-    with own:
-        if slots is None:
-            slots = torch.empty(n_rows, dtype=torch.int32, device=lens.device)
-        if positions is None:
-            positions = torch.empty(n_rows, dtype=torch.int32, device=lens.device)
-        if status is None:
-            status = torch.empty(B, dtype=torch.int32, device=lens.device)
+    if slots is None:
+        slots = _empty(n_rows, i32, dev, stream)
+    if positions is None:
+        positions = _empty(n_rows, i32, dev, stream)
+    if status is None:
+        status = _empty(B, i32, dev, stream)
     held_out = held if held_out is None else held_out
     n_free_out = n_free if n_free_out is None else n_free_out
-    L.check(lib.sf_page_plan(
-        _ints("lens", lens, (B,)), _ints("starts", starts, (B + 1,)), B, page, _ints("tables", tables, (B, W)), W,
-        _ints("held", held, (B,)), _ints("free", free, free.shape), free.shape[0], _ints("n_free", n_free, (1,)),
-        n_rows, _ints("slots", slots, (n_rows,)), _ints("positions", positions, (n_rows,)),
-        _ints("held_out", held_out, (B,)), _ints("n_free_out", n_free_out, (1,)), _ints("status", status, (B,)), st))
+    b1, n1 = (B,), (n_rows,)
+    s = lib.sf_page_plan(
+        _ptr("lens", lens, b1, i32, dev), _ptr("starts", starts, (B + 1,), i32, dev), B, page,
+        _ptr("tables", tables, (B, W), i32, dev), W, _ptr("held", held, b1, i32, dev),
+        _ptr("free", free, (cap,), i32, dev), cap, _ptr("n_free", n_free, (1,), i32, dev), n_rows,
+        _ptr("slots", slots, n1, i32, dev), _ptr("positions", positions, n1, i32, dev),
+        _ptr("held_out", held_out, b1, i32, dev), _ptr("n_free_out", n_free_out, (1,), i32, dev),
+        _ptr("status", status, b1, i32, dev), st)
+    if s:
+        L.check(s)
     return PagePlan(slots, positions, held_out, n_free_out, status)
 
 
 def rope_table(n_pos: int, head_dim: int, theta: float, stream=None) -> torch.Tensor:
     """The engine's RoPE table (sf_rope_table): fp32 [n_pos, head_dim // 2, 2],
     (cos, sin) of pos * theta ** (-2 i / head_dim)."""
-    st, own = _stream(stream)
-    with own:
-        out = torch.empty((n_pos, head_dim // 2, 2), dtype=torch.float32, device="cuda")
+    dev, st = _device(stream)
+    out = _empty((n_pos, head_dim // 2, 2), torch.float32, dev, stream)
     L.check(L.load().sf_rope_table(out.data_ptr(), n_pos, head_dim, theta, st))
     return out
 
@@ -135,31 +145,27 @@ def kv_append(k, v, slots, k_cache, v_cache, q=None, q_out=None, positions=None,
     positions int32 [n] first. Returns q_out (allocated in the cache's type
     unless given; its padding rows are then undefined), or None without q."""
     lib = L.load()
-    dev = torch.cuda.current_device()
-    _on_gpu(dev, k=k, v=v, slots=slots, k_cache=k_cache, v_cache=v_cache, q=q, q_out=q_out, positions=positions,
-            rope=rope)
-    cache = _cache(k_cache, v_cache)
-    n, hd = k.shape[0], cache.head_dim
-    st, own = _stream(stream)
-    rq = ro = None
+    dev, st = _device(stream)
+    cache, _, hd = _cache(k_cache, v_cache, dev)
+    n = k.shape[0]
+    rq = ro = pos = cs = None
+    n_pos = 0
     if q is not None:
         if q_out is None:
-            with own:
-                q_out = torch.empty(q.shape, dtype=k_cache.dtype, device=q.device)
-        rq, ro = _rows("q", q, n, hd), _rows("q_out", q_out, n, hd)
+            q_out = _empty(q.shape, k_cache.dtype, dev, stream)
+        rq, ro = _rows("q", q, n, hd, dev), _rows("q_out", q_out, n, hd, dev)
     elif q_out is not None:
         raise ValueError("q_out without q")
-    pos = cs = None
-    n_pos = 0
     if rope is not None:
-        if positions is None or rope.dim() != 3 or rope.shape[1:] != (hd // 2, 2) or rope.dtype != torch.float32 \
-                or not rope.is_contiguous():
-            raise ValueError(f"rope: expected positions and a contiguous fp32 table [n_pos, {hd // 2}, 2]")
-        pos, cs, n_pos = _ints("positions", positions, (n,)), rope.data_ptr(), rope.shape[0]
-    rk, rv = _rows("k", k, n, hd), _rows("v", v, n, hd)
-    L.check(lib.sf_kv_append(ctypes.byref(cache), n, ctypes.byref(rk), ctypes.byref(rv),
-                             _ints("slots", slots, (n,)), None if rq is None else ctypes.byref(rq),
-                             None if ro is None else ctypes.byref(ro), pos, cs, n_pos, st))
+        if positions is None:
+            raise ValueError("rope without positions")
+        n_pos = rope.shape[0]
+        pos = _ptr("positions", positions, (n,), torch.int32, dev)
+        cs = _ptr("rope", rope, (n_pos, hd // 2, 2), torch.float32, dev)
+    s = lib.sf_kv_append(cache, n, _rows("k", k, n, hd, dev), _rows("v", v, n, hd, dev),
+                         _ptr("slots", slots, (n,), torch.int32, dev), rq, ro, pos, cs, n_pos, st)
+    if s:
+        L.check(s)
     return q_out
 
 
@@ -185,35 +191,28 @@ def paged_attention(q, k_cache, v_cache, tables, lens, starts=None, max_rows=Non
     allocated unless given; lse float32 [n, heads] is written when given.
     Rows outside every request are left as they were."""
     lib = L.load()
-    dev = torch.cuda.current_device()
-    _on_gpu(dev, q=q, k_cache=k_cache, v_cache=v_cache, tables=tables, lens=lens, starts=starts, mask=mask, out=out,
-            lse=lse, workspace=workspace)
-    cache = _cache(k_cache, v_cache)
+    dev, st = _device(stream)
+    cache, nkv, hd = _cache(k_cache, v_cache, dev)
     if tables.dim() != 2:
         raise ValueError("tables must be [B, W]")
-    n, hd = q.shape[0], cache.head_dim
-    B, W = tables.shape
+    n, nq, (B, W), i32 = q.shape[0], q.shape[1], tables.shape, torch.int32
     if max_rows is None:
         if starts is not None:
             raise ValueError("max_rows is needed with starts")
         max_rows = max(1, n // max(1, B))
-    st, own = _stream(stream)
-    with own:
-        if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        if workspace is None:
-            workspace = paged_attention_workspace(q, k_cache, tables, max_rows)
-    need = lib.sf_paged_attention_workspace_bytes(q.shape[1], k_cache.shape[1], hd, max_rows)
-    if not workspace.is_contiguous() or workspace.numel() * workspace.element_size() < need:
-        raise ValueError(f"workspace: expected {need} contiguous bytes")
-    if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != tuple(q.shape[:2])
-                            or not lse.is_contiguous()):
-        raise ValueError(f"lse: expected a contiguous float32 tensor {tuple(q.shape[:2])}")
-    rq, ro = _rows("q", q, n, hd), _rows("out", out, n, hd)
-    L.check(lib.sf_paged_attention(
-        ctypes.byref(cache), ctypes.byref(rq), ctypes.byref(ro), n, _ints("tables", tables, (B, W)), W,
-        _ints("lens", lens, (B,)), None if starts is None else _ints("starts", starts, (B + 1,)), B, max_rows,
-        None if mask is None else _ints("mask", mask, (n,), torch.int64),
-        1.0 / math.sqrt(hd) if scale is None else scale, None if lse is None else lse.data_ptr(),
-        workspace.data_ptr(), st))
+    if out is None:
+        out = _empty(q.shape, q.dtype, dev, stream)
+    need = lib.sf_paged_attention_workspace_bytes(nq, nkv, hd, max_rows)
+    if workspace is None:
+        workspace = _empty(need, torch.uint8, dev, stream)
+    elif workspace.get_device() != dev or not workspace.is_contiguous() or workspace.nbytes < need:
+        raise ValueError(f"workspace: expected {need} contiguous bytes on cuda:{dev}")
+    s = lib.sf_paged_attention(
+        cache, _rows("q", q, n, hd, dev), _rows("out", out, n, hd, dev), n, _ptr("tables", tables, (B, W), i32, dev), W,
+        _ptr("lens", lens, (B,), i32, dev), None if starts is None else _ptr("starts", starts, (B + 1,), i32, dev), B,
+        max_rows, None if mask is None else _ptr("mask", mask, (n,), torch.int64, dev),
+        1.0 / math.sqrt(hd) if scale is None else scale,
+        None if lse is None else _ptr("lse", lse, (n, nq), torch.float32, dev), workspace.data_ptr(), st)
+    if s:
+        L.check(s)
     return out
