@@ -139,6 +139,7 @@ extern "C" sf_status sf_paged_attention(const sf_paged_cache* cache, const sf_ro
   a.part_ml = reinterpret_cast<float2*>(ws + lay.ml);
   a.part = reinterpret_cast<float*>(ws + lay.part);
   const long max_units = items(a.mt) * units;
+  a.by_warp = batch <= 32 * pa::kChunks && max_units <= INT32_MAX;
   sms = std::min(sms, pa::kMaxCtas / 2);
   cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
   e = cache->head_dim == 128 ? pa::launch_hd128(a, q->dtype, sms, max_units, st)

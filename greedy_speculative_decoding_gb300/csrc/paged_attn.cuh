@@ -48,6 +48,7 @@ struct Args {
   int mt;                  // queries of a tile (MT)
   int mt_max;              // queries of an item at most (min(MT, max_rows * group))
   int ntq_max;             // items of a (request, KV head) at most
+  int by_warp;             // few requests: every warp finds the CTA's units by itself
   int by_item;             // descriptors by item (else by the CTA that starts it)
   int4* desc;              // {first CTA, CTAs, request, KV head * ntq + query tile}
   float* part;             // [CTA][2][mt_max][HD]: output parts (0: of an item begun before, 1: begun here)
@@ -79,9 +80,16 @@ __device__ __forceinline__ Request request(const Args& a, int b) {
   return r;
 }
 
-// CTA c of G takes units [c * T / G, (c + 1) * T / G) of T.
-__device__ __forceinline__ long first_unit(long c, long T, long G) { return c * T / G; }
-__device__ __forceinline__ int cta_of_unit(long u, long T, long G) { return (int)(((u + 1) * G - 1) / T); }
+// T units over G CTAs: T / G each, and the first T % G one more.
+struct Deal {
+  long each, more;
+  __device__ __forceinline__ Deal(long T, long G) : each(T / G), more(T - T / G * G) {}
+  __device__ __forceinline__ long first(long c) const { return c * each + min(c, more); }
+  __device__ __forceinline__ int cta_of(long u) const {
+    const long big = more * (each + 1);
+    return (int)(u < big ? u / (each + 1) : more + (u - big) / each);
+  }
+};
 
 template <typename T>
 struct Num;
@@ -169,14 +177,72 @@ struct Shape {
   static constexpr int kSmem = 1024 + kStages * kStage + kExtra;
 };
 
-// The CTA's first unit: (request, unit within it). Every thread calls it.
+// Where a CTA's units begin.
 struct Start {
   long T;       // units in all
   long base;    // units before request b
   int b;
+  Request r;    // request b
 };
+
+// Every warp by itself, for at most 32 * kChunks requests and 2^31 units: the
+// first copies need not wait for the other warps.
+constexpr int kChunks = 4;
+template <int MT>
+__device__ __forceinline__ Start locate_warp(const Args& a) {
+  const int lane = threadIdx.x & 31;
+  Request r[kChunks];
+  int incl[kChunks], n[kChunks], T = 0;
+#pragma unroll
+  for (int c = 0; c < kChunks; ++c) {
+    n[c] = 0;
+    if (32 * c + lane < a.B) {
+      r[c] = request<MT>(a, 32 * c + lane);
+      n[c] = a.nkv * r[c].ntq * r[c].nt;
+    }
+  }
+#pragma unroll
+  for (int c = 0; c < kChunks; ++c) {
+    incl[c] = n[c];
+    if (c > 0 && 32 * c >= a.B) continue;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, incl[c], o);
+      if (lane >= o) incl[c] += x;
+    }
+    incl[c] += T;
+    T = __shfl_sync(0xffffffffu, incl[c], 31);
+  }
+  Start s;
+  s.T = T;
+  s.base = 0;
+  s.b = 0;
+  const long G = min((long)gridDim.x, s.T);
+  if ((long)blockIdx.x >= G) return s;
+  const int u0 = (int)Deal(T, G).first(blockIdx.x);
+  bool found = false;
+#pragma unroll
+  for (int c = 0; c < kChunks; ++c) {
+    if (found || (c > 0 && 32 * c >= a.B)) continue;
+    const unsigned past = __ballot_sync(0xffffffffu, incl[c] > u0);
+    if (!past) continue;
+    found = true;
+    const int l = __ffs(past) - 1;
+    s.b = 32 * c + l;
+    s.base = __shfl_sync(0xffffffffu, incl[c] - n[c], l);
+    s.r.s0 = __shfl_sync(0xffffffffu, r[c].s0, l);
+    s.r.rows = __shfl_sync(0xffffffffu, r[c].rows, l);
+    s.r.len = __shfl_sync(0xffffffffu, r[c].len, l);
+    s.r.p0 = __shfl_sync(0xffffffffu, r[c].p0, l);
+    s.r.nt = __shfl_sync(0xffffffffu, r[c].nt, l);
+    s.r.ntq = __shfl_sync(0xffffffffu, r[c].ntq, l);
+  }
+  return s;
+}
+
+// All threads of the CTA together, for any number of requests.
 template <int MT, int NT>
-__device__ __forceinline__ Start locate(const Args& a, long G, long* sh) {
+__device__ __forceinline__ Start locate_cta(const Args& a, long* sh) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   constexpr int NW = NT / 32;
   const int per = (a.B + NT - 1) / NT;
@@ -194,14 +260,16 @@ __device__ __forceinline__ Start locate(const Args& a, long G, long* sh) {
   }
   if (lane == 31) sh[warp] = incl;
   __syncthreads();
-  long before = 0, T = 0;
+  Start s;
+  long before = 0;
+  s.T = 0;
 #pragma unroll
   for (int w = 0; w < NW; ++w) {
     if (w < warp) before += sh[w];
-    T += sh[w];
+    s.T += sh[w];
   }
-  const long g = min(G, T);
-  const long u0 = (long)blockIdx.x < g ? first_unit(blockIdx.x, T, g) : -1;
+  const long G = min((long)gridDim.x, s.T);
+  const long u0 = (long)blockIdx.x < G ? Deal(s.T, G).first(blockIdx.x) : -1;
   const long lo = before + incl - mine;
   if (u0 >= lo && u0 < lo + mine) {
     long base = lo;
@@ -217,7 +285,10 @@ __device__ __forceinline__ Start locate(const Args& a, long G, long* sh) {
     }
   }
   __syncthreads();
-  return {T, sh[NW], (int)sh[NW + 1]};
+  s.base = u0 < 0 ? 0 : sh[NW];
+  s.b = u0 < 0 ? 0 : (int)sh[NW + 1];
+  s.r = request<MT>(a, s.b);
+  return s;
 }
 
 // Walks the pieces of items that a CTA's units [u, u1) make up.
@@ -228,10 +299,8 @@ struct Walk {
   int b;
   Request r;
   int item, kvh, qt, t0, t1;   // the current piece: item within the request, units t0 .. t1 - 1
-  __device__ __forceinline__ Walk(const Args& a, const Start& s, long first, long last)
-      : u(first), left((int)(last - first)), rem((int)(first - s.base)), b(s.b) {
-    r = request<MT>(a, b);
-  }
+  __device__ __forceinline__ Walk(const Start& s, long first, long last)
+      : u(first), left((int)(last - first)), rem((int)(first - s.base)), b(s.b), r(s.r) {}
   // The next piece; false at the end.
   __device__ __forceinline__ bool next(const Args& a) {
     if (left <= 0) return false;
@@ -280,16 +349,21 @@ __global__ void __launch_bounds__(Shape<HD, WM, WK, F32>::kThreads, Shape<HD, WM
       mbar_init(&empty[s], S::kWarps);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  } else if (tid >= S::kWarps * 32 && lane < 2) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(lane ? &a.vm : &a.km)) : "memory");
   }
-  const Start st = locate<MT, S::kThreads>(a, gridDim.x, sh_loc);   // (its barriers publish the mbarriers too)
+  __syncthreads();
+  pdl_wait();          // the kernels before this one have finished
+  pdl_launch_next();   // the join may come up meanwhile (it waits for this kernel's end)
+  const Start st = a.by_warp ? locate_warp<MT>(a) : locate_cta<MT, S::kThreads>(a, sh_loc);
   const long G = min((long)gridDim.x, st.T);
   if ((long)blockIdx.x >= G) {
     if (tid == 0 && !a.by_item) a.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
-    pdl_launch_next();
     return;
   }
-  const long u0 = first_unit(blockIdx.x, st.T, G), u1 = first_unit(blockIdx.x + 1, st.T, G);
-  Walk<MT> w(a, st, u0, u1);
+  const Deal deal(st.T, G);
+  const long u0 = deal.first(blockIdx.x), u1 = deal.first(blockIdx.x + 1);
+  Walk<MT> w(st, u0, u1);
 
   if (warp == S::kWarps) {
     // ---------------------------------------------------------- producer warp
@@ -356,28 +430,35 @@ __global__ void __launch_bounds__(Shape<HD, WM, WK, F32>::kThreads, Shape<HD, WM
       // The tile's queries in shared memory (fp32 ones as three bf16 terms).
       TC* sq = reinterpret_cast<TC*>(extra);
       cta_sync();   // the region's last readers are done
-      for (int e = tid; e < MT * (HD / 4); e += S::kWarps * 32) {
-        const int m = e / (HD / 4), d = 4 * (e - m * (HD / 4));
+      constexpr int E = F32 ? 4 : 8;                      // elements of a 16-byte load
+      constexpr int NL = MT * HD / E / (S::kWarps * 32);  // loads of a thread, all in flight together
+      uint4 f[NL];
+#pragma unroll
+      for (int y = 0; y < NL; ++y) {
+        const int e = tid + y * S::kWarps * 32, m = e / (HD / E), d = E * (e - m * (HD / E));
         const int x = w.qt * MT + m, jj = x / a.group, hh = w.kvh * a.group + x - jj * a.group;
-        const TQ* src = static_cast<const TQ*>(a.q) + (r.s0 + jj) * a.q_row + hh * a.q_head + d;
+        f[y] = make_uint4(0u, 0u, 0u, 0u);
+        if (x < Mq)
+          f[y] = *reinterpret_cast<const uint4*>(static_cast<const TQ*>(a.q) + (r.s0 + jj) * a.q_row + hh * a.q_head + d);
+      }
+#pragma unroll
+      for (int y = 0; y < NL; ++y) {
+        const int e = tid + y * S::kWarps * 32, m = e / (HD / E), d = E * (e - m * (HD / E));
         if constexpr (F32) {
-          float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (x < Mq) f = *reinterpret_cast<const float4*>(src);
-          float v[4] = {f.x, f.y, f.z, f.w};
+          float v[4] = {__uint_as_float(f[y].x), __uint_as_float(f[y].y), __uint_as_float(f[y].z), __uint_as_float(f[y].w)};
 #pragma unroll
           for (int k = 0; k < 3; ++k) {
             uint32_t p[2];
 #pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              p[y] = Num<bf16>::pack(v[2 * y], v[2 * y + 1]);
-              v[2 * y] -= Num<bf16>::lo(p[y]);
-              v[2 * y + 1] -= Num<bf16>::hi(p[y]);
+            for (int z = 0; z < 2; ++z) {
+              p[z] = Num<bf16>::pack(v[2 * z], v[2 * z + 1]);
+              v[2 * z] -= Num<bf16>::lo(p[z]);
+              v[2 * z + 1] -= Num<bf16>::hi(p[z]);
             }
             *reinterpret_cast<uint2*>(sq + (k * MT + m) * S::QP + d) = make_uint2(p[0], p[1]);
           }
         } else {
-          *reinterpret_cast<uint2*>(sq + m * S::QP + d) =
-              x < Mq ? *reinterpret_cast<const uint2*>(src) : make_uint2(0u, 0u);
+          *reinterpret_cast<uint4*>(sq + m * S::QP + d) = f[y];
         }
       }
       cta_sync();
@@ -398,12 +479,12 @@ __global__ void __launch_bounds__(Shape<HD, WM, WK, F32>::kThreads, Shape<HD, WM
     for (int d = 0; d < ND; ++d) o[d][0] = o[d][1] = o[d][2] = o[d][3] = 0.f;
 
     // One unit. Every row sees all slots of a plain one; a tail unit holds
-    // slots of the pass itself, or slots past the end.
-    auto unit = [&](auto tail_type, int t) {
-      constexpr bool TAIL = decltype(tail_type)::value;
+    // slots of the pass itself, or slots past the end; in an odd one, some of
+    // the pass's values are no finite numbers.
+    constexpr int PLAIN = 0, TAILED = 1, ODD = 2;
+    auto unit = [&](auto kind, int t) {
+      constexpr bool TAIL = decltype(kind)::value != PLAIN, CLEAN = decltype(kind)::value == ODD;
       const int s = n % S::kStages;
-      if (ok && !mbar_wait(&full[s], (n / S::kStages) & 1, kWaitIters)) ok = false;
-      ok = __all_sync(0xffffffffu, ok);
       const uint32_t ks = smem_u32(ring) + s * S::kStage, vs = ks + S::kHalf * S::kBox;
       const int base = t * kTile + wk * SW;         // this warp's first slot
       // ---- scores
@@ -439,24 +520,29 @@ __global__ void __launch_bounds__(Shape<HD, WM, WK, F32>::kThreads, Shape<HD, WM
 #pragma unroll
         for (int e = 0; e < 4; ++e) x[i][e] *= a.scale2;
       // ---- what a row does not see is -infinity (set, not added: what such
-      // slots hold, NaN included, does not matter)
-      int j[2] = {0, 0};
-      unsigned long long bits[2] = {0, 0};
-      auto sees = [&](int e, int slot) {
-        const int i = slot - r.p0;
-        return q0 + 8 * e < Mq && slot < r.len && (i < 0 || (a.mask ? i < 64 && ((bits[e] >> i) & 1) : i <= j[e]));
-      };
+      // slots hold, NaN included, does not matter). vis[e]: the slots of the
+      // unit that row e sees, one bit each, this lane's own from bit 0 on.
+      unsigned long long vis[2] = {0, 0};
       if constexpr (TAIL) {
+        const int first = r.p0 - t * kTile;          // the pass's first slot, within the unit
+        auto low = [](int k) { return k <= 0 ? 0ull : k >= 64 ? ~0ull : (1ull << k) - 1; };
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          j[e] = (q0 + 8 * e) / a.group;
-          if (a.mask && q0 + 8 * e < Mq) bits[e] = a.mask[r.s0 + j[e]];
+          const int q = q0 + 8 * e, j = q / a.group;
+          if (q < Mq) {
+            vis[e] = low(first + j + 1);
+            if (a.mask) {
+              const unsigned long long bits = a.mask[r.s0 + j];
+              vis[e] = low(first) | (first >= 64 || first <= -64 ? 0ull : first >= 0 ? bits << first : bits >> -first);
+            }
+            vis[e] = (vis[e] & low(r.len - t * kTile)) >> (wk * SW + 2 * c4);
+          }
         }
 #pragma unroll
         for (int i = 0; i < NS; ++i)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            if (!sees(e >> 1, base + 8 * i + 2 * c4 + (e & 1))) x[i][e] = -INFINITY;
+            if (!(vis[e >> 1] >> (8 * i + (e & 1)) & 1)) x[i][e] = -INFINITY;
       }
       // ---- running maximum and sum
       float ref[2];
@@ -494,11 +580,10 @@ __global__ void __launch_bounds__(Shape<HD, WM, WK, F32>::kThreads, Shape<HD, WM
           l[e >> 1] += x[i][e];
         }
       // ---- output: probabilities (the cache's type, or three bf16 terms) x
-      // values. In a tail unit values past the end are cut off, and values of
-      // the pass that are no finite numbers are taken out of the product (a
-      // probability 0 times NaN is NaN) and added for the rows that see them.
-      bool odd = false;
-      const bool clean = TAIL && (r.len - r.p0 > 1 || a.mask);
+      // values. In a tail unit values past the end are cut off; in an odd one
+      // the pass's values that are no finite numbers are taken out of the
+      // product (a probability 0 times NaN is NaN) and added for the rows that
+      // see them.
 #pragma unroll
       for (int i = 0; i < NS / 2; ++i) {
         uint32_t p[NQ][4];
@@ -530,11 +615,11 @@ __global__ void __launch_bounds__(Shape<HD, WM, WK, F32>::kThreads, Shape<HD, WM
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               vb[e] &= keep[e & 1];
-              if (clean) {
+              if constexpr (CLEAN) {
                 constexpr uint32_t X = Num<TC>::kExp;
                 const int sl = s0 + 8 * (e & 1);
-                if ((vb[e] & X) == X && sl >= r.p0) vb[e] &= 0xffff0000u, odd = true;
-                if ((vb[e] >> 16 & X) == X && sl + 1 >= r.p0) vb[e] &= 0xffffu, odd = true;
+                if ((vb[e] & X) == X && sl >= r.p0) vb[e] &= 0xffff0000u;
+                if ((vb[e] >> 16 & X) == X && sl + 1 >= r.p0) vb[e] &= 0xffffu;
               }
             }
           }
@@ -545,45 +630,75 @@ __global__ void __launch_bounds__(Shape<HD, WM, WK, F32>::kThreads, Shape<HD, WM
           }
         }
       }
-      if constexpr (TAIL) {
-        if (clean && __any_sync(0xffffffffu, odd)) {
+      if constexpr (CLEAN) {
 #pragma unroll
-          for (int i = 0; i < NS; ++i)
+        for (int i = 0; i < NS; ++i)
 #pragma unroll 1
-            for (int c = 0; c < 8; ++c) {
-              const int slot = base + 8 * i + c, src = (lane & ~3) + (c >> 1);
-              const float pa = __shfl_sync(0xffffffffu, c & 1 ? x[i][1] : x[i][0], src);
-              const float pb = __shfl_sync(0xffffffffu, c & 1 ? x[i][3] : x[i][2], src);
-              if (slot < r.p0 || slot >= r.len) continue;
-              const bool sa = sees(0, slot), sb = sees(1, slot);
-              const int sl = slot & (kTile - 1);
+          for (int c = 0; c < 8; ++c) {
+            const int slot = base + 8 * i + c, src = (lane & ~3) + (c >> 1);
+            const float pa = __shfl_sync(0xffffffffu, c & 1 ? x[i][1] : x[i][0], src);
+            const float pb = __shfl_sync(0xffffffffu, c & 1 ? x[i][3] : x[i][2], src);
+            // (the other lane's bits start at its own slots)
+            const bool sa = __shfl_sync(0xffffffffu, (int)(vis[0] >> (8 * i + (c & 1)) & 1), src);
+            const bool sb = __shfl_sync(0xffffffffu, (int)(vis[1] >> (8 * i + (c & 1)) & 1), src);
+            if (slot < r.p0 || slot >= r.len) continue;
+            const int sl = slot & (kTile - 1);
 #pragma unroll
-              for (int d = 0; d < ND; ++d) {
-                uint32_t v;
-                asm volatile("ld.shared.b32 %0, [%1];"
-                             : "=r"(v)
-                             : "r"(vs + (d >> 3) * S::kBox + sl * 128 + (((d & 7) ^ (sl & 7)) << 4) + 4 * c4));
-                constexpr uint32_t X = Num<TC>::kExp;
-                if ((v & X) == X) {
-                  if (sa) o[d][0] = fmaf(pa, Num<TC>::lo(v), o[d][0]);
-                  if (sb) o[d][2] = fmaf(pb, Num<TC>::lo(v), o[d][2]);
-                }
-                if ((v >> 16 & X) == X) {
-                  if (sa) o[d][1] = fmaf(pa, Num<TC>::hi(v), o[d][1]);
-                  if (sb) o[d][3] = fmaf(pb, Num<TC>::hi(v), o[d][3]);
-                }
+            for (int d = 0; d < ND; ++d) {
+              uint32_t v;
+              asm volatile("ld.shared.b32 %0, [%1];"
+                           : "=r"(v)
+                           : "r"(vs + (d >> 3) * S::kBox + sl * 128 + (((d & 7) ^ (sl & 7)) << 4) + 4 * c4));
+              constexpr uint32_t X = Num<TC>::kExp;
+              if ((v & X) == X) {
+                if (sa) o[d][0] = fmaf(pa, Num<TC>::lo(v), o[d][0]);
+                if (sb) o[d][2] = fmaf(pb, Num<TC>::lo(v), o[d][2]);
+              }
+              if ((v >> 16 & X) == X) {
+                if (sa) o[d][1] = fmaf(pa, Num<TC>::hi(v), o[d][1]);
+                if (sb) o[d][3] = fmaf(pb, Num<TC>::hi(v), o[d][3]);
               }
             }
-        }
+          }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[s]);
       ++n;
     };
+    auto arrived = [&] {
+      if (ok && !mbar_wait(&full[n % S::kStages], (n / S::kStages) & 1, kWaitIters)) ok = false;
+      ok = __all_sync(0xffffffffu, ok);
+    };
+    // Whether this warp's slots hold values of the pass that are no finite
+    // numbers and that some row may not see (one row sees all there is).
+    auto odd_values = [&](int t) {
+      if (r.len - r.p0 <= 1 && !a.mask) return false;
+      const uint32_t vs = smem_u32(ring) + n % S::kStages * S::kStage + S::kHalf * S::kBox;
+      const int s0 = max(wk * SW, r.p0 - t * kTile), s1 = min((wk + 1) * SW, r.len - t * kTile);
+      bool odd = false;
+      for (int e = lane; e < (s1 - s0) * 8 * S::kHalf; e += 32) {   // 16-byte pieces, in any order
+        const int sl = s0 + e / (8 * S::kHalf), p = e % (8 * S::kHalf);
+        uint32_t v[4];
+        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                     : "r"(vs + (p >> 3) * S::kBox + sl * 128 + (p & 7) * 16));
+        constexpr uint32_t X = Num<TC>::kExp;
+#pragma unroll
+        for (int y = 0; y < 4; ++y) odd |= (v[y] & X) == X || (v[y] >> 16 & X) == X;
+      }
+      return (bool)__any_sync(0xffffffffu, odd);
+    };
     const int plain = max(0, min(r.p0, r.len)) / kTile;   // units whose slots every row sees
     int t = w.t0;
-    for (; t < min(w.t1, plain); ++t) unit(std::false_type{}, t);
-    for (; t < w.t1; ++t) unit(std::true_type{}, t);
+    for (; t < min(w.t1, plain); ++t) {
+      arrived();
+      unit(std::integral_constant<int, PLAIN>{}, t);
+    }
+    for (; t < w.t1; ++t) {
+      arrived();
+      if (odd_values(t)) unit(std::integral_constant<int, ODD>{}, t);
+      else unit(std::integral_constant<int, TAILED>{}, t);
+    }
 
     // ---- the end of the piece
 #pragma unroll
@@ -595,7 +710,7 @@ __global__ void __launch_bounds__(Shape<HD, WM, WK, F32>::kThreads, Shape<HD, WM
     const bool begins = w.t0 == 0, whole = begins && w.t1 == r.nt;
     if (begins && tid == 0) {
       const long first = w.u - (w.t1 - w.t0);
-      const int c1 = whole ? (int)blockIdx.x : cta_of_unit(first + r.nt - 1, st.T, G);
+      const int c1 = whole ? (int)blockIdx.x : deal.cta_of(first + r.nt - 1);
       const int4 d = make_int4(blockIdx.x, c1 - (int)blockIdx.x + 1, w.b, w.item);
       if (a.by_item) a.desc[((long)w.b * a.nkv + w.kvh) * a.ntq_max + w.qt] = d;
       else if (!whole) a.desc[blockIdx.x] = d;
@@ -685,7 +800,6 @@ __global__ void __launch_bounds__(Shape<HD, WM, WK, F32>::kThreads, Shape<HD, WM
     }();
     if (!shared) a.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
   }
-  pdl_launch_next();
 }
 
 // The join: one CTA per (shared item, query). The parts lie with the CTAs
@@ -700,12 +814,13 @@ __global__ void __launch_bounds__(kJoinThreads) k_paged_join(const __grid_consta
   __shared__ float2 sml[4];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int x = blockIdx.y;
-  pdl_wait();
+  pdl_launch_next();
   if (a.by_item) {   // items of requests with fewer rows have no descriptor
     const int b = blockIdx.x / (a.nkv * a.ntq_max), qt = blockIdx.x % a.ntq_max;
     const Request r = request<MT>(a, b);
     if (qt >= r.ntq) return;
   }
+  pdl_wait();
   const int4 d = a.desc[blockIdx.x];
   if (d.y < 2) return;
   const Request r = request<MT>(a, d.z);

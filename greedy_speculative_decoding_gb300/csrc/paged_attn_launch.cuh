@@ -33,17 +33,20 @@ cudaError_t launch(Args& a, int sms, long max_units, cudaStream_t st) {
   }
   const long most = (long)sms * S::kCtas;
   const int grid = (int)(max_units < most ? max_units : most);
-  fn<<<grid, S::kThreads, S::kSmem, st>>>(a);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(a.by_item ? a.B * a.nkv * a.ntq_max : grid, a.mt_max);
-  cfg.blockDim = dim3(kJoinThreads);
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(S::kThreads);
+  cfg.dynamicSmemBytes = S::kSmem;
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  if ((e = cudaLaunchKernelEx(&cfg, fn, a)) != cudaSuccess) return e;
+  cfg.gridDim = dim3(a.by_item ? a.B * a.nkv * a.ntq_max : grid, a.mt_max);
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, k_paged_join<HD, TQ, S::MT>, a);
 }
 
