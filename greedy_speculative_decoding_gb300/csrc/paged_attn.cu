@@ -1,6 +1,7 @@
 // Attention over a paged key-value cache: the C entry (the kernels are in
 // paged_attn.cuh).
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 
 #include "paged_attn_launch.cuh"
@@ -119,7 +120,9 @@ extern "C" sf_status sf_paged_attention(const sf_paged_cache* cache, const sf_ro
   a.B = batch, a.N = n, a.W = table_width, a.nq = q->n_heads, a.nkv = cache->n_kv_heads;
   a.group = q->n_heads / cache->n_kv_heads;
   a.shift = log2_of(cache->page), a.max_rows = max_rows, a.rows_each = n / batch;
-  a.scale2 = scale * 1.44269504088896f;
+  // (never 0: the mask's -infinity times 0 would be NaN)
+  a.scale2 = std::max(std::fabs(scale) * 1.44269504088896f, FLT_TRUE_MIN);
+  a.flip = scale >= 0.f ? 0u : q->dtype == SF_DT_F32 ? 0x80000000u : 0x80008000u;
   // A smaller tile where the larger one's units could not occupy the GPU even
   // if every request filled its table: the cache is then read once for each
   // tile (from L2), by CTAs that would be idle.

@@ -44,11 +44,13 @@ struct Args {
   const int *tables, *lens, *starts;
   const unsigned long long* mask;
   int B, N, W, nq, nkv, group, shift, max_rows, rows_each;
-  float scale2;            // scale * log2(e)
+  float scale2;            // |scale| * log2(e)
+  uint32_t flip;           // sign bits that turn q into -q where scale is negative, or 0
   int mt;                  // queries of a tile (MT)
   int mt_max;              // queries of an item at most (min(MT, max_rows * group))
   int ntq_max;             // items of a (request, KV head) at most
   int by_warp;             // few requests: every warp finds the CTA's units by itself
+  int wide;                // few items: a CTA joins one query, else four
   int by_item;             // descriptors by item (else by the CTA that starts it)
   int4* desc;              // {first CTA, CTAs, request, KV head * ntq + query tile}
   float* part;             // [CTA][2][mt_max][HD]: output parts (0: of an item begun before, 1: begun here)
@@ -83,11 +85,14 @@ __device__ __forceinline__ Request request(const Args& a, int b) {
 // T units over G CTAs: T / G each, and the first T % G one more.
 struct Deal {
   long each, more;
-  __device__ __forceinline__ Deal(long T, long G) : each(T / G), more(T - T / G * G) {}
+  __device__ __forceinline__ Deal(long T, long G) : each(div(T, G)), more(T - each * G) {}
+  static __device__ __forceinline__ long div(long x, long y) {   // (a 64-bit division is a long call)
+    return (x | y) >> 32 ? x / y : (long)((unsigned)x / (unsigned)y);
+  }
   __device__ __forceinline__ long first(long c) const { return c * each + min(c, more); }
   __device__ __forceinline__ int cta_of(long u) const {
     const long big = more * (each + 1);
-    return (int)(u < big ? u / (each + 1) : more + (u - big) / each);
+    return (int)(u < big ? div(u, each + 1) : more + div(u - big, each));
   }
 };
 
@@ -444,6 +449,7 @@ __global__ void __launch_bounds__(Shape<HD, WM, WK, F32>::kThreads, Shape<HD, WM
 #pragma unroll
       for (int y = 0; y < NL; ++y) {
         const int e = tid + y * S::kWarps * 32, m = e / (HD / E), d = E * (e - m * (HD / E));
+        f[y].x ^= a.flip, f[y].y ^= a.flip, f[y].z ^= a.flip, f[y].w ^= a.flip;
         if constexpr (F32) {
           float v[4] = {__uint_as_float(f[y].x), __uint_as_float(f[y].y), __uint_as_float(f[y].z), __uint_as_float(f[y].w)};
 #pragma unroll
@@ -469,8 +475,8 @@ __global__ void __launch_bounds__(Shape<HD, WM, WK, F32>::kThreads, Shape<HD, WM
         const TQ* src = static_cast<const TQ*>(a.q) + (r.s0 + jj) * a.q_row + hh * a.q_head + 2 * c4;
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
-          qf[k][e] = x < Mq ? *reinterpret_cast<const uint32_t*>(src + 16 * k) : 0u;
-          qf[k][e + 2] = x < Mq ? *reinterpret_cast<const uint32_t*>(src + 16 * k + 8) : 0u;
+          qf[k][e] = x < Mq ? *reinterpret_cast<const uint32_t*>(src + 16 * k) ^ a.flip : 0u;
+          qf[k][e + 2] = x < Mq ? *reinterpret_cast<const uint32_t*>(src + 16 * k + 8) ^ a.flip : 0u;
         }
       }
     }
@@ -515,10 +521,6 @@ __global__ void __launch_bounds__(Shape<HD, WM, WK, F32>::kThreads, Shape<HD, WM
           }
         }
       }
-#pragma unroll
-      for (int i = 0; i < NS; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[i][e] *= a.scale2;
       // ---- what a row does not see is -infinity (set, not added: what such
       // slots hold, NaN included, does not matter). vis[e]: the slots of the
       // unit that row e sees, one bit each, this lane's own from bit 0 on.
@@ -544,7 +546,7 @@ __global__ void __launch_bounds__(Shape<HD, WM, WK, F32>::kThreads, Shape<HD, WM
           for (int e = 0; e < 4; ++e)
             if (!(vis[e >> 1] >> (8 * i + (e & 1)) & 1)) x[i][e] = -INFINITY;
       }
-      // ---- running maximum and sum
+      // ---- running maximum (of q . k; the scale is not negative) and sum
       float ref[2];
       bool raise = false;
 #pragma unroll
@@ -560,7 +562,7 @@ __global__ void __launch_bounds__(Shape<HD, WM, WK, F32>::kThreads, Shape<HD, WM
       if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const float f = m[e] == -INFINITY ? 0.f : exp2_approx(m[e] - ref[e]);
+          const float f = m[e] == -INFINITY ? 0.f : exp2_approx((m[e] - ref[e]) * a.scale2);
           m[e] = ref[e];
           l[e] *= f;
 #pragma unroll
@@ -571,12 +573,12 @@ __global__ void __launch_bounds__(Shape<HD, WM, WK, F32>::kThreads, Shape<HD, WM
         }
       }
 #pragma unroll
-      for (int e = 0; e < 2; ++e) ref[e] = m[e] == -INFINITY ? 0.f : m[e];
+      for (int e = 0; e < 2; ++e) ref[e] = m[e] == -INFINITY ? 0.f : -m[e] * a.scale2;
 #pragma unroll
       for (int i = 0; i < NS; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          x[i][e] = exp2_approx(x[i][e] - ref[e >> 1]);
+          x[i][e] = exp2_approx(fmaf(x[i][e], a.scale2, ref[e >> 1]));
           l[e >> 1] += x[i][e];
         }
       // ---- output: probabilities (the cache's type, or three bf16 terms) x
@@ -690,6 +692,13 @@ __global__ void __launch_bounds__(Shape<HD, WM, WK, F32>::kThreads, Shape<HD, WM
     };
     const int plain = max(0, min(r.p0, r.len)) / kTile;   // units whose slots every row sees
     int t = w.t0;
+    if (w.qt * MT + 16 * wm >= Mq) {   // no query for this warp: it only keeps the ring going
+      for (; t < w.t1; ++t, ++n) {
+        arrived();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[n % S::kStages]);
+      }
+    }
     for (; t < min(w.t1, plain); ++t) {
       arrived();
       unit(std::integral_constant<int, PLAIN>{}, t);
@@ -706,6 +715,7 @@ __global__ void __launch_bounds__(Shape<HD, WM, WK, F32>::kThreads, Shape<HD, WM
       l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
       l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
       if (!ok) l[e] = __int_as_float(0x7fc00000);   // an expired wait: NaN
+      if (m[e] != -INFINITY) m[e] *= a.scale2;
     }
     const bool begins = w.t0 == 0, whole = begins && w.t1 == r.nt;
     if (begins && tid == 0) {
@@ -802,9 +812,10 @@ __global__ void __launch_bounds__(Shape<HD, WM, WK, F32>::kThreads, Shape<HD, WM
   }
 }
 
-// The join: one CTA per (shared item, query). The parts lie with the CTAs
-// first .. first + count - 1; the warps take them in turn and their four
-// sums are added in order.
+// The join of the items that several CTAs share: the parts lie with the CTAs
+// first .. first + count - 1. With few items (`wide`: many parts each) one CTA
+// per (item, query), its four warps taking the parts in turn and their sums
+// added in order; else a warp per (item, query).
 constexpr int kJoinThreads = 128;
 
 template <int HD, typename TQ, int MT>
@@ -813,32 +824,42 @@ __global__ void __launch_bounds__(kJoinThreads) k_paged_join(const __grid_consta
   __shared__ float so[4][HD];
   __shared__ float2 sml[4];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int x = blockIdx.y;
+  const int x = a.wide ? blockIdx.y : 4 * blockIdx.y + warp;   // query of the tile
   pdl_launch_next();
+  Request r;
+  int kvh = 0, qt = 0;
   if (a.by_item) {   // items of requests with fewer rows have no descriptor
-    const int b = blockIdx.x / (a.nkv * a.ntq_max), qt = blockIdx.x % a.ntq_max;
-    const Request r = request<MT>(a, b);
-    if (qt >= r.ntq) return;
+    const int b = blockIdx.x / (a.nkv * a.ntq_max), i = blockIdx.x - b * a.nkv * a.ntq_max;
+    kvh = i / a.ntq_max;
+    qt = i - kvh * a.ntq_max;
+    r = request<MT>(a, b);
+    if (qt * MT + x >= r.rows * a.group) return;   // (all of a wide join's CTA)
   }
   pdl_wait();
   const int4 d = a.desc[blockIdx.x];
   if (d.y < 2) return;
-  const Request r = request<MT>(a, d.z);
-  const int kvh = d.w / r.ntq, q = (d.w - kvh * r.ntq) * MT + x;
+  if (!a.by_item) {
+    r = request<MT>(a, d.z);
+    kvh = d.w / r.ntq;
+    qt = d.w - kvh * r.ntq;
+  }
+  const int q = qt * MT + x;
   if (q >= r.rows * a.group) return;
   auto slot = [&](int k) { return (2l * (d.x + k) + (k == 0 ? 1 : 0)) * a.mt_max + x; };
-  float mm = -INFINITY;
-  for (int k = lane; k < d.y; k += 32) mm = fmaxf(mm, a.part_ml[slot(k)].x);
-  mm = warp_max(mm);
-  float l = 0.f, o[V];
+  const int k0 = a.wide ? warp : 0, step = a.wide ? 4 : 1;
+  // A running maximum again, over batches of eight parts loaded together.
+  float m = -INFINITY, l = 0.f, o[V];
 #pragma unroll
   for (int e = 0; e < V; ++e) o[e] = 0.f;
-  for (int k0 = warp; k0 < d.y; k0 += 4 * 8) {
+  for (int kb = k0; kb < d.y; kb += 8 * step) {
     float v[8][V];
     float2 ml[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int k = k0 + 4 * i;
+      const int k = kb + i * step;
+      ml[i] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+      for (int e = 0; e < V; ++e) v[i][e] = 0.f;
       if (k < d.y) {
         ml[i] = a.part_ml[slot(k)];
         const float* p = a.part + slot(k) * HD + V * lane;
@@ -849,34 +870,48 @@ __global__ void __launch_bounds__(kJoinThreads) k_paged_join(const __grid_consta
           const float2 f = *reinterpret_cast<const float2*>(p);
           v[i][0] = f.x, v[i][1] = f.y;
         }
-      } else {
-        ml[i] = make_float2(-INFINITY, 0.f);
-#pragma unroll
-        for (int e = 0; e < V; ++e) v[i][e] = 0.f;
       }
     }
+    float mm = m;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) mm = fmaxf(mm, ml[i].x);
+    const float f0 = m == -INFINITY ? 0.f : exp2_approx(m - mm);
+    m = mm;
+    if (m != -INFINITY) l *= f0 == 0.f && l != l ? 1.f : f0;   // (a NaN stays)
+#pragma unroll
+    for (int e = 0; e < V; ++e) o[e] *= f0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float f = ml[i].x == -INFINITY ? 0.f : exp2_approx(ml[i].x - mm);
-      l += ml[i].x == -INFINITY ? ml[i].y : ml[i].y * f;
+      const float f = ml[i].x == -INFINITY ? 0.f : exp2_approx(ml[i].x - m);
+      l += ml[i].x == -INFINITY ? ml[i].y : ml[i].y * f;   // (a part that saw nothing has sum 0, a failed one NaN)
 #pragma unroll
       for (int e = 0; e < V; ++e) o[e] = fmaf(v[i][e], f, o[e]);
     }
   }
+  if (a.wide) {
 #pragma unroll
-  for (int e = 0; e < V; ++e) so[warp][V * lane + e] = o[e];
-  if (lane == 0) sml[warp] = make_float2(mm, l);
-  __syncthreads();
-  if (threadIdx.x * 2 >= HD) return;
-  l = ((sml[0].y + sml[1].y) + sml[2].y) + sml[3].y;
-  const int d0 = 2 * threadIdx.x;
-  const float y0 = ((so[0][d0] + so[1][d0]) + so[2][d0]) + so[3][d0];
-  const float y1 = ((so[0][d0 + 1] + so[1][d0 + 1]) + so[2][d0 + 1]) + so[3][d0 + 1];
+    for (int e = 0; e < V; ++e) so[warp][V * lane + e] = o[e];
+    if (lane == 0) sml[warp] = make_float2(m, l);
+    __syncthreads();
+    if (warp > 0) return;
+    m = fmaxf(fmaxf(sml[0].x, sml[1].x), fmaxf(sml[2].x, sml[3].x));
+    l = 0.f;
+#pragma unroll
+    for (int e = 0; e < V; ++e) o[e] = 0.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float f = sml[k].x == -INFINITY ? 0.f : exp2_approx(sml[k].x - m);
+      l += sml[k].x == -INFINITY ? sml[k].y : sml[k].y * f;
+#pragma unroll
+      for (int e = 0; e < V; ++e) o[e] = fmaf(so[k][V * lane + e], f, o[e]);
+    }
+  }
   const int jj = q / a.group, hh = kvh * a.group + q - jj * a.group;
   const float inv = l == 0.f ? 0.f : 1.f / l;
-  store2<TQ>(static_cast<TQ*>(a.out) + (r.s0 + jj) * a.o_row + hh * a.o_head + d0, y0 * inv, y1 * inv);
-  if (a.lse && threadIdx.x == 0)
-    a.lse[(long)(r.s0 + jj) * a.nq + hh] = l == 0.f ? -INFINITY : mm * 0.693147180559945f + logf(l);
+  TQ* dst = static_cast<TQ*>(a.out) + (r.s0 + jj) * a.o_row + hh * a.o_head + V * lane;
+  store2<TQ>(dst, o[0] * inv, o[1] * inv);
+  if constexpr (V == 4) store2<TQ>(dst + 2, o[2] * inv, o[3] * inv);
+  if (a.lse && lane == 0) a.lse[(long)(r.s0 + jj) * a.nq + hh] = l == 0.f ? -INFINITY : m * 0.693147180559945f + logf(l);
 }
 
 }  // namespace pa

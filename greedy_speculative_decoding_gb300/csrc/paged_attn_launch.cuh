@@ -31,8 +31,9 @@ cudaError_t launch(Args& a, int sms, long max_units, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     if (dev < 64) ready.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
   }
-  const long most = (long)sms * S::kCtas;
+  const long most = (long)sms * S::kCtas, items = (long)a.B * a.nkv * a.ntq_max;
   const int grid = (int)(max_units < most ? max_units : most);
+  a.wide = items * 8 <= grid;   // an item's parts: one and as many as CTAs share it
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -44,7 +45,7 @@ cudaError_t launch(Args& a, int sms, long max_units, cudaStream_t st) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   if ((e = cudaLaunchKernelEx(&cfg, fn, a)) != cudaSuccess) return e;
-  cfg.gridDim = dim3(a.by_item ? a.B * a.nkv * a.ntq_max : grid, a.mt_max);
+  cfg.gridDim = dim3(a.by_item ? (int)items : grid, a.wide ? a.mt_max : (a.mt_max + 3) / 4);
   cfg.blockDim = dim3(kJoinThreads);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, k_paged_join<HD, TQ, S::MT>, a);
