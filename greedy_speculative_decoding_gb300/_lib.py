@@ -25,7 +25,9 @@ EXPORTS = (
     "sf_destroy", "sf_nf4_quantize", "sf_linear_workspace_bytes", "sf_linear", "sf_linear_noalloc",
     "sf_trace", "sf_trace_label", "sf_frag_bytes", "sf_to_frag", "sf_linear_frag", "sf_round_launches",
     "sf_tree_draft", "sf_set_tree_candidates", "sf_tree_winner",
-    "sf_page_plan", "sf_rope_table", "sf_kv_append", "sf_paged_attention_workspace_bytes", "sf_paged_attention",
+    "sf_page_plan", "sf_rope_table", "sf_kv_append",
+    "sf_kv_pool_bytes", "sf_paged_engine_workspace_bytes", "sf_create_paged", "sf_get_pages",
+    "sf_paged_attention_workspace_bytes", "sf_paged_attention",
 )
 
 
@@ -107,6 +109,10 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "sf_tree_draft": (ST, [P, I32, I32, I32, P, P]),
         "sf_set_tree_candidates": (ST, [P, I32]),
         "sf_tree_winner": (ST, [P, PI32]),
+        "sf_kv_pool_bytes": (SZ, [PCFG, I32]),
+        "sf_paged_engine_workspace_bytes": (SZ, [PCFG, PCFG, I32, I32, I32, I32]),
+        "sf_create_paged": (ST, [PCFG, P, PCFG, P, I32, I32, I32, I32, P, P, P, P, ctypes.POINTER(P)]),
+        "sf_get_pages": (ST, [P, PI32, PI32]),
         "sf_page_plan": (ST, [P, P, I32, I32, P, I32, P, P, I32, P, I32, P, P, P, P, P, P]),
         "sf_rope_table": (ST, [P, I32, I32, ctypes.c_float, P]),
         "sf_kv_append": (ST, [P, I32, P, P, P, P, P, P, P, I32, P]),

@@ -17,6 +17,7 @@
 #include <string>
 #include <vector>
 
+#include "paged.h"
 #include "sf_kernels.h"
 
 using namespace sf;
@@ -84,6 +85,7 @@ struct Model {
   const void* norm = nullptr;
   const void* lm = nullptr;
   int lm_ld = 0;
+  int n_pages = 0;         // > 0: the cache is a pool of pages of 64 slots (sf_create_paged), else s_max slots per sequence
   CUtensorMap lm_tm;
   CUtensorMap lm_tmu;      // 64-row boxes: the LM head of forwards of more than 16 rows (tcgen05)
   bf16* kv = nullptr;
@@ -247,6 +249,35 @@ Layout make_layout(const sf_model_cfg* t, const sf_model_cfg* d, int B, int K, i
   return L;
 }
 
+// Workspace of the page tables and the paged attention, behind make_layout's
+// (offsets from its end): block tables, pages held, the stack of free pages,
+// its height, plan statuses, cache slots and positions of a forward's rows,
+// masks of candidate rows, attention scratch.
+struct PagedLayout {
+  size_t tables, held, free, n_free, status, slots, positions, mask, attn, total;
+};
+
+PagedLayout paged_layout(const sf_model_cfg* t, int B, int s_max, int n_pages) {
+  PagedLayout L{};
+  size_t p = 0;
+  auto take = [&](size_t bytes) {
+    size_t r = p;
+    p = align256(p + bytes);
+    return r;
+  };
+  L.tables = take((size_t)B * (s_max / kKvChunk) * 4);
+  L.held = take((size_t)B * 4);
+  L.free = take((size_t)n_pages * 4);
+  L.n_free = take(4);
+  L.status = take((size_t)B * 4);
+  L.slots = take((size_t)kRows * 4);
+  L.positions = take((size_t)kRows * 4);
+  L.mask = take((size_t)kRows * 8);
+  L.attn = take(sf_paged_attention_workspace_bytes(t->n_heads, t->n_kv_heads, t->head_dim, kRows));
+  L.total = p;
+  return L;
+}
+
 }  // namespace
 
 sf_status sf::set_error(sf_status s, const char* fmt, ...) {
@@ -282,6 +313,11 @@ struct sf_engine {
   int *counters = nullptr, *done = nullptr, *zeros = nullptr;
   unsigned long long* keys = nullptr;
   SpecState st{};
+  // The target's pages (tgt.n_pages > 0).
+  int *pg_tables = nullptr, *pg_held = nullptr, *pg_free = nullptr, *pg_n_free = nullptr, *pg_status = nullptr,
+      *pg_slots = nullptr, *pg_positions = nullptr;
+  unsigned long long* pg_mask = nullptr;
+  void* pg_attn = nullptr;
   int* pin = nullptr;   // pinned host copy of the report block
   cudaGraphExec_t graph[4] = {};   // whole round, per drafter (SF_DRAFT_*)
   size_t graph_kernels[4] = {};    // kernel launches in each round graph
@@ -351,7 +387,7 @@ sf_status bind_model(sf_engine* e, Model& md, const sf_model_cfg* c, const void*
     if (!check(md.lm, "lm_head", false)) return fail(SF_ERR_ARG, "lm_head pointer null or misaligned");
   }
   md.kv = kv;
-  {
+  if (md.n_pages == 0) {   // (the attention over pages makes its own maps)
     const long rows = (long)c->layers * 2 * e->B * c->n_kv_heads * e->s_max;
     cudaError_t ce = make_kv_map(&md.kvmap, kv, rows, c->head_dim);
     if (ce == cudaSuccess) ce = make_kv_map(&md.kvmap8, kv, rows, c->head_dim, 8);
@@ -491,6 +527,39 @@ struct TokOut {
   int lg_stride = 0, lg_off = 0;
 };
 
+// Pages for the rows of a forward over the target's pool: those that its
+// sequences lack for them are taken, those behind the last round's rewind go
+// back, and every row gets its cache slot. One sequence alone when seq >= 0.
+cudaError_t plan_pages(sf_engine* e, const int* pos_base, int len_add, int rows, int seq, cudaStream_t s) {
+  const int W = e->s_max / kKvChunk, b0 = seq >= 0 ? seq : 0;
+  PlanArgs p{};
+  p.lens = pos_base;
+  p.len_add = len_add;
+  p.rows_each = rows;
+  p.tables = e->pg_tables + (size_t)b0 * W;
+  p.held = p.held_out = e->pg_held + b0;
+  p.free = e->pg_free;
+  p.n_free = p.n_free_out = e->pg_n_free;
+  p.slots = e->pg_slots;
+  p.positions = e->pg_positions;
+  p.status = e->pg_status;
+  p.B = seq >= 0 ? 1 : e->B;
+  p.W = W;
+  p.cap = e->tgt.n_pages;
+  p.shift = 6;
+  p.N = p.B * rows;
+  return launch_page_plan(p, s);
+}
+
+// Whether the target's pool has the pages for n tokens more than every
+// sequence has in the cache (all it has committed but the pending token).
+bool pages_fit(const sf_engine* e, const std::vector<int>& committed, int n) {
+  if (e->tgt.n_pages == 0) return true;
+  long need = 0;
+  for (int c : committed) need += (c - 1 + n + kKvChunk - 1) / kKvChunk;
+  return need <= e->tgt.n_pages;
+}
+
 // Enqueue one forward pass of `md` over the rows `rs`. With `lm` the final
 // norm + LM head + argmax run too and write tokens (and optional logits).
 // seq >= 0: every row belongs to sequence `seq` alone (its cache is addressed
@@ -522,7 +591,12 @@ sf_status forward(sf_engine* e, Model& md, const RowSet& rs, bool lm, const TokO
   };
   // At most four rows (a decode step): one persistent kernel for the whole
   // forward up to the LM head's input.
-  const bool use_dec = e->dec_on && rs.M <= md.dec_rows && rs.rps <= 2 && rs.tree_g == 0 && seq < 0;
+  const bool paged = md.n_pages > 0;
+  const bool use_dec = e->dec_on && !paged && rs.M <= md.dec_rows && rs.rps <= 2 && rs.tree_g == 0 && seq < 0;
+  if (paged) {
+    CK(plan_pages(e, rs.pos_base, rs.pos_off + rs.rps, rs.rps, seq, s));
+    if (rs.tree_g > 0) CK(launch_tree_mask(e->pg_mask, e->B, rs.rps, rs.tree_g, s, e->pdl));
+  }
   if (use_dec) {
     DecArgs d{};
     d.layers = md.dlay;
@@ -577,13 +651,14 @@ sf_status forward(sf_engine* e, Model& md, const RowSet& rs, bool lm, const TokO
   if (!use_dec) {
     ea.rs = traced(e, rs, "embed");
     CK(launch_embed(ea, s, e->pdl));
-    const size_t seq_elems = (size_t)c.n_kv_heads * e->s_max * c.head_dim;   // one sequence's keys of a layer
-    const size_t layer_elems = 2 * e->B * seq_elems;
+    // One sequence's keys of a layer; in a pool, one page's.
+    const size_t seq_elems = (size_t)c.n_kv_heads * (paged ? kKvChunk : e->s_max) * c.head_dim;
+    const size_t layer_elems = 2 * (paged ? md.n_pages : e->B) * seq_elems;
     for (int l = 0; l < c.layers; ++l) {
       const LayerW& lw = md.L[l];
       bf16* kc = md.kv + (size_t)l * layer_elems;
       bf16* vc = kc + layer_elems / 2;
-      if (seq >= 0) {
+      if (seq >= 0 && !paged) {
         kc += seq * seq_elems;
         vc += seq * seq_elems;
       }
@@ -621,43 +696,66 @@ sf_status forward(sf_engine* e, Model& md, const RowSet& rs, bool lm, const TokO
       a.s_max = e->s_max;
       a.kc = kc;
       a.vc = vc;
+      a.slots = paged ? e->pg_slots : nullptr;
       a.rope = md.rope;
       a.rs = traced(e, rs, "qkv");
       CK(gemm(a, EPI_QKV));
       // attention
-      AttnArgs t{};
-      t.kvmap = md.kvmap;
-      t.kvmap8 = md.kvmap8;
-      t.kc = kc;
-      t.vc = vc;
-      t.box8 = e->box8 ? 1 : 0;
-      t.kv_brows = c.n_kv_heads * e->s_max;
-      t.kv_vrows = e->B * t.kv_brows;
-      t.kv_row0 = (2 * l * e->B + (seq >= 0 ? seq : 0)) * t.kv_brows;
-      t.R = md.attn_R;
-      // Query tiles per work item (a row's result does not depend on it):
-      // one, or every tile of a KV head's queries together, up to four, one
-      // team of warps each.
-      {
-        const int ntiles = (rs.rps * (c.n_heads / c.n_kv_heads) + 15) / 16;
-        t.TG = !md.attn_group ? 1 : (ntiles >= 3 ? 4 : ntiles);
+      if (paged) {
+        EngineAttn p{};
+        const int64_t page = (int64_t)seq_elems;
+        p.cache = sf_paged_cache{kc, vc, SF_DT_BF16, md.n_pages, c.n_kv_heads, kKvChunk, c.head_dim, 0,
+                                 page, page / c.n_kv_heads, c.head_dim, page, page / c.n_kv_heads, c.head_dim};
+        p.q = e->q;
+        p.out = e->fo;
+        p.umma = tc;
+        p.table_width = e->s_max / kKvChunk;
+        p.tables = e->pg_tables + (seq >= 0 ? (size_t)seq * p.table_width : 0);
+        p.lens = rs.pos_base;
+        p.len_add = rs.pos_off + rs.rps;
+        p.B = seq >= 0 ? 1 : e->B;
+        p.rows = rs.rps;
+        p.nq = c.n_heads;
+        p.mask = rs.tree_g > 0 ? e->pg_mask : nullptr;
+        p.scale = 1.0f / sqrtf((float)c.head_dim);
+        p.err = e->st.err;
+        p.workspace = e->pg_attn;
+        CK(launch_engine_paged_attention(p, e->num_sms, s));
+      } else {
+        AttnArgs t{};
+        t.kvmap = md.kvmap;
+        t.kvmap8 = md.kvmap8;
+        t.kc = kc;
+        t.vc = vc;
+        t.box8 = e->box8 ? 1 : 0;
+        t.kv_brows = c.n_kv_heads * e->s_max;
+        t.kv_vrows = e->B * t.kv_brows;
+        t.kv_row0 = (2 * l * e->B + (seq >= 0 ? seq : 0)) * t.kv_brows;
+        t.R = md.attn_R;
+        // Query tiles per work item (a row's result does not depend on it):
+        // one, or every tile of a KV head's queries together, up to four, one
+        // team of warps each.
+        {
+          const int ntiles = (rs.rps * (c.n_heads / c.n_kv_heads) + 15) / 16;
+          t.TG = !md.attn_group ? 1 : (ntiles >= 3 ? 4 : ntiles);
+        }
+        t.stages = md.attn_stages;
+        t.q = e->q;
+        t.part = e->apart;
+        t.out = e->fo;
+        t.nq = c.n_heads;
+        t.nkv = c.n_kv_heads;
+        t.hd = c.head_dim;
+        t.s_max = e->s_max;
+        t.B = seq >= 0 ? 1 : e->B;
+        t.n_kv_chunks = e->lay.n_kv_chunks;
+        t.scale = 1.0f / sqrtf((float)c.head_dim);
+        t.err = e->st.err;
+        t.umma = tc;
+        t.rs = traced(e, rs, "attention");
+        t.merge_trace_id = traced(e, rs, "merge").trace_id;
+        CK(launch_attention(t, e->num_sms, s, e->pdl));
       }
-      t.stages = md.attn_stages;
-      t.q = e->q;
-      t.part = e->apart;
-      t.out = e->fo;
-      t.nq = c.n_heads;
-      t.nkv = c.n_kv_heads;
-      t.hd = c.head_dim;
-      t.s_max = e->s_max;
-      t.B = seq >= 0 ? 1 : e->B;
-      t.n_kv_chunks = e->lay.n_kv_chunks;
-      t.scale = 1.0f / sqrtf((float)c.head_dim);
-      t.err = e->st.err;
-      t.umma = tc;
-      t.rs = traced(e, rs, "attention");
-      t.merge_trace_id = traced(e, rs, "merge").trace_id;
-      CK(launch_attention(t, e->num_sms, s, e->pdl));
       // o-projection + residual
       a = base_args(e, md, tc ? md.u_o : md.p_o, rs);
       a.w[0] = lw.w[W_O];
@@ -1027,6 +1125,18 @@ size_t sf_workspace_bytes(const sf_model_cfg* tgt, const sf_model_cfg* dft, int3
   return make_layout(tgt, dft, batch, K, s_max).total;
 }
 
+size_t sf_kv_pool_bytes(const sf_model_cfg* cfg, int32_t n_pages) {
+  if (!cfg || n_pages < 1) return 0;
+  return (size_t)cfg->layers * 2 * n_pages * cfg->n_kv_heads * (size_t)kKvChunk * cfg->head_dim * 2;
+}
+
+size_t sf_paged_engine_workspace_bytes(const sf_model_cfg* tgt, const sf_model_cfg* dft, int32_t batch, int32_t K,
+                                       int32_t s_max, int32_t n_pages) {
+  const size_t base = sf_workspace_bytes(tgt, dft, batch, K, s_max);
+  if (base == 0 || n_pages < 1 || n_pages > (1 << 24)) return 0;
+  return base + paged_layout(tgt, batch, s_max, n_pages).total;
+}
+
 const char* sf_status_str(sf_status s) {
   switch (s) {
     case SF_OK: return "ok";
@@ -1043,9 +1153,10 @@ const char* sf_status_str(sf_status s) {
 
 const char* sf_last_error(void) { return g_err.c_str(); }
 
-sf_status sf_create(const sf_model_cfg* tgt, const void* const* tgt_w, const sf_model_cfg* dft,
-                    const void* const* dft_w, int32_t batch, int32_t K, int32_t s_max, void* kv_t, void* kv_d,
-                    void* workspace, void* cuda_stream, sf_handle* out) {
+// n_pages 0: kv_t holds s_max slots per sequence; else it is a pool of pages.
+static sf_status create_engine(const sf_model_cfg* tgt, const void* const* tgt_w, const sf_model_cfg* dft,
+                               const void* const* dft_w, int32_t batch, int32_t K, int32_t s_max, int32_t n_pages,
+                               void* kv_t, void* kv_d, void* workspace, void* cuda_stream, sf_handle* out) {
   if (!out) return fail(SF_ERR_ARG, "out is null");
   *out = nullptr;
   std::string why;
@@ -1106,6 +1217,7 @@ sf_status sf_create(const sf_model_cfg* tgt, const void* const* tgt_w, const sf_
     const cudaError_t ge = gemm_init();   // before planning: cluster occupancy queries need it
     if (ge != cudaSuccess) return bail(fail(SF_ERR_CUDA, "gemm_init: %s", cudaGetErrorString(ge)));
   }
+  e->tgt.n_pages = n_pages;
   sf_status r = bind_model(e, e->tgt, tgt, tgt_w, static_cast<bf16*>(kv_t));
   if (r != SF_OK) return bail(r);
   if (dft && (r = bind_model(e, e->dft, dft, dft_w, static_cast<bf16*>(kv_d))) != SF_OK) return bail(r);
@@ -1156,6 +1268,32 @@ sf_status sf_create(const sf_model_cfg* tgt, const void* const* tgt_w, const sf_
   st.K = K;
   st.s_max = s_max;
   e->C.assign(batch, 0);
+  if (n_pages > 0) {
+    const PagedLayout pl = paged_layout(tgt, batch, s_max, n_pages);
+    unsigned char* pw = ws + e->lay.total;
+    e->pg_tables = reinterpret_cast<int*>(pw + pl.tables);
+    e->pg_held = reinterpret_cast<int*>(pw + pl.held);
+    e->pg_free = reinterpret_cast<int*>(pw + pl.free);
+    e->pg_n_free = reinterpret_cast<int*>(pw + pl.n_free);
+    e->pg_status = reinterpret_cast<int*>(pw + pl.status);
+    e->pg_slots = reinterpret_cast<int*>(pw + pl.slots);
+    e->pg_positions = reinterpret_cast<int*>(pw + pl.positions);
+    e->pg_mask = reinterpret_cast<unsigned long long*>(pw + pl.mask);
+    e->pg_attn = pw + pl.attn;
+    st.tables = e->pg_tables;
+    st.n_pages = n_pages;
+    // No sequence holds a page (their tables are all -1); the whole pool is
+    // free, page 0 on top.
+    std::vector<int> all(n_pages);
+    for (int i = 0; i < n_pages; ++i) all[i] = n_pages - 1 - i;
+    cudaError_t pe;
+    if ((pe = cudaMemsetAsync(pw, 0xff, pl.held, e->user)) ||
+        (pe = cudaMemsetAsync(pw + pl.held, 0, pl.free - pl.held, e->user)) ||
+        (pe = cudaMemcpyAsync(e->pg_free, all.data(), (size_t)n_pages * 4, cudaMemcpyHostToDevice, e->user)) ||
+        (pe = cudaMemcpyAsync(e->pg_n_free, &n_pages, 4, cudaMemcpyHostToDevice, e->user)) ||
+        (pe = cudaStreamSynchronize(e->user)))
+      return bail(fail(SF_ERR_CUDA, "page tables: %s", cudaGetErrorString(pe)));
+  }
 
   cudaError_t ce;
   if ((ce = attn_init()) != cudaSuccess) return bail(fail(SF_ERR_CUDA, "attn_init: %s", cudaGetErrorString(ce)));
@@ -1190,6 +1328,29 @@ sf_status sf_create(const sf_model_cfg* tgt, const void* const* tgt_w, const sf_
   return SF_OK;
 }
 
+sf_status sf_create(const sf_model_cfg* tgt, const void* const* tgt_w, const sf_model_cfg* dft,
+                    const void* const* dft_w, int32_t batch, int32_t K, int32_t s_max, void* kv_t, void* kv_d,
+                    void* workspace, void* cuda_stream, sf_handle* out) {
+  return create_engine(tgt, tgt_w, dft, dft_w, batch, K, s_max, 0, kv_t, kv_d, workspace, cuda_stream, out);
+}
+
+sf_status sf_create_paged(const sf_model_cfg* tgt, const void* const* tgt_w, const sf_model_cfg* dft,
+                          const void* const* dft_w, int32_t batch, int32_t K, int32_t s_max, int32_t n_pages,
+                          void* kv_pool, void* kv_d, void* workspace, void* cuda_stream, sf_handle* out) {
+  if (out) *out = nullptr;
+  if (n_pages < 1 || n_pages > (1 << 24)) return fail(SF_ERR_ARG, "n_pages must be in 1..2^24");
+  return create_engine(tgt, tgt_w, dft, dft_w, batch, K, s_max, n_pages, kv_pool, kv_d, workspace, cuda_stream, out);
+}
+
+sf_status sf_get_pages(sf_handle h, int32_t* h_held, int32_t* h_free) {
+  if (!h) return fail(SF_ERR_ARG, "null handle");
+  if (h->tgt.n_pages == 0) return fail(SF_ERR_STATE, "the engine's cache does not lie in pages");
+  if (h_held) CK(cudaMemcpyAsync(h_held, h->pg_held, h->B * sizeof(int), cudaMemcpyDeviceToHost, h->user));
+  if (h_free) CK(cudaMemcpyAsync(h_free, h->pg_n_free, sizeof(int), cudaMemcpyDeviceToHost, h->user));
+  CK(cudaStreamSynchronize(h->user));
+  return SF_OK;
+}
+
 void sf_destroy(sf_handle h) {
   if (!h) return;
   for (auto& g : h->graph)
@@ -1219,6 +1380,8 @@ sf_status sf_prefill(sf_handle h, const int32_t* h_tokens, const int32_t* h_lens
     }
     equal = equal && P == lens[0];
   }
+  if (!pages_fit(h, lens, h->K + 1))
+    return fail(SF_ERR_CAPACITY, "the prompts and a round need more than the pool's %d pages", h->tgt.n_pages);
   for (int b = 0; b < h->B; ++b)
     CK(cudaMemcpyAsync(h->st.hist + (size_t)b * h->s_max, h_tokens + (size_t)b * stride, lens[b] * sizeof(int),
                        cudaMemcpyHostToDevice, h->user));
@@ -1227,6 +1390,7 @@ sf_status sf_prefill(sf_handle h, const int32_t* h_tokens, const int32_t* h_lens
   // Fill the caches with prompt[0..P-1) in chunks of up to SF_MAX_ROWS rows:
   // all sequences side by side when the prompts have one length, else one
   // sequence at a time.
+  if (h->tgt.n_pages > 0) CK(plan_pages(h, h->zeros, 0, 0, -1, h->user));   // earlier prompts' pages go back
   for (Model* md : {&h->tgt, &h->dft}) {
     if (md == &h->dft && !h->has_dft) continue;
     if (equal) {
@@ -1312,6 +1476,7 @@ sf_status sf_draft(sf_handle h, int32_t* d_draft, float* d_logits) {
   if (h->phase != 1) return fail(SF_ERR_STATE, "sf_draft needs a prefilled engine between rounds");
   if (h->draft_stale) return fail(SF_ERR_STATE, "draft cache is behind after n-gram rounds; call sf_reset or sf_prefill");
   if (max_committed(h) + h->K + 1 > h->s_max) return fail(SF_ERR_CAPACITY, "round would exceed s_max");
+  if (!pages_fit(h, h->C, h->K + 1)) return fail(SF_ERR_CAPACITY, "round would exceed the pool's pages");
   sf_status r;
   if (!d_draft && !d_logits) {
     if ((r = build_graph(h, CAP_DRAFT)) != SF_OK) return r;
@@ -1332,6 +1497,7 @@ sf_status sf_ngram_draft(sf_handle h, int32_t max_guess, int32_t min_n, int32_t 
   if (max_guess < 1 || max_guess > h->K || min_n < 1 || max_n < min_n || max_n > 64)
     return fail(SF_ERR_ARG, "need 1 <= max_guess <= K and 1 <= min_n <= max_n <= 64");
   if (max_committed(h) + h->K + 1 > h->s_max) return fail(SF_ERR_CAPACITY, "round would exceed s_max");
+  if (!pages_fit(h, h->C, h->K + 1)) return fail(SF_ERR_CAPACITY, "round would exceed the pool's pages");
   CK(launch_ngram(h->st, max_guess, min_n, max_n, d_prop, d_count, h->user, false));
   h->phase = 2;
   h->drafted_mode = SF_DRAFT_NGRAM;
@@ -1345,6 +1511,7 @@ sf_status sf_tree_draft(sf_handle h, int32_t n_cand, int32_t min_n, int32_t max_
   if (n_cand < 1 || n_cand > h->K || min_n < 1 || max_n < min_n || max_n > 64)
     return fail(SF_ERR_ARG, "need 1 <= n_cand <= K and 1 <= min_n <= max_n <= 64");
   if (max_committed(h) + h->K + 1 > h->s_max) return fail(SF_ERR_CAPACITY, "round would exceed s_max");
+  if (!pages_fit(h, h->C, h->K + 1)) return fail(SF_ERR_CAPACITY, "round would exceed the pool's pages");
   CK(launch_ngram_tree(h->st, n_cand, h->K / n_cand, min_n, max_n, d_prop, d_len, h->user, false));
   h->phase = 2;
   h->drafted_mode = SF_DRAFT_TREE;
@@ -1411,6 +1578,7 @@ sf_status sf_step(sf_handle h, int32_t* h_n_committed, int32_t* h_committed) {
   if (mode == SF_DRAFT_NEURAL && h->draft_stale)
     return fail(SF_ERR_STATE, "draft cache is behind after n-gram rounds; call sf_reset or sf_prefill");
   if (max_committed(h) + h->K + 1 > h->s_max) return fail(SF_ERR_CAPACITY, "round would exceed s_max");
+  if (!pages_fit(h, h->C, h->K + 1)) return fail(SF_ERR_CAPACITY, "round would exceed the pool's pages");
   sf_status r = build_graph(h, mode);
   if (r != SF_OK) return r;
   CK(cudaGraphLaunch(h->graph[mode], h->user));
@@ -1440,13 +1608,16 @@ sf_status sf_generate(sf_handle h, int32_t n_new, int32_t* h_out, int32_t* h_rou
     // synchronises once at the end.
     if (gen_min() < n_new) {
       if (max_committed(h) + 2 * K1 > h->s_max) return fail(SF_ERR_CAPACITY, "s_max reached after %d new tokens", gen_min());
+      if (!pages_fit(h, h->C, 2 * K1))
+        return fail(SF_ERR_CAPACITY, "the pool's pages run out after %d new tokens", gen_min());
       if ((r = build_loop_graph(h, mode)) != SF_OK) return r;
       CK(launch_loop_init(h->st, n_new, h->user));
       CK(cudaGraphLaunch(h->loop[mode], h->user));
       if (mode != SF_DRAFT_NEURAL && h->has_dft) h->draft_stale = true;
       if ((r = sync_report(h)) != SF_OK) return r;
       rounds = h->pin[h->so.rounds - h->so.report];
-      if (gen_min() < n_new) return fail(SF_ERR_CAPACITY, "s_max reached after %d new tokens", gen_min());
+      if (gen_min() < n_new)
+        return fail(SF_ERR_CAPACITY, "s_max or the pool's pages reached after %d new tokens", gen_min());
     }
   } else {
     if ((r = build_graph(h, mode)) != SF_OK) return r;
@@ -1458,7 +1629,8 @@ sf_status sf_generate(sf_handle h, int32_t n_new, int32_t* h_out, int32_t* h_rou
       int R = (remaining + K1 - 1) / K1;
       const int room = (h->s_max - h->K - 1 - max_committed(h)) / K1;
       R = std::min(R, room);
-      if (R < 1) return fail(SF_ERR_CAPACITY, "s_max reached after %d new tokens", gen_min());
+      while (R > 0 && !pages_fit(h, h->C, R * K1)) --R;
+      if (R < 1) return fail(SF_ERR_CAPACITY, "s_max or the pool's pages reached after %d new tokens", gen_min());
       for (int i = 0; i < R; ++i) CK(cudaGraphLaunch(h->graph[mode], h->user));
       rounds += R;
       if (mode != SF_DRAFT_NEURAL && h->has_dft) h->draft_stale = true;

@@ -95,6 +95,18 @@ __device__ void epi_resid(const GemmArgs& a, float* ys, int rb, int m0, int M, i
   }
 }
 
+// Cache row (in head_dim-wide rows of kc or vc) of token row m of sequence b,
+// cache slot pos, KV head kvh; -1: the row has no slot (reported).
+__device__ __forceinline__ long cache_row(const GemmArgs& a, int m, int b, int pos, int kvh) {
+  if (!a.slots) return ((long)b * a.nkv + kvh) * a.s_max + pos;
+  const int slot = a.slots[m];
+  if (slot < 0) {
+    report_err(a.err, kErrCapacity);
+    return -1;
+  }
+  return ((long)(slot / kKvChunk) * a.nkv + kvh) * kKvChunk + slot % kKvChunk;
+}
+
 template <int T>
 __device__ void epi_qkv(const GemmArgs& a, const float* ys, int rb, int m0, int M, const EpiPre<T>& pre,
                         const int* spos) {
@@ -114,7 +126,8 @@ __device__ void epi_qkv(const GemmArgs& a, const float* ys, int rb, int m0, int 
     const int pos = spos[m];
     if (s == 2) {
       const int kvh = local / a.hd;
-      a.vc[(((size_t)b * a.nkv + kvh) * a.s_max + pos) * a.hd + d] = __float2bfloat16_rn(ys[i] + pre.v0[e]);
+      const long row = cache_row(a, m0 + m, b, pos, kvh);
+      if (row >= 0) a.vc[row * a.hd + d] = __float2bfloat16_rn(ys[i] + pre.v0[e]);
       continue;
     }
     if (d >= half) continue;
@@ -129,7 +142,9 @@ __device__ void epi_qkv(const GemmArgs& a, const float* ys, int rb, int m0, int 
       q[half] = y2;
     } else {
       const int kvh = local / a.hd;
-      bf16* kp = a.kc + (((size_t)b * a.nkv + kvh) * a.s_max + pos) * a.hd + d;
+      const long row = cache_row(a, m0 + m, b, pos, kvh);
+      if (row < 0) continue;
+      bf16* kp = a.kc + row * a.hd + d;
       kp[0] = __float2bfloat16_rn(y1);
       kp[half] = __float2bfloat16_rn(y2);
     }

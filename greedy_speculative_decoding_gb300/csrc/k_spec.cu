@@ -301,9 +301,17 @@ __global__ void k_tree_compact(const __grid_constant__ SpecState s, bf16* kv, in
     const int rest = i - kvsel * nkv * per_head;
     const int h = rest / per_head, rr = rest - h * per_head;
     const int row = rr / units, u = rr - row * units;
-    bf16* base = kv + ((((size_t)l * 2 + kvsel) * s.B + b) * nkv + h) * (size_t)s.s_max * hd;
-    const uint4 v = *reinterpret_cast<const uint4*>(base + (size_t)(C + c * g + row) * hd + 8 * u);
-    *reinterpret_cast<uint4*>(base + (size_t)(C + row) * hd + 8 * u) = v;
+    auto at = [&](int slot) {   // the entry of cache slot `slot`
+      size_t r;
+      if (s.tables) {   // pages of 64 slots
+        const int page = s.tables[(size_t)b * (s.s_max / kKvChunk) + slot / kKvChunk];
+        r = ((((size_t)l * 2 + kvsel) * s.n_pages + page) * nkv + h) * kKvChunk + slot % kKvChunk;
+      } else {
+        r = ((((size_t)l * 2 + kvsel) * s.B + b) * nkv + h) * (size_t)s.s_max + slot;
+      }
+      return reinterpret_cast<uint4*>(kv + r * hd + 8 * u);
+    };
+    *at(C + row) = *at(C + c * g + row);
   }
 }
 
@@ -325,7 +333,8 @@ cudaError_t launch_tree_compact(const SpecState& s, bf16* kv, int layers, int nk
 // round followed by k_loop_ctl. The control kernel counts the round and lets
 // the loop run again while some sequence has fewer than the target number of
 // new tokens, every sequence has room for two more rounds (so acceptance
-// never raises the capacity flag), no error bit is set, and fewer rounds than
+// never raises the capacity flag) and the target's pool, when its cache lies
+// in pages, has the pages for them, no error bit is set, and fewer rounds than
 // the target have run (each round commits at least one token per sequence,
 // so that bound never stops a loop that still has work).
 __global__ void k_loop_init(const __grid_constant__ SpecState s, int n_new) {
@@ -338,10 +347,13 @@ __global__ void k_loop_ctl(const __grid_constant__ SpecState s, cudaGraphConditi
   *s.rounds = r;
   const int target = *s.loop_target;
   bool need = false, room = true;
+  long pages = 0;   // of two more rounds
   for (int b = 0; b < s.B; ++b) {
     need = need || s.total[b] < target;
     room = room && s.len_t[b] + 1 + 2 * (s.K + 1) <= s.s_max;
+    pages += (s.len_t[b] + 2 * (s.K + 1) + kKvChunk - 1) / kKvChunk;
   }
+  if (s.n_pages > 0) room = room && pages <= s.n_pages;
   cudaGraphSetConditional(h, (need && room && *s.err == 0 && r < target) ? 1u : 0u);
 }
 

@@ -15,6 +15,45 @@ inline int log2_of(int x) {
   return s;
 }
 
+struct PlanArgs {
+  const int* lens;     // [B]; a request has lens[b] + len_add tokens
+  int len_add;
+  const int* starts;   // [B + 1] row starts, or null: rows_each rows each
+  int rows_each;
+  int* tables;         // [B][W]
+  const int* held;
+  int* free;
+  const int* n_free;
+  int* slots;
+  int* positions;
+  int* held_out;
+  int* n_free_out;
+  int* status;
+  int B, W, cap, shift, N;
+};
+cudaError_t launch_page_plan(const PlanArgs& a, cudaStream_t st);
+
+// The engine's attention over its target's pages: fp32 queries [M][nq * hd],
+// `rows` token rows of each of B sequences, the last of them at position
+// lens[b] + len_add - 1; the output goes where the output projection reads it.
+struct EngineAttn {
+  sf_paged_cache cache;
+  const float* q;
+  bf16* out;                 // fragment order, or the tensor-core operand order (umma)
+  int umma;
+  const int* tables;
+  int table_width;
+  const int* lens;
+  int len_add, B, rows, nq;
+  const unsigned long long* mask;   // [B * rows], or null: causal
+  float scale;
+  int* err;
+  void* workspace;
+};
+cudaError_t launch_engine_paged_attention(const EngineAttn& e, int num_sms, cudaStream_t st);
+// Row masks of a verify pass over candidate guesses of g tokens (see RowSet).
+cudaError_t launch_tree_mask(unsigned long long* mask, int B, int rows, int g, cudaStream_t st, bool pdl);
+
 // Checks a cache descriptor; on failure records the message and returns the status.
 sf_status check_cache(const sf_paged_cache* c, const char* who);
 

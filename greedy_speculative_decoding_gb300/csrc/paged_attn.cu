@@ -64,7 +64,107 @@ static cudaError_t cache_map(CUtensorMap* map, int* nhd, const sf_paged_cache& c
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+// Units of an item at most (its request fills its table), the query tile, and
+// the items of the whole call.
+struct Sizes {
+  long units, items;
+  int mt, ntq;
+};
+static Sizes sizes(const sf_paged_cache& c, int n_heads, int max_rows, int q_dtype, int batch, int table_width, int sms) {
+  Sizes z;
+  const int queries = max_rows * (n_heads / c.n_kv_heads);
+  z.units = std::max(1l, ((long)table_width * c.page + kTile - 1) / kTile);
+  auto items = [&](int mt) { return (long)batch * c.n_kv_heads * ((queries + mt - 1) / mt); };
+  // A smaller tile where the larger one's units could not occupy the GPU even
+  // if every request filled its table: the cache is then read once for each
+  // tile (from L2), by CTAs that would be idle.
+  z.mt = tile_of(queries, q_dtype == SF_DT_F32);
+  while (z.mt > 16 && items(z.mt) * z.units < 2 * sms) z.mt /= 2;
+  z.ntq = (queries + z.mt - 1) / z.mt;
+  z.items = items(z.mt);
+  return z;
+}
+// The kernel counts a request's units in 32 bits.
+static bool units_fit(const sf_paged_cache& c, int n_heads, int max_rows, int q_dtype, int batch, int table_width,
+                      int sms) {
+  const Sizes z = sizes(c, n_heads, max_rows, q_dtype, batch, table_width, sms);
+  return c.n_kv_heads * (long)z.ntq * z.units <= INT32_MAX;
+}
+
+// Enqueue a checked call: `a` holds rows, tables and lengths.
+static cudaError_t enqueue(Args& a, const sf_paged_cache& c, int q_dtype, float scale, void* workspace, int sms,
+                           cudaStream_t st) {
+  cudaError_t e = cache_map(&a.km, &a.k_nhd, c, c.k, c.k_page, c.k_head, c.k_slot);
+  if (e == cudaSuccess) e = cache_map(&a.vm, &a.v_nhd, c, c.v, c.v_page, c.v_head, c.v_slot);
+  if (e != cudaSuccess) return e;
+  a.nkv = c.n_kv_heads;
+  a.group = a.nq / a.nkv;
+  a.shift = log2_of(c.page);
+  // (never 0: the mask's -infinity times 0 would be NaN)
+  a.scale2 = std::max(std::fabs(scale) * 1.44269504088896f, FLT_TRUE_MIN);
+  a.flip = scale >= 0.f ? 0u : q_dtype == SF_DT_F32 ? 0x80000000u : 0x80008000u;
+  const Sizes z = sizes(c, a.nq, a.max_rows, q_dtype, a.B, a.W, sms);
+  a.mt = z.mt;
+  a.mt_max = std::min(a.max_rows * a.group, a.mt);
+  a.ntq_max = z.ntq;
+  a.by_item = z.items <= kMaxDesc;
+  const Layout lay = layout(a.nq, a.nkv, c.head_dim, a.max_rows);
+  unsigned char* ws = static_cast<unsigned char*>(workspace);
+  a.desc = reinterpret_cast<int4*>(ws);
+  a.part_ml = reinterpret_cast<float2*>(ws + lay.ml);
+  a.part = reinterpret_cast<float*>(ws + lay.part);
+  const long max_units = z.items * z.units;
+  a.by_warp = a.B <= 32 * kChunks && max_units <= INT32_MAX;
+  sms = std::min(sms, kMaxCtas / 2);
+  return c.head_dim == 128 ? launch_hd128(a, q_dtype, sms, max_units, st) : launch_hd64(a, q_dtype, sms, max_units, st);
+}
+
+__global__ void k_tree_mask(unsigned long long* mask, int n, int rows, int g) {
+  pdl_wait();
+  pdl_launch_next();
+  const int i = blockIdx.x * blockDim.x + threadIdx.x;
+  if (i >= n) return;
+  const int j = i % rows;
+  unsigned long long m = 1;   // row 0; of candidate (j - 1) / g, the rows up to this one
+  for (int r = j - (j > 0 ? (j - 1) % g : 0); r <= j; ++r) m |= 1ull << r;
+  mask[i] = m;
+}
+
 }  // namespace pa
+
+cudaError_t launch_engine_paged_attention(const EngineAttn& e, int num_sms, cudaStream_t st) {
+  pa::Args a{};
+  a.q = e.q;
+  a.q_row = (long)e.nq * e.cache.head_dim;
+  a.q_head = e.cache.head_dim;
+  a.frag = e.out;
+  a.frag_umma = e.umma;
+  a.err = e.err;
+  a.tables = e.tables;
+  a.W = e.table_width;
+  a.lens = e.lens;
+  a.len_add = e.len_add;
+  a.mask = e.mask;
+  a.B = e.B;
+  a.N = e.B * e.rows;
+  a.nq = e.nq;
+  a.max_rows = a.rows_each = e.rows;
+  return pa::enqueue(a, e.cache, SF_DT_F32, e.scale, e.workspace, num_sms, st);
+}
+
+cudaError_t launch_tree_mask(unsigned long long* mask, int B, int rows, int g, cudaStream_t st, bool pdl) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((B * rows + 127) / 128);
+  cfg.blockDim = dim3(128);
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, pa::k_tree_mask, mask, B * rows, rows, g);
+}
+
 }  // namespace sf
 
 using namespace sf;
@@ -105,48 +205,19 @@ extern "C" sf_status sf_paged_attention(const sf_paged_cache* cache, const sf_ro
         (r->n_heads > 1 && r->head % al))
       return set_error(SF_ERR_ARG, "sf_paged_attention: q and out must be 16-byte aligned with strides of multiples of 16 bytes");
   if (!std::isfinite(scale)) return set_error(SF_ERR_ARG, "sf_paged_attention: scale must be finite");
-  pa::Args a{};
-  cudaError_t e = pa::cache_map(&a.km, &a.k_nhd, *cache, cache->k, cache->k_page, cache->k_head, cache->k_slot);
-  if (e == cudaSuccess) e = pa::cache_map(&a.vm, &a.v_nhd, *cache, cache->v, cache->v_page, cache->v_head, cache->v_slot);
   int dev = 0, sms = 0;
-  if (e == cudaSuccess) e = cudaGetDevice(&dev);
+  cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e != cudaSuccess) return set_error(SF_ERR_CUDA, "sf_paged_attention: %s", cudaGetErrorString(e));
+  pa::Args a{};
   a.q = q->data, a.q_row = q->row, a.q_head = q->head;
   a.out = out->data, a.o_row = out->row, a.o_head = out->head;
   a.lse = d_lse;
   a.tables = d_tables, a.lens = d_lens, a.starts = d_starts;
   a.mask = reinterpret_cast<const unsigned long long*>(d_mask);
-  a.B = batch, a.N = n, a.W = table_width, a.nq = q->n_heads, a.nkv = cache->n_kv_heads;
-  a.group = q->n_heads / cache->n_kv_heads;
-  a.shift = log2_of(cache->page), a.max_rows = max_rows, a.rows_each = n / batch;
-  // (never 0: the mask's -infinity times 0 would be NaN)
-  a.scale2 = std::max(std::fabs(scale) * 1.44269504088896f, FLT_TRUE_MIN);
-  a.flip = scale >= 0.f ? 0u : q->dtype == SF_DT_F32 ? 0x80000000u : 0x80008000u;
-  // A smaller tile where the larger one's units could not occupy the GPU even
-  // if every request filled its table: the cache is then read once for each
-  // tile (from L2), by CTAs that would be idle.
-  const int queries = max_rows * a.group;
-  const long units = ((long)table_width * cache->page + pa::kTile - 1) / pa::kTile;   // of an item, at most
-  auto items = [&](int mt) { return (long)batch * a.nkv * ((queries + mt - 1) / mt); };
-  a.mt = pa::tile_of(queries, q->dtype == SF_DT_F32);
-  while (a.mt > 16 && items(a.mt) * units < 2 * sms) a.mt /= 2;
-  a.mt_max = std::min(queries, a.mt);
-  a.ntq_max = (queries + a.mt - 1) / a.mt;
-  a.by_item = items(a.mt) <= pa::kMaxDesc;
-  if (a.nkv * (long)a.ntq_max * units > INT32_MAX)
+  a.B = batch, a.N = n, a.W = table_width, a.nq = q->n_heads, a.max_rows = max_rows, a.rows_each = n / batch;
+  if (!pa::units_fit(*cache, q->n_heads, max_rows, q->dtype, batch, table_width, sms))
     return set_error(SF_ERR_UNSUPPORTED, "sf_paged_attention: table_width * page too large for this many heads and rows");
-  const pa::Layout lay = pa::layout(q->n_heads, cache->n_kv_heads, cache->head_dim, max_rows);
-  unsigned char* ws = static_cast<unsigned char*>(d_workspace);
-  a.desc = reinterpret_cast<int4*>(ws);
-  a.part_ml = reinterpret_cast<float2*>(ws + lay.ml);
-  a.part = reinterpret_cast<float*>(ws + lay.part);
-  const long max_units = items(a.mt) * units;
-  a.by_warp = batch <= 32 * pa::kChunks && max_units <= INT32_MAX;
-  sms = std::min(sms, pa::kMaxCtas / 2);
-  cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
-  e = cache->head_dim == 128 ? pa::launch_hd128(a, q->dtype, sms, max_units, st)
-                             : pa::launch_hd64(a, q->dtype, sms, max_units, st);
+  if (e == cudaSuccess) e = pa::enqueue(a, *cache, q->dtype, scale, d_workspace, sms, static_cast<cudaStream_t>(cuda_stream));
   if (e != cudaSuccess) return set_error(SF_ERR_CUDA, "sf_paged_attention: %s", cudaGetErrorString(e));
   return SF_OK;
 }

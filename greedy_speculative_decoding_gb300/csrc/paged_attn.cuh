@@ -43,7 +43,7 @@ struct Args {
   float* lse;
   const int *tables, *lens, *starts;
   const unsigned long long* mask;
-  int B, N, W, nq, nkv, group, shift, max_rows, rows_each;
+  int B, N, W, nq, nkv, group, shift, max_rows, rows_each, len_add;
   float scale2;            // |scale| * log2(e)
   uint32_t flip;           // sign bits that turn q into -q where scale is negative, or 0
   int mt;                  // queries of a tile (MT)
@@ -55,6 +55,9 @@ struct Args {
   int4* desc;              // {first CTA, CTAs, request, KV head * ntq + query tile}
   float* part;             // [CTA][2][mt_max][HD]: output parts (0: of an item begun before, 1: begun here)
   float2* part_ml;         // [CTA][2][mt_max]: (maximum, sum)
+  bf16* frag;              // fp32 queries: the output in a projection's operand order instead of rows (act_store)
+  int frag_umma;
+  int* err;                // status word, or null
 };
 
 // A request as the kernel sees it: whatever lens and starts hold, rows lie in
@@ -74,7 +77,7 @@ __device__ __forceinline__ Request request(const Args& a, int b) {
     r.s0 = b * a.rows_each;
     rows = a.rows_each;
   }
-  r.len = (int)min((long)max(a.lens[b], 0), (long)a.W << a.shift);
+  r.len = (int)min((long)max(a.lens[b] + a.len_add, 0), (long)a.W << a.shift);
   r.p0 = r.len - rows;
   r.rows = (r.s0 < 0 || r.s0 >= a.N) ? 0 : max(0, min(min(rows, a.max_rows), a.N - r.s0));
   r.nt = r.rows > 0 ? max(1, (r.len + kTile - 1) / kTile) : 0;
@@ -332,6 +335,20 @@ __device__ __forceinline__ void store2(TQ* p, float x, float y) {
 template <>
 __device__ __forceinline__ void store2<float>(float* p, float x, float y) {
   *reinterpret_cast<float2*>(p) = make_float2(x, y);
+}
+
+// Two neighbouring elements of row `row`, head `head` of the output.
+template <int HD, typename TQ>
+__device__ __forceinline__ void put2(const Args& a, int row, int head, int d, float x, float y) {
+  if constexpr (std::is_same<TQ, float>::value) {
+    if (a.frag) {
+      const int T = (a.N + 3) / 4;
+      act_store(a.frag, row, head * HD + d, T, x, a.frag_umma);
+      act_store(a.frag, row, head * HD + d + 1, T, y, a.frag_umma);
+      return;
+    }
+  }
+  store2<TQ>(static_cast<TQ*>(a.out) + row * a.o_row + head * a.o_head + d, x, y);
 }
 
 // TC: the cache's type. F32: fp32 queries and output over a bf16 cache, the
@@ -737,9 +754,9 @@ __global__ void __launch_bounds__(Shape<HD, WM, WK, F32>::kThreads, Shape<HD, WM
         if (whole) {
           const int jj = q / a.group, hh = w.kvh * a.group + q - jj * a.group;
           const float inv = l[e] == 0.f ? 0.f : 1.f / l[e];
-          TQ* dst = static_cast<TQ*>(a.out) + (r.s0 + jj) * a.o_row + hh * a.o_head + 2 * c4;
 #pragma unroll
-          for (int d = 0; d < ND; ++d) store2<TQ>(dst + 8 * d, o[d][2 * e] * inv, o[d][2 * e + 1] * inv);
+          for (int d = 0; d < ND; ++d)
+            put2<HD, TQ>(a, r.s0 + jj, hh, 8 * d + 2 * c4, o[d][2 * e] * inv, o[d][2 * e + 1] * inv);
           if (a.lse && c4 == 0)
             a.lse[(long)(r.s0 + jj) * a.nq + hh] = l[e] == 0.f ? -INFINITY : m[e] * kLn2 + logf(l[e]);
         } else {
@@ -790,9 +807,8 @@ __global__ void __launch_bounds__(Shape<HD, WM, WK, F32>::kThreads, Shape<HD, WM
         if (whole) {
           const int jj = q / a.group, hh = w.kvh * a.group + q - jj * a.group;
           const float inv = ll == 0.f ? 0.f : 1.f / ll;
-          TQ* dst = static_cast<TQ*>(a.out) + (r.s0 + jj) * a.o_row + hh * a.o_head + d;
-          store2<TQ>(dst, v.x * inv, v.y * inv);
-          store2<TQ>(dst + 2, v.z * inv, v.w * inv);
+          put2<HD, TQ>(a, r.s0 + jj, hh, d, v.x * inv, v.y * inv);
+          put2<HD, TQ>(a, r.s0 + jj, hh, d + 2, v.z * inv, v.w * inv);
           if (a.lse && d == 0) a.lse[(long)(r.s0 + jj) * a.nq + hh] = ll == 0.f ? -INFINITY : mm * kLn2 + logf(ll);
         } else {
           *reinterpret_cast<float4*>(part + x * HD + d) = v;
@@ -802,6 +818,7 @@ __global__ void __launch_bounds__(Shape<HD, WM, WK, F32>::kThreads, Shape<HD, WM
       cta_sync();   // the region is free again
     }
   }
+  if (!ok && lane == 0) report_err(a.err, kErrWait);
   // No item begins here that others share (descriptors by CTA).
   if (!a.by_item && tid == 0) {
     const bool shared = u1 < st.T && [&] {
@@ -833,9 +850,9 @@ __global__ void __launch_bounds__(kJoinThreads) k_paged_join(const __grid_consta
     kvh = i / a.ntq_max;
     qt = i - kvh * a.ntq_max;
     r = request<MT>(a, b);
-    if (qt * MT + x >= r.rows * a.group) return;   // (all of a wide join's CTA)
   }
-  pdl_wait();
+  pdl_wait();   // (before any return: what follows the join relies on the main kernel's end as well)
+  if (a.by_item && qt * MT + x >= r.rows * a.group) return;   // (all of a wide join's CTA)
   const int4 d = a.desc[blockIdx.x];
   if (d.y < 2) return;
   if (!a.by_item) {
@@ -908,9 +925,8 @@ __global__ void __launch_bounds__(kJoinThreads) k_paged_join(const __grid_consta
   }
   const int jj = q / a.group, hh = kvh * a.group + q - jj * a.group;
   const float inv = l == 0.f ? 0.f : 1.f / l;
-  TQ* dst = static_cast<TQ*>(a.out) + (r.s0 + jj) * a.o_row + hh * a.o_head + V * lane;
-  store2<TQ>(dst, o[0] * inv, o[1] * inv);
-  if constexpr (V == 4) store2<TQ>(dst + 2, o[2] * inv, o[3] * inv);
+  put2<HD, TQ>(a, r.s0 + jj, hh, V * lane, o[0] * inv, o[1] * inv);
+  if constexpr (V == 4) put2<HD, TQ>(a, r.s0 + jj, hh, V * lane + 2, o[2] * inv, o[3] * inv);
   if (a.lse && lane == 0) a.lse[(long)(r.s0 + jj) * a.nq + hh] = l == 0.f ? -INFINITY : m * 0.693147180559945f + logf(l);
 }
 

@@ -18,6 +18,10 @@
 namespace sf {
 namespace {
 
+// Tokens and first row of a request (starts null: rows_each rows each).
+__device__ __forceinline__ int plan_len(const PlanArgs& a, int b) { return a.lens[b] + a.len_add; }
+__device__ __forceinline__ int plan_start(const PlanArgs& a, int b) { return a.starts ? a.starts[b] : b * a.rows_each; }
+
 constexpr int kPlanThreads = 1024;   // of a CTA, at most
 constexpr int kPlanCluster = 8;      // CTAs of a pass with many pieces
 // From 64 requests or 1024 rows the pieces (a finished request gives back all
@@ -30,21 +34,6 @@ constexpr int kPlanClusterRequests = 64, kPlanClusterRows = 1024;
 // 512000 rows 66 and 9.8 us.
 constexpr int kPlanManyRows = 32768;
 constexpr int kRowThreads = 256, kRowCtas = 608;
-
-struct PlanArgs {
-  const int* lens;
-  const int* starts;
-  int* tables;
-  const int* held;
-  int* free;
-  const int* n_free;
-  int* slots;
-  int* positions;
-  int* held_out;
-  int* n_free_out;
-  int* status;
-  int B, W, cap, shift, N;
-};
 
 // Sums that stop at `most` (at most 2^28, so that two of them fit an int).
 __device__ __forceinline__ int add_to(int a, int b, int most) { return min(a + b, most); }
@@ -108,9 +97,9 @@ __global__ void __launch_bounds__(kPlanThreads) k_page_plan(const PlanArgs a) {
     const int b = b0 + tid;
     int back = 0, want = 0, held = 0, need = 0, len = -1;
     if (b < a.B) {
-      const int s = a.starts[b], rows = a.starts[b + 1] - s;
+      const int s = plan_start(a, b), rows = plan_start(a, b + 1) - s;
       held = a.held[b];
-      len = a.lens[b];
+      len = plan_len(a, b);
       need = (int)(((long long)len + (1 << a.shift) - 1) >> a.shift);
       const bool bad = len < 0 || need > a.W || rows > len || held < 0 || held > a.W;
       if (bad) {
@@ -208,7 +197,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_page_plan(const PlanArgs a) {
 // and one or two pages, mostly), CTAs a stretch of rows each.
 __global__ void __launch_bounds__(kRowThreads) k_plan_rows(const PlanArgs a) {
   extern __shared__ int s_start[];   // [B + 1]
-  for (int b = threadIdx.x; b <= a.B; b += kRowThreads) s_start[b] = a.starts[b];
+  for (int b = threadIdx.x; b <= a.B; b += kRowThreads) s_start[b] = plan_start(a, b);
   const int p2 = a.B > 1 ? 1 << (31 - __clz(a.B)) : 1;
   const bool vec = ((reinterpret_cast<uintptr_t>(a.slots) | reinterpret_cast<uintptr_t>(a.positions)) & 15) == 0;
   const long quads = ((long)a.N + 3) / 4;
@@ -219,7 +208,7 @@ __global__ void __launch_bounds__(kRowThreads) k_plan_rows(const PlanArgs a) {
     const int i0 = 4 * (int)q;
     // The request that holds the row, kept while the next rows are its own.
     int b = i0 >= s_start[0] ? min(last_at_most(s_start, a.B, p2, i0), a.B - 1) : 0;
-    int first = s_start[b], end = s_start[b + 1], len = a.status[b] ? -1 : a.lens[b], known = -1, page = 0;
+    int first = s_start[b], end = s_start[b + 1], len = a.status[b] ? -1 : plan_len(a, b), known = -1, page = 0;
     int slot[4], pos[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -230,7 +219,7 @@ __global__ void __launch_bounds__(kRowThreads) k_plan_rows(const PlanArgs a) {
         ++b;
         first = end;
         end = s_start[b + 1];
-        len = a.status[b] ? -1 : a.lens[b];
+        len = a.status[b] ? -1 : plan_len(a, b);
         known = -1;
       }
       const int x = len - (end - i);
@@ -259,6 +248,46 @@ __global__ void __launch_bounds__(kRowThreads) k_plan_rows(const PlanArgs a) {
 size_t plan_smem_bytes(int B) { return (size_t)(3 * (B + 1) + 3 * B) * sizeof(int); }
 
 }  // namespace
+
+cudaError_t launch_page_plan(const PlanArgs& a, cudaStream_t st) {
+  static std::atomic<uint64_t> ready{0};   // devices whose shared-memory limit for the kernel is set
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess && (dev >= 64 || !(ready.load(std::memory_order_relaxed) >> dev & 1))) {
+    e = cudaFuncSetAttribute(k_page_plan, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)plan_smem_bytes(kMaxPlanBatch));
+    if (e == cudaSuccess && dev < 64) ready.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
+  }
+  if (e == cudaSuccess) {
+    const bool apart = a.N >= kPlanManyRows;
+    const int ctas = a.B >= kPlanClusterRequests || a.N >= kPlanClusterRows ? kPlanCluster : 1;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = ctas;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(ctas > 1 ? kPlanThreads : std::max(128, (std::max(a.B, a.N) + 31) / 32 * 32));
+    cfg.dynamicSmemBytes = plan_smem_bytes(a.B);
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = ctas > 1 ? 1 : 0;
+    PlanArgs plan = a;
+    if (apart) plan.N = 0;
+    e = cudaLaunchKernelEx(&cfg, k_page_plan, plan);
+    if (e == cudaSuccess && apart) {
+      attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+      attr[0].val.programmaticStreamSerializationAllowed = 1;
+      cfg.gridDim = dim3(kRowCtas);
+      cfg.blockDim = dim3(kRowThreads);
+      cfg.dynamicSmemBytes = (size_t)(a.B + 1) * sizeof(int);
+      cfg.numAttrs = 1;
+      e = cudaLaunchKernelEx(&cfg, k_plan_rows, a);
+    }
+  }
+  return e;
+}
+
 }  // namespace sf
 
 using namespace sf;
@@ -277,43 +306,12 @@ extern "C" sf_status sf_page_plan(const int32_t* d_lens, const int32_t* d_starts
     return set_error(SF_ERR_ARG, "sf_page_plan: need 1 <= table_width <= 2^30 / page, 1 <= capacity, capacity * page < 2^31");
   if (n_rows < 0 || (n_rows > 0 && (!d_slots || !d_positions)))
     return set_error(SF_ERR_ARG, "sf_page_plan: n_rows negative, or rows without slots and positions");
-  const PlanArgs a{d_lens,      d_starts,   d_tables,     d_held,   d_free, d_n_free,    d_slots,  d_positions,
-                   d_held_out, d_n_free_out, d_status, batch,  table_width, capacity, log2_of(page), n_rows};
-  static std::atomic<uint64_t> ready{0};   // devices whose shared-memory limit for the kernel is set
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess && (dev >= 64 || !(ready.load(std::memory_order_relaxed) >> dev & 1))) {
-    e = cudaFuncSetAttribute(k_page_plan, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)plan_smem_bytes(kMaxPlanBatch));
-    if (e == cudaSuccess && dev < 64) ready.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
-  }
-  if (e == cudaSuccess) {
-    const bool apart = n_rows >= kPlanManyRows;
-    const int ctas = batch >= kPlanClusterRequests || n_rows >= kPlanClusterRows ? kPlanCluster : 1;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = ctas;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(ctas);
-    cfg.blockDim = dim3(ctas > 1 ? kPlanThreads : std::max(128, (std::max(batch, n_rows) + 31) / 32 * 32));
-    cfg.dynamicSmemBytes = plan_smem_bytes(batch);
-    cfg.stream = static_cast<cudaStream_t>(cuda_stream);
-    cfg.attrs = attr;
-    cfg.numAttrs = ctas > 1 ? 1 : 0;
-    PlanArgs plan = a;
-    if (apart) plan.N = 0;
-    e = cudaLaunchKernelEx(&cfg, k_page_plan, plan);
-    if (e == cudaSuccess && apart) {
-      attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-      attr[0].val.programmaticStreamSerializationAllowed = 1;
-      cfg.gridDim = dim3(kRowCtas);
-      cfg.blockDim = dim3(kRowThreads);
-      cfg.dynamicSmemBytes = (size_t)(batch + 1) * sizeof(int);
-      cfg.numAttrs = 1;
-      e = cudaLaunchKernelEx(&cfg, k_plan_rows, a);
-    }
-  }
+  PlanArgs a{};
+  a.lens = d_lens, a.starts = d_starts, a.tables = d_tables, a.held = d_held, a.free = d_free, a.n_free = d_n_free;
+  a.slots = d_slots, a.positions = d_positions, a.held_out = d_held_out, a.n_free_out = d_n_free_out;
+  a.status = d_status;
+  a.B = batch, a.W = table_width, a.cap = capacity, a.shift = log2_of(page), a.N = n_rows;
+  const cudaError_t e = launch_page_plan(a, static_cast<cudaStream_t>(cuda_stream));
   if (e != cudaSuccess) return set_error(SF_ERR_CUDA, "sf_page_plan: %s", cudaGetErrorString(e));
   return SF_OK;
 }

@@ -52,6 +52,7 @@ struct GemmArgs {
   int q_dim, kv_dim, hd, nkv, s_max;
   bf16* kc;                   // this layer's key cache [B][nkv][s_max][hd]
   bf16* vc;
+  const int* slots;           // QKV over pages of 64 slots: row m's slot in kc / vc [pages][nkv][64][hd]; else null
   const float2* rope;         // [s_max][hd/2] (cos, sin)
   unsigned long long* keys;   // ARGMAX: [kRows] packed (value, index)
   int* done;                  // ARGMAX: finished-block counter
@@ -200,6 +201,8 @@ struct SpecState {
   int* rounds;      // device-resident loop: rounds run by the current sf_generate
   int* clen;        // [B][K] multi-candidate draft: tokens of each candidate guess (0: none)
   int* tree_c;      // [B] multi-candidate draft: the candidate the last round took
+  const int* tables;   // target cache in pages: [B][s_max / 64] page numbers; else null
+  int n_pages;         // pages of the target's pool (0: no pages)
   int B, K, s_max;
 };
 

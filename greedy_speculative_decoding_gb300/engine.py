@@ -100,24 +100,31 @@ class SpecEngine:
     Weight dicts map the canonical names (embed, layers.i.*, norm, lm_head)
     to CUDA tensors that must outlive the engine: bf16, fp32 (every tensor),
     or bf16 with NF4 codes + scales for the linear maps.
+
+    pages: the target's cache as a pool of that many pages of 64 slots which
+    the sequences share (sf_create_paged), instead of s_max slots for each.
     """
 
     def __init__(self, target_shape, target_w: dict, draft_shape=None, draft_w=None, batch: int = 1,
-                 K: int = 8, s_max: int = 4096, stream=None):
+                 K: int = 8, s_max: int = 4096, stream=None, pages: int = None):
         self.lib = L.load()
-        self.B, self.K, self.s_max = batch, K, s_max
+        self.B, self.K, self.s_max, self.pages = batch, K, s_max, pages
         self.target_shape, self.draft_shape = target_shape, draft_shape
         self.tc = model_cfg(target_shape, wdtype_of(target_w))
         self.dc = None
         if draft_shape is not None:
             self.dc = model_cfg(draft_shape, wdtype_of(draft_w))
         pdc = ctypes.byref(self.dc) if self.dc is not None else None
-        ws = self.lib.sf_workspace_bytes(ctypes.byref(self.tc), pdc, batch, K, s_max)
+        if pages is None:
+            ws = self.lib.sf_workspace_bytes(ctypes.byref(self.tc), pdc, batch, K, s_max)
+            kv = self.lib.sf_kv_bytes(ctypes.byref(self.tc), batch, s_max)
+        else:
+            ws = self.lib.sf_paged_engine_workspace_bytes(ctypes.byref(self.tc), pdc, batch, K, s_max, pages)
+            kv = self.lib.sf_kv_pool_bytes(ctypes.byref(self.tc), pages)
         if ws == 0:
             raise L.SFError(L.SF_ERR_ARG, "sf_workspace_bytes rejected the configuration")
         dev = torch.device("cuda", torch.cuda.current_device())
-        self.kv_t = torch.empty(self.lib.sf_kv_bytes(ctypes.byref(self.tc), batch, s_max), dtype=torch.uint8,
-                                device=dev)
+        self.kv_t = torch.empty(kv, dtype=torch.uint8, device=dev)
         self.kv_d = None
         if self.dc is not None:
             self.kv_d = torch.empty(self.lib.sf_kv_bytes(ctypes.byref(self.dc), batch, s_max),
@@ -129,9 +136,12 @@ class SpecEngine:
             dw, self._keep_d = _ptr_array(draft_shape, draft_w)
         self.stream = stream if stream is not None else torch.cuda.current_stream()
         h = ctypes.c_void_p()
-        L.check(self.lib.sf_create(ctypes.byref(self.tc), tw, pdc, dw, batch, K, s_max,
-                                   self.kv_t.data_ptr(), None if self.kv_d is None else self.kv_d.data_ptr(),
-                                   self.ws.data_ptr(), ctypes.c_void_p(self.stream.cuda_stream), ctypes.byref(h)))
+        buffers = (self.kv_t.data_ptr(), None if self.kv_d is None else self.kv_d.data_ptr(), self.ws.data_ptr(),
+                   ctypes.c_void_p(self.stream.cuda_stream), ctypes.byref(h))
+        if pages is None:
+            L.check(self.lib.sf_create(ctypes.byref(self.tc), tw, pdc, dw, batch, K, s_max, *buffers))
+        else:
+            L.check(self.lib.sf_create_paged(ctypes.byref(self.tc), tw, pdc, dw, batch, K, s_max, pages, *buffers))
         self.h = h
         self._tw, self._dw = tw, dw
 
@@ -252,10 +262,20 @@ class SpecEngine:
             out.append((self.lib.sf_trace_label(self.h, j).decode(), buf[2 * j], buf[2 * j + 1]))
         return out
 
+    def pages_held(self):
+        """(pages held by each sequence, free pages) of an engine with pages."""
+        held, free = np.zeros(self.B, np.int32), np.zeros(1, np.int32)
+        L.check(self.lib.sf_get_pages(self.h, _i32(held), _i32(free)))
+        return held, int(free[0])
+
     # ------------------------------------------------------------ views
     def kv_view(self, which: str = "target") -> torch.Tensor:
-        """[layers][2][batch][n_kv_heads][s_max][head_dim] bf16 view of a cache."""
+        """[layers][2][batch][n_kv_heads][s_max][head_dim] bf16 view of a cache;
+        [layers][2][pages][n_kv_heads][64][head_dim] of a target cache in pages."""
         shape = self.target_shape if which == "target" else self.draft_shape
+        if which == "target" and self.pages is not None:
+            return self.kv_t.view(torch.bfloat16).view(shape.layers, 2, self.pages, shape.n_kv_heads, 64,
+                                                       shape.head_dim)
         buf = self.kv_t if which == "target" else self.kv_d
         return buf.view(torch.bfloat16).view(shape.layers, 2, self.B, shape.n_kv_heads, self.s_max,
                                               shape.head_dim)

@@ -148,6 +148,32 @@ SF_API sf_status sf_create(const sf_model_cfg* tgt, const void* const* tgt_w,
                     sf_handle* out);
 
 /*
+ * The same engine with the target's cache in pages: kv_pool is a pool of
+ * n_pages (1..2^24) pages of 64 slots, layout [layers][2 (k, v)][n_pages]
+ * [n_kv_heads][64][head_dim] bf16, that the sequences share. Each holds the
+ * pages of the tokens it has and of the round under way instead of s_max
+ * slots: every target pass begins with a page plan (sf_page_plan below) on the
+ * device that takes the pages its rows need and gives back those that the last
+ * rewind left behind, and attends over the pages (sf_paged_attention below).
+ * The draft model's cache stays s_max slots per sequence. s_max is the most
+ * tokens of a sequence. Calls that need more pages than the pool has return
+ * SF_ERR_CAPACITY like those that pass s_max. workspace:
+ * sf_paged_engine_workspace_bytes(...) bytes. SF_PERSISTENT applies to the
+ * draft model only, and the timeline (sf_trace) leaves the target's attention
+ * out. sf_get_pages: pages held per sequence (host [batch]) and free pages
+ * (host [1]), each may be NULL.
+ */
+SF_API size_t sf_kv_pool_bytes(const sf_model_cfg* cfg, int32_t n_pages);
+SF_API size_t sf_paged_engine_workspace_bytes(const sf_model_cfg* tgt, const sf_model_cfg* dft, int32_t batch,
+                                              int32_t K, int32_t s_max, int32_t n_pages);
+SF_API sf_status sf_create_paged(const sf_model_cfg* tgt, const void* const* tgt_w,
+                    const sf_model_cfg* dft, const void* const* dft_w,
+                    int32_t batch, int32_t K, int32_t s_max, int32_t n_pages,
+                    void* kv_pool, void* kv_d, void* workspace, void* cuda_stream,
+                    sf_handle* out);
+SF_API sf_status sf_get_pages(sf_handle h, int32_t* h_held, int32_t* h_free);
+
+/*
  * Load prompts and fill both caches (the step before the speculative loop;
  * "Qwen3.5-397B on 20 GPUs", "What made it faster": prompts go through in
  * pieces). h_tokens: host [batch][stride] int32,
