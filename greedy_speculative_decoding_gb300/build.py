@@ -3,8 +3,9 @@
 Usage: python -m greedy_speculative_decoding_gb300.build [--force]
 
 Each .cu file under csrc/ is compiled in parallel, then linked into
-libsf.so next to this file. A stamp of the sources and flags skips the build
-when nothing changed.
+libsf.so next to this file; the paged operators' Python binding
+(csrc/paged_py.c) becomes the extension module _paged beside it. A stamp of
+the sources and flags skips the build when nothing changed.
 """
 
 import concurrent.futures as cf
@@ -13,11 +14,13 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 OUT = os.path.join(HERE, "libsf.so")
+PY_OUT = os.path.join(HERE, "_paged" + sysconfig.get_config_var("EXT_SUFFIX"))
 BUILD_DIR = os.path.join(HERE, "_build")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
@@ -38,7 +41,7 @@ def _sources():
 def _stamp(srcs) -> str:
     h = hashlib.sha256()
     h.update(" ".join(ARCH + FLAGS).encode())
-    for f in sorted(os.listdir(CSRC)) + [os.path.join(INCLUDE, "sf.h")]:
+    for f in sorted(os.listdir(CSRC)) + [os.path.join(INCLUDE, "sf.h"), os.path.abspath(__file__)]:
         p = f if os.path.isabs(f) else os.path.join(CSRC, f)
         with open(p, "rb") as fh:
             h.update(p.encode())
@@ -50,7 +53,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     srcs = _sources()
     stamp = _stamp(srcs)
     stamp_file = os.path.join(BUILD_DIR, "stamp")
-    if not force and os.path.exists(OUT) and os.path.exists(stamp_file):
+    if not force and os.path.exists(OUT) and os.path.exists(PY_OUT) and os.path.exists(stamp_file):
         with open(stamp_file) as fh:
             if fh.read() == stamp:
                 return OUT
@@ -75,6 +78,14 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, OUT)
+    cc = shutil.which("gcc") or "cc"
+    cmd = [cc, "-O2", "-shared", "-fPIC", "-std=gnu11", "-fvisibility=hidden", "-I", sysconfig.get_paths()["include"],
+           "-I", INCLUDE, os.path.join(CSRC, "paged_py.c"), "-o", PY_OUT + ".tmp", "-L", HERE,
+           "-l:libsf.so", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"building the Python binding failed:\n{r.stderr}")
+    os.replace(PY_OUT + ".tmp", PY_OUT)
     with open(stamp_file, "w") as fh:
         fh.write(stamp)
     return OUT
