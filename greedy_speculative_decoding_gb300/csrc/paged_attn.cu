@@ -9,7 +9,7 @@
 namespace sf {
 namespace pa {
 
-constexpr int kMaxCtas = 512;   // CTAs of a launch, at most
+constexpr int kMaxCtas = 320;   // CTAs of a launch, at most (two on each of 152 SMs)
 constexpr int kMaxDesc = 1024;  // item descriptors
 
 struct Layout {
@@ -79,7 +79,7 @@ static Sizes sizes(const sf_paged_cache& c, int n_heads, int max_rows, int q_dty
   // if every request filled its table: the cache is then read once for each
   // tile (from L2), by CTAs that would be idle.
   z.mt = tile_of(queries, q_dtype == SF_DT_F32);
-  while (z.mt > 16 && items(z.mt) * z.units < 2 * sms) z.mt /= 2;
+  while (z.mt > 16 && items(z.mt) * z.units < 2 * sms) z.mt = z.mt == 128 ? 32 : 16;
   z.ntq = (queries + z.mt - 1) / z.mt;
   z.items = items(z.mt);
   return z;

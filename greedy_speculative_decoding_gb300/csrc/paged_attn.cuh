@@ -27,12 +27,13 @@
 #include <type_traits>
 
 #include "paged.h"
+#include "umma.cuh"
 
 namespace sf {
 namespace pa {
 
 constexpr int kTile = 64;                 // slots of a unit
-constexpr uint32_t kWaitIters = 1u << 24; // bound of every wait
+constexpr uint64_t kWaitNs = 1000000000;  // bound of every wait
 
 struct Args {
   CUtensorMap km, vm;      // cache as {head_dim, slot or head, head or slot, page}
@@ -99,6 +100,19 @@ struct Deal {
   }
 };
 
+// Wait on an mbarrier phase; false after a second without it (the copies and
+// products waited for take microseconds).
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
+  if (mbar_wait(bar, parity, 32)) return true;
+  uint64_t t0, t;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
+  do {
+    if (mbar_wait(bar, parity, 32)) return true;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+  } while (t - t0 < kWaitNs);
+  return false;
+}
+
 template <typename T>
 struct Num;
 template <>
@@ -157,10 +171,6 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar)), "l"(policy)
       : "memory");
 }
-__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
-
 template <int HD, int WM, int WK, bool F32>
 struct Shape {
   static constexpr int MT = 16 * WM;                 // queries of an item
@@ -337,6 +347,69 @@ __device__ __forceinline__ void store2<float>(float* p, float x, float y) {
   *reinterpret_cast<float2*>(p) = make_float2(x, y);
 }
 
+// The producer warp: the pieces' units, 64 slots of keys and values each, into
+// the ring.
+template <int STAGES, int HALF, int BOX, int STAGE, int MT>
+__device__ __forceinline__ void produce(const Args& a, Walk<MT>& w, unsigned char* ring, uint64_t* full,
+                                        uint64_t* empty, bool& ok) {
+  const int lane = threadIdx.x & 31;
+  const int bp = min(1 << a.shift, kTile);        // slots of a box
+  const int np = kTile / bp;                      // boxes of a column
+  const int boxes = np * HALF * 2;
+  const int i = lane % np, h = (lane / np) % HALF, is_v = lane / (np * HALF);
+  const uint32_t dst0 = smem_u32(ring) + (is_v * HALF + h) * BOX + i * bp * 128;
+  const CUtensorMap* map = is_v ? &a.vm : &a.km;
+  const int nhd = is_v ? a.v_nhd : a.k_nhd;
+  int win_b = -1, win = -1, entry = 0;            // the 32 table entries at hand, one per lane
+  int n = 0;
+  while (ok && w.next(a)) {
+    const uint64_t policy = w.r.ntq == 1 ? policy_evict_first() : policy_evict_normal();
+    for (int t = w.t0; t < w.t1; ++t, ++n) {
+      const int s = n % STAGES;
+      const int first = (t * kTile) >> a.shift;
+      if (w.b != win_b || (first >> 5) != win) {
+        win_b = w.b;
+        win = first >> 5;
+        const int e = 32 * win + lane;
+        entry = e < a.W ? a.tables[(long)w.b * a.W + e] : -1;
+      }
+      if (n >= STAGES) ok = wait(&empty[s], (n / STAGES - 1) & 1);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      const int left = w.r.len - t * kTile;       // slots from here on
+      const int nb = max(0, min(np, (left + bp - 1) / bp));
+      const int page = __shfl_sync(0xffffffffu, entry, (first + i) & 31);
+      if (lane == 0) mbar_expect_tx(&full[s], nb * bp * 128 * HALF * 2);
+      __syncwarp();
+      if (lane < boxes && i < nb) {
+        const int off = (t * kTile) & ((1 << a.shift) - 1) & ~(kTile - 1);
+        tma_load_4d(dst0 + s * STAGE, map, 64 * h, nhd ? w.kvh : off, nhd ? off : w.kvh, page, &full[s], policy);
+      }
+    }
+  }
+  // An expired wait: the copies in flight land before the CTA may end.
+  if (!ok)
+    for (int k = max(0, n - STAGES); k < n; ++k) wait(&full[k % STAGES], (k / STAGES) & 1);
+}
+
+// The join's descriptor of an item that begins in this CTA (one thread).
+template <int MT>
+__device__ __forceinline__ void describe(const Args& a, const Walk<MT>& w, const Deal& deal, bool whole) {
+  const long first = w.u - (w.t1 - w.t0);
+  const int c1 = whole ? (int)blockIdx.x : deal.cta_of(first + w.r.nt - 1);
+  const int4 d = make_int4(blockIdx.x, c1 - (int)blockIdx.x + 1, w.b, w.item);
+  if (a.by_item) a.desc[((long)w.b * a.nkv + w.kvh) * a.ntq_max + w.qt] = d;
+  else if (!whole) a.desc[blockIdx.x] = d;
+}
+// Descriptors by CTA: none when no item begins here that others share.
+template <int MT>
+__device__ __forceinline__ void describe_none(const Args& a, const Walk<MT>& w, const Start& st, long u1, bool idle) {
+  if (a.by_item) return;
+  // (the last piece begins an item that goes on in the next CTA)
+  const bool shared = !idle && u1 < st.T && w.t0 == 0 && w.t1 < w.r.nt;
+  if (!shared) a.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
+}
+
 // Two neighbouring elements of row `row`, head `head` of the output.
 template <int HD, typename TQ>
 __device__ __forceinline__ void put2(const Args& a, int row, int head, int d, float x, float y) {
@@ -387,47 +460,9 @@ __global__ void __launch_bounds__(Shape<HD, WM, WK, F32>::kThreads, Shape<HD, WM
   const long u0 = deal.first(blockIdx.x), u1 = deal.first(blockIdx.x + 1);
   Walk<MT> w(st, u0, u1);
 
+  bool ok = true;
   if (warp == S::kWarps) {
-    // ---------------------------------------------------------- producer warp
-    const int bp = min(1 << a.shift, kTile);        // slots of a box
-    const int np = kTile / bp;                      // boxes of a column
-    const int boxes = np * S::kHalf * 2;
-    const int i = lane % np, h = (lane / np) % S::kHalf, is_v = lane / (np * S::kHalf);
-    const uint32_t dst0 = smem_u32(ring) + (is_v * S::kHalf + h) * S::kBox + i * bp * 128;
-    const CUtensorMap* map = is_v ? &a.vm : &a.km;
-    const int nhd = is_v ? a.v_nhd : a.k_nhd;
-    int win_b = -1, win = -1, entry = 0;            // the 32 table entries at hand, one per lane
-    int n = 0;
-    bool ok = true;
-    while (ok && w.next(a)) {
-      const uint64_t policy = w.r.ntq == 1 ? policy_evict_first() : policy_evict_normal();
-      for (int t = w.t0; t < w.t1; ++t, ++n) {
-        const int s = n % S::kStages;
-        const int first = (t * kTile) >> a.shift;
-        if (w.b != win_b || (first >> 5) != win) {
-          win_b = w.b;
-          win = first >> 5;
-          const int e = 32 * win + lane;
-          entry = e < a.W ? a.tables[(long)w.b * a.W + e] : -1;
-        }
-        if (n >= S::kStages) ok = mbar_wait(&empty[s], (n / S::kStages - 1) & 1, kWaitIters);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        const int left = w.r.len - t * kTile;       // slots from here on
-        const int nb = max(0, min(np, (left + bp - 1) / bp));
-        const int page = __shfl_sync(0xffffffffu, entry, (first + i) & 31);
-        if (lane == 0) mbar_expect_tx(&full[s], nb * bp * 128 * S::kHalf * 2);
-        __syncwarp();
-        if (lane < boxes && i < nb) {
-          const int off = (t * kTile) & ((1 << a.shift) - 1) & ~(kTile - 1);
-          tma_load_4d(dst0 + s * S::kStage, map, 64 * h, nhd ? w.kvh : off, nhd ? off : w.kvh, page, &full[s], policy);
-        }
-      }
-    }
-    // An expired wait: the copies in flight land before the CTA may end.
-    if (!ok)
-      for (int k = max(0, n - S::kStages); k < n; ++k)
-        mbar_wait(&full[k % S::kStages], (k / S::kStages) & 1, kWaitIters);
+    produce<S::kStages, S::kHalf, S::kBox, S::kStage, MT>(a, w, ring, full, empty, ok);
     return;
   }
 
@@ -442,7 +477,6 @@ __global__ void __launch_bounds__(Shape<HD, WM, WK, F32>::kThreads, Shape<HD, WM
   const uint32_t k_off = (k_slot * 128 + ((k_slot & 7) << 4)) ^ (((lane >> 3) & 1) << 4);
   const uint32_t v_off = (v_slot * 128 + ((v_slot & 7) << 4)) ^ ((lane >> 4) << 4);
   int n = 0;
-  bool ok = true;
   while (w.next(a)) {
     const Request r = w.r;
     const int q0 = w.qt * MT + 16 * wm + g;        // this lane's queries: q0 and q0 + 8
@@ -685,7 +719,7 @@ __global__ void __launch_bounds__(Shape<HD, WM, WK, F32>::kThreads, Shape<HD, WM
       ++n;
     };
     auto arrived = [&] {
-      if (ok && !mbar_wait(&full[n % S::kStages], (n / S::kStages) & 1, kWaitIters)) ok = false;
+      if (ok && !wait(&full[n % S::kStages], (n / S::kStages) & 1)) ok = false;
       ok = __all_sync(0xffffffffu, ok);
     };
     // Whether this warp's slots hold values of the pass that are no finite
@@ -735,13 +769,7 @@ __global__ void __launch_bounds__(Shape<HD, WM, WK, F32>::kThreads, Shape<HD, WM
       if (m[e] != -INFINITY) m[e] *= a.scale2;
     }
     const bool begins = w.t0 == 0, whole = begins && w.t1 == r.nt;
-    if (begins && tid == 0) {
-      const long first = w.u - (w.t1 - w.t0);
-      const int c1 = whole ? (int)blockIdx.x : deal.cta_of(first + r.nt - 1);
-      const int4 d = make_int4(blockIdx.x, c1 - (int)blockIdx.x + 1, w.b, w.item);
-      if (a.by_item) a.desc[((long)w.b * a.nkv + w.kvh) * a.ntq_max + w.qt] = d;
-      else if (!whole) a.desc[blockIdx.x] = d;
-    }
+    if (begins && tid == 0) describe(a, w, deal, whole);
     const long slot = 2l * blockIdx.x + (begins ? 1 : 0);
     float* part = a.part + slot * a.mt_max * HD;
     float2* part_ml = a.part_ml + slot * a.mt_max;
@@ -819,14 +847,7 @@ __global__ void __launch_bounds__(Shape<HD, WM, WK, F32>::kThreads, Shape<HD, WM
     }
   }
   if (!ok && lane == 0) report_err(a.err, kErrWait);
-  // No item begins here that others share (descriptors by CTA).
-  if (!a.by_item && tid == 0) {
-    const bool shared = u1 < st.T && [&] {
-      // The last unit's item begins in this CTA and goes on in the next one.
-      return w.t0 == 0 && w.t1 < w.r.nt;
-    }();
-    if (!shared) a.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
-  }
+  if (tid == 0) describe_none(a, w, st, u1, false);
 }
 
 // The join of the items that several CTAs share: the parts lie with the CTAs

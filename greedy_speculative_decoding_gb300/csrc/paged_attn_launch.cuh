@@ -4,34 +4,32 @@
 
 #include <atomic>
 
-#include "paged_attn.cuh"
+#include "paged_attn_tc.cuh"
 
 namespace sf {
 namespace pa {
 
 // Query tile of a launch, from the queries that a KV head can have in one
-// request (max_rows * group): one m16 tile shared by four warps that split
-// the slots, two by two, or four tiles with a warp each. fp32 queries take at
-// most 32 a tile: their three terms of 64 would leave room for one CTA an SM.
-inline int tile_of(int queries, bool f32) { return queries <= 16 ? 16 : queries <= 32 || f32 ? 32 : 64; }
+// request (max_rows * group): one m16 tile shared by four warps that split the
+// slots, two by two, or the tcgen05 kernel's 128. fp32 queries take at most 32
+// a tile (their three terms are computed with mma.sync).
+inline int tile_of(int queries, bool f32) { return queries <= 16 ? 16 : queries <= 32 || f32 ? 32 : 128; }
 
-template <int HD, typename TC, bool F32, int WM, int WK>
-cudaError_t launch(Args& a, int sms, long max_units, cudaStream_t st) {
-  using S = Shape<HD, WM, WK, F32>;
-  using TQ = typename std::conditional<F32, float, TC>::type;
-  auto* fn = k_paged_attn<HD, TC, F32, WM, WK>;
-  static std::atomic<uint64_t> ready{0};   // devices whose shared-memory limit for this kernel is set
+// Launch a main kernel (two CTAs an SM) and the join.
+template <int HD, typename TQ, int MT>
+cudaError_t launch(void (*fn)(Args), int threads, int smem, std::atomic<uint64_t>& ready, Args& a, int sms, int ctas,
+                   long max_units, cudaStream_t st) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev >= 64 || !(ready.load(std::memory_order_relaxed) >> dev & 1)) {
-    e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+    e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e == cudaSuccess)
       e = cudaFuncSetAttribute(fn, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
     if (e != cudaSuccess) return e;
     if (dev < 64) ready.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
   }
-  const long most = (long)sms * S::kCtas, items = (long)a.B * a.nkv * a.ntq_max;
+  const long most = (long)sms * ctas, items = (long)a.B * a.nkv * a.ntq_max;
   const int grid = (int)(max_units < most ? max_units : most);
   a.wide = items * 8 <= grid;   // an item's parts: one and as many as CTAs share it
   cudaLaunchAttribute attr[1];
@@ -39,8 +37,8 @@ cudaError_t launch(Args& a, int sms, long max_units, cudaStream_t st) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(S::kThreads);
-  cfg.dynamicSmemBytes = S::kSmem;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
@@ -48,14 +46,32 @@ cudaError_t launch(Args& a, int sms, long max_units, cudaStream_t st) {
   cfg.gridDim = dim3(a.by_item ? (int)items : grid, a.wide ? a.mt_max : (a.mt_max + 3) / 4);
   cfg.blockDim = dim3(kJoinThreads);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, k_paged_join<HD, TQ, S::MT>, a);
+  return cudaLaunchKernelEx(&cfg, k_paged_join<HD, TQ, MT>, a);
+}
+
+template <int HD, typename TC, bool F32, int WM, int WK>
+cudaError_t launch_mma(Args& a, int sms, long max_units, cudaStream_t st) {
+  using S = Shape<HD, WM, WK, F32>;
+  using TQ = typename std::conditional<F32, float, TC>::type;
+  static std::atomic<uint64_t> ready{0};   // devices whose shared-memory limit for this kernel is set
+  return launch<HD, TQ, S::MT>(k_paged_attn<HD, TC, F32, WM, WK>, S::kThreads, S::kSmem, ready, a, sms, S::kCtas,
+                               max_units, st);
+}
+
+template <int HD, typename TC>
+cudaError_t launch_tc(Args& a, int sms, long max_units, cudaStream_t st) {
+  using S = TcShape<HD>;
+  static std::atomic<uint64_t> ready{0};
+  return launch<HD, TC, S::MT>(k_paged_attn_tc<HD, TC>, S::kThreads, S::kSmem, ready, a, sms, 2, max_units, st);
 }
 
 template <int HD, typename TC, bool F32>
 cudaError_t launch_tiles(Args& a, int sms, long max_units, cudaStream_t st) {
-  if (a.mt == 16) return launch<HD, TC, F32, 1, 4>(a, sms, max_units, st);
-  if (F32 || a.mt == 32) return launch<HD, TC, F32, 2, 2>(a, sms, max_units, st);
-  return launch<HD, TC, F32, F32 ? 2 : 4, F32 ? 2 : 1>(a, sms, max_units, st);
+  if (a.mt == 16) return launch_mma<HD, TC, F32, 1, 4>(a, sms, max_units, st);
+  if constexpr (!F32) {
+    if (a.mt == 128) return launch_tc<HD, TC>(a, sms, max_units, st);
+  }
+  return launch_mma<HD, TC, F32, 2, 2>(a, sms, max_units, st);
 }
 
 template <int HD>

@@ -1,0 +1,414 @@
+// Paged attention for many queries per KV head (several rows times the query
+// heads that share the KV head), on the tcgen05 tensor cores: tiles of 128
+// queries, 16-bit queries. The work is dealt out as in paged_attn.cuh; beside
+// the producer warp a CTA has
+//   * one MMA thread: S = Q K^T (128 x 64, queries and keys in shared memory)
+//     and O += P V (P in tensor memory, values in shared memory with the slots
+//     as the MMA's K side), both accumulators in tensor memory. S of the next
+//     unit is computed while the softmax works on this one: two S buffers of 64
+//     columns, P of a unit lying over its S; O takes head_dim columns. At 256
+//     columns two CTAs share an SM;
+//   * four softmax warps, a thread per query row: row maximum and sum without
+//     shuffles. O is rescaled only when a row's maximum has grown by more than
+//     2^8 since its reference was set (probabilities then stay below 256, which
+//     costs no precision in floating point), so seldom after the first unit.
+//
+// mma.sync reaches 590 TFLOP/s on this GPU (measured, four or more warps an
+// SM), where the 45 queries of a 9-row verify at 5 heads per KV head need
+// about 800 to keep up with the cache's bytes; tcgen05 leaves the memory as
+// the bound.
+#pragma once
+
+#include "paged_attn.cuh"
+
+namespace sf {
+namespace pa {
+
+template <int HD>
+struct TcShape {
+  static constexpr int MT = 128;
+  static constexpr int kThreads = 192;                 // 4 softmax warps, producer, MMA
+  static constexpr int kHalf = HD / 64;
+  static constexpr int kBox = kTile * 128;
+  static constexpr int kStage = 2 * kHalf * kBox;
+  static constexpr int kQBox = MT * 128;               // 64 dimensions of the queries
+  static constexpr int kQ = kHalf * kQBox;
+  static constexpr int kFit = (kHalfSmBytes - 1024 - kQ) / kStage;
+  static constexpr int kStages = kFit < 4 ? kFit : 4;
+  static constexpr int kSmem = 1024 + kQ + kStages * kStage;
+  static constexpr int kCols = 256;                    // tensor-memory columns: O, S0, S1
+  static constexpr int kO = 0, kS = 128;               // (S b at kS + 64 b)
+  static_assert(kStages >= 2, "two units in flight");
+};
+
+// B operand with the slots as K: rows of 128 bytes are 64 dimensions of one
+// slot (the MN side contiguous), 8 slots to a 1024-byte swizzle atom. Leading
+// offset: from 64 dimensions to the next 64 (one box); stride: from 8 slots to
+// the next 8.
+__device__ __forceinline__ uint64_t sw128_desc_mn(uint32_t saddr, uint32_t box_bytes) {
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(box_bytes >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+
+template <typename TC>
+__host__ __device__ constexpr uint32_t tc_idesc(int M, int N, bool b_mn) {
+  const uint32_t fmt = std::is_same<TC, bf16>::value ? 1 : 0;   // operand type: bf16 or fp16
+  return (1u << 4) | (fmt << 7) | (fmt << 10) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) |
+         ((uint32_t)(M >> 4) << 24);
+}
+
+template <int HD, typename TC>
+__global__ void __launch_bounds__(TcShape<HD>::kThreads, 2) k_paged_attn_tc(const __grid_constant__ Args a) {
+  using S = TcShape<HD>;
+  constexpr int MT = S::MT;
+  extern __shared__ unsigned char pa_smem_raw[];
+  unsigned char* sq = pa_smem_raw + ((1024 - (smem_u32(pa_smem_raw) & 1023)) & 1023);   // queries
+  unsigned char* ring = sq + S::kQ;
+  __shared__ long sh_loc[S::kThreads / 32 + 2];
+  __shared__ __align__(8) uint64_t full[S::kStages], empty[S::kStages], s_full[2], p_full[2], o_done, q_full, drain;
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_keep[2];     // the unit adds to what the softmax put into O (see odd values)
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) {
+    for (int s = 0; s < S::kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&s_full[b], 1);
+      mbar_init(&p_full[b], 4);
+      s_keep[b] = 0;
+    }
+    mbar_init(&o_done, 1);
+    mbar_init(&q_full, 4);
+    mbar_init(&drain, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  } else if (warp == 4 && lane < 2) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(lane ? &a.vm : &a.km)) : "memory");
+  }
+  if (warp == 5) {
+    tmem_alloc(&s_tmem, S::kCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+  pdl_wait();
+  pdl_launch_next();
+  const Start st = a.by_warp ? locate_warp<MT>(a) : locate_cta<MT, S::kThreads>(a, sh_loc);
+  const long G = min((long)gridDim.x, st.T);
+  const bool idle = (long)blockIdx.x >= G;
+  const Deal deal(max(st.T, 1l), max(G, 1l));
+  const long u0 = deal.first(blockIdx.x), u1 = idle ? u0 : deal.first(blockIdx.x + 1);
+  Walk<MT> w(st, u0, u1);
+  bool ok = true;
+
+  if (warp == 4) {
+    // ---------------------------------------------------------- producer warp
+    produce<S::kStages, S::kHalf, S::kBox, S::kStage, MT>(a, w, ring, full, empty, ok);
+  } else if (warp == 5) {
+    // -------------------------------------------------------------- MMA thread
+    if (lane == 0) {
+      const uint32_t id_s = tc_idesc<TC>(MT, kTile, false), id_o = tc_idesc<TC>(MT, HD, true);
+      const uint32_t q_addr = smem_u32(sq), r_addr = smem_u32(ring);
+      auto scores = [&](int n) {   // S of unit n
+        const int s = n % S::kStages;
+        ok = ok && wait(&full[s], (n / S::kStages) & 1);
+        tc_fence_after();
+#pragma unroll
+        for (int k = 0; k < HD / 16; ++k)
+          umma_bf16(tmem + S::kS + 64 * (n & 1), sw128_desc(q_addr + (k >> 2) * S::kQBox + 32 * (k & 3)),
+                    sw128_desc(r_addr + s * S::kStage + (k >> 2) * S::kBox + 32 * (k & 3)), id_s, k > 0);
+        umma_commit(&s_full[n & 1]);
+      };
+      int n = 0, piece = 0;
+      while (ok && w.next(a)) {
+        ok = wait(&q_full, piece++ & 1);
+        const int units = w.t1 - w.t0;
+        scores(n);
+        for (int u = 0; ok && u < units; ++u, ++n) {
+          if (u + 1 < units) scores(n + 1);
+          ok = ok && wait(&p_full[n & 1], (n >> 1) & 1);
+          if (!ok) break;
+          tc_fence_after();
+          const int keep = u > 0 || s_keep[n & 1];
+          const uint32_t vs = r_addr + n % S::kStages * S::kStage + S::kHalf * S::kBox;
+#pragma unroll
+          for (int k = 0; k < kTile / 16; ++k)
+            umma_bf16_tmem_a(tmem + S::kO, tmem + S::kS + 64 * (n & 1) + 8 * k, sw128_desc_mn(vs + 2048 * k, S::kBox),
+                             id_o, keep || k > 0);
+          umma_commit(&empty[n % S::kStages]);
+          umma_commit(&o_done);
+        }
+      }
+      if (!ok) {   // an expired wait: what was issued ends before the CTA does
+        umma_commit(&drain);
+        wait(&drain, 0);
+      }
+    }
+    __syncwarp();
+  } else {
+    // ----------------------------------------------------------- softmax warps
+    const int row = tid;                                  // query of the tile = tensor-memory lane
+    const uint32_t lanes = tmem + ((uint32_t)(32 * warp) << 16);
+    auto sync4 = [] { asm volatile("bar.sync 1, 128;" ::: "memory"); };
+    int n = 0, o_seen = 0;
+    // Waits for the output products up to unit k. A parity tells neighbouring
+    // phases apart only, so no warp may fall two behind: each waits for the
+    // product of a unit before it hands over the next one's probabilities.
+    auto o_upto = [&](int k) {
+      for (; o_seen <= k; ++o_seen)
+        if (ok && !wait(&o_done, o_seen & 1)) ok = false;
+      ok = __all_sync(0xffffffffu, ok);
+      tc_fence_after();
+    };
+    while (w.next(a)) {
+      const Request r = w.r;
+      const int Mq = r.rows * a.group;
+      const int q = w.qt * MT + row, j = q / a.group, hh = w.kvh * a.group + q - j * a.group;
+      const bool live = q < Mq, warp_live = w.qt * MT + 32 * warp < Mq;
+      const unsigned long long bits = a.mask && live ? a.mask[r.s0 + j] : 0;
+      // The tile's queries, rows past the end as zeros, in the MMA's layout.
+      {
+        constexpr int NL = MT * HD / 8 / 128, B = NL < 8 ? NL : 8;
+#pragma unroll
+        for (int y0 = 0; y0 < NL; y0 += B) {
+          uint4 f[B];
+#pragma unroll
+          for (int y = 0; y < B; ++y) {
+            const int e = tid + (y0 + y) * 128, m = e / (HD / 8), d = 8 * (e - m * (HD / 8));
+            const int x = w.qt * MT + m, jj = x / a.group, xh = w.kvh * a.group + x - jj * a.group;
+            f[y] = make_uint4(0u, 0u, 0u, 0u);
+            if (x < Mq)
+              f[y] = *reinterpret_cast<const uint4*>(static_cast<const TC*>(a.q) + (r.s0 + jj) * a.q_row + xh * a.q_head + d);
+          }
+#pragma unroll
+          for (int y = 0; y < B; ++y) {
+            const int e = tid + (y0 + y) * 128, m = e / (HD / 8), p = e - m * (HD / 8);
+            f[y].x ^= a.flip, f[y].y ^= a.flip, f[y].z ^= a.flip, f[y].w ^= a.flip;
+            *reinterpret_cast<uint4*>(sq + (p >> 3) * S::kQBox + m * 128 + (((p & 7) ^ (m & 7)) << 4)) = f[y];
+          }
+        }
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&q_full);
+      }
+      float m = -INFINITY, l = 0.f;
+      for (int t = w.t0; t < w.t1; ++t, ++n) {
+        const int b = n & 1;
+        const bool tail = t * kTile + kTile > min(r.p0, r.len);
+        if (ok && !wait(&s_full[b], (n >> 1) & 1)) ok = false;
+        ok = __all_sync(0xffffffffu, ok);
+        tc_fence_after();
+        float x[kTile];
+        if (warp_live) {
+          uint32_t v[4][16];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld16(lanes + S::kS + 64 * b + 16 * c, v[c]);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < kTile; ++i) {
+            asm volatile("" : "+r"(v[i >> 4][i & 15]));   // (read behind the wait only)
+            x[i] = __uint_as_float(v[i >> 4][i & 15]);
+          }
+        }
+        // ---- what the row does not see is -infinity
+        unsigned long long vis = ~0ull;
+        if (tail) {
+          const int first = r.p0 - t * kTile;             // the pass's first slot, within the unit
+          auto low = [](int k) { return k <= 0 ? 0ull : k >= 64 ? ~0ull : (1ull << k) - 1; };
+          vis = low(first + j + 1);
+          if (a.mask) vis = low(first) | (first >= 64 || first <= -64 ? 0ull : first >= 0 ? bits << first : bits >> -first);
+          vis = live ? vis & low(r.len - t * kTile) : 0ull;
+          if (warp_live) {
+#pragma unroll
+            for (int i = 0; i < kTile; ++i)
+              if (!((i < 32 ? (uint32_t)vis : (uint32_t)(vis >> 32)) >> (i & 31) & 1)) x[i] = -INFINITY;
+          }
+        }
+        if (warp_live) {
+          // ---- maximum; a new reference when it has outgrown the old one
+          float mx4[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+          for (int i = 4; i < kTile; ++i) mx4[i & 3] = fmaxf(mx4[i & 3], x[i]);
+          const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
+          const bool grow = m != -INFINITY && (mx - m) * a.scale2 > 8.f;
+          if (__any_sync(0xffffffffu, grow)) {
+            const float f = grow ? exp2_approx((m - mx) * a.scale2) : 1.f;
+            if (grow) m = mx;
+            l *= f;
+            o_upto(n - 1);   // (never at the piece's first unit: m was -infinity)
+#pragma unroll 1
+            for (int c = 0; c < HD / 16; ++c) {
+              uint32_t v[16];
+              tmem_ld16(lanes + S::kO + 16 * c, v);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                asm volatile("" : "+r"(v[i]));
+                v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
+              }
+              tmem_st16(lanes + S::kO + 16 * c, v);
+            }
+            tmem_st_wait();
+          }
+          if (m == -INFINITY) m = mx;                     // (what came before saw nothing: O is 0)
+          const float ref = m == -INFINITY ? 0.f : -m * a.scale2;
+          float l4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int i = 0; i < kTile; ++i) {
+            x[i] = exp2_approx(fmaf(x[i], a.scale2, ref));
+            l4[i & 3] += x[i];
+          }
+          l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+        }
+        // ---- values of a tail unit: slots past the end become 0; values of
+        // the pass that are no finite numbers (odd: a probability 0 times NaN
+        // is NaN) are added to O here for the rows that see them, and become 0.
+        int keep = 0;
+        if (tail) {
+          unsigned char* vs = ring + n % S::kStages * S::kStage + S::kHalf * S::kBox;
+          if (ok && !wait(&full[n % S::kStages], (n / S::kStages) & 1)) ok = false;
+          ok = __all_sync(0xffffffffu, ok);
+          constexpr int PP = 8 * S::kHalf;                // 16-byte pieces of a slot
+          const int s0 = min(max(0, r.p0 - t * kTile), kTile), s1 = min(max(0, r.len - t * kTile), kTile);
+          auto piece = [&](int sl, int p) {               // in any order within a slot
+            return reinterpret_cast<uint4*>(vs + (p >> 3) * S::kBox + sl * 128 + (p & 7) * 16);
+          };
+          for (int e = tid; e < (kTile - s1) * PP; e += 128) *piece(s1 + e / PP, e % PP) = make_uint4(0u, 0u, 0u, 0u);
+          constexpr uint32_t X = Num<TC>::kExp;
+          auto bad = [](uint32_t v) { return ((v & X) == X ? 1 : 0) | ((v >> 16 & X) == X ? 2 : 0); };
+          if (r.len - r.p0 > 1 || a.mask) {
+            int odd = 0;
+            for (int e = tid; e < (s1 - s0) * PP; e += 128) {
+              const uint4 v = *piece(s0 + e / PP, e % PP);
+              odd |= bad(v.x) | bad(v.y) | bad(v.z) | bad(v.w);
+            }
+            int any;
+            __syncwarp();
+            asm volatile(
+                "{\n .reg .pred p, q;\n setp.ne.s32 p, %1, 0;\n barrier.cta.red.or.aligned.pred q, 1, 128, p;\n"
+                " selp.s32 %0, 1, 0, q;\n}"
+                : "=r"(any)
+                : "r"(odd)
+                : "memory");
+            if (any) {
+              if (warp_live) {
+                float p[kTile];                           // (indexed at run time: local memory)
+#pragma unroll
+                for (int i = 0; i < kTile; ++i) p[i] = x[i];
+                const bool fresh = t == w.t0;
+                o_upto(n - 1);
+#pragma unroll 1
+                for (int c = 0; c < HD / 16; ++c) {
+                  uint32_t v[16];
+                  if (fresh) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) v[i] = 0u;
+                  } else {
+                    tmem_ld16(lanes + S::kO + 16 * c, v);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(v[i]));
+                  }
+#pragma unroll 1
+                  for (int sl = s0; sl < s1; ++sl) {
+                    if (!(vis >> sl & 1)) continue;
+#pragma unroll
+                    for (int h = 0; h < 8; ++h) {         // dimensions 16 c + 2 h, + 1
+                      const int d = 16 * c + 2 * h;
+                      const uint32_t y = *reinterpret_cast<const uint32_t*>(
+                          vs + (d >> 6) * S::kBox + sl * 128 + (((d >> 3 & 7) ^ (sl & 7)) << 4) + 2 * (d & 7));
+                      if (bad(y) & 1) v[2 * h] = __float_as_uint(fmaf(p[sl], Num<TC>::lo(y), __uint_as_float(v[2 * h])));
+                      if (bad(y) & 2)
+                        v[2 * h + 1] = __float_as_uint(fmaf(p[sl], Num<TC>::hi(y), __uint_as_float(v[2 * h + 1])));
+                    }
+                  }
+                  __syncwarp();
+                  tmem_st16(lanes + S::kO + 16 * c, v);
+                }
+                tmem_st_wait();
+              }
+              keep = 1;
+              __syncwarp();
+              sync4();   // everyone has read them
+              for (int e = tid; e < (s1 - s0) * PP; e += 128) {
+                uint4 v = *piece(s0 + e / PP, e % PP);
+                auto clean = [&](uint32_t y) {
+                  return (bad(y) & 1 ? 0u : y & 0xffffu) | (bad(y) & 2 ? 0u : y & 0xffff0000u);
+                };
+                *piece(s0 + e / PP, e % PP) = make_uint4(clean(v.x), clean(v.y), clean(v.z), clean(v.w));
+              }
+            }
+          }
+          fence_proxy_async();
+        }
+        // ---- probabilities over the scores, in the cache's type
+        if (warp_live) {
+          uint32_t p[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) p[i] = Num<TC>::pack(x[2 * i], x[2 * i + 1]);
+          tmem_st32(lanes + S::kS + 64 * b, p);
+          tmem_st_wait();
+        }
+        if (tid == 0) s_keep[b] = keep;
+        o_upto(n - 1);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[b]);
+      }
+
+      // ---- the end of the piece
+      o_upto(n - 1);
+      if (!ok) l = __int_as_float(0x7fc00000);   // an expired wait: NaN
+      if (m != -INFINITY) m *= a.scale2;
+      const bool begins = w.t0 == 0, whole = begins && w.t1 == r.nt;
+      if (begins && tid == 0) describe(a, w, deal, whole);
+      const long slot = 2l * blockIdx.x + (begins ? 1 : 0);
+      if (warp_live) {
+        const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+        float* part = a.part + (slot * a.mt_max + row) * HD;
+        TC* dst = static_cast<TC*>(a.out) + (r.s0 + j) * a.o_row + hh * a.o_head;
+#pragma unroll 1
+        for (int c = 0; c < HD / 16; ++c) {
+          uint32_t v[16];
+          __syncwarp();
+          tmem_ld16(lanes + S::kO + 16 * c, v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(v[i]));
+          if (!live) continue;
+          // (a row that saw nothing: l = 0 and O = 0)
+          if (whole) {
+            uint32_t o[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              o[i] = Num<TC>::pack(__uint_as_float(v[2 * i]) * inv, __uint_as_float(v[2 * i + 1]) * inv);
+            *reinterpret_cast<uint4*>(dst + 16 * c) = make_uint4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<uint4*>(dst + 16 * c + 8) = make_uint4(o[4], o[5], o[6], o[7]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 16; i += 4)
+              *reinterpret_cast<uint4*>(part + 16 * c + i) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+          }
+        }
+        if (live && whole && a.lse)
+          a.lse[(long)(r.s0 + j) * a.nq + hh] = l == 0.f ? -INFINITY : m * 0.693147180559945f + logf(l);
+        if (live && !whole) a.part_ml[slot * a.mt_max + row] = make_float2(m, l);
+      }
+      tc_fence_before();   // O has been read: the next piece's first product may replace it
+    }
+    if (!ok && lane == 0) report_err(a.err, kErrWait);
+    if (tid == 0) describe_none(a, w, st, u1, idle);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 5) {
+    tc_fence_after();
+    tmem_dealloc(tmem, S::kCols);
+  }
+}
+
+}  // namespace pa
+}  // namespace sf
