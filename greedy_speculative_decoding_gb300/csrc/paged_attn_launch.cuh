@@ -62,7 +62,8 @@ template <int HD, typename TC>
 cudaError_t launch_tc(Args& a, int sms, long max_units, cudaStream_t st) {
   using S = TcShape<HD>;
   static std::atomic<uint64_t> ready{0};
-  return launch<HD, TC, S::MT>(k_paged_attn_tc<HD, TC>, S::kThreads, S::kSmem, ready, a, sms, 2, max_units, st);
+  return launch<HD, TC, S::MT>(k_paged_attn_tc<HD, TC>, S::kThreads, S::kSmem, ready, a, sms, S::kCtas,
+                          max_units, st);
 }
 
 template <int HD, typename TC, bool F32>

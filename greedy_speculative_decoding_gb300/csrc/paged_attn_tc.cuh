@@ -6,8 +6,7 @@
 //     and O += P V (P in tensor memory, values in shared memory with the slots
 //     as the MMA's K side), both accumulators in tensor memory. S of the next
 //     unit is computed while the softmax works on this one: two S buffers of 64
-//     columns, P of a unit lying over its S; O takes head_dim columns. At 256
-//     columns two CTAs share an SM;
+//     columns, P of a unit lying over its S; O takes head_dim columns;
 //   * four softmax warps, a thread per query row: row maximum and sum without
 //     shuffles. O is rescaled only when a row's maximum has grown by more than
 //     2^8 since its reference was set (probabilities then stay below 256, which
@@ -33,8 +32,11 @@ struct TcShape {
   static constexpr int kStage = 2 * kHalf * kBox;
   static constexpr int kQBox = MT * 128;               // 64 dimensions of the queries
   static constexpr int kQ = kHalf * kQBox;
-  static constexpr int kFit = (kHalfSmBytes - 1024 - kQ) / kStage;
-  static constexpr int kStages = kFit < 4 ? kFit : 4;
+  // Two CTAs an SM where their rings hold the units in flight that the memory
+  // needs; at head dimension 128 the queries leave room for two units each,
+  // and one CTA with six does better.
+  static constexpr int kCtas = HD == 64 ? 2 : 1;
+  static constexpr int kStages = ((kCtas == 2 ? kHalfSmBytes : 224 * 1024) - 1024 - kQ) / kStage;
   static constexpr int kSmem = 1024 + kQ + kStages * kStage;
   static constexpr int kCols = 256;                    // tensor-memory columns: O, S0, S1
   static constexpr int kO = 0, kS = 128;               // (S b at kS + 64 b)
@@ -50,6 +52,13 @@ __device__ __forceinline__ uint64_t sw128_desc_mn(uint32_t saddr, uint32_t box_b
          ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
 
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(r));
+  return r != 0;
+}
+
 template <typename TC>
 __host__ __device__ constexpr uint32_t tc_idesc(int M, int N, bool b_mn) {
   const uint32_t fmt = std::is_same<TC, bf16>::value ? 1 : 0;   // operand type: bf16 or fp16
@@ -58,7 +67,7 @@ __host__ __device__ constexpr uint32_t tc_idesc(int M, int N, bool b_mn) {
 }
 
 template <int HD, typename TC>
-__global__ void __launch_bounds__(TcShape<HD>::kThreads, 2) k_paged_attn_tc(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(TcShape<HD>::kThreads, TcShape<HD>::kCtas) k_paged_attn_tc(const __grid_constant__ Args a) {
   using S = TcShape<HD>;
   constexpr int MT = S::MT;
   extern __shared__ unsigned char pa_smem_raw[];
@@ -108,44 +117,61 @@ __global__ void __launch_bounds__(TcShape<HD>::kThreads, 2) k_paged_attn_tc(cons
     // ---------------------------------------------------------- producer warp
     produce<S::kStages, S::kHalf, S::kBox, S::kStage, MT>(a, w, ring, full, empty, ok);
   } else if (warp == 5) {
-    // -------------------------------------------------------------- MMA thread
-    if (lane == 0) {
-      const uint32_t id_s = tc_idesc<TC>(MT, kTile, false), id_o = tc_idesc<TC>(MT, HD, true);
-      const uint32_t q_addr = smem_u32(sq), r_addr = smem_u32(ring);
-      auto scores = [&](int n) {   // S of unit n
-        const int s = n % S::kStages;
-        ok = ok && wait(&full[s], (n / S::kStages) & 1);
-        tc_fence_after();
+    // ---------------------------------------------------------------- MMA warp
+    // The whole warp runs the loop and one lane issues: control flow and
+    // descriptors are the same in all lanes, and the shuffles and votes say so
+    // to the compiler, which then keeps the descriptors in uniform registers
+    // (moving them there for every MMA took 100 cycles an MMA).
+    constexpr uint32_t id_s = tc_idesc<TC>(MT, kTile, false), id_o = tc_idesc<TC>(MT, HD, true);
+    const uint32_t utmem = __shfl_sync(0xffffffffu, tmem, 0);
+    const uint64_t dq = sw128_desc(__shfl_sync(0xffffffffu, smem_u32(sq), 0));
+    const uint64_t dk = sw128_desc(__shfl_sync(0xffffffffu, smem_u32(ring), 0));
+    const uint64_t dv = sw128_desc_mn(__shfl_sync(0xffffffffu, smem_u32(ring) + S::kHalf * S::kBox, 0), S::kBox);
+    bool good = true;
+    auto await = [&](uint64_t* bar, uint32_t parity) {
+      if (good) good = __all_sync(0xffffffffu, wait(bar, parity));
+    };
+    auto scores = [&](int n) {   // S of unit n
+      const int s = n % S::kStages;
+      await(&full[s], (n / S::kStages) & 1);
+      tc_fence_after();
+      const uint64_t d = dk + (uint64_t)(s * (S::kStage >> 4));
+      const uint32_t t = utmem + S::kS + 64 * (n & 1);
+      if (elect_one()) {
 #pragma unroll
         for (int k = 0; k < HD / 16; ++k)
-          umma_bf16(tmem + S::kS + 64 * (n & 1), sw128_desc(q_addr + (k >> 2) * S::kQBox + 32 * (k & 3)),
-                    sw128_desc(r_addr + s * S::kStage + (k >> 2) * S::kBox + 32 * (k & 3)), id_s, k > 0);
+          umma_bf16(t, dq + (((k >> 2) * S::kQBox + 32 * (k & 3)) >> 4), d + (((k >> 2) * S::kBox + 32 * (k & 3)) >> 4),
+                    id_s, k > 0);
         umma_commit(&s_full[n & 1]);
-      };
-      int n = 0, piece = 0;
-      while (ok && w.next(a)) {
-        ok = wait(&q_full, piece++ & 1);
-        const int units = w.t1 - w.t0;
-        scores(n);
-        for (int u = 0; ok && u < units; ++u, ++n) {
-          if (u + 1 < units) scores(n + 1);
-          ok = ok && wait(&p_full[n & 1], (n >> 1) & 1);
-          if (!ok) break;
-          tc_fence_after();
-          const int keep = u > 0 || s_keep[n & 1];
-          const uint32_t vs = r_addr + n % S::kStages * S::kStage + S::kHalf * S::kBox;
+      }
+      __syncwarp();
+    };
+    int n = 0, piece = 0;
+    while (__shfl_sync(0xffffffffu, (int)(good && w.next(a)), 0)) {
+      const int units = __shfl_sync(0xffffffffu, w.t1 - w.t0, 0);
+      await(&q_full, piece++ & 1);
+      scores(n);
+      for (int u = 0; u < units; ++u, ++n) {
+        if (u + 1 < units) scores(n + 1);
+        await(&p_full[n & 1], (n >> 1) & 1);
+        if (!good) break;
+        tc_fence_after();
+        const uint32_t keep = u > 0 ? 1u : (uint32_t)__shfl_sync(0xffffffffu, s_keep[n & 1], 0);
+        const uint64_t d = dv + (uint64_t)(n % S::kStages * (S::kStage >> 4));
+        const uint32_t t = utmem + S::kS + 64 * (n & 1);
+        if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < kTile / 16; ++k)
-            umma_bf16_tmem_a(tmem + S::kO, tmem + S::kS + 64 * (n & 1) + 8 * k, sw128_desc_mn(vs + 2048 * k, S::kBox),
-                             id_o, keep || k > 0);
+            umma_bf16_tmem_a(utmem + S::kO, t + 8 * k, d + (2048 * k >> 4), id_o, k > 0 ? 1u : keep);
           umma_commit(&empty[n % S::kStages]);
           umma_commit(&o_done);
         }
+        __syncwarp();
       }
-      if (!ok) {   // an expired wait: what was issued ends before the CTA does
-        umma_commit(&drain);
-        wait(&drain, 0);
-      }
+    }
+    if (!good) {   // an expired wait: what was issued ends before the CTA does
+      if (elect_one()) umma_commit(&drain);
+      wait(&drain, 0);
     }
     __syncwarp();
   } else {
@@ -171,23 +197,28 @@ __global__ void __launch_bounds__(TcShape<HD>::kThreads, 2) k_paged_attn_tc(cons
       const unsigned long long bits = a.mask && live ? a.mask[r.s0 + j] : 0;
       // The tile's queries, rows past the end as zeros, in the MMA's layout.
       {
-        constexpr int NL = MT * HD / 8 / 128, B = NL < 8 ? NL : 8;
-#pragma unroll
-        for (int y0 = 0; y0 < NL; y0 += B) {
+        constexpr int P = HD / 8, RS = 128 / P;            // 16-byte pieces of a row; rows of a step
+        const int p = tid % P, m0 = tid / P;
+        const uint32_t off = (p >> 3) * S::kQBox + m0 * 128 + (((p & 7) ^ (m0 & 7)) << 4);   // (RS is a multiple of 8)
+        static_assert(RS % 8 == 0, "the swizzle of a thread's rows");
+        int x = w.qt * MT + m0, xj = x / a.group, xh = x - xj * a.group;
+        constexpr int B = 8;                               // loads in flight
+        for (int y0 = 0; y0 < MT / RS; y0 += B) {
           uint4 f[B];
 #pragma unroll
           for (int y = 0; y < B; ++y) {
-            const int e = tid + (y0 + y) * 128, m = e / (HD / 8), d = 8 * (e - m * (HD / 8));
-            const int x = w.qt * MT + m, jj = x / a.group, xh = w.kvh * a.group + x - jj * a.group;
             f[y] = make_uint4(0u, 0u, 0u, 0u);
-            if (x < Mq)
-              f[y] = *reinterpret_cast<const uint4*>(static_cast<const TC*>(a.q) + (r.s0 + jj) * a.q_row + xh * a.q_head + d);
+            if (x < Mq) {
+              f[y] = *reinterpret_cast<const uint4*>(static_cast<const TC*>(a.q) + (r.s0 + xj) * a.q_row +
+                                                     (w.kvh * a.group + xh) * a.q_head + 8 * p);
+              x += RS;
+              for (xh += RS; xh >= a.group; xh -= a.group) ++xj;
+            }
           }
 #pragma unroll
           for (int y = 0; y < B; ++y) {
-            const int e = tid + (y0 + y) * 128, m = e / (HD / 8), p = e - m * (HD / 8);
             f[y].x ^= a.flip, f[y].y ^= a.flip, f[y].z ^= a.flip, f[y].w ^= a.flip;
-            *reinterpret_cast<uint4*>(sq + (p >> 3) * S::kQBox + m * 128 + (((p & 7) ^ (m & 7)) << 4)) = f[y];
+            *reinterpret_cast<uint4*>(sq + off + (y0 + y) * RS * 128) = f[y];
           }
         }
         fence_proxy_async();
