@@ -2,11 +2,12 @@
 // heads that share the KV head), on the tcgen05 tensor cores: tiles of 128
 // queries, 16-bit queries. The work is dealt out as in paged_attn.cuh; beside
 // the producer warp a CTA has
-//   * one MMA thread: S = Q K^T (128 x 64, queries and keys in shared memory)
-//     and O += P V (P in tensor memory, values in shared memory with the slots
-//     as the MMA's K side), both accumulators in tensor memory. S of the next
-//     unit is computed while the softmax works on this one: two S buffers of 64
-//     columns, P of a unit lying over its S; O takes head_dim columns;
+//   * an MMA warp: S = Q K^T (128 x 64, queries and keys in shared memory) and
+//     O += P V (P in tensor memory, values in shared memory with the slots as
+//     the MMA's K side), accumulators in tensor memory. Scores are computed two
+//     units ahead, as soon as the softmax has read the S that they replace;
+//     computed only one ahead, they came at the end of the softmax's work on a
+//     unit and held up its store of P by 450 cycles;
 //   * four softmax warps, a thread per query row: row maximum and sum without
 //     shuffles. O is rescaled only when a row's maximum has grown by more than
 //     2^8 since its reference was set (probabilities then stay below 256, which
@@ -38,9 +39,10 @@ struct TcShape {
   static constexpr int kCtas = HD == 64 ? 2 : 1;
   static constexpr int kStages = ((kCtas == 2 ? kHalfSmBytes : 224 * 1024) - 1024 - kQ) / kStage;
   static constexpr int kSmem = 1024 + kQ + kStages * kStage;
-  static constexpr int kCols = 256;                    // tensor-memory columns: O, S0, S1
-  static constexpr int kO = 0, kS = 128;               // (S b at kS + 64 b)
-  static_assert(kStages >= 2, "two units in flight");
+  // Tensor-memory columns: O, two S, two P.
+  static constexpr int kO = 0, kS = HD, kP = HD + 128;   // (S b at kS + 64 b, P b at kP + 32 b)
+  static constexpr int kCols = HD == 64 ? 256 : 512;
+  static_assert(kP + 64 <= kCols && kStages >= 3, "three units at a time");
 };
 
 // B operand with the slots as K: rows of 128 bytes are 64 dimensions of one
@@ -74,7 +76,7 @@ __global__ void __launch_bounds__(TcShape<HD>::kThreads, TcShape<HD>::kCtas) k_p
   unsigned char* sq = pa_smem_raw + ((1024 - (smem_u32(pa_smem_raw) & 1023)) & 1023);   // queries
   unsigned char* ring = sq + S::kQ;
   __shared__ long sh_loc[S::kThreads / 32 + 2];
-  __shared__ __align__(8) uint64_t full[S::kStages], empty[S::kStages], s_full[2], p_full[2], o_done, q_full, drain;
+  __shared__ __align__(8) uint64_t full[S::kStages], empty[S::kStages], s_full[2], s_free[2], p_full[2], o_done[2], q_full, drain;
   __shared__ uint32_t s_tmem;
   __shared__ int s_keep[2];     // the unit adds to what the softmax put into O (see odd values)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -85,10 +87,11 @@ __global__ void __launch_bounds__(TcShape<HD>::kThreads, TcShape<HD>::kCtas) k_p
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&s_full[b], 1);
+      mbar_init(&s_free[b], 4);
       mbar_init(&p_full[b], 4);
+      mbar_init(&o_done[b], 1);
       s_keep[b] = 0;
     }
-    mbar_init(&o_done, 1);
     mbar_init(&q_full, 4);
     mbar_init(&drain, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -150,21 +153,25 @@ __global__ void __launch_bounds__(TcShape<HD>::kThreads, TcShape<HD>::kCtas) k_p
     while (__shfl_sync(0xffffffffu, (int)(good && w.next(a)), 0)) {
       const int units = __shfl_sync(0xffffffffu, w.t1 - w.t0, 0);
       await(&q_full, piece++ & 1);
-      scores(n);
+      scores(n);   // (both S are free: the units before have handed over their P)
+      if (units > 1) scores(n + 1);
       for (int u = 0; u < units; ++u, ++n) {
-        if (u + 1 < units) scores(n + 1);
+        if (u + 2 < units) {
+          await(&s_free[n & 1], (n >> 1) & 1);
+          scores(n + 2);
+        }
         await(&p_full[n & 1], (n >> 1) & 1);
         if (!good) break;
         tc_fence_after();
         const uint32_t keep = u > 0 ? 1u : (uint32_t)__shfl_sync(0xffffffffu, s_keep[n & 1], 0);
         const uint64_t d = dv + (uint64_t)(n % S::kStages * (S::kStage >> 4));
-        const uint32_t t = utmem + S::kS + 64 * (n & 1);
+        const uint32_t t = utmem + S::kP + 32 * (n & 1);
         if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < kTile / 16; ++k)
             umma_bf16_tmem_a(utmem + S::kO, t + 8 * k, d + (2048 * k >> 4), id_o, k > 0 ? 1u : keep);
           umma_commit(&empty[n % S::kStages]);
-          umma_commit(&o_done);
+          umma_commit(&o_done[n & 1]);
         }
         __syncwarp();
       }
@@ -181,11 +188,14 @@ __global__ void __launch_bounds__(TcShape<HD>::kThreads, TcShape<HD>::kCtas) k_p
     auto sync4 = [] { asm volatile("bar.sync 1, 128;" ::: "memory"); };
     int n = 0, o_seen = 0;
     // Waits for the output products up to unit k. A parity tells neighbouring
-    // phases apart only, so no warp may fall two behind: each waits for the
-    // product of a unit before it hands over the next one's probabilities.
+    // phases apart only, so no warp may fall two behind on a barrier: there
+    // are two in turn, and before a warp hands over a unit's probabilities it
+    // has waited for the product two units before (waiting for the one just
+    // before cost 450 cycles a unit: its arrival comes with the scores that
+    // were issued behind it).
     auto o_upto = [&](int k) {
       for (; o_seen <= k; ++o_seen)
-        if (ok && !wait(&o_done, o_seen & 1)) ok = false;
+        if (ok && !wait(&o_done[o_seen & 1], (o_seen >> 1) & 1)) ok = false;
       ok = __all_sync(0xffffffffu, ok);
       tc_fence_after();
     };
@@ -244,6 +254,9 @@ __global__ void __launch_bounds__(TcShape<HD>::kThreads, TcShape<HD>::kCtas) k_p
             x[i] = __uint_as_float(v[i >> 4][i & 15]);
           }
         }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s_free[b]);
         // ---- what the row does not see is -infinity
         unsigned long long vis = ~0ull;
         if (tail) {
@@ -375,16 +388,16 @@ __global__ void __launch_bounds__(TcShape<HD>::kThreads, TcShape<HD>::kCtas) k_p
           }
           fence_proxy_async();
         }
-        // ---- probabilities over the scores, in the cache's type
+        // ---- probabilities, in the cache's type
         if (warp_live) {
           uint32_t p[32];
 #pragma unroll
           for (int i = 0; i < 32; ++i) p[i] = Num<TC>::pack(x[2 * i], x[2 * i + 1]);
-          tmem_st32(lanes + S::kS + 64 * b, p);
+          tmem_st32(lanes + S::kP + 32 * b, p);
           tmem_st_wait();
         }
         if (tid == 0) s_keep[b] = keep;
-        o_upto(n - 1);
+        o_upto(n - 2);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[b]);
