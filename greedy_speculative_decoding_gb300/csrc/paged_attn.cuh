@@ -102,8 +102,7 @@ struct Deal {
 
 // Wait on an mbarrier phase; false after a second without it (the copies and
 // products waited for take microseconds).
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
-  if (mbar_wait(bar, parity, 32)) return true;
+static __device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity) {
   uint64_t t0, t;
   asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
   do {
@@ -111,6 +110,12 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
     asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
   } while (t - t0 < kWaitNs);
   return false;
+}
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
+#pragma unroll 1
+  for (int i = 0; i < 64; ++i)
+    if (mbar_wait(bar, parity, 1)) return true;
+  return wait_long(bar, parity);   // (out of line: a call costs nothing then)
 }
 
 template <typename T>

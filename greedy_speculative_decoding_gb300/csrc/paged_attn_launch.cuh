@@ -15,7 +15,7 @@ namespace pa {
 // a tile (their three terms are computed with mma.sync).
 inline int tile_of(int queries, bool f32) { return queries <= 16 ? 16 : queries <= 32 || f32 ? 32 : 128; }
 
-// Launch a main kernel (two CTAs an SM) and the join.
+// Launch a main kernel (`ctas` CTAs an SM) and the join.
 template <int HD, typename TQ, int MT>
 cudaError_t launch(void (*fn)(Args), int threads, int smem, std::atomic<uint64_t>& ready, Args& a, int sms, int ctas,
                    long max_units, cudaStream_t st) {

@@ -2,12 +2,12 @@
 // heads that share the KV head), on the tcgen05 tensor cores: tiles of 128
 // queries, 16-bit queries. The work is dealt out as in paged_attn.cuh; beside
 // the producer warp a CTA has
-//   * an MMA warp: S = Q K^T (128 x 64, queries and keys in shared memory) and
-//     O += P V (P in tensor memory, values in shared memory with the slots as
-//     the MMA's K side), accumulators in tensor memory. Scores are computed two
-//     units ahead, as soon as the softmax has read the S that they replace;
-//     computed only one ahead, they came at the end of the softmax's work on a
-//     unit and held up its store of P by 450 cycles;
+//   * an MMA warp: S = Q K^T (128 x 64) and O += P V, queries, probabilities
+//     and both accumulators in tensor memory, keys and values in shared memory
+//     (the values with the slots as the MMA's K side). Queries in shared memory
+//     took all its bandwidth during S. The scores of a unit come behind the
+//     output of the one two before, whose S and P they replace: a unit's scores
+//     there means that output complete;
 //   * four softmax warps, a thread per query row: row maximum and sum without
 //     shuffles. O is rescaled only when a row's maximum has grown by more than
 //     2^8 since its reference was set (probabilities then stay below 256, which
@@ -31,18 +31,14 @@ struct TcShape {
   static constexpr int kHalf = HD / 64;
   static constexpr int kBox = kTile * 128;
   static constexpr int kStage = 2 * kHalf * kBox;
-  static constexpr int kQBox = MT * 128;               // 64 dimensions of the queries
-  static constexpr int kQ = kHalf * kQBox;
-  // Two CTAs an SM where their rings hold the units in flight that the memory
-  // needs; at head dimension 128 the queries leave room for two units each,
-  // and one CTA with six does better.
-  static constexpr int kCtas = HD == 64 ? 2 : 1;
-  static constexpr int kStages = ((kCtas == 2 ? kHalfSmBytes : 224 * 1024) - 1024 - kQ) / kStage;
-  static constexpr int kSmem = 1024 + kQ + kStages * kStage;
-  // Tensor-memory columns: O, two S, two P.
-  static constexpr int kO = 0, kS = HD, kP = HD + 128;   // (S b at kS + 64 b, P b at kP + 32 b)
-  static constexpr int kCols = HD == 64 ? 256 : 512;
-  static_assert(kP + 64 <= kCols && kStages >= 3, "three units at a time");
+  // Tensor-memory columns (32 bits): O, two S (P of a unit over its S), the
+  // queries. At head dimension 64 two CTAs share an SM (the softmax of one
+  // alone takes longer than its units' bytes).
+  static constexpr int kO = 0, kS = HD, kQ = HD + 128;   // (S b at kS + 64 b)
+  static constexpr int kCols = HD == 64 ? 256 : 512, kCtas = HD == 64 ? 2 : 1;
+  static constexpr int kStages = 6;
+  static constexpr int kSmem = 1024 + kStages * kStage;
+  static_assert(kQ + HD / 2 <= kCols, "tensor memory");
 };
 
 // B operand with the slots as K: rows of 128 bytes are 64 dimensions of one
@@ -73,10 +69,9 @@ __global__ void __launch_bounds__(TcShape<HD>::kThreads, TcShape<HD>::kCtas) k_p
   using S = TcShape<HD>;
   constexpr int MT = S::MT;
   extern __shared__ unsigned char pa_smem_raw[];
-  unsigned char* sq = pa_smem_raw + ((1024 - (smem_u32(pa_smem_raw) & 1023)) & 1023);   // queries
-  unsigned char* ring = sq + S::kQ;
+  unsigned char* ring = pa_smem_raw + ((1024 - (smem_u32(pa_smem_raw) & 1023)) & 1023);
   __shared__ long sh_loc[S::kThreads / 32 + 2];
-  __shared__ __align__(8) uint64_t full[S::kStages], empty[S::kStages], s_full[2], s_free[2], p_full[2], o_done[2], q_full, drain;
+  __shared__ __align__(8) uint64_t full[S::kStages], empty[S::kStages], s_full[2], p_full[2], o_done[2], q_full, drain;
   __shared__ uint32_t s_tmem;
   __shared__ int s_keep[2];     // the unit adds to what the softmax put into O (see odd values)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -87,7 +82,6 @@ __global__ void __launch_bounds__(TcShape<HD>::kThreads, TcShape<HD>::kCtas) k_p
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&s_full[b], 1);
-      mbar_init(&s_free[b], 4);
       mbar_init(&p_full[b], 4);
       mbar_init(&o_done[b], 1);
       s_keep[b] = 0;
@@ -127,7 +121,6 @@ __global__ void __launch_bounds__(TcShape<HD>::kThreads, TcShape<HD>::kCtas) k_p
     // (moving them there for every MMA took 100 cycles an MMA).
     constexpr uint32_t id_s = tc_idesc<TC>(MT, kTile, false), id_o = tc_idesc<TC>(MT, HD, true);
     const uint32_t utmem = __shfl_sync(0xffffffffu, tmem, 0);
-    const uint64_t dq = sw128_desc(__shfl_sync(0xffffffffu, smem_u32(sq), 0));
     const uint64_t dk = sw128_desc(__shfl_sync(0xffffffffu, smem_u32(ring), 0));
     const uint64_t dv = sw128_desc_mn(__shfl_sync(0xffffffffu, smem_u32(ring) + S::kHalf * S::kBox, 0), S::kBox);
     bool good = true;
@@ -143,8 +136,7 @@ __global__ void __launch_bounds__(TcShape<HD>::kThreads, TcShape<HD>::kCtas) k_p
       if (elect_one()) {
 #pragma unroll
         for (int k = 0; k < HD / 16; ++k)
-          umma_bf16(t, dq + (((k >> 2) * S::kQBox + 32 * (k & 3)) >> 4), d + (((k >> 2) * S::kBox + 32 * (k & 3)) >> 4),
-                    id_s, k > 0);
+          umma_bf16_tmem_a(t, utmem + S::kQ + 8 * k, d + (((k >> 2) * S::kBox + 32 * (k & 3)) >> 4), id_s, k > 0);
         umma_commit(&s_full[n & 1]);
       }
       __syncwarp();
@@ -153,19 +145,16 @@ __global__ void __launch_bounds__(TcShape<HD>::kThreads, TcShape<HD>::kCtas) k_p
     while (__shfl_sync(0xffffffffu, (int)(good && w.next(a)), 0)) {
       const int units = __shfl_sync(0xffffffffu, w.t1 - w.t0, 0);
       await(&q_full, piece++ & 1);
+      tc_fence_after();
       scores(n);   // (both S are free: the units before have handed over their P)
       if (units > 1) scores(n + 1);
       for (int u = 0; u < units; ++u, ++n) {
-        if (u + 2 < units) {
-          await(&s_free[n & 1], (n >> 1) & 1);
-          scores(n + 2);
-        }
         await(&p_full[n & 1], (n >> 1) & 1);
         if (!good) break;
         tc_fence_after();
         const uint32_t keep = u > 0 ? 1u : (uint32_t)__shfl_sync(0xffffffffu, s_keep[n & 1], 0);
         const uint64_t d = dv + (uint64_t)(n % S::kStages * (S::kStage >> 4));
-        const uint32_t t = utmem + S::kP + 32 * (n & 1);
+        const uint32_t t = utmem + S::kS + 64 * (n & 1);
         if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < kTile / 16; ++k)
@@ -174,6 +163,7 @@ __global__ void __launch_bounds__(TcShape<HD>::kThreads, TcShape<HD>::kCtas) k_p
           umma_commit(&o_done[n & 1]);
         }
         __syncwarp();
+        if (u + 2 < units) scores(n + 2);
       }
     }
     if (!good) {   // an expired wait: what was issued ends before the CTA does
@@ -186,16 +176,12 @@ __global__ void __launch_bounds__(TcShape<HD>::kThreads, TcShape<HD>::kCtas) k_p
     const int row = tid;                                  // query of the tile = tensor-memory lane
     const uint32_t lanes = tmem + ((uint32_t)(32 * warp) << 16);
     auto sync4 = [] { asm volatile("bar.sync 1, 128;" ::: "memory"); };
-    int n = 0, o_seen = 0;
-    // Waits for the output products up to unit k. A parity tells neighbouring
-    // phases apart only, so no warp may fall two behind on a barrier: there
-    // are two in turn, and before a warp hands over a unit's probabilities it
-    // has waited for the product two units before (waiting for the one just
-    // before cost 450 cycles a unit: its arrival comes with the scores that
-    // were issued behind it).
-    auto o_upto = [&](int k) {
-      for (; o_seen <= k; ++o_seen)
-        if (ok && !wait(&o_done[o_seen & 1], (o_seen >> 1) & 1)) ok = false;
+    int n = 0;
+    // Waits for unit k's output, k the unit before the one at hand. (Two
+    // barriers in turn: at that point the barrier is in unit k's phase or the
+    // next, never further, so that the parity tells.)
+    auto o_wait = [&](int k) {
+      if (ok && !wait(&o_done[k & 1], (k >> 1) & 1)) ok = false;
       ok = __all_sync(0xffffffffu, ok);
       tc_fence_after();
     };
@@ -205,40 +191,33 @@ __global__ void __launch_bounds__(TcShape<HD>::kThreads, TcShape<HD>::kCtas) k_p
       const int q = w.qt * MT + row, j = q / a.group, hh = w.kvh * a.group + q - j * a.group;
       const bool live = q < Mq, warp_live = w.qt * MT + 32 * warp < Mq;
       const unsigned long long bits = a.mask && live ? a.mask[r.s0 + j] : 0;
-      // The tile's queries, rows past the end as zeros, in the MMA's layout.
-      {
-        constexpr int P = HD / 8, RS = 128 / P;            // 16-byte pieces of a row; rows of a step
-        const int p = tid % P, m0 = tid / P;
-        const uint32_t off = (p >> 3) * S::kQBox + m0 * 128 + (((p & 7) ^ (m0 & 7)) << 4);   // (RS is a multiple of 8)
-        static_assert(RS % 8 == 0, "the swizzle of a thread's rows");
-        int x = w.qt * MT + m0, xj = x / a.group, xh = x - xj * a.group;
-        constexpr int B = 8;                               // loads in flight
-        for (int y0 = 0; y0 < MT / RS; y0 += B) {
-          uint4 f[B];
+      // The row's query (rows past the end: zeros).
+      if (warp_live) {
+        const TC* src = static_cast<const TC*>(a.q) + (r.s0 + j) * a.q_row + hh * a.q_head;
 #pragma unroll
-          for (int y = 0; y < B; ++y) {
-            f[y] = make_uint4(0u, 0u, 0u, 0u);
-            if (x < Mq) {
-              f[y] = *reinterpret_cast<const uint4*>(static_cast<const TC*>(a.q) + (r.s0 + xj) * a.q_row +
-                                                     (w.kvh * a.group + xh) * a.q_head + 8 * p);
-              x += RS;
-              for (xh += RS; xh >= a.group; xh -= a.group) ++xj;
-            }
-          }
+        for (int c = 0; c < HD / 64; ++c) {
+          uint32_t v[32];
 #pragma unroll
-          for (int y = 0; y < B; ++y) {
-            f[y].x ^= a.flip, f[y].y ^= a.flip, f[y].z ^= a.flip, f[y].w ^= a.flip;
-            *reinterpret_cast<uint4*>(sq + off + (y0 + y) * RS * 128) = f[y];
+          for (int i = 0; i < 8; ++i) {
+            uint4 f = make_uint4(0u, 0u, 0u, 0u);
+            if (live) f = *reinterpret_cast<const uint4*>(src + 64 * c + 8 * i);
+            v[4 * i] = f.x ^ a.flip, v[4 * i + 1] = f.y ^ a.flip, v[4 * i + 2] = f.z ^ a.flip, v[4 * i + 3] = f.w ^ a.flip;
           }
+          __syncwarp();
+          tmem_st32(lanes + S::kQ + 32 * c, v);
         }
-        fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&q_full);
+        tmem_st_wait();
       }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&q_full);
       float m = -INFINITY, l = 0.f;
-      for (int t = w.t0; t < w.t1; ++t, ++n) {
+      // One unit: every row sees all slots of a plain one; a tail unit holds
+      // slots of the pass itself, or slots past the end. (Apart, so that the
+      // plain units' loop is short straight code.)
+      auto unit = [&](auto kind, int t) {
+        constexpr bool TAIL = decltype(kind)::value;
         const int b = n & 1;
-        const bool tail = t * kTile + kTile > min(r.p0, r.len);
         if (ok && !wait(&s_full[b], (n >> 1) & 1)) ok = false;
         ok = __all_sync(0xffffffffu, ok);
         tc_fence_after();
@@ -254,12 +233,9 @@ __global__ void __launch_bounds__(TcShape<HD>::kThreads, TcShape<HD>::kCtas) k_p
             x[i] = __uint_as_float(v[i >> 4][i & 15]);
           }
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&s_free[b]);
         // ---- what the row does not see is -infinity
         unsigned long long vis = ~0ull;
-        if (tail) {
+        if constexpr (TAIL) {
           const int first = r.p0 - t * kTile;             // the pass's first slot, within the unit
           auto low = [](int k) { return k <= 0 ? 0ull : k >= 64 ? ~0ull : (1ull << k) - 1; };
           vis = low(first + j + 1);
@@ -282,7 +258,7 @@ __global__ void __launch_bounds__(TcShape<HD>::kThreads, TcShape<HD>::kCtas) k_p
             const float f = grow ? exp2_approx((m - mx) * a.scale2) : 1.f;
             if (grow) m = mx;
             l *= f;
-            o_upto(n - 1);   // (never at the piece's first unit: m was -infinity)
+            o_wait(n - 1);   // (never at the piece's first unit: m was -infinity)
 #pragma unroll 1
             for (int c = 0; c < HD / 16; ++c) {
               uint32_t v[16];
@@ -311,7 +287,7 @@ __global__ void __launch_bounds__(TcShape<HD>::kThreads, TcShape<HD>::kCtas) k_p
         // the pass that are no finite numbers (odd: a probability 0 times NaN
         // is NaN) are added to O here for the rows that see them, and become 0.
         int keep = 0;
-        if (tail) {
+        if constexpr (TAIL) {
           unsigned char* vs = ring + n % S::kStages * S::kStage + S::kHalf * S::kBox;
           if (ok && !wait(&full[n % S::kStages], (n / S::kStages) & 1)) ok = false;
           ok = __all_sync(0xffffffffu, ok);
@@ -343,7 +319,7 @@ __global__ void __launch_bounds__(TcShape<HD>::kThreads, TcShape<HD>::kCtas) k_p
 #pragma unroll
                 for (int i = 0; i < kTile; ++i) p[i] = x[i];
                 const bool fresh = t == w.t0;
-                o_upto(n - 1);
+                if (!fresh) o_wait(n - 1);
 #pragma unroll 1
                 for (int c = 0; c < HD / 16; ++c) {
                   uint32_t v[16];
@@ -393,18 +369,22 @@ __global__ void __launch_bounds__(TcShape<HD>::kThreads, TcShape<HD>::kCtas) k_p
           uint32_t p[32];
 #pragma unroll
           for (int i = 0; i < 32; ++i) p[i] = Num<TC>::pack(x[2 * i], x[2 * i + 1]);
-          tmem_st32(lanes + S::kP + 32 * b, p);
+          tmem_st32(lanes + S::kS + 64 * b, p);
           tmem_st_wait();
         }
-        if (tid == 0) s_keep[b] = keep;
-        o_upto(n - 2);
+        if (tid == 0 && t == w.t0) s_keep[b] = keep;   // (the MMA warp reads it at a piece's first unit)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[b]);
-      }
+        ++n;
+      };
+      const int plain = max(0, min(r.p0, r.len)) / kTile;   // units whose slots every row sees
+      int t = w.t0;
+      for (; t < min(w.t1, plain); ++t) unit(std::false_type{}, t);
+      for (; t < w.t1; ++t) unit(std::true_type{}, t);
 
       // ---- the end of the piece
-      o_upto(n - 1);
+      o_wait(n - 1);
       if (!ok) l = __int_as_float(0x7fc00000);   // an expired wait: NaN
       if (m != -INFINITY) m *= a.scale2;
       const bool begins = w.t0 == 0, whole = begins && w.t1 == r.nt;
