@@ -77,9 +77,18 @@ static Sizes sizes(const sf_paged_cache& c, int n_heads, int max_rows, int q_dty
   auto items = [&](int mt) { return (long)batch * c.n_kv_heads * ((queries + mt - 1) / mt); };
   // A smaller tile where the larger one's units could not occupy the GPU even
   // if every request filled its table: the cache is then read once for each
-  // tile (from L2), by CTAs that would be idle.
+  // tile (from L2), by CTAs that would be idle. The tcgen05 kernel also starts
+  // more slowly, which shows at head dimension 64 with its small units: 16
+  // requests of 4099 tokens with 91 queries (2080 units) take 19.3 us with it
+  // and 15.4 in tiles of 32, of 8192 tokens and eight KV heads with 128 queries
+  // (16384 units) 57 and 93 us. At head dimension 128 it wins from 128 units a
+  // KV head: 8 requests of 1000 tokens with 45 queries take 16 and 22 us.
   z.mt = tile_of(queries, q_dtype == SF_DT_F32);
-  while (z.mt > 16 && items(z.mt) * z.units < 2 * sms) z.mt = z.mt == 128 ? 32 : 16;
+  auto few = [&](int mt) {
+    const long total = items(mt) * z.units;
+    return total < 2 * sms || (mt == 128 && c.head_dim == 64 && total < 4096);
+  };
+  while (z.mt > 16 && few(z.mt)) z.mt = z.mt == 128 ? 32 : 16;
   z.ntq = (queries + z.mt - 1) / z.mt;
   z.items = items(z.mt);
   return z;
@@ -114,7 +123,7 @@ static cudaError_t enqueue(Args& a, const sf_paged_cache& c, int q_dtype, float 
   a.part_ml = reinterpret_cast<float2*>(ws + lay.ml);
   a.part = reinterpret_cast<float*>(ws + lay.part);
   const long max_units = z.items * z.units;
-  a.by_warp = a.B <= 32 * kChunks && max_units <= INT32_MAX;
+  a.by_warp = a.B <= 32 && max_units <= INT32_MAX;
   sms = std::min(sms, kMaxCtas / 2);
   return c.head_dim == 128 ? launch_hd128(a, q_dtype, sms, max_units, st) : launch_hd64(a, q_dtype, sms, max_units, st);
 }

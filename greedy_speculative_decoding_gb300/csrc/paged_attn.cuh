@@ -208,58 +208,34 @@ struct Start {
   Request r;    // request b
 };
 
-// Every warp by itself, for at most 32 * kChunks requests and 2^31 units: the
-// first copies need not wait for the other warps.
-constexpr int kChunks = 4;
+// Every warp by itself, for at most 32 requests and 2^31 units: the first
+// copies need not wait for the other warps.
 template <int MT>
 __device__ __forceinline__ Start locate_warp(const Args& a) {
   const int lane = threadIdx.x & 31;
-  Request r[kChunks];
-  int incl[kChunks], n[kChunks], T = 0;
+  Request r{};
+  if (lane < a.B) r = request<MT>(a, lane);
+  const int n = a.nkv * r.ntq * r.nt;
+  int incl = n;
 #pragma unroll
-  for (int c = 0; c < kChunks; ++c) {
-    n[c] = 0;
-    if (32 * c + lane < a.B) {
-      r[c] = request<MT>(a, 32 * c + lane);
-      n[c] = a.nkv * r[c].ntq * r[c].nt;
-    }
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += x;
   }
-#pragma unroll
-  for (int c = 0; c < kChunks; ++c) {
-    incl[c] = n[c];
-    if (c > 0 && 32 * c >= a.B) continue;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int x = __shfl_up_sync(0xffffffffu, incl[c], o);
-      if (lane >= o) incl[c] += x;
-    }
-    incl[c] += T;
-    T = __shfl_sync(0xffffffffu, incl[c], 31);
-  }
-  Start s;
+  const int T = __shfl_sync(0xffffffffu, incl, 31);
+  Start s{};
   s.T = T;
-  s.base = 0;
-  s.b = 0;
   const long G = min((long)gridDim.x, s.T);
   if ((long)blockIdx.x >= G) return s;
   const int u0 = (int)Deal(T, G).first(blockIdx.x);
-  bool found = false;
-#pragma unroll
-  for (int c = 0; c < kChunks; ++c) {
-    if (found || (c > 0 && 32 * c >= a.B)) continue;
-    const unsigned past = __ballot_sync(0xffffffffu, incl[c] > u0);
-    if (!past) continue;
-    found = true;
-    const int l = __ffs(past) - 1;
-    s.b = 32 * c + l;
-    s.base = __shfl_sync(0xffffffffu, incl[c] - n[c], l);
-    s.r.s0 = __shfl_sync(0xffffffffu, r[c].s0, l);
-    s.r.rows = __shfl_sync(0xffffffffu, r[c].rows, l);
-    s.r.len = __shfl_sync(0xffffffffu, r[c].len, l);
-    s.r.p0 = __shfl_sync(0xffffffffu, r[c].p0, l);
-    s.r.nt = __shfl_sync(0xffffffffu, r[c].nt, l);
-    s.r.ntq = __shfl_sync(0xffffffffu, r[c].ntq, l);
-  }
+  s.b = __ffs(__ballot_sync(0xffffffffu, incl > u0)) - 1;
+  s.base = __shfl_sync(0xffffffffu, incl - n, s.b);
+  s.r.s0 = __shfl_sync(0xffffffffu, r.s0, s.b);
+  s.r.rows = __shfl_sync(0xffffffffu, r.rows, s.b);
+  s.r.len = __shfl_sync(0xffffffffu, r.len, s.b);
+  s.r.p0 = __shfl_sync(0xffffffffu, r.p0, s.b);
+  s.r.nt = __shfl_sync(0xffffffffu, r.nt, s.b);
+  s.r.ntq = __shfl_sync(0xffffffffu, r.ntq, s.b);
   return s;
 }
 

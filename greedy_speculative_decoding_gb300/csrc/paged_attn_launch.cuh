@@ -31,7 +31,8 @@ cudaError_t launch(void (*fn)(Args), int threads, int smem, std::atomic<uint64_t
   }
   const long most = (long)sms * ctas, items = (long)a.B * a.nkv * a.ntq_max;
   const int grid = (int)(max_units < most ? max_units : most);
-  a.wide = items * 8 <= grid;   // an item's parts: one and as many as CTAs share it
+  // Many parts an item, and not so many queries that their CTAs come in waves.
+  a.wide = items * 8 <= grid && items * a.mt_max <= 1024;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
