@@ -3,9 +3,10 @@
 // Bound by memory: every projected element is read once and written once. A
 // thread takes eight elements of the lower half of one head and the eight
 // they are paired with (16-byte accesses): few registers, so that as many
-// loads as possible are in flight. 16411 bf16 rows of 36 heads of 128: 58 us
-// (5.3 TB/s) with eight CTAs of 256 threads on an SM, 70 us with five; two
-// heads a thread, the rotation loaded once, was slower (78 us).
+// loads as possible are in flight. 16411 bf16 rows of 36 heads of 128: 56 us
+// (5.5 TB/s) with all threads of an SM in CTAs of 128, 58 us in CTAs of 256,
+// 69 of 1024, 70 with five CTAs of 256; two heads a thread, the rotation loaded
+// once, was slower (78 us).
 #include <cmath>
 #include <type_traits>
 
@@ -14,7 +15,7 @@
 namespace sf {
 namespace {
 
-constexpr int kAppendThreads = 256;
+constexpr int kAppendThreads = 128;
 
 struct AppendArgs {
   const void *q, *k, *v;
@@ -73,7 +74,7 @@ struct Raw<float> {
 
 // TI: type of the rows; TC: of the cache; TO: of q_out.
 template <typename TI, typename TC, typename TO>
-__global__ void __launch_bounds__(kAppendThreads, sizeof(TI) == 2 ? 8 : 5)
+__global__ void __launch_bounds__(kAppendThreads, sizeof(TI) == 2 ? 16 : 10)
     k_append(const __grid_constant__ AppendArgs a) {
   const int half = a.hd >> 1;
   const unsigned per_head = half >> 3;                              // threads of a head
