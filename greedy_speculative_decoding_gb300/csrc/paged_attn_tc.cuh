@@ -10,13 +10,19 @@
 //     there means that output complete;
 //   * four softmax warps, a thread per query row: row maximum and sum without
 //     shuffles. O is rescaled only when a row's maximum has grown by more than
-//     2^8 since its reference was set (probabilities then stay below 256, which
-//     costs no precision in floating point), so seldom after the first unit.
+//     2^8 since its reference was set (probabilities then stay below 256), so
+//     seldom after the first unit. Probabilities are rounded to the cache's
+//     type, by half a step each; with a lagging reference that includes the
+//     largest, which is exactly 1 in the mma.sync kernel.
 //
 // mma.sync reaches 590 TFLOP/s on this GPU (measured, four or more warps an
-// SM), where the 45 queries of a 9-row verify at 5 heads per KV head need
-// about 800 to keep up with the cache's bytes; tcgen05 leaves the memory as
-// the bound.
+// SM); the 45 queries of a 9-row verify with 5 heads per KV head, padded to 48,
+// need 430 of them to keep up with the cache's bytes, 128 queries 1150. A unit
+// takes 1.07 thousand cycles here (600 the softmax warps' arithmetic: 64
+// exponentials a thread are 512 cycles of an SM quarter's unit; the rest
+// waits and hand-overs), its bytes 1.4 thousand at head dimension 128. Eight
+// sequences of 4096 to 8192 tokens, head_dim 128, 128 queries: 49 us (519
+// TFLOP/s; mma.sync in tiles of 64: 85 us), 45 queries: 42 us (46).
 #pragma once
 
 #include "paged_attn.cuh"
@@ -383,7 +389,8 @@ __global__ void __launch_bounds__(TcShape<HD>::kThreads, TcShape<HD>::kCtas) k_p
       for (; t < min(w.t1, plain); ++t) unit(std::false_type{}, t);
       for (; t < w.t1; ++t) unit(std::true_type{}, t);
 
-      // ---- the end of the piece
+      // ---- the end of the piece (both barriers are then past its units)
+      if (w.t1 - w.t0 > 1) o_wait(n - 2);
       o_wait(n - 1);
       if (!ok) l = __int_as_float(0x7fc00000);   // an expired wait: NaN
       if (m != -INFINITY) m *= a.scale2;

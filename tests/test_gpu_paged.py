@@ -12,10 +12,11 @@ paged_attention: with x the scaled scores, p the probabilities and A = sum p|v|
   * a relative error of every probability from its score: fp32 sums of hd
     products (each step may truncate: 2^-23 of the sum of magnitudes, qk), two
     roundings of the score and the exponential's 2^-22, which reach numerator
-    and denominator: eps = 2 (hd + 8) 2^-23 max(qk, 1) + 2^-18 (running sums
-    over at most 1000 pieces at 2^-23 each and rescalings) times A and |out|.
-The logarithm lse is off by eps. Sizes keep the sums under 1000 pieces per
-lane.
+    and denominator; and the running sums, which add a piece for every 8 slots
+    at least, each to 2^-23 of the sum: eps = 2 (hd + 8) 2^-23 max(qk, 1) +
+    n / 8 * 2^-23 for n slots (2^-18 at least, for the rescalings and the join)
+    times A and |out|.
+The logarithm lse is off by eps.
 """
 
 import ctypes
@@ -111,7 +112,7 @@ def test_plan_in_place_and_repeated(pkg, seed):
     check_plan(pkg, case, repeat=3)
 
 
-@pytest.mark.parametrize("B,W,page,tight", [(1, 300, 16, False), (5, 700, 16, True), (200, 30, 64, True), (9, 1, 256, False)])
+@pytest.mark.parametrize("B,W,page,tight", [(150, 120, 16, True), (9, 1500, 32, False), (1, 300, 16, False), (5, 700, 16, True), (200, 30, 64, True), (9, 1, 256, False)])
 def test_plan_of_whole_prompts(pkg, B, W, page, tight):
     check_plan(pkg, plan_case(7 * B, B, W, page, tight, prompts=True))
 
@@ -275,7 +276,8 @@ def check_attn(c, out, lse, scale=None):
     out, lse = out.double().cpu(), lse.double().cpu()
     assert bool((out[~live] == 7).all() and (lse[~live] == 7).all())
     up = 0.0 if c["q"].dtype == F4 else U[c["k"].dtype]
-    eps = 2 * (hd + 8) * 2.0 ** -23 * qk.clamp(min=1.0) + 2.0 ** -18
+    slots = min(max(c["lens"]), len(c["tables"][0]) * c["k"].shape[2])
+    eps = 2 * (hd + 8) * 2.0 ** -23 * qk.clamp(min=1.0) + max(2.0 ** -18, slots / 8 * 2.0 ** -23)
     bound = (up + eps[..., None]) * A + (U[c["q"].dtype] + eps[..., None]) * ref.abs() + TINY[c["q"].dtype]
     err = (out - ref).abs()
     assert bool((err[live] <= bound[live]).all()), float((err / bound)[live].max())
@@ -406,6 +408,30 @@ def test_masked_nan_and_inf_change_nothing(pkg, dq, dc, bad, tree):
     keep = [i for i in range(good.shape[0]) if i not in spoiled]
     assert torch.equal(out[keep], good[keep]) and torch.equal(lse[keep], lgood[keep])
     assert spoiled and not bool(torch.isfinite(out[spoiled][:, 7:]).any())   # head 1: V alone is spoiled
+
+
+@pytest.mark.parametrize("dq,hd,nq,nkv,rows,lens", [
+    (BF, 128, 10, 2, 9, [20011, 64, 9000]), (FH, 64, 14, 2, 13, [9000, 30000]), (BF, 64, 16, 2, 16, [40000]),
+    (BF, 128, 8, 2, 1, [33000, 1, 700]), (F4, 128, 14, 2, 9, [7000]), (BF, 128, 12, 4, 11, [300] * 40)])
+@pytest.mark.parametrize("tree", [False, True])
+def test_long_contexts(pkg, dq, hd, nq, nkv, rows, lens, tree):
+    """Many units a CTA, items shared by many CTAs, several items a CTA."""
+    c = attn_case(rows + hd, lens, [min(n, rows) for n in lens], nq, nkv, hd, 64, dq, BF if dq == F4 else dq, tree=tree)
+    check_attn(c, *call(pkg, c))
+
+
+@pytest.mark.parametrize("dq", [BF, F4])
+@pytest.mark.parametrize("rows", [1, 5, 9])
+@pytest.mark.parametrize("down", [False, True])
+def test_maxima_that_grow_along_the_cache(pkg, dq, rows, down):
+    """Keys grow (or shrink) with the slot, so that the running maximum rises
+    by many powers of two from unit to unit."""
+    n = 2000
+    c = attn_case(31, [n, 130], [rows, rows], 14, 2, 64, 32, dq, BF, q_scale=1.0)
+    f = torch.logspace(2, -2, n, base=10.0) if down else torch.logspace(-2, 2, n, base=10.0)
+    for s in range(n):
+        c["k"][c["tables"][0][s // 32], :, s % 32] *= float(f[s])
+    check_attn(c, *call(pkg, c))
 
 
 def test_large_scores(pkg):
