@@ -190,10 +190,13 @@ struct Shape {
   static constexpr int kQBytes = kQSmem ? (F32 ? 3 : 1) * MT * QP * 2 : 0;
   static constexpr int kOBytes = WK > 1 ? WK * MT * (OP + 2) * 4 : 0;
   static constexpr int kExtra = kQBytes > kOBytes ? kQBytes : kOBytes;   // one region: never both at once
-  static constexpr int kMaxStages = 4;
-  // Two CTAs on an SM when at least two stages fit in half its shared memory.
+  static constexpr int kMaxStages = 6;
+  // Two CTAs on an SM when at least two stages fit in half its shared memory
+  // and the registers do: the 16-bit kernel with two query tiles at head
+  // dimension 128 would spill (8 sequences of 4096 to 8192 tokens, 8 KV heads,
+  // 20 queries: 39.4 us with one CTA, 45.3 with two).
   static constexpr int kFit2 = (kHalfSmBytes - 1024 - kExtra) / kStage;
-  static constexpr int kCtas = kFit2 >= 2 ? 2 : 1;
+  static constexpr int kCtas = kFit2 >= 2 && !(HD == 128 && WK == 2 && !F32) ? 2 : 1;
   static constexpr int kFit1 = (220 * 1024 - 1024 - kExtra) / kStage;
   static constexpr int kFit = kCtas == 2 ? kFit2 : kFit1;
   static constexpr int kStages = kFit < kMaxStages ? kFit : kMaxStages;

@@ -12,7 +12,9 @@ namespace pa {
 // Query tile of a launch, from the queries that a KV head can have in one
 // request (max_rows * group): one m16 tile shared by four warps that split the
 // slots, two by two, or the tcgen05 kernel's 128. fp32 queries take at most 32
-// a tile (their three terms are computed with mma.sync).
+// a tile (their three terms are computed with mma.sync). 8 sequences of 4096 to
+// 8192 tokens, 20 queries a KV head: 25.0 us on mma.sync and 29.4 on tcgen05 at
+// head dimension 64, 39.8 and 40.6 at 128; 45 queries: 46 and 42.
 inline int tile_of(int queries, bool f32) { return queries <= 16 ? 16 : queries <= 32 || f32 ? 32 : 128; }
 
 // Launch a main kernel (`ctas` CTAs an SM) and the join.
