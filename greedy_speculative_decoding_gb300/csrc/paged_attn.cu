@@ -17,7 +17,7 @@ struct Layout {
 };
 static Layout layout(int n_heads, int n_kv_heads, int head_dim, int max_rows) {   // (whatever the tile)
   const int queries = max_rows * (n_heads / n_kv_heads);
-  const size_t mt = std::min(queries, tile_of(queries, false));
+  const size_t mt = std::min(queries, tile_of(queries));
   Layout l;
   l.ml = kMaxDesc * sizeof(int4);
   l.part = l.ml + 2 * kMaxCtas * mt * sizeof(float2);
@@ -82,11 +82,14 @@ static Sizes sizes(const sf_paged_cache& c, int n_heads, int max_rows, int q_dty
   // requests of 4099 tokens with 91 queries (2080 units) take 19.3 us with it
   // and 15.4 in tiles of 32, of 8192 tokens and eight KV heads with 128 queries
   // (16384 units) 57 and 93 us. At head dimension 128 it wins from 128 units a
-  // KV head: 8 requests of 1000 tokens with 45 queries take 16 and 22 us.
-  z.mt = tile_of(queries, q_dtype == SF_DT_F32);
+  // KV head: 8 requests of 1000 tokens with 45 queries take 16 and 22 us. fp32
+  // queries, head dimension 64, 1024 units: 45 queries 19.8 us with it and 18.0
+  // in two tiles of 32, 128 queries 25.2 and in four tiles 29.1.
+  z.mt = tile_of(queries);
   auto few = [&](int mt) {
     const long total = items(mt) * z.units;
-    return total < 2 * sms || (mt == 128 && c.head_dim == 64 && total < 4096);
+    if (mt == 128 && c.head_dim == 64 && (q_dtype == SF_DT_F32 ? items(32) * z.units : total) < 4096) return true;
+    return total < 2 * sms;
   };
   while (z.mt > 16 && few(z.mt)) z.mt = z.mt == 128 ? 32 : 16;
   z.ntq = (queries + z.mt - 1) / z.mt;

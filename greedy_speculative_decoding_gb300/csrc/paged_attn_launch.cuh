@@ -11,11 +11,11 @@ namespace pa {
 
 // Query tile of a launch, from the queries that a KV head can have in one
 // request (max_rows * group): one m16 tile shared by four warps that split the
-// slots, two by two, or the tcgen05 kernel's 128. fp32 queries take at most 32
-// a tile (their three terms are computed with mma.sync). 8 sequences of 4096 to
-// 8192 tokens, 20 queries a KV head: 25.0 us on mma.sync and 29.4 on tcgen05 at
-// head dimension 64, 39.8 and 40.6 at 128; 45 queries: 46 and 42.
-inline int tile_of(int queries, bool f32) { return queries <= 16 ? 16 : queries <= 32 || f32 ? 32 : 128; }
+// slots, two by two, or the tcgen05 kernel's 128. 8 sequences of 4096 to 8192
+// tokens, 16-bit, 20 queries a KV head: 25.0 us on mma.sync and 29.4 on tcgen05
+// at head dimension 64, 39.8 and 40.6 at 128; 45 queries: 46 and 42. fp32: 27
+// queries 58 and 58 us, 45 queries (two tiles) 102 and 64.
+inline int tile_of(int queries) { return queries <= 16 ? 16 : queries <= 32 ? 32 : 128; }
 
 // Launch a main kernel (`ctas` CTAs an SM) and the join.
 template <int HD, typename TQ, int MT>
@@ -61,20 +61,19 @@ cudaError_t launch_mma(Args& a, int sms, long max_units, cudaStream_t st) {
                                max_units, st);
 }
 
-template <int HD, typename TC>
+template <int HD, typename TC, bool F32>
 cudaError_t launch_tc(Args& a, int sms, long max_units, cudaStream_t st) {
-  using S = TcShape<HD>;
+  using S = TcShape<HD, F32>;
+  using TQ = typename std::conditional<F32, float, TC>::type;
   static std::atomic<uint64_t> ready{0};
-  return launch<HD, TC, S::MT>(k_paged_attn_tc<HD, TC>, S::kThreads, S::kSmem, ready, a, sms, S::kCtas,
+  return launch<HD, TQ, S::MT>(k_paged_attn_tc<HD, TC, F32>, S::kThreads, S::kSmem, ready, a, sms, S::kCtas,
                           max_units, st);
 }
 
 template <int HD, typename TC, bool F32>
 cudaError_t launch_tiles(Args& a, int sms, long max_units, cudaStream_t st) {
   if (a.mt == 16) return launch_mma<HD, TC, F32, 1, 4>(a, sms, max_units, st);
-  if constexpr (!F32) {
-    if (a.mt == 128) return launch_tc<HD, TC>(a, sms, max_units, st);
-  }
+  if (a.mt == 128) return launch_tc<HD, TC, F32>(a, sms, max_units, st);
   return launch_mma<HD, TC, F32, 2, 2>(a, sms, max_units, st);
 }
 

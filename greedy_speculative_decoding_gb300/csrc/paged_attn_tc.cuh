@@ -1,7 +1,7 @@
 // Paged attention for many queries per KV head (several rows times the query
 // heads that share the KV head), on the tcgen05 tensor cores: tiles of 128
-// queries, 16-bit queries. The work is dealt out as in paged_attn.cuh; beside
-// the producer warp a CTA has
+// queries. The work is dealt out as in paged_attn.cuh; beside the producer warp
+// a CTA has
 //   * an MMA warp: S = Q K^T (128 x 64) and O += P V, queries, probabilities
 //     and both accumulators in tensor memory, keys and values in shared memory
 //     (the values with the slots as the MMA's K side). Queries in shared memory
@@ -11,9 +11,11 @@
 //   * four softmax warps, a thread per query row: row maximum and sum without
 //     shuffles. O is rescaled only when a row's maximum has grown by more than
 //     2^8 since its reference was set (probabilities then stay below 256), so
-//     seldom after the first unit. Probabilities are rounded to the cache's
-//     type, by half a step each; with a lagging reference that includes the
-//     largest, which is exactly 1 in the mma.sync kernel.
+//     seldom after the first unit. Probabilities of 16-bit queries are rounded
+//     to the cache's type, by half a step each; with a lagging reference that
+//     includes the largest, which is exactly 1 in the mma.sync kernel.
+//   * fp32 queries and their probabilities are three bf16 terms each (24 bits:
+//     exact), so three products in place of one, the small terms first.
 //
 // mma.sync reaches 590 TFLOP/s on this GPU (measured, four or more warps an
 // SM); the 45 queries of a 9-row verify with 5 heads per KV head, padded to 48,
@@ -22,7 +24,10 @@
 // exponentials a thread are 512 cycles of an SM quarter's unit; the rest
 // waits and hand-overs), its bytes 1.4 thousand at head dimension 128. Eight
 // sequences of 4096 to 8192 tokens, head_dim 128, 128 queries: 49 us (519
-// TFLOP/s; mma.sync in tiles of 64: 85 us), 45 queries: 42 us (46).
+// TFLOP/s; mma.sync in tiles of 64: 85 us), 45 queries: 42 us (46). With fp32
+// queries 74 us (mma.sync in tiles of 32: 194 us) and 64 us (102): the products
+// are 1.6 thousand cycles a unit there, the terms of the probabilities nearly
+// as many again in the softmax warps, behind the products.
 #pragma once
 
 #include "paged_attn.cuh"
@@ -30,7 +35,7 @@
 namespace sf {
 namespace pa {
 
-template <int HD>
+template <int HD, bool F32>
 struct TcShape {
   static constexpr int MT = 128;
   static constexpr int kThreads = 192;                 // 4 softmax warps, producer, MMA
@@ -38,13 +43,17 @@ struct TcShape {
   static constexpr int kBox = kTile * 128;
   static constexpr int kStage = 2 * kHalf * kBox;
   // Tensor-memory columns (32 bits): O, two S (P of a unit over its S), the
-  // queries. At head dimension 64 two CTAs share an SM (the softmax of one
-  // alone takes longer than its units' bytes).
-  static constexpr int kO = 0, kS = HD, kQ = HD + 128;   // (S b at kS + 64 b)
-  static constexpr int kCols = HD == 64 ? 256 : 512, kCtas = HD == 64 ? 2 : 1;
-  static constexpr int kStages = 6;
+  // queries; fp32 queries and probabilities as three 16-bit terms. At head
+  // dimension 64 two CTAs share an SM where that fits (the softmax of one alone
+  // takes longer than its units' bytes).
+  static constexpr int kTerms = F32 ? 3 : 1;
+  static constexpr int kSCols = F32 ? 96 : 64;           // of S (64), then of P (32 a term)
+  static constexpr int kO = 0, kS = HD, kQ = HD + 2 * kSCols;
+  static constexpr int kQTerm = HD / 2;
+  static constexpr int kCtas = HD == 64 && !F32 ? 2 : 1, kCols = 512 / kCtas;
+  static constexpr int kStages = HD == 64 && F32 ? 12 : 6;   // (192 KB an SM)
   static constexpr int kSmem = 1024 + kStages * kStage;
-  static_assert(kQ + HD / 2 <= kCols, "tensor memory");
+  static_assert(kQ + kTerms * kQTerm <= kCols, "tensor memory");
 };
 
 // B operand with the slots as K: rows of 128 bytes are 64 dimensions of one
@@ -70,9 +79,29 @@ __host__ __device__ constexpr uint32_t tc_idesc(int M, int N, bool b_mn) {
          ((uint32_t)(M >> 4) << 24);
 }
 
-template <int HD, typename TC>
-__global__ void __launch_bounds__(TcShape<HD>::kThreads, TcShape<HD>::kCtas) k_paged_attn_tc(const __grid_constant__ Args a) {
-  using S = TcShape<HD>;
+// 64 fp32 values as three 16-bit terms, the largest first, into tensor-memory
+// columns `pitch` apart (the values become the rest, about 2^-24 of them).
+template <int PITCH, typename TC>
+__device__ __forceinline__ void put_terms(uint32_t taddr, float (&x)[64]) {
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    uint32_t p[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      p[i] = Num<TC>::pack(x[2 * i], x[2 * i + 1]);
+      x[2 * i] -= Num<TC>::lo(p[i]);
+      x[2 * i + 1] -= Num<TC>::hi(p[i]);
+    }
+    tmem_st32(taddr + PITCH * k, p);
+  }
+}
+
+// TC: the cache's type. F32: fp32 queries and output over a bf16 cache.
+template <int HD, typename TC, bool F32>
+__global__ void __launch_bounds__(TcShape<HD, F32>::kThreads, TcShape<HD, F32>::kCtas)
+    k_paged_attn_tc(const __grid_constant__ Args a) {
+  using S = TcShape<HD, F32>;
+  using TQ = typename std::conditional<F32, float, TC>::type;
   constexpr int MT = S::MT;
   extern __shared__ unsigned char pa_smem_raw[];
   unsigned char* ring = pa_smem_raw + ((1024 - (smem_u32(pa_smem_raw) & 1023)) & 1023);
@@ -138,11 +167,14 @@ __global__ void __launch_bounds__(TcShape<HD>::kThreads, TcShape<HD>::kCtas) k_p
       await(&full[s], (n / S::kStages) & 1);
       tc_fence_after();
       const uint64_t d = dk + (uint64_t)(s * (S::kStage >> 4));
-      const uint32_t t = utmem + S::kS + 64 * (n & 1);
+      const uint32_t t = utmem + S::kS + S::kSCols * (n & 1);
       if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < HD / 16; ++k)
-          umma_bf16_tmem_a(t, utmem + S::kQ + 8 * k, d + (((k >> 2) * S::kBox + 32 * (k & 3)) >> 4), id_s, k > 0);
+        for (int i = S::kTerms - 1; i >= 0; --i)   // the small terms first
+#pragma unroll
+          for (int k = 0; k < HD / 16; ++k)
+            umma_bf16_tmem_a(t, utmem + S::kQ + S::kQTerm * i + 8 * k,
+                             d + (((k >> 2) * S::kBox + 32 * (k & 3)) >> 4), id_s, i < S::kTerms - 1 || k > 0);
         umma_commit(&s_full[n & 1]);
       }
       __syncwarp();
@@ -160,11 +192,14 @@ __global__ void __launch_bounds__(TcShape<HD>::kThreads, TcShape<HD>::kCtas) k_p
         tc_fence_after();
         const uint32_t keep = u > 0 ? 1u : (uint32_t)__shfl_sync(0xffffffffu, s_keep[n & 1], 0);
         const uint64_t d = dv + (uint64_t)(n % S::kStages * (S::kStage >> 4));
-        const uint32_t t = utmem + S::kS + 64 * (n & 1);
+        const uint32_t t = utmem + S::kS + S::kSCols * (n & 1);
         if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < kTile / 16; ++k)
-            umma_bf16_tmem_a(utmem + S::kO, t + 8 * k, d + (2048 * k >> 4), id_o, k > 0 ? 1u : keep);
+          for (int i = S::kTerms - 1; i >= 0; --i)
+#pragma unroll
+            for (int k = 0; k < kTile / 16; ++k)
+              umma_bf16_tmem_a(utmem + S::kO, t + 32 * i + 8 * k, d + (2048 * k >> 4), id_o,
+                               i < S::kTerms - 1 || k > 0 ? 1u : keep);
           umma_commit(&empty[n % S::kStages]);
           umma_commit(&o_done[n & 1]);
         }
@@ -199,18 +234,26 @@ __global__ void __launch_bounds__(TcShape<HD>::kThreads, TcShape<HD>::kCtas) k_p
       const unsigned long long bits = a.mask && live ? a.mask[r.s0 + j] : 0;
       // The row's query (rows past the end: zeros).
       if (warp_live) {
-        const TC* src = static_cast<const TC*>(a.q) + (r.s0 + j) * a.q_row + hh * a.q_head;
+        const TQ* src = static_cast<const TQ*>(a.q) + (r.s0 + j) * a.q_row + hh * a.q_head;
 #pragma unroll
         for (int c = 0; c < HD / 64; ++c) {
-          uint32_t v[32];
+          constexpr int W = 16 * sizeof(TQ);              // 32-bit words of 64 dimensions
+          uint32_t v[W];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
+          for (int i = 0; i < W / 4; ++i) {
             uint4 f = make_uint4(0u, 0u, 0u, 0u);
-            if (live) f = *reinterpret_cast<const uint4*>(src + 64 * c + 8 * i);
+            if (live) f = *reinterpret_cast<const uint4*>(src + 64 * c + (64 * 4 / W) * i);
             v[4 * i] = f.x ^ a.flip, v[4 * i + 1] = f.y ^ a.flip, v[4 * i + 2] = f.z ^ a.flip, v[4 * i + 3] = f.w ^ a.flip;
           }
           __syncwarp();
-          tmem_st32(lanes + S::kQ + 32 * c, v);
+          if constexpr (F32) {
+            float x[64];
+#pragma unroll
+            for (int i = 0; i < 64; ++i) x[i] = __uint_as_float(v[i]);
+            put_terms<S::kQTerm, TC>(lanes + S::kQ + 32 * c, x);
+          } else {
+            tmem_st32(lanes + S::kQ + 32 * c, v);
+          }
         }
         tmem_st_wait();
       }
@@ -231,7 +274,7 @@ __global__ void __launch_bounds__(TcShape<HD>::kThreads, TcShape<HD>::kCtas) k_p
         if (warp_live) {
           uint32_t v[4][16];
 #pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld16(lanes + S::kS + 64 * b + 16 * c, v[c]);
+          for (int c = 0; c < 4; ++c) tmem_ld16(lanes + S::kS + S::kSCols * b + 16 * c, v[c]);
           tmem_ld_wait();
 #pragma unroll
           for (int i = 0; i < kTile; ++i) {
@@ -370,12 +413,16 @@ __global__ void __launch_bounds__(TcShape<HD>::kThreads, TcShape<HD>::kCtas) k_p
           }
           fence_proxy_async();
         }
-        // ---- probabilities, in the cache's type
+        // ---- probabilities, in the cache's type (of fp32 queries: three terms)
         if (warp_live) {
-          uint32_t p[32];
+          if constexpr (F32) {
+            put_terms<32, TC>(lanes + S::kS + S::kSCols * b, x);
+          } else {
+            uint32_t p[32];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) p[i] = Num<TC>::pack(x[2 * i], x[2 * i + 1]);
-          tmem_st32(lanes + S::kS + 64 * b, p);
+            for (int i = 0; i < 32; ++i) p[i] = Num<TC>::pack(x[2 * i], x[2 * i + 1]);
+            tmem_st32(lanes + S::kS + S::kSCols * b, p);
+          }
           tmem_st_wait();
         }
         if (tid == 0 && t == w.t0) s_keep[b] = keep;   // (the MMA warp reads it at a piece's first unit)
@@ -400,7 +447,7 @@ __global__ void __launch_bounds__(TcShape<HD>::kThreads, TcShape<HD>::kCtas) k_p
       if (warp_live) {
         const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
         float* part = a.part + (slot * a.mt_max + row) * HD;
-        TC* dst = static_cast<TC*>(a.out) + (r.s0 + j) * a.o_row + hh * a.o_head;
+        TQ* dst = static_cast<TQ*>(a.out) + (r.s0 + j) * a.o_row + hh * a.o_head;
 #pragma unroll 1
         for (int c = 0; c < HD / 16; ++c) {
           uint32_t v[16];
@@ -411,7 +458,11 @@ __global__ void __launch_bounds__(TcShape<HD>::kThreads, TcShape<HD>::kCtas) k_p
           for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(v[i]));
           if (!live) continue;
           // (a row that saw nothing: l = 0 and O = 0)
-          if (whole) {
+          if (whole && F32) {
+#pragma unroll
+            for (int i = 0; i < 16; i += 2)
+              put2<HD, float>(a, r.s0 + j, hh, 16 * c + i, __uint_as_float(v[i]) * inv, __uint_as_float(v[i + 1]) * inv);
+          } else if (whole) {
             uint32_t o[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i)
