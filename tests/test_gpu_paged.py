@@ -579,3 +579,83 @@ def test_wrapper_refusals(pkg):
         pkg.page_plan(i32([1]), i32([0, 1]), i32([[0]]), i32([0]), i32([0]), i32([1]), 16)
     with pytest.raises(pkg.SFError):
         pkg.page_plan(i32([1]), i32([0, 1]), i32([[0]]), i32([0]), i32([0]), i32([1]), 17, n_rows=1)
+
+
+# ------------------------------------------- the larger tiles, on small inputs
+# A table wide enough for long requests: the query tile is chosen from what the
+# tables can hold, so these run in tiles of 32 (17 to 32 queries a KV head) and
+# of 128 queries, as long caches do.
+def wide(c):
+    c["tables"] = [t + [-1] * (70000 // c["k"].shape[2]) for t in c["tables"]]
+    return c
+
+
+TILES = [(3, 14, 2), (9, 14, 2), (40, 8, 2), (64, 5, 1), (30, 14, 2)]   # 21, 63, 160, 320, 210 queries
+TYPES = [(BF, BF), (FH, FH), (F4, BF)]
+
+
+@pytest.mark.parametrize("dq,dc", TYPES)
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("rows,nq,nkv", TILES)
+@pytest.mark.parametrize("tree", [False, True])
+def test_large_tiles(pkg, dq, dc, hd, rows, nq, nkv, tree):
+    """Requests that are nothing but the pass's rows (with a mask, rows that
+    see nothing among them), empty ones, ones that end at a unit's border."""
+    lens = [rows, 300 + rows, 0, rows + 1, 128, 192 + rows, 64]
+    c = wide(attn_case(rows + hd, lens, [min(rows, n) if n != 128 else 1 for n in lens], nq, nkv, hd, 32, dq, dc, tree=tree))
+    check_attn(c, *call(pkg, c))
+
+
+@pytest.mark.parametrize("dq,dc", TYPES)
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("rows", [3, 9])
+@pytest.mark.parametrize("down", [False, True])
+def test_large_tiles_with_growing_maxima(pkg, dq, dc, hd, rows, down):
+    n = 1500
+    c = wide(attn_case(37, [n, 130], [rows, rows], 14, 2, hd, 32, dq, dc, q_scale=1.0))
+    f = torch.logspace(2, -2, n, base=10.0) if down else torch.logspace(-2, 2, n, base=10.0)
+    for s in range(n):
+        c["k"][c["tables"][0][s // 32], :, s % 32] *= float(f[s])
+    check_attn(c, *call(pkg, c))
+
+
+@pytest.mark.parametrize("dq,dc", TYPES)
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("rows", [3, 9])
+@pytest.mark.parametrize("tree", [False, True])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+def test_large_tiles_with_masked_nan_and_inf(pkg, dq, dc, hd, rows, tree, bad):
+    """As test_masked_nan_and_inf_change_nothing."""
+    c = wide(attn_case(14, [200, rows, 64 + 3], [rows, rows, min(rows, 6)], 14, 2, hd, 16, dq, dc, tree=tree, stale=bad))
+    good, lgood = call(pkg, c)
+    check_attn(c, good, lgood)
+    spoiled = []
+    for b, n in enumerate(c["lens"]):
+        pg, off = c["tables"][b][(n - 1) // 16], (n - 1) % 16
+        c["k"][pg, 0, off] = bad
+        c["v"][pg, :, off] = bad
+        r = c["starts"][b + 1] - c["starts"][b]
+        for j in range(r):
+            m = c["mask"][c["starts"][b] + j] if tree else (1 << (j + 1)) - 1
+            if (m >> (r - 1)) & 1:
+                spoiled.append(c["starts"][b] + j)
+    out, lse = call(pkg, c)
+    keep = [i for i in range(good.shape[0]) if i not in spoiled]
+    assert torch.equal(out[keep], good[keep]) and torch.equal(lse[keep], lgood[keep])
+    assert spoiled and not bool(torch.isfinite(out[spoiled][:, 7:]).any())   # head 1: V alone is spoiled
+
+
+@pytest.mark.parametrize("dq,dc", TYPES)
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("rows", [3, 9])
+def test_large_tiles_of_strided_queries_and_other_scales(pkg, dq, dc, hd, rows):
+    for scale in (1.0, -0.3, 0.0):
+        c = wide(attn_case(41, [90, 333, 2], [1, rows, 2], 14, 2, hd, 64, dq, dc, q_scale=1.0, strided_q=True))
+        check_attn(c, *call(pkg, c, scale=scale), scale)
+        c["q"] = c["q"] * 40.0   # scores far apart
+        check_attn(c, *call(pkg, c), None)
+    c = wide(attn_case(43, [30, 70, 12], [rows] * 3, 14, 2, hd, 16, dq, dc, pad=0))
+    c["max_rows"] = 2            # rows behind it are left as they were
+    check_attn(c, *call(pkg, c))
+    c["lens"] = [2, 70, -1]      # rows before position 0 see nothing
+    check_attn(c, *call(pkg, c))
