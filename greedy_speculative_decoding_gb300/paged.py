@@ -24,7 +24,7 @@ _native = None
 
 
 def _binding():
-    """The extension module that checks and marshals the tensors (csrc/paged_py.c)."""
+    """The extension module that checks and marshals the tensors (csrc/paged_py.cpp)."""
     global _native
     if _native is None:
         L.load()
