@@ -100,7 +100,7 @@ static Sizes sizes(const sf_paged_cache& c, int n_heads, int max_rows, int q_dty
 static bool units_fit(const sf_paged_cache& c, int n_heads, int max_rows, int q_dtype, int batch, int table_width,
                       int sms) {
   const Sizes z = sizes(c, n_heads, max_rows, q_dtype, batch, table_width, sms);
-  return c.n_kv_heads * (long)z.ntq * z.units <= INT32_MAX;
+  return c.n_kv_heads * (long)z.ntq * (z.units + kMaxPiece) <= INT32_MAX;
 }
 
 // Enqueue a checked call: `a` holds rows, tables and lengths.
@@ -126,7 +126,7 @@ static cudaError_t enqueue(Args& a, const sf_paged_cache& c, int q_dtype, float 
   a.part_ml = reinterpret_cast<float2*>(ws + lay.ml);
   a.part = reinterpret_cast<float*>(ws + lay.part);
   const long max_units = z.items * z.units;
-  a.by_warp = a.B <= 32 && max_units <= INT32_MAX;
+  a.by_warp = a.B <= 32 && max_units + kMaxPiece * z.items <= INT32_MAX;
   sms = std::min(sms, kMaxCtas / 2);
   return c.head_dim == 128 ? launch_hd128(a, q_dtype, sms, max_units, st) : launch_hd64(a, q_dtype, sms, max_units, st);
 }

@@ -7,10 +7,11 @@
 //
 // Work. An item is (request, KV head, tile of MT queries): the queries are
 // the request's rows times the query heads that read this KV head. An item
-// has one unit per 64 slots of the request. The units of all items, in
-// order, are dealt out evenly to the CTAs, so lengths that differ by orders
-// of magnitude load the GPU evenly and a single long request is spread over
-// all of it. A CTA that holds an item from end to end writes the result; of
+// has one unit per 64 slots of the request, and before them a few that stand
+// for the beginning of an item (queries to load, a result to leave). The units
+// of all items, in order, are dealt out evenly to the CTAs, so lengths that
+// differ by orders of magnitude load the GPU evenly and a single long request
+// is spread over all of it. A CTA that holds an item from end to end writes the result; of
 // an item that several CTAs share each leaves its part (output, maximum, sum)
 // in the workspace, and the join kernel adds the parts in slot order.
 //
@@ -33,6 +34,7 @@ namespace sf {
 namespace pa {
 
 constexpr int kTile = 64;                 // slots of a unit
+constexpr int kMaxPiece = 8;              // units that an item's beginning counts for, at most
 constexpr uint64_t kWaitNs = 1000000000;  // bound of every wait
 
 struct Args {
@@ -50,6 +52,7 @@ struct Args {
   int mt;                  // queries of a tile (MT)
   int mt_max;              // queries of an item at most (min(MT, max_rows * group))
   int ntq_max;             // items of a (request, KV head) at most
+  int piece;               // units that an item's beginning counts for
   int by_warp;             // few requests: every warp finds the CTA's units by itself
   int wide;                // few items: a CTA joins one query, else four
   int by_item;             // descriptors by item (else by the CTA that starts it)
@@ -201,11 +204,17 @@ struct Shape {
   static constexpr int kFit = kCtas == 2 ? kFit2 : kFit1;
   static constexpr int kStages = kFit < kMaxStages ? kFit : kMaxStages;
   static constexpr int kSmem = 1024 + kStages * kStage + kExtra;
+  // Units that an item's beginning counts for: a CTA that begins one in the
+  // midst of its units otherwise ends that much later. 32 sequences of 0 to
+  // 8191 tokens, 7 queries: 47.4 us, 48.4 with none (2 to 5 are alike, 49.1
+  // with 14); 120 of up to 1000 tokens 29.3 and 36.5; fp32, one of 2057 tokens,
+  // 63 queries 10.5 and 13.1; 16 of 5 to 4099 tokens, 91 queries 12.8 and 15.8.
+  static constexpr int kPiece = 4;
 };
 
 // Where a CTA's units begin.
 struct Start {
-  long T;       // units in all
+  long T;       // units in all (items' beginnings included)
   long base;    // units before request b
   int b;
   Request r;    // request b
@@ -218,7 +227,7 @@ __device__ __forceinline__ Start locate_warp(const Args& a) {
   const int lane = threadIdx.x & 31;
   Request r{};
   if (lane < a.B) r = request<MT>(a, lane);
-  const int n = a.nkv * r.ntq * r.nt;
+  const int n = a.nkv * r.ntq * (r.nt + a.piece);
   int incl = n;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -252,7 +261,7 @@ __device__ __forceinline__ Start locate_cta(const Args& a, long* sh) {
   long mine = 0;
   for (int b = b0; b < b1; ++b) {
     const Request r = request<MT>(a, b);
-    mine += (long)a.nkv * r.ntq * r.nt;
+    mine += (long)a.nkv * r.ntq * (r.nt + a.piece);
   }
   long incl = mine;
 #pragma unroll
@@ -277,7 +286,7 @@ __device__ __forceinline__ Start locate_cta(const Args& a, long* sh) {
     long base = lo;
     for (int b = b0; b < b1; ++b) {
       const Request r = request<MT>(a, b);
-      const long n = (long)a.nkv * r.ntq * r.nt;
+      const long n = (long)a.nkv * r.ntq * (r.nt + a.piece);
       if (u0 < base + n) {
         sh[NW] = base;
         sh[NW + 1] = b;
@@ -300,25 +309,33 @@ struct Walk {
   int left, rem;   // units of the CTA from there on; units of request b before it
   int b;
   Request r;
-  int item, kvh, qt, t0, t1;   // the current piece: item within the request, units t0 .. t1 - 1
+  int item, kvh, qt, t0, t1;   // the current piece: item within the request, units of slots t0 .. t1 - 1
+  bool open = false;           // its item begins here and goes on in the next CTA
   __device__ __forceinline__ Walk(const Start& s, long first, long last)
       : u(first), left((int)(last - first)), rem((int)(first - s.base)), b(s.b), r(s.r) {}
   // The next piece; false at the end.
   __device__ __forceinline__ bool next(const Args& a) {
-    if (left <= 0) return false;
-    while (rem >= a.nkv * r.ntq * r.nt) {
-      rem = 0;
-      r = request<MT>(a, ++b);
+    while (left > 0) {
+      const int len = r.nt + a.piece;
+      if (rem >= a.nkv * r.ntq * len) {
+        rem = 0;
+        r = request<MT>(a, ++b);
+        continue;
+      }
+      const int it = rem / len, first = rem - it * len, take = min(len - first, left);
+      u += take;
+      rem += take;
+      left -= take;
+      if (first + take <= a.piece) continue;   // (no slots: the item's pieces are the next CTAs')
+      item = it;
+      t0 = max(0, first - a.piece);
+      t1 = first + take - a.piece;
+      kvh = item / r.ntq;
+      qt = item - kvh * r.ntq;
+      open = t0 == 0 && t1 < r.nt;
+      return true;
     }
-    item = rem / r.nt;
-    t0 = rem - item * r.nt;
-    t1 = min(r.nt, t0 + left);
-    kvh = item / r.ntq;
-    qt = item - kvh * r.ntq;
-    u += t1 - t0;
-    rem += t1 - t0;
-    left -= t1 - t0;
-    return true;
+    return false;
   }
 };
 
@@ -379,19 +396,15 @@ __device__ __forceinline__ void produce(const Args& a, Walk<MT>& w, unsigned cha
 // The join's descriptor of an item that begins in this CTA (one thread).
 template <int MT>
 __device__ __forceinline__ void describe(const Args& a, const Walk<MT>& w, const Deal& deal, bool whole) {
-  const long first = w.u - (w.t1 - w.t0);
-  const int c1 = whole ? (int)blockIdx.x : deal.cta_of(first + w.r.nt - 1);
+  const int c1 = whole ? (int)blockIdx.x : deal.cta_of(w.u - w.t1 + w.r.nt - 1);
   const int4 d = make_int4(blockIdx.x, c1 - (int)blockIdx.x + 1, w.b, w.item);
   if (a.by_item) a.desc[((long)w.b * a.nkv + w.kvh) * a.ntq_max + w.qt] = d;
   else if (!whole) a.desc[blockIdx.x] = d;
 }
 // Descriptors by CTA: none when no item begins here that others share.
 template <int MT>
-__device__ __forceinline__ void describe_none(const Args& a, const Walk<MT>& w, const Start& st, long u1, bool idle) {
-  if (a.by_item) return;
-  // (the last piece begins an item that goes on in the next CTA)
-  const bool shared = !idle && u1 < st.T && w.t0 == 0 && w.t1 < w.r.nt;
-  if (!shared) a.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
+__device__ __forceinline__ void describe_none(const Args& a, const Walk<MT>& w) {
+  if (!a.by_item && !w.open) a.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
 }
 
 // Two neighbouring elements of row `row`, head `head` of the output.
@@ -831,7 +844,7 @@ __global__ void __launch_bounds__(Shape<HD, WM, WK, F32>::kThreads, Shape<HD, WM
     }
   }
   if (!ok && lane == 0) report_err(a.err, kErrWait);
-  if (tid == 0) describe_none(a, w, st, u1, false);
+  if (tid == 0) describe_none(a, w);
 }
 
 // The join of the items that several CTAs share: the parts lie with the CTAs

@@ -19,8 +19,8 @@ inline int tile_of(int queries) { return queries <= 16 ? 16 : queries <= 32 ? 32
 
 // Launch a main kernel (`ctas` CTAs an SM) and the join.
 template <int HD, typename TQ, int MT>
-cudaError_t launch(void (*fn)(Args), int threads, int smem, std::atomic<uint64_t>& ready, Args& a, int sms, int ctas,
-                   long max_units, cudaStream_t st) {
+cudaError_t launch(void (*fn)(Args), int threads, int smem, int piece, std::atomic<uint64_t>& ready, Args& a,
+                   int sms, int ctas, long max_units, cudaStream_t st) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -32,6 +32,8 @@ cudaError_t launch(void (*fn)(Args), int threads, int smem, std::atomic<uint64_t
     if (dev < 64) ready.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
   }
   const long most = (long)sms * ctas, items = (long)a.B * a.nkv * a.ntq_max;
+  a.piece = piece;
+  max_units += piece * items;
   const int grid = (int)(max_units < most ? max_units : most);
   // Many parts an item, and not so many queries that their CTAs come in waves.
   a.wide = items * 8 <= grid && items * a.mt_max <= 1024;
@@ -55,19 +57,21 @@ cudaError_t launch(void (*fn)(Args), int threads, int smem, std::atomic<uint64_t
 template <int HD, typename TC, bool F32, int WM, int WK>
 cudaError_t launch_mma(Args& a, int sms, long max_units, cudaStream_t st) {
   using S = Shape<HD, WM, WK, F32>;
+  static_assert(S::kPiece <= kMaxPiece);
   using TQ = typename std::conditional<F32, float, TC>::type;
   static std::atomic<uint64_t> ready{0};   // devices whose shared-memory limit for this kernel is set
-  return launch<HD, TQ, S::MT>(k_paged_attn<HD, TC, F32, WM, WK>, S::kThreads, S::kSmem, ready, a, sms, S::kCtas,
-                               max_units, st);
+  return launch<HD, TQ, S::MT>(k_paged_attn<HD, TC, F32, WM, WK>, S::kThreads, S::kSmem, S::kPiece, ready, a, sms,
+                               S::kCtas, max_units, st);
 }
 
 template <int HD, typename TC, bool F32>
 cudaError_t launch_tc(Args& a, int sms, long max_units, cudaStream_t st) {
   using S = TcShape<HD, F32>;
+  static_assert(S::kPiece <= kMaxPiece);
   using TQ = typename std::conditional<F32, float, TC>::type;
   static std::atomic<uint64_t> ready{0};
-  return launch<HD, TQ, S::MT>(k_paged_attn_tc<HD, TC, F32>, S::kThreads, S::kSmem, ready, a, sms, S::kCtas,
-                          max_units, st);
+  return launch<HD, TQ, S::MT>(k_paged_attn_tc<HD, TC, F32>, S::kThreads, S::kSmem, S::kPiece, ready, a, sms,
+                               S::kCtas, max_units, st);
 }
 
 template <int HD, typename TC, bool F32>

@@ -53,6 +53,9 @@ struct TcShape {
   static constexpr int kCtas = HD == 64 && !F32 ? 2 : 1, kCols = 512 / kCtas;
   static constexpr int kStages = HD == 64 && F32 ? 12 : 6;   // (192 KB an SM)
   static constexpr int kSmem = 1024 + kStages * kStage;
+  // (as in paged_attn.cuh: 64 sequences of 100 to 2000 tokens, 8 KV heads, 45
+  // queries: 64.8 us, 93.2 with none, 71.8 with 4, 68.3 with 14)
+  static constexpr int kPiece = 8;
   static_assert(kQ + kTerms * kQTerm <= kCols, "tensor memory");
 };
 
@@ -482,7 +485,7 @@ __global__ void __launch_bounds__(TcShape<HD, F32>::kThreads, TcShape<HD, F32>::
       tc_fence_before();   // O has been read: the next piece's first product may replace it
     }
     if (!ok && lane == 0) report_err(a.err, kErrWait);
-    if (tid == 0) describe_none(a, w, st, u1, idle);
+    if (tid == 0) describe_none(a, w);
   }
   tc_fence_before();
   __syncthreads();
