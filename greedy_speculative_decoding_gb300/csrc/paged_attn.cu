@@ -17,7 +17,7 @@ struct Layout {
 };
 static Layout layout(int n_heads, int n_kv_heads, int head_dim, int max_rows) {   // (whatever the tile)
   const int queries = max_rows * (n_heads / n_kv_heads);
-  const size_t mt = std::min(queries, tile_of(queries));
+  const size_t mt = std::min(queries, 128);
   Layout l;
   l.ml = kMaxDesc * sizeof(int4);
   l.part = l.ml + 2 * kMaxCtas * mt * sizeof(float2);
@@ -75,23 +75,23 @@ static Sizes sizes(const sf_paged_cache& c, int n_heads, int max_rows, int q_dty
   const int queries = max_rows * (n_heads / c.n_kv_heads);
   z.units = std::max(1l, ((long)table_width * c.page + kTile - 1) / kTile);
   auto items = [&](int mt) { return (long)batch * c.n_kv_heads * ((queries + mt - 1) / mt); };
-  // A smaller tile where the larger one's units could not occupy the GPU even
-  // if every request filled its table: the cache is then read once for each
-  // tile (from L2), by CTAs that would be idle. The tcgen05 kernel also starts
-  // more slowly, which shows at head dimension 64 with its small units: 16
-  // requests of 4099 tokens with 91 queries (2080 units) take 19.3 us with it
-  // and 15.4 in tiles of 32, of 8192 tokens and eight KV heads with 128 queries
-  // (16384 units) 57 and 93 us. At head dimension 128 it wins from 128 units a
-  // KV head: 8 requests of 1000 tokens with 45 queries take 16 and 22 us. fp32
-  // queries, head dimension 64, 1024 units: 45 queries 19.8 us with it and 18.0
-  // in two tiles of 32, 128 queries 25.2 and in four tiles 29.1.
-  z.mt = tile_of(queries);
-  auto few = [&](int mt) {
-    const long total = items(mt) * z.units;
-    if (mt == 128 && c.head_dim == 64 && (q_dtype == SF_DT_F32 ? items(32) * z.units : total) < 4096) return true;
-    return total < 2 * sms;
-  };
-  while (z.mt > 16 && few(z.mt)) z.mt = z.mt == 128 ? 32 : 16;
+  auto total = [&](int mt) { return items(mt) * z.units; };   // if every request filled its table
+  // Larger tiles read the cache less often (again from L2), smaller ones spread
+  // few units over more of the GPU and start sooner. Measured, in us, for
+  // requests x tokens x KV heads and queries, in tiles of 16 / 32 / 128:
+  //   16-bit, head dimension 128: 1 x 4000 x 4, 45: 10.3 / 10.1 / 11.5; 8 x
+  //     1000 x 8, 45: 18.4 / 20.6 / 15.8; 20: 14.4 / 13.2 / 14.3
+  //   16-bit, 64: 16 x 5..4099 x 2, 91: 19.8 / 16.0 / 16.6; 8 x 4096..8192 x 8,
+  //     45: 40.5 / 35.1 / 27.2; 20: 29.8 / 24.1 / 26.4
+  //   fp32, 128: 1 x 8000 x 4, 45: 14.5 / 19.9 / 16.2; 8 x 1000 x 8, 45: 24.1 /
+  //     30.2 / 23.7; 20: 18.4 / 20.1 / 21.4; 8 x 4096..8192 x 8, 20: 61.3 /
+  //     55.0 / 56.2
+  //   fp32, 64: 8 x 1000 x 8, 45: 17.0 / 18.8 / 18.6; 91: 26.6 / 25.1 / 20.5;
+  //     20: 13.9 / 13.5 / 18.2; 8 x 4096..8192 x 8, 20: 40.5 / 34.7 / 44.0
+  if (queries <= 16) z.mt = 16;
+  else if (q_dtype != SF_DT_F32) z.mt = queries > 32 && total(128) >= (c.head_dim == 64 ? 4096 : 2 * sms) ? 128 : 32;
+  else if (queries > 32) z.mt = total(16) >= 4000 ? 128 : 16;
+  else z.mt = total(16) < 8192 ? 16 : c.head_dim == 64 ? 32 : 128;
   z.ntq = (queries + z.mt - 1) / z.mt;
   z.items = items(z.mt);
   return z;

@@ -20,9 +20,9 @@
 // dimensions by min(page, 64) slots, 128-byte swizzle); WM x WK consumer
 // warps compute on them with mma.sync: warp (wm, wk) takes 16 queries and
 // 64 / WK of the slots, with a running maximum, sum and output of its own,
-// joined over wk at the end of the item. Few queries (one new token: the
-// query heads of one KV head) share the slots out between the warps, many
-// queries share out the queries.
+// joined over wk at the end of the item: 1 x 4 warps for tiles of 16 queries
+// (one new token: the query heads of one KV head), 2 x 2 for tiles of 32.
+// Tiles of 128 queries are paged_attn_tc.cuh's.
 #pragma once
 
 #include <type_traits>
@@ -187,11 +187,10 @@ struct Shape {
   static constexpr int kHalf = HD / 64;              // 64-dimension boxes of a key
   static constexpr int kBox = kTile * 128;           // bytes of one box column: 64 slots x 64 dimensions
   static constexpr int kStage = 2 * kHalf * kBox;    // keys and values of a unit
-  static constexpr bool kQSmem = F32 || WK == 1;     // queries in shared memory (else in registers)
-  static constexpr int QP = HD + 8;                  // pitch of the queries there
+  static constexpr int QP = HD + 8;                  // pitch of fp32 queries in shared memory (others: registers)
   static constexpr int OP = HD + 8;                  // pitch of the parts joined over wk
-  static constexpr int kQBytes = kQSmem ? (F32 ? 3 : 1) * MT * QP * 2 : 0;
-  static constexpr int kOBytes = WK > 1 ? WK * MT * (OP + 2) * 4 : 0;
+  static constexpr int kQBytes = F32 ? 3 * MT * QP * 2 : 0;
+  static constexpr int kOBytes = WK * MT * (OP + 2) * 4;
   static constexpr int kExtra = kQBytes > kOBytes ? kQBytes : kOBytes;   // one region: never both at once
   static constexpr int kMaxStages = 6;
   // Two CTAs on an SM when at least two stages fit in half its shared memory
@@ -199,7 +198,7 @@ struct Shape {
   // dimension 128 would spill (8 sequences of 4096 to 8192 tokens, 8 KV heads,
   // 20 queries: 39.4 us with one CTA, 45.3 with two).
   static constexpr int kFit2 = (kHalfSmBytes - 1024 - kExtra) / kStage;
-  static constexpr int kCtas = kFit2 >= 2 && !(HD == 128 && WK == 2 && !F32) ? 2 : 1;
+  static constexpr int kCtas = kFit2 >= 2 && !(HD == 128 && WK == 2) ? 2 : 1;
   static constexpr int kFit1 = (220 * 1024 - 1024 - kExtra) / kStage;
   static constexpr int kFit = kCtas == 2 ? kFit2 : kFit1;
   static constexpr int kStages = kFit < kMaxStages ? kFit : kMaxStages;
@@ -478,12 +477,12 @@ __global__ void __launch_bounds__(Shape<HD, WM, WK, F32>::kThreads, Shape<HD, WM
     const Request r = w.r;
     const int q0 = w.qt * MT + 16 * wm + g;        // this lane's queries: q0 and q0 + 8
     const int Mq = r.rows * a.group;
-    uint32_t qf[S::kQSmem ? 1 : KS][4];
-    if constexpr (S::kQSmem) {
-      // The tile's queries in shared memory (fp32 ones as three bf16 terms).
+    uint32_t qf[F32 ? 1 : KS][4];
+    if constexpr (F32) {
+      // The tile's queries in shared memory, as three bf16 terms.
       TC* sq = reinterpret_cast<TC*>(extra);
       cta_sync();   // the region's last readers are done
-      constexpr int E = F32 ? 4 : 8;                      // elements of a 16-byte load
+      constexpr int E = 4;                                // elements of a 16-byte load
       constexpr int NL = MT * HD / E / (S::kWarps * 32);  // loads of a thread, all in flight together
       uint4 f[NL];
 #pragma unroll
@@ -497,22 +496,18 @@ __global__ void __launch_bounds__(Shape<HD, WM, WK, F32>::kThreads, Shape<HD, WM
 #pragma unroll
       for (int y = 0; y < NL; ++y) {
         const int e = tid + y * S::kWarps * 32, m = e / (HD / E), d = E * (e - m * (HD / E));
-        f[y].x ^= a.flip, f[y].y ^= a.flip, f[y].z ^= a.flip, f[y].w ^= a.flip;
-        if constexpr (F32) {
-          float v[4] = {__uint_as_float(f[y].x), __uint_as_float(f[y].y), __uint_as_float(f[y].z), __uint_as_float(f[y].w)};
+        float v[4] = {__uint_as_float(f[y].x ^ a.flip), __uint_as_float(f[y].y ^ a.flip),
+                      __uint_as_float(f[y].z ^ a.flip), __uint_as_float(f[y].w ^ a.flip)};
 #pragma unroll
-          for (int k = 0; k < 3; ++k) {
-            uint32_t p[2];
+        for (int k = 0; k < 3; ++k) {
+          uint32_t p[2];
 #pragma unroll
-            for (int z = 0; z < 2; ++z) {
-              p[z] = Num<bf16>::pack(v[2 * z], v[2 * z + 1]);
-              v[2 * z] -= Num<bf16>::lo(p[z]);
-              v[2 * z + 1] -= Num<bf16>::hi(p[z]);
-            }
-            *reinterpret_cast<uint2*>(sq + (k * MT + m) * S::QP + d) = make_uint2(p[0], p[1]);
+          for (int z = 0; z < 2; ++z) {
+            p[z] = Num<bf16>::pack(v[2 * z], v[2 * z + 1]);
+            v[2 * z] -= Num<bf16>::lo(p[z]);
+            v[2 * z + 1] -= Num<bf16>::hi(p[z]);
           }
-        } else {
-          *reinterpret_cast<uint4*>(sq + m * S::QP + d) = f[y];
+          *reinterpret_cast<uint2*>(sq + (k * MT + m) * S::QP + d) = make_uint2(p[0], p[1]);
         }
       }
       cta_sync();
@@ -548,7 +543,7 @@ __global__ void __launch_bounds__(Shape<HD, WM, WK, F32>::kThreads, Shape<HD, WM
 #pragma unroll
       for (int k = 0; k < KS; ++k) {
         uint32_t qk[NQ][4];
-        if constexpr (S::kQSmem) {
+        if constexpr (F32) {
           const TC* sq = reinterpret_cast<const TC*>(extra);
 #pragma unroll
           for (int e = 0; e < NQ; ++e)
@@ -771,77 +766,54 @@ __global__ void __launch_bounds__(Shape<HD, WM, WK, F32>::kThreads, Shape<HD, WM
     float* part = a.part + slot * a.mt_max * HD;
     float2* part_ml = a.part_ml + slot * a.mt_max;
     const float kLn2 = 0.693147180559945f;
-    if constexpr (WK == 1) {
+    // Joined over the warps that shared out the slots.
+    float* so = reinterpret_cast<float*>(extra);                 // [WK][MT][OP]
+    float2* sml = reinterpret_cast<float2*>(so + WK * MT * S::OP);   // [WK][MT]
+    if (F32) cta_sync();   // the queries' terms have been read
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int q = q0 + 8 * e;
-        if (q >= Mq) continue;
-        if (whole) {
-          const int jj = q / a.group, hh = w.kvh * a.group + q - jj * a.group;
-          const float inv = l[e] == 0.f ? 0.f : 1.f / l[e];
+    for (int e = 0; e < 2; ++e) {
+      const int x = wk * MT + 16 * wm + g + 8 * e;
 #pragma unroll
-          for (int d = 0; d < ND; ++d)
-            put2<HD, TQ>(a, r.s0 + jj, hh, 8 * d + 2 * c4, o[d][2 * e] * inv, o[d][2 * e + 1] * inv);
-          if (a.lse && c4 == 0)
-            a.lse[(long)(r.s0 + jj) * a.nq + hh] = l[e] == 0.f ? -INFINITY : m[e] * kLn2 + logf(l[e]);
-        } else {
-          const int x = 16 * wm + g + 8 * e;
-#pragma unroll
-          for (int d = 0; d < ND; ++d)
-            *reinterpret_cast<float2*>(part + x * HD + 8 * d + 2 * c4) = make_float2(o[d][2 * e], o[d][2 * e + 1]);
-          if (c4 == 0) part_ml[x] = make_float2(m[e], l[e]);
-        }
-      }
-    } else {
-      // Joined over the warps that shared out the slots.
-      float* so = reinterpret_cast<float*>(extra);                 // [WK][MT][OP]
-      float2* sml = reinterpret_cast<float2*>(so + WK * MT * S::OP);   // [WK][MT]
-      if (F32) cta_sync();   // the queries' terms have been read
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int x = wk * MT + 16 * wm + g + 8 * e;
-#pragma unroll
-        for (int d = 0; d < ND; ++d)
-          *reinterpret_cast<float2*>(so + x * S::OP + 8 * d + 2 * c4) = make_float2(o[d][2 * e], o[d][2 * e + 1]);
-        if (c4 == 0) sml[x] = make_float2(m[e], l[e]);
-      }
-      cta_sync();
-      for (int e = tid; e < MT * (HD / 4); e += S::kWarps * 32) {
-        const int x = e / (HD / 4), d = 4 * (e - x * (HD / 4));
-        const int q = w.qt * MT + x;
-        if (q >= Mq) break;
-        float mm = -INFINITY, ll = 0.f, f[WK];
-        float2 ml[WK];
-#pragma unroll
-        for (int k = 0; k < WK; ++k) {
-          ml[k] = sml[k * MT + x];
-          mm = fmaxf(mm, ml[k].x);
-        }
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int k = 0; k < WK; ++k) {
-          f[k] = ml[k].x == -INFINITY ? 0.f : exp2_approx(ml[k].x - mm);
-          // (a warp that saw nothing has l = 0; one whose wait expired, NaN)
-          ll += ml[k].x == -INFINITY ? ml[k].y : ml[k].y * f[k];
-          const float4 y = *reinterpret_cast<const float4*>(so + (k * MT + x) * S::OP + d);
-          v.x = fmaf(y.x, f[k], v.x);
-          v.y = fmaf(y.y, f[k], v.y);
-          v.z = fmaf(y.z, f[k], v.z);
-          v.w = fmaf(y.w, f[k], v.w);
-        }
-        if (whole) {
-          const int jj = q / a.group, hh = w.kvh * a.group + q - jj * a.group;
-          const float inv = ll == 0.f ? 0.f : 1.f / ll;
-          put2<HD, TQ>(a, r.s0 + jj, hh, d, v.x * inv, v.y * inv);
-          put2<HD, TQ>(a, r.s0 + jj, hh, d + 2, v.z * inv, v.w * inv);
-          if (a.lse && d == 0) a.lse[(long)(r.s0 + jj) * a.nq + hh] = ll == 0.f ? -INFINITY : mm * kLn2 + logf(ll);
-        } else {
-          *reinterpret_cast<float4*>(part + x * HD + d) = v;
-          if (d == 0) part_ml[x] = make_float2(mm, ll);
-        }
-      }
-      cta_sync();   // the region is free again
+      for (int d = 0; d < ND; ++d)
+        *reinterpret_cast<float2*>(so + x * S::OP + 8 * d + 2 * c4) = make_float2(o[d][2 * e], o[d][2 * e + 1]);
+      if (c4 == 0) sml[x] = make_float2(m[e], l[e]);
     }
+    cta_sync();
+    for (int e = tid; e < MT * (HD / 4); e += S::kWarps * 32) {
+      const int x = e / (HD / 4), d = 4 * (e - x * (HD / 4));
+      const int q = w.qt * MT + x;
+      if (q >= Mq) break;
+      float mm = -INFINITY, ll = 0.f, f[WK];
+      float2 ml[WK];
+#pragma unroll
+      for (int k = 0; k < WK; ++k) {
+        ml[k] = sml[k * MT + x];
+        mm = fmaxf(mm, ml[k].x);
+      }
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int k = 0; k < WK; ++k) {
+        f[k] = ml[k].x == -INFINITY ? 0.f : exp2_approx(ml[k].x - mm);
+        // (a warp that saw nothing has l = 0; one whose wait expired, NaN)
+        ll += ml[k].x == -INFINITY ? ml[k].y : ml[k].y * f[k];
+        const float4 y = *reinterpret_cast<const float4*>(so + (k * MT + x) * S::OP + d);
+        v.x = fmaf(y.x, f[k], v.x);
+        v.y = fmaf(y.y, f[k], v.y);
+        v.z = fmaf(y.z, f[k], v.z);
+        v.w = fmaf(y.w, f[k], v.w);
+      }
+      if (whole) {
+        const int jj = q / a.group, hh = w.kvh * a.group + q - jj * a.group;
+        const float inv = ll == 0.f ? 0.f : 1.f / ll;
+        put2<HD, TQ>(a, r.s0 + jj, hh, d, v.x * inv, v.y * inv);
+        put2<HD, TQ>(a, r.s0 + jj, hh, d + 2, v.z * inv, v.w * inv);
+        if (a.lse && d == 0) a.lse[(long)(r.s0 + jj) * a.nq + hh] = ll == 0.f ? -INFINITY : mm * kLn2 + logf(ll);
+      } else {
+        *reinterpret_cast<float4*>(part + x * HD + d) = v;
+        if (d == 0) part_ml[x] = make_float2(mm, ll);
+      }
+    }
+    cta_sync();   // the region is free again
   }
   if (!ok && lane == 0) report_err(a.err, kErrWait);
   if (tid == 0) describe_none(a, w);

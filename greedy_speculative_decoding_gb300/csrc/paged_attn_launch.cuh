@@ -9,14 +9,6 @@
 namespace sf {
 namespace pa {
 
-// Query tile of a launch, from the queries that a KV head can have in one
-// request (max_rows * group): one m16 tile shared by four warps that split the
-// slots, two by two, or the tcgen05 kernel's 128. 8 sequences of 4096 to 8192
-// tokens, 16-bit, 20 queries a KV head: 25.0 us on mma.sync and 29.4 on tcgen05
-// at head dimension 64, 39.8 and 40.6 at 128; 45 queries: 46 and 42. fp32: 27
-// queries 58 and 58 us, 45 queries (two tiles) 102 and 64.
-inline int tile_of(int queries) { return queries <= 16 ? 16 : queries <= 32 ? 32 : 128; }
-
 // Launch a main kernel (`ctas` CTAs an SM) and the join.
 template <int HD, typename TQ, int MT>
 cudaError_t launch(void (*fn)(Args), int threads, int smem, int piece, std::atomic<uint64_t>& ready, Args& a,
@@ -77,8 +69,10 @@ cudaError_t launch_tc(Args& a, int sms, long max_units, cudaStream_t st) {
 template <int HD, typename TC, bool F32>
 cudaError_t launch_tiles(Args& a, int sms, long max_units, cudaStream_t st) {
   if (a.mt == 16) return launch_mma<HD, TC, F32, 1, 4>(a, sms, max_units, st);
-  if (a.mt == 128) return launch_tc<HD, TC, F32>(a, sms, max_units, st);
-  return launch_mma<HD, TC, F32, 2, 2>(a, sms, max_units, st);
+  if constexpr (HD == 64 || !F32) {
+    if (a.mt == 32) return launch_mma<HD, TC, F32, 2, 2>(a, sms, max_units, st);
+  }
+  return launch_tc<HD, TC, F32>(a, sms, max_units, st);
 }
 
 template <int HD>
