@@ -3,10 +3,11 @@
 // Bound by memory: every projected element is read once and written once. A
 // thread takes eight elements of the lower half of one head and the eight
 // they are paired with (16-byte accesses): few registers, so that as many
-// loads as possible are in flight. 16411 bf16 rows of 36 heads of 128: 56 us
-// (5.5 TB/s) with all threads of an SM in CTAs of 128, 58 us in CTAs of 256,
-// 69 of 1024, 70 with five CTAs of 256; two heads a thread, the rotation loaded
-// once, was slower (78 us).
+// loads as possible are in flight. 16411 bf16 rows of 36 heads of 128: 53.7 us
+// (5.8 TB/s) with all threads of an SM in CTAs of 128 and everything streamed
+// (56.3 with plain stores, 55.2 with plain loads); with plain stores 58 us in
+// CTAs of 256, 69 of 1024, 70 with five CTAs of 256; two heads a thread, the
+// rotation loaded once, was slower (78 us).
 #include <cmath>
 #include <type_traits>
 
@@ -35,7 +36,7 @@ template <typename T>
 struct Raw {
   uint4 w;
   __device__ __forceinline__ void load(const T* p) { w = __ldcs(reinterpret_cast<const uint4*>(p)); }
-  __device__ __forceinline__ void store(T* p) const { *reinterpret_cast<uint4*>(p) = w; }
+  __device__ __forceinline__ void store(T* p) const { __stcs(reinterpret_cast<uint4*>(p), w); }
   __device__ __forceinline__ uint32_t& word(int i) { return i == 0 ? w.x : i == 1 ? w.y : i == 2 ? w.z : w.w; }
   __device__ __forceinline__ float2 get(int i) {
     if constexpr (std::is_same<T, bf16>::value)
@@ -60,8 +61,8 @@ struct Raw<float> {
     w[1] = __ldcs(reinterpret_cast<const float4*>(p) + 1);
   }
   __device__ __forceinline__ void store(float* p) const {
-    *reinterpret_cast<float4*>(p) = w[0];
-    *(reinterpret_cast<float4*>(p) + 1) = w[1];
+    __stcs(reinterpret_cast<float4*>(p), w[0]);
+    __stcs(reinterpret_cast<float4*>(p) + 1, w[1]);
   }
   __device__ __forceinline__ float2 get(int i) {
     return i & 1 ? make_float2(w[i >> 1].z, w[i >> 1].w) : make_float2(w[i >> 1].x, w[i >> 1].y);
