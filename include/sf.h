@@ -402,7 +402,7 @@ SF_API sf_status sf_nf4_quantize(const void* d_w, int32_t rows, int32_t cols, in
 /* ------------------------------------------------------------------------
  * A key-value cache in pages, for programs that serve sequences of different
  * lengths from one pool (the engine's own caches are s_max slots per
- * sequence). Three operators run one after the other in a pass:
+ * sequence, unless it is made with pages). Three operators run one after the other in a pass:
  * sf_page_plan (block tables, cache slots and positions from the requests'
  * lengths), sf_kv_append (RoPE and the new rows' keys and values into their
  * slots) and sf_paged_attention (the new rows over their requests' pages).

@@ -27,4 +27,5 @@ Modules:
   decode  -- greedy decoding, acceptance, in-place rollback, n-gram lookup and
              the speculative loop
   nf4     -- NormalFloat-4 codebook, blockwise quantisation, dequantisation
+  paged   -- page plan, RoPE and append, attention over a cache in pages
 """
