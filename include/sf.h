@@ -402,15 +402,16 @@ SF_API sf_status sf_nf4_quantize(const void* d_w, int32_t rows, int32_t cols, in
 /* ------------------------------------------------------------------------
  * A key-value cache in pages, for programs that serve sequences of different
  * lengths from one pool (the engine's own caches are s_max slots per
- * sequence, unless it is made with pages). Three operators run one after the other in a pass:
- * sf_page_plan (block tables, cache slots and positions from the requests'
- * lengths), sf_kv_append (RoPE and the new rows' keys and values into their
- * slots) and sf_paged_attention (the new rows over their requests' pages).
- * Everything they need to know about a pass lies in device memory, so a pass
- * is captured into a CUDA graph once and replayed with other lengths. No call
- * synchronises or allocates; all work is enqueued on cuda_stream. A pass's
- * token rows lie request after request: starts[b] .. starts[b + 1] - 1 are
- * the newest rows of request b, the last of them at position lens[b] - 1.
+ * sequence, unless it is made with pages). Three operators run one after the
+ * other in a pass: sf_page_plan (block tables, cache slots and positions
+ * from the requests' lengths), sf_kv_append (RoPE and the new rows' keys and
+ * values into their slots) and sf_paged_attention (the new rows over their
+ * requests' pages). Everything they need to know about a pass lies in device
+ * memory, so a pass is captured into a CUDA graph once and replayed with
+ * other lengths. No call synchronises or allocates; all work is enqueued on
+ * cuda_stream. A pass's token rows lie request after request: starts[b] ..
+ * starts[b + 1] - 1 are the newest rows of request b, the last of them at
+ * position lens[b] - 1.
  */
 
 /* Element types of rows and caches. */
