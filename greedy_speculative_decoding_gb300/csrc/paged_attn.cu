@@ -83,11 +83,10 @@ static Sizes sizes(const sf_paged_cache& c, int n_heads, int max_rows, int q_dty
   //     1000 x 8, 45: 18.4 / 20.6 / 15.8; 20: 14.4 / 13.2 / 14.3
   //   16-bit, 64: 16 x 5..4099 x 2, 91: 19.8 / 16.0 / 16.6; 8 x 4096..8192 x 8,
   //     45: 40.5 / 35.1 / 27.2; 20: 29.8 / 24.1 / 26.4
-  //   fp32, 128: 1 x 8000 x 4, 45: 14.5 / 19.9 / 16.2; 8 x 1000 x 8, 45: 24.1 /
-  //     30.2 / 23.7; 20: 18.4 / 20.1 / 21.4; 8 x 4096..8192 x 8, 20: 61.3 /
-  //     55.0 / 56.2
-  //   fp32, 64: 8 x 1000 x 8, 45: 17.0 / 18.8 / 18.6; 91: 26.6 / 25.1 / 20.5;
-  //     20: 13.9 / 13.5 / 18.2; 8 x 4096..8192 x 8, 20: 40.5 / 34.7 / 44.0
+  //   fp32, 128 (not in tiles of 32): 1 x 8000 x 4, 45: 15.9 / 17.9; 8 x 1000 x
+  //     8, 45: 26.4 / 25.7; 20: 19.9 / 22.8; 8 x 4096..8192 x 8, 20: 65.5 / 58.6
+  //   fp32, 64: 8 x 1000 x 8, 45: 17.4 / 19.5 / 20.9; 91: 27.0 / 25.9 / 22.8;
+  //     20: 13.9 / 14.2 / 20.3; 8 x 4096..8192 x 8, 20: 41.2 / 36.2 / 51.7
   if (queries <= 16) z.mt = 16;
   else if (q_dtype != SF_DT_F32) z.mt = queries > 32 && total(128) >= (c.head_dim == 64 ? 4096 : 2 * sms) ? 128 : 32;
   else if (queries > 32) z.mt = total(16) >= 4000 ? 128 : 16;

@@ -207,7 +207,7 @@ struct Shape {
   // midst of its units otherwise ends that much later. 32 sequences of 0 to
   // 8191 tokens, 7 queries: 47.4 us, 48.4 with none (2 to 5 are alike, 49.1
   // with 14); 120 of up to 1000 tokens 29.3 and 36.5; fp32, one of 2057 tokens,
-  // 63 queries 10.5 and 13.1; 16 of 5 to 4099 tokens, 91 queries 12.8 and 15.8.
+  // 63 queries 11.1 and 13.6; 16 of 5 to 4099 tokens, 91 queries 12.8 and 15.8.
   static constexpr int kPiece = 4;
 };
 
@@ -668,10 +668,21 @@ __global__ void __launch_bounds__(Shape<HD, WM, WK, F32>::kThreads, Shape<HD, WM
               }
             }
           }
+          if constexpr (F32) {
+            // (the tensor cores cut off what they add, so the sums over units
+            // are added here: error 1.5e-6 where it was 4e-6 after 80 units; 11.1
+            // us for one of 2057 tokens with 63 queries, 10.5 before)
+            float y[2][4] = {};
 #pragma unroll
-          for (int k = NQ - 1; k >= 0; --k) {
-            Num<TC>::mma(o[2 * d], p[k], vb[0], vb[1]);
-            Num<TC>::mma(o[2 * d + 1], p[k], vb[2], vb[3]);
+            for (int k = NQ - 1; k >= 0; --k) {
+              Num<TC>::mma(y[0], p[k], vb[0], vb[1]);
+              Num<TC>::mma(y[1], p[k], vb[2], vb[3]);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[2 * d][e] += y[0][e], o[2 * d + 1][e] += y[1][e];
+          } else {
+            Num<TC>::mma(o[2 * d], p[0], vb[0], vb[1]);
+            Num<TC>::mma(o[2 * d + 1], p[0], vb[2], vb[3]);
           }
         }
       }

@@ -15,7 +15,10 @@
 //     to the cache's type, by half a step each; with a lagging reference that
 //     includes the largest, which is exactly 1 in the mma.sync kernel.
 //   * fp32 queries and their probabilities are three bf16 terms each (24 bits:
-//     exact), so three products in place of one, the small terms first.
+//     exact), so three products in place of one, the small terms first. The
+//     tensor cores cut off what they add to the output (54 units of 12 products
+//     left it 8e-6 too small), so it moves every 16 units to sums in shared
+//     memory that are rounded.
 //
 // mma.sync reaches 590 TFLOP/s on this GPU (measured, four or more warps an
 // SM); the 45 queries of a 9-row verify with 5 heads per KV head, padded to 48,
@@ -25,9 +28,10 @@
 // waits and hand-overs), its bytes 1.4 thousand at head dimension 128. Eight
 // sequences of 4096 to 8192 tokens, head_dim 128, 128 queries: 49 us (519
 // TFLOP/s; mma.sync in tiles of 64: 85 us), 45 queries: 42 us (46). With fp32
-// queries 74 us (mma.sync in tiles of 32: 194 us) and 64 us (102): the products
+// queries 75 us (mma.sync in tiles of 16: 233 us) and 67 us (93): the products
 // are 1.6 thousand cycles a unit there, the terms of the probabilities nearly
-// as many again in the softmax warps, behind the products.
+// as many again in the softmax warps, behind the products; the sums' 4 us are
+// the price of an error of 3e-6.
 #pragma once
 
 #include "paged_attn.cuh"
@@ -51,8 +55,10 @@ struct TcShape {
   static constexpr int kO = 0, kS = HD, kQ = HD + 2 * kSCols;
   static constexpr int kQTerm = HD / 2;
   static constexpr int kCtas = HD == 64 && !F32 ? 2 : 1, kCols = 512 / kCtas;
-  static constexpr int kStages = HD == 64 && F32 ? 12 : 6;   // (192 KB an SM)
-  static constexpr int kSmem = 1024 + kStages * kStage;
+  static constexpr int kFold = F32 ? 16 : 1 << 30;      // units after which O moves to the sums
+  static constexpr int kSums = F32 ? MT * HD * 4 : 0;
+  static constexpr int kStages = !F32 ? 6 : HD == 64 ? 10 : 4;
+  static constexpr int kSmem = 1024 + kStages * kStage + kSums;
   // (as in paged_attn.cuh: 64 sequences of 100 to 2000 tokens, 8 KV heads, 45
   // queries: 64.8 us, 93.2 with none, 71.8 with 4, 68.3 with 14)
   static constexpr int kPiece = 8;
@@ -193,7 +199,7 @@ __global__ void __launch_bounds__(TcShape<HD, F32>::kThreads, TcShape<HD, F32>::
         await(&p_full[n & 1], (n >> 1) & 1);
         if (!good) break;
         tc_fence_after();
-        const uint32_t keep = u > 0 ? 1u : (uint32_t)__shfl_sync(0xffffffffu, s_keep[n & 1], 0);
+        const uint32_t keep = u % S::kFold ? 1u : (uint32_t)__shfl_sync(0xffffffffu, s_keep[n & 1], 0);
         const uint64_t d = dv + (uint64_t)(n % S::kStages * (S::kStage >> 4));
         const uint32_t t = utmem + S::kS + S::kSCols * (n & 1);
         if (elect_one()) {
@@ -219,6 +225,7 @@ __global__ void __launch_bounds__(TcShape<HD, F32>::kThreads, TcShape<HD, F32>::
     // ----------------------------------------------------------- softmax warps
     const int row = tid;                                  // query of the tile = tensor-memory lane
     const uint32_t lanes = tmem + ((uint32_t)(32 * warp) << 16);
+    float4* const sums = reinterpret_cast<float4*>(ring + S::kStages * S::kStage) + row;   // (128 apart)
     auto sync4 = [] { asm volatile("bar.sync 1, 128;" ::: "memory"); };
     int n = 0;
     // Waits for unit k's output, k the unit before the one at hand. (Two
@@ -264,6 +271,7 @@ __global__ void __launch_bounds__(TcShape<HD, F32>::kThreads, TcShape<HD, F32>::
       __syncwarp();
       if (lane == 0) mbar_arrive(&q_full);
       float m = -INFINITY, l = 0.f;
+      bool folded = false;                                // the sums hold a part of O
       // One unit: every row sees all slots of a plain one; a tail unit holds
       // slots of the pass itself, or slots past the end. (Apart, so that the
       // plain units' loop is short straight code.)
@@ -324,6 +332,13 @@ __global__ void __launch_bounds__(TcShape<HD, F32>::kThreads, TcShape<HD, F32>::
               tmem_st16(lanes + S::kO + 16 * c, v);
             }
             tmem_st_wait();
+            if (F32 && folded) {
+#pragma unroll 4
+              for (int c = 0; c < HD / 4; ++c) {
+                const float4 y = sums[128 * c];
+                sums[128 * c] = make_float4(y.x * f, y.y * f, y.z * f, y.w * f);
+              }
+            }
           }
           if (m == -INFINITY) m = mx;                     // (what came before saw nothing: O is 0)
           const float ref = m == -INFINITY ? 0.f : -m * a.scale2;
@@ -334,6 +349,30 @@ __global__ void __launch_bounds__(TcShape<HD, F32>::kThreads, TcShape<HD, F32>::
             l4[i & 3] += x[i];
           }
           l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+        }
+        // ---- O starts anew with the piece and after moving to the sums
+        const bool fresh = (t - w.t0) % S::kFold == 0;
+        if constexpr (F32) {
+          if (fresh && t > w.t0) {
+            o_wait(n - 1);
+            if (warp_live) {
+#pragma unroll 1
+              for (int c = 0; c < HD / 16; ++c) {
+                uint32_t v[16];
+                tmem_ld16(lanes + S::kO + 16 * c, v);
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 16; i += 4) {
+                  asm volatile("" : "+r"(v[i]), "+r"(v[i + 1]), "+r"(v[i + 2]), "+r"(v[i + 3]));
+                  float4* const p = sums + 128 * (4 * c + i / 4);
+                  const float4 y = folded ? *p : make_float4(0.f, 0.f, 0.f, 0.f);
+                  *p = make_float4(y.x + __uint_as_float(v[i]), y.y + __uint_as_float(v[i + 1]),
+                                   y.z + __uint_as_float(v[i + 2]), y.w + __uint_as_float(v[i + 3]));
+                }
+              }
+            }
+            folded = true;
+          }
         }
         // ---- values of a tail unit: slots past the end become 0; values of
         // the pass that are no finite numbers (odd: a probability 0 times NaN
@@ -370,7 +409,6 @@ __global__ void __launch_bounds__(TcShape<HD, F32>::kThreads, TcShape<HD, F32>::
                 float p[kTile];                           // (indexed at run time: local memory)
 #pragma unroll
                 for (int i = 0; i < kTile; ++i) p[i] = x[i];
-                const bool fresh = t == w.t0;
                 if (!fresh) o_wait(n - 1);
 #pragma unroll 1
                 for (int c = 0; c < HD / 16; ++c) {
@@ -428,7 +466,7 @@ __global__ void __launch_bounds__(TcShape<HD, F32>::kThreads, TcShape<HD, F32>::
           }
           tmem_st_wait();
         }
-        if (tid == 0 && t == w.t0) s_keep[b] = keep;   // (the MMA warp reads it at a piece's first unit)
+        if (tid == 0 && fresh) s_keep[b] = keep;       // (the MMA warp reads it where O starts anew)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[b]);
@@ -459,6 +497,16 @@ __global__ void __launch_bounds__(TcShape<HD, F32>::kThreads, TcShape<HD, F32>::
           tmem_ld_wait();
 #pragma unroll
           for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(v[i]));
+          if (F32 && folded) {
+#pragma unroll
+            for (int i = 0; i < 16; i += 4) {
+              const float4 y = sums[128 * (4 * c + i / 4)];
+              v[i] = __float_as_uint(__uint_as_float(v[i]) + y.x);
+              v[i + 1] = __float_as_uint(__uint_as_float(v[i + 1]) + y.y);
+              v[i + 2] = __float_as_uint(__uint_as_float(v[i + 2]) + y.z);
+              v[i + 3] = __float_as_uint(__uint_as_float(v[i + 3]) + y.w);
+            }
+          }
           if (!live) continue;
           // (a row that saw nothing: l = 0 and O = 0)
           if (whole && F32) {

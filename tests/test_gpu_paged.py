@@ -659,3 +659,26 @@ def test_large_tiles_of_strided_queries_and_other_scales(pkg, dq, dc, hd, rows):
     check_attn(c, *call(pkg, c))
     c["lens"] = [2, 70, -1]      # rows before position 0 see nothing
     check_attn(c, *call(pkg, c))
+
+
+@pytest.mark.parametrize("hd,nq", [(64, 40), (128, 40), (128, 7)])
+def test_fp32_sums_over_long_caches(pkg, hd, nq):
+    """Sums over hundreds of units a CTA keep fp32 accuracy: the tensor cores
+    cut off each product's addition, but no sum they keep is of more than 16
+    units of 12 products, 2^-23 of it each. Beside that, the fp32 additions of
+    those sums and of the parts (128 of 2^-24 at most), and the scores, small
+    here (qk): 2 (2^-22 + (hd + 8) 2^-23 qk). The values are positive, so that
+    the bound is relative to the output. The table repeats 40 pages, which
+    leaves the softmax's mean as it is."""
+    g = torch.Generator(device="cuda").manual_seed(hd + nq)
+    page, cycle, times, B = 256, 40, 190, 2
+    k = torch.randn((cycle, 1, page, hd), dtype=BF, device="cuda", generator=g)
+    v = torch.randn((cycle, 1, page, hd), dtype=BF, device="cuda", generator=g).abs()
+    q = torch.randn((B, nq, hd), device="cuda", generator=g) * 1e-3
+    tables = i32([list(range(cycle)) * times] * B)
+    out = pkg.paged_attention(q, k, v, tables, i32([page * cycle * times] * B)).double()
+    kd, vd = k.double().reshape(-1, hd), v.double().reshape(-1, hd)
+    ref = torch.softmax(q.double() @ kd.T / math.sqrt(hd), -1) @ vd
+    qk = float((q.double().abs() @ kd.abs().T).max()) / math.sqrt(hd)
+    bound = 192 * 2.0 ** -23 + 128 * 2.0 ** -24 + 2 * (2.0 ** -22 + (hd + 8) * 2.0 ** -23 * qk)
+    assert float(((out - ref).abs() / ref).max()) <= bound
