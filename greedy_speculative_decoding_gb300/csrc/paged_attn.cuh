@@ -207,7 +207,7 @@ struct Shape {
   // midst of its units otherwise ends that much later. 32 sequences of 0 to
   // 8191 tokens, 7 queries: 47.4 us, 48.4 with none (2 to 5 are alike, 49.1
   // with 14); 120 of up to 1000 tokens 29.3 and 36.5; fp32, one of 2057 tokens,
-  // 63 queries 11.1 and 13.6; 16 of 5 to 4099 tokens, 91 queries 12.8 and 15.8.
+  // 63 queries 11.1 and 14.1; 16 of 5 to 4099 tokens, 91 queries 12.8 and 15.8.
   static constexpr int kPiece = 4;
 };
 
