@@ -30,6 +30,10 @@ struct PlanArgs {
   int* n_free_out;
   int* status;
   int B, W, cap, shift, N;
+  // 1: the launch overlaps the end of the kernel before it, the next launch its own (plan, append and attention of one
+  // row: 13.3 us a pass in a stream, 16.7 without this and the append's overlap). 0 in the engine, whose projections
+  // count on everything but the kernel just before them being done.
+  int early;
 };
 cudaError_t launch_page_plan(const PlanArgs& a, cudaStream_t st);
 

@@ -77,6 +77,7 @@ struct Raw<float> {
 template <typename TI, typename TC, typename TO>
 __global__ void __launch_bounds__(kAppendThreads, sizeof(TI) == 2 ? 16 : 10)
     k_append(const __grid_constant__ AppendArgs a) {
+  pdl_wait();   // (the next kernel is not let in early: waiting beside 16411 rows it slowed them by 1.5 us)
   const int half = a.hd >> 1;
   const unsigned per_head = half >> 3;                              // threads of a head
   const unsigned per_row = (a.nq + 2 * a.nkv) * per_head;           // threads of a row
@@ -125,9 +126,16 @@ __global__ void __launch_bounds__(kAppendThreads, sizeof(TI) == 2 ? 16 : 10)
 
 template <typename TI, typename TC>
 cudaError_t launch_append(const AppendArgs& a, bool q_as_cache, int grid, cudaStream_t st) {
-  if (q_as_cache) k_append<TI, TC, TC><<<grid, kAppendThreads, 0, st>>>(a);
-  else k_append<TI, TC, TI><<<grid, kAppendThreads, 0, st>>>(a);
-  return cudaGetLastError();
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kAppendThreads);
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return q_as_cache ? cudaLaunchKernelEx(&cfg, k_append<TI, TC, TC>, a) : cudaLaunchKernelEx(&cfg, k_append<TI, TC, TI>, a);
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }

@@ -87,6 +87,8 @@ __global__ void __launch_bounds__(kPlanThreads) k_page_plan(const PlanArgs a) {
   __shared__ int2 warp_sums[32];
   __shared__ int s_granted;
   const int tid = threadIdx.x, NT = blockDim.x;
+  pdl_wait();
+  if (a.early) pdl_launch_next();
   const int n_free = min(max(*a.n_free, 0), a.cap);
 
   // The sums, cut off at one page more than there are (a sum past the stack's
@@ -261,26 +263,27 @@ cudaError_t launch_page_plan(const PlanArgs& a, cudaStream_t st) {
   if (e == cudaSuccess) {
     const bool apart = a.N >= kPlanManyRows;
     const int ctas = a.B >= kPlanClusterRequests || a.N >= kPlanClusterRows ? kPlanCluster : 1;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = ctas;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = ctas;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ctas);
     cfg.blockDim = dim3(ctas > 1 ? kPlanThreads : std::max(128, (std::max(a.B, a.N) + 31) / 32 * 32));
     cfg.dynamicSmemBytes = plan_smem_bytes(a.B);
     cfg.stream = st;
-    cfg.attrs = attr;
-    cfg.numAttrs = ctas > 1 ? 1 : 0;
+    cfg.attrs = a.early ? attr : attr + 1;
+    cfg.numAttrs = a.early + (ctas > 1);
     PlanArgs plan = a;
     if (apart) plan.N = 0;
     e = cudaLaunchKernelEx(&cfg, k_page_plan, plan);
     if (e == cudaSuccess && apart) {
-      attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-      attr[0].val.programmaticStreamSerializationAllowed = 1;
       cfg.gridDim = dim3(kRowCtas);
       cfg.blockDim = dim3(kRowThreads);
       cfg.dynamicSmemBytes = (size_t)(a.B + 1) * sizeof(int);
+      cfg.attrs = attr;
       cfg.numAttrs = 1;
       e = cudaLaunchKernelEx(&cfg, k_plan_rows, a);
     }
@@ -310,6 +313,7 @@ extern "C" sf_status sf_page_plan(const int32_t* d_lens, const int32_t* d_starts
   a.lens = d_lens, a.starts = d_starts, a.tables = d_tables, a.held = d_held, a.free = d_free, a.n_free = d_n_free;
   a.slots = d_slots, a.positions = d_positions, a.held_out = d_held_out, a.n_free_out = d_n_free_out;
   a.status = d_status;
+  a.early = 1;
   a.B = batch, a.W = table_width, a.cap = capacity, a.shift = log2_of(page), a.N = n_rows;
   const cudaError_t e = launch_page_plan(a, static_cast<cudaStream_t>(cuda_stream));
   if (e != cudaSuccess) return set_error(SF_ERR_CUDA, "sf_page_plan: %s", cudaGetErrorString(e));

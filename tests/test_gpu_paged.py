@@ -682,3 +682,49 @@ def test_fp32_sums_over_long_caches(pkg, hd, nq):
     qk = float((q.double().abs() @ kd.abs().T).max()) / math.sqrt(hd)
     bound = 192 * 2.0 ** -23 + 128 * 2.0 ** -24 + 2 * (2.0 ** -22 + (hd + 8) * 2.0 ** -23 * qk)
     assert float(((out - ref).abs() / ref).max()) <= bound
+
+
+@pytest.mark.parametrize("B,rows", [(3, 2), (90, 1), (90, 5)])
+def test_passes_back_to_back(pkg, B, rows):
+    """Sixty passes enqueued without a pause (each kernel may come up while
+    the one before it ends) leave what the same calls leave one at a time."""
+    nq, nkv, hd, page, W, passes = 8, 2, 64, 16, 24, 60
+    cap, n = B * W, B * rows
+    g = torch.Generator(device="cuda").manual_seed(B + rows)
+    r = random.Random(B)
+    at, lens = [r.randint(0, 60) for _ in range(B)], []
+    for p in range(passes):
+        for b in range(B):   # some requests end and begin again
+            at[b] = rows if r.random() < 0.05 or at[b] + rows > W * page else at[b] + rows
+        lens.append(i32(at))
+    starts = i32([b * rows for b in range(B + 1)])
+    rope = pkg.rope_table(W * page, hd, 1e4)
+    q, k, v = (torch.randn((passes, n, h, hd), dtype=BF, device="cuda", generator=g) for h in (nq, nkv, nkv))
+
+    def run(pause):
+        tables = torch.zeros((B, W), dtype=torch.int32, device="cuda")
+        held, free, nf = i32([0] * B), torch.arange(cap, dtype=torch.int32, device="cuda"), i32([cap])
+        kc = torch.zeros((cap, nkv, page, hd), dtype=BF, device="cuda")
+        vc = torch.zeros_like(kc)
+        slots, pos, status = i32([0] * n), i32([0] * n), i32([0] * B)
+        qr = torch.zeros((n, nq, hd), dtype=BF, device="cuda")
+        out = torch.zeros((passes, n, nq, hd), dtype=BF, device="cuda")
+        ws = pkg.paged_attention_workspace(q[0], kc, tables, rows)
+        steps = []
+        for p in range(passes):
+            steps.append(lambda p=p: pkg.page_plan(lens[p], starts, tables, held, free, nf, page, slots=slots, positions=pos,
+                                                   status=status))
+            steps.append(lambda p=p: pkg.kv_append(k[p], v[p], slots, kc, vc, q=q[p], q_out=qr, positions=pos, rope=rope))
+            steps.append(lambda p=p: pkg.paged_attention(qr, kc, vc, tables, lens[p], starts=starts, max_rows=rows,
+                                                         out=out[p], workspace=ws))
+        torch.cuda.synchronize()
+        for s in steps:
+            s()
+            if pause:
+                torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        assert int(status.abs().sum()) == 0
+        return out, kc, vc, tables, held, nf
+
+    for a, b in zip(run(True), run(False)):
+        assert torch.equal(a, b)
