@@ -31,7 +31,7 @@ constexpr int kPlanCluster = 8;      // CTAs of a pass with many pieces
 constexpr int kPlanClusterRequests = 64, kPlanClusterRows = 1024;
 // Rows from which they get a kernel of their own over the whole GPU: 16000 rows
 // take 5.5 us in the plan's cluster and 6.8 us so, 32000 rows 7.8 and 7.0 us,
-// 512000 rows 66 and 9.8 us.
+// 512000 rows 66 and 8.4 us.
 constexpr int kPlanManyRows = 32768;
 constexpr int kRowThreads = 256, kRowCtas = 608;
 
