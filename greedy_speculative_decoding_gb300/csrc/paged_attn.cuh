@@ -3,7 +3,8 @@
 // For a token row and query head, out = sum_s p_s v_s / sum_s p_s with
 // p_s = 2^(x_s - max x), x_s = (q . k_s) * scale * log2(e), over the slots s
 // that the row sees. The cache is read once: the maximum, the sum and the
-// output run along with the slots (in fp32; a new maximum rescales them).
+// output run along with the slots (in fp32; a new maximum rescales them). For
+// fp16 the p_s are a power of two larger (Num::kUp), and so are both sums.
 //
 // Work. An item is (request, KV head, tile of MT queries): the queries are
 // the request's rows times the query heads that read this KV head. An item
@@ -126,6 +127,7 @@ struct Num;
 template <>
 struct Num<bf16> {
   static constexpr uint32_t kExp = 0x7f80u;   // exponent bits: all set in infinities and NaN
+  static constexpr int kUp = 0;
   static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&v);
@@ -142,6 +144,11 @@ struct Num<bf16> {
 template <>
 struct Num<__half> {
   static constexpr uint32_t kExp = 0x7c00u;
+  // Probabilities are at most 2^kUp, so that fp16 holds those down to 2^-29 of
+  // the largest with all their bits and the rest to 2^-40 of it. (At most 1,
+  // they lost bits from 2^-14 on and everything from 2^-25: behind one slot far
+  // above the others the others' values were gone while the sum counted them.)
+  static constexpr int kUp = 15;
   static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
     const __half2 v = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&v);
@@ -616,7 +623,7 @@ __global__ void __launch_bounds__(Shape<HD, WM, WK, F32>::kThreads, Shape<HD, WM
         }
       }
 #pragma unroll
-      for (int e = 0; e < 2; ++e) ref[e] = m[e] == -INFINITY ? 0.f : -m[e] * a.scale2;
+      for (int e = 0; e < 2; ++e) ref[e] = m[e] == -INFINITY ? 0.f : fmaf(-m[e], a.scale2, (float)Num<TC>::kUp);
 #pragma unroll
       for (int i = 0; i < NS; ++i)
 #pragma unroll
@@ -769,7 +776,7 @@ __global__ void __launch_bounds__(Shape<HD, WM, WK, F32>::kThreads, Shape<HD, WM
       l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
       l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
       if (!ok) l[e] = __int_as_float(0x7fc00000);   // an expired wait: NaN
-      if (m[e] != -INFINITY) m[e] *= a.scale2;
+      if (m[e] != -INFINITY) m[e] = fmaf(m[e], a.scale2, (float)-Num<TC>::kUp);
     }
     const bool begins = w.t0 == 0, whole = begins && w.t1 == r.nt;
     if (begins && tid == 0) describe(a, w, deal, whole);

@@ -58,7 +58,7 @@ cudaError_t launch_mma(Args& a, int sms, long max_units, cudaStream_t st) {
 
 template <int HD, typename TC, bool F32>
 cudaError_t launch_tc(Args& a, int sms, long max_units, cudaStream_t st) {
-  using S = TcShape<HD, F32>;
+  using S = TcShape<HD, TC, F32>;
   static_assert(S::kPiece <= kMaxPiece);
   using TQ = typename std::conditional<F32, float, TC>::type;
   static std::atomic<uint64_t> ready{0};

@@ -10,10 +10,13 @@
 //     there means that output complete;
 //   * four softmax warps, a thread per query row: row maximum and sum without
 //     shuffles. O is rescaled only when a row's maximum has grown by more than
-//     2^8 since its reference was set (probabilities then stay below 256), so
-//     seldom after the first unit. Probabilities of 16-bit queries are rounded
-//     to the cache's type, by half a step each; with a lagging reference that
-//     includes the largest, which is exactly 1 in the mma.sync kernel.
+//     2^kLag since its reference was set, so seldom after the first unit.
+//     Probabilities of 16-bit queries are rounded to the cache's type, by half a
+//     step each; with a lagging reference that includes the largest, which is
+//     exactly a power of two in the mma.sync kernel. bf16 has the range for a
+//     lag of 2^8; fp16 probabilities are taken times 2^12 and may lag by 2^3, so
+//     that the largest stay below 2^15 and those down to 2^-26 of it keep their
+//     bits (the others are off by 2^-37 of it at most).
 //   * fp32 queries and their probabilities are three bf16 terms each (24 bits:
 //     exact), so three products in place of one, the small terms first. The
 //     tensor cores cut off what they add to the output (54 units of 12 products
@@ -39,7 +42,7 @@
 namespace sf {
 namespace pa {
 
-template <int HD, bool F32>
+template <int HD, typename TC, bool F32>
 struct TcShape {
   static constexpr int MT = 128;
   static constexpr int kThreads = 192;                 // 4 softmax warps, producer, MMA
@@ -50,6 +53,8 @@ struct TcShape {
   // queries; fp32 queries and probabilities as three 16-bit terms. At head
   // dimension 64 two CTAs share an SM where that fits (the softmax of one alone
   // takes longer than its units' bytes).
+  static constexpr int kLag = std::is_same<TC, __half>::value ? 3 : 8;   // (in powers of two, as kUp)
+  static constexpr int kUp = std::is_same<TC, __half>::value ? 12 : 0;
   static constexpr int kTerms = F32 ? 3 : 1;
   static constexpr int kSCols = F32 ? 96 : 64;           // of S (64), then of P (32 a term)
   static constexpr int kO = 0, kS = HD, kQ = HD + 2 * kSCols;
@@ -107,9 +112,9 @@ __device__ __forceinline__ void put_terms(uint32_t taddr, float (&x)[64]) {
 
 // TC: the cache's type. F32: fp32 queries and output over a bf16 cache.
 template <int HD, typename TC, bool F32>
-__global__ void __launch_bounds__(TcShape<HD, F32>::kThreads, TcShape<HD, F32>::kCtas)
+__global__ void __launch_bounds__(TcShape<HD, TC, F32>::kThreads, TcShape<HD, TC, F32>::kCtas)
     k_paged_attn_tc(const __grid_constant__ Args a) {
-  using S = TcShape<HD, F32>;
+  using S = TcShape<HD, TC, F32>;
   using TQ = typename std::conditional<F32, float, TC>::type;
   constexpr int MT = S::MT;
   extern __shared__ unsigned char pa_smem_raw[];
@@ -313,10 +318,11 @@ __global__ void __launch_bounds__(TcShape<HD, F32>::kThreads, TcShape<HD, F32>::
 #pragma unroll
           for (int i = 4; i < kTile; ++i) mx4[i & 3] = fmaxf(mx4[i & 3], x[i]);
           const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
-          const bool grow = m != -INFINITY && (mx - m) * a.scale2 > 8.f;
-          if (__any_sync(0xffffffffu, grow)) {
-            const float f = grow ? exp2_approx((m - mx) * a.scale2) : 1.f;
-            if (grow) m = mx;
+          const bool grow = m != -INFINITY && (mx - m) * a.scale2 > (float)S::kLag;
+          if (__any_sync(0xffffffffu, grow)) {            // (then for every row whose maximum is a new one)
+            const bool raise = m != -INFINITY && mx > m;
+            const float f = raise ? exp2_approx((m - mx) * a.scale2) : 1.f;
+            if (raise) m = mx;
             l *= f;
             o_wait(n - 1);   // (never at the piece's first unit: m was -infinity)
 #pragma unroll 1
@@ -341,7 +347,7 @@ __global__ void __launch_bounds__(TcShape<HD, F32>::kThreads, TcShape<HD, F32>::
             }
           }
           if (m == -INFINITY) m = mx;                     // (what came before saw nothing: O is 0)
-          const float ref = m == -INFINITY ? 0.f : -m * a.scale2;
+          const float ref = m == -INFINITY ? 0.f : fmaf(-m, a.scale2, (float)S::kUp);
           float l4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int i = 0; i < kTile; ++i) {
@@ -481,7 +487,7 @@ __global__ void __launch_bounds__(TcShape<HD, F32>::kThreads, TcShape<HD, F32>::
       if (w.t1 - w.t0 > 1) o_wait(n - 2);
       o_wait(n - 1);
       if (!ok) l = __int_as_float(0x7fc00000);   // an expired wait: NaN
-      if (m != -INFINITY) m *= a.scale2;
+      if (m != -INFINITY) m = fmaf(m, a.scale2, (float)-S::kUp);
       const bool begins = w.t0 == 0, whole = begins && w.t1 == r.nt;
       if (begins && tid == 0) describe(a, w, deal, whole);
       const long slot = 2l * blockIdx.x + (begins ? 1 : 0);

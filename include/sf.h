@@ -506,8 +506,9 @@ SF_API sf_status sf_kv_append(const sf_paged_cache* cache, int32_t n, const sf_r
  * every request are left as they were. lens[b] is cut to table_width * page,
  * and a table entry that is no page of the cache reads as zeros.
  * q and out have one type: the cache's, or F32 over a BF16 cache (exact in the
- * queries and probabilities: each is three bf16 terms). n_heads a multiple of
- * n_kv_heads. workspace: sf_paged_attention_workspace_bytes(...) bytes of
+ * queries and probabilities: each is three bf16 terms). Probabilities of 16-bit
+ * queries are rounded to that type, by half a step of each, or in fp16 by 2^-37
+ * of the row's largest if that is more. n_heads a multiple of n_kv_heads. workspace: sf_paged_attention_workspace_bytes(...) bytes of
  * device scratch, 256-byte aligned, any contents; calls that may overlap on
  * the GPU need one each. A result depends on the whole batch's lengths in its
  * last bits (the split over the cache's length follows them) and is the same

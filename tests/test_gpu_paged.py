@@ -728,3 +728,50 @@ def test_passes_back_to_back(pkg, B, rows):
 
     for a, b in zip(run(True), run(False)):
         assert torch.equal(a, b)
+
+
+# One item (request and KV head) a CTA, in tiles of 16, 32 or 128 queries: as
+# many requests as it takes, all over the same pages.
+ITEMS = [(1, 7), (3, 7), (9, 7)]   # rows, query heads of a KV head
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("rows,group", ITEMS)
+@pytest.mark.parametrize("gap", [12, 16, 18])
+@pytest.mark.parametrize("at", [0, 40000])
+def test_fp16_tail_behind_dominant_slots(pkg, hd, rows, group, gap, at):
+    """Four slots (of one unit, apart) whose score lies `gap` above that of
+    65536 others and whose values are 0: the output is the others' alone, each
+    with a probability of e^-gap of the largest. Scores are exact here. Beside
+    half a step of each probability and of the output, a probability in fp16
+    may be off by 2^-37 of the largest (half its smallest step, 2^-25, as the
+    probabilities are scaled by 2^12 at least). eps: rounding of the scaled
+    score (|x| <= 2 gap log2 e: two roundings of 2^-24, to the base 2) and of
+    the exponential (2^-22); the sums of probabilities and values lose at most
+    2^-23 for every 16 slots."""
+    nkv, page, n = 2, 256, 65536 + 256
+    B = 160
+    g = torch.Generator(device="cuda").manual_seed(gap)
+    k = torch.zeros((n // page, nkv, page, hd), dtype=FH, device="cuda")
+    v = torch.randn((n // page, nkv, page, hd), dtype=FH, device="cuda", generator=g).abs()
+    for s in (0, 16, 32, 48):
+        k[(at + s) // page, :, (at + s) % page, 0] = gap
+        v[(at + s) // page, :, (at + s) % page] = 0
+    q = torch.zeros((B * rows, nkv * group, hd), dtype=FH, device="cuda")
+    q[:, :, 0] = 1.0
+    width = 140000 // page   # (wide enough for tiles of 128)
+    tables = torch.arange(width, dtype=torch.int32, device="cuda").clamp(max=n // page - 1).repeat(B, 1)
+    lse = torch.zeros((B * rows, nkv * group), device="cuda")
+    out = pkg.paged_attention(q, k, v, tables, i32([n] * B), max_rows=rows, scale=1.0, lse=lse).double()
+    w = torch.full((n,), math.exp(-gap), dtype=torch.float64, device="cuda")
+    w[at:at + 64:16] = 1.0
+    vd = v.transpose(0, 1).reshape(nkv, n, hd).double()
+    eps = 2 * (4 * gap * 1.4427 * 2.0 ** -24 + 2.0 ** -22) + n / 16 * 2.0 ** -23
+    for j in range(rows):
+        m = n - rows + j + 1
+        total = w[:m].sum()
+        ref = ((w[:m, None] * vd[:, :m]).sum(1) / total).repeat_interleave(group, 0)        # [heads, hd]
+        bound = 2 * (U[FH] + eps) * ref + m * 2.0 ** -37 * float(vd.max()) / total + TINY[FH]
+        err = (out[j::rows] - ref).abs()
+        assert bool((err <= bound).all()), float((err / bound).max())
+        assert float((lse[j::rows].double() - gap - torch.log(total)).abs().max()) <= eps
