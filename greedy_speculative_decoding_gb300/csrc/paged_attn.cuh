@@ -195,10 +195,12 @@ struct Shape {
   static constexpr int kBox = kTile * 128;           // bytes of one box column: 64 slots x 64 dimensions
   static constexpr int kStage = 2 * kHalf * kBox;    // keys and values of a unit
   static constexpr int QP = HD + 8;                  // pitch of fp32 queries in shared memory (others: registers)
-  static constexpr int OP = HD + 8;                  // pitch of the parts joined over wk
+  // Parts (output, and behind it maximum and sum) in shared memory: pitch (4
+  // more would cost 32 fp32 queries a stage of the ring).
+  static constexpr int OP = HD + (F32 && WM == 2 ? 4 : 8);
   static constexpr int kQBytes = F32 ? 3 * MT * QP * 2 : 0;
-  static constexpr int kOBytes = WK * MT * (OP + 2) * 4;
-  static constexpr int kExtra = kQBytes > kOBytes ? kQBytes : kOBytes;   // one region: never both at once
+  static constexpr int kOBytes = WK * MT * OP * 4;
+  static constexpr int kExtra = kQBytes + kOBytes;
   static constexpr int kMaxStages = 6;
   // Two CTAs on an SM when at least two stages fit in half its shared memory
   // and the registers do: the 16-bit kernel with two query tiles at head
@@ -216,6 +218,12 @@ struct Shape {
   // with 14); 120 of up to 1000 tokens 29.3 and 36.5; fp32, one of 2057 tokens,
   // 63 queries 11.1 and 14.1; 16 of 5 to 4099 tokens, 91 queries 12.8 and 15.8.
   static constexpr int kPiece = 4;
+  // Units after which a warp's output and sum move to the part in shared
+  // memory. The tensor cores cut off what they add, always towards zero, and
+  // rounded sums of many like terms err one way as well: over 2^20 slots in one
+  // CTA outputs were 0.08% too small in tiles of 16 and 0.25% in tiles of 32,
+  // sums of equal probabilities 1e-4 off.
+  static constexpr int kFold = 128;
 };
 
 // Where a CTA's units begin.
@@ -533,6 +541,40 @@ __global__ void __launch_bounds__(Shape<HD, WM, WK, F32>::kThreads, Shape<HD, WM
     float o[ND][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 #pragma unroll
     for (int d = 0; d < ND; ++d) o[d][0] = o[d][1] = o[d][2] = o[d][3] = 0.f;
+    float* const so = reinterpret_cast<float*>(extra + S::kQBytes);   // parts: [WK][MT][OP]
+    auto so_ml = [&](int x) { return reinterpret_cast<float2*>(so + x * S::OP + HD); };
+    // Adds what the warp's part holds to output and sum; its reference may be an
+    // older maximum.
+    auto unfold = [&] {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int x = wk * MT + 16 * wm + g + 8 * e;
+        const float2 ml = *so_ml(x);
+        const float f = ml.x == -INFINITY ? 0.f : exp2_approx((ml.x - m[e]) * a.scale2);
+        if (c4 == 0) l[e] = fmaf(ml.y, f, l[e]);   // (a lane's l is a quarter of the row's)
+#pragma unroll
+        for (int d = 0; d < ND; ++d) {
+          const float2 y = *reinterpret_cast<const float2*>(so + x * S::OP + 8 * d + 2 * c4);
+          o[d][2 * e] = fmaf(y.x, f, o[d][2 * e]);
+          o[d][2 * e + 1] = fmaf(y.y, f, o[d][2 * e + 1]);
+        }
+      }
+    };
+    // Output, sum and maximum to the warp's part.
+    auto leave = [&] {
+      __syncwarp();   // (what it held has been read)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int x = wk * MT + 16 * wm + g + 8 * e;
+        l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
+        l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
+#pragma unroll
+        for (int d = 0; d < ND; ++d)
+          *reinterpret_cast<float2*>(so + x * S::OP + 8 * d + 2 * c4) = make_float2(o[d][2 * e], o[d][2 * e + 1]);
+        if (c4 == 0) *so_ml(x) = make_float2(m[e], l[e]);
+      }
+      __syncwarp();
+    };
 
     // One unit. Every row sees all slots of a plain one; a tail unit holds
     // slots of the pass itself, or slots past the end; in an odd one, some of
@@ -624,13 +666,16 @@ __global__ void __launch_bounds__(Shape<HD, WM, WK, F32>::kThreads, Shape<HD, WM
       }
 #pragma unroll
       for (int e = 0; e < 2; ++e) ref[e] = m[e] == -INFINITY ? 0.f : fmaf(-m[e], a.scale2, (float)Num<TC>::kUp);
+      float sum[2] = {0.f, 0.f};
 #pragma unroll
       for (int i = 0; i < NS; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           x[i][e] = exp2_approx(fmaf(x[i][e], a.scale2, ref[e >> 1]));
-          l[e >> 1] += x[i][e];
+          sum[e >> 1] += x[i][e];
         }
+      l[0] += sum[0];
+      l[1] += sum[1];
       // ---- output: probabilities (the cache's type, or three bf16 terms) x
       // values. In a tail unit values past the end are cut off; in an odd one
       // the pass's values that are no finite numbers are taken out of the
@@ -760,24 +805,34 @@ __global__ void __launch_bounds__(Shape<HD, WM, WK, F32>::kThreads, Shape<HD, WM
         if (lane == 0) mbar_arrive(&empty[n % S::kStages]);
       }
     }
+    auto fold_now = [&] {
+      if ((t - w.t0) % S::kFold || t == w.t0) return;
+      if (t - w.t0 > S::kFold) unfold();
+      leave();
+      l[0] = l[1] = 0.f;
+#pragma unroll
+      for (int d = 0; d < ND; ++d) o[d][0] = o[d][1] = o[d][2] = o[d][3] = 0.f;
+    };
     for (; t < min(w.t1, plain); ++t) {
+      fold_now();
       arrived();
       unit(std::integral_constant<int, PLAIN>{}, t);
     }
     for (; t < w.t1; ++t) {
+      fold_now();
       arrived();
       if (odd_values(t)) unit(std::integral_constant<int, ODD>{}, t);
       else unit(std::integral_constant<int, TAILED>{}, t);
     }
 
-    // ---- the end of the piece
+    // ---- the end of the piece: everything to this warp's part
+    if (w.t1 - w.t0 > S::kFold) unfold();
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
-      l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
       if (!ok) l[e] = __int_as_float(0x7fc00000);   // an expired wait: NaN
       if (m[e] != -INFINITY) m[e] = fmaf(m[e], a.scale2, (float)-Num<TC>::kUp);
     }
+    leave();
     const bool begins = w.t0 == 0, whole = begins && w.t1 == r.nt;
     if (begins && tid == 0) describe(a, w, deal, whole);
     const long slot = 2l * blockIdx.x + (begins ? 1 : 0);
@@ -785,17 +840,6 @@ __global__ void __launch_bounds__(Shape<HD, WM, WK, F32>::kThreads, Shape<HD, WM
     float2* part_ml = a.part_ml + slot * a.mt_max;
     const float kLn2 = 0.693147180559945f;
     // Joined over the warps that shared out the slots.
-    float* so = reinterpret_cast<float*>(extra);                 // [WK][MT][OP]
-    float2* sml = reinterpret_cast<float2*>(so + WK * MT * S::OP);   // [WK][MT]
-    if (F32) cta_sync();   // the queries' terms have been read
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int x = wk * MT + 16 * wm + g + 8 * e;
-#pragma unroll
-      for (int d = 0; d < ND; ++d)
-        *reinterpret_cast<float2*>(so + x * S::OP + 8 * d + 2 * c4) = make_float2(o[d][2 * e], o[d][2 * e + 1]);
-      if (c4 == 0) sml[x] = make_float2(m[e], l[e]);
-    }
     cta_sync();
     for (int e = tid; e < MT * (HD / 4); e += S::kWarps * 32) {
       const int x = e / (HD / 4), d = 4 * (e - x * (HD / 4));
@@ -805,7 +849,7 @@ __global__ void __launch_bounds__(Shape<HD, WM, WK, F32>::kThreads, Shape<HD, WM
       float2 ml[WK];
 #pragma unroll
       for (int k = 0; k < WK; ++k) {
-        ml[k] = sml[k * MT + x];
+        ml[k] = *so_ml(k * MT + x);
         mm = fmaxf(mm, ml[k].x);
       }
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);

@@ -21,7 +21,7 @@
 //     exact), so three products in place of one, the small terms first. The
 //     tensor cores cut off what they add to the output (54 units of 12 products
 //     left it 8e-6 too small), so it moves every 16 units to sums in shared
-//     memory that are rounded.
+//     memory that are rounded (of 16-bit queries every 256 units).
 //
 // mma.sync reaches 590 TFLOP/s on this GPU (measured, four or more warps an
 // SM); the 45 queries of a 9-row verify with 5 heads per KV head, padded to 48,
@@ -60,7 +60,10 @@ struct TcShape {
   static constexpr int kO = 0, kS = HD, kQ = HD + 2 * kSCols;
   static constexpr int kQTerm = HD / 2;
   static constexpr int kCtas = HD == 64 && !F32 ? 2 : 1, kCols = 512 / kCtas;
-  static constexpr int kFold = F32 ? 16 : 1 << 30;      // units after which O moves to the sums
+  // Units after which O moves to the sums. Of 16-bit queries the sums are the
+  // piece's place in the workspace (over 2^20 slots in one CTA outputs were 0.5%
+  // too small without).
+  static constexpr int kFold = F32 ? 16 : 256;
   static constexpr int kSums = F32 ? MT * HD * 4 : 0;
   static constexpr int kStages = !F32 ? 6 : HD == 64 ? 10 : 4;
   static constexpr int kSmem = 1024 + kStages * kStage + kSums;
@@ -123,6 +126,7 @@ __global__ void __launch_bounds__(TcShape<HD, TC, F32>::kThreads, TcShape<HD, TC
   __shared__ __align__(8) uint64_t full[S::kStages], empty[S::kStages], s_full[2], p_full[2], o_done[2], q_full, drain;
   __shared__ uint32_t s_tmem;
   __shared__ int s_keep[2];     // the unit adds to what the softmax put into O (see odd values)
+  __shared__ float s_sum[F32 ? MT : 1];   // the part of l that goes with the sums
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) {
     for (int s = 0; s < S::kStages; ++s) {
@@ -277,6 +281,39 @@ __global__ void __launch_bounds__(TcShape<HD, TC, F32>::kThreads, TcShape<HD, TC
       if (lane == 0) mbar_arrive(&q_full);
       float m = -INFINITY, l = 0.f;
       bool folded = false;                                // the sums hold a part of O
+      if constexpr (F32) s_sum[row] = 0.f;
+      const long slot = 2l * blockIdx.x + (w.t0 == 0 ? 1 : 0);
+      float* const part = a.part + (slot * a.mt_max + row) * HD;     // (of a live row)
+      float2* const part_ml = a.part_ml + slot * a.mt_max + row;
+      // 16-bit queries, between two units: O and l move to the part (`first`:
+      // which holds nothing yet), whose reference may be an older maximum.
+      auto fold = [&](bool first) {
+        o_wait(n - 1);
+        const float2 ml = live && !first ? *part_ml : make_float2(-INFINITY, 0.f);
+        const float f = ml.x == -INFINITY ? 0.f : exp2_approx((ml.x - m) * a.scale2);
+        if (live) *part_ml = make_float2(m, fmaf(ml.y, f, l));
+        l = 0.f;
+        if (warp_live) {
+#pragma unroll 1
+          for (int c = 0; c < HD / 16; ++c) {
+            uint32_t v[16];
+            tmem_ld16(lanes + S::kO + 16 * c, v);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(v[i]));
+            if (live) {
+#pragma unroll
+              for (int i = 0; i < 16; i += 4) {
+                float4* const p = reinterpret_cast<float4*>(part + 16 * c + i);
+                const float4 y = first ? make_float4(0.f, 0.f, 0.f, 0.f) : *p;
+                *p = make_float4(fmaf(y.x, f, __uint_as_float(v[i])), fmaf(y.y, f, __uint_as_float(v[i + 1])),
+                                 fmaf(y.z, f, __uint_as_float(v[i + 2])), fmaf(y.w, f, __uint_as_float(v[i + 3])));
+              }
+            }
+            __syncwarp();
+          }
+        }
+      };
       // One unit: every row sees all slots of a plain one; a tail unit holds
       // slots of the pass itself, or slots past the end. (Apart, so that the
       // plain units' loop is short straight code.)
@@ -339,6 +376,7 @@ __global__ void __launch_bounds__(TcShape<HD, TC, F32>::kThreads, TcShape<HD, TC
             }
             tmem_st_wait();
             if (F32 && folded) {
+              s_sum[row] *= f;
 #pragma unroll 4
               for (int c = 0; c < HD / 4; ++c) {
                 const float4 y = sums[128 * c];
@@ -378,6 +416,8 @@ __global__ void __launch_bounds__(TcShape<HD, TC, F32>::kThreads, TcShape<HD, TC
               }
             }
             folded = true;
+            s_sum[row] += l;
+            l = 0.f;
           }
         }
         // ---- values of a tail unit: slots past the end become 0; values of
@@ -480,20 +520,38 @@ __global__ void __launch_bounds__(TcShape<HD, TC, F32>::kThreads, TcShape<HD, TC
       };
       const int plain = max(0, min(r.p0, r.len)) / kTile;   // units whose slots every row sees
       int t = w.t0;
-      for (; t < min(w.t1, plain); ++t) unit(std::false_type{}, t);
-      for (; t < w.t1; ++t) unit(std::true_type{}, t);
+      auto fold_now = [&] {
+        if (!F32 && (t - w.t0) % S::kFold == 0 && t > w.t0) {
+          fold(!folded);
+          folded = true;
+        }
+      };
+      for (; t < min(w.t1, plain); ++t) {
+        fold_now();
+        unit(std::false_type{}, t);
+      }
+      for (; t < w.t1; ++t) {
+        fold_now();
+        unit(std::true_type{}, t);
+      }
 
       // ---- the end of the piece (both barriers are then past its units)
       if (w.t1 - w.t0 > 1) o_wait(n - 2);
       o_wait(n - 1);
+      float f = 0.f;                             // of what lies in the part
+      if (F32) {
+        l += s_sum[row];
+      } else if (folded && live) {
+        const float2 ml = *part_ml;
+        f = ml.x == -INFINITY ? 0.f : exp2_approx((ml.x - m) * a.scale2);
+        l = fmaf(ml.y, f, l);
+      }
       if (!ok) l = __int_as_float(0x7fc00000);   // an expired wait: NaN
       if (m != -INFINITY) m = fmaf(m, a.scale2, (float)-S::kUp);
       const bool begins = w.t0 == 0, whole = begins && w.t1 == r.nt;
       if (begins && tid == 0) describe(a, w, deal, whole);
-      const long slot = 2l * blockIdx.x + (begins ? 1 : 0);
       if (warp_live) {
         const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
-        float* part = a.part + (slot * a.mt_max + row) * HD;
         TQ* dst = static_cast<TQ*>(a.out) + (r.s0 + j) * a.o_row + hh * a.o_head;
 #pragma unroll 1
         for (int c = 0; c < HD / 16; ++c) {
@@ -514,6 +572,16 @@ __global__ void __launch_bounds__(TcShape<HD, TC, F32>::kThreads, TcShape<HD, TC
             }
           }
           if (!live) continue;
+          if (!F32 && folded) {
+#pragma unroll
+            for (int i = 0; i < 16; i += 4) {
+              const float4 y = *reinterpret_cast<const float4*>(part + 16 * c + i);
+              v[i] = __float_as_uint(fmaf(y.x, f, __uint_as_float(v[i])));
+              v[i + 1] = __float_as_uint(fmaf(y.y, f, __uint_as_float(v[i + 1])));
+              v[i + 2] = __float_as_uint(fmaf(y.z, f, __uint_as_float(v[i + 2])));
+              v[i + 3] = __float_as_uint(fmaf(y.w, f, __uint_as_float(v[i + 3])));
+            }
+          }
           // (a row that saw nothing: l = 0 and O = 0)
           if (whole && F32) {
 #pragma unroll
@@ -534,7 +602,7 @@ __global__ void __launch_bounds__(TcShape<HD, TC, F32>::kThreads, TcShape<HD, TC
         }
         if (live && whole && a.lse)
           a.lse[(long)(r.s0 + j) * a.nq + hh] = l == 0.f ? -INFINITY : m * 0.693147180559945f + logf(l);
-        if (live && !whole) a.part_ml[slot * a.mt_max + row] = make_float2(m, l);
+        if (live && !whole) *part_ml = make_float2(m, l);
       }
       tc_fence_before();   // O has been read: the next piece's first product may replace it
     }

@@ -775,3 +775,65 @@ def test_fp16_tail_behind_dominant_slots(pkg, hd, rows, group, gap, at):
         err = (out[j::rows] - ref).abs()
         assert bool((err <= bound).all()), float((err / bound).max())
         assert float((lse[j::rows].double() - gap - torch.log(total)).abs().max()) <= eps
+
+
+@pytest.mark.parametrize("dt", [BF, FH])
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("rows,group", ITEMS)
+def test_16_bit_sums_over_long_items(pkg, dt, hd, rows, group):
+    """Items of 2^20 slots, one a CTA. The tensor cores cut off what they add,
+    always to the same side, so no sum that they keep is of more than 256 units
+    of four products, 2^-23 of it each; the additions of those sums are 64 of
+    2^-24. Keys are 0 (every probability exactly the largest, sums of them
+    exact) and values positive; the output's own rounding, half a step at most
+    for each element, averages out over the outputs that differ (five standard
+    deviations of a uniform error)."""
+    nkv, page, cycle, B = 8, 256, 16, 40
+    g = torch.Generator(device="cuda").manual_seed(hd)
+    k = torch.zeros((cycle, nkv, page, hd), dtype=dt, device="cuda")
+    v = torch.randn((cycle, nkv, page, hd), dtype=dt, device="cuda", generator=g).abs() + 0.5
+    q = torch.ones((B * rows, nkv * group, hd), dtype=dt, device="cuda")
+    W = 2 ** 20 // page
+    tables = (torch.arange(W, dtype=torch.int32, device="cuda") % cycle).repeat(B, 1)
+    lse = torch.zeros((B * rows, nkv * group), device="cuda")
+    out = pkg.paged_attention(q, k, v, tables, i32([2 ** 20] * B), max_rows=rows, lse=lse).double()
+    ends = v[-1].double().flip(1).cumsum(1)                    # sums of the last slots
+    mean = []
+    for j in range(rows):                                      # row j does not see the last rows - 1 - j
+        x = v.double().sum((0, 2)) * (W // cycle) - (ends[:, rows - 2 - j] if j < rows - 1 else 0)
+        mean.append((x / (2 ** 20 - (rows - 1 - j))).repeat_interleave(group, 0))
+    ref = torch.stack(mean).repeat(B, 1, 1)
+    rel = out / ref - 1
+    sums = 1024 * 2.0 ** -23 + 64 * 2.0 ** -24
+    assert float(rel.abs().max()) <= U[dt] + sums
+    assert abs(float(rel.mean())) <= sums + 5 * U[dt] / math.sqrt(3 * nkv * hd)
+    seen = torch.tensor([2 ** 20 - (rows - 1 - j) for j in range(rows)], dtype=torch.float64, device="cuda").log()
+    assert float((lse.double() - seen.repeat(B)[:, None]).abs().max()) <= 2.0 ** -17
+
+
+@pytest.mark.parametrize("dq,dc", TYPES)
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("rows,group", ITEMS)
+def test_sums_of_like_probabilities(pkg, dq, dc, hd, rows, group):
+    """Items of 2^20 slots, one a CTA, nearly all with one probability that is
+    no power of two: fp32 sums of them err the same way at every step, half a
+    step (2^-24) at most. No sum is of more than 1024 + 16 + 32 steps (fp32
+    queries in tiles of 128: 32 within a unit, 16 units, 1024 times those;
+    others have 128 or 256 units and 128 or 64 times those). Beside that the
+    exponential (2^-22), the rounding of the scaled score (two of 2^-24, times
+    log2 e * 1.25) and of the logarithm (2^-24 * 16, twice)."""
+    nkv, page, cycle, B = 8, 256, 16, 40
+    g = torch.Generator(device="cuda").manual_seed(hd)
+    k = torch.zeros((cycle, nkv, page, hd), dtype=dc, device="cuda")
+    k[:, :, 1:, 0] = -1.2
+    q = torch.zeros((B * rows, nkv * group, hd), dtype=dq, device="cuda")
+    q[:, :, 0] = 1.0
+    W = 2 ** 20 // page
+    tables = (torch.arange(W, dtype=torch.int32, device="cuda") % cycle).repeat(B, 1)
+    lse = torch.zeros((B * rows, nkv * group), device="cuda")
+    v = torch.randn((cycle, nkv, page, hd), dtype=dc, device="cuda", generator=g)
+    pkg.paged_attention(q, k, v, tables, i32([2 ** 20] * B), max_rows=rows, scale=1.0, lse=lse)
+    p = math.exp(float(k[0, 0, 1, 0]))
+    want = torch.tensor([math.log(W + (W * 255 - (rows - 1 - j)) * p) for j in range(rows)], dtype=torch.float64)
+    bound = 1072 * 2.0 ** -24 + 2.0 ** -22 + 4 * 2.0 ** -24 + 32 * 2.0 ** -24
+    assert float((lse.double().cpu() - want.repeat(B)[:, None]).abs().max()) <= bound
