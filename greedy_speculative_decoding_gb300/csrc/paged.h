@@ -1,6 +1,8 @@
 // Launch interface of the paged-cache operators (paged_plan.cu, paged_append.cu, paged_attn.cu).
 #pragma once
 
+#include <utility>
+
 #include "sf_kernels.h"
 
 namespace sf {
@@ -57,6 +59,24 @@ struct EngineAttn {
 cudaError_t launch_engine_paged_attention(const EngineAttn& e, int num_sms, cudaStream_t st);
 // Row masks of a verify pass over candidate guesses of g tokens (see RowSet).
 cudaError_t launch_tree_mask(unsigned long long* mask, int B, int rows, int g, cudaStream_t st, bool pdl);
+
+// Whether two of n1 x n2 vectors of hd elements, s1 and s2 apart, share an
+// element (a call that writes them would leave whichever came last).
+inline bool vectors_overlap(int64_t n1, int64_t s1, int64_t n2, int64_t s2, int64_t hd) {
+  __int128 s = s1 < 0 ? -(__int128)s1 : s1, t = s2 < 0 ? -(__int128)s2 : s2;
+  if ((n1 > 1 && s < hd) || (n2 > 1 && t < hd)) return true;
+  if (n1 <= 1 || n2 <= 1) return false;
+  if (s > t) {
+    std::swap(s, t);
+    std::swap(n1, n2);
+  }
+  if (t >= (n1 - 1) * s + hd) return false;   // one after the other, as nearly always
+  for (int64_t b = 1; b < n2 && b * t < n1 * s; ++b) {
+    const __int128 a = b * t / s, r = b * t - a * s;
+    if (r < hd || (a + 1 < n1 && s - r < hd)) return true;
+  }
+  return false;
+}
 
 // Checks a cache descriptor; on failure records the message and returns the status.
 sf_status check_cache(const sf_paged_cache* c, const char* who);

@@ -209,8 +209,18 @@ extern "C" sf_status sf_kv_append(const sf_paged_cache* cache, int32_t n, const 
     else if (q_out->dtype != q->dtype && q_out->dtype != cache->dtype) why = "q_out must have q's or the cache's type";
     else why = rows_bad(q, q->n_heads, n);
     if (!why) why = rows_bad(q_out, q->n_heads, n);
+    if (!why && vectors_overlap(n, q_out->row, q->n_heads, q_out->head, cache->head_dim)) why = "rows of q_out overlap";
   }
   if (why) return set_error(SF_ERR_ARG, "sf_kv_append: %s", why);
+  // What is written must not lie on itself: pages one after the other, within
+  // them no two slots on one another.
+  const int64_t nkv = cache->n_kv_heads, page = cache->page, hd = cache->head_dim;
+  const int64_t kv[2][3] = {{cache->k_page, cache->k_head, cache->k_slot}, {cache->v_page, cache->v_head, cache->v_slot}};
+  for (const auto& s : kv)
+    if (vectors_overlap(nkv, s[1], page, s[2], hd) ||
+        (cache->n_pages > 1 && s[0] < (nkv > 1 ? (nkv - 1) * s[1] : 0) + (page - 1) * s[2] + hd))
+      return set_error(SF_ERR_ARG, "sf_kv_append: slots of the cache overlap");
+  if (cache->k == cache->v) return set_error(SF_ERR_ARG, "sf_kv_append: k and v of the cache are one");
   AppendArgs a{};
   a.k = k->data, a.k_row = k->row, a.k_head = k->head;
   a.v = v->data, a.v_row = v->row, a.v_head = v->head;

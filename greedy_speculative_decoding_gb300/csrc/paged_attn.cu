@@ -215,6 +215,8 @@ extern "C" sf_status sf_paged_attention(const sf_paged_cache* cache, const sf_ro
     if (!r->data || (reinterpret_cast<uintptr_t>(r->data) & 15) || (n > 1 && r->row % al) ||
         (r->n_heads > 1 && r->head % al))
       return set_error(SF_ERR_ARG, "sf_paged_attention: q and out must be 16-byte aligned with strides of multiples of 16 bytes");
+  if (vectors_overlap(n, out->row, out->n_heads, out->head, cache->head_dim))
+    return set_error(SF_ERR_ARG, "sf_paged_attention: rows of out overlap");
   if (!std::isfinite(scale)) return set_error(SF_ERR_ARG, "sf_paged_attention: scale must be finite");
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);

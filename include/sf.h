@@ -433,7 +433,8 @@ typedef struct {
 } sf_paged_cache;
 
 /* n token rows of n_heads heads each: element (i, h, d) at
- * data[i * row + h * head + d] (row and head strides in elements). */
+ * data[i * row + h * head + d] (row and head strides in elements; rows that a
+ * call writes may not overlap). */
 typedef struct {
   void* data;
   int32_t dtype, n_heads;
@@ -482,7 +483,8 @@ SF_API sf_status sf_rope_table(float* d_table, int32_t n_pos, int32_t head_dim, 
  * q's or the cache's type; it may be q itself when the types are equal). Rows
  * whose slot lies outside the cache, or whose position lies outside the table,
  * are padding: nothing is written for them. The slots of a call are distinct
- * (of two rows with one slot, it is open whose elements stay). positions is
+ * (of two rows with one slot, it is open whose elements stay), and the cache's
+ * own slots may not overlap (refused by their strides). positions is
  * read only with d_rope. k and v have one type, F32, BF16 or F16, and q the
  * same. Data 16-byte aligned, strides multiples of 8 (of 4 for F32).
  */

@@ -152,3 +152,38 @@ def test_oracle_plan_keeps_every_page_in_one_place(seed):
         assert len(used) == len(set(used))
         for b in range(B_):
             assert res["status"][b] == 1 or held[b] == -(-lens[b] // page)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(row=0), dict(head=0), dict(row=32, head=512), dict(row=256, head=256), dict(row=64), dict(row=192, head=128),
+    dict(row=-64)])
+def test_rows_written_on_one_another(lib, kw):
+    """Broadcast and overlapping outputs (three rows of four heads of 64)."""
+    assert append(lib, q=rows(4), q_out=rows(4, **kw)) == L.SF_ERR_ARG
+    assert attend(lib, out=rows(4, **kw)) == L.SF_ERR_ARG
+
+
+@pytest.mark.parametrize("kw", [
+    dict(k_slot=8, k_head=512), dict(k_head=64), dict(v_head=2048), dict(k_page=4096), dict(v_page=8184), dict(v=PTR)])
+def test_cache_slots_written_on_one_another(lib, kw):
+    """Two heads of 64 slots of 64 in a page; keys and values in one place."""
+    c = cache(**{"v": 2 * PTR, **kw})
+    assert append(lib, c=c) == L.SF_ERR_ARG
+    assert b"overlap" in lib.sf_last_error() or b"are one" in lib.sf_last_error()
+
+
+def test_overlap_is_told_exactly(lib):
+    """Row layouts of every kind: refused exactly where two rows share an
+    element (an allowed layout goes on to be refused for its scale)."""
+    r = random.Random(3)
+    seen = set()
+    for _ in range(400):
+        n, heads = r.randint(1, 5), r.choice([2, 4, 6])
+        row, head = 8 * r.randint(0, 60), 8 * r.randint(0, 60)
+        at = sorted(i * row + h * head for i in range(n) for h in range(heads))
+        want = any(b - a < 64 for a, b in zip(at, at[1:]))
+        seen.add(want)
+        assert attend(lib, q=rows(heads), out=rows(heads, row=row, head=head), n=n, starts=PTR, batch=1,
+                      scale=float("inf")) == L.SF_ERR_ARG
+        assert (b"overlap" in lib.sf_last_error()) == want, (n, heads, row, head)
+    assert seen == {False, True}
