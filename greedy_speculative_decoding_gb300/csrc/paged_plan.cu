@@ -233,13 +233,13 @@ __global__ void __launch_bounds__(kRowThreads) k_plan_rows(const PlanArgs a) {
       slot[e] = (page << a.shift) + (x & ((1 << a.shift) - 1));
       pos[e] = slot[e] < 0 ? 0 : x;
     }
-    if (vec && i0 + 4 <= a.N) {
+    if (vec && a.N - i0 >= 4) {   // (i0 + 4 may be 2^31)
       *reinterpret_cast<int4*>(a.slots + i0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
       *reinterpret_cast<int4*>(a.positions + i0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
     } else {
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        if (i0 + e < a.N) {
+        if (e < a.N - i0) {
           a.slots[i0 + e] = slot[e];
           a.positions[i0 + e] = pos[e];
         }

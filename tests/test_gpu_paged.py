@@ -837,3 +837,19 @@ def test_sums_of_like_probabilities(pkg, dq, dc, hd, rows, group):
     want = torch.tensor([math.log(W + (W * 255 - (rows - 1 - j)) * p) for j in range(rows)], dtype=torch.float64)
     bound = 1072 * 2.0 ** -24 + 2.0 ** -22 + 4 * 2.0 ** -24 + 32 * 2.0 ** -24
     assert float((lse.double().cpu() - want.repeat(B)[:, None]).abs().max()) <= bound
+
+
+def test_plan_of_the_most_rows(pkg):
+    """2^31 - 1 rows, the last 300 those of one request: nothing is written
+    behind them, where the last four indexes end at 2^31."""
+    n = 2 ** 31 - 1
+    slots, pos = (torch.full((n + 5,), 77, dtype=torch.int32, device="cuda") for _ in range(2))
+    tables, held = torch.zeros((1, 8), dtype=torch.int32, device="cuda"), i32([0])
+    res = pkg.page_plan(i32([500]), i32([n - 300, n]), tables, held, torch.arange(40, dtype=torch.int32, device="cuda"),
+                        i32([40]), 64, slots=slots[:n], positions=pos[:n])
+    assert res.status.tolist() == [0] and tables.tolist() == [list(range(39, 31, -1))]
+    p = torch.arange(200, 500)
+    assert pos[n - 300:].tolist() == p.tolist() + [77] * 5
+    assert slots[n - 300:].tolist() == ((39 - p // 64) * 64 + p % 64).tolist() + [77] * 5
+    assert int(slots[:n - 300].max()) == -1 and int(slots[:n - 300].min()) == -1
+    assert int(pos[:n - 300].max()) == 0 and int(pos[:n - 300].min()) == 0
