@@ -6,6 +6,7 @@
  * 5, launches included.
  */
 #define PY_SSIZE_T_CLEAN
+#include <ATen/core/grad_mode.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <algorithm>
@@ -47,9 +48,13 @@ const char* type_name(at::ScalarType t) {
          t.is_cuda() ? ("cuda:" + std::to_string(t.get_device())).c_str() : "another device");
 }
 
+/* The calls have no gradients: a tensor that wants one is refused while gradients are on. */
 const at::Tensor& tensor(PyObject* o, const char* name) {
   if (!THPVariable_Check(o)) refuse("%s: expected a tensor, got %.60s", name, Py_TYPE(o)->tp_name);
-  return THPVariable_Unpack(o);
+  const at::Tensor& t = THPVariable_Unpack(o);
+  if (t.requires_grad() && at::GradMode::is_enabled())
+    refuse("%s requires grad, and this call has no gradient (detach it, or call under torch.no_grad())", name);
+  return t;
 }
 
 bool on_device(const at::Tensor& t, int dev) { return t.layout() == at::kStrided && t.is_cuda() && t.get_device() == dev; }

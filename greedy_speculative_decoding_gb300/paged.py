@@ -10,7 +10,8 @@ its tokens including them.
 
 Every call takes tensors of the current CUDA device and enqueues its work on
 ``stream`` (default: the current stream). Tensors that a call allocates itself
-belong to that stream.
+belong to that stream. The calls have no gradients: tensors that require grad
+are refused unless gradients are off.
 """
 
 import importlib

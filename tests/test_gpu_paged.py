@@ -853,3 +853,24 @@ def test_plan_of_the_most_rows(pkg):
     assert slots[n - 300:].tolist() == ((39 - p // 64) * 64 + p % 64).tolist() + [77] * 5
     assert int(slots[:n - 300].max()) == -1 and int(slots[:n - 300].min()) == -1
     assert int(pos[:n - 300].max()) == 0 and int(pos[:n - 300].min()) == 0
+
+
+def test_inputs_that_require_grad(pkg):
+    """No gradient would come back: refused, unless gradients are off."""
+    c = attn_case(51, [30, 9], [2, 1], 4, 2, 64, 16)
+    ref, _ = call(pkg, c)
+    for name in ("q", "k", "v"):
+        d = dict(c)
+        d[name] = c[name].clone().requires_grad_()
+        with pytest.raises(ValueError, match="requires grad"):
+            call(pkg, d)
+        with torch.no_grad():
+            assert torch.equal(call(pkg, d)[0], ref)
+    k, v, q = (torch.zeros((3, h, 64), dtype=BF, device="cuda") for h in (2, 2, 4))
+    rope, pos = pkg.rope_table(9, 64, 1e4), i32([0, 1, 2])
+    for name in ("k", "v", "q", "rope", "q_out"):
+        a = dict(k=k, v=v, q=q, rope=rope, q_out=torch.zeros_like(q))
+        a[name] = a[name].clone().requires_grad_()
+        with pytest.raises(ValueError, match="requires grad"):
+            pkg.kv_append(a["k"], a["v"], i32([1, 2, -1]), c["k"], c["v"], q=a["q"], q_out=a["q_out"], positions=pos,
+                          rope=a["rope"])

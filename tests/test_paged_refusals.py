@@ -187,3 +187,42 @@ def test_overlap_is_told_exactly(lib):
                       scale=float("inf")) == L.SF_ERR_ARG
         assert (b"overlap" in lib.sf_last_error()) == want, (n, heads, row, head)
     assert seen == {False, True}
+
+
+@pytest.fixture(scope="module")
+def native():
+    B.build()
+    from greedy_speculative_decoding_gb300 import paged
+    return paged._binding()
+
+
+def plain_calls(native):
+    """One call of each operator on CPU tensors: refused for that, if for nothing else (caches are looked at first)."""
+    z = lambda *s, **kw: torch.zeros(s, **kw)
+    i = lambda *s: torch.zeros(s, dtype=torch.int32)
+    return {
+        "page_plan": (native.page_plan, [0, 0, 16, 3, i(2), i(3), i(2, 4), i(2), i(9), i(1), i(3), i(3), i(2), i(1), i(2)],
+                      []),
+        "kv_append": (native.kv_append, [0, 0, z(3, 2, 64), z(3, 2, 64), i(3), z(4, 2, 16, 64), z(4, 2, 16, 64),
+                                         z(3, 4, 64), z(3, 4, 64), i(3), z(9, 32, 2)], [5, 6]),
+        "paged_attention": (native.paged_attention, [0, 0, 1, None, z(3, 4, 64), z(4, 2, 16, 64), z(4, 2, 16, 64), i(2, 2),
+                                                     i(2), i(3), None, z(3, 4, 64), None, i(9)], [5, 6]),
+    }
+
+
+@pytest.mark.parametrize("op", ["kv_append", "paged_attention"])
+def test_tensors_that_require_grad(native, op):
+    f, args, floats = plain_calls(native)[op]
+    for k in floats:
+        a = list(args)
+        a[k] = a[k].clone().requires_grad_()
+        with pytest.raises(ValueError, match="requires grad"):
+            f(*a)
+        with torch.no_grad(), pytest.raises(ValueError, match="on another device"):
+            f(*a)
+
+
+def test_binding_refuses_tensors_of_another_device(native):
+    for f, args, _ in plain_calls(native).values():
+        with pytest.raises(ValueError, match="on another device"):
+            f(*args)
