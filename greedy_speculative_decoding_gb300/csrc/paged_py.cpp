@@ -139,6 +139,18 @@ int64_t integer(PyObject* o, const char* name, int64_t lo, int64_t hi) {
 }
 void* stream_of(PyObject* o) { return reinterpret_cast<void*>(integer(o, "stream", INT64_MIN, INT64_MAX)); }
 
+/* Tells autograd that tensors (or None) have been written in place: one that a
+ * graph has saved is then noticed. */
+sf_status written(sf_status s, PyObject* const* a, std::initializer_list<int> which) {
+  if (s != SF_OK) return s;
+  for (const int i : which) {
+    if (a[i] == Py_None) continue;
+    const at::Tensor& t = THPVariable_Unpack(a[i]);
+    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+  }
+  return s;
+}
+
 /* A call: C++ exceptions become Python's. */
 template <int N, sf_status (*F)(PyObject* const*)>
 PyObject* method(PyObject*, PyObject* const* a, Py_ssize_t n) {
@@ -163,11 +175,12 @@ sf_status page_plan(PyObject* const* a) {
   auto i32 = [&](int i, const char* name, int64_t size) {
     return static_cast<int32_t*>(flat(a[i], name, at::kInt, dev, {size}));
   };
-  return sf_page_plan(i32(4, "lens", B), i32(5, "starts", B + 1), (int32_t)B, page,
-                      static_cast<int32_t*>(flat(a[6], "tables", at::kInt, dev, {B, W})), (int32_t)W,
-                      i32(7, "held", B), i32(8, "free", cap), (int32_t)cap, i32(9, "n_free", 1), n, i32(10, "slots", n),
-                      i32(11, "positions", n), i32(12, "held_out", B), i32(13, "n_free_out", 1), i32(14, "status", B),
-                      stream_of(a[1]));
+  const sf_status s = sf_page_plan(
+      i32(4, "lens", B), i32(5, "starts", B + 1), (int32_t)B, page,
+      static_cast<int32_t*>(flat(a[6], "tables", at::kInt, dev, {B, W})), (int32_t)W, i32(7, "held", B),
+      i32(8, "free", cap), (int32_t)cap, i32(9, "n_free", 1), n, i32(10, "slots", n), i32(11, "positions", n),
+      i32(12, "held_out", B), i32(13, "n_free_out", 1), i32(14, "status", B), stream_of(a[1]));
+  return written(s, a, {6, 8, 10, 11, 12, 13, 14});
 }
 
 /* dev, stream, k, v, slots, k_cache, v_cache, q, q_out, positions, rope */
@@ -189,9 +202,11 @@ sf_status kv_append(PyObject* const* a) {
     positions = flat(a[9], "positions", at::kInt, dev, {n});
     rope = flat(a[10], "rope", at::kFloat, dev, {n_pos, cache.head_dim / 2, 2});
   }
-  return sf_kv_append(&cache, (int32_t)n, &k, &v, static_cast<int32_t*>(flat(a[4], "slots", at::kInt, dev, {n})),
-                      has_q ? &q : nullptr, has_q ? &q_out : nullptr, static_cast<int32_t*>(positions),
-                      static_cast<float*>(rope), (int32_t)n_pos, stream_of(a[1]));
+  auto* slots = static_cast<int32_t*>(flat(a[4], "slots", at::kInt, dev, {n}));
+  const sf_status s =
+      sf_kv_append(&cache, (int32_t)n, &k, &v, slots, has_q ? &q : nullptr, has_q ? &q_out : nullptr,
+                   static_cast<int32_t*>(positions), static_cast<float*>(rope), (int32_t)n_pos, stream_of(a[1]));
+  return written(s, a, {5, 6, 8});
 }
 
 /* dev, stream, max_rows, scale or None, q, k_cache, v_cache, tables, lens, starts, mask, out, lse, workspace */
@@ -220,9 +235,10 @@ sf_status paged_attention(PyObject* const* a) {
     snprintf(text, sizeof(text), "at least %zu contiguous bytes on cuda:%d", need, dev);
     wrong("workspace", text, ws);
   }
-  return sf_paged_attention(&cache, &q, &out, (int32_t)n, tables, (int32_t)W, lens, starts, (int32_t)B, max_rows,
-                            static_cast<uint64_t*>(mask), scale, static_cast<float*>(lse),
-                            flat(a[13], "workspace", at::kByte, dev, {ws.size(0)}), stream_of(a[1]));
+  const sf_status s = sf_paged_attention(
+      &cache, &q, &out, (int32_t)n, tables, (int32_t)W, lens, starts, (int32_t)B, max_rows, static_cast<uint64_t*>(mask),
+      scale, static_cast<float*>(lse), flat(a[13], "workspace", at::kByte, dev, {ws.size(0)}), stream_of(a[1]));
+  return written(s, a, {11, 12, 13});
 }
 
 template <int N, sf_status (*F)(PyObject* const*)>

@@ -874,3 +874,26 @@ def test_inputs_that_require_grad(pkg):
         with pytest.raises(ValueError, match="requires grad"):
             pkg.kv_append(a["k"], a["v"], i32([1, 2, -1]), c["k"], c["v"], q=a["q"], q_out=a["q_out"], positions=pos,
                           rope=a["rope"])
+
+
+def test_tensors_written_in_place_are_marked_so(pkg):
+    """What a call writes counts as changed in place, so that a graph which has
+    saved it notices; with tensors of inference mode nothing is counted."""
+    c = attn_case(52, [30, 9], [2, 1], 4, 2, 64, 16)
+    tables, held, free, n_free = i32([[0] * 4] * 2), i32([0, 0]), i32(list(range(9))), i32([9])
+    q, out, lse = c["q"], torch.zeros_like(c["q"]), torch.zeros(c["q"].shape[:2], device="cuda")
+    x = torch.ones_like(c["k"], requires_grad=True)
+    y = (x * c["k"]).sum()
+    new = [tables, held, free, n_free, c["k"], c["v"], out, lse]
+    before, kept = [t._version for t in new], q._version
+    plan = pkg.page_plan(i32([30, 9]), i32(c["starts"]), tables, held, free, n_free, 16, n_rows=3)
+    rows = torch.randn((3, 2, 64), device="cuda").to(BF)
+    pkg.kv_append(rows, rows, i32([1, 2, 3]), c["k"], c["v"])
+    call(pkg, c, out=out, lse=lse)
+    assert all(t._version > b for t, b in zip(new, before)) and q._version == kept and plan.slots._version > 0
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.backward()
+    with torch.inference_mode():
+        k, v = torch.zeros_like(c["k"]), torch.zeros_like(c["v"])
+    pkg.kv_append(rows, rows, i32([1, 2, 3]), k, v)
+    assert torch.equal(k[0, :, 1:4], rows.transpose(0, 1))
