@@ -897,3 +897,81 @@ def test_tensors_written_in_place_are_marked_so(pkg):
         k, v = torch.zeros_like(c["k"]), torch.zeros_like(c["v"])
     pkg.kv_append(rows, rows, i32([1, 2, 3]), k, v)
     assert torch.equal(k[0, :, 1:4], rows.transpose(0, 1))
+
+
+def terms(x, n):
+    """x rounded to n bf16 terms (as fp32 queries and probabilities are held: n = 3)."""
+    x, out = x.float(), torch.zeros_like(x.float())
+    for _ in range(n):
+        t = (x - out).bfloat16().float()
+        out = out + t
+    return out.double()
+
+
+def third_term_case(hd, rows, prior):
+    """fp32 queries over `prior` slots that all rows see (keys 0 but for slot 1),
+    and nothing of the pass's own; tiles of 16, 32 (hd 64) or 128 queries."""
+    nkv, group, page = 2, 7, 64
+    pages = -(-(prior + rows) // page)
+    k = torch.zeros((pages, nkv, page, hd), dtype=BF, device="cuda")
+    v = torch.zeros_like(k)
+    tables = torch.zeros((1, 140000 // page), dtype=torch.int32, device="cuda")
+    tables[0, :pages] = torch.arange(pages, dtype=torch.int32, device="cuda")
+    mask = torch.zeros(rows, dtype=torch.int64, device="cuda")
+    return k, v, tables, mask, nkv * group
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("rows", [1, 3, 9])
+@pytest.mark.parametrize("prior", [2, 128])
+def test_third_term_of_fp32_queries(pkg, hd, rows, prior):
+    """Scores that are the third term alone: a query of 1 + 2^-9 + d and 1 +
+    2^-9 (d below 2^-17) against a key of 1 and -1. The other two terms cancel,
+    and the products of each term are one step of the tensor cores, which cut
+    off at most 2^-23 of the magnitudes: 2 in the last step, 2^-8 before. The
+    scale 2^17 makes that 2^-5 and the score d * 2^17 = 0.5 to 1."""
+    k, v, tables, mask, nq = third_term_case(hd, rows, prior)
+    k[0, :, 1, 0::2], k[0, :, 1, 1::2] = 1.0, -1.0
+    q = torch.zeros((rows, nq, hd), device="cuda")
+    d = torch.zeros((rows, nq), dtype=torch.float64)
+    for j in range(rows):
+        for h in range(nq):
+            i = (j * nq + h) * 5 % (hd // 2) * 2          # a pair of dimensions
+            big = 2.0 ** -18 + (1 + (j + 3 * h) % 15) * 2.0 ** -22
+            d[j, h] = big
+            a, b = (1 + 2.0 ** -9 + big, 1 + 2.0 ** -9) if h % 2 else (-(1 + 2.0 ** -9), -(1 + 2.0 ** -9 + big))
+            q[j, h, i], q[j, h, i + 1] = a, b
+    assert torch.equal(terms(q, 3), q.double()) and torch.equal(q[:, :, 0::2].sum(2) - q[:, :, 1::2].sum(2), d.float().cuda())
+    lse = torch.zeros((rows, nq), device="cuda")
+    pkg.paged_attention(q, k, v, tables, i32([prior + rows]), starts=i32([0, rows]), max_rows=rows, mask=mask,
+                        scale=2.0 ** 17, lse=lse)
+    s = d * 2.0 ** 17
+    want = torch.log(torch.exp(s) + (prior - 1))
+    bound = 1.01 * 2.0 ** -5 * torch.exp(s - want) * math.exp(2.0 ** -5) + 2.0 ** -20
+    gone = (want - math.log(prior)).abs()                  # what the score is without the third term: 0
+    assert bool((gone > 4 * bound).all())
+    assert bool(((lse.double().cpu() - want).abs() <= bound).all())
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("rows", [1, 3, 9])
+@pytest.mark.parametrize("prior", [2, 128])
+def test_third_term_of_fp32_probabilities(pkg, hd, rows, prior):
+    """Outputs 1 - p, with p from 1/2 to 1 next to a slot of probability 1: p is
+    off by 2^-22 of it from the exponential and 2^-23 from the scaled score (two
+    roundings of 2^-24, times ln 2), the last step of the tensor cores by 2^-23 of
+    a magnitude of 2, fp32 sums, the division and the output by 2^-23 together,
+    relative to 1 and not to the difference: 2^-20 in all. The third term is up
+    to 2^-18."""
+    k, v, tables, mask, nq = third_term_case(hd, rows, prior)
+    k[0, :, 1, 0] = -1.0
+    v[0, :, 0], v[0, :, 1] = 1.0, -1.0
+    q = torch.zeros((rows, nq, hd), device="cuda")
+    q[:, :, 0] = 0.03 + 0.65 * torch.linspace(0, 1, rows * nq, dtype=torch.float64).view(rows, nq).float()
+    out = torch.zeros_like(q)
+    pkg.paged_attention(q, k, v, tables, i32([prior + rows]), starts=i32([0, rows]), max_rows=rows, mask=mask, scale=1.0,
+                        out=out)
+    p = torch.exp(-q[:, :, 0].double().cpu())
+    total = prior - 1 + p
+    assert float((terms(p, 2) - p).abs().max()) > 3 * 2.0 ** -20
+    assert float((out.double().cpu() * total[..., None] - (1 - p)[..., None]).abs().max()) <= 2.0 ** -20
