@@ -975,3 +975,90 @@ def test_third_term_of_fp32_probabilities(pkg, hd, rows, prior):
     total = prior - 1 + p
     assert float((terms(p, 2) - p).abs().max()) > 3 * 2.0 ** -20
     assert float((out.double().cpu() * total[..., None] - (1 - p)[..., None]).abs().max()) <= 2.0 ** -20
+
+
+@pytest.mark.parametrize("dt", [BF, FH])
+@pytest.mark.parametrize("R,group,cap", [(2, 2, 20), (9, 5, 20), (9, 5, 6)])
+def test_captured_pass_step_by_step(pkg, dt, R, group, cap):
+    """A captured plan, append and attention, replayed over requests that grow,
+    give guesses back, finish and begin anew: after every replay the plan's
+    numbers are the oracle's, every slot of the cache holds what was put there
+    last to one rounding, and the attention is the oracle's over the cache and
+    the rotated queries that are there."""
+    nkv, hd, page, B, W = 2, 64, 16, 3, 8
+    nq, n = nkv * group, 3 * R
+    g = torch.Generator(device="cuda").manual_seed(8)
+    r = random.Random(6)
+    kc, vc = make_cache(cap, nkv, page, hd, dt, fill=0.0)
+    lens, starts = i32([0] * B), i32([0, R, 2 * R, 3 * R])
+    tables, held, free, n_free = i32([[0] * W] * B), i32([0] * B), i32(list(range(cap))), i32([cap])
+    q, k, v = (torch.zeros((n, h, hd), dtype=dt, device="cuda") for h in (nq, nkv, nkv))
+    cs = pkg.rope_table(W * page, hd, 1e4)
+    qr, out, lse = torch.zeros_like(q), torch.zeros_like(q), torch.zeros((n, nq), device="cuda")
+    ws = pkg.paged_attention_workspace(q, kc, tables, R)
+    slots, pos, status = i32([0] * n), i32([0] * n), i32([0] * B)
+
+    def one_pass():
+        pkg.page_plan(lens, starts, tables, held, free, n_free, page, slots=slots, positions=pos, status=status)
+        pkg.kv_append(k, v, slots, kc, vc, q=q, q_out=qr, positions=pos, rope=cs)
+        pkg.paged_attention(qr, kc, vc, tables, lens, starts=starts, max_rows=R, out=out, lse=lse, workspace=ws)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        one_pass()                     # (more rows than tokens: every request is refused)
+    torch.cuda.current_stream().wait_stream(side)
+    assert status.tolist() == [2] * B
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        one_pass()
+    book = dict(tables=tables.tolist(), held=held.tolist(), free=free.tolist(), n_free=cap)
+    want_k, want_v = (torch.zeros((cap * page, nkv, hd), dtype=torch.float64) for _ in range(2))
+    mag = torch.zeros_like(want_k)
+    now, short = [0] * B, 0
+    t = cs.cpu()
+    for step in range(25):
+        for x, h in ((q, nq), (k, nkv), (v, nkv)):
+            x.copy_(torch.randn((n, h, hd), device="cuda", generator=g))
+        out.fill_(7.0)
+        lse.fill_(7.0)
+        now = [x + R if x + R <= W * page else R for x in now]
+        lens.copy_(i32(now))
+        graph.replay()
+        torch.cuda.synchronize()
+        ref = op.page_plan(now, starts.tolist(), book["tables"], book["held"], book["free"], book["n_free"], page, n)
+        got = dict(tables=tables, held=held, free=free, status=status, slots=slots, positions=pos)
+        for name, x in got.items():
+            assert x.tolist() == ref[name], (step, name)
+        assert n_free.tolist() == [ref["n_free"]]
+        book = {x: ref[x] for x in ("tables", "held", "free", "n_free")}
+        hk, hv, hq, hr = k.cpu(), v.cpu(), q.cpu(), qr.cpu().double()
+        for i in range(n):
+            s, p = ref["slots"][i], ref["positions"][i]
+            if s < 0:
+                continue
+            for h in range(nkv):
+                want_k[s, h], mag[s, h] = op.rotate(hk[i, h], t[p]), hk[i, h].abs() + hk[i, h].roll(hd // 2).abs()
+                want_v[s, h] = hv[i, h].double()
+            for h in range(nq):
+                y = op.rotate(hq[i, h], t[p])
+                m = (hq[i, h].abs() + hq[i, h].roll(hd // 2).abs()).double()
+                assert bool(((hr[i, h] - y).abs() <= U[dt] * y.abs() + 4 * 2.0 ** -24 * m + TINY[dt]).all())
+        flat_k, flat_v = (c.transpose(1, 2).reshape(-1, nkv, hd).cpu().double() for c in (kc, vc))
+        assert bool(((flat_k - want_k).abs() <= U[dt] * want_k.abs() + 4 * 2.0 ** -24 * mag + TINY[dt]).all())
+        assert torch.equal(flat_v, want_v)
+        # (a request that got no pages keeps its table: its rows are not looked at)
+        served = [x == 0 for x in ref["status"]]
+        short += served.count(False)
+        rows = torch.tensor([b * R + j for b in range(B) if served[b] for j in range(R)], dtype=torch.long)
+        at, some = [b for b in range(B) if served[b]], [0]
+        for _ in at:
+            some.append(some[-1] + R)
+        o, l = torch.full_like(out, 7.0), torch.full_like(lse, 7.0)
+        o[:len(rows)], l[:len(rows)] = out[rows.cuda()], lse[rows.cuda()]
+        if at:
+            check_attn(dict(q=torch.cat([qr[rows.cuda()], qr[:n - len(rows)]]), k=kc, v=vc, starts=some, mask=None,
+                            max_rows=R, tables=[book["tables"][b] for b in at], lens=[now[b] for b in at]), o, l)
+        # Some guesses are rejected, some requests finish: the next pass starts from fewer tokens.
+        now = [max(0, (x if s else x - R) - r.randint(0, R)) if r.random() < 0.9 else 0 for x, s in zip(now, served)]
+    assert cap > 6 or short > 0
