@@ -192,3 +192,46 @@ def test_page_calls_of_an_engine_without_pages(pkg, tiny):
     eng.close()
     with pytest.raises(pkg.SFError):
         engine(pkg, tiny, 0)
+
+
+@pytest.mark.parametrize("drafter", ["NGRAM", "TREE", "NONE"])
+def test_nf4_target_over_many_rounds(pkg, drafter):
+    """NF4 weights: after every rewind the verify logits are the dense engine's
+    (within the engine tests' tolerance), and what both then generate is the
+    oracle's stream on the dequantised weights, up to the NF4 tolerance."""
+    from test_gpu_nf4 import NF4_TOL, _oracle_nf4
+    shape, K = TINY_TARGET.with_(ffn=768), 4
+    gw, rw = _oracle_nf4(shape, make_weights(shape, seed=4))
+    prompts = [ngram_prompt(90, 0.8, V, seed=2, base_len=40)[0].tolist(), [7, 9, 11] * 11]
+    engines = [pkg.SpecEngine(shape, gw, batch=2, K=K, s_max=256, pages=p) for p in (None, 7)]
+    for e in engines:
+        e.prefill(prompts)
+    rounds = 0
+    for _ in range(12):
+        res = []
+        for e in engines:
+            if drafter == "TREE":
+                e.tree_draft(2, 1, 3)
+            else:
+                e.ngram_draft(4 if drafter == "NGRAM" else 1, 1, 3)
+            logits, arg = torch.zeros(2, K + 1, V, device="cuda"), torch.zeros(2, K + 1, dtype=torch.int32, device="cuda")
+            e.verify(arg, logits)
+            res.append((logits, arg, e.accept_rollback()[0].tolist(), e.lengths()[0].tolist()))
+        for b in range(2):
+            for j in range(K + 1):
+                assert logit_err(res[1][0][b, j], res[0][0][b, j]) < LOGIT_TOL_BF16
+        rounds += 1
+        if not torch.equal(res[0][1], res[1][1]):
+            break   # a near tie: from here the two commit different tokens
+        assert res[0][2:] == res[1][2:]
+    assert rounds >= 3
+    for e in engines:
+        e.reset()
+        e.set_drafter(getattr(pkg, "SF_DRAFT_" + drafter), 1, 3)
+    outs = [e.generate(40)[0] for e in engines]
+    m = om.Model(shape, rw)
+    for out in outs:
+        for b in range(2):
+            stream_report(m, prompts[b], out[b].tolist(), NF4_TOL)
+    for e in engines:
+        e.close()
