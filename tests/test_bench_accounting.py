@@ -89,3 +89,13 @@ def test_launch_bound_per_round():
     # K draft forwards and one verify forward (embed + 6 per layer + LM
     # head each) and the acceptance kernel.
     assert bench.launches_per_round(QWEN7B, QWEN05B_SHARED, 8) == 8 * (2 + 6 * 24) + (2 + 6 * 28) + 1
+
+
+def test_stored_traffic_is_of_these_sources():
+    """The roofline kernel's measured traffic goes with the sources it was
+    measured on: a change to them asks for a new capture (the bench prints null
+    until then). At least the bytes that the kernel cannot do without, and less
+    than 2% above them."""
+    need = 37888 * 3584 * 2 + 9 * (3584 * 4 + 37888 * 4)
+    assert bench._gemm_traffic() is not None
+    assert need <= bench._gemm_traffic() <= 1.02 * need
