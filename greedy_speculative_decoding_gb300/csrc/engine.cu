@@ -1078,6 +1078,10 @@ sf_status sync_report(sf_engine* e) {
   CK(cudaMemcpyAsync(e->pin, e->st.ncommit, e->so.report_ints * sizeof(int), cudaMemcpyDeviceToHost, e->user));
   CK(cudaStreamSynchronize(e->user));
   const int err = e->pin[e->so.err - e->so.report];
+  // The lengths the next call's capacity checks go by: the device's, whatever
+  // the round came to.
+  const int* tot = e->pin + (e->so.total - e->so.report);
+  for (int b = 0; b < e->B; ++b) e->C[b] = e->P[b] + tot[b];
   if (err) {
     CK(cudaMemsetAsync(e->st.err, 0, sizeof(int), e->user));
     // A barrier wait that gave up leaves the persistent kernel's barrier
@@ -1088,8 +1092,6 @@ sf_status sync_report(sf_engine* e) {
     if (err & kErrNonfinite) return fail(SF_ERR_NONFINITE, "non-finite logits (device flag %d)", err);
     return fail(SF_ERR_CAPACITY, "cache capacity or token range exceeded on the device (flag %d)", err);
   }
-  const int* tot = e->pin + (e->so.total - e->so.report);
-  for (int b = 0; b < e->B; ++b) e->C[b] = e->P[b] + tot[b];
   return SF_OK;
 }
 

@@ -54,7 +54,7 @@ __global__ void k_accept(const __grid_constant__ SpecState s, int ngram) {
     s.dtok0[2 * b] = before_last;
     s.dtok0[2 * b + 1] = tt[n];
     s.vtok[b * K1] = tt[n];
-    if (Cn + s.K + 1 > s.s_max) atomicOr(s.err, kErrCapacity);
+    if (C + s.K + 1 > s.s_max) atomicOr(s.err, kErrCapacity);   // this round has run past the cache's end
   }
 }
 
@@ -267,7 +267,7 @@ __global__ void k_accept_tree(const __grid_constant__ SpecState s, int n_cand, i
     s.dtok0[2 * b] = before_last;
     s.dtok0[2 * b + 1] = last;
     s.vtok[b * K1] = last;
-    if (Cn + s.K + 1 > s.s_max) atomicOr(s.err, kErrCapacity);
+    if (C + s.K + 1 > s.s_max) atomicOr(s.err, kErrCapacity);   // this round has run past the cache's end
   }
 }
 
@@ -332,9 +332,8 @@ cudaError_t launch_tree_compact(const SpecState& s, bf16* kv, int layers, int nk
 // sf_generate as one graph launch: a WHILE conditional node whose body is one
 // round followed by k_loop_ctl. The control kernel counts the round and lets
 // the loop run again while some sequence has fewer than the target number of
-// new tokens, every sequence has room for two more rounds (so acceptance
-// never raises the capacity flag) and the target's pool, when its cache lies
-// in pages, has the pages for them, no error bit is set, and fewer rounds than
+// new tokens, every sequence has room for two more rounds and the target's
+// pool, when its cache lies in pages, has the pages for them, no error bit is set, and fewer rounds than
 // the target have run (each round commits at least one token per sequence,
 // so that bound never stops a loop that still has work).
 __global__ void k_loop_init(const __grid_constant__ SpecState s, int n_new) {

@@ -235,3 +235,46 @@ def test_nf4_target_over_many_rounds(pkg, drafter):
             stream_report(m, prompts[b], out[b].tolist(), NF4_TOL)
     for e in engines:
         e.close()
+
+
+@pytest.mark.parametrize("pages", [None, 6])
+@pytest.mark.parametrize("drafter", ["NEURAL", "NGRAM", "NONE", "TREE"])
+@pytest.mark.parametrize("whole", [True, False])
+def test_rounds_up_to_the_end_of_the_cache(pkg, tiny, pages, drafter, whole):
+    """Every round that fits gives its tokens; the first that does not is
+    refused, with everything as it was, and so is the one after it (with a
+    cache per sequence, and in pages)."""
+    m, _, _ = tiny
+    K, s_max, prompts = 4, 128, [[5, 6, 7] * 20, ngram_prompt(90, 0.8, V, seed=3, base_len=64)[0].tolist()]
+    eng = engine(pkg, tiny, pages, batch=2, K=K, s_max=s_max, draft=drafter == "NEURAL")
+    eng.prefill(prompts)
+    eng.set_drafter(getattr(pkg, "SF_DRAFT_" + drafter), 2, 4)
+
+    def one_round():
+        if whole:
+            return eng.step()
+        {"NEURAL": eng.draft, "TREE": lambda: eng.tree_draft(2, 2, 4)}.get(drafter, lambda: eng.ngram_draft(K, 2, 4))()
+        eng.verify()
+        return eng.accept_rollback()[1]
+
+    got, committed = [[], []], [60, 90]
+    for _ in range(s_max):
+        fits = max(committed) + K + 1 <= s_max
+        if not fits:
+            break
+        for b, t in enumerate(one_round()):
+            got[b] += t
+            committed[b] += len(t)
+        assert [n + 1 for n in eng.lengths()[0].tolist()] == committed
+    assert not fits
+    for _ in range(2):
+        with pytest.raises(pkg.SFError) as e:
+            one_round()
+        assert e.value.status == 2
+        assert [n + 1 for n in eng.lengths()[0].tolist()] == committed
+    for b in range(2):
+        stream_report(m, prompts[b], got[b], LOGIT_TOL_BF16)
+    eng.reset()
+    first = one_round()
+    assert all(t == g[:len(t)] for t, g in zip(first, got))
+    eng.close()
