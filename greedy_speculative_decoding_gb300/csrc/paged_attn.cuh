@@ -36,7 +36,7 @@ namespace pa {
 
 constexpr int kTile = 64;                 // slots of a unit
 constexpr int kMaxPiece = 8;              // units that an item's beginning counts for, at most
-constexpr uint64_t kWaitNs = 1000000000;  // bound of every wait
+constexpr uint32_t kWaitPolls = 750000;   // bound of every wait: one second at 1.33 us a poll (measured)
 
 struct Args {
   CUtensorMap km, vm;      // cache as {head_dim, slot or head, head or slot, page}
@@ -105,15 +105,10 @@ struct Deal {
 };
 
 // Wait on an mbarrier phase; false after a second without it (the copies and
-// products waited for take microseconds).
+// products waited for take microseconds). Counted in polls: a kernel that is
+// switched out while it waits, whatever the clock says, has not waited.
 static __device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity) {
-  uint64_t t0, t;
-  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
-  do {
-    if (mbar_wait(bar, parity, 32)) return true;
-    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-  } while (t - t0 < kWaitNs);
-  return false;
+  return mbar_wait(bar, parity, kWaitPolls);
 }
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
 #pragma unroll 1

@@ -512,7 +512,9 @@ SF_API sf_status sf_kv_append(const sf_paged_cache* cache, int32_t n, const sf_r
  * queries are rounded to that type, by half a step of each, or in fp16 by 2^-37
  * of the row's largest if that is more. n_heads a multiple of n_kv_heads. workspace: sf_paged_attention_workspace_bytes(...) bytes of
  * device scratch, 256-byte aligned, any contents; calls that may overlap on
- * the GPU need one each. A result depends on the whole batch's lengths in its
+ * the GPU need one each. Waits inside the kernels are bounded (a second; what
+ * they wait for takes microseconds): one that runs out leaves NaN in the rows
+ * concerned. A result depends on the whole batch's lengths in its
  * last bits (the split over the cache's length follows them) and is the same
  * in every run.
  */
