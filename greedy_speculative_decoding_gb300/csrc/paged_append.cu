@@ -5,9 +5,10 @@
 // they are paired with (16-byte accesses): few registers, so that as many
 // loads as possible are in flight. 16411 bf16 rows of 36 heads of 128: 53.7 us
 // (5.8 TB/s) with all threads of an SM in CTAs of 128 and everything streamed
-// (56.3 with plain stores, 55.2 with plain loads); with plain stores 58 us in
-// CTAs of 256, 69 of 1024, 70 with five CTAs of 256; two heads a thread, the
-// rotation loaded once, was slower (78 us).
+// (56.3 with plain stores, 55.2 with plain loads; with the attention of the
+// last row behind it 75.1, and 76.1 with plain stores; at 4000 rows 25.7 and
+// 27.6); with plain stores 58 us in CTAs of 256, 69 of 1024, 70 with five CTAs
+// of 256; two heads a thread, the rotation loaded once, was slower (78 us).
 #include <cmath>
 #include <type_traits>
 

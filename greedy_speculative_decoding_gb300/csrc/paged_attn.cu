@@ -78,15 +78,20 @@ static Sizes sizes(const sf_paged_cache& c, int n_heads, int max_rows, int q_dty
   auto total = [&](int mt) { return items(mt) * z.units; };   // if every request filled its table
   // Larger tiles read the cache less often (again from L2), smaller ones spread
   // few units over more of the GPU and start sooner. Measured, in us, for
-  // requests x tokens x KV heads and queries, in tiles of 16 / 32 / 128:
-  //   16-bit, head dimension 128: 1 x 4000 x 4, 45: 10.3 / 10.1 / 11.5; 8 x
-  //     1000 x 8, 45: 18.4 / 20.6 / 15.8; 20: 14.4 / 13.2 / 14.3
-  //   16-bit, 64: 16 x 5..4099 x 2, 91: 19.8 / 16.0 / 16.6; 8 x 4096..8192 x 8,
-  //     45: 40.5 / 35.1 / 27.2; 20: 29.8 / 24.1 / 26.4
-  //   fp32, 128 (not in tiles of 32): 1 x 8000 x 4, 45: 15.9 / 17.9; 8 x 1000 x
-  //     8, 45: 26.4 / 25.7; 20: 19.9 / 22.8; 8 x 4096..8192 x 8, 20: 65.5 / 58.6
-  //   fp32, 64: 8 x 1000 x 8, 45: 17.4 / 19.5 / 20.9; 91: 27.0 / 25.9 / 22.8;
-  //     20: 13.9 / 14.2 / 20.3; 8 x 4096..8192 x 8, 20: 41.2 / 36.2 / 51.7
+  // requests x tokens x KV heads and queries in tables that the requests fill,
+  // in tiles of 16 / 32 / 128:
+  //   16-bit, head dimension 128: 1 x 4000 x 4, 45: 10.3 / 10.1 / 11.7; 8 x
+  //     1000 x 8, 45: 20.9 / 21.7 / 17.2; 20: 16.8 / 14.7 / 15.9
+  //   16-bit, 64: 16 x 5..4099 x 2, 91: 21.5 / 17.0 / 17.7; 8 x 4096..8192 x 8,
+  //     45: 41.8 / 36.0 / 28.4; 20: 30.9 / 23.6 / 26.9
+  //   fp32, 128 (not in tiles of 32): 1 x 8000 x 4, 45: 17.1 / 18.0; 8 x 1000 x
+  //     8, 45: 28.4 / 26.3; 20: 21.9 / 23.6; 8 x 4096..8192 x 8, 20: 66.5 / 58.3
+  //   fp32, 64: 8 x 1000 x 8, 45: 18.2 / 19.5 / 20.4; 91: 28.3 / 26.4 / 22.3;
+  //     20: 14.3 / 14.1 / 19.8; 8 x 4096..8192 x 8, 20: 42.3 / 36.3 / 50.5
+  // Wider tables move the choice towards the larger tiles, whatever the lengths
+  // (which the host does not know): 1 x 2057 x 4, 63 fp32 queries 10.9 in a table
+  // of 2112 tokens, 15.6 in one of 32768; bf16 9.3 and 11.2; 16 x 5..4099 x 2, 91
+  // fp16 queries 16.5 and 19.1.
   if (queries <= 16) z.mt = 16;
   else if (q_dtype != SF_DT_F32) z.mt = queries > 32 && total(128) >= (c.head_dim == 64 ? 4096 : 2 * sms) ? 128 : 32;
   else if (queries > 32) z.mt = total(16) >= 4000 ? 128 : 16;

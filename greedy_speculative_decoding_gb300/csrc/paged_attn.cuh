@@ -200,7 +200,7 @@ struct Shape {
   // Two CTAs on an SM when at least two stages fit in half its shared memory
   // and the registers do: the 16-bit kernel with two query tiles at head
   // dimension 128 would spill (8 sequences of 4096 to 8192 tokens, 8 KV heads,
-  // 20 queries: 39.4 us with one CTA, 45.3 with two).
+  // 20 queries: 38.6 us with one CTA, 45.3 with two).
   static constexpr int kFit2 = (kHalfSmBytes - 1024 - kExtra) / kStage;
   static constexpr int kCtas = kFit2 >= 2 && !(HD == 128 && WK == 2) ? 2 : 1;
   static constexpr int kFit1 = (220 * 1024 - 1024 - kExtra) / kStage;
@@ -211,7 +211,7 @@ struct Shape {
   // midst of its units otherwise ends that much later. 32 sequences of 0 to
   // 8191 tokens, 7 queries: 47.4 us, 48.4 with none (2 to 5 are alike, 49.1
   // with 14); 120 of up to 1000 tokens 29.3 and 36.5; fp32, one of 2057 tokens,
-  // 63 queries 11.1 and 14.1; 16 of 5 to 4099 tokens, 91 queries 12.8 and 15.8.
+  // 63 queries 11.1 and 14.1; 16 of 5 to 4099 tokens, 91 queries 13.1 and 15.8.
   static constexpr int kPiece = 4;
   // Units after which a warp's output and sum move to the part in shared
   // memory. The tensor cores cut off what they add, always towards zero, and

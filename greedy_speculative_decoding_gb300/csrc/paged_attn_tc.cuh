@@ -29,12 +29,12 @@
 // takes 1.07 thousand cycles here (600 the softmax warps' arithmetic: 64
 // exponentials a thread are 512 cycles of an SM quarter's unit; the rest
 // waits and hand-overs), its bytes 1.4 thousand at head dimension 128. Eight
-// sequences of 4096 to 8192 tokens, head_dim 128, 128 queries: 49 us (519
-// TFLOP/s; mma.sync in tiles of 64: 85 us), 45 queries: 42 us (46). With fp32
-// queries 75 us (mma.sync in tiles of 16: 233 us) and 67 us (93): the products
-// are 1.6 thousand cycles a unit there, the terms of the probabilities nearly
-// as many again in the softmax warps, behind the products; the sums' 4 us are
-// the price of an error of 3e-6.
+// sequences of 4096 to 8192 tokens, head_dim 128, 128 queries: 48 us (530
+// TFLOP/s; mma.sync in tiles of 32: 126 us), in fp16 51, as its references are
+// raised more often; 45 queries: 41 us (67). With fp32 queries 75 us (mma.sync
+// in tiles of 16: 236 us) and 67 us (94): the products are 1.6 thousand cycles a
+// unit there, the terms of the probabilities nearly as many again in the softmax
+// warps, behind the products; the sums' 4 us are the price of an error of 3e-6.
 #pragma once
 
 #include "paged_attn.cuh"
