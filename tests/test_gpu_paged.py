@@ -1062,3 +1062,47 @@ def test_captured_pass_step_by_step(pkg, dt, R, group, cap):
         # Some guesses are rejected, some requests finish: the next pass starts from fewer tokens.
         now = [max(0, (x if s else x - R) - r.randint(0, R)) if r.random() < 0.9 else 0 for x, s in zip(now, served)]
     assert cap > 6 or short > 0
+
+
+def test_every_call_on_a_stream_of_its_own(pkg):
+    """A pass on a stream that is not the current one: the same as on the
+    current one, what the calls allocate included."""
+    B, R, nq, nkv, hd, page, W = 3, 2, 8, 2, 64, 16, 6
+    g = torch.Generator(device="cuda").manual_seed(9)
+    q, k, v = (torch.randn((B * R, h, hd), dtype=BF, device="cuda", generator=g) for h in (nq, nkv, nkv))
+    lens, starts = i32([5, 40, 96]), i32([0, R, 2 * R, 3 * R])
+
+    def one_pass(stream):
+        tables, held, free, nf = torch.zeros((B, W), dtype=torch.int32, device="cuda"), i32([0] * B), i32(list(range(20))), i32([20])
+        kc, vc = make_cache(20, nkv, page, hd, BF, fill=0.5)
+        if stream is not None:
+            stream.wait_stream(torch.cuda.current_stream())
+        rope = pkg.rope_table(W * page, hd, 1e4, stream=stream)
+        plan = pkg.page_plan(lens, starts, tables, held, free, nf, page, n_rows=B * R, stream=stream)
+        qr = pkg.kv_append(k, v, plan.slots, kc, vc, q=q, positions=plan.positions, rope=rope, stream=stream)
+        out = pkg.paged_attention(qr, kc, vc, tables, lens, starts=starts, max_rows=R, stream=stream)
+        if stream is not None:
+            torch.cuda.current_stream().wait_stream(stream)
+        torch.cuda.synchronize()
+        return [rope, *plan, tables, free, kc, vc, qr, out]
+
+    want = one_pass(None)
+    for a, b in zip(want, one_pass(torch.cuda.Stream())):
+        assert torch.equal(a, b)
+
+
+def test_calls_with_nothing_to_do(pkg):
+    """No rows, no requests: nothing is written, nothing is refused."""
+    c = attn_case(53, [30, 9], [2, 1], 4, 2, 64, 16)
+    kept = c["k"].clone()
+    none = torch.empty((0, 2, 64), dtype=BF, device="cuda")
+    q0 = torch.empty((0, 4, 64), dtype=BF, device="cuda")
+    rope = pkg.rope_table(4, 64, 1e4)
+    assert pkg.kv_append(none, none, i32([]), c["k"], c["v"], q=q0, positions=i32([]), rope=rope).shape == (0, 4, 64)
+    assert torch.equal(c["k"].nan_to_num(3.0), kept.nan_to_num(3.0))
+    assert pkg.paged_attention(q0, c["k"], c["v"], i32(c["tables"]), i32([30, 9]), starts=i32([0, 0, 0]),
+                               max_rows=1).shape == (0, 4, 64)
+    out = torch.full_like(c["q"], 7.0)
+    pkg.paged_attention(c["q"], c["k"], c["v"], torch.empty((0, 3), dtype=torch.int32, device="cuda"), i32([]), out=out)
+    pkg.paged_attention(c["q"], c["k"], c["v"], i32(c["tables"]), i32([30, 9]), starts=i32([0, 0, 0]), max_rows=3, out=out)
+    assert bool((out == 7).all())
