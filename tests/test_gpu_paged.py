@@ -1106,3 +1106,48 @@ def test_calls_with_nothing_to_do(pkg):
     pkg.paged_attention(c["q"], c["k"], c["v"], torch.empty((0, 3), dtype=torch.int32, device="cuda"), i32([]), out=out)
     pkg.paged_attention(c["q"], c["k"], c["v"], i32(c["tables"]), i32([30, 9]), starts=i32([0, 0, 0]), max_rows=3, out=out)
     assert bool((out == 7).all())
+
+
+@pytest.mark.parametrize("dq,dc", TYPES)
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("rows,group", [(3, 7), (9, 7), (9, 1)])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("start", [16384, 16383, 16380])
+def test_masked_nan_where_sums_move(pkg, dq, dc, hd, rows, group, bad, start):
+    """Items of 257 units, one a CTA, whose last unit is where output and sums
+    move to the part and holds the pass's own rows (for some starts the unit
+    before it as well): values there that are no finite numbers reach no row
+    that does not see them, and the rest is the mean it should be."""
+    nkv, page, B, cycle = 2, 64, 160, 8
+    n = start + rows
+    g = torch.Generator(device="cuda").manual_seed(start + rows)
+    k, v = (torch.randn((cycle + 2, nkv, page, hd), dtype=dc, device="cuda", generator=g) for _ in range(2))
+    W = 140000 // page
+    tables = (torch.arange(W, dtype=torch.int32, device="cuda") % cycle).repeat(B, 1)
+    tables[:, start // page:start // page + 2] = torch.tensor([cycle, cycle + 1], dtype=torch.int32, device="cuda")
+    q = torch.randn((rows, nkv * group, hd), device="cuda", generator=g).to(dq).repeat(B, 1, 1)
+    lse = torch.zeros(q.shape[:2], device="cuda")
+    good = pkg.paged_attention(q, k, v, tables, i32([n] * B), max_rows=rows, lse=lse)
+    at = start + rows - 1                      # the last row's slot: only that row sees it
+    k[cycle + at // page - start // page, :, at % page] = bad
+    v[cycle + at // page - start // page, :, at % page] = bad
+    l2 = torch.zeros_like(lse)
+    out = pkg.paged_attention(q, k, v, tables, i32([n] * B), max_rows=rows, lse=l2)
+    keep = torch.tensor([i for i in range(B * rows) if i % rows != rows - 1], device="cuda")
+    assert torch.equal(out[keep], good[keep]) and torch.equal(l2[keep], lse[keep])
+    assert not bool(torch.isfinite(out[rows - 1::rows]).any())
+    ids = tables[0, :n // page + 1].long()
+    kd, vd = (c[ids].transpose(0, 1).reshape(nkv, -1, hd).double() for c in (k, v))
+    for j in range(rows - 1):
+        x = torch.einsum("hgd,hsd->hgs", q[j].double().view(nkv, group, hd), kd[:, :start + j + 1]) / math.sqrt(hd)
+        qk = torch.einsum("hgd,hsd->hgs", q[j].double().abs().view(nkv, group, hd), kd[:, :start + j + 1].abs()).amax(-1)
+        p = torch.softmax(x, -1)
+        ref, A = torch.einsum("hgs,hsd->hgd", p, vd[:, :start + j + 1]), torch.einsum("hgs,hsd->hgd", p, vd[:, :start + j + 1].abs())
+        # (as check_attn; the sums over units: 512 of the tensor cores' steps and the folds)
+        eps = 2 * (hd + 8) * 2.0 ** -23 * (qk / math.sqrt(hd)).clamp(min=1.0)[..., None] + 1100 * 2.0 ** -23
+        up = 0.0 if dq == F4 else U[dc]
+        bound = (up + eps) * A + (U[dq] + eps) * ref.abs() + TINY[dq]
+        if dq == FH:
+            bound = bound + n * 2.0 ** -37 * float(vd[:, :start + j + 1].abs().max()) * p.amax(-1)[..., None]
+        err = (good[j::rows].double().view(B, nkv, group, hd) - ref).abs()
+        assert bool((err <= bound).all()), float((err / bound).max())
