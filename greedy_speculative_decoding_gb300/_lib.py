@@ -28,6 +28,8 @@ EXPORTS = (
     "sf_page_plan", "sf_rope_table", "sf_kv_append",
     "sf_kv_pool_bytes", "sf_paged_engine_workspace_bytes", "sf_create_paged", "sf_get_pages",
     "sf_paged_attention_workspace_bytes", "sf_paged_attention",
+    "sf_chunk_attention_workspace_bytes", "sf_chunk_attention",
+    "sf_page_free", "sf_page_fork", "sf_page_compact", "sf_page_copy", "sf_token_logprobs",
 )
 
 
@@ -118,6 +120,13 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "sf_kv_append": (ST, [P, I32, P, P, P, P, P, P, P, I32, P]),
         "sf_paged_attention_workspace_bytes": (SZ, [I32, I32, I32, I32]),
         "sf_paged_attention": (ST, [P, P, P, I32, P, I32, P, P, I32, I32, P, ctypes.c_float, P, P, P]),
+        "sf_chunk_attention_workspace_bytes": (SZ, [I32, I32, I32, I32]),
+        "sf_chunk_attention": (ST, [P, P, P, I32, P, I32, P, P, I32, I32, ctypes.c_float, P, P, P]),
+        "sf_page_free": (ST, [P, P, I32, I32, I32, P, I32, P, P, I32, P, I32, P, P, P]),
+        "sf_page_fork": (ST, [P, P, I32, P, I32, I32, P, I32, P, P, I32, P, I32, P, P, P, P, P, P]),
+        "sf_page_compact": (ST, [P, I32, I32, P, P, I32, P, P, P, I32, P, P, P, I32, P, P]),
+        "sf_page_copy": (ST, [P, I32, ctypes.c_int64, ctypes.c_int64, P, P, P, I32, P, P]),
+        "sf_token_logprobs": (ST, [P, I32, ctypes.c_int64, I32, I32, P, I32, P, P, P, P, P, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)

@@ -8,6 +8,7 @@
 namespace sf {
 
 constexpr int kMaxPlanBatch = 8192;   // requests of one page plan (their prefix sums lie in shared memory)
+constexpr int kMaxChunk = 1 << 20;    // rows of a request in one chunk
 constexpr int kMinPage = 16, kMaxPage = 256;
 
 inline bool page_ok(int page) { return page >= kMinPage && page <= kMaxPage && (page & (page - 1)) == 0; }

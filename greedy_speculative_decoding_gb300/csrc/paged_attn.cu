@@ -16,8 +16,8 @@ struct Layout {
   size_t ml, part, total;
 };
 static Layout layout(int n_heads, int n_kv_heads, int head_dim, int max_rows) {   // (whatever the tile)
-  const int queries = max_rows * (n_heads / n_kv_heads);
-  const size_t mt = std::min(queries, 128);
+  const long queries = (long)max_rows * (n_heads / n_kv_heads);
+  const size_t mt = std::min(queries, 128l);
   Layout l;
   l.ml = kMaxDesc * sizeof(int4);
   l.part = l.ml + 2 * kMaxCtas * mt * sizeof(float2);
@@ -193,36 +193,38 @@ extern "C" size_t sf_paged_attention_workspace_bytes(int32_t n_heads, int32_t n_
   return pa::layout(n_heads, n_kv_heads, head_dim, max_rows).total;
 }
 
-extern "C" sf_status sf_paged_attention(const sf_paged_cache* cache, const sf_rows* q, const sf_rows* out, int32_t n,
-                                        const int32_t* d_tables, int32_t table_width, const int32_t* d_lens,
-                                        const int32_t* d_starts, int32_t batch, int32_t max_rows,
-                                        const uint64_t* d_mask, float scale, float* d_lse, void* d_workspace,
-                                        void* cuda_stream) {
-  const sf_status cs = check_cache(cache, "sf_paged_attention");
+// The checks and the launch of both entries (a chunk has no mask and up to kMaxChunk rows).
+static sf_status attention(const char* who, int most_rows, const sf_paged_cache* cache, const sf_rows* q,
+                           const sf_rows* out, int32_t n, const int32_t* d_tables, int32_t table_width,
+                           const int32_t* d_lens, const int32_t* d_starts, int32_t batch, int32_t max_rows,
+                           const uint64_t* d_mask, float scale, float* d_lse, void* d_workspace, void* cuda_stream) {
+  const sf_status cs = check_cache(cache, who);
   if (cs != SF_OK) return cs;
-  if (!q || !out || n < 0 || batch < 0) return set_error(SF_ERR_ARG, "sf_paged_attention: no q or out, or n or batch negative");
+  if (!q || !out || n < 0 || batch < 0) return set_error(SF_ERR_ARG, "%s: no q or out, or n or batch negative", who);
   if (n == 0 || batch == 0) return SF_OK;
-  if (!d_tables || !d_lens || !d_workspace) return set_error(SF_ERR_ARG, "sf_paged_attention: null tables, lens or workspace");
+  if (!d_tables || !d_lens || !d_workspace) return set_error(SF_ERR_ARG, "%s: null tables, lens or workspace", who);
   if (reinterpret_cast<uintptr_t>(d_workspace) & 255)
-    return set_error(SF_ERR_ARG, "sf_paged_attention: the workspace must be 256-byte aligned");
+    return set_error(SF_ERR_ARG, "%s: the workspace must be 256-byte aligned", who);
   if (q->dtype != out->dtype || (q->dtype != cache->dtype && !(q->dtype == SF_DT_F32 && cache->dtype == SF_DT_BF16)))
-    return set_error(SF_ERR_UNSUPPORTED, "sf_paged_attention: q and out must have the cache's type, or be fp32 over a bf16 cache");
+    return set_error(SF_ERR_UNSUPPORTED, "%s: q and out must have the cache's type, or be fp32 over a bf16 cache", who);
   if (q->n_heads < 1 || q->n_heads > 65535 || q->n_heads % cache->n_kv_heads || out->n_heads != q->n_heads)
-    return set_error(SF_ERR_ARG, "sf_paged_attention: heads must be a multiple of the cache's, the same in q and out");
-  if (max_rows < 1 || max_rows > (d_mask ? 64 : SF_MAX_ROWS))
-    return set_error(SF_ERR_ARG, "sf_paged_attention: need 1 <= max_rows <= %d (64 with a mask)", SF_MAX_ROWS);
+    return set_error(SF_ERR_ARG, "%s: heads must be a multiple of the cache's, the same in q and out", who);
+  if (max_rows < 1 || max_rows > most_rows)
+    return set_error(SF_ERR_ARG, "%s: need 1 <= max_rows <= %d%s", who, most_rows, d_mask ? " with a mask" : "");
+  if ((int64_t)max_rows * (q->n_heads / cache->n_kv_heads) > 1 << 30)
+    return set_error(SF_ERR_UNSUPPORTED, "%s: more than 2^30 queries of one KV head", who);
   if (!d_starts && (n % batch || n / batch > max_rows))
-    return set_error(SF_ERR_ARG, "sf_paged_attention: without starts, n must be batch times at most max_rows rows");
+    return set_error(SF_ERR_ARG, "%s: without starts, n must be batch times at most max_rows rows", who);
   if (table_width < 1 || table_width > (1 << 30) / cache->page)
-    return set_error(SF_ERR_ARG, "sf_paged_attention: need 1 <= table_width <= 2^30 / page");
+    return set_error(SF_ERR_ARG, "%s: need 1 <= table_width <= 2^30 / page", who);
   const int al = q->dtype == SF_DT_F32 ? 4 : 8;
   for (const sf_rows* r : {q, out})
     if (!r->data || (reinterpret_cast<uintptr_t>(r->data) & 15) || (n > 1 && r->row % al) ||
         (r->n_heads > 1 && r->head % al))
-      return set_error(SF_ERR_ARG, "sf_paged_attention: q and out must be 16-byte aligned with strides of multiples of 16 bytes");
+      return set_error(SF_ERR_ARG, "%s: q and out must be 16-byte aligned with strides of multiples of 16 bytes", who);
   if (vectors_overlap(n, out->row, out->n_heads, out->head, cache->head_dim))
-    return set_error(SF_ERR_ARG, "sf_paged_attention: rows of out overlap");
-  if (!std::isfinite(scale)) return set_error(SF_ERR_ARG, "sf_paged_attention: scale must be finite");
+    return set_error(SF_ERR_ARG, "%s: rows of out overlap", who);
+  if (!std::isfinite(scale)) return set_error(SF_ERR_ARG, "%s: scale must be finite", who);
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
@@ -234,8 +236,33 @@ extern "C" sf_status sf_paged_attention(const sf_paged_cache* cache, const sf_ro
   a.mask = reinterpret_cast<const unsigned long long*>(d_mask);
   a.B = batch, a.N = n, a.W = table_width, a.nq = q->n_heads, a.max_rows = max_rows, a.rows_each = n / batch;
   if (!pa::units_fit(*cache, q->n_heads, max_rows, q->dtype, batch, table_width, sms))
-    return set_error(SF_ERR_UNSUPPORTED, "sf_paged_attention: table_width * page too large for this many heads and rows");
+    return set_error(SF_ERR_UNSUPPORTED, "%s: table_width * page too large for this many heads and rows", who);
   if (e == cudaSuccess) e = pa::enqueue(a, *cache, q->dtype, scale, d_workspace, sms, static_cast<cudaStream_t>(cuda_stream));
-  if (e != cudaSuccess) return set_error(SF_ERR_CUDA, "sf_paged_attention: %s", cudaGetErrorString(e));
+  if (e != cudaSuccess) return set_error(SF_ERR_CUDA, "%s: %s", who, cudaGetErrorString(e));
   return SF_OK;
+}
+
+extern "C" sf_status sf_paged_attention(const sf_paged_cache* cache, const sf_rows* q, const sf_rows* out, int32_t n,
+                                        const int32_t* d_tables, int32_t table_width, const int32_t* d_lens,
+                                        const int32_t* d_starts, int32_t batch, int32_t max_rows,
+                                        const uint64_t* d_mask, float scale, float* d_lse, void* d_workspace,
+                                        void* cuda_stream) {
+  return attention("sf_paged_attention", d_mask ? 64 : SF_MAX_ROWS, cache, q, out, n, d_tables, table_width, d_lens,
+                   d_starts, batch, max_rows, d_mask, scale, d_lse, d_workspace, cuda_stream);
+}
+
+extern "C" size_t sf_chunk_attention_workspace_bytes(int32_t n_heads, int32_t n_kv_heads, int32_t head_dim,
+                                                     int32_t max_rows) {
+  if (n_heads < 1 || n_kv_heads < 1 || n_heads % n_kv_heads || n_heads > 65535 || (head_dim != 64 && head_dim != 128) ||
+      max_rows < 1 || max_rows > kMaxChunk)
+    return 0;
+  return pa::layout(n_heads, n_kv_heads, head_dim, max_rows).total;
+}
+
+extern "C" sf_status sf_chunk_attention(const sf_paged_cache* cache, const sf_rows* q, const sf_rows* out, int32_t n,
+                                        const int32_t* d_tables, int32_t table_width, const int32_t* d_lens,
+                                        const int32_t* d_starts, int32_t batch, int32_t max_rows, float scale,
+                                        float* d_lse, void* d_workspace, void* cuda_stream) {
+  return attention("sf_chunk_attention", kMaxChunk, cache, q, out, n, d_tables, table_width, d_lens, d_starts, batch,
+                   max_rows, nullptr, scale, d_lse, d_workspace, cuda_stream);
 }

@@ -1,5 +1,5 @@
 /*
- * The paged operators' Python binding (module _paged): checks the tensors and
+ * The paged operators' and token_logprobs' Python binding (module _paged): checks the tensors and
  * calls the C ABI. A call of the operators on a few rows takes the GPU 3 to 6
  * us; marshalling it over ctypes took the host 9 to 14 us, reading the
  * tensors' Python attributes from C 6 to 8, the tensors themselves (here) 3 to
@@ -97,8 +97,7 @@ sf_rows rows_of(PyObject* o, const char* name, int64_t n, int64_t hd, int dev) {
   return r;
 }
 
-sf_paged_cache cache_of(PyObject* ok, PyObject* ov, int dev) {
-  const at::Tensor &k = tensor(ok, "k_cache"), &v = tensor(ov, "v_cache");
+sf_paged_cache layer_of(const at::Tensor& k, const at::Tensor& v, int dev) {
   const int dt = sf_type(k.scalar_type());
   bool good = dt >= 0 && k.scalar_type() == v.scalar_type() && k.dim() == 4 && k.sizes() == v.sizes() &&
               on_device(k, dev) && on_device(v, dev) && k.stride(3) == 1 && v.stride(3) == 1;
@@ -120,6 +119,10 @@ sf_paged_cache cache_of(PyObject* ok, PyObject* ov, int dev) {
   c.k_page = k.stride(0), c.k_head = k.stride(1), c.k_slot = k.stride(2);
   c.v_page = v.stride(0), c.v_head = v.stride(1), c.v_slot = v.stride(2);
   return c;
+}
+
+sf_paged_cache cache_of(PyObject* ok, PyObject* ov, int dev) {
+  return layer_of(tensor(ok, "k_cache"), tensor(ov, "v_cache"), dev);
 }
 
 /* A tensor's size along its first dimensions, each within 32 bits. */
@@ -209,8 +212,10 @@ sf_status kv_append(PyObject* const* a) {
   return written(s, a, {5, 6, 8});
 }
 
-/* dev, stream, max_rows, scale or None, q, k_cache, v_cache, tables, lens, starts, mask, out, lse, workspace */
-sf_status paged_attention(PyObject* const* a) {
+/* Both attentions. dev, stream, max_rows, scale or None, q, k_cache, v_cache, tables, lens, starts, mask, out, lse,
+ * workspace */
+template <bool CHUNK>
+sf_status attention(PyObject* const* a) {
   const int dev = (int)integer(a[0], "device", 0, INT32_MAX), max_rows = (int)integer(a[2], "max_rows", 0, INT32_MAX);
   const sf_paged_cache cache = cache_of(a[5], a[6], dev);
   const int64_t n = shaped(a[4], "q", 3, "rows [n, heads, head_dim]").size(0);
@@ -228,17 +233,112 @@ sf_status paged_attention(PyObject* const* a) {
   };
   const int32_t *tables = i32(7, "tables", {B, W}), *lens = i32(8, "lens", {B}), *starts = i32(9, "starts", {B + 1});
   void *mask = flat(a[10], "mask", at::kLong, dev, {n}), *lse = flat(a[12], "lse", at::kFloat, dev, {n, q.n_heads});
-  const size_t need = sf_paged_attention_workspace_bytes(q.n_heads, cache.n_kv_heads, cache.head_dim, max_rows);
+  const size_t need = (CHUNK ? sf_chunk_attention_workspace_bytes : sf_paged_attention_workspace_bytes)(
+      q.n_heads, cache.n_kv_heads, cache.head_dim, max_rows);
   const at::Tensor& ws = tensor(a[13], "workspace");
   if (ws.dim() != 1 || (size_t)ws.size(0) < need) {
     char text[80];
     snprintf(text, sizeof(text), "at least %zu contiguous bytes on cuda:%d", need, dev);
     wrong("workspace", text, ws);
   }
-  const sf_status s = sf_paged_attention(
-      &cache, &q, &out, (int32_t)n, tables, (int32_t)W, lens, starts, (int32_t)B, max_rows, static_cast<uint64_t*>(mask),
-      scale, static_cast<float*>(lse), flat(a[13], "workspace", at::kByte, dev, {ws.size(0)}), stream_of(a[1]));
+  void* scratch = flat(a[13], "workspace", at::kByte, dev, {ws.size(0)});
+  const sf_status s =
+      CHUNK ? sf_chunk_attention(&cache, &q, &out, (int32_t)n, tables, (int32_t)W, lens, starts, (int32_t)B, max_rows,
+                                 scale, static_cast<float*>(lse), scratch, stream_of(a[1]))
+            : sf_paged_attention(&cache, &q, &out, (int32_t)n, tables, (int32_t)W, lens, starts, (int32_t)B, max_rows,
+                                 static_cast<uint64_t*>(mask), scale, static_cast<float*>(lse), scratch, stream_of(a[1]));
   return written(s, a, {11, 12, 13});
+}
+
+/* The address of a contiguous int32 tensor [size]. */
+int32_t* ints(PyObject* o, const char* name, int dev, int64_t size) {
+  return static_cast<int32_t*>(flat(o, name, at::kInt, dev, {size}));
+}
+int64_t size_of(PyObject* o, const char* name) { return shaped(o, name, 1, "int32 [n]").size(0); }
+
+/* dev, stream, page, requests, keep, tables, held, shares, free, n_free, status */
+sf_status page_free(PyObject* const* a) {
+  const int dev = (int)integer(a[0], "device", 0, INT32_MAX), page = (int)integer(a[2], "page", INT32_MIN, INT32_MAX);
+  const at::Tensor& tab = shaped(a[5], "tables", 2, "block tables [B, W]");
+  const int64_t B = tab.size(0), W = tab.size(1), n = size_of(a[3], "requests"), P = size_of(a[7], "shares"),
+                cap = size_of(a[8], "free");
+  const sf_status s =
+      sf_page_free(ints(a[3], "requests", dev, n), ints(a[4], "keep", dev, n), (int32_t)n, (int32_t)B, page,
+                   static_cast<int32_t*>(flat(a[5], "tables", at::kInt, dev, {B, W})), (int32_t)W,
+                   ints(a[6], "held", dev, B), ints(a[7], "shares", dev, P), (int32_t)P, ints(a[8], "free", dev, cap),
+                   (int32_t)cap, ints(a[9], "n_free", dev, 1), ints(a[10], "status", dev, n), stream_of(a[1]));
+  return written(s, a, {6, 7, 8, 9, 10});
+}
+
+/* dev, stream, page, src, dst, lens, tables, held, shares, free, n_free, source, target, slots, status */
+sf_status page_fork(PyObject* const* a) {
+  const int dev = (int)integer(a[0], "device", 0, INT32_MAX), page = (int)integer(a[2], "page", INT32_MIN, INT32_MAX);
+  const at::Tensor& tab = shaped(a[6], "tables", 2, "block tables [B, W]");
+  const int64_t B = tab.size(0), W = tab.size(1), n = size_of(a[3], "src"), P = size_of(a[8], "shares"),
+                cap = size_of(a[9], "free");
+  const sf_status s = sf_page_fork(
+      ints(a[3], "src", dev, n), ints(a[4], "dst", dev, n), (int32_t)n, ints(a[5], "lens", dev, B), (int32_t)B, page,
+      static_cast<int32_t*>(flat(a[6], "tables", at::kInt, dev, {B, W})), (int32_t)W, ints(a[7], "held", dev, B),
+      ints(a[8], "shares", dev, P), (int32_t)P, ints(a[9], "free", dev, cap), (int32_t)cap,
+      ints(a[10], "n_free", dev, 1), ints(a[11], "source", dev, n), ints(a[12], "target", dev, n),
+      ints(a[13], "slots", dev, n), ints(a[14], "status", dev, n), stream_of(a[1]));
+  return written(s, a, {6, 7, 8, 10, 11, 12, 13, 14});
+}
+
+/* dev, stream, tables, held, shares, tables_out, shares_out, free, n_free, source, target, count */
+sf_status page_compact(PyObject* const* a) {
+  const int dev = (int)integer(a[0], "device", 0, INT32_MAX);
+  const at::Tensor& tab = shaped(a[2], "tables", 2, "block tables [B, W]");
+  const int64_t B = tab.size(0), W = tab.size(1), P = size_of(a[4], "shares"), cap = size_of(a[7], "free"),
+                moves = size_of(a[9], "source");
+  const sf_status s = sf_page_compact(
+      static_cast<int32_t*>(flat(a[2], "tables", at::kInt, dev, {B, W})), (int32_t)B, (int32_t)W,
+      ints(a[3], "held", dev, B), ints(a[4], "shares", dev, P), (int32_t)P,
+      static_cast<int32_t*>(flat(a[5], "tables_out", at::kInt, dev, {B, W})), ints(a[6], "shares_out", dev, P),
+      ints(a[7], "free", dev, cap), (int32_t)cap, ints(a[8], "n_free", dev, 1), ints(a[9], "source", dev, moves),
+      ints(a[10], "target", dev, moves), (int32_t)moves, ints(a[11], "count", dev, 1), stream_of(a[1]));
+  return written(s, a, {5, 6, 7, 8, 9, 10, 11});
+}
+
+/* dev, stream, source, target, k_cache, v_cache, slots, count */
+sf_status page_copy(PyObject* const* a) {
+  const int dev = (int)integer(a[0], "device", 0, INT32_MAX);
+  const at::Tensor &k = tensor(a[4], "k_cache"), &v = tensor(a[5], "v_cache");
+  const bool deep = k.dim() == 5 && v.dim() == 5;   // [layers, ...]
+  sf_paged_cache cache;
+  int64_t layers = 1;
+  if (deep) {
+    layers = k.size(0);
+    if (v.size(0) != layers || layers < 1 || layers > INT32_MAX)
+      wrong("v_cache", "as many layers as k_cache, one at least", v);
+    const at::Tensor k0 = k.select(0, 0), v0 = v.select(0, 0);
+    cache = layer_of(k0, v0, dev);
+  } else {
+    cache = layer_of(k, v, dev);
+  }
+  const int64_t n = size_of(a[2], "source");
+  const sf_status s = sf_page_copy(&cache, (int32_t)layers, deep ? k.stride(0) : 0, deep ? v.stride(0) : 0,
+                                   ints(a[2], "source", dev, n), ints(a[3], "target", dev, n),
+                                   ints(a[6], "slots", dev, n), (int32_t)n, ints(a[7], "count", dev, 1), stream_of(a[1]));
+  return written(s, a, {4, 5});
+}
+
+/* dev, stream, top, logits, tokens, logprob, entropy, rank, top_ids, top_logprobs */
+sf_status token_logprobs(PyObject* const* a) {
+  const int dev = (int)integer(a[0], "device", 0, INT32_MAX), top = (int)integer(a[2], "top", INT32_MIN, INT32_MAX);
+  const at::Tensor& x = shaped(a[3], "logits", 2, "rows of logits [n, vocab]");
+  const int64_t n = x.size(0), vocab = x.size(1);
+  if (sf_type(x.scalar_type()) < 0 || !on_device(x, dev) || (vocab > 1 && x.stride(1) != 1))
+    wrong("logits", "rows [n, vocab] (fp32, bf16 or fp16, last dimension contiguous) on the current device", x);
+  auto f32 = [&](int i, const char* name, std::initializer_list<int64_t> shape) {
+    return static_cast<float*>(flat(a[i], name, at::kFloat, dev, shape));
+  };
+  const sf_status s = sf_token_logprobs(
+      x.data_ptr(), sf_type(x.scalar_type()), n > 1 ? x.stride(0) : 0, (int32_t)n, (int32_t)vocab,
+      ints(a[4], "tokens", dev, n), top, f32(5, "logprob", {n}), f32(6, "entropy", {n}), ints(a[7], "rank", dev, n),
+      static_cast<int32_t*>(flat(a[8], "top_ids", at::kInt, dev, {n, top})), f32(9, "top_logprobs", {n, top}),
+      stream_of(a[1]));
+  return written(s, a, {5, 6, 7, 8, 9});
 }
 
 template <int N, sf_status (*F)(PyObject* const*)>
@@ -250,7 +350,11 @@ constexpr PyMethodDef entry(const char* name) {
 
 PyMODINIT_FUNC PyInit__paged(void) {
   static PyMethodDef methods[] = {entry<15, page_plan>("page_plan"), entry<11, kv_append>("kv_append"),
-                                  entry<14, paged_attention>("paged_attention"), {nullptr, nullptr, 0, nullptr}};
+                                  entry<14, attention<false>>("paged_attention"),
+                                  entry<14, attention<true>>("chunk_attention"), entry<11, page_free>("page_free"),
+                                  entry<15, page_fork>("page_fork"), entry<12, page_compact>("page_compact"),
+                                  entry<8, page_copy>("page_copy"), entry<10, token_logprobs>("token_logprobs"),
+                                  {nullptr, nullptr, 0, nullptr}};
   static PyModuleDef module = {PyModuleDef_HEAD_INIT, "_paged", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
   return PyModule_Create(&module);
 }

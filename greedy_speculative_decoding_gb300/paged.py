@@ -1,12 +1,19 @@
 """A key-value cache in pages: block tables and slot maps from request
-lengths, RoPE and append, and attention over the pages. Argument marshalling
-over the C ABI, as in the engine's wrapper.
+lengths, RoPE and append, attention over the pages, and pages that several
+requests hold. Argument marshalling over the C ABI, as in the engine's wrapper.
 
 A pass over a batch of requests of different lengths runs the three in order
 (``page_plan``, ``kv_append``, ``paged_attention``); what they need to know of
 it lies on the device, so a captured pass can be replayed with other lengths.
 ``starts`` [B + 1] gives each request's token rows in the pass, ``lens`` [B]
-its tokens including them.
+its tokens including them. ``chunk_attention`` takes the attention's place for
+prompts and long pieces of them.
+
+Requests that continue one another share pages: ``page_fork``, ``page_free``
+and ``page_compact`` change tables, counts and the stack of free pages, and
+``page_copy`` moves what the first and the last of them say in every layer.
+``shares`` int32 [n_pages] counts a page's holders beyond the first (zeros to
+begin with).
 
 Every call takes tensors of the current CUDA device and enqueues its work on
 ``stream`` (default: the current stream). Tensors that a call allocates itself
@@ -163,3 +170,125 @@ def paged_attention(q, k_cache, v_cache, tables, lens, starts=None, max_rows=Non
     if s:
         L.check(s)
     return out
+
+
+def chunk_attention_workspace(q, k_cache, tables, max_rows: int) -> torch.Tensor:
+    """Scratch for chunk_attention calls with these head counts and at most
+    max_rows rows a request. Any contents will do; calls that may overlap on
+    the GPU (on two streams, or in two graphs) need one each."""
+    return torch.empty(_chunk_bytes(q, k_cache, max_rows), dtype=torch.uint8, device=q.device)
+
+
+def _chunk_bytes(q, k_cache, max_rows):
+    n = L.load().sf_chunk_attention_workspace_bytes(q.shape[1], k_cache.shape[1], k_cache.shape[3], max_rows)
+    if n == 0:
+        raise L.SFError(L.SF_ERR_ARG, "sf_chunk_attention_workspace_bytes rejected the heads, head_dim or max_rows")
+    return n
+
+
+def chunk_attention(q, k_cache, v_cache, tables, lens, starts=None, max_rows=None, scale=None, out=None, lse=None,
+                    workspace=None, stream=None) -> torch.Tensor:
+    """Attention of a chunk of new tokens over the pages (sf_chunk_attention):
+    as paged_attention without a mask, for requests of up to 2^20 rows. q [n,
+    heads, head_dim]; row j of request b's n_b rows sees its slots 0 ..
+    lens[b] - n_b + j. max_rows (needed with starts): the most rows of one
+    request. Rows outside every request are left as they were."""
+    call = (_native or _binding()).chunk_attention
+    dev, st = _device(stream)
+    if max_rows is None:
+        if starts is not None:
+            raise ValueError("max_rows is needed with starts")
+        max_rows = max(1, q.shape[0] // max(1, tables.shape[0]))
+    if out is None:
+        out = _empty(q.shape, q.dtype, dev, stream)
+    if workspace is None:
+        workspace = _empty(_chunk_bytes(q, k_cache, max_rows), torch.uint8, dev, stream)
+    s = call(dev, st, max_rows, scale, q, k_cache, v_cache, tables, lens, starts, None, out, lse, workspace)
+    if s:
+        L.check(s)
+    return out
+
+
+class PageFork(NamedTuple):
+    """What page_fork leaves for page_copy: page source[i] to be copied into
+    target[i], its first slots[i] slots (-1, -1, 0: nothing), and each fork's
+    status (0 forked, 1 not enough pages, 2 refused)."""
+    source: torch.Tensor
+    target: torch.Tensor
+    slots: torch.Tensor
+    status: torch.Tensor
+
+
+class PageMoves(NamedTuple):
+    """What page_compact leaves: the new tables and shares, and for page_copy
+    the count pairs of pages, source[i] to be copied into target[i]."""
+    tables: torch.Tensor
+    shares: torch.Tensor
+    source: torch.Tensor
+    target: torch.Tensor
+    count: torch.Tensor
+
+
+def page_free(requests, tables, held, shares, free, n_free, page, keep=None, status=None, stream=None) -> torch.Tensor:
+    """Requests cut short or ended (sf_page_free): requests[i] keeps the pages
+    of its first keep[i] tokens (None: none). Pages that nobody else holds go
+    onto the stack. requests and keep int32 [n]; tables, held, shares, free and
+    n_free are updated in place. Returns status int32 [n]: 0, or 2 where the
+    request was refused and left as it is."""
+    call = (_native or _binding()).page_free
+    dev, st = _device(stream)
+    if status is None:
+        status = _empty(requests.shape, torch.int32, dev, stream)
+    s = call(dev, st, page, requests, keep, tables, held, shares, free, n_free, status)
+    if s:
+        L.check(s)
+    return status
+
+
+def page_fork(src, dst, lens, tables, held, shares, free, n_free, page, source=None, target=None, slots=None,
+              status=None, stream=None) -> PageFork:
+    """Requests forked (sf_page_fork): dst[i], which holds nothing, shares the
+    full pages of src[i]'s first lens[src[i]] tokens and gets a page off the
+    stack for the rest, whose contents page_copy brings. src and dst int32 [n],
+    lens int32 [B]; tables, held, shares and n_free are updated in place;
+    source, target, slots and status int32 [n] are allocated unless given."""
+    call = (_native or _binding()).page_fork
+    dev, st = _device(stream)
+    source, target, slots, status = (_empty(src.shape, torch.int32, dev, stream) if x is None else x
+                                     for x in (source, target, slots, status))
+    s = call(dev, st, page, src, dst, lens, tables, held, shares, free, n_free, source, target, slots, status)
+    if s:
+        L.check(s)
+    return PageFork(source, target, slots, status)
+
+
+def page_compact(tables, held, shares, free, n_free, tables_out=None, shares_out=None, source=None, target=None,
+                 count=None, stream=None) -> PageMoves:
+    """The held pages moved to the lowest numbers (sf_page_compact). tables and
+    shares are updated in place unless tables_out and shares_out are given;
+    free and n_free are written anew: every page that no table holds counts as
+    free. source and target int32 [n_pages // 2] at least and count int32 [1]
+    are allocated unless given."""
+    call = (_native or _binding()).page_compact
+    dev, st = _device(stream)
+    tables_out = tables if tables_out is None else tables_out
+    shares_out = shares if shares_out is None else shares_out
+    source, target = (_empty(shares.shape[0] // 2, torch.int32, dev, stream) if x is None else x for x in (source, target))
+    count = _empty(1, torch.int32, dev, stream) if count is None else count
+    s = call(dev, st, tables, held, shares, tables_out, shares_out, free, n_free, source, target, count)
+    if s:
+        L.check(s)
+    return PageMoves(tables_out, shares_out, source, target, count)
+
+
+def page_copy(source, target, k_cache, v_cache, slots=None, count=None, stream=None):
+    """Pages copied (sf_page_copy): page source[i] into page target[i], or its
+    first slots[i] slots, for the first count pairs (int32 [1] on the device;
+    None: all). Caches [pages, kv_heads, page, head_dim] of one layer, or
+    [layers, pages, kv_heads, page, head_dim]: every layer is copied. Pairs
+    with a negative number are passed over."""
+    call = (_native or _binding()).page_copy
+    dev, st = _device(stream)
+    s = call(dev, st, source, target, k_cache, v_cache, slots, count)
+    if s:
+        L.check(s)

@@ -533,6 +533,122 @@ SF_API sf_status sf_paged_attention(const sf_paged_cache* cache, const sf_rows* 
                                     const uint64_t* d_mask, float scale, float* d_lse, void* d_workspace,
                                     void* cuda_stream);
 
+/*
+ * Attention of a chunk of new tokens over the pages: a whole prompt, or a long
+ * piece of one, behind what its request holds already. As sf_paged_attention
+ * without a mask, for requests of up to max_rows rows, 1..2^20 (max_rows *
+ * n_heads / n_kv_heads at most 2^30): row j of the n_b rows of request b sees
+ * the slots 0 .. lens[b] - n_b + j, and writes out and lse by the same rules
+ * (types, strides, rows that see nothing, rows outside every request, odd
+ * values, waits, the workspace).
+ */
+SF_API size_t sf_chunk_attention_workspace_bytes(int32_t n_heads, int32_t n_kv_heads, int32_t head_dim,
+                                                 int32_t max_rows);
+SF_API sf_status sf_chunk_attention(const sf_paged_cache* cache, const sf_rows* q, const sf_rows* out, int32_t n,
+                                    const int32_t* d_tables, int32_t table_width, const int32_t* d_lens,
+                                    const int32_t* d_starts, int32_t batch, int32_t max_rows, float scale,
+                                    float* d_lse, void* d_workspace, void* cuda_stream);
+
+/*
+ * Pages that several requests hold. shares[p] (int32 [n_pages]) counts page p's
+ * holders beyond the first: 0 for a page that one request holds, or none. Only
+ * whole pages are shared, and nobody writes into one: a request appends behind
+ * them, into pages of its own. sf_page_plan knows nothing of shares: requests
+ * that hold shared pages may grow by it, but are cut and ended by sf_page_free.
+ * All arrays int32, updated in place unless said otherwise; entries of tables
+ * that are no page (outside 0..n_pages - 1) are passed over, not counted.
+ */
+
+/*
+ * Cuts requests short or ends them: request requests[i] is to hold keep[i]
+ * tokens (keep NULL: 0), so the first ceil(keep[i] / page) of its pages. Of the
+ * pages that it gives up, those that nobody else holds any more go onto the
+ * stack (in the order of the list, within a request in table order, each at its
+ * first place there), and the others' shares go down. status [n]: 0, or 2
+ * where the call leaves the request as it is: a number outside 0..batch - 1 or
+ * named earlier in the list, a negative keep, more than it holds, or a cut that
+ * would end inside a page that others hold on entry (what is appended next
+ * would change it for them). n 0..8192; batch 1..8192; batch * table_width and
+ * n * table_width below 2^30. The stack has room for every page.
+ */
+SF_API sf_status sf_page_free(const int32_t* d_requests, const int32_t* d_keep, int32_t n, int32_t batch, int32_t page,
+                              int32_t* d_tables, int32_t table_width, int32_t* d_held, int32_t* d_shares,
+                              int32_t n_pages, int32_t* d_free, int32_t capacity, int32_t* d_n_free,
+                              int32_t* d_status, void* cuda_stream);
+
+/*
+ * Forks requests: dst[i], which holds nothing, becomes a second holder of the
+ * first lens[src[i]] tokens of src[i]. The pages that these fill are shared; for
+ * a partly filled last one dst[i] gets a page off the stack, in the order of the
+ * list, and source[i], target[i] and slots[i] say what sf_page_copy has to copy
+ * into it in every layer (page, page, filled slots; -1, -1, 0: nothing).
+ * status [n]: 0 forked; 1 not enough pages (for this one and those before it);
+ * 2 refused: a number outside 0..batch - 1, src = dst, a dst that holds pages
+ * on entry or is named earlier in the list, a negative length, or more tokens
+ * than src holds pages for. Where it is not 0 nothing is changed for that fork.
+ * One request may be forked many times. lens [batch] is not changed. Sizes as
+ * in sf_page_free.
+ */
+SF_API sf_status sf_page_fork(const int32_t* d_src, const int32_t* d_dst, int32_t n, const int32_t* d_lens,
+                              int32_t batch, int32_t page, int32_t* d_tables, int32_t table_width, int32_t* d_held,
+                              int32_t* d_shares, int32_t n_pages, const int32_t* d_free, int32_t capacity,
+                              int32_t* d_n_free, int32_t* d_source, int32_t* d_target, int32_t* d_slots,
+                              int32_t* d_status, void* cuda_stream);
+
+/*
+ * Moves the held pages to the lowest numbers. Of U pages that the tables hold
+ * (each counted once), those numbered U and up move, in ascending order, to the
+ * pages below U that nobody holds. tables_out and shares_out (they may be tables
+ * and shares themselves) say the same with the new numbers; entries behind a
+ * request's pages stay as they are, and pages that nobody holds have shares 0.
+ * The stack is written anew: every page that no table holds, the lowest on
+ * top. source and target [moves], moves at least n_pages / 2, list what
+ * sf_page_copy has to copy in every layer, count [1] how many they are; entries
+ * behind them are -1. No target is a source. With tables_out and shares_out
+ * apart from tables and shares a call can be repeated. batch 1..8192, batch *
+ * table_width below 2^30, n_pages up to 2^20, capacity at least n_pages.
+ */
+SF_API sf_status sf_page_compact(const int32_t* d_tables, int32_t batch, int32_t table_width, const int32_t* d_held,
+                                 const int32_t* d_shares, int32_t n_pages, int32_t* d_tables_out,
+                                 int32_t* d_shares_out, int32_t* d_free, int32_t capacity, int32_t* d_n_free,
+                                 int32_t* d_source, int32_t* d_target, int32_t moves, int32_t* d_count,
+                                 void* cuda_stream);
+
+/*
+ * Copies pages: the first slots[i] slots (NULL: all) of page source[i] into page
+ * target[i], keys and values of every KV head, in each of `layers` layers;
+ * cache describes the first, and layer l lies l * k_layer and l * v_layer
+ * elements behind it (one after the other, or the layers of a page side by side
+ * within it). The first *count of the n pairs count (NULL: all); a pair with a
+ * number that is no page of the cache is passed over. A page is a target at most
+ * once and no source of the same call (else it is open what it holds). layers *
+ * n_kv_heads at most 2^24.
+ */
+SF_API sf_status sf_page_copy(const sf_paged_cache* cache, int32_t layers, int64_t k_layer, int64_t v_layer,
+                              const int32_t* d_source, const int32_t* d_target, const int32_t* d_slots, int32_t n,
+                              const int32_t* d_count, void* cuda_stream);
+
+/*
+ * Log probabilities of given tokens. Row i of logits (n rows of vocab elements,
+ * fp32, bf16 or fp16, row_stride elements apart) and token tokens[i] give, in
+ * fp32 throughout:
+ *   logprob [n]        x_t - lse, lse = log sum_v e^x_v
+ *   entropy [n]        -sum_v p_v log p_v, in nats
+ *   rank [n]           how many tokens stand in front of the given one
+ *   top_ids, top_logprobs [n][top]   the first `top` tokens, 0..32 and at most
+ *                      vocab, and their log probabilities
+ * in the order of larger logits first, of equal ones the lower token (a NaN
+ * counts as -infinity there, and -0 is 0). Any output may be NULL. A logit of
+ * -infinity is a token that cannot come; of a row that has no other, every log
+ * probability is -infinity and the entropy 0. A row that holds a NaN or
+ * +infinity gives NaN for log probabilities and entropy. Rows whose token lies
+ * outside 0..vocab - 1 are padding: nothing is written for them. vocab 1..2^31 -
+ * 65; logits aligned to their type, with any row stride from 0 to 2^38.
+ */
+SF_API sf_status sf_token_logprobs(const void* d_logits, int32_t dtype, int64_t row_stride, int32_t n, int32_t vocab,
+                                   const int32_t* d_tokens, int32_t top, float* d_logprob, float* d_entropy,
+                                   int32_t* d_rank, int32_t* d_top_ids, float* d_top_logprobs, void* cuda_stream);
+
 #ifdef __cplusplus
 }
 #endif

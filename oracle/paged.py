@@ -99,3 +99,107 @@ def paged_attention(q, k_cache, v_cache, tables, lens, starts, scale, mask=None,
                 for h in range(kvh * (nq // nkv), (kvh + 1) * (nq // nkv)):
                     out[i, h], lse[i, h], a[i, h], qk[i, h] = attention(q[i, h], k, v, scale, seen)
     return out, lse, a, qk, live
+
+
+def chunk_attention(q, k_cache, v_cache, tables, lens, starts, scale):
+    """As paged_attention without a mask, a KV head's rows of a request at a
+    time: (out, lse, a, qk, live)."""
+    n, nq, hd = q.shape
+    nkv, page = k_cache.shape[1], k_cache.shape[2]
+    g = nq // nkv
+    out, a = torch.zeros(n, nq, hd, dtype=F64), torch.zeros(n, nq, hd, dtype=F64)
+    lse, qk = torch.full((n, nq), float("-inf"), dtype=F64), torch.zeros(n, nq, dtype=F64)
+    live = torch.zeros(n, dtype=torch.bool)
+    for b, ln in enumerate(lens):
+        ln = max(0, min(ln, len(tables[0]) * page))
+        s, e = starts[b], starts[b + 1]
+        live[s:e] = True
+        first = ln - (e - s)                                   # position of row s
+        at = max(s, s - first)                                 # rows in front of it see nothing
+        if at >= e:
+            continue
+        pos = torch.arange(first + at - s, ln)
+        unseen = torch.arange(ln)[None] > pos[:, None]
+        for h in range(nkv):
+            k, v = (gather(c, tables[b], ln, page, h).to(F64) for c in (k_cache, v_cache))
+            x = q[at:e, h * g:(h + 1) * g].to(F64).transpose(0, 1) @ k.t() * scale          # [g, rows, ln]
+            m = q[at:e, h * g:(h + 1) * g].to(F64).abs().transpose(0, 1) @ k.abs().t() * abs(scale)
+            x = x.masked_fill(unseen, float("-inf"))
+            z = torch.logsumexp(x, -1)
+            p = torch.exp(x - z[..., None])
+            out[at:e, h * g:(h + 1) * g] = (p @ v).transpose(0, 1)
+            a[at:e, h * g:(h + 1) * g] = (p @ v.abs()).transpose(0, 1)
+            lse[at:e, h * g:(h + 1) * g] = z.t()
+            qk[at:e, h * g:(h + 1) * g] = m.masked_fill(unseen, 0.0).amax(-1).t()
+    return out, lse, a, qk, live
+
+
+def page_free(requests, keep, tables, held, shares, free, n_free, page):
+    """Lists in, a dict of lists out (tables is not changed)."""
+    B, W, P = len(held), len(tables[0]), len(shares)
+    held, free = list(held), list(free)
+    holders = [s + 1 for s in shares]
+    status, released, named = [], [], set()
+    for r, k in zip(requests, keep or [0] * len(requests)):
+        first = -(-k // page)
+        bad = not 0 <= r < B or r in named or k < 0 or not 0 <= held[r] <= W or first > held[r]
+        if 0 <= r < B:
+            named.add(r)
+        if not bad and k % page and 0 <= tables[r][first - 1] < P:
+            bad = shares[tables[r][first - 1]] > 0
+        status.append(2 if bad else 0)
+        if not bad:
+            released += [p for p in tables[r][first:held[r]] if 0 <= p < P]
+            held[r] = first
+    for p in released:
+        holders[p] -= 1
+    top = n_free
+    for i, p in enumerate(released):
+        if holders[p] <= 0 and p not in released[:i]:
+            free[top] = p
+            top += 1
+    return dict(held=held, shares=[max(h - 1, 0) for h in holders], free=free, n_free=top, status=status)
+
+
+def page_fork(src, dst, lens, tables, held, shares, free, n_free, page):
+    """Lists in, a dict of lists out."""
+    B, W, P = len(held), len(tables[0]), len(shares)
+    tables, new_held, shares, top = [list(t) for t in tables], list(held), list(shares), n_free
+    res = dict(source=[], target=[], slots=[], status=[])
+    named, short = set(), False
+    for s, d in zip(src, dst):
+        bad = not (0 <= s < B and 0 <= d < B) or s == d or d in named or held[d] != 0
+        bad = bad or lens[s] < 0 or held[s] > W or -(-lens[s] // page) > held[s]
+        named.add(d)
+        part = 0 if bad else lens[s] % page
+        short = short or (part > 0 and top == 0)
+        status = 2 if bad else 1 if part and short else 0
+        source, target = -1, -1
+        if status == 0:
+            full = lens[s] // page
+            for j in range(full):
+                tables[d][j] = tables[s][j]
+                if 0 <= tables[s][j] < P:
+                    shares[tables[s][j]] += 1
+            if part:
+                top -= 1
+                source, target = tables[s][full], free[top]
+                tables[d][full] = target
+            new_held[d] = -(-lens[s] // page)
+        for name, x in (("source", source), ("target", target), ("slots", part if target >= 0 else 0), ("status", status)):
+            res[name].append(x)
+    return dict(tables=tables, held=new_held, shares=shares, n_free=top, **res)
+
+
+def page_compact(tables, held, shares):
+    """Lists in, a dict of lists out."""
+    P = len(shares)
+    live = sorted({p for t, h in zip(tables, held) for p in t[:h] if 0 <= p < P})
+    u = len(live)
+    source, target = [p for p in live if p >= u], [p for p in range(u) if p not in set(live)]
+    to = dict(zip(source, target))
+    new = [0] * P
+    for p in live:
+        new[to.get(p, p)] = shares[p]
+    return dict(tables=[[to.get(p, p) if j < h else p for j, p in enumerate(t)] for t, h in zip(tables, held)],
+                shares=new, free=list(range(P - 1, u - 1, -1)), n_free=P - u, source=source, target=target)
