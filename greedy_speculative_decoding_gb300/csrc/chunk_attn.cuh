@@ -1,0 +1,726 @@
+// Attention of a chunk of new tokens over a paged cache: many rows a request,
+// so that the products bound it and not the cache's bytes.
+//
+// The formula is paged_attn.cuh's, and so are an item (request, KV head, tile
+// of queries), the deal of the items' units over the CTAs and the join of items
+// that several CTAs share. Here a unit is 128 slots, an item 256 queries in two
+// tiles of 128, and an item has only the units that its last row sees: of a
+// prompt's first tokens few. The number of units of item q of a request with g
+// query heads a KV head and the pass's first row in slot p0 is
+//   ceil((p0 + floor((256 q + 255) / g) + 1) / 128) = floor((2 q + C) / g),
+//   C = floor((255 + g (p0 + 128)) / 128),
+// whose sums have a closed form, so a CTA finds its units without a plan.
+//
+// A CTA (one on an SM), twelve warps:
+//   * two times four softmax warps, one tile each, a thread per query: they read
+//     the scores from tensor memory, write the probabilities in their place, and
+//     rescale the output when a row's maximum has outgrown its reference;
+//   * a producer warp, which finds the CTA's pieces of items, tells the other
+//     warps, and brings keys and values, 128 slots at a time, into a ring of
+//     tiles (TMA, 128-byte swizzle);
+//   * an MMA warp: S = Q K^T (queries and keys in shared memory) and O += P V
+//     (probabilities in tensor memory), tile by tile in turn, so that the tensor
+//     cores work on one tile while the other's softmax runs;
+//   * two warps that look through the values of slots that some row does not
+//     see, as a probability 0 times NaN is NaN: slots past the end become 0, and
+//     values that are no finite numbers become 0 as well, while the rows that do
+//     see them become NaN.
+// Tensor memory holds both tiles' O and S (P over S), 512 columns at head
+// dimension 128.
+#pragma once
+
+#include "paged_attn_tc.cuh"
+
+namespace sf {
+namespace pa {
+
+template <int HD, typename TC>
+struct ChunkShape {
+  static constexpr int MT = 256;                        // queries of an item
+  static constexpr int kSlots = 128;                    // of a unit
+  static constexpr int kThreads = 384;
+  // Registers of a softmax thread and of the other warps': 2 x 128 x 216 + 128 x 72 = 384 x 168, the launch's.
+  static constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
+  static constexpr int kHalf = HD / 64;
+  static constexpr int kBox = 128 * 128;                // 128 rows of 64 dimensions
+  static constexpr int kTileBytes = kHalf * kBox;       // of queries, keys or values
+  static constexpr int kStages = HD == 128 ? 5 : 10;
+  static constexpr int kSmem = 1024 + (2 + kStages) * kTileBytes;
+  static constexpr int kO = 0, kS = 2 * HD;             // tensor-memory columns: O of both tiles, S of both
+  // As in TcShape: bounds of a reference's lag and the scale of fp16 probabilities, in powers of two.
+  static constexpr int kLag = std::is_same<TC, __half>::value ? 3 : 8;
+  static constexpr int kUp = std::is_same<TC, __half>::value ? 12 : 0;
+  static constexpr int kFold = 128;                     // units after which O moves to the part (16384 slots, as there)
+  static constexpr int kPiece = 2;                      // units that an item's beginning counts for
+};
+
+// The units of a request's items.
+struct ItemUnits {
+  int g, ntq, last, c1, c0, piece;
+  __device__ __forceinline__ ItemUnits() {}
+  __device__ __forceinline__ ItemUnits(const Args& a, const Request& r) : g(a.group), ntq(r.ntq), piece(a.piece) {
+    const int p0 = max(r.p0, 0);   // (rows in front of slot 0 see nothing and count as if they saw the first slots)
+    const int C = (int)((255 + (long)g * (p0 + 128)) >> 7);
+    c1 = (int)((unsigned)C / (unsigned)g);
+    c0 = C - c1 * g;
+    last = (p0 + r.rows + 127) >> 7;
+  }
+  // Units of item q.
+  __device__ __forceinline__ int of(int q) const {
+    return q == ntq - 1 ? last : c1 + (int)((unsigned)(2 * q + c0) / (unsigned)g);
+  }
+  // Units before item n < ntq of a head, items' beginnings included: the sum
+  // over q < n of floor((2 q + c0) / g) counts for every v >= 1 the q with
+  // 2 q + c0 >= v g.
+  __device__ __forceinline__ long before(int n) const {
+    if (n == 0) return 0;
+    const long M = (unsigned)(2 * (n - 1) + c0) / (unsigned)g;   // the largest term
+    const long odd = g & 1 ? (c0 & 1 ? M / 2 : (M + 1) / 2) : (c0 & 1 ? M : 0);
+    return (long)n * (piece + c1) + M * n - ((g * (M * (M + 1) / 2) - M * c0 + odd) >> 1);
+  }
+  __device__ __forceinline__ long head() const { return ntq > 0 ? before(ntq - 1) + piece + last : 0; }
+  // The item with unit x of a head (by a warp together).
+  __device__ __forceinline__ int find(long x) const {
+    int lo = 0, n = ntq;   // the item lies in lo .. lo + n - 1
+    while (n > 1) {
+      const int step = (n + 31) >> 5, q = lo + step * (int)(threadIdx.x & 31);
+      const unsigned in = __ballot_sync(0xffffffffu, q < lo + n && before(q) <= x);
+      const int k = 31 - __clz(in);
+      n = min(step, n - k * step);
+      lo += k * step;
+    }
+    return lo;
+  }
+};
+
+// Walks the pieces of items that a CTA's units make up (Walk's counterpart).
+struct ChunkWalk {
+  long u;          // units before the next piece
+  long left;       // units of the CTA from there on
+  int b;
+  Request r;
+  ItemUnits iu;
+  int kvh, qt, at; // the item at hand and its units done, its beginning included
+  int t0, t1, nt;  // the piece: units t0 .. t1 - 1 of nt
+  bool open = false;
+  __device__ __forceinline__ bool next(const Args& a) {
+    while (left > 0) {
+      if (r.ntq == 0 || kvh == a.nkv) {
+        r = request<256>(a, ++b);
+        iu = ItemUnits(a, r);
+        kvh = qt = at = 0;
+        continue;
+      }
+      nt = iu.of(qt);
+      const int all = nt + iu.piece, first = at, take = (int)min((long)(all - at), left);
+      const int q = qt, h = kvh;
+      u += take;
+      left -= take;
+      at += take;
+      if (at == all) {
+        at = 0;
+        if (++qt == iu.ntq) {
+          qt = 0;
+          ++kvh;
+        }
+      }
+      if (first + take <= iu.piece) continue;   // (no slots: the item's pieces are the next CTAs')
+      item_q = q;
+      item_h = h;
+      t0 = max(0, first - iu.piece);
+      t1 = first + take - iu.piece;
+      open = t0 == 0 && t1 < nt;
+      return true;
+    }
+    return false;
+  }
+  int item_q, item_h;   // query tile and KV head of the piece
+};
+
+// Where a CTA's units begin: all threads of the CTA together.
+template <int NT>
+__device__ __forceinline__ ChunkWalk chunk_walk(const Args& a, long* sh, Deal& deal) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  constexpr int NW = NT / 32;
+  const int per = (a.B + NT - 1) / NT;
+  const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
+  long mine = 0;
+  for (int b = b0; b < b1; ++b) mine += a.nkv * ItemUnits(a, request<256>(a, b)).head();
+  long incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long x = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += x;
+  }
+  if (lane == 31) sh[warp] = incl;
+  __syncthreads();
+  long before = 0, T = 0;
+#pragma unroll
+  for (int w = 0; w < NW; ++w) {
+    if (w < warp) before += sh[w];
+    T += sh[w];
+  }
+  const long G = min((long)gridDim.x, T);
+  deal = Deal(max(T, 1l), max(G, 1l));
+  const bool idle = (long)blockIdx.x >= G;
+  const long u0 = idle ? -1 : deal.first(blockIdx.x);
+  const long lo = before + incl - mine;
+  if (u0 >= lo && u0 < lo + mine) {
+    long base = lo;
+    for (int b = b0; b < b1; ++b) {
+      const long n = a.nkv * ItemUnits(a, request<256>(a, b)).head();
+      if (u0 < base + n) {
+        sh[NW] = base;
+        sh[NW + 1] = b;
+        break;
+      }
+      base += n;
+    }
+  }
+  __syncthreads();
+  ChunkWalk w;
+  w.u = max(u0, 0l);
+  w.left = 0;
+  w.b = 0;
+  if (!idle) {
+    w.left = deal.first(blockIdx.x + 1) - u0;
+    w.b = (int)sh[NW + 1];
+    w.r = request<256>(a, w.b);
+    w.iu = ItemUnits(a, w.r);
+    const long rest = u0 - sh[NW], head = w.iu.head();
+    w.kvh = (int)Deal::div(rest, head);
+    w.qt = w.iu.find(rest - w.kvh * head);
+    w.at = (int)(rest - w.kvh * head - w.iu.before(w.qt));
+  }
+  return w;
+}
+
+// A piece of an item as the producer warp hands it to the others.
+struct Piece {
+  int s0, rows, len, p0;   // of the request
+  int kvh, q;              // KV head, query tile
+  int t0, t1;              // units; none: there are no more pieces
+  int whole;               // all of the item's units
+};
+// The ring of tiles lets the producer be at most six units ahead, so as many pieces.
+constexpr int kPieces = 16, kChecks = 8;
+
+// The join's descriptor of an item that begins in this CTA (one thread).
+__device__ __forceinline__ void describe(const Args& a, const ChunkWalk& w, const Deal& deal, bool whole) {
+  const int c1 = whole ? (int)blockIdx.x : deal.cta_of(w.u - w.t1 + w.nt - 1);
+  const int4 d = make_int4(blockIdx.x, c1 - (int)blockIdx.x + 1, w.b, w.item_h * w.r.ntq + w.item_q);
+  if (a.by_item) a.desc[((long)w.b * a.nkv + w.item_h) * a.ntq_max + w.item_q] = d;
+  else if (!whole) a.desc[blockIdx.x] = d;
+}
+
+// Pairs of fp32 numbers at once.
+__device__ __forceinline__ uint64_t pair(float x, float y) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(__float_as_uint(x)), "r"(__float_as_uint(y)));
+  return d;
+}
+__device__ __forceinline__ float2 unpair(uint64_t d) {
+  uint32_t x, y;
+  asm("mov.b64 {%0, %1}, %2;" : "=r"(x), "=r"(y) : "l"(d));
+  return make_float2(__uint_as_float(x), __uint_as_float(y));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+
+// As wait, without a call (setmaxnreg's register counts allow none).
+__device__ __forceinline__ bool poll(uint64_t* bar, uint32_t parity) { return mbar_wait(bar, parity, kWaitPolls); }
+
+template <int HD, typename TC>
+__global__ void __launch_bounds__(ChunkShape<HD, TC>::kThreads, 1) k_chunk_attn(const __grid_constant__ Args a) {
+  using S = ChunkShape<HD, TC>;
+  constexpr int NS = S::kStages, SL = S::kSlots;
+  extern __shared__ unsigned char pa_smem_raw[];
+  unsigned char* const qbuf = pa_smem_raw + ((1024 - (smem_u32(pa_smem_raw) & 1023)) & 1023);   // both tiles' queries
+  unsigned char* const ring = qbuf + 2 * S::kTileBytes;
+  __shared__ long sh_loc[S::kThreads / 32 + 2];
+  // full: a tile of the ring has landed; empty: it may be loaded anew; checked: a unit's values may be used.
+  __shared__ __align__(8) uint64_t full[NS], empty[NS], checked[kChecks], q_full[2], s_full[2], p_full[2], o_done[2], drain;
+  __shared__ __align__(8) uint64_t piece_full[kPieces];
+  __shared__ Piece s_piece[kPieces];
+  __shared__ int s_odd[kPieces];   // the first slot with a value that is no finite number, among those looked at
+  __shared__ uint32_t s_tmem;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) {
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int i = 0; i < kChecks; ++i) mbar_init(&checked[i], 2);
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&q_full[x], 4);
+      mbar_init(&s_full[x], 1);
+      mbar_init(&p_full[x], 4);
+      mbar_init(&o_done[x], 1);
+    }
+    for (int i = 0; i < kPieces; ++i) mbar_init(&piece_full[i], 1);
+    mbar_init(&drain, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  } else if (warp == 8 && lane < 2) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(lane ? &a.vm : &a.km)) : "memory");
+  }
+  if (tid < kPieces) s_odd[tid] = INT32_MAX;
+  if (warp == 9) {
+    tmem_alloc(&s_tmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+  pdl_wait();
+  pdl_launch_next();
+  Deal deal(1, 1);
+  ChunkWalk w = chunk_walk<S::kThreads>(a, sh_loc, deal);   // (the producer warp's from here on)
+  bool ok = true;
+  // Piece i of the CTA, for the other warps; no units at the end.
+  auto piece_at = [&](int i) {
+    if (ok && !poll(&piece_full[i % kPieces], i / kPieces & 1)) ok = false;
+    ok = __all_sync(0xffffffffu, ok);
+    Piece p = s_piece[i % kPieces];
+    if (!ok) p.t1 = p.t0 = 0;
+    return p;
+  };
+
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kOtherRegs));
+    if (warp == 8) {
+      // -------------------------------------------------------- producer warp
+      const int bp = min(1 << a.shift, SL);           // slots of a box
+      const int np = SL / bp;                         // boxes of a column
+      const int i = lane % np, h = lane / np;         // this lane's box of a tile: np * kHalf <= 16 lanes
+      const uint32_t dst0 = smem_u32(ring) + h * S::kBox + i * bp * 128;
+      const uint64_t policy = policy_evict_normal();
+      int win_b = -1, win = -1, entry = 0;            // the 32 table entries at hand, one per lane
+      int s = 0, phase = 1, loaded = 0;               // (a new barrier's phase 1 counts as past)
+      int piece = 0;
+      while (true) {
+        const bool more = ok && w.next(a);
+        if (lane == 0) {
+          const bool whole = more && w.t0 == 0 && w.t1 == w.nt;
+          s_piece[piece % kPieces] = more ? Piece{w.r.s0, w.r.rows, w.r.len, w.r.p0, w.item_h, w.item_q, w.t0, w.t1, whole}
+                                          : Piece{};
+          mbar_arrive(&piece_full[piece % kPieces]);
+          if (more && w.t0 == 0) describe(a, w, deal, whole);
+        }
+        ++piece;
+        if (!more) break;
+        for (int t = w.t0; ok && t < w.t1; ++t) {
+          const int first = (t * SL) >> a.shift;
+          if (w.b != win_b || (first >> 5) != win) {
+            win_b = w.b;
+            win = first >> 5;
+            const int e = 32 * win + lane;
+            entry = e < a.W ? a.tables[(long)w.b * a.W + e] : -1;
+          }
+          const int left = w.r.len - t * SL;          // slots from here on
+          const int nb = max(0, min(np, (left + bp - 1) / bp));
+          const int page = __shfl_sync(0xffffffffu, entry, (first + i) & 31);
+          const int off = (t * SL) & ((1 << a.shift) - 1);
+#pragma unroll
+          for (int v = 0; v < 2; ++v) {               // keys, then values
+            ok = __all_sync(0xffffffffu, poll(&empty[s], phase));
+            if (!ok) break;
+            if (lane == 0) mbar_expect_tx(&full[s], nb * bp * 128 * S::kHalf);
+            __syncwarp();
+            const int nhd = v ? a.v_nhd : a.k_nhd;
+            if (h < S::kHalf && i < nb)
+              tma_load_4d(dst0 + s * S::kTileBytes, v ? &a.vm : &a.km, 64 * h, nhd ? w.item_h : off,
+                          nhd ? off : w.item_h, page, &full[s], policy);
+            ++loaded;
+            if (++s == NS) s = 0, phase ^= 1;
+          }
+        }
+      }
+      if (lane == 0 && !a.by_item && !w.open) a.desc[blockIdx.x] = make_int4(0, 0, 0, 0);   // no item begins here that others share
+      // An expired wait: the copies in flight land before the CTA may end.
+      if (!ok)
+        for (int k = max(0, loaded - NS); k < loaded; ++k) poll(&full[k % NS], (k / NS) & 1);
+    } else if (warp == 9) {
+      // ------------------------------------------------------------- MMA warp
+      // (control flow and descriptors the same in all lanes, one lane issues: as in k_paged_attn_tc)
+      constexpr uint32_t id_s = tc_idesc<TC>(128, SL, false), id_o = tc_idesc<TC>(128, HD, true);
+      const uint32_t utmem = __shfl_sync(0xffffffffu, tmem, 0);
+      const uint64_t dq = sw128_desc(__shfl_sync(0xffffffffu, smem_u32(qbuf), 0));
+      const uint64_t dk = sw128_desc(__shfl_sync(0xffffffffu, smem_u32(ring), 0));
+      const uint64_t dv = sw128_desc_mn(__shfl_sync(0xffffffffu, smem_u32(ring), 0), S::kBox);
+      bool good = true;
+      auto await = [&](uint64_t* bar, uint32_t parity) {
+        if (good) good = __all_sync(0xffffffffu, poll(bar, parity));
+      };
+      // S of tile x with the keys in stage s; the last tile frees the stage.
+      auto scores = [&](int x, int s, bool last) {
+        const uint64_t q = dq + (uint64_t)(x * (S::kTileBytes >> 4)), d = dk + (uint64_t)(s * (S::kTileBytes >> 4));
+        if (good && elect_one()) {
+#pragma unroll
+          for (int k = 0; k < HD / 16; ++k) {
+            const uint64_t o = ((k >> 2) * S::kBox + 32 * (k & 3)) >> 4;
+            umma_bf16(utmem + S::kS + SL * x, q + o, d + o, id_s, k > 0);
+          }
+          umma_commit(&s_full[x]);
+          if (last) umma_commit(&empty[s]);
+        }
+        __syncwarp();
+      };
+      // O of tile x += P V with the values in stage s.
+      auto output = [&](int x, int s, uint32_t keep, bool last, bool end) {
+        const uint64_t d = dv + (uint64_t)(s * (S::kTileBytes >> 4));
+        if (good && elect_one()) {
+#pragma unroll
+          for (int k = 0; k < SL / 16; ++k)
+            umma_bf16_tmem_a(utmem + S::kO + HD * x, utmem + S::kS + SL * x + 8 * k, d + (2048 * k >> 4), id_o,
+                             k > 0 ? 1u : keep);
+          if (last) umma_commit(&empty[s]);
+          if (end) umma_commit(&o_done[x]);
+        }
+        __syncwarp();
+      };
+      int s = 0, phase = 0, n = 0;                  // stage, units
+      uint32_t piece[2] = {0, 0}, done[2] = {0, 0};   // parities of each tile's next piece and unit
+      auto advance = [&] { if (++s == NS) s = 0, phase ^= 1; };
+      for (int i = 0; good; ++i) {
+        const Piece w = piece_at(i);
+        const int units = __shfl_sync(0xffffffffu, w.t1 - w.t0, 0);
+        if (units == 0) break;
+        const int tiles = __shfl_sync(0xffffffffu, w.rows * a.group - w.q * 256 > 128 ? 2 : 1, 0);
+        await(&full[s], phase);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          if (x == tiles) break;
+          await(&q_full[x], piece[x]);
+          piece[x] ^= 1;
+          tc_fence_after();
+          scores(x, s, x == tiles - 1);
+        }
+        advance();
+        for (int u = 0; u < units; ++u, ++n) {
+          const int sv = s;
+          advance();
+          await(&checked[n % kChecks], n / kChecks & 1);
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            if (x == tiles) break;
+            await(&p_full[x], done[x]);
+            done[x] ^= 1;
+            tc_fence_after();
+            output(x, sv, u % S::kFold ? 1u : 0u, x == tiles - 1, u == units - 1);
+            if (u + 1 < units) {
+              if (x == 0) await(&full[s], phase);
+              scores(x, s, x == tiles - 1);
+            }
+          }
+          if (u + 1 < units) advance();
+        }
+      }
+      if (!good) {   // an expired wait: what was issued ends before the CTA does
+        if (elect_one()) umma_commit(&drain);
+        poll(&drain, 0);
+      }
+      __syncwarp();
+    } else {
+      // ------------------------------------------- warps that look at values
+      constexpr int PP = HD / 8;                      // 16-byte pieces of a slot
+      constexpr uint32_t X = Num<TC>::kExp;
+      const int me = tid - 320;                       // 0 .. 63
+      int s = 1, phase = 0, n = 0;                    // (keys in one stage, values in the next)
+      for (int piece = 0; ok; ++piece) {
+        const Piece w = piece_at(piece);
+        if (w.t1 == 0) break;
+        if (me == 0) s_odd[(piece + 8) % kPieces] = INT32_MAX;   // (nobody is that many pieces behind)
+        // From slot `seen` on some row of the item does not see a slot.
+        const int seen = w.p0 + w.q * 256 / a.group + 1;
+        for (int t = w.t0; t < w.t1; ++t, ++n) {
+          if (ok && !poll(&full[s], phase)) ok = false;
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          const int s0 = min(max(seen - t * SL, 0), SL), s1 = min(max(w.len - t * SL, 0), SL);
+          if (s0 < SL) {
+            unsigned char* vs = ring + s * S::kTileBytes;
+            auto at = [&](int sl, int p) {            // in any order within a slot
+              return reinterpret_cast<uint4*>(vs + (p >> 3) * S::kBox + sl * 128 + (p & 7) * 16);
+            };
+            auto bad = [](uint32_t v) { return (v & X) == X || (v >> 16 & X) == X; };
+            auto clean = [](uint32_t v) { return ((v & X) == X ? 0u : v & 0xffffu) | ((v >> 16 & X) == X ? 0u : v & 0xffff0000u); };
+            int odd = INT32_MAX;
+#pragma unroll 4
+            for (int e = s0 * PP + me; e < s1 * PP; e += 64) {
+              uint4* const p = at(e / PP, e % PP);
+              const uint4 v = *p;
+              if (bad(v.x) || bad(v.y) || bad(v.z) || bad(v.w)) {
+                *p = make_uint4(clean(v.x), clean(v.y), clean(v.z), clean(v.w));
+                odd = min(odd, t * SL + e / PP);
+              }
+            }
+            if (odd != INT32_MAX) atomicMin(&s_odd[piece % kPieces], odd);
+            for (int e = s1 * PP + me; e < SL * PP; e += 64) *at(e / PP, e % PP) = make_uint4(0u, 0u, 0u, 0u);
+            fence_proxy_async();
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&checked[n % kChecks]);
+          s += 2;
+          if (s >= NS) s -= NS, phase ^= 1;
+        }
+      }
+    }
+  } else {
+    // ----------------------------------------------------------- softmax warps
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::kSoftmaxRegs));
+    const int x = warp >> 2, row = tid & 127;                 // the tile, and the query of it = tensor-memory lane
+    const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+    const uint32_t t_s = lanes + S::kS + SL * x, t_o = lanes + S::kO + HD * x;
+    unsigned char* const qs = qbuf + x * S::kTileBytes;
+    int n = 0, my_pieces = 0;                                 // units and pieces of this tile
+    auto s_wait = [&] {
+      if (ok && !poll(&s_full[x], n & 1)) ok = false;
+      ok = __all_sync(0xffffffffu, ok);
+      tc_fence_after();
+    };
+    // The piece's queries into shared memory (rows past the end: zeros).
+    auto load_queries = [&](const Piece& w) {
+      constexpr int PP = HD / 8, RW = 32 / PP;                // pieces of a row, rows of a load
+      constexpr long kNone = INT64_MIN;
+      const int q = w.q * 256 + 128 * x + row, j = q / a.group, hh = w.kvh * a.group + q - j * a.group;
+      const long off = q < w.rows * a.group ? (w.s0 + j) * a.q_row + hh * a.q_head : kNone;
+      const int p = lane % PP;
+#pragma unroll 4
+      for (int i = 0; i < 32 / RW; ++i) {
+        const int rr = RW * i + lane / PP;
+        const long o = __shfl_sync(0xffffffffu, off, rr);
+        uint4 f = make_uint4(0u, 0u, 0u, 0u);
+        if (o != kNone) f = *reinterpret_cast<const uint4*>(static_cast<const TC*>(a.q) + o + 8 * p);
+        f.x ^= a.flip, f.y ^= a.flip, f.z ^= a.flip, f.w ^= a.flip;
+        const int r = 32 * (warp & 3) + rr;
+        *reinterpret_cast<uint4*>(qs + (p >> 3) * S::kBox + r * 128 + (((p & 7) ^ (r & 7)) << 4)) = f;
+      }
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&q_full[x]);
+    };
+    // The next piece with queries for this tile, its queries on their way.
+    int i = 0;
+    auto next_piece = [&] {
+      while (true) {
+        const Piece p = piece_at(i);
+        if (p.t1 == 0) return p;
+        if (p.rows * a.group - p.q * 256 > 128 * x) {
+          load_queries(p);
+          return p;
+        }
+        ++i;
+      }
+    };
+    for (Piece w = next_piece(); w.t1 != 0;) {
+      const int q = w.q * 256 + 128 * x + row, j = q / a.group, hh = w.kvh * a.group + q - j * a.group;
+      const int Mq = w.rows * a.group;
+      const bool live = q < Mq, warp_live = (q & ~31) < Mq;
+      const int out_row = w.s0 + j;
+      const int lim = live ? w.p0 + j + 1 : INT32_MAX;      // slots that the row sees (0 .. lim - 1)
+      const int lim_warp = __shfl_sync(0xffffffffu, lim, 0);  // (the least: rows see more and more)
+      const int t0 = w.t0, t1 = w.t1;
+      const bool whole = w.whole;
+      const long slot = 2l * blockIdx.x + (t0 == 0 ? 1 : 0);
+      float* const part = a.part + (slot * a.mt_max + 128 * x + row) * HD;     // (of a live row)
+      float2* const part_ml = a.part_ml + slot * a.mt_max + 128 * x + row;
+      float m = -INFINITY, l = 0.f;
+      bool folded = false;                                    // the part holds sums
+      auto unit = [&](int t) {
+        s_wait();
+        if (warp_live) {
+          uint32_t v[SL];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld32(t_s + 32 * c, v + 32 * c);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < SL; ++i) asm volatile("" : "+r"(v[i]));   // (read behind the wait only)
+          // ---- what the row does not see is -infinity
+          if ((t + 1) * SL > lim_warp) {
+            const int vis = lim - t * SL;
+#pragma unroll
+            for (int i = 0; i < SL; ++i)
+              if (i >= vis) v[i] = 0xff800000u;
+          }
+          // ---- maximum; a new reference when it has outgrown the old one
+          float mx4[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) mx4[i] = fmaxf(__uint_as_float(v[i]), __uint_as_float(v[i + 4]));
+#pragma unroll
+          for (int i = 8; i < SL; i += 8)
+#pragma unroll
+            for (int y = 0; y < 4; ++y) mx4[y] = fmaxf(fmaxf(mx4[y], __uint_as_float(v[i + y])), __uint_as_float(v[i + y + 4]));
+          const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
+          const bool grow = m != -INFINITY && (mx - m) * a.scale2 > (float)S::kLag;
+          if (__any_sync(0xffffffffu, grow)) {                // (each row by itself: its result does not depend on the others)
+            const float f = grow ? exp2_approx((m - mx) * a.scale2) : 1.f;
+            if (grow) m = mx;
+            l *= f;
+#pragma unroll 1
+            for (int c = 0; c < HD / 16; ++c) {
+              uint32_t o[16];
+              tmem_ld16(t_o + 16 * c, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                asm volatile("" : "+r"(o[i]));
+                o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+              }
+              tmem_st16(t_o + 16 * c, o);
+            }
+            tmem_st_wait();
+          }
+          if (m == -INFINITY) m = mx;                         // (what came before saw nothing: O is 0)
+          const float ref = m == -INFINITY ? 0.f : fmaf(-m, a.scale2, (float)S::kUp);
+          const uint64_t sc2 = pair(a.scale2, a.scale2), ref2 = pair(ref, ref);
+          uint64_t l2[4] = {0, 0, 0, 0};
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            uint32_t p[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const int e = 64 * c + 2 * i;
+              const float2 y = unpair(fma2(pair(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), sc2, ref2));
+              const float p0 = exp2_approx(y.x), p1 = exp2_approx(y.y);
+              l2[i & 3] = add2(l2[i & 3], pair(p0, p1));
+              p[i] = Num<TC>::pack(p0, p1);
+            }
+            tmem_st32(t_s + 32 * c, p);
+          }
+          const float2 ls = unpair(add2(add2(l2[0], l2[1]), add2(l2[2], l2[3])));
+          l += ls.x + ls.y;
+          tmem_st_wait();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[x]);
+        ++n;
+      };
+      // Between two units: O and l move to the part (`first`: which holds
+      // nothing yet), whose reference may be an older maximum.
+      auto fold = [&](bool first) {
+        s_wait();   // (the next unit's scores lie behind the last output)
+        const float2 ml = live && !first ? *part_ml : make_float2(-INFINITY, 0.f);
+        const float f = ml.x == -INFINITY ? 0.f : exp2_approx((ml.x - m) * a.scale2);
+        if (live) *part_ml = make_float2(m, fmaf(ml.y, f, l));
+        l = 0.f;
+        if (warp_live) {
+#pragma unroll 1
+          for (int c = 0; c < HD / 16; ++c) {
+            uint32_t o[16];
+            tmem_ld16(t_o + 16 * c, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(o[i]));
+            if (live) {
+#pragma unroll
+              for (int i = 0; i < 16; i += 4) {
+                float4* const p = reinterpret_cast<float4*>(part + 16 * c + i);
+                const float4 y = first ? make_float4(0.f, 0.f, 0.f, 0.f) : *p;
+                *p = make_float4(fmaf(y.x, f, __uint_as_float(o[i])), fmaf(y.y, f, __uint_as_float(o[i + 1])),
+                                 fmaf(y.z, f, __uint_as_float(o[i + 2])), fmaf(y.w, f, __uint_as_float(o[i + 3])));
+              }
+            }
+            __syncwarp();
+          }
+        }
+      };
+#pragma unroll 1
+      for (int t = t0; t < t1; ++t) {
+        if ((t - t0) % S::kFold == 0 && t > t0) {
+          fold(!folded);
+          folded = true;
+        }
+        unit(t);
+      }
+      // ---- the next piece's queries (the scores have been read, so these have too)
+      const int odd_at = i++ % kPieces;
+      w = next_piece();
+
+      // ---- the end of the piece
+      if (ok && !poll(&o_done[x], my_pieces & 1)) ok = false;
+      ok = __all_sync(0xffffffffu, ok);
+      tc_fence_after();
+      ++my_pieces;
+      float f = 0.f;                                          // of what lies in the part
+      if (folded && live) {
+        const float2 ml = *part_ml;
+        f = ml.x == -INFINITY ? 0.f : exp2_approx((ml.x - m) * a.scale2);
+        l = fmaf(ml.y, f, l);
+      }
+      if (!ok || s_odd[odd_at] < lim) l = __int_as_float(0x7fc00000);   // an expired wait, a value that is no number: NaN
+      if (m != -INFINITY) m = fmaf(m, a.scale2, (float)-S::kUp);
+      if (warp_live) {
+        const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+        TC* dst = static_cast<TC*>(a.out) + out_row * a.o_row + hh * a.o_head;
+#pragma unroll 1
+        for (int c = 0; c < HD / 32; ++c) {
+          uint32_t o[32];
+          __syncwarp();
+          tmem_ld32(t_o + 32 * c, o);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(o[i]));
+          if (!live) continue;
+          if (folded) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) {
+              const float4 y = *reinterpret_cast<const float4*>(part + 32 * c + i);
+              o[i] = __float_as_uint(fmaf(y.x, f, __uint_as_float(o[i])));
+              o[i + 1] = __float_as_uint(fmaf(y.y, f, __uint_as_float(o[i + 1])));
+              o[i + 2] = __float_as_uint(fmaf(y.z, f, __uint_as_float(o[i + 2])));
+              o[i + 3] = __float_as_uint(fmaf(y.w, f, __uint_as_float(o[i + 3])));
+            }
+          }
+          // (a row that saw nothing: l = 0 and O = 0)
+          if (whole) {
+            uint32_t y[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              y[i] = Num<TC>::pack(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);
+#pragma unroll
+            for (int i = 0; i < 16; i += 4)
+              *reinterpret_cast<uint4*>(dst + 32 * c + 2 * i) = make_uint4(y[i], y[i + 1], y[i + 2], y[i + 3]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; i += 4)
+              *reinterpret_cast<uint4*>(part + 32 * c + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+          }
+        }
+        if (live && whole && a.lse)
+          a.lse[(long)out_row * a.nq + hh] = l == 0.f ? -INFINITY : m * 0.693147180559945f + logf(l);
+        if (live && !whole) *part_ml = make_float2(m, l);
+      }
+      tc_fence_before();   // O has been read: the next piece's first product may replace it
+    }
+    if (!ok && lane == 0) report_err(a.err, kErrWait);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+}  // namespace pa
+}  // namespace sf

@@ -26,9 +26,10 @@ static Layout layout(int n_heads, int n_kv_heads, int head_dim, int max_rows) { 
 }
 
 // Tensor map of the keys or values, {head_dim, slots, heads, pages}: the
-// two middle dimensions by ascending stride (*nhd: the heads come first).
+// two middle dimensions by ascending stride (*nhd: the heads come first). A box
+// holds up to `unit` slots of a page.
 static cudaError_t cache_map(CUtensorMap* map, int* nhd, const sf_paged_cache& c, const void* base, int64_t s_page,
-                             int64_t s_head, int64_t s_slot) {
+                             int64_t s_head, int64_t s_slot, int unit) {
   typedef CUresult (*encode_fn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -47,7 +48,7 @@ static cudaError_t cache_map(CUtensorMap* map, int* nhd, const sf_paged_cache& c
   if (c.n_kv_heads == 1) s_head = std::max<int64_t>(s_slot, c.head_dim) * c.page;
   if (c.n_pages == 1) s_page = std::max(s_head * c.n_kv_heads, s_slot * c.page);
   *nhd = c.n_kv_heads > 1 && s_head < s_slot;
-  const cuuint32_t bp = std::min(c.page, kTile);
+  const cuuint32_t bp = std::min(c.page, unit);
   cuuint64_t dims[4] = {(cuuint64_t)c.head_dim, (cuuint64_t)c.page, (cuuint64_t)c.n_kv_heads, (cuuint64_t)c.n_pages};
   cuuint64_t strides[3] = {(cuuint64_t)s_slot * 2, (cuuint64_t)s_head * 2, (cuuint64_t)s_page * 2};
   cuuint32_t box[4] = {64, bp, 1, 1};
@@ -107,11 +108,10 @@ static bool units_fit(const sf_paged_cache& c, int n_heads, int max_rows, int q_
   return c.n_kv_heads * (long)z.ntq * (z.units + kMaxPiece) <= INT32_MAX;
 }
 
-// Enqueue a checked call: `a` holds rows, tables and lengths.
-static cudaError_t enqueue(Args& a, const sf_paged_cache& c, int q_dtype, float scale, void* workspace, int sms,
-                           cudaStream_t st) {
-  cudaError_t e = cache_map(&a.km, &a.k_nhd, c, c.k, c.k_page, c.k_head, c.k_slot);
-  if (e == cudaSuccess) e = cache_map(&a.vm, &a.v_nhd, c, c.v, c.v_page, c.v_head, c.v_slot);
+// What the kernels are told of the cache and the scale; a CTA's unit has `unit` slots.
+static cudaError_t describe_cache(Args& a, const sf_paged_cache& c, int q_dtype, float scale, int unit) {
+  cudaError_t e = cache_map(&a.km, &a.k_nhd, c, c.k, c.k_page, c.k_head, c.k_slot, unit);
+  if (e == cudaSuccess) e = cache_map(&a.vm, &a.v_nhd, c, c.v, c.v_page, c.v_head, c.v_slot, unit);
   if (e != cudaSuccess) return e;
   a.nkv = c.n_kv_heads;
   a.group = a.nq / a.nkv;
@@ -119,6 +119,14 @@ static cudaError_t enqueue(Args& a, const sf_paged_cache& c, int q_dtype, float 
   // (never 0: the mask's -infinity times 0 would be NaN)
   a.scale2 = std::max(std::fabs(scale) * 1.44269504088896f, FLT_TRUE_MIN);
   a.flip = scale >= 0.f ? 0u : q_dtype == SF_DT_F32 ? 0x80000000u : 0x80008000u;
+  return cudaSuccess;
+}
+
+// Enqueue a checked call: `a` holds rows, tables and lengths.
+static cudaError_t enqueue(Args& a, const sf_paged_cache& c, int q_dtype, float scale, void* workspace, int sms,
+                           cudaStream_t st) {
+  const cudaError_t e = describe_cache(a, c, q_dtype, scale, kTile);
+  if (e != cudaSuccess) return e;
   const Sizes z = sizes(c, a.nq, a.max_rows, q_dtype, a.B, a.W, sms);
   a.mt = z.mt;
   a.mt_max = std::min(a.max_rows * a.group, a.mt);
@@ -133,6 +141,37 @@ static cudaError_t enqueue(Args& a, const sf_paged_cache& c, int q_dtype, float 
   a.by_warp = a.B <= 32 && max_units + kMaxPiece * z.items <= INT32_MAX;
   sms = std::min(sms, kMaxCtas / 2);
   return c.head_dim == 128 ? launch_hd128(a, q_dtype, sms, max_units, st) : launch_hd64(a, q_dtype, sms, max_units, st);
+}
+
+// The same with the kernel for chunks (16-bit queries): items of 256 queries,
+// units of 128 slots, one CTA an SM (half as many, of twice the queries: the
+// workspace's layout is the same).
+constexpr int kChunkQueries = 256, kChunkUnit = 128;
+static cudaError_t enqueue_chunk(Args& a, const sf_paged_cache& c, int q_dtype, float scale, void* workspace, int sms,
+                                 cudaStream_t st) {
+  const cudaError_t e = describe_cache(a, c, q_dtype, scale, kChunkUnit);
+  if (e != cudaSuccess) return e;
+  const long queries = (long)a.max_rows * a.group;
+  a.mt = kChunkQueries;
+  a.mt_max = (int)std::min<long>(queries, kChunkQueries);
+  a.ntq_max = (int)((queries + kChunkQueries - 1) / kChunkQueries);
+  const long items = (long)a.B * a.nkv * a.ntq_max;
+  a.by_item = items <= kMaxDesc;
+  const Layout lay = layout(a.nq, a.nkv, c.head_dim, a.max_rows);
+  unsigned char* ws = static_cast<unsigned char*>(workspace);
+  a.desc = reinterpret_cast<int4*>(ws);
+  a.part_ml = reinterpret_cast<float2*>(ws + lay.ml);
+  a.part = reinterpret_cast<float*>(ws + lay.part);
+  const long max_units = items * (((long)a.W * c.page + kChunkUnit - 1) / kChunkUnit);
+  sms = std::min(sms, kMaxCtas / 2);
+  return c.head_dim == 128 ? launch_chunk_hd128(a, q_dtype, sms, max_units, st)
+                           : launch_chunk_hd64(a, q_dtype, sms, max_units, st);
+}
+// The kernel counts a request's units as (group * slots) / 128 and its items in 32 bits.
+static bool chunk_fits(const sf_paged_cache& c, int n_heads, int max_rows, int table_width) {
+  const long group = n_heads / c.n_kv_heads;
+  return group * ((long)table_width * c.page + kChunkUnit) < 1l << 37 &&
+         c.n_kv_heads * (max_rows * group / kChunkQueries + 1) <= INT32_MAX;
 }
 
 __global__ void k_tree_mask(unsigned long long* mask, int n, int rows, int g) {
@@ -235,9 +274,13 @@ static sf_status attention(const char* who, int most_rows, const sf_paged_cache*
   a.tables = d_tables, a.lens = d_lens, a.starts = d_starts;
   a.mask = reinterpret_cast<const unsigned long long*>(d_mask);
   a.B = batch, a.N = n, a.W = table_width, a.nq = q->n_heads, a.max_rows = max_rows, a.rows_each = n / batch;
-  if (!pa::units_fit(*cache, q->n_heads, max_rows, q->dtype, batch, table_width, sms))
+  const bool chunk = most_rows == kMaxChunk && q->dtype != SF_DT_F32;
+  if (chunk ? !pa::chunk_fits(*cache, q->n_heads, max_rows, table_width)
+            : !pa::units_fit(*cache, q->n_heads, max_rows, q->dtype, batch, table_width, sms))
     return set_error(SF_ERR_UNSUPPORTED, "%s: table_width * page too large for this many heads and rows", who);
-  if (e == cudaSuccess) e = pa::enqueue(a, *cache, q->dtype, scale, d_workspace, sms, static_cast<cudaStream_t>(cuda_stream));
+  if (e == cudaSuccess)
+    e = (chunk ? pa::enqueue_chunk : pa::enqueue)(a, *cache, q->dtype, scale, d_workspace, sms,
+                                                  static_cast<cudaStream_t>(cuda_stream));
   if (e != cudaSuccess) return set_error(SF_ERR_CUDA, "%s: %s", who, cudaGetErrorString(e));
   return SF_OK;
 }

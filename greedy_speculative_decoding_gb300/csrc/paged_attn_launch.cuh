@@ -86,6 +86,8 @@ cudaError_t launch_types(Args& a, int q_dtype, int sms, long max_units, cudaStre
 
 cudaError_t launch_hd64(Args& a, int q_dtype, int sms, long max_units, cudaStream_t st);
 cudaError_t launch_hd128(Args& a, int q_dtype, int sms, long max_units, cudaStream_t st);
+cudaError_t launch_chunk_hd64(Args& a, int dtype, int sms, long max_units, cudaStream_t st);
+cudaError_t launch_chunk_hd128(Args& a, int dtype, int sms, long max_units, cudaStream_t st);
 
 }  // namespace pa
 }  // namespace sf

@@ -158,7 +158,11 @@ def test_masked_nan_and_inf_change_nothing(pkg, dq, dc, hd, bad):
         c["k"][pg, :, off, 9] = bad
         last = c["starts"][b + 1]
         first[row0:last] = False
-    check(clean, *call(pkg, c), rows=first)
+    out, lse = call(pkg, c)
+    check(clean, out, lse, rows=first)
+    if dq != F4:                                                # (fp32: another row's new maximum may move a rounding)
+        ref, ref_lse = call(pkg, clean)
+        assert torch.equal(out[first], ref[first]) and torch.equal(lse[first], ref_lse[first])
 
 
 @pytest.mark.parametrize("dq,dc", TYPES)
