@@ -20,7 +20,14 @@
 //     tiles (TMA, 128-byte swizzle);
 //   * an MMA warp: S = Q K^T (queries and keys in shared memory) and O += P V
 //     (probabilities in tensor memory), tile by tile in turn, so that the tensor
-//     cores work on one tile while the other's softmax runs;
+//     cores work on one tile while the other's softmax runs. Their queue holds
+//     about four MMAs (256 cycles), so what happens between two of them counts:
+//     with the whole warp in the loop, one lane elected for every few MMAs, a
+//     wait takes 130 to 160 cycles even when there is nothing to wait for, and
+//     two tiles' 32 MMAs and four waits 2200 to 2500 cycles; with the loop in
+//     one lane, 2048, which is the tensor cores' rate. (A warp for each tile:
+//     the tiles' products mix, both end together, and the tensor cores idle
+//     through both softmaxes.)
 //   * two warps that look through the values of slots that some row does not
 //     see, as a probability 0 times NaN is NaN: slots past the end become 0, and
 //     values that are no finite numbers become 0 as well, while the rows that do
@@ -245,8 +252,14 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
       : "r"(taddr));
 }
 
-// As wait, without a call (setmaxnreg's register counts allow none).
-__device__ __forceinline__ bool poll(uint64_t* bar, uint32_t parity) { return mbar_wait(bar, parity, kWaitPolls); }
+// As wait, without a call (setmaxnreg's register counts allow none), for a
+// converged warp; once a wait has run out (ok false) no further one is begun.
+// The lanes do not vote on it: that would cost 100 cycles a wait. Whoever gave up
+// goes on without waiting to the end of the piece and leaves NaN.
+__device__ __forceinline__ void await(bool& ok, uint64_t* bar, uint32_t parity) {
+  if (ok) ok = mbar_wait(bar, parity, kWaitPolls);
+  __syncwarp();
+}
 
 template <int HD, typename TC>
 __global__ void __launch_bounds__(ChunkShape<HD, TC>::kThreads, 1) k_chunk_attn(const __grid_constant__ Args a) {
@@ -257,11 +270,12 @@ __global__ void __launch_bounds__(ChunkShape<HD, TC>::kThreads, 1) k_chunk_attn(
   unsigned char* const ring = qbuf + 2 * S::kTileBytes;
   __shared__ long sh_loc[S::kThreads / 32 + 2];
   // full: a tile of the ring has landed; empty: it may be loaded anew; checked: a unit's values may be used.
-  __shared__ __align__(8) uint64_t full[NS], empty[NS], checked[kChecks], q_full[2], s_full[2], p_full[2], o_done[2], drain;
+  __shared__ __align__(8) uint64_t full[NS], empty[NS], checked[kChecks], q_full[2], s_full[2], p_full[2][2], o_done[2], drain;
   __shared__ __align__(8) uint64_t piece_full[kPieces];
   __shared__ Piece s_piece[kPieces];
   __shared__ int s_odd[kPieces];   // the first slot with a value that is no finite number, among those looked at
   __shared__ uint32_t s_tmem;
+  __shared__ volatile int s_fail;   // a wait has run out
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) {
     for (int s = 0; s < NS; ++s) {
@@ -272,16 +286,18 @@ __global__ void __launch_bounds__(ChunkShape<HD, TC>::kThreads, 1) k_chunk_attn(
     for (int x = 0; x < 2; ++x) {
       mbar_init(&q_full[x], 4);
       mbar_init(&s_full[x], 1);
-      mbar_init(&p_full[x], 4);
+      mbar_init(&p_full[x][0], 4);
+      mbar_init(&p_full[x][1], 4);
       mbar_init(&o_done[x], 1);
     }
-    for (int i = 0; i < kPieces; ++i) mbar_init(&piece_full[i], 1);
     mbar_init(&drain, 1);
+    for (int i = 0; i < kPieces; ++i) mbar_init(&piece_full[i], 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   } else if (warp == 8 && lane < 2) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(lane ? &a.vm : &a.km)) : "memory");
   }
   if (tid < kPieces) s_odd[tid] = INT32_MAX;
+  if (tid == kPieces) s_fail = 0;
   if (warp == 9) {
     tmem_alloc(&s_tmem, 512);
     tmem_relinquish();
@@ -297,10 +313,10 @@ __global__ void __launch_bounds__(ChunkShape<HD, TC>::kThreads, 1) k_chunk_attn(
   bool ok = true;
   // Piece i of the CTA, for the other warps; no units at the end.
   auto piece_at = [&](int i) {
-    if (ok && !poll(&piece_full[i % kPieces], i / kPieces & 1)) ok = false;
+    await(ok, &piece_full[i % kPieces], i / kPieces & 1);
     ok = __all_sync(0xffffffffu, ok);
     Piece p = s_piece[i % kPieces];
-    if (!ok) p.t1 = p.t0 = 0;
+    if (!ok) p.t1 = p.t0 = 0, s_fail = 1;
     return p;
   };
 
@@ -341,8 +357,11 @@ __global__ void __launch_bounds__(ChunkShape<HD, TC>::kThreads, 1) k_chunk_attn(
           const int off = (t * SL) & ((1 << a.shift) - 1);
 #pragma unroll
           for (int v = 0; v < 2; ++v) {               // keys, then values
-            ok = __all_sync(0xffffffffu, poll(&empty[s], phase));
-            if (!ok) break;
+            await(ok, &empty[s], phase);
+            if (!__all_sync(0xffffffffu, ok)) {
+              ok = false;
+              break;
+            }
             if (lane == 0) mbar_expect_tx(&full[s], nb * bp * 128 * S::kHalf);
             __syncwarp();
             const int nhd = v ? a.v_nhd : a.k_nhd;
@@ -355,88 +374,89 @@ __global__ void __launch_bounds__(ChunkShape<HD, TC>::kThreads, 1) k_chunk_attn(
         }
       }
       if (lane == 0 && !a.by_item && !w.open) a.desc[blockIdx.x] = make_int4(0, 0, 0, 0);   // no item begins here that others share
-      // An expired wait: the copies in flight land before the CTA may end.
-      if (!ok)
-        for (int k = max(0, loaded - NS); k < loaded; ++k) poll(&full[k % NS], (k / NS) & 1);
+      if (!ok) s_fail = 1;
+      // The copies in flight land before the CTA may end, whatever the others did.
+      for (int k = max(0, loaded - NS); k < loaded; ++k) mbar_wait(&full[k % NS], (k / NS) & 1, kWaitPolls);
     } else if (warp == 9) {
       // ------------------------------------------------------------- MMA warp
-      // (control flow and descriptors the same in all lanes, one lane issues: as in k_paged_attn_tc)
-      constexpr uint32_t id_s = tc_idesc<TC>(128, SL, false), id_o = tc_idesc<TC>(128, HD, true);
-      const uint32_t utmem = __shfl_sync(0xffffffffu, tmem, 0);
-      const uint64_t dq = sw128_desc(__shfl_sync(0xffffffffu, smem_u32(qbuf), 0));
-      const uint64_t dk = sw128_desc(__shfl_sync(0xffffffffu, smem_u32(ring), 0));
-      const uint64_t dv = sw128_desc_mn(__shfl_sync(0xffffffffu, smem_u32(ring), 0), S::kBox);
-      bool good = true;
-      auto await = [&](uint64_t* bar, uint32_t parity) {
-        if (good) good = __all_sync(0xffffffffu, poll(bar, parity));
-      };
-      // S of tile x with the keys in stage s; the last tile frees the stage.
-      auto scores = [&](int x, int s, bool last) {
-        const uint64_t q = dq + (uint64_t)(x * (S::kTileBytes >> 4)), d = dk + (uint64_t)(s * (S::kTileBytes >> 4));
-        if (good && elect_one()) {
+      // One lane does it all.
+      if (elect_one()) {
+        constexpr uint32_t id_s = tc_idesc<TC>(128, SL, false), id_o = tc_idesc<TC>(128, HD, true);
+        const uint64_t dq = sw128_desc(smem_u32(qbuf)), dk = sw128_desc(smem_u32(ring));
+        const uint64_t dv = sw128_desc_mn(smem_u32(ring), S::kBox);
+        auto wait_for = [&](uint64_t* bar, uint32_t parity) {
+          if (ok && !mbar_wait(bar, parity, 1)) ok = mbar_wait(bar, parity, kWaitPolls);
+          tc_fence_after();
+        };
+        // S of tile x with the keys in stage s; the last tile frees the stage.
+        auto scores = [&](int x, int s, bool last) {
+          const uint64_t q = dq + (uint64_t)(x * (S::kTileBytes >> 4)), d = dk + (uint64_t)(s * (S::kTileBytes >> 4));
 #pragma unroll
           for (int k = 0; k < HD / 16; ++k) {
             const uint64_t o = ((k >> 2) * S::kBox + 32 * (k & 3)) >> 4;
-            umma_bf16(utmem + S::kS + SL * x, q + o, d + o, id_s, k > 0);
+            umma_bf16(tmem + S::kS + SL * x, q + o, d + o, id_s, k > 0);
           }
           umma_commit(&s_full[x]);
           if (last) umma_commit(&empty[s]);
-        }
-        __syncwarp();
-      };
-      // O of tile x += P V with the values in stage s.
-      auto output = [&](int x, int s, uint32_t keep, bool last, bool end) {
-        const uint64_t d = dv + (uint64_t)(s * (S::kTileBytes >> 4));
-        if (good && elect_one()) {
+        };
+        // O of tile x += P V for half h of the unit's slots, the values in stage s.
+        auto output = [&](int x, int s, int h, uint32_t keep) {
+          const uint64_t d = dv + (uint64_t)(s * (S::kTileBytes >> 4));
 #pragma unroll
-          for (int k = 0; k < SL / 16; ++k)
-            umma_bf16_tmem_a(utmem + S::kO + HD * x, utmem + S::kS + SL * x + 8 * k, d + (2048 * k >> 4), id_o,
-                             k > 0 ? 1u : keep);
-          if (last) umma_commit(&empty[s]);
-          if (end) umma_commit(&o_done[x]);
-        }
-        __syncwarp();
-      };
-      int s = 0, phase = 0, n = 0;                  // stage, units
-      uint32_t piece[2] = {0, 0}, done[2] = {0, 0};   // parities of each tile's next piece and unit
-      auto advance = [&] { if (++s == NS) s = 0, phase ^= 1; };
-      for (int i = 0; good; ++i) {
-        const Piece w = piece_at(i);
-        const int units = __shfl_sync(0xffffffffu, w.t1 - w.t0, 0);
-        if (units == 0) break;
-        const int tiles = __shfl_sync(0xffffffffu, w.rows * a.group - w.q * 256 > 128 ? 2 : 1, 0);
-        await(&full[s], phase);
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          if (x == tiles) break;
-          await(&q_full[x], piece[x]);
-          piece[x] ^= 1;
-          tc_fence_after();
-          scores(x, s, x == tiles - 1);
-        }
-        advance();
-        for (int u = 0; u < units; ++u, ++n) {
-          const int sv = s;
-          advance();
-          await(&checked[n % kChecks], n / kChecks & 1);
+          for (int k = 0; k < SL / 32; ++k) {
+            const int kk = h * (SL / 32) + k;
+            umma_bf16_tmem_a(tmem + S::kO + HD * x, tmem + S::kS + SL * x + 8 * kk, d + (2048 * kk >> 4), id_o,
+                             kk > 0 ? 1u : keep);
+          }
+        };
+        int s = 0, phase = 0, n = 0;                    // stage, units
+        uint32_t piece[2] = {0, 0}, done[2] = {0, 0};   // parities of each tile's next piece and unit
+        auto advance = [&] { if (++s == NS) s = 0, phase ^= 1; };
+        for (int i = 0;; ++i) {
+          wait_for(&piece_full[i % kPieces], i / kPieces & 1);
+          if (!ok) break;
+          const Piece w = s_piece[i % kPieces];
+          const int units = w.t1 - w.t0;
+          if (units == 0) break;
+          const int tiles = w.rows * a.group - w.q * 256 > 128 ? 2 : 1;
+          wait_for(&full[s], phase);
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             if (x == tiles) break;
-            await(&p_full[x], done[x]);
-            done[x] ^= 1;
-            tc_fence_after();
-            output(x, sv, u % S::kFold ? 1u : 0u, x == tiles - 1, u == units - 1);
-            if (u + 1 < units) {
-              if (x == 0) await(&full[s], phase);
-              scores(x, s, x == tiles - 1);
-            }
+            wait_for(&q_full[x], piece[x]);
+            piece[x] ^= 1;
+            scores(x, s, x == tiles - 1);
           }
-          if (u + 1 < units) advance();
+          advance();
+          for (int u = 0; u < units; ++u, ++n) {
+            const int sv = s;
+            const bool more = u + 1 < units;
+            advance();
+            wait_for(&checked[n % kChecks], n / kChecks & 1);
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              if (x == tiles) break;
+              const bool last = x == tiles - 1;
+              wait_for(&p_full[x][0], done[x]);
+              output(x, sv, 0, u % S::kFold ? 1u : 0u);
+              wait_for(&p_full[x][1], done[x]);
+              done[x] ^= 1;
+              output(x, sv, 1, 1u);
+              if (last) umma_commit(&empty[sv]);
+              if (more) {
+                if (x == 0) wait_for(&full[s], phase);
+                scores(x, s, last);
+              } else {
+                umma_commit(&o_done[x]);
+              }
+            }
+            if (more) advance();
+          }
         }
-      }
-      if (!good) {   // an expired wait: what was issued ends before the CTA does
-        if (elect_one()) umma_commit(&drain);
-        poll(&drain, 0);
+        if (!ok) s_fail = 1;
+        // What was issued ends before the CTA does, also when a wait has run out.
+        umma_commit(&drain);
+        mbar_wait(&drain, 0, kWaitPolls);
       }
       __syncwarp();
     } else {
@@ -445,16 +465,14 @@ __global__ void __launch_bounds__(ChunkShape<HD, TC>::kThreads, 1) k_chunk_attn(
       constexpr uint32_t X = Num<TC>::kExp;
       const int me = tid - 320;                       // 0 .. 63
       int s = 1, phase = 0, n = 0;                    // (keys in one stage, values in the next)
-      for (int piece = 0; ok; ++piece) {
+      for (int piece = 0;; ++piece) {
         const Piece w = piece_at(piece);
         if (w.t1 == 0) break;
         if (me == 0) s_odd[(piece + 8) % kPieces] = INT32_MAX;   // (nobody is that many pieces behind)
         // From slot `seen` on some row of the item does not see a slot.
         const int seen = w.p0 + w.q * 256 / a.group + 1;
         for (int t = w.t0; t < w.t1; ++t, ++n) {
-          if (ok && !poll(&full[s], phase)) ok = false;
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
+          await(ok, &full[s], phase);
           const int s0 = min(max(seen - t * SL, 0), SL), s1 = min(max(w.len - t * SL, 0), SL);
           if (s0 < SL) {
             unsigned char* vs = ring + s * S::kTileBytes;
@@ -493,8 +511,7 @@ __global__ void __launch_bounds__(ChunkShape<HD, TC>::kThreads, 1) k_chunk_attn(
     unsigned char* const qs = qbuf + x * S::kTileBytes;
     int n = 0, my_pieces = 0;                                 // units and pieces of this tile
     auto s_wait = [&] {
-      if (ok && !poll(&s_full[x], n & 1)) ok = false;
-      ok = __all_sync(0xffffffffu, ok);
+      await(ok, &s_full[x], n & 1);
       tc_fence_after();
     };
     // The piece's queries into shared memory (rows past the end: zeros).
@@ -605,14 +622,18 @@ __global__ void __launch_bounds__(ChunkShape<HD, TC>::kThreads, 1) k_chunk_attn(
               p[i] = Num<TC>::pack(p0, p1);
             }
             tmem_st32(t_s + 32 * c, p);
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&p_full[x][c]);        // (the product with one half runs beside the other's exponentials)
           }
           const float2 ls = unpair(add2(add2(l2[0], l2[1]), add2(l2[2], l2[3])));
           l += ls.x + ls.y;
-          tmem_st_wait();
+        } else {
+          tc_fence_before();
+          __syncwarp();
+          if (lane < 2) mbar_arrive(&p_full[x][lane]);
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[x]);
         ++n;
       };
       // Between two units: O and l move to the part (`first`: which holds
@@ -657,8 +678,7 @@ __global__ void __launch_bounds__(ChunkShape<HD, TC>::kThreads, 1) k_chunk_attn(
       w = next_piece();
 
       // ---- the end of the piece
-      if (ok && !poll(&o_done[x], my_pieces & 1)) ok = false;
-      ok = __all_sync(0xffffffffu, ok);
+      await(ok, &o_done[x], my_pieces & 1);
       tc_fence_after();
       ++my_pieces;
       float f = 0.f;                                          // of what lies in the part
@@ -667,7 +687,7 @@ __global__ void __launch_bounds__(ChunkShape<HD, TC>::kThreads, 1) k_chunk_attn(
         f = ml.x == -INFINITY ? 0.f : exp2_approx((ml.x - m) * a.scale2);
         l = fmaf(ml.y, f, l);
       }
-      if (!ok || s_odd[odd_at] < lim) l = __int_as_float(0x7fc00000);   // an expired wait, a value that is no number: NaN
+      if (!ok || s_fail || s_odd[odd_at] < lim) l = __int_as_float(0x7fc00000);   // an expired wait, a value that is no number: NaN
       if (m != -INFINITY) m = fmaf(m, a.scale2, (float)-S::kUp);
       if (warp_live) {
         const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
@@ -712,7 +732,7 @@ __global__ void __launch_bounds__(ChunkShape<HD, TC>::kThreads, 1) k_chunk_attn(
       }
       tc_fence_before();   // O has been read: the next piece's first product may replace it
     }
-    if (!ok && lane == 0) report_err(a.err, kErrWait);
+    if (!ok) report_err(a.err, kErrWait);
   }
   tc_fence_before();
   __syncthreads();
