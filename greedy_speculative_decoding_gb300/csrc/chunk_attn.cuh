@@ -51,8 +51,9 @@ struct ChunkShape {
   static constexpr int kHalf = HD / 64;
   static constexpr int kBox = 128 * 128;                // 128 rows of 64 dimensions
   static constexpr int kTileBytes = kHalf * kBox;       // of queries, keys or values
-  static constexpr int kStages = HD == 128 ? 5 : 10;
-  static constexpr int kSmem = 1024 + (2 + kStages) * kTileBytes;
+  static constexpr int kStages = HD == 128 ? 4 : 10;
+  static constexpr int kStaging = 4096;                 // bytes of a softmax warp: 128 of each row on their way out
+  static constexpr int kSmem = 1024 + (2 + kStages) * kTileBytes + 8 * kStaging;
   static constexpr int kO = 0, kS = 2 * HD;             // tensor-memory columns: O of both tiles, S of both
   // As in TcShape: bounds of a reference's lag and the scale of fp16 probabilities, in powers of two.
   static constexpr int kLag = std::is_same<TC, __half>::value ? 3 : 8;
@@ -343,6 +344,15 @@ __global__ void __launch_bounds__(ChunkShape<HD, TC>::kThreads, 1) k_chunk_attn(
         }
         ++piece;
         if (!more) break;
+        // Its queries towards L2: the softmax warps load them when they are done with the piece before.
+        for (int i = lane; i < 256; i += 32) {
+          const int q = w.item_q * 256 + i, j = q / a.group, hh = w.item_h * a.group + q - j * a.group;
+          if (q < w.r.rows * a.group) {
+            const TC* p = static_cast<const TC*>(a.q) + (w.r.s0 + j) * a.q_row + hh * a.q_head;
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+            if (HD == 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(p + 64));
+          }
+        }
         for (int t = w.t0; ok && t < w.t1; ++t) {
           const int first = (t * SL) >> a.shift;
           if (w.b != win_b || (first >> 5) != win) {
@@ -521,15 +531,18 @@ __global__ void __launch_bounds__(ChunkShape<HD, TC>::kThreads, 1) k_chunk_attn(
       const int q = w.q * 256 + 128 * x + row, j = q / a.group, hh = w.kvh * a.group + q - j * a.group;
       const long off = q < w.rows * a.group ? (w.s0 + j) * a.q_row + hh * a.q_head : kNone;
       const int p = lane % PP;
-#pragma unroll 4
+      uint4 f[32 / RW];                                       // (all on their way together)
+#pragma unroll
       for (int i = 0; i < 32 / RW; ++i) {
-        const int rr = RW * i + lane / PP;
-        const long o = __shfl_sync(0xffffffffu, off, rr);
-        uint4 f = make_uint4(0u, 0u, 0u, 0u);
-        if (o != kNone) f = *reinterpret_cast<const uint4*>(static_cast<const TC*>(a.q) + o + 8 * p);
-        f.x ^= a.flip, f.y ^= a.flip, f.z ^= a.flip, f.w ^= a.flip;
-        const int r = 32 * (warp & 3) + rr;
-        *reinterpret_cast<uint4*>(qs + (p >> 3) * S::kBox + r * 128 + (((p & 7) ^ (r & 7)) << 4)) = f;
+        const long o = __shfl_sync(0xffffffffu, off, RW * i + lane / PP);
+        f[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (o != kNone) f[i] = *reinterpret_cast<const uint4*>(static_cast<const TC*>(a.q) + o + 8 * p);
+      }
+#pragma unroll
+      for (int i = 0; i < 32 / RW; ++i) {
+        f[i].x ^= a.flip, f[i].y ^= a.flip, f[i].z ^= a.flip, f[i].w ^= a.flip;
+        const int r = 32 * (warp & 3) + RW * i + lane / PP;
+        *reinterpret_cast<uint4*>(qs + (p >> 3) * S::kBox + r * 128 + (((p & 7) ^ (r & 7)) << 4)) = f[i];
       }
       fence_proxy_async();
       __syncwarp();
@@ -691,20 +704,41 @@ __global__ void __launch_bounds__(ChunkShape<HD, TC>::kThreads, 1) k_chunk_attn(
       if (m != -INFINITY) m = fmaf(m, a.scale2, (float)-S::kUp);
       if (warp_live) {
         const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
-        TC* dst = static_cast<TC*>(a.out) + out_row * a.o_row + hh * a.o_head;
-#pragma unroll 1
-        for (int c = 0; c < HD / 32; ++c) {
-          uint32_t o[32];
+        // 128 bytes of each row (32 words a lane, its row's) through shared
+        // memory, so that a store is four rows' 128 bytes (a lane's own row at a
+        // time would be 32 rows' 16 bytes: items' ends took 4 us).
+        unsigned char* const sw = ring + NS * S::kTileBytes + warp * S::kStaging;
+        char* const dst = !live ? nullptr
+                          : whole ? reinterpret_cast<char*>(static_cast<TC*>(a.out) + out_row * a.o_row + hh * a.o_head)
+                                  : reinterpret_cast<char*>(part);
+        auto put = [&](const uint32_t* y, int at) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            *reinterpret_cast<uint4*>(sw + lane * 128 + ((i ^ (lane & 7)) << 4)) =
+                make_uint4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
           __syncwarp();
-          tmem_ld32(t_o + 32 * c, o);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int r = 4 * i + (lane >> 3), k = lane & 7;
+            char* const d = reinterpret_cast<char*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(dst), r));
+            const uint4 v = *reinterpret_cast<const uint4*>(sw + r * 128 + ((k ^ (r & 7)) << 4));
+            if (d) *reinterpret_cast<uint4*>(d + at + 16 * k) = v;
+          }
+          __syncwarp();
+        };
+#pragma unroll 1
+        for (int c = 0; c < HD / 64; ++c) {
+          uint32_t o[64];
+          __syncwarp();
+          tmem_ld32(t_o + 64 * c, o);
+          tmem_ld32(t_o + 64 * c + 32, o + 32);
           tmem_ld_wait();
 #pragma unroll
-          for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(o[i]));
-          if (!live) continue;
-          if (folded) {
+          for (int i = 0; i < 64; ++i) asm volatile("" : "+r"(o[i]));
+          if (folded && live) {
 #pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-              const float4 y = *reinterpret_cast<const float4*>(part + 32 * c + i);
+            for (int i = 0; i < 64; i += 4) {
+              const float4 y = *reinterpret_cast<const float4*>(part + 64 * c + i);
               o[i] = __float_as_uint(fmaf(y.x, f, __uint_as_float(o[i])));
               o[i + 1] = __float_as_uint(fmaf(y.y, f, __uint_as_float(o[i + 1])));
               o[i + 2] = __float_as_uint(fmaf(y.z, f, __uint_as_float(o[i + 2])));
@@ -713,17 +747,14 @@ __global__ void __launch_bounds__(ChunkShape<HD, TC>::kThreads, 1) k_chunk_attn(
           }
           // (a row that saw nothing: l = 0 and O = 0)
           if (whole) {
-            uint32_t y[16];
+            uint32_t y[32];
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
+            for (int i = 0; i < 32; ++i)
               y[i] = Num<TC>::pack(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);
-#pragma unroll
-            for (int i = 0; i < 16; i += 4)
-              *reinterpret_cast<uint4*>(dst + 32 * c + 2 * i) = make_uint4(y[i], y[i + 1], y[i + 2], y[i + 3]);
+            put(y, 128 * c);
           } else {
-#pragma unroll
-            for (int i = 0; i < 32; i += 4)
-              *reinterpret_cast<uint4*>(part + 32 * c + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+            put(o, 256 * c);
+            put(o + 32, 256 * c + 128);
           }
         }
         if (live && whole && a.lse)
