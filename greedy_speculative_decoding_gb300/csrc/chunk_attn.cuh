@@ -59,7 +59,7 @@ struct ChunkShape {
   static constexpr int kLag = std::is_same<TC, __half>::value ? 3 : 8;
   static constexpr int kUp = std::is_same<TC, __half>::value ? 12 : 0;
   static constexpr int kFold = 128;                     // units after which O moves to the part (16384 slots, as there)
-  static constexpr int kPiece = 2;                      // units that an item's beginning counts for
+  static constexpr int kPiece = 4;                      // units that an item's beginning counts for
 };
 
 // The units of a request's items.
@@ -221,6 +221,52 @@ __device__ __forceinline__ void describe(const Args& a, const ChunkWalk& w, cons
   else if (!whole) a.desc[blockIdx.x] = d;
 }
 
+// A wait ran out: every row of the CTA's pieces becomes NaN (one warp, which
+// finds the pieces by itself).
+template <int HD, typename TC>
+__device__ __noinline__ void leave_nan(const Args& a) {
+  const int lane = threadIdx.x & 31;
+  const float nan = __int_as_float(0x7fc00000);
+  long T = 0;
+  for (int b = 0; b < a.B; ++b) T += a.nkv * ItemUnits(a, request<256>(a, b)).head();
+  const long G = min((long)gridDim.x, T);
+  if ((long)blockIdx.x >= G) return;
+  const Deal deal(T, G);
+  ChunkWalk w;
+  w.u = deal.first(blockIdx.x);
+  w.left = deal.first(blockIdx.x + 1) - w.u;
+  long base = 0;
+  for (w.b = 0;; ++w.b) {
+    w.r = request<256>(a, w.b);
+    w.iu = ItemUnits(a, w.r);
+    const long n = a.nkv * w.iu.head();
+    if (w.u < base + n) break;
+    base += n;
+  }
+  const long head = w.iu.head(), rest = w.u - base;
+  w.kvh = (int)(rest / head);
+  w.qt = w.iu.find(rest - w.kvh * head);
+  w.at = (int)(rest - w.kvh * head - w.iu.before(w.qt));
+  while (w.next(a)) {
+    const bool whole = w.t0 == 0 && w.t1 == w.nt;
+    if (lane == 0 && w.t0 == 0) describe(a, w, deal, whole);
+    const long slot = 2l * blockIdx.x + (w.t0 == 0 ? 1 : 0);
+    for (int i = lane; i < 256; i += 32) {
+      const int q = w.item_q * 256 + i, j = q / a.group, hh = w.item_h * a.group + q - j * a.group;
+      if (q >= w.r.rows * a.group) break;
+      if (!whole) {
+        a.part_ml[slot * a.mt_max + i] = make_float2(0.f, nan);
+        continue;
+      }
+      TC* dst = static_cast<TC*>(a.out) + (w.r.s0 + j) * a.o_row + hh * a.o_head;
+      for (int d = 0; d < HD; d += 2) *reinterpret_cast<uint32_t*>(dst + d) = Num<TC>::pack(nan, nan);
+      if (a.lse) a.lse[(long)(w.r.s0 + j) * a.nq + hh] = nan;
+    }
+  }
+  if (lane == 0 && !a.by_item && !w.open) a.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
+  report_err(a.err, kErrWait);
+}
+
 // Pairs of fp32 numbers at once.
 __device__ __forceinline__ uint64_t pair(float x, float y) {
   uint64_t d;
@@ -256,7 +302,8 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
 // As wait, without a call (setmaxnreg's register counts allow none), for a
 // converged warp; once a wait has run out (ok false) no further one is begun.
 // The lanes do not vote on it: that would cost 100 cycles a wait. Whoever gave up
-// goes on without waiting to the end of the piece and leaves NaN.
+// goes on without waiting, to the end of the piece at least; the CTA's rows
+// become NaN in the end.
 __device__ __forceinline__ void await(bool& ok, uint64_t* bar, uint32_t parity) {
   if (ok) ok = mbar_wait(bar, parity, kWaitPolls);
   __syncwarp();
@@ -327,8 +374,8 @@ __global__ void __launch_bounds__(ChunkShape<HD, TC>::kThreads, 1) k_chunk_attn(
       // -------------------------------------------------------- producer warp
       const int bp = min(1 << a.shift, SL);           // slots of a box
       const int np = SL / bp;                         // boxes of a column
-      const int i = lane % np, h = lane / np;         // this lane's box of a tile: np * kHalf <= 16 lanes
-      const uint32_t dst0 = smem_u32(ring) + h * S::kBox + i * bp * 128;
+      const int bi = lane % np, h = lane / np;        // this lane's box of a tile: np * kHalf <= 16 lanes
+      const uint32_t dst0 = smem_u32(ring) + h * S::kBox + bi * bp * 128;
       const uint64_t policy = policy_evict_normal();
       int win_b = -1, win = -1, entry = 0;            // the 32 table entries at hand, one per lane
       int s = 0, phase = 1, loaded = 0;               // (a new barrier's phase 1 counts as past)
@@ -363,7 +410,7 @@ __global__ void __launch_bounds__(ChunkShape<HD, TC>::kThreads, 1) k_chunk_attn(
           }
           const int left = w.r.len - t * SL;          // slots from here on
           const int nb = max(0, min(np, (left + bp - 1) / bp));
-          const int page = __shfl_sync(0xffffffffu, entry, (first + i) & 31);
+          const int page = __shfl_sync(0xffffffffu, entry, (first + bi) & 31);
           const int off = (t * SL) & ((1 << a.shift) - 1);
 #pragma unroll
           for (int v = 0; v < 2; ++v) {               // keys, then values
@@ -375,7 +422,7 @@ __global__ void __launch_bounds__(ChunkShape<HD, TC>::kThreads, 1) k_chunk_attn(
             if (lane == 0) mbar_expect_tx(&full[s], nb * bp * 128 * S::kHalf);
             __syncwarp();
             const int nhd = v ? a.v_nhd : a.k_nhd;
-            if (h < S::kHalf && i < nb)
+            if (h < S::kHalf && bi < nb)
               tma_load_4d(dst0 + s * S::kTileBytes, v ? &a.vm : &a.km, 64 * h, nhd ? w.item_h : off,
                           nhd ? off : w.item_h, page, &full[s], policy);
             ++loaded;
@@ -511,6 +558,7 @@ __global__ void __launch_bounds__(ChunkShape<HD, TC>::kThreads, 1) k_chunk_attn(
           if (s >= NS) s -= NS, phase ^= 1;
         }
       }
+      if (!ok) s_fail = 1;
     }
   } else {
     // ----------------------------------------------------------- softmax warps
@@ -700,7 +748,7 @@ __global__ void __launch_bounds__(ChunkShape<HD, TC>::kThreads, 1) k_chunk_attn(
         f = ml.x == -INFINITY ? 0.f : exp2_approx((ml.x - m) * a.scale2);
         l = fmaf(ml.y, f, l);
       }
-      if (!ok || s_fail || s_odd[odd_at] < lim) l = __int_as_float(0x7fc00000);   // an expired wait, a value that is no number: NaN
+      if (s_odd[odd_at] < lim) l = __int_as_float(0x7fc00000);   // the row sees a value that is no number: NaN
       if (m != -INFINITY) m = fmaf(m, a.scale2, (float)-S::kUp);
       if (warp_live) {
         const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
@@ -763,7 +811,7 @@ __global__ void __launch_bounds__(ChunkShape<HD, TC>::kThreads, 1) k_chunk_attn(
       }
       tc_fence_before();   // O has been read: the next piece's first product may replace it
     }
-    if (!ok) report_err(a.err, kErrWait);
+    if (!ok) s_fail = 1;
   }
   tc_fence_before();
   __syncthreads();
@@ -771,6 +819,7 @@ __global__ void __launch_bounds__(ChunkShape<HD, TC>::kThreads, 1) k_chunk_attn(
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
+  if (warp == 0 && s_fail) leave_nan<HD, TC>(a);
 }
 
 }  // namespace pa

@@ -167,6 +167,24 @@ static cudaError_t enqueue_chunk(Args& a, const sf_paged_cache& c, int q_dtype, 
   return c.head_dim == 128 ? launch_chunk_hd128(a, q_dtype, sms, max_units, st)
                            : launch_chunk_hd64(a, q_dtype, sms, max_units, st);
 }
+// Whether a chunk of 16-bit queries is so little work that paged_attention's
+// kernels finish first: they start sooner and share it out more finely, but read
+// the cache more often and compute what causality masks. `total` counts tiles of
+// 128 queries by 64 slots, in requests that fill their tables. Measured, us of
+// the chunk kernel / of those, bf16, requests x rows of tokens:
+//   head_dim 64, 14 / 2 heads: 1 x 97 of 97 11.5 / 9.4; 1 x 256 of 512 14.9 / 14.6;
+//     1 x 64 of 4096 14.4 / 12.7; 1 x 512 of 512 16.9 / 22.5; 8 x 64 of 2048 20.8 / 26.8
+//   128, 28 / 4: 1 x 97 of 97 13.7 / 11.6; 4 x 100 of 300 21.5 / 18.5; 1 x 64 of 4096
+//     19.6 / 18.0; 1 x 256 of 512 22.1 / 21.1; 1 x 512 of 512 24.8 / 25.6; 8 x 64 of
+//     2048 35.0 / 38.6; 2 x 512 of 2048 51.4 / 68.8
+//   128, 40 / 8: 1 x 64 of 4096 21.2 / 19.2; 1 x 256 of 512 24.4 / 20.5; 1 x 150 of
+//     150 17.0 / 22.0; 16 x 200 of 200 74.8 / 103.6
+// At up to 128 queries the chunk kernel's second tile has nothing to do.
+static bool little_chunk(const sf_paged_cache& c, int n_heads, int max_rows, int batch, int table_width) {
+  const long queries = (long)max_rows * (n_heads / c.n_kv_heads);
+  const long total = batch * c.n_kv_heads * ((queries + 127) / 128) * (((long)table_width * c.page + kTile - 1) / kTile);
+  return queries <= 128 || total < 256 || (queries <= 768 && total <= 1536);
+}
 // The kernel counts a request's units as (group * slots) / 128 and its items in 32 bits.
 static bool chunk_fits(const sf_paged_cache& c, int n_heads, int max_rows, int table_width) {
   const long group = n_heads / c.n_kv_heads;
@@ -274,7 +292,8 @@ static sf_status attention(const char* who, int most_rows, const sf_paged_cache*
   a.tables = d_tables, a.lens = d_lens, a.starts = d_starts;
   a.mask = reinterpret_cast<const unsigned long long*>(d_mask);
   a.B = batch, a.N = n, a.W = table_width, a.nq = q->n_heads, a.max_rows = max_rows, a.rows_each = n / batch;
-  const bool chunk = most_rows == kMaxChunk && q->dtype != SF_DT_F32;
+  const bool chunk = most_rows == kMaxChunk && q->dtype != SF_DT_F32 &&
+                     !pa::little_chunk(*cache, q->n_heads, max_rows, batch, table_width);
   if (chunk ? !pa::chunk_fits(*cache, q->n_heads, max_rows, table_width)
             : !pa::units_fit(*cache, q->n_heads, max_rows, q->dtype, batch, table_width, sms))
     return set_error(SF_ERR_UNSUPPORTED, "%s: table_width * page too large for this many heads and rows", who);
