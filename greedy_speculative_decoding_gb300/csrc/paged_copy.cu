@@ -1,6 +1,6 @@
 // Whole pages, or their first slots, copied in every layer of a cache
-// (sf_page_copy). Bound by memory: a unit is one head's keys or values of one
-// page in one layer, taken by a CTA; a thread has four 16-byte loads in flight.
+// (sf_page_copy). Bound by memory: a unit is the keys or the values of one page
+// in one layer, taken by a CTA; a thread has four 16-byte loads in flight.
 #include <algorithm>
 
 #include "paged.h"
@@ -20,30 +20,31 @@ struct CopyArgs {
 __global__ void __launch_bounds__(kCopyThreads, kCopyCtas) k_page_copy(const __grid_constant__ CopyArgs a) {
   pdl_wait();
   const int n = a.count ? min(max(*a.count, 0), a.n) : a.n;
-  const long per = 2l * a.layers * a.nkv, units = n * per;
+  const long per = 2l * a.layers, units = n * per;
+  const int mask = (1 << a.hd_shift) - 1;
   for (long u = blockIdx.x; u < units; u += gridDim.x) {
     const long i = u / per;
-    const int r = (int)(u - i * per), h = r % a.nkv, kv = r / a.nkv & 1, layer = r / a.nkv >> 1;
+    const int r = (int)(u - i * per), kv = r & 1, layer = r >> 1;
     const int s = a.source[i], t = a.target[i];
-    if (s < 0 || s >= a.n_pages || t < 0 || t >= a.n_pages) continue;
-    const int pieces = (a.slots ? min(max(a.slots[i], 0), a.page) : a.page) << a.hd_shift;
-    uint16_t* base = kv ? a.v + layer * a.v_layer + h * a.v_head : a.k + layer * a.k_layer + h * a.k_head;
+    const int slots = a.slots ? min(max(a.slots[i], 0), a.page) : a.page;
+    if (s < 0 || s >= a.n_pages || t < 0 || t >= a.n_pages || slots == 0) continue;
+    uint16_t* base = kv ? a.v + layer * a.v_layer : a.k + layer * a.k_layer;
     const uint16_t* from = base + s * (kv ? a.v_page : a.k_page);
     uint16_t* to = base + t * (kv ? a.v_page : a.k_page);
-    const long slot = kv ? a.v_slot : a.k_slot;
-    const int mask = (1 << a.hd_shift) - 1;
-    for (int e0 = threadIdx.x; e0 < pieces; e0 += 4 * kCopyThreads) {
+    const long slot = kv ? a.v_slot : a.k_slot, head = kv ? a.v_head : a.k_head;
+    const unsigned each = slots << a.hd_shift, pieces = each * a.nkv;   // of 16 bytes, of a head and of all (below 2^28)
+    for (unsigned e0 = threadIdx.x; e0 < pieces; e0 += 4 * kCopyThreads) {
       uint4 w[4];
+      long at[4];
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
-        const int e = e0 + x * kCopyThreads;
-        if (e < pieces) w[x] = __ldcs(reinterpret_cast<const uint4*>(from + (e >> a.hd_shift) * slot + (e & mask) * 8));
+        const unsigned e = e0 + x * kCopyThreads, h = e / each, p = e - h * each;
+        at[x] = h * head + (p >> a.hd_shift) * slot + (p & mask) * 8;
+        if (e < pieces) w[x] = __ldcs(reinterpret_cast<const uint4*>(from + at[x]));
       }
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const int e = e0 + x * kCopyThreads;
-        if (e < pieces) __stcs(reinterpret_cast<uint4*>(to + (e >> a.hd_shift) * slot + (e & mask) * 8), w[x]);
-      }
+      for (int x = 0; x < 4; ++x)
+        if (e0 + x * kCopyThreads < pieces) __stcs(reinterpret_cast<uint4*>(to + at[x]), w[x]);
     }
   }
 }
@@ -96,7 +97,7 @@ extern "C" sf_status sf_page_copy(const sf_paged_cache* cache, int32_t layers, i
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)std::min<long>((long)sms * kCopyCtas, 2l * n * layers * cache->n_kv_heads));
+    cfg.gridDim = dim3((unsigned)std::min<long>((long)sms * kCopyCtas, 2l * n * layers));
     cfg.blockDim = dim3(kCopyThreads);
     cfg.stream = static_cast<cudaStream_t>(cuda_stream);
     cfg.attrs = attr;

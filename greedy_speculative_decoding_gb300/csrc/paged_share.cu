@@ -2,12 +2,15 @@
 // forked (sf_page_fork), and the held pages moved to the lowest numbers
 // (sf_page_compact). shares[p] counts page p's holders beyond the first.
 //
-// Each is one cluster of CTAs. What must be known of every request of the
-// list (its entries' place among all entries, whether an earlier one names the
-// same request) every CTA finds for itself in shared memory; the entries are
-// then dealt out to all threads. Counts change by atomic additions of whole
-// numbers, whose order does not matter, and where order matters (which of the
-// releases of one page puts it onto the stack) the first in the list wins.
+// Each is one cluster of CTAs, or one small CTA. What must be known of every
+// request of the list (its entries' place among all entries, whether an earlier
+// one names the same request) every CTA finds for itself in shared memory; the
+// entries are then dealt out, a stretch to each CTA and eight in a row to each
+// thread, so that their loads are on their way together. Counts change by atomic
+// additions of whole numbers, whose order does not matter, and where order
+// matters (which of the releases of one page puts it onto the stack) the first
+// in the list wins. What bounds all three is the chain of barriers and of loads
+// that depend on one another.
 #include <algorithm>
 #include <atomic>
 #include <climits>
@@ -17,7 +20,9 @@
 namespace sf {
 namespace {
 
-constexpr int kThreads = 1024, kCluster = 8;
+constexpr int kThreads = 1024, kCluster = 8;   // of many entries; few: one CTA of kFewThreads
+constexpr int kFewThreads = 256;
+constexpr int kRun = 8;              // entries of a thread, one after the other
 constexpr int kMaxPages = 1 << 20;   // of a compaction (its bit map lies in shared memory)
 
 // Exclusive sum of x over the CTA's threads and its total.
@@ -60,9 +65,9 @@ __device__ __forceinline__ int ceil_pages(int tokens, int shift) {
 
 // Marks for every request the first of the list that names it.
 __device__ __forceinline__ void first_of(const int* list, int n, int B, int* s_first) {
-  for (int b = threadIdx.x; b < B; b += kThreads) s_first[b] = INT_MAX;
+  for (int b = threadIdx.x; b < B; b += blockDim.x) s_first[b] = INT_MAX;
   __syncthreads();
-  for (int i = threadIdx.x; i < n; i += kThreads) {
+  for (int i = threadIdx.x; i < n; i += blockDim.x) {
     const int r = list[i];
     if (r >= 0 && r < B) atomicMin(&s_first[r], i);
   }
@@ -88,12 +93,13 @@ __global__ void __launch_bounds__(kThreads) k_page_free(const FreeArgs a) {
   int* s_row = s_at + a.n + 1;      // [n] the request, or -1
   int* s_from = s_row + a.n;        // [n] its first entry released
   __shared__ int warp_sums[32], s_mine;
-  const int tid = threadIdx.x, ctas = gridDim.x, rank = blockIdx.x;
+  const int tid = threadIdx.x, NT = blockDim.x, ctas = gridDim.x, rank = blockIdx.x;
   pdl_wait();
+  pdl_launch_next();
   first_of(a.requests, a.n, a.B, s_first);
   const int n_free = min(max(*a.n_free, 0), a.cap);
   int total = 0;
-  for (int i0 = 0; i0 < a.n; i0 += kThreads) {
+  for (int i0 = 0; i0 < a.n; i0 += NT) {
     const int i = i0 + tid;
     int count = 0, r = -1, from = 0;
     if (i < a.n) {
@@ -122,34 +128,66 @@ __global__ void __launch_bounds__(kThreads) k_page_free(const FreeArgs a) {
   }
   if (tid == 0) s_at[a.n] = total;
   cluster_sync();   // held, n_free and shares have been read
-  auto page_at = [&](int k) {   // of release k, or -1
-    const int i = place_of(s_at, a.n - 1, k);
-    const int p = a.tables[(size_t)s_row[i] * a.W + s_from[i] + (k - s_at[i])];
-    return p >= 0 && p < a.P ? p : -1;
+  // A stretch of the releases for each CTA, in rounds of kRun for each thread:
+  // their pages, or -1 (one round, nearly always: they are looked up once).
+  const int k0 = (int)((long long)total * rank / ctas), k1 = (int)((long long)total * (rank + 1) / ctas);
+  const int round = NT * kRun, rounds = (k1 - k0 + round - 1) / round;
+  int page[kRun];
+  auto look_up = [&](int rd) {
+    const int first = k0 + rd * round + tid * kRun;
+    int i = first < k1 ? place_of(s_at, a.n - 1, first) : 0;
+#pragma unroll
+    for (int e = 0; e < kRun; ++e) {
+      const int k = first + e;
+      page[e] = -1;
+      if (k < k1) {
+        while (k >= s_at[i + 1]) ++i;
+        const int p = a.tables[(size_t)s_row[i] * a.W + s_from[i] + (k - s_at[i])];
+        page[e] = p >= 0 && p < a.P ? p : -1;
+      }
+    }
   };
+  if (rounds == 1) look_up(0);
   // Count the releases. A page that has as many as holders is left at -1.
-  for (int k = rank * kThreads + tid; k < total; k += ctas * kThreads) {
-    const int p = page_at(k);
-    if (p >= 0) atomicSub(&a.shares[p], 1);
+  for (int rd = 0; rd < rounds; ++rd) {
+    if (rounds > 1) look_up(rd);
+#pragma unroll
+    for (int e = 0; e < kRun; ++e)
+      if (page[e] >= 0) atomicSub(&a.shares[page[e]], 1);
   }
   cluster_sync();
   // Its first release claims it (claims lie below all counts: total < 2^30).
-  for (int k = rank * kThreads + tid; k < total; k += ctas * kThreads) {
-    const int p = page_at(k);
-    if (p >= 0 && __ldcg(&a.shares[p]) < 0) atomicMin(&a.shares[p], INT_MIN + k);
+  for (int rd = 0; rd < rounds; ++rd) {
+    if (rounds > 1) look_up(rd);
+    const int first = k0 + rd * round + tid * kRun;
+    int count[kRun];
+#pragma unroll
+    for (int e = 0; e < kRun; ++e) count[e] = page[e] >= 0 ? __ldcg(&a.shares[page[e]]) : 0;
+#pragma unroll
+    for (int e = 0; e < kRun; ++e)
+      if (count[e] < 0) atomicMin(&a.shares[page[e]], INT_MIN + first + e);
   }
   cluster_sync();
-  // Claimed pages go onto the stack in the list's order: a stretch of releases
-  // a CTA.
-  const int k0 = (int)((long long)total * rank / ctas), k1 = (int)((long long)total * (rank + 1) / ctas);
-  auto claimed = [&](int k) {
-    const int p = k < k1 ? page_at(k) : -1;
-    return p >= 0 && __ldcg(&a.shares[p]) == INT_MIN + k ? p : -1;
+  // Claimed pages go onto the stack in the list's order: first how many they
+  // are in each CTA's stretch, then where they go.
+  auto claimed = [&](int rd) {   // bit e: release e of the thread's has its page
+    const int first = k0 + rd * round + tid * kRun;
+    int count[kRun], bits = 0;
+#pragma unroll
+    for (int e = 0; e < kRun; ++e) count[e] = page[e] >= 0 ? __ldcg(&a.shares[page[e]]) : 0;
+#pragma unroll
+    for (int e = 0; e < kRun; ++e) bits |= (page[e] >= 0 && count[e] == INT_MIN + first + e) << e;
+    return bits;
   };
-  int mine = 0;
-  for (int k = k0 + tid; k < k1; k += kThreads) mine += claimed(k) >= 0;
-  scan_cta(mine, mine, warp_sums);
-  if (tid == 0) s_mine = mine;
+  int mine = 0, bits = 0;
+  for (int rd = 0; rd < rounds; ++rd) {
+    if (rounds > 1) look_up(rd);
+    bits = claimed(rd);
+    mine += __popc(bits);
+  }
+  int of_cta;
+  scan_cta(mine, of_cta, warp_sums);
+  if (tid == 0) s_mine = of_cta;
   cluster_sync();
   int at = n_free, all = 0;
   for (int c = 0; c < ctas; ++c) {
@@ -158,18 +196,24 @@ __global__ void __launch_bounds__(kThreads) k_page_free(const FreeArgs a) {
     at += c < rank ? x : 0;
     all += x;
   }
-  for (int k = k0; k < k1; k += kThreads) {
-    const int p = claimed(k + tid);
-    int t;
-    const int pos = at + scan_cta(p >= 0, t, warp_sums);
-    at += t;
-    if (p >= 0) {
-      if (pos < a.cap) a.free[pos] = p;
-      a.shares[p] = 0;
+  for (int rd = 0; rd < rounds; ++rd) {
+    if (rounds > 1) {
+      look_up(rd);
+      bits = claimed(rd);
     }
+    int t;
+    int pos = at + scan_cta(__popc(bits), t, warp_sums);
+    at += t;
+#pragma unroll
+    for (int e = 0; e < kRun; ++e)
+      if (bits >> e & 1) {
+        if (pos < a.cap) a.free[pos] = page[e];
+        a.shares[page[e]] = 0;
+        ++pos;
+      }
   }
   if (rank == 0) {
-    for (int i = tid; i < a.n; i += kThreads) {
+    for (int i = tid; i < a.n; i += NT) {
       const int r = s_row[i];
       if (r >= 0) a.held[r] = s_from[i];
       a.status[i] = r >= 0 ? 0 : 2;
@@ -198,12 +242,13 @@ __global__ void __launch_bounds__(kThreads) k_page_fork(const ForkArgs a) {
   int* s_src = s_at + a.n + 1;      // [n] source, or -1 when the fork is not made
   int* s_dst = s_src + a.n;         // [n]
   __shared__ int warp_sums[32];
-  const int tid = threadIdx.x, ctas = gridDim.x, rank = blockIdx.x;
+  const int tid = threadIdx.x, NT = blockDim.x, ctas = gridDim.x, rank = blockIdx.x;
   pdl_wait();
+  pdl_launch_next();
   first_of(a.dst, a.n, a.B, s_first);
   const int top = min(max(*a.n_free, 0), a.cap);
   int total = 0, wants = 0;
-  for (int i0 = 0; i0 < a.n; i0 += kThreads) {
+  for (int i0 = 0; i0 < a.n; i0 += NT) {
     const int i = i0 + tid;
     int s = -1, d = -1, len = 0, status = 2, want = 0;
     if (i < a.n) {
@@ -245,14 +290,31 @@ __global__ void __launch_bounds__(kThreads) k_page_fork(const ForkArgs a) {
   }
   if (tid == 0) s_at[a.n] = total;
   cluster_sync();   // held and n_free have been read
-  for (int k = rank * kThreads + tid; k < total; k += ctas * kThreads) {
-    const int i = place_of(s_at, a.n - 1, k), j = k - s_at[i];
-    const int p = a.tables[(size_t)s_src[i] * a.W + j];
-    a.tables[(size_t)s_dst[i] * a.W + j] = p;
-    if (p >= 0 && p < a.P) atomicAdd(&a.shares[p], 1);
+  for (int first = (rank * NT + tid) * kRun; first < total; first += ctas * NT * kRun) {
+    int page[kRun];
+    const int i0 = place_of(s_at, a.n - 1, first);
+    int i = i0;
+#pragma unroll
+    for (int e = 0; e < kRun; ++e) {
+      const int k = first + e;
+      if (k < total) {
+        while (k >= s_at[i + 1]) ++i;
+        page[e] = a.tables[(size_t)s_src[i] * a.W + (k - s_at[i])];
+      }
+    }
+    i = i0;
+#pragma unroll
+    for (int e = 0; e < kRun; ++e) {
+      const int k = first + e;
+      if (k < total) {
+        while (k >= s_at[i + 1]) ++i;
+        a.tables[(size_t)s_dst[i] * a.W + (k - s_at[i])] = page[e];
+        if (page[e] >= 0 && page[e] < a.P) atomicAdd(&a.shares[page[e]], 1);
+      }
+    }
   }
   if (rank == 0) {
-    for (int i = tid; i < a.n; i += kThreads)
+    for (int i = tid; i < a.n; i += NT)
       if (s_src[i] >= 0) a.held[s_dst[i]] = ceil_pages(a.lens[s_src[i]], a.shift);
     if (tid == 0) *a.n_free = top - min(wants, top);
   }
@@ -302,11 +364,12 @@ __global__ void __launch_bounds__(kThreads) k_page_compact(const CompactArgs a) 
   int* s_block = share_smem + words;                            // [blocks + 1]
   int* s_at = s_block + blocks + 1;                             // [B + 1] entries before
   __shared__ int warp_sums[32];
-  const int tid = threadIdx.x, ctas = gridDim.x, rank = blockIdx.x;
+  const int tid = threadIdx.x, NT = blockDim.x, ctas = gridDim.x, rank = blockIdx.x;
   pdl_wait();
-  for (int w = tid; w < words; w += kThreads) s_word[w] = 0;
+  pdl_launch_next();
+  for (int w = tid; w < words; w += NT) s_word[w] = 0;
   int total = 0;
-  for (int b0 = 0; b0 < a.B; b0 += kThreads) {
+  for (int b0 = 0; b0 < a.B; b0 += NT) {
     const int b = b0 + tid;
     int t;
     const int at = total + scan_cta(b < a.B ? min(max(a.held[b], 0), a.W) : 0, t, warp_sums);
@@ -317,13 +380,13 @@ __global__ void __launch_bounds__(kThreads) k_page_compact(const CompactArgs a) 
   __syncthreads();
   // Every CTA marks the pages of its share of the entries; then each joins all
   // marks of its share of the words.
-  for (int k = rank * kThreads + tid; k < total; k += ctas * kThreads) {
+  for (int k = rank * NT + tid; k < total; k += ctas * NT) {
     const int b = place_of(s_at, a.B - 1, k);
     const int p = a.tables[(size_t)b * a.W + (k - s_at[b])];
     if (p >= 0 && p < a.P) atomicOr(&s_word[p >> 5], 1u << (p & 31));
   }
   cluster_sync();
-  for (int w = rank * kThreads + tid; w < words; w += ctas * kThreads) {
+  for (int w = rank * NT + tid; w < words; w += ctas * NT) {
     uint32_t x = 0;
     for (int c = 0; c < ctas; ++c) {
       uint32_t y;
@@ -335,7 +398,7 @@ __global__ void __launch_bounds__(kThreads) k_page_compact(const CompactArgs a) 
   }
   cluster_sync();   // (and all have read the tables)
   int held = 0;
-  for (int q0 = 0; q0 < blocks; q0 += kThreads) {
+  for (int q0 = 0; q0 < blocks; q0 += NT) {
     const int q = q0 + tid;
     int c = 0;
     if (q < blocks)
@@ -350,7 +413,7 @@ __global__ void __launch_bounds__(kThreads) k_page_compact(const CompactArgs a) 
   const Used used{s_word, s_block, blocks};
   const int low = held < a.P ? used.before(held) : held;   // held pages that stay
   auto to = [&](int p) { return p < held ? p : used.unheld(used.before(p) - low); };
-  const int first = rank * kThreads + tid, step = ctas * kThreads;
+  const int first = rank * NT + tid, step = ctas * NT;
   for (int k = first; k < a.B * a.W; k += step) {
     const int b = k / a.W, p = a.tables[k];
     const bool live = k - b * a.W < s_at[b + 1] - s_at[b] && p >= 0 && p < a.P;
@@ -379,9 +442,13 @@ __global__ void __launch_bounds__(kThreads) k_page_compact(const CompactArgs a) 
   }
 }
 
-// Launches a cluster of CTAs, one for little work.
+// Launches a cluster of CTAs, or one small CTA for at most kFew entries and
+// requests (a fork and a release of two requests with 10 pages each: 5.9 us so,
+// 14.7 in clusters; 19000 entries 18 us).
+constexpr long kFew = 4096;
 template <typename Args>
-cudaError_t launch_share(void (*fn)(Args), const Args& a, size_t smem, std::atomic<uint64_t>& ready, cudaStream_t st) {
+cudaError_t launch_share(void (*fn)(Args), const Args& a, long entries, size_t smem, std::atomic<uint64_t>& ready,
+                         cudaStream_t st) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess && (dev >= 64 || !(ready.load(std::memory_order_relaxed) >> dev & 1))) {
@@ -393,11 +460,11 @@ cudaError_t launch_share(void (*fn)(Args), const Args& a, size_t smem, std::atom
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = kCluster;
+  attr[1].val.clusterDim.x = entries <= kFew ? 1 : kCluster;
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(kCluster);
-  cfg.blockDim = dim3(kThreads);
+  cfg.gridDim = dim3(entries <= kFew ? 1 : kCluster);
+  cfg.blockDim = dim3(entries <= kFew ? kFewThreads : kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cfg.attrs = attr;
@@ -440,7 +507,7 @@ extern "C" sf_status sf_page_free(const int32_t* d_requests, const int32_t* d_ke
   static std::atomic<uint64_t> ready{0};
   const FreeArgs a{d_requests, d_keep, n, d_tables, d_held, d_shares, d_free, d_n_free, d_status, batch, table_width,
                    n_pages, capacity, log2_of(page)};
-  const cudaError_t e = launch_share(k_page_free, a, ((size_t)batch + 3 * n + 1) * sizeof(int), ready,
+  const cudaError_t e = launch_share(k_page_free, a, (long)n * table_width + batch, ((size_t)batch + 3 * n + 1) * sizeof(int), ready,
                                      static_cast<cudaStream_t>(cuda_stream));
   if (e != cudaSuccess) return set_error(SF_ERR_CUDA, "sf_page_free: %s", cudaGetErrorString(e));
   return SF_OK;
@@ -461,7 +528,7 @@ extern "C" sf_status sf_page_fork(const int32_t* d_src, const int32_t* d_dst, in
   static std::atomic<uint64_t> ready{0};
   const ForkArgs a{d_src, d_dst, d_lens, n, d_tables, d_held, d_shares, d_free, d_n_free, d_source, d_target, d_slots,
                    d_status, batch, table_width, n_pages, capacity, log2_of(page)};
-  const cudaError_t e = launch_share(k_page_fork, a, ((size_t)batch + 3 * n + 1) * sizeof(int), ready,
+  const cudaError_t e = launch_share(k_page_fork, a, (long)n * table_width + batch, ((size_t)batch + 3 * n + 1) * sizeof(int), ready,
                                      static_cast<cudaStream_t>(cuda_stream));
   if (e != cudaSuccess) return set_error(SF_ERR_CUDA, "sf_page_fork: %s", cudaGetErrorString(e));
   return SF_OK;
@@ -484,7 +551,7 @@ extern "C" sf_status sf_page_compact(const int32_t* d_tables, int32_t batch, int
   const CompactArgs a{d_tables, d_held, d_shares, d_tables_out, d_shares_out, d_free, d_n_free, d_source, d_target,
                       d_count, batch, table_width, n_pages, moves};
   const size_t blocks = ((size_t)n_pages + 255) / 256;
-  const cudaError_t e = launch_share(k_page_compact, a, (9 * blocks + 1 + batch + 1) * sizeof(int), ready,
+  const cudaError_t e = launch_share(k_page_compact, a, (long)batch * table_width + n_pages, (9 * blocks + 1 + batch + 1) * sizeof(int), ready,
                                      static_cast<cudaStream_t>(cuda_stream));
   if (e != cudaSuccess) return set_error(SF_ERR_CUDA, "sf_page_compact: %s", cudaGetErrorString(e));
   return SF_OK;

@@ -16,23 +16,38 @@
 //
 // Order: larger logits first, equal ones by token; a NaN counts as -infinity.
 //
-// Bound by memory: a row is read once.
+// A row is read once; it is one CTA's, or with few rows a cluster's, each CTA a
+// stretch of it, joined through distributed shared memory. 1021 rows of 151665
+// bf16 logits take 74 us (4.2 TB/s), 400 rows of 152064 fp32 ones 48 (5.1), 72
+// rows 13.6 and with 20 alternatives 20.0, one row 6.8 and with five 9.6: few rows
+// are a chain of loads, reductions, the second look and the cluster's barriers;
+// many are bound by memory in fp32, and in 16 bits by the seven or eight
+// instructions of an element. CTAs of 256 threads, four on an SM, so that some
+// stream while others choose (of 512: 1021 rows 89 us, 72 rows 19.1; of 128: 76
+// and 30); four vectors of a thread on their way (two, six CTAs on an SM: 81).
+#include <algorithm>
+#include <type_traits>
+
 #include "paged.h"
 
 namespace sf {
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kGroups = kThreads / 4;   // groups of four threads, for the top alternatives
 constexpr int kMaxTop = 32;
-constexpr int kBuffer = 2048;           // elements that reach the bound; more (rows made for it) are handled apart
+constexpr int kMaxCluster = 8;           // (of 4: one row 8.9 us for 6.8)
+constexpr int kBuffer = 1024;           // elements that reach the bound; more (rows made for it) are handled apart
+constexpr int kAhead = 4;               // vectors that a thread has on their way
 constexpr float kLog2E = 1.44269504088896f;
 
 struct ScoreArgs {
   const void* x;
   long row;
   const int* tokens;
-  int n, vocab, top;
+  long first;             // the launch's first row
+  int ctas, vocab, top;   // (CTAs of a row)
+  // 1: another launch does the rest of the rows. 2: that launch, which starts when the first's last CTAs have: what comes
+  // before both is done then, and it waits for the first one's end before its own.
+  int chain;
   float *logprob, *entropy;
   int *rank, *top_ids;
   float* top_logprobs;
@@ -47,17 +62,102 @@ __device__ __forceinline__ float exp2_fast(float x) {   // relative error 2^-22;
 template <typename T>
 __device__ __forceinline__ float to_float(T v) { return static_cast<float>(v); }
 
-// Sixteen bytes of a row as floats.
+// Pairs of fp32 numbers at once.
+__device__ __forceinline__ uint64_t pair(float x, float y) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(__float_as_uint(x)), "r"(__float_as_uint(y)));
+  return d;
+}
+__device__ __forceinline__ float2 unpair(uint64_t d) {
+  uint32_t x, y;
+  asm("mov.b64 {%0, %1}, %2;" : "=r"(x), "=r"(y) : "l"(d));
+  return make_float2(__uint_as_float(x), __uint_as_float(y));
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {   // NaN if either is
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
+// Sixteen bytes of a row.
 template <typename T>
 struct Vec {
   static constexpr int N = 16 / sizeof(T);
+  using T2 = typename std::conditional<std::is_same<T, bf16>::value, __nv_bfloat162, __half2>::type;
   uint4 w;
+  __device__ __forceinline__ uint32_t word(int i) const { return i == 0 ? w.x : i == 1 ? w.y : i == 2 ? w.z : w.w; }
   __device__ __forceinline__ float get(int i) const {
-    const uint32_t u = (i * (int)sizeof(T)) / 4 == 0 ? w.x : (i * (int)sizeof(T)) / 4 == 1 ? w.y
-                     : (i * (int)sizeof(T)) / 4 == 2 ? w.z : w.w;
+    const uint32_t u = word(i * (int)sizeof(T) / 4);
     if constexpr (sizeof(T) == 4) return __uint_as_float(u);
     else if constexpr (std::is_same<T, bf16>::value) return __uint_as_float(i & 1 ? u & 0xffff0000u : u << 16);
     else return i & 1 ? __high2float(*reinterpret_cast<const __half2*>(&u)) : __low2float(*reinterpret_cast<const __half2*>(&u));
+  }
+  // The larger of its elements and mx (a NaN counts as -infinity); 16 bits: in pairs.
+  static __device__ __forceinline__ float max_of(const Vec (&v)[kAhead]) {
+    if constexpr (sizeof(T) == 4) {
+      float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int u = 0; u < kAhead; u += 2)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) m[i] = fmaxf(fmaxf(m[i], v[u].get(i)), v[u + 1].get(i));
+      return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+    } else {
+      T2 m[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t x = v[0].word(i);
+        m[i] = *reinterpret_cast<const T2*>(&x);
+      }
+#pragma unroll
+      for (int u = 1; u < kAhead; ++u)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t x = v[u].word(i);
+          m[i] = __hmax2(m[i], *reinterpret_cast<const T2*>(&x));
+        }
+      const T2 r = __hmax2(__hmax2(m[0], m[1]), __hmax2(m[2], m[3]));
+      return fmaxf(fmaxf(__low2float(r), __high2float(r)), -INFINITY);   // (two NaN: -infinity)
+    }
+  }
+  // How many of the elements are above `bound` (OR_EQUAL: or equal to it), a number of the type or an infinity.
+  template <bool OR_EQUAL>
+  static __device__ __forceinline__ int above(const Vec (&v)[kAhead], float bound) {
+    int n = 0;
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) n += OR_EQUAL ? v[u].get(i) >= bound : v[u].get(i) > bound;
+    } else {
+      T2 b, sum;
+      if constexpr (std::is_same<T, bf16>::value) b = __float2bfloat162_rn(bound), sum = __float2bfloat162_rn(0.f);
+      else b = __float2half2_rn(bound), sum = __float2half2_rn(0.f);
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t x = v[u].word(i);
+          const T2 y = *reinterpret_cast<const T2*>(&x);
+          sum = __hadd2(sum, OR_EQUAL ? __hge2(y, b) : __hgt2(y, b));   // (ones and zeros; exact)
+        }
+      n = (int)(__low2float(sum) + __high2float(sum));
+    }
+    return n;
   }
 };
 
@@ -75,10 +175,14 @@ struct Sums {
       m = to;
     }
   }
-  __device__ __forceinline__ void add(float x) {   // m is at least x, and finite
-    const float d = x - m, e = exp2_fast(d * kLog2E);
+  __device__ __forceinline__ void add(float x) {   // m is at least x
+    if (m == -INFINITY) {                          // (then it adds nothing; a NaN stays)
+      if (x != x) s = x;
+      return;
+    }
+    const float d = max_nan(x - m, -1.0e30f), e = exp2_fast(d * kLog2E);   // (e = 0 times -infinity is NaN)
     s += e;
-    t = fmaf(e, fmaxf(d, -1.0e30f), t);            // (e = 0 times -infinity is NaN)
+    t = fmaf(e, d, t);
   }
   __device__ __forceinline__ void join(Sums o) {
     const float to = fmaxf(m, o.m);
@@ -101,204 +205,357 @@ __device__ __forceinline__ float key_value(unsigned long long k) {
   return __uint_as_float(u & 0x80000000u ? u & 0x7fffffffu : ~u);
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads) k_token_logprobs(const __grid_constant__ ScoreArgs a) {
+// What a CTA of a cluster leaves for the first one.
+struct Share {
+  Sums sums;
+  int rank;
+  unsigned long long top[kMaxTop];
+};
+
+template <typename T, int kThreads>
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads) k_token_logprobs(const __grid_constant__ ScoreArgs a) {
   using V = Vec<T>;
+  constexpr int kGroups = kThreads / 4;   // groups of four threads, for the top alternatives
   __shared__ Sums s_sums[kThreads / 32];
   __shared__ int s_rank[kThreads / 32];
-  __shared__ float s_max[kGroups];
-  __shared__ int s_first[kGroups];       // (ties at the bound: first token of the group that is equal to it)
+  __shared__ __align__(16) float s_max[kGroups];
+  __shared__ int s_first[kGroups], s_tied[kGroups];   // (ties at the bound: first token of a group that is equal to it)
   __shared__ int s_groups[kMaxTop];      // the groups whose elements are looked at again
-  __shared__ unsigned long long s_bound, s_top[kMaxTop], s_buffer[kBuffer], s_best[kThreads / 32];
+  __shared__ unsigned long long s_bound, s_buffer[kBuffer], s_best[kThreads / 32], s_final[kMaxTop];
   __shared__ int s_count, s_picked, s_ties;
+  __shared__ Share s_share;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, group = tid >> 2;
-  pdl_wait();
-  const long row = blockIdx.x;
+  const int ctas = a.ctas, part = ctas > 1 ? (int)cluster_rank() : 0;
+  if (a.chain < 2) pdl_wait();
+  if (a.chain == 1) pdl_launch_next();
+  const long row = a.first + (ctas > 1 ? blockIdx.x / ctas : blockIdx.x);
   const int token = a.tokens[row];
-  if (token < 0 || token >= a.vocab) return;
   const T* x = static_cast<const T*>(a.x) + row * a.row;
-  // The row as a few elements up to a 16-byte boundary, vectors, a few elements.
+  // The row as a few elements up to a 16-byte boundary, vectors, a few elements:
+  // of the vectors each CTA has a stretch, the first one the rest as well.
   const int head = min(a.vocab, (int)((-reinterpret_cast<uintptr_t>(x) & 15) / sizeof(T)));
   const int nv = (a.vocab - head) / V::N, body = head + nv * V::N;
+  const int v0 = (int)((long)nv * part / ctas), v1 = (int)((long)nv * (part + 1) / ctas);
   const uint4* xv = reinterpret_cast<const uint4*>(x + head);
 
-  // The element or so of the head and the tail that this thread has: a token, or -1.
-  const int odd = tid < head ? tid : tid >= 16 && tid - 16 < a.vocab - body ? body + tid - 16 : -1;
+  // The element of the head or the tail that a thread has: a token, or -1.
+  auto odd_of = [&](int t) {
+    return part > 0 ? -1 : t < head ? t : t >= 16 && t - 16 < a.vocab - body ? body + t - 16 : -1;
+  };
+  // Vectors i, i + kThreads, ... of this thread; behind the stretch: -infinity.
+  const uint32_t none_bits = sizeof(T) == 4 ? 0xff800000u : std::is_same<T, bf16>::value ? 0xff80ff80u : 0xfc00fc00u;
+  auto load = [&](V (&v)[kAhead], int i) {
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      v[u].w = make_uint4(none_bits, none_bits, none_bits, none_bits);
+      if (i + u * kThreads < v1) v[u].w = __ldg(xv + i + u * kThreads);
+    }
+  };
+  int i = v0 + tid;
+  V v[kAhead];
+  load(v, i);                                  // (before the token is known)
+  if (token < 0 || token >= a.vocab) {         // (the whole cluster)
+    if (a.chain == 2) pdl_wait();
+    return;
+  }
+  const int odd = odd_of(tid);
   const float odd_x = odd >= 0 ? to_float(x[odd]) : -INFINITY;
-
-  // In front of the given token: larger logits, equal ones of lower tokens. For
-  // those, equal means above the next lower number. With a given -infinity (or
-  // NaN) every lower token is in front.
-  float given = to_float(x[token]);
-  if (!(given == given)) given = -INFINITY;
+  const float given_x = to_float(x[token]);
+  const float given = given_x == given_x ? given_x : -INFINITY;
+  // In front of the given token: larger logits, equal ones of lower tokens (with
+  // -infinity or NaN given, every lower token, counted at the end).
   const bool all_before = given == -INFINITY;
-  const float above = given;
-  const float before = all_before ? INFINITY : given == 0.f ? -1.0e-45f
-                     : __uint_as_float(__float_as_uint(given) + (given > 0.f ? -1 : 1));
-  int rank = tid == 0 && all_before ? token : 0;
+  const int given_v = token >= head && token < body ? (token - head) / V::N : -1;   // its vector
+  int rank = 0;
+  auto count_one = [&](float f, int v) { rank += all_before ? v > token && f > given : v < token ? f >= given : f > given; };
 
   Sums z = {-INFINITY, 0.f, 0.f};
-  auto odd_nan = [&](float v) { if (v != v) z.s = v; };
   if (odd >= 0) {
     z.raise(odd_x);
-    if (z.m == -INFINITY) odd_nan(odd_x);
-    else z.add(odd_x);
-    rank += odd_x > (odd < token ? before : above);
+    z.add(odd_x);
+    count_one(odd_x, odd);
   }
 #pragma unroll 1
-  for (int i = tid; i < nv; i += kThreads) {
-    const V v = {__ldg(xv + i)};
-    float mx = v.get(0);
-#pragma unroll
-    for (int e = 1; e < V::N; ++e) mx = fmaxf(mx, v.get(e));
-    z.raise(mx);
+  for (; i < v1; i += kAhead * kThreads) {
+    z.raise(V::max_of(v));
     if (z.m == -INFINITY) {
 #pragma unroll
-      for (int e = 0; e < V::N; ++e) odd_nan(v.get(e));
+      for (int u = 0; u < kAhead; ++u)
+#pragma unroll
+        for (int e = 0; e < V::N; ++e) z.add(v[u].get(e));
     } else {
+      const uint64_t m2 = pair(-z.m, -z.m), c2 = pair(kLog2E, kLog2E);
+      uint64_t s2[2] = {pair(z.s, 0.f), 0}, t2[2] = {pair(z.t, 0.f), 0};
 #pragma unroll
-      for (int e = 0; e < V::N; ++e) z.add(v.get(e));
+      for (int u = 0; u < kAhead; ++u)
+#pragma unroll
+        for (int e = 0; e < V::N; e += 2) {
+          float2 d = unpair(add2(pair(v[u].get(e), v[u].get(e + 1)), m2));
+          d.x = max_nan(d.x, -1.0e30f), d.y = max_nan(d.y, -1.0e30f);   // (e = 0 times -infinity is NaN)
+          const uint64_t d2 = pair(d.x, d.y);
+          const float2 y = unpair(mul2(d2, c2));
+          const uint64_t e2 = pair(exp2_fast(y.x), exp2_fast(y.y));
+          s2[e / 2 & 1] = add2(s2[e / 2 & 1], e2);
+          t2[e / 2 & 1] = fma2(e2, d2, t2[e / 2 & 1]);
+        }
+      const float2 s = unpair(add2(s2[0], s2[1])), t = unpair(add2(t2[0], t2[1]));
+      z.s = s.x + s.y;
+      z.t = t.x + t.y;
     }
-    const int v0 = head + i * V::N;
+    if (i + (kAhead - 1) * kThreads < given_v || (given_v < 0 && token >= body)) {   // all of them before it
+      if (!all_before) rank += V::template above<true>(v, given);
+    } else if (i > given_v) {
+      rank += V::template above<false>(v, given);
+    } else {
+#pragma unroll 1
+      for (int u = 0; u < kAhead; ++u)
 #pragma unroll
-    for (int e = 0; e < V::N; ++e) rank += v.get(e) > (v0 + e < token ? before : above);
+        for (int e = 0; e < V::N; ++e)
+          count_one((u == 0 ? v[0] : u == 1 ? v[1] : u == 2 ? v[2] : v[3]).get(e), head + (i + u * kThreads) * V::N + e);
+    }
+    load(v, i + kAhead * kThreads);
   }
+  if (all_before && tid == 0 && part == 0) rank += token;
 
   // ---- join the threads' sums
-  Sums all = z;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    all.join(all.shuffled(o));
-    rank += __shfl_xor_sync(0xffffffffu, rank, o);
-  }
-  if (lane == 0) {
-    s_sums[warp] = all;
-    s_rank[warp] = rank;
-  }
   float gm = z.m;
   gm = fmaxf(gm, __shfl_xor_sync(0xffffffffu, gm, 1));
   gm = fmaxf(gm, __shfl_xor_sync(0xffffffffu, gm, 2));
   if ((tid & 3) == 0) s_max[group] = gm;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    z.join(z.shuffled(o));
+    rank += __shfl_xor_sync(0xffffffffu, rank, o);
+  }
+  if (lane == 0) {
+    s_sums[warp] = z;
+    s_rank[warp] = rank;
+  }
   if (tid == 0) s_count = s_picked = s_ties = 0;
+  if (tid < kMaxTop) s_share.top[tid] = 0;
   __syncthreads();
-  all = s_sums[0];
-  rank = s_rank[0];
-  for (int w = 1; w < kThreads / 32; ++w) {
-    all.join(s_sums[w]);
-    rank += s_rank[w];
+  if (warp == 0) {
+    z = lane < kThreads / 32 ? s_sums[lane] : Sums{-INFINITY, 0.f, 0.f};
+    rank = lane < kThreads / 32 ? s_rank[lane] : 0;
+#pragma unroll
+    for (int o = kThreads / 64; o > 0; o >>= 1) {
+      z.join(z.shuffled(o));
+      rank += __shfl_xor_sync(0xffffffffu, rank, o);
+    }
+    if (lane == 0) {
+      s_share.sums = z;
+      s_share.rank = rank;
+    }
   }
-  // log p = (x - m) - log s; a row of -infinity alone has none above -infinity.
-  const float logs = logf(all.s);
-  auto logp = [&](float v) { return all.m == -INFINITY && all.s == 0.f ? -INFINITY : (v - all.m) - logs; };
-  if (tid == 0) {
-    if (a.logprob) a.logprob[row] = logp(to_float(x[token]));
-    if (a.entropy) a.entropy[row] = all.m == -INFINITY && all.s == 0.f ? 0.f : logs - all.t / all.s;
-    if (a.rank) a.rank[row] = rank;
-  }
-  if (a.top == 0) return;
 
   // ---- the groups with the k largest maxima
   const int k = a.top;
-  int larger = 0, equal = 0;
-  if (tid < kGroups) {
-    const float mine = s_max[tid];
-    for (int g = 0; g < kGroups; ++g) {
-      larger += s_max[g] > mine;
-      equal += s_max[g] == mine;
-    }
-    if (larger < k && larger + equal >= k) {   // the k-th largest
-      s_bound = (unsigned long long)float_key(mine + 0.f) << 32;
-      s_ties = larger + equal > k ? equal : 0;
-    }
-  }
-  __syncthreads();
-  const float at = key_value(s_bound);
-  // The elements of n groups, by the threads of the CTA together.
-  const int per = 4 + (nv + kThreads - 1) / kThreads * 4;   // a group's odd elements and vectors, places for them at least
-  auto each = [&](const int* groups, int n, auto f) {
-    for (int i = tid; i < n * per; i += kThreads) {
-      const int p = i / per, r = i - p * per, g = groups ? groups[p] : p;
-      if (r < 4) {
-        const int t = 4 * g + r;
-        const int v = t < head ? t : t >= 16 && t - 16 < a.vocab - body ? body + t - 16 : -1;
-        if (v >= 0) f(to_float(x[v]), v, g);
-      } else {
-        const int j = (r - 4) / 4 * kThreads + 4 * g + (r & 3);
-        if (j < nv) {
-          const V v = {__ldg(xv + j)};
+  if (k > 0) {
+    const float mine = s_max[group];
+    int larger = 0, equal = 0;
 #pragma unroll
-          for (int e = 0; e < V::N; ++e) f(v.get(e), head + j * V::N + e, g);
+    for (int g = 0; g < kGroups / 16; ++g) {   // (a thread of the group a quarter of them)
+      const float4 o = reinterpret_cast<const float4*>(s_max)[(tid & 3) * (kGroups / 16) + g];
+      larger += (o.x > mine) + (o.y > mine) + (o.z > mine) + (o.w > mine);
+      equal += (o.x == mine) + (o.y == mine) + (o.z == mine) + (o.w == mine);
+    }
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) {
+      larger += __shfl_xor_sync(0xffffffffu, larger, o);
+      equal += __shfl_xor_sync(0xffffffffu, equal, o);
+    }
+    const bool first = (tid & 3) == 0;         // (a group's first thread decides)
+    if (first && larger < k && larger + equal >= k) {   // the k-th largest
+      s_bound = (unsigned long long)float_key(mine + 0.f) << 32;
+      s_ties = larger + equal > k;
+    }
+    __syncthreads();
+    const float at = key_value(s_bound);
+    // The elements of n groups, by the threads of the CTA together (n <= kGroups).
+    const int per = (v1 - v0 + kThreads - 1) / kThreads * 4;   // places for a group's vectors
+    auto each = [&](const int* groups, int n, auto f) {
+      if (tid < 4 * n) {
+        const int g = groups[tid >> 2], w = odd_of(4 * g + (tid & 3));
+        if (w >= 0) f(to_float(x[w]), w, g);
+      }
+#pragma unroll 1
+      for (int j = tid; j < n * per; j += kThreads) {
+        const int p = j / per, r = j - p * per, g = groups[p], w = v0 + (r >> 2) * kThreads + 4 * g + (r & 3);
+        if (w < v1) {
+          const V y = {__ldg(xv + w)};
+#pragma unroll
+          for (int e = 0; e < V::N; ++e) f(y.get(e), head + w * V::N + e, g);
         }
       }
+    };
+    if (s_ties) {   // more maxima equal to the bound than there is room for: the lowest tokens first
+      if (first) s_first[group] = INT32_MAX;
+      if (first && mine == at) s_tied[atomicAdd(&s_count, 1)] = group;
+      __syncthreads();
+      each(s_tied, s_count, [&](float v, int t, int g) {
+        if ((v == v ? v : -INFINITY) == at) atomicMin(&s_first[g], t);
+      });
+      __syncthreads();
+      if (tid == 0) s_count = 0;
+      if (first && mine == at) {
+        int before_me = larger;
+        for (int g = 0; g < kGroups; ++g) before_me += s_max[g] == at && s_first[g] < s_first[group];
+        if (before_me < k && s_first[group] != INT32_MAX) s_groups[atomicAdd(&s_picked, 1)] = group;   // (not one without elements)
+        if (before_me == k - 1 && s_first[group] != INT32_MAX) s_bound = order_key(at, s_first[group]);
+      } else if (first && larger < k) {
+        s_groups[atomicAdd(&s_picked, 1)] = group;
+      }
+    } else if (first && mine >= at) {
+      s_groups[atomicAdd(&s_picked, 1)] = group;
     }
-  };
-  if (s_ties) {   // more maxima equal to the bound than there is room for: the lowest tokens first
-    if (tid < kGroups) s_first[tid] = INT32_MAX;
     __syncthreads();
-    each(nullptr, kGroups, [&](float v, int t, int g) {
-      if (s_max[g] == at && (v == v ? v : -INFINITY) == at) atomicMin(&s_first[g], t);
+
+    // ---- their elements from the bound on, put in order
+    const unsigned long long bound = s_bound;
+    each(s_groups, s_picked, [&](float v, int t, int) {
+      const unsigned long long key = order_key(v, t);
+      if (key >= bound) {
+        const int c = atomicAdd(&s_count, 1);
+        if (c < kBuffer) s_buffer[c] = key;
+      }
     });
     __syncthreads();
-    if (tid < kGroups && s_max[tid] == at) {
-      int before_me = larger;
-      for (int g = 0; g < kGroups; ++g) before_me += s_max[g] == at && s_first[g] < s_first[tid];
-      if (before_me < k && s_first[tid] != INT32_MAX) s_groups[atomicAdd(&s_picked, 1)] = tid;   // (not one without elements)
-      if (before_me == k - 1 && s_first[tid] != INT32_MAX) s_bound = order_key(at, s_first[tid]);
-    } else if (tid < kGroups && larger < k) {
-      s_groups[atomicAdd(&s_picked, 1)] = tid;
-    }
-  } else if (tid < kGroups && s_max[tid] >= at) {
-    s_groups[atomicAdd(&s_picked, 1)] = tid;
-  }
-  __syncthreads();
-
-  // ---- their elements from the bound on, put in order
-  const unsigned long long bound = s_bound;
-  each(s_groups, s_picked, [&](float v, int t, int) {
-    const unsigned long long key = order_key(v, t);
-    if (key >= bound) {
-      const int c = atomicAdd(&s_count, 1);
-      if (c < kBuffer) s_buffer[c] = key;
-    }
-  });
-  if (tid < k) s_top[tid] = 0;
-  __syncthreads();
-  const int count = s_count;
-  if (count <= kBuffer) {
-    for (int c = tid; c < count; c += kThreads) {
-      const unsigned long long mine = s_buffer[c];
-      int r = 0;
-      for (int i = 0; i < count; ++i) r += s_buffer[i] > mine;
-      if (r < k) s_top[r] = mine;
-    }
-  } else {   // one after the other
-    unsigned long long last = ~0ull;
-    for (int r = 0; r < k; ++r) {
-      unsigned long long best = 0;
-      each(s_groups, s_picked, [&](float v, int t, int) {
-        const unsigned long long key = order_key(v, t);
-        if (key < last && key > best) best = key;
-      });
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        const unsigned long long u = __shfl_xor_sync(0xffffffffu, best, o);
-        best = u > best ? u : best;
+    const int count = s_count;
+    if (count <= kBuffer) {
+      for (int c = tid; c < count; c += kThreads) {
+        const unsigned long long key = s_buffer[c];
+        int r = 0;
+        for (int j = 0; j < count; ++j) r += s_buffer[j] > key;
+        if (r < k) s_share.top[r] = key;
       }
-      if (lane == 0) s_best[warp] = best;
-      __syncthreads();
-      best = s_best[0];
-      for (int w = 1; w < kThreads / 32; ++w) best = s_best[w] > best ? s_best[w] : best;
-      if (tid == 0) s_top[r] = best;
-      last = best;
-      __syncthreads();
+    } else {   // one after the other
+      unsigned long long last = ~0ull;
+      for (int r = 0; r < k; ++r) {
+        unsigned long long best = 0;
+        each(s_groups, s_picked, [&](float v, int t, int) {
+          const unsigned long long key = order_key(v, t);
+          if (key < last && key > best) best = key;
+        });
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+          const unsigned long long u = __shfl_xor_sync(0xffffffffu, best, o);
+          best = u > best ? u : best;
+        }
+        if (lane == 0) s_best[warp] = best;
+        __syncthreads();
+        best = s_best[0];
+        for (int w = 1; w < kThreads / 32; ++w) best = s_best[w] > best ? s_best[w] : best;
+        if (tid == 0) s_share.top[r] = best;
+        last = best;
+        __syncthreads();
+      }
     }
   }
-  __syncthreads();
+
+  // ---- the cluster's shares, joined by its first CTA
+  const unsigned long long* top = s_share.top;
+  if (ctas > 1) {
+    cluster_sync();
+    if (part == 0) {
+      if (k > 0) {
+        for (int c = tid; c < ctas * k; c += kThreads) {
+          unsigned long long key;
+          asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(key) : "r"(dsmem_addr(smem_u32(&s_share.top[c % k]), c / k)) : "memory");
+          s_buffer[c] = key;
+        }
+        __syncthreads();
+        for (int c = tid; c < ctas * k; c += kThreads) {
+          const unsigned long long key = s_buffer[c];
+          if (key == 0) continue;              // (a stretch of fewer than k elements)
+          int r = 0;                           // the larger ones, list by list (each in order)
+          for (int q = 0; q < ctas; ++q) {
+            int lo = 0;
+#pragma unroll
+            for (int step = kMaxTop / 2; step > 0; step >>= 1)
+              if (lo + step <= k && s_buffer[q * k + lo + step - 1] > key) lo += step;
+            if (lo < k && s_buffer[q * k + lo] > key) ++lo;
+            r += lo;
+          }
+          if (r < k) s_final[r] = key;
+        }
+        top = s_final;
+      }
+      if (tid < ctas) {
+        const uint32_t at = dsmem_addr(smem_u32(&s_share), tid);
+        s_sums[tid] = {ld_dsmem(at), ld_dsmem(at + 4), ld_dsmem(at + 8)};
+        s_rank[tid] = __float_as_int(ld_dsmem(at + 12));
+      }
+      __syncthreads();
+      if (tid == 0) {
+        z = s_sums[0];
+        rank = s_rank[0];
+        for (int c = 1; c < ctas; ++c) {
+          z.join(s_sums[c]);
+          rank += s_rank[c];
+        }
+        s_share.sums = z;
+        s_share.rank = rank;
+      }
+    }
+    cluster_sync();   // (the shares have been read)
+    if (part > 0) {
+      if (a.chain == 2) pdl_wait();
+      return;
+    }
+  } else {
+    __syncthreads();
+  }
+  // log p = (x - m) - log s; a row of -infinity alone has none above -infinity.
+  const Sums all = s_share.sums;
+  const bool none = all.m == -INFINITY && all.s == 0.f;
+  const float logs = logf(all.s);
+  auto logp = [&](float v) { return none ? -INFINITY : (v - all.m) - logs; };
+  if (tid == 0) {
+    if (a.logprob) a.logprob[row] = logp(given_x);
+    if (a.entropy) a.entropy[row] = none ? 0.f : logs - all.t / all.s;
+    if (a.rank) a.rank[row] = s_share.rank;
+  }
   if (tid < k) {
-    const unsigned long long key = s_top[tid];
+    const unsigned long long key = top[tid];
     if (a.top_ids) a.top_ids[row * k + tid] = key_index(key);
     if (a.top_logprobs) a.top_logprobs[row * k + tid] = logp(key_value(key));
   }
+  if (a.chain == 2) pdl_wait();
+}
+
+constexpr int kCtaThreads = 256;
+
+// CTAs of a row for n rows, `slots` CTAs at a time: the least waves times a
+// CTA's share of the row and what it takes beside that (0.15 of a long row).
+int ctas_of(long n, int vocab, long slots) {
+  int best = 1;
+  double least = 1e30;
+  for (int c = 1; c <= kMaxCluster && (c == 1 || vocab / c >= 4096); c *= 2) {
+    const double cost = (double)((n * c + slots - 1) / slots) * (1.0 / c + 0.15);
+    if (cost < least) least = cost, best = c;
+  }
+  return best;
+}
+
+// Rows first .. first + n - 1.
+cudaError_t launch_rows(ScoreArgs a, int dtype, long first, long n, int ctas, cudaStream_t st) {
+  a.first = first;
+  a.ctas = ctas;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = ctas;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(n * ctas));
+  cfg.blockDim = dim3(kCtaThreads);
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = ctas > 1 ? 2 : 1;
+  return dtype == SF_DT_F32    ? cudaLaunchKernelEx(&cfg, k_token_logprobs<float, kCtaThreads>, a)
+         : dtype == SF_DT_BF16 ? cudaLaunchKernelEx(&cfg, k_token_logprobs<bf16, kCtaThreads>, a)
+                               : cudaLaunchKernelEx(&cfg, k_token_logprobs<__half, kCtaThreads>, a);
 }
 
 }  // namespace
@@ -321,19 +578,23 @@ extern "C" sf_status sf_token_logprobs(const void* d_logits, int32_t dtype, int6
     return set_error(SF_ERR_ARG, "sf_token_logprobs: null logits or tokens, or logits not aligned to their type");
   if (row_stride < 0 || row_stride > (int64_t(1) << 38))
     return set_error(SF_ERR_ARG, "sf_token_logprobs: the row stride must be in 0..2^38");
-  ScoreArgs a{d_logits, row_stride, d_tokens, n, vocab, top, d_logprob, d_entropy, d_rank, d_top_ids, d_top_logprobs};
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(n);
-  cfg.blockDim = dim3(kThreads);
-  cfg.stream = static_cast<cudaStream_t>(cuda_stream);
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  const cudaError_t e = dtype == SF_DT_F32    ? cudaLaunchKernelEx(&cfg, k_token_logprobs<float>, a)
-                        : dtype == SF_DT_BF16 ? cudaLaunchKernelEx(&cfg, k_token_logprobs<bf16>, a)
-                                              : cudaLaunchKernelEx(&cfg, k_token_logprobs<__half>, a);
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return set_error(SF_ERR_CUDA, "sf_token_logprobs: %s", cudaGetErrorString(e));
+  ScoreArgs a{d_logits, row_stride, d_tokens, 0, 1, vocab, top, 0, d_logprob, d_entropy, d_rank, d_top_ids, d_top_logprobs};
+  // Whole waves of rows, a CTA each, then the rest spread over the GPU.
+  const long slots = (long)sms * (1024 / kCtaThreads), rest = n > slots ? n % slots : n;
+  const cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
+  const int ctas = rest ? ctas_of(rest, vocab, slots) : 1;
+  if (rest < n && ctas > 1) {
+    a.chain = 1;
+    e = launch_rows(a, dtype, 0, n - rest, 1, st);
+    a.chain = 2;
+    if (e == cudaSuccess) e = launch_rows(a, dtype, n - rest, rest, ctas, st);
+  } else {
+    e = launch_rows(a, dtype, 0, n, ctas, st);
+  }
   if (e != cudaSuccess) return set_error(SF_ERR_CUDA, "sf_token_logprobs: %s", cudaGetErrorString(e));
   return SF_OK;
 }

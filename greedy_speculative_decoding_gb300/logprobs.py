@@ -6,7 +6,8 @@ from typing import NamedTuple
 import torch
 
 from . import _lib as L
-from .paged import _binding, _device, _empty
+from . import paged
+from .paged import _device, _empty
 
 
 class TokenLogprobs(NamedTuple):
@@ -30,16 +31,18 @@ def token_logprobs(logits, tokens, top: int = 0, logprob=None, entropy=None, ran
     the vocabulary (-1, say) are padding: nothing is written for them, so what
     is allocated here is undefined there. Work is enqueued on ``stream``
     (default: the current stream); there is no gradient."""
-    call = _binding().token_logprobs
+    call = (paged._native or paged._binding()).token_logprobs
     dev, st = _device(stream)
-    n = logits.shape[0]
-    logprob, entropy = (_empty(n, torch.float32, dev, stream) if x is None else x for x in (logprob, entropy))
+    if logprob is None:
+        logprob = _empty(logits.shape[0], torch.float32, dev, stream)
+    if entropy is None:
+        entropy = _empty(logits.shape[0], torch.float32, dev, stream)
     if rank is None:
-        rank = _empty(n, torch.int32, dev, stream)
+        rank = _empty(logits.shape[0], torch.int32, dev, stream)
     if top_ids is None:
-        top_ids = _empty((n, top), torch.int32, dev, stream)
+        top_ids = _empty((logits.shape[0], top), torch.int32, dev, stream)
     if top_logprobs is None:
-        top_logprobs = _empty((n, top), torch.float32, dev, stream)
+        top_logprobs = _empty((logits.shape[0], top), torch.float32, dev, stream)
     s = call(dev, st, top, logits, tokens, logprob, entropy, rank, top_ids, top_logprobs)
     if s:
         L.check(s)

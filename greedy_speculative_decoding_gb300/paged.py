@@ -254,8 +254,14 @@ def page_fork(src, dst, lens, tables, held, shares, free, n_free, page, source=N
     source, target, slots and status int32 [n] are allocated unless given."""
     call = (_native or _binding()).page_fork
     dev, st = _device(stream)
-    source, target, slots, status = (_empty(src.shape, torch.int32, dev, stream) if x is None else x
-                                     for x in (source, target, slots, status))
+    if source is None:
+        source = _empty(src.shape, torch.int32, dev, stream)
+    if target is None:
+        target = _empty(src.shape, torch.int32, dev, stream)
+    if slots is None:
+        slots = _empty(src.shape, torch.int32, dev, stream)
+    if status is None:
+        status = _empty(src.shape, torch.int32, dev, stream)
     s = call(dev, st, page, src, dst, lens, tables, held, shares, free, n_free, source, target, slots, status)
     if s:
         L.check(s)
@@ -271,10 +277,16 @@ def page_compact(tables, held, shares, free, n_free, tables_out=None, shares_out
     are allocated unless given."""
     call = (_native or _binding()).page_compact
     dev, st = _device(stream)
-    tables_out = tables if tables_out is None else tables_out
-    shares_out = shares if shares_out is None else shares_out
-    source, target = (_empty(shares.shape[0] // 2, torch.int32, dev, stream) if x is None else x for x in (source, target))
-    count = _empty(1, torch.int32, dev, stream) if count is None else count
+    if tables_out is None:
+        tables_out = tables
+    if shares_out is None:
+        shares_out = shares
+    if source is None:
+        source = _empty(shares.shape[0] // 2, torch.int32, dev, stream)
+    if target is None:
+        target = _empty(shares.shape[0] // 2, torch.int32, dev, stream)
+    if count is None:
+        count = _empty(1, torch.int32, dev, stream)
     s = call(dev, st, tables, held, shares, tables_out, shares_out, free, n_free, source, target, count)
     if s:
         L.check(s)
