@@ -97,11 +97,12 @@ sf_rows rows_of(PyObject* o, const char* name, int64_t n, int64_t hd, int dev) {
   return r;
 }
 
-sf_paged_cache layer_of(const at::Tensor& k, const at::Tensor& v, int dev) {
+/* The cache, or its first layer where the tensors have `layers` (0 or 1) dimensions in front. */
+sf_paged_cache layer_of(const at::Tensor& k, const at::Tensor& v, int dev, int layers = 0) {
   const int dt = sf_type(k.scalar_type());
-  bool good = dt >= 0 && k.scalar_type() == v.scalar_type() && k.dim() == 4 && k.sizes() == v.sizes() &&
-              on_device(k, dev) && on_device(v, dev) && k.stride(3) == 1 && v.stride(3) == 1;
-  for (int i = 0; good && i < 4; ++i) good = k.size(i) <= INT32_MAX;
+  bool good = dt >= 0 && k.scalar_type() == v.scalar_type() && k.dim() == 4 + layers && k.sizes() == v.sizes() &&
+              on_device(k, dev) && on_device(v, dev) && k.stride(3 + layers) == 1 && v.stride(3 + layers) == 1;
+  for (int i = 0; good && i < 4 + layers; ++i) good = k.size(i) <= INT32_MAX;
   if (!good) {
     char text[160];
     snprintf(text, sizeof(text), "k and v [pages, kv_heads, page, head_dim] of one shape and type on cuda:%d, the last "
@@ -112,12 +113,12 @@ sf_paged_cache layer_of(const at::Tensor& k, const at::Tensor& v, int dev) {
   c.k = k.data_ptr();
   c.v = v.data_ptr();
   c.dtype = dt;
-  c.n_pages = (int32_t)k.size(0);
-  c.n_kv_heads = (int32_t)k.size(1);
-  c.page = (int32_t)k.size(2);
-  c.head_dim = (int32_t)k.size(3);
-  c.k_page = k.stride(0), c.k_head = k.stride(1), c.k_slot = k.stride(2);
-  c.v_page = v.stride(0), c.v_head = v.stride(1), c.v_slot = v.stride(2);
+  c.n_pages = (int32_t)k.size(layers);
+  c.n_kv_heads = (int32_t)k.size(layers + 1);
+  c.page = (int32_t)k.size(layers + 2);
+  c.head_dim = (int32_t)k.size(layers + 3);
+  c.k_page = k.stride(layers), c.k_head = k.stride(layers + 1), c.k_slot = k.stride(layers + 2);
+  c.v_page = v.stride(layers), c.v_head = v.stride(layers + 1), c.v_slot = v.stride(layers + 2);
   return c;
 }
 
@@ -304,18 +305,9 @@ sf_status page_compact(PyObject* const* a) {
 sf_status page_copy(PyObject* const* a) {
   const int dev = (int)integer(a[0], "device", 0, INT32_MAX);
   const at::Tensor &k = tensor(a[4], "k_cache"), &v = tensor(a[5], "v_cache");
-  const bool deep = k.dim() == 5 && v.dim() == 5;   // [layers, ...]
-  sf_paged_cache cache;
-  int64_t layers = 1;
-  if (deep) {
-    layers = k.size(0);
-    if (v.size(0) != layers || layers < 1 || layers > INT32_MAX)
-      wrong("v_cache", "as many layers as k_cache, one at least", v);
-    const at::Tensor k0 = k.select(0, 0), v0 = v.select(0, 0);
-    cache = layer_of(k0, v0, dev);
-  } else {
-    cache = layer_of(k, v, dev);
-  }
+  const bool deep = k.dim() == 5;   // [layers, ...]
+  const sf_paged_cache cache = layer_of(k, v, dev, deep);
+  const int64_t layers = deep ? k.size(0) : 1;
   const int64_t n = size_of(a[2], "source");
   const sf_status s = sf_page_copy(&cache, (int32_t)layers, deep ? k.stride(0) : 0, deep ? v.stride(0) : 0,
                                    ints(a[2], "source", dev, n), ints(a[3], "target", dev, n),
