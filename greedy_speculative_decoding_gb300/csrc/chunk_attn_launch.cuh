@@ -12,7 +12,15 @@ template <int HD, typename TC>
 cudaError_t launch_chunk(Args& a, int sms, long max_units, cudaStream_t st) {
   using S = ChunkShape<HD, TC>;
   static std::atomic<uint64_t> ready{0};
-  return launch<HD, TC, S::MT>(k_chunk_attn<HD, TC>, S::kThreads, S::kSmem, S::kPiece, ready, a, sms, 1, max_units, st);
+  cudaLaunchConfig_t cfg;
+  cudaLaunchAttribute attr[1];
+  const cudaError_t e = launch_main(k_chunk_attn<HD, TC>, S::kThreads, S::kSmem, S::kPiece, ready, a, sms, 1, max_units,
+                                    st, cfg, attr);
+  if (e != cudaSuccess) return e;
+  cfg.gridDim.y = (a.mt_max + kChunkJoinQueries - 1) / kChunkJoinQueries;
+  cfg.blockDim = dim3(kChunkJoinThreads);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, k_chunk_join<HD, TC>, a);
 }
 
 template <int HD>

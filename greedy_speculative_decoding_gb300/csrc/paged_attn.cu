@@ -156,7 +156,6 @@ static cudaError_t enqueue_chunk(Args& a, const sf_paged_cache& c, int q_dtype, 
   a.mt_max = (int)std::min<long>(queries, kChunkQueries);
   a.ntq_max = (int)((queries + kChunkQueries - 1) / kChunkQueries);
   const long items = (long)a.B * a.nkv * a.ntq_max;
-  a.by_item = items <= kMaxDesc;
   const Layout lay = layout(a.nq, a.nkv, c.head_dim, a.max_rows);
   unsigned char* ws = static_cast<unsigned char*>(workspace);
   a.desc = reinterpret_cast<int4*>(ws);

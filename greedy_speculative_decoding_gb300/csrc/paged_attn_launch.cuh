@@ -9,10 +9,10 @@
 namespace sf {
 namespace pa {
 
-// Launch a main kernel (`ctas` CTAs an SM) and the join.
-template <int HD, typename TQ, int MT>
-cudaError_t launch(void (*fn)(Args), int threads, int smem, int piece, std::atomic<uint64_t>& ready, Args& a,
-                   int sms, int ctas, long max_units, cudaStream_t st) {
+// Launch a main kernel (`ctas` CTAs an SM); leaves the launch's configuration.
+inline cudaError_t launch_main(void (*fn)(Args), int threads, int smem, int piece, std::atomic<uint64_t>& ready, Args& a,
+                               int sms, int ctas, long max_units, cudaStream_t st, cudaLaunchConfig_t& cfg,
+                               cudaLaunchAttribute (&attr)[1]) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -29,18 +29,28 @@ cudaError_t launch(void (*fn)(Args), int threads, int smem, int piece, std::atom
   const int grid = (int)(max_units < most ? max_units : most);
   // Many parts an item, and not so many queries that their CTAs come in waves.
   a.wide = items * 8 <= grid && items * a.mt_max <= 1024;
-  cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
+  cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if ((e = cudaLaunchKernelEx(&cfg, fn, a)) != cudaSuccess) return e;
-  cfg.gridDim = dim3(a.by_item ? (int)items : grid, a.wide ? a.mt_max : (a.mt_max + 3) / 4);
+  return cudaLaunchKernelEx(&cfg, fn, a);
+}
+
+// A main kernel and the join.
+template <int HD, typename TQ, int MT>
+cudaError_t launch(void (*fn)(Args), int threads, int smem, int piece, std::atomic<uint64_t>& ready, Args& a,
+                   int sms, int ctas, long max_units, cudaStream_t st) {
+  cudaLaunchConfig_t cfg;
+  cudaLaunchAttribute attr[1];
+  const cudaError_t e = launch_main(fn, threads, smem, piece, ready, a, sms, ctas, max_units, st, cfg, attr);
+  if (e != cudaSuccess) return e;
+  if (a.by_item) cfg.gridDim.x = (unsigned)((long)a.B * a.nkv * a.ntq_max);
+  cfg.gridDim.y = a.wide ? a.mt_max : (a.mt_max + 3) / 4;
   cfg.blockDim = dim3(kJoinThreads);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, k_paged_join<HD, TQ, MT>, a);
