@@ -71,7 +71,9 @@ struct Sizes {
   long units, items;
   int mt, ntq;
 };
-static Sizes sizes(const sf_paged_cache& c, int n_heads, int max_rows, int q_dtype, int batch, int table_width, int sms) {
+// `chunk`: for chunk_attention, whose requests have many rows.
+static Sizes sizes(const sf_paged_cache& c, int n_heads, int max_rows, int q_dtype, int batch, int table_width, int sms,
+                   bool chunk) {
   Sizes z;
   const int queries = max_rows * (n_heads / c.n_kv_heads);
   z.units = std::max(1l, ((long)table_width * c.page + kTile - 1) / kTile);
@@ -95,7 +97,11 @@ static Sizes sizes(const sf_paged_cache& c, int n_heads, int max_rows, int q_dty
   // fp16 queries 16.5 and 19.1.
   if (queries <= 16) z.mt = 16;
   else if (q_dtype != SF_DT_F32) z.mt = queries > 32 && total(128) >= (c.head_dim == 64 ? 4096 : 2 * sms) ? 128 : 32;
-  else if (queries > 32) z.mt = total(16) >= 4000 ? 128 : 16;
+  // (fp32 chunks, 16 / 128, requests x rows of tokens: head dimension 128, 28 / 4
+  // heads 1 x 150 of 150, total(16) 792, 16.7 / 25.4; 1 x 100 of 1000, 2816, 26.6 /
+  // 22.1; 1 x 256 of 512, 3584, 40.5 / 29.4; 64, 14 / 2: 4 x 100 of 300, 1760, 17.2 /
+  // 20.4; 1 x 512 of 512, 3584, 29.5 / 23.7)
+  else if (queries > 32) z.mt = total(16) >= (chunk ? 2200 : 4000) ? 128 : 16;
   else z.mt = total(16) < 8192 ? 16 : c.head_dim == 64 ? 32 : 128;
   z.ntq = (queries + z.mt - 1) / z.mt;
   z.items = items(z.mt);
@@ -103,8 +109,8 @@ static Sizes sizes(const sf_paged_cache& c, int n_heads, int max_rows, int q_dty
 }
 // The kernel counts a request's units in 32 bits.
 static bool units_fit(const sf_paged_cache& c, int n_heads, int max_rows, int q_dtype, int batch, int table_width,
-                      int sms) {
-  const Sizes z = sizes(c, n_heads, max_rows, q_dtype, batch, table_width, sms);
+                      int sms, bool chunk) {
+  const Sizes z = sizes(c, n_heads, max_rows, q_dtype, batch, table_width, sms, chunk);
   return c.n_kv_heads * (long)z.ntq * (z.units + kMaxPiece) <= INT32_MAX;
 }
 
@@ -124,10 +130,10 @@ static cudaError_t describe_cache(Args& a, const sf_paged_cache& c, int q_dtype,
 
 // Enqueue a checked call: `a` holds rows, tables and lengths.
 static cudaError_t enqueue(Args& a, const sf_paged_cache& c, int q_dtype, float scale, void* workspace, int sms,
-                           cudaStream_t st) {
+                           cudaStream_t st, bool chunk = false) {
   const cudaError_t e = describe_cache(a, c, q_dtype, scale, kTile);
   if (e != cudaSuccess) return e;
-  const Sizes z = sizes(c, a.nq, a.max_rows, q_dtype, a.B, a.W, sms);
+  const Sizes z = sizes(c, a.nq, a.max_rows, q_dtype, a.B, a.W, sms, chunk);
   a.mt = z.mt;
   a.mt_max = std::min(a.max_rows * a.group, a.mt);
   a.ntq_max = z.ntq;
@@ -291,14 +297,17 @@ static sf_status attention(const char* who, int most_rows, const sf_paged_cache*
   a.tables = d_tables, a.lens = d_lens, a.starts = d_starts;
   a.mask = reinterpret_cast<const unsigned long long*>(d_mask);
   a.B = batch, a.N = n, a.W = table_width, a.nq = q->n_heads, a.max_rows = max_rows, a.rows_each = n / batch;
-  const bool chunk = most_rows == kMaxChunk && q->dtype != SF_DT_F32 &&
-                     !pa::little_chunk(*cache, q->n_heads, max_rows, batch, table_width);
-  if (chunk ? !pa::chunk_fits(*cache, q->n_heads, max_rows, table_width)
-            : !pa::units_fit(*cache, q->n_heads, max_rows, q->dtype, batch, table_width, sms))
+  const bool chunk = most_rows == kMaxChunk;
+  if (chunk) max_rows = a.max_rows = std::min(max_rows, n);   // (the choice of the kernel follows it)
+  const bool chunk_kernel = chunk && q->dtype != SF_DT_F32 &&
+                            !pa::little_chunk(*cache, q->n_heads, max_rows, batch, table_width);
+  if (chunk_kernel ? !pa::chunk_fits(*cache, q->n_heads, max_rows, table_width)
+                   : !pa::units_fit(*cache, q->n_heads, max_rows, q->dtype, batch, table_width, sms, chunk))
     return set_error(SF_ERR_UNSUPPORTED, "%s: table_width * page too large for this many heads and rows", who);
+  const cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
   if (e == cudaSuccess)
-    e = (chunk ? pa::enqueue_chunk : pa::enqueue)(a, *cache, q->dtype, scale, d_workspace, sms,
-                                                  static_cast<cudaStream_t>(cuda_stream));
+    e = chunk_kernel ? pa::enqueue_chunk(a, *cache, q->dtype, scale, d_workspace, sms, st)
+                     : pa::enqueue(a, *cache, q->dtype, scale, d_workspace, sms, st, chunk);
   if (e != cudaSuccess) return set_error(SF_ERR_CUDA, "%s: %s", who, cudaGetErrorString(e));
   return SF_OK;
 }

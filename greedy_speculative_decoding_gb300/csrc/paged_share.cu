@@ -443,8 +443,9 @@ __global__ void __launch_bounds__(kThreads) k_page_compact(const CompactArgs a) 
 }
 
 // Launches a cluster of CTAs, or one small CTA for at most kFew entries and
-// requests (a fork and a release of two requests with 10 pages each: 5.9 us so,
-// 14.7 in clusters; 19000 entries 18 us).
+// requests (us, one CTA and a cluster: a release that finds nothing 4.6 and 6.2, a
+// compaction of 97 pages 5.3 and 6.1; a release and a fork of 256 requests with
+// 18997 entries 131 and 29, a compaction of 50191 pages 470 and 30).
 constexpr long kFew = 4096;
 template <typename Args>
 cudaError_t launch_share(void (*fn)(Args), const Args& a, long entries, size_t smem, std::atomic<uint64_t>& ready,
