@@ -45,8 +45,12 @@ struct ScoreArgs {
   const int* tokens;
   long first;             // the launch's first row
   int ctas, vocab, top;   // (CTAs of a row)
-  // 1: another launch does the rest of the rows. 2: that launch, which starts when the first's last CTAs have: what comes
-  // before both is done then, and it waits for the first one's end before its own.
+  // 1: another launch does the rest of the rows. 2: that launch. It starts when
+  // every CTA of the first has waited for what comes before both, so that is
+  // done, and it touches nothing that the first one writes; before its own end it
+  // waits for the first one's, as what follows looks at the second alone. (620
+  // rows of 152064 bf16 logits 52 us; with the wait in front of its reads 62, both
+  // in one launch of clusters 67.)
   int chain;
   float *logprob, *entropy;
   int *rank, *top_ids;

@@ -191,6 +191,44 @@ def test_same_result_in_every_run_and_on_another_stream(pkg):
     assert all(torch.equal(p, q) for p, q in zip(outs, pkg.token_logprobs(x, tokens, top=32)))
 
 
+@pytest.mark.parametrize("n", [607, 609, 640, 700, 1300])
+def test_passes_behind_one_another(pkg, n):
+    """Logits written by the kernel before, results read by the one behind, at
+    sizes that take whole waves of rows and a rest; padding in both."""
+    tokens = i32(pick(23, n, 20011))
+    tokens[::5] = -1
+    outs = [torch.zeros_like(y) for y in pkg.token_logprobs(rand(24, n, 20011, BF), tokens, top=3)]   # (padding: left)
+    xs = [rand(25 + i, n, 20011, BF) for i in range(6)]
+    want = [[y.clone() for y in pkg.token_logprobs(x, tokens, 3, *outs)] for x in xs]
+    torch.cuda.synchronize()
+    x, got = torch.empty_like(xs[0]), []
+    for src in xs:
+        x.copy_(src)
+        pkg.token_logprobs(x, tokens, 3, *outs)
+        got.append([y.clone() for y in outs])
+    for a, b in zip(got, want):
+        assert all(torch.equal(p, q) for p, q in zip(a, b))
+
+
+def test_the_engines_verify_logits(pkg):
+    """The target's choices are the logits' first ones; their log probabilities as
+    the oracle has them from the same logits."""
+    from synth import TINY_TARGET, make_weights
+    shape, V = TINY_TARGET, TINY_TARGET.vocab
+    eng = pkg.SpecEngine(shape, make_weights(shape, seed=11, device="cuda"), batch=2, K=4, s_max=128)
+    eng.prefill([list(range(1, 30)), [5, 9, 5, 9, 5, 9, 5]])
+    eng.set_drafter(pkg.SF_DRAFT_NGRAM, 2, 4)
+    eng.ngram_draft(4)
+    choice = torch.empty(2, 5, dtype=torch.int32, device="cuda")
+    logits = torch.empty(2, 5, V, device="cuda")
+    eng.verify(choice, logits)
+    got = check(pkg, logits.view(10, V), choice.view(-1).tolist(), min(V, 8))
+    assert bool((got.rank == 0).all()) and torch.equal(got.top_ids[:, 0], choice.view(-1))
+    assert torch.equal(got.top_logprobs[:, 0], got.logprob)
+    eng.accept_rollback()
+    eng.close()
+
+
 def test_outputs_left_out(pkg):
     import ctypes
     from greedy_speculative_decoding_gb300 import _lib as L
