@@ -17,14 +17,19 @@
 // Order: larger logits first, equal ones by token; a NaN counts as -infinity.
 //
 // A row is read once; it is one CTA's, or with few rows a cluster's, each CTA a
-// stretch of it, joined through distributed shared memory. 1021 rows of 151665
-// bf16 logits take 74 us (4.2 TB/s), 400 rows of 152064 fp32 ones 48 (5.1), 72
-// rows 13.6 and with 20 alternatives 20.0, one row 6.8 and with five 9.6: few rows
-// are a chain of loads, reductions, the second look and the cluster's barriers;
-// many are bound by memory in fp32, and in 16 bits by the seven or eight
-// instructions of an element. CTAs of 256 threads, four on an SM, so that some
-// stream while others choose (of 512: 1021 rows 89 us, 72 rows 19.1; of 128: 76
-// and 30); four vectors of a thread on their way (two, six CTAs on an SM: 81).
+// stretch of it, joined through distributed shared memory. A thread copies its
+// vectors to places of its own in shared memory (cp.async), two times four on
+// their way while it works on four, so that memory does not wait for the
+// arithmetic (us: loaded into registers behind it, 1021 rows of 152064 bf16
+// logits 74, now 65; 400 fp32 rows 47.5, now 40; once four on their way 73 and 49,
+// three or four times two 71 and 42). 1021 rows of bf16 run at 4.8 TB/s, 400 of
+// fp32 at 6.0; 72 fp32 rows take 13 and with 20 alternatives 20, one row 6.5 and
+// with five 9.6: few rows are a chain of loads, reductions, the second look and
+// the cluster's barriers; many are bound by memory in fp32, and in 16 bits by the
+// six instructions of an element and by the last wave's empty places. CTAs of 256
+// threads, four on an SM, so that some stream while others choose (with loads
+// into registers, 1021 rows 74 and 72 rows 13.6: of 512 threads 89 and 19.1, of
+// 128 76 and 30).
 #include <algorithm>
 #include <type_traits>
 
@@ -36,7 +41,8 @@ namespace {
 constexpr int kMaxTop = 32;
 constexpr int kMaxCluster = 8;           // (of 4: one row 8.9 us for 6.8)
 constexpr int kBuffer = 1024;           // elements that reach the bound; more (rows made for it) are handled apart
-constexpr int kAhead = 4;               // vectors that a thread has on their way
+constexpr int kAhead = 4;               // vectors that a thread works on together
+constexpr int kStages = 2;              // as often as many on their way
 constexpr float kLog2E = 1.44269504088896f;
 
 struct ScoreArgs {
@@ -110,6 +116,29 @@ struct Vec {
     if constexpr (sizeof(T) == 4) return __uint_as_float(u);
     else if constexpr (std::is_same<T, bf16>::value) return __uint_as_float(i & 1 ? u & 0xffff0000u : u << 16);
     else return i & 1 ? __high2float(*reinterpret_cast<const __half2*>(&u)) : __low2float(*reinterpret_cast<const __half2*>(&u));
+  }
+  // A number whose exponential is 0 under every reference from half of it on.
+  static constexpr float kLow = std::is_same<T, __half>::value ? -65504.f : -1.0e30f;
+  // The elements, those below kLow raised to it (of -infinity, an exponential 0
+  // times the exponent would be NaN); a NaN stays. 16 bits: in pairs.
+  __device__ __forceinline__ Vec raised() const {
+    Vec r;
+    uint32_t u[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      u[i] = word(i);
+      if constexpr (sizeof(T) == 4) {
+        u[i] = __float_as_uint(max_nan(__uint_as_float(u[i]), kLow));
+      } else {
+        T2 low;
+        if constexpr (std::is_same<T, bf16>::value) low = __float2bfloat162_rn(kLow);
+        else low = __float2half2_rn(kLow);
+        const T2 y = __hmax2_nan(*reinterpret_cast<const T2*>(&u[i]), low);
+        u[i] = *reinterpret_cast<const uint32_t*>(&y);
+      }
+    }
+    r.w = make_uint4(u[0], u[1], u[2], u[3]);
+    return r;
   }
   // The larger of its elements and mx (a NaN counts as -infinity); 16 bits: in pairs.
   static __device__ __forceinline__ float max_of(const Vec (&v)[kAhead]) {
@@ -209,6 +238,11 @@ __device__ __forceinline__ float key_value(unsigned long long k) {
   return __uint_as_float(u & 0x80000000u ? u & 0x7fffffffu : ~u);
 }
 
+template <int N>
+__device__ __forceinline__ void copy_wait() {   // until all but the last N groups of cp_async16 have landed
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // What a CTA of a cluster leaves for the first one.
 struct Share {
   Sums sums;
@@ -220,6 +254,7 @@ template <typename T, int kThreads>
 __global__ void __launch_bounds__(kThreads, 1024 / kThreads) k_token_logprobs(const __grid_constant__ ScoreArgs a) {
   using V = Vec<T>;
   constexpr int kGroups = kThreads / 4;   // groups of four threads, for the top alternatives
+  __shared__ uint4 s_ring[kStages][kAhead][kThreads];   // (each thread its own places)
   __shared__ Sums s_sums[kThreads / 32];
   __shared__ int s_rank[kThreads / 32];
   __shared__ __align__(16) float s_max[kGroups];
@@ -246,19 +281,21 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) k_token_logprobs(co
   auto odd_of = [&](int t) {
     return part > 0 ? -1 : t < head ? t : t >= 16 && t - 16 < a.vocab - body ? body + t - 16 : -1;
   };
-  // Vectors i, i + kThreads, ... of this thread; behind the stretch: -infinity.
+  // Vectors i, i + kThreads, ... of this thread on their way; behind the stretch: -infinity.
   const uint32_t none_bits = sizeof(T) == 4 ? 0xff800000u : std::is_same<T, bf16>::value ? 0xff80ff80u : 0xfc00fc00u;
-  auto load = [&](V (&v)[kAhead], int i) {
+  auto fetch = [&](int s, int i) {
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
-      v[u].w = make_uint4(none_bits, none_bits, none_bits, none_bits);
-      if (i + u * kThreads < v1) v[u].w = __ldg(xv + i + u * kThreads);
+      if (i + u * kThreads < v1) cp_async16(&s_ring[s][u][tid], xv + i + u * kThreads);
+      else s_ring[s][u][tid] = make_uint4(none_bits, none_bits, none_bits, none_bits);
     }
+    cp_async_commit();
   };
-  int i = v0 + tid;
-  V v[kAhead];
-  load(v, i);                                  // (before the token is known)
+  int i = v0 + tid, stage = 0;
+#pragma unroll
+  for (int s = 0; s < kStages; ++s) fetch(s, i + s * kAhead * kThreads);   // (before the token is known)
   if (token < 0 || token >= a.vocab) {         // (the whole cluster)
+    cp_async_wait_all();
     if (a.chain == 2) pdl_wait();
     return;
   }
@@ -281,8 +318,12 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) k_token_logprobs(co
   }
 #pragma unroll 1
   for (; i < v1; i += kAhead * kThreads) {
+    copy_wait<kStages - 1>();
+    V v[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) v[u].w = s_ring[stage][u][tid];
     z.raise(V::max_of(v));
-    if (z.m == -INFINITY) {
+    if (z.m < V::kLow / 2) {
 #pragma unroll
       for (int u = 0; u < kAhead; ++u)
 #pragma unroll
@@ -291,17 +332,17 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) k_token_logprobs(co
       const uint64_t m2 = pair(-z.m, -z.m), c2 = pair(kLog2E, kLog2E);
       uint64_t s2[2] = {pair(z.s, 0.f), 0}, t2[2] = {pair(z.t, 0.f), 0};
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u)
+      for (int u = 0; u < kAhead; ++u) {
+        const V x = v[u].raised();
 #pragma unroll
         for (int e = 0; e < V::N; e += 2) {
-          float2 d = unpair(add2(pair(v[u].get(e), v[u].get(e + 1)), m2));
-          d.x = max_nan(d.x, -1.0e30f), d.y = max_nan(d.y, -1.0e30f);   // (e = 0 times -infinity is NaN)
-          const uint64_t d2 = pair(d.x, d.y);
+          const uint64_t d2 = add2(pair(x.get(e), x.get(e + 1)), m2);
           const float2 y = unpair(mul2(d2, c2));
           const uint64_t e2 = pair(exp2_fast(y.x), exp2_fast(y.y));
           s2[e / 2 & 1] = add2(s2[e / 2 & 1], e2);
           t2[e / 2 & 1] = fma2(e2, d2, t2[e / 2 & 1]);
         }
+      }
       const float2 s = unpair(add2(s2[0], s2[1])), t = unpair(add2(t2[0], t2[1]));
       z.s = s.x + s.y;
       z.t = t.x + t.y;
@@ -312,12 +353,14 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) k_token_logprobs(co
       rank += V::template above<false>(v, given);
     } else {
 #pragma unroll 1
-      for (int u = 0; u < kAhead; ++u)
+      for (int u = 0; u < kAhead; ++u) {
+        const V y = {s_ring[stage][u][tid]};
 #pragma unroll
-        for (int e = 0; e < V::N; ++e)
-          count_one((u == 0 ? v[0] : u == 1 ? v[1] : u == 2 ? v[2] : v[3]).get(e), head + (i + u * kThreads) * V::N + e);
+        for (int e = 0; e < V::N; ++e) count_one(y.get(e), head + (i + u * kThreads) * V::N + e);
+      }
     }
-    load(v, i + kAhead * kThreads);
+    fetch(stage, i + kStages * kAhead * kThreads);
+    stage = stage + 1 == kStages ? 0 : stage + 1;
   }
   if (all_before && tid == 0 && part == 0) rank += token;
 
