@@ -34,7 +34,7 @@
 // Tensor memory holds both tiles' O and S (P over S), 512 columns at head
 // dimension 128.
 //
-// Measured: 2048 rows over 16384 tokens, 40 / 8 heads of 128, 361 us (1783
+// Measured: 2048 rows over 16384 tokens, 40 / 8 heads of 128, 365 us (1770
 // TFLOP/s), of 64 300; a whole prompt of 8192, 28 / 4 heads of 128, 299 (1607);
 // nine prompts of 33..4099 tokens 314. Tried, at 128 and 64, for what stood then:
 // the maximum of half a unit at a time 458 for 405 and 463 for 320; P apart from
@@ -54,8 +54,9 @@ struct ChunkShape {
   static constexpr int MT = 256;                        // queries of an item
   static constexpr int kSlots = 128;                    // of a unit
   static constexpr int kThreads = 384;
-  // Registers of a softmax thread and of the other warps': 2 x 128 x 216 + 128 x 72 = 384 x 168, the launch's.
-  static constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
+  // Registers of a softmax thread and of the other warps': 2 x 128 x 200 + 128 x 104 = 384 x 168, the launch's (216 and
+  // 72: the producer spills, 4 us of nine prompts' 316).
+  static constexpr int kSoftmaxRegs = 200, kOtherRegs = 104;
   static constexpr int kHalf = HD / 64;
   static constexpr int kBox = 128 * 128;                // 128 rows of 64 dimensions
   static constexpr int kTileBytes = kHalf * kBox;       // of queries, keys or values
@@ -71,6 +72,8 @@ struct ChunkShape {
   // first scores and last output, which nothing runs beside). Nine whole prompts
   // at the 7B shape: 2 356 us, 3 327, 4 319, 5 341.
   static constexpr int kPiece = 4;
+  // Units of 128 slots whose keys and values stay in L2 (64 MB of 129; at 96 MB 24576 tokens take 588 us; chunk_walk).
+  static constexpr long kRound = (64l << 20) / (kSlots * HD * 4);
 };
 
 // The units of a request's items.
@@ -156,57 +159,107 @@ struct ChunkWalk {
   int item_q, item_h;   // query tile and KV head of the piece
 };
 
-// Where a CTA's units begin: all threads of the CTA together.
-template <int NT>
-__device__ __forceinline__ ChunkWalk chunk_walk(const Args& a, long* sh, Deal& deal) {
+// Where one of a CTA's shares of the units begins.
+struct ShareStart {
+  long u, left;   // units before it, and its own
+  long base;      // units before its request
+  int b;
+};
+// What the CTA's warps know of its shares, in shared memory.
+struct Shares {
+  long each, more;   // Deal's
+  int rounds;
+  ShareStart start[kRounds];
+  __device__ __forceinline__ int cta_of(long u) const {
+    Deal d(1, 1);
+    d.each = each, d.more = more;
+    return d.cta_of(u);
+  }
+};
+
+// A CTA's shares of the units: all threads of the CTA together.
+//
+// With one share a CTA, all requests and heads are at work at the same time, and
+// where their keys and values are more than L2 holds, items bring them from memory
+// again. So then the units are dealt out in up to three rounds, one after the
+// other over all CTAs (share v = CTA + round * CTAs), if items are enough that a
+// round still shares keys and values and the shares stay long. 2048 rows, 40 / 8
+// heads of 128, us in one round and so: 16384 tokens (67 MB) 363 and 365 (two),
+// 24576 588 and 575, 32768 811 and 763 (without a pause, at the power cap, 927 to
+// 969 and 850 to 875), 65536 1695 and 1592 (three).
+template <int HD, typename TC>
+__device__ __forceinline__ void chunk_walk(const Args& a, long* sh, Shares& shares) {
+  using S = ChunkShape<HD, TC>;
+  constexpr int NT = S::kThreads, NW = NT / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  constexpr int NW = NT / 32;
   const int per = (a.B + NT - 1) / NT;
   const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
-  long mine = 0;
-  for (int b = b0; b < b1; ++b) mine += a.nkv * ItemUnits(a, request<256>(a, b)).head();
+  long mine = 0, cache = 0;   // units; units of all items' longest, of each head
+  for (int b = b0; b < b1; ++b) {
+    const ItemUnits iu(a, request<256>(a, b));
+    mine += a.nkv * iu.head();
+    if (iu.ntq > 0) cache += (long)a.nkv * iu.last;
+  }
   long incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const long x = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += x;
   }
-  if (lane == 31) sh[warp] = incl;
+  if (a.rounds > 1) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) cache += __shfl_xor_sync(0xffffffffu, cache, o);
+  }
+  if (lane == 31) {
+    sh[warp] = incl;
+    sh[NW + warp] = cache;
+  }
   __syncthreads();
   long before = 0, T = 0;
+  cache = 0;
 #pragma unroll
   for (int w = 0; w < NW; ++w) {
     if (w < warp) before += sh[w];
     T += sh[w];
+    cache += sh[NW + w];
   }
-  const long G = min((long)gridDim.x, T);
-  deal = Deal(max(T, 1l), max(G, 1l));
-  const bool idle = (long)blockIdx.x >= G;
-  const long u0 = idle ? -1 : deal.first(blockIdx.x);
+  int rounds = 1;
+  while (rounds < a.rounds && cache > rounds * S::kRound && T >= 8 * cache && T >= 64l * (rounds + 1) * gridDim.x) ++rounds;
+  const long G = min((long)rounds * gridDim.x, T);
+  const Deal deal(max(T, 1l), max(G, 1l));
+  if (tid == 0) {
+    shares.each = deal.each;
+    shares.more = deal.more;
+    shares.rounds = rounds;
+  }
   const long lo = before + incl - mine;
-  if (u0 >= lo && u0 < lo + mine) {
-    long base = lo;
-    for (int b = b0; b < b1; ++b) {
-      const long n = a.nkv * ItemUnits(a, request<256>(a, b)).head();
-      if (u0 < base + n) {
-        sh[NW] = base;
-        sh[NW + 1] = b;
-        break;
+  for (int i = 0; i < rounds; ++i) {
+    const long v = blockIdx.x + (long)i * gridDim.x, u0 = v < G ? deal.first(v) : -1;
+    if (tid == 0 && v >= G) shares.start[i] = ShareStart{0, 0, 0, 0};
+    if (u0 >= lo && u0 < lo + mine) {
+      long base = lo;
+      for (int b = b0; b < b1; ++b) {
+        const long n = a.nkv * ItemUnits(a, request<256>(a, b)).head();
+        if (u0 < base + n) {
+          shares.start[i] = ShareStart{u0, deal.first(v + 1) - u0, base, b};
+          break;
+        }
+        base += n;
       }
-      base += n;
     }
   }
   __syncthreads();
+}
+// The walk over a share (by a warp together).
+__device__ __forceinline__ ChunkWalk walk_from(const Args& a, const ShareStart& s) {
   ChunkWalk w;
-  w.u = max(u0, 0l);
-  w.left = 0;
-  w.b = 0;
-  if (!idle) {
-    w.left = deal.first(blockIdx.x + 1) - u0;
-    w.b = (int)sh[NW + 1];
+  w.u = s.u;
+  w.left = s.left;
+  w.b = s.b;
+  if (s.left > 0) {
     w.r = request<256>(a, w.b);
     w.iu = ItemUnits(a, w.r);
-    const long rest = u0 - sh[NW], head = w.iu.head();
+    const long rest = s.u - s.base, head = w.iu.head();
     w.kvh = (int)Deal::div(rest, head);
     w.qt = w.iu.find(rest - w.kvh * head);
     w.at = (int)(rest - w.kvh * head - w.iu.before(w.qt));
@@ -220,60 +273,49 @@ struct Piece {
   int kvh, q;              // KV head, query tile
   int t0, t1;              // units; none: there are no more pieces
   int whole;               // all of the item's units
+  int v;                   // the share
 };
 // The ring of tiles lets the producer be at most six units ahead, so as many pieces.
 constexpr int kPieces = 16, kChecks = 8;
 
-// The join's descriptor of an item that begins in this CTA (one thread).
-__device__ __forceinline__ void describe(const Args& a, const ChunkWalk& w, const Deal& deal, bool whole) {
-  const int c1 = whole ? (int)blockIdx.x : deal.cta_of(w.u - w.t1 + w.nt - 1);
-  const int4 d = make_int4(blockIdx.x, c1 - (int)blockIdx.x + 1, w.b, w.item_h * w.r.ntq + w.item_q);
-  if (!whole) a.desc[blockIdx.x] = d;
+// The join's descriptor of an item that begins in share v (one thread).
+__device__ __forceinline__ void describe(const Args& a, const ChunkWalk& w, int v, const Shares& shares, bool whole) {
+  const int c1 = whole ? v : shares.cta_of(w.u - w.t1 + w.nt - 1);
+  const int4 d = make_int4(v, c1 - v + 1, w.b, w.item_h * w.r.ntq + w.item_q);
+  if (!whole) a.desc[v] = d;
 }
+// None begins there that others share.
+__device__ __forceinline__ void describe_none(const Args& a, int v) { a.desc[v] = make_int4(0, 0, 0, 0); }
 
 // A wait ran out: every row of the CTA's pieces becomes NaN (one warp, which
 // finds the pieces by itself).
 template <int HD, typename TC>
-__device__ __noinline__ void leave_nan(const Args& a) {
+__device__ __noinline__ void leave_nan(const Args& a, const Shares& shares) {
   const int lane = threadIdx.x & 31;
   const float nan = __int_as_float(0x7fc00000);
-  long T = 0;
-  for (int b = 0; b < a.B; ++b) T += a.nkv * ItemUnits(a, request<256>(a, b)).head();
-  const long G = min((long)gridDim.x, T);
-  if ((long)blockIdx.x >= G) return;
-  const Deal deal(T, G);
-  ChunkWalk w;
-  w.u = deal.first(blockIdx.x);
-  w.left = deal.first(blockIdx.x + 1) - w.u;
-  long base = 0;
-  for (w.b = 0;; ++w.b) {
-    w.r = request<256>(a, w.b);
-    w.iu = ItemUnits(a, w.r);
-    const long n = a.nkv * w.iu.head();
-    if (w.u < base + n) break;
-    base += n;
-  }
-  const long head = w.iu.head(), rest = w.u - base;
-  w.kvh = (int)(rest / head);
-  w.qt = w.iu.find(rest - w.kvh * head);
-  w.at = (int)(rest - w.kvh * head - w.iu.before(w.qt));
-  while (w.next(a)) {
-    const bool whole = w.t0 == 0 && w.t1 == w.nt;
-    if (lane == 0 && w.t0 == 0) describe(a, w, deal, whole);
-    const long slot = 2l * blockIdx.x + (w.t0 == 0 ? 1 : 0);
-    for (int i = lane; i < 256; i += 32) {
-      const int q = w.item_q * 256 + i, j = q / a.group, hh = w.item_h * a.group + q - j * a.group;
-      if (q >= w.r.rows * a.group) break;
-      if (!whole) {
-        a.part_ml[slot * a.mt_max + i] = make_float2(0.f, nan);
-        continue;
+  for (int round = 0; round < shares.rounds; ++round) {
+    ChunkWalk w = walk_from(a, shares.start[round]);
+    const int v = blockIdx.x + round * gridDim.x;
+    while (w.next(a)) {
+      const bool whole = w.t0 == 0 && w.t1 == w.nt;
+      if (lane == 0 && w.t0 == 0) describe(a, w, v, shares, whole);
+      const long slot = 2l * v + (w.t0 == 0 ? 1 : 0);
+      for (int i = lane; i < 256; i += 32) {
+        const int q = w.item_q * 256 + i, j = q / a.group, hh = w.item_h * a.group + q - j * a.group;
+        if (q >= w.r.rows * a.group) break;
+        if (!whole) {
+          a.part_ml[slot * a.mt_max + i] = make_float2(0.f, nan);
+          continue;
+        }
+        TC* dst = static_cast<TC*>(a.out) + (w.r.s0 + j) * a.o_row + hh * a.o_head;
+        for (int d = 0; d < HD; d += 2) *reinterpret_cast<uint32_t*>(dst + d) = Num<TC>::pack(nan, nan);
+        if (a.lse) a.lse[(long)(w.r.s0 + j) * a.nq + hh] = nan;
       }
-      TC* dst = static_cast<TC*>(a.out) + (w.r.s0 + j) * a.o_row + hh * a.o_head;
-      for (int d = 0; d < HD; d += 2) *reinterpret_cast<uint32_t*>(dst + d) = Num<TC>::pack(nan, nan);
-      if (a.lse) a.lse[(long)(w.r.s0 + j) * a.nq + hh] = nan;
     }
+    if (lane == 0 && !w.open) describe_none(a, v);
   }
-  if (lane == 0 && !w.open) a.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
+  if (lane == 0)
+    for (int round = shares.rounds; round < a.rounds; ++round) describe_none(a, blockIdx.x + round * gridDim.x);
   report_err(a.err, kErrWait);
 }
 
@@ -326,7 +368,8 @@ __global__ void __launch_bounds__(ChunkShape<HD, TC>::kThreads, 1) k_chunk_attn(
   extern __shared__ unsigned char pa_smem_raw[];
   unsigned char* const qbuf = pa_smem_raw + ((1024 - (smem_u32(pa_smem_raw) & 1023)) & 1023);   // both tiles' queries
   unsigned char* const ring = qbuf + 2 * S::kTileBytes;
-  __shared__ long sh_loc[S::kThreads / 32 + 2];
+  __shared__ long sh_loc[2 * (S::kThreads / 32)];
+  __shared__ Shares s_shares;
   // full: a tile of the ring has landed; empty: it may be loaded anew; checked: a unit's values may be used.
   __shared__ __align__(8) uint64_t full[NS], empty[NS], checked[kChecks], q_full[2], s_full[2], p_full[2][2], o_done[2], drain;
   __shared__ __align__(8) uint64_t piece_full[kPieces];
@@ -366,8 +409,7 @@ __global__ void __launch_bounds__(ChunkShape<HD, TC>::kThreads, 1) k_chunk_attn(
   const uint32_t tmem = s_tmem;
   pdl_wait();
   pdl_launch_next();
-  Deal deal(1, 1);
-  ChunkWalk w = chunk_walk<S::kThreads>(a, sh_loc, deal);   // (the producer warp's from here on)
+  chunk_walk<HD, TC>(a, sh_loc, s_shares);
   bool ok = true;
   // Piece i of the CTA, for the other warps; no units at the end.
   auto piece_at = [&](int i) {
@@ -389,15 +431,23 @@ __global__ void __launch_bounds__(ChunkShape<HD, TC>::kThreads, 1) k_chunk_attn(
       const uint64_t policy = policy_evict_normal();
       int win_b = -1, win = -1, entry = 0;            // the 32 table entries at hand, one per lane
       int s = 0, phase = 1, loaded = 0;               // (a new barrier's phase 1 counts as past)
-      int piece = 0;
+      int piece = 0, round = -1;
+      ChunkWalk w;
+      w.left = 0;
       while (true) {
         const bool more = ok && w.next(a);
+        if (ok && !more && round + 1 < s_shares.rounds) {        // (this share is done)
+          if (lane == 0 && round >= 0 && !w.open) describe_none(a, blockIdx.x + round * gridDim.x);
+          w = walk_from(a, s_shares.start[++round]);
+          continue;
+        }
+        const int v = blockIdx.x + round * gridDim.x;
         if (lane == 0) {
           const bool whole = more && w.t0 == 0 && w.t1 == w.nt;
-          s_piece[piece % kPieces] = more ? Piece{w.r.s0, w.r.rows, w.r.len, w.r.p0, w.item_h, w.item_q, w.t0, w.t1, whole}
-                                          : Piece{};
+          s_piece[piece % kPieces] =
+              more ? Piece{w.r.s0, w.r.rows, w.r.len, w.r.p0, w.item_h, w.item_q, w.t0, w.t1, whole, v} : Piece{};
           mbar_arrive(&piece_full[piece % kPieces]);
-          if (more && w.t0 == 0) describe(a, w, deal, whole);
+          if (more && w.t0 == 0) describe(a, w, v, s_shares, whole);
         }
         ++piece;
         if (!more) break;
@@ -440,7 +490,10 @@ __global__ void __launch_bounds__(ChunkShape<HD, TC>::kThreads, 1) k_chunk_attn(
           }
         }
       }
-      if (lane == 0 && !w.open) a.desc[blockIdx.x] = make_int4(0, 0, 0, 0);   // no item begins here that others share
+      if (lane == 0) {
+        if (!w.open) describe_none(a, blockIdx.x + max(round, 0) * gridDim.x);
+        for (int r = s_shares.rounds; r < a.rounds; ++r) describe_none(a, blockIdx.x + r * gridDim.x);
+      }
       if (!ok) s_fail = 1;
       // The copies in flight land before the CTA may end, whatever the others did.
       for (int k = max(0, loaded - NS); k < loaded; ++k) mbar_wait(&full[k % NS], (k / NS) & 1, kWaitPolls);
@@ -645,7 +698,7 @@ __global__ void __launch_bounds__(ChunkShape<HD, TC>::kThreads, 1) k_chunk_attn(
       const int lim_warp = __shfl_sync(0xffffffffu, lim, 0);  // (the least: rows see more and more)
       const int t0 = w.t0, t1 = w.t1;
       const bool whole = w.whole;
-      const long slot = 2l * blockIdx.x + (t0 == 0 ? 1 : 0);
+      const long slot = 2l * w.v + (t0 == 0 ? 1 : 0);
       float* const part = a.part + (slot * a.mt_max + 128 * x + row) * HD;     // (of a live row)
       float2* const part_ml = a.part_ml + slot * a.mt_max + 128 * x + row;
       float m = -INFINITY, l = 0.f;
@@ -846,7 +899,7 @@ __global__ void __launch_bounds__(ChunkShape<HD, TC>::kThreads, 1) k_chunk_attn(
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
-  if (warp == 0 && s_fail) leave_nan<HD, TC>(a);
+  if (warp == 0 && s_fail) leave_nan<HD, TC>(a, s_shares);
 }
 
 // The join of the items that several CTAs share: the parts lie with the CTAs

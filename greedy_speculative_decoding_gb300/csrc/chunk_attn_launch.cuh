@@ -17,6 +17,7 @@ cudaError_t launch_chunk(Args& a, int sms, long max_units, cudaStream_t st) {
   const cudaError_t e = launch_main(k_chunk_attn<HD, TC>, S::kThreads, S::kSmem, S::kPiece, ready, a, sms, 1, max_units,
                                     st, cfg, attr);
   if (e != cudaSuccess) return e;
+  cfg.gridDim.x *= a.rounds;
   cfg.gridDim.y = (a.mt_max + kChunkJoinQueries - 1) / kChunkJoinQueries;
   cfg.blockDim = dim3(kChunkJoinThreads);
   cfg.dynamicSmemBytes = 0;

@@ -15,13 +15,13 @@ constexpr int kMaxDesc = 1024;  // item descriptors
 struct Layout {
   size_t ml, part, total;
 };
-static Layout layout(int n_heads, int n_kv_heads, int head_dim, int max_rows) {   // (whatever the tile)
+static Layout layout(int n_heads, int n_kv_heads, int head_dim, int max_rows, int rounds = 1) {   // (whatever the tile)
   const long queries = (long)max_rows * (n_heads / n_kv_heads);
   const size_t mt = std::min(queries, 128l);
   Layout l;
   l.ml = kMaxDesc * sizeof(int4);
-  l.part = l.ml + 2 * kMaxCtas * mt * sizeof(float2);
-  l.total = l.part + 2 * kMaxCtas * mt * head_dim * sizeof(float);
+  l.part = l.ml + 2 * rounds * kMaxCtas * mt * sizeof(float2);
+  l.total = l.part + 2 * rounds * kMaxCtas * mt * head_dim * sizeof(float);
   return l;
 }
 
@@ -150,8 +150,8 @@ static cudaError_t enqueue(Args& a, const sf_paged_cache& c, int q_dtype, float 
 }
 
 // The same with the kernel for chunks (16-bit queries): items of 256 queries,
-// units of 128 slots, one CTA an SM (half as many, of twice the queries: the
-// workspace's layout is the same).
+// units of 128 slots, one CTA an SM (half as many, of twice the queries), and in
+// the workspace room for kRounds times as many.
 constexpr int kChunkQueries = 256, kChunkUnit = 128;
 static cudaError_t enqueue_chunk(Args& a, const sf_paged_cache& c, int q_dtype, float scale, void* workspace, int sms,
                                  cudaStream_t st) {
@@ -162,11 +162,13 @@ static cudaError_t enqueue_chunk(Args& a, const sf_paged_cache& c, int q_dtype, 
   a.mt_max = (int)std::min<long>(queries, kChunkQueries);
   a.ntq_max = (int)((queries + kChunkQueries - 1) / kChunkQueries);
   const long items = (long)a.B * a.nkv * a.ntq_max;
-  const Layout lay = layout(a.nq, a.nkv, c.head_dim, a.max_rows);
+  const Layout lay = layout(a.nq, a.nkv, c.head_dim, a.max_rows, kRounds);
   unsigned char* ws = static_cast<unsigned char*>(workspace);
   a.desc = reinterpret_cast<int4*>(ws);
   a.part_ml = reinterpret_cast<float2*>(ws + lay.ml);
   a.part = reinterpret_cast<float*>(ws + lay.part);
+  // Rounds, where the tables can hold more than L2 (the kernel looks at the lengths).
+  a.rounds = (long)a.B * a.W * c.page * a.nkv * c.head_dim * 4 > 64l << 20 ? kRounds : 1;
   const long max_units = items * (((long)a.W * c.page + kChunkUnit - 1) / kChunkUnit);
   sms = std::min(sms, kMaxCtas / 2);
   return c.head_dim == 128 ? launch_chunk_hd128(a, q_dtype, sms, max_units, st)
@@ -326,7 +328,7 @@ extern "C" size_t sf_chunk_attention_workspace_bytes(int32_t n_heads, int32_t n_
   if (n_heads < 1 || n_kv_heads < 1 || n_heads % n_kv_heads || n_heads > 65535 || (head_dim != 64 && head_dim != 128) ||
       max_rows < 1 || max_rows > kMaxChunk)
     return 0;
-  return pa::layout(n_heads, n_kv_heads, head_dim, max_rows).total;
+  return pa::layout(n_heads, n_kv_heads, head_dim, max_rows, pa::kRounds).total;
 }
 
 extern "C" sf_status sf_chunk_attention(const sf_paged_cache* cache, const sf_rows* q, const sf_rows* out, int32_t n,

@@ -54,6 +54,7 @@ struct Args {
   int mt_max;              // queries of an item at most (min(MT, max_rows * group))
   int ntq_max;             // items of a (request, KV head) at most
   int piece;               // units that an item's beginning counts for
+  int rounds;              // of a chunk's units, at most
   int by_warp;             // few requests: every warp finds the CTA's units by itself
   int wide;                // few items: a CTA joins one query, else four
   int by_item;             // descriptors by item (else by the CTA that starts it)
@@ -64,6 +65,8 @@ struct Args {
   int frag_umma;
   int* err;                // status word, or null
 };
+
+constexpr int kRounds = 3;   // that a chunk's units may be dealt out in
 
 // A request as the kernel sees it: whatever lens and starts hold, rows lie in
 // [0, N) and slots within the table.

@@ -290,6 +290,29 @@ def test_sums_that_move(pkg, dt, hd):
         check(part, out[a:b], lse[a:b])
 
 
+@pytest.mark.parametrize("hd,nkv,group,lens,rows", [
+    (128, 4, 1, [40000], [3000]), (64, 16, 1, [40000], [2500]),
+    (128, 2, 3, [30011, 7, 45000, 0, 25000], [3000, 7, 1500, 0, 2111]), (64, 8, 2, [30000, 41234], [2000, 1700])])
+def test_rounds(pkg, hd, nkv, group, lens, rows):
+    """More keys and values than L2 holds, and items that share them: two and
+    three rounds. Some of the rows are compared, as above."""
+    c = attn_case(43, lens, rows, nkv * group, nkv, hd, 128, BF, BF, q_scale=1.0)
+    out, lse = call(pkg, c)
+    for b, m in enumerate(rows):
+        s0 = c["starts"][b]
+        for a, e in ((0, 5), (m // 2 + 100, m // 2 + 103), (m - 6, m)):
+            if not 0 <= a < e <= m:
+                continue
+            part = dict(c, q=c["q"][s0 + a:s0 + e], tables=[c["tables"][b]], lens=[lens[b] - m + e], starts=[0, e - a])
+            check(part, out[s0 + a:s0 + e], lse[s0 + a:s0 + e])
+    for _ in range(3):
+        again = call(pkg, c)
+        assert torch.equal(again[0], out) and torch.equal(again[1], lse)
+    again = call(pkg, c, True)
+    ends = torch.tensor(c["starts"][1:], device="cuda") - 1
+    assert bool(torch.isfinite(again[0].float()).all()) and bool((again[0][ends].float() - out[ends].float()).abs().max() < 0.1)
+
+
 @pytest.mark.parametrize("hd", [64, 128])
 @pytest.mark.parametrize("page", [16, 256])
 def test_large_batches_of_prompts(pkg, hd, page):
