@@ -61,6 +61,22 @@ cudaError_t launch_engine_paged_attention(const EngineAttn& e, int num_sms, cuda
 // Row masks of a verify pass over candidate guesses of g tokens (see RowSet).
 cudaError_t launch_tree_mask(unsigned long long* mask, int B, int rows, int g, cudaStream_t st, bool pdl);
 
+// Arrays of a call: whether none that it writes lies over another (null or empty ones do not count).
+struct Range {
+  const void* at;
+  uint64_t bytes;
+  bool written;
+};
+inline bool ranges_apart(const Range* r, int n) {
+  for (int x = 0; x < n; ++x)
+    for (int y = 0; y < x; ++y) {
+      if (!(r[x].written || r[y].written) || !r[x].at || !r[y].at || !r[x].bytes || !r[y].bytes) continue;
+      const uintptr_t a = reinterpret_cast<uintptr_t>(r[x].at), b = reinterpret_cast<uintptr_t>(r[y].at);
+      if (a < b + r[y].bytes && b < a + r[x].bytes) return false;
+    }
+  return true;
+}
+
 // Whether two of n1 x n2 vectors of hd elements, s1 and s2 apart, share an
 // element (a call that writes them would leave whichever came last).
 inline bool vectors_overlap(int64_t n1, int64_t s1, int64_t n2, int64_t s2, int64_t hd) {

@@ -14,6 +14,7 @@
 #include <algorithm>
 #include <atomic>
 #include <climits>
+#include <initializer_list>
 
 #include "paged.h"
 
@@ -473,6 +474,18 @@ cudaError_t launch_share(void (*fn)(Args), const Args& a, long entries, size_t s
   return cudaLaunchKernelEx(&cfg, fn, a);
 }
 
+struct Array {
+  const int32_t* at;
+  int64_t n;
+  bool written;
+};
+sf_status check_apart(const char* who, std::initializer_list<Array> arrays) {
+  Range r[16];
+  int n = 0;
+  for (const Array& x : arrays) r[n++] = Range{x.at, (uint64_t)x.n * sizeof(int32_t), x.written};
+  return ranges_apart(r, n) ? SF_OK : set_error(SF_ERR_ARG, "%s: an array that the call writes overlaps another", who);
+}
+
 // What the three calls refuse alike.
 sf_status check_tables(const char* who, int32_t batch, int32_t table_width, int32_t n_pages) {
   if (batch < 1 || batch > kMaxPlanBatch)
@@ -505,6 +518,10 @@ extern "C" sf_status sf_page_free(const int32_t* d_requests, const int32_t* d_ke
   if (n == 0) return SF_OK;
   if (!d_requests || !d_tables || !d_held || !d_shares || !d_free || !d_n_free || !d_status)
     return set_error(SF_ERR_ARG, "sf_page_free: null pointer");
+  s = check_apart("sf_page_free", {{d_requests, n, false}, {d_keep, n, false}, {d_tables, (int64_t)batch * table_width, false},
+                                   {d_held, batch, true}, {d_shares, n_pages, true}, {d_free, capacity, true},
+                                   {d_n_free, 1, true}, {d_status, n, true}});
+  if (s != SF_OK) return s;
   static std::atomic<uint64_t> ready{0};
   const FreeArgs a{d_requests, d_keep, n, d_tables, d_held, d_shares, d_free, d_n_free, d_status, batch, table_width,
                    n_pages, capacity, log2_of(page)};
@@ -526,6 +543,11 @@ extern "C" sf_status sf_page_fork(const int32_t* d_src, const int32_t* d_dst, in
   if (!d_src || !d_dst || !d_lens || !d_tables || !d_held || !d_shares || !d_free || !d_n_free || !d_source || !d_target ||
       !d_slots || !d_status)
     return set_error(SF_ERR_ARG, "sf_page_fork: null pointer");
+  s = check_apart("sf_page_fork", {{d_src, n, false}, {d_dst, n, false}, {d_lens, batch, false},
+                                   {d_tables, (int64_t)batch * table_width, true}, {d_held, batch, true},
+                                   {d_shares, n_pages, true}, {d_free, capacity, false}, {d_n_free, 1, true},
+                                   {d_source, n, true}, {d_target, n, true}, {d_slots, n, true}, {d_status, n, true}});
+  if (s != SF_OK) return s;
   static std::atomic<uint64_t> ready{0};
   const ForkArgs a{d_src, d_dst, d_lens, n, d_tables, d_held, d_shares, d_free, d_n_free, d_source, d_target, d_slots,
                    d_status, batch, table_width, n_pages, capacity, log2_of(page)};
@@ -540,7 +562,7 @@ extern "C" sf_status sf_page_compact(const int32_t* d_tables, int32_t batch, int
                                      int32_t* d_shares_out, int32_t* d_free, int32_t capacity, int32_t* d_n_free,
                                      int32_t* d_source, int32_t* d_target, int32_t moves, int32_t* d_count,
                                      void* cuda_stream) {
-  const sf_status s = check_tables("sf_page_compact", batch, table_width, n_pages);
+  sf_status s = check_tables("sf_page_compact", batch, table_width, n_pages);
   if (s != SF_OK) return s;
   if (n_pages > kMaxPages) return set_error(SF_ERR_UNSUPPORTED, "sf_page_compact: n_pages %d above %d", n_pages, kMaxPages);
   if (capacity < n_pages || moves < n_pages / 2)
@@ -548,6 +570,13 @@ extern "C" sf_status sf_page_compact(const int32_t* d_tables, int32_t batch, int
   if (!d_tables || !d_held || !d_shares || !d_tables_out || !d_shares_out || !d_free || !d_n_free || !d_count ||
       (moves > 0 && (!d_source || !d_target)))
     return set_error(SF_ERR_ARG, "sf_page_compact: null pointer");
+  const int64_t entries = (int64_t)batch * table_width;
+  s = check_apart("sf_page_compact", {{d_tables == d_tables_out ? nullptr : d_tables, entries, false},
+                                      {d_shares == d_shares_out ? nullptr : d_shares, n_pages, false},
+                                      {d_held, batch, false}, {d_tables_out, entries, true}, {d_shares_out, n_pages, true},
+                                      {d_free, capacity, true}, {d_n_free, 1, true}, {d_source, moves, true},
+                                      {d_target, moves, true}, {d_count, 1, true}});
+  if (s != SF_OK) return s;
   static std::atomic<uint64_t> ready{0};
   const CompactArgs a{d_tables, d_held, d_shares, d_tables_out, d_shares_out, d_free, d_n_free, d_source, d_target,
                       d_count, batch, table_width, n_pages, moves};

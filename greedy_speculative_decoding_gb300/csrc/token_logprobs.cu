@@ -625,6 +625,12 @@ extern "C" sf_status sf_token_logprobs(const void* d_logits, int32_t dtype, int6
     return set_error(SF_ERR_ARG, "sf_token_logprobs: null logits or tokens, or logits not aligned to their type");
   if (row_stride < 0 || row_stride > (int64_t(1) << 38))
     return set_error(SF_ERR_ARG, "sf_token_logprobs: the row stride must be in 0..2^38");
+  const uint64_t each = (uint64_t)n * 4, tops = each * top;
+  const Range arrays[] = {{d_logits, ((uint64_t)(n - 1) * row_stride + vocab) * size, false}, {d_tokens, each, false},
+                          {d_logprob, each, true}, {d_entropy, each, true}, {d_rank, each, true},
+                          {d_top_ids, tops, true}, {d_top_logprobs, tops, true}};
+  if (!ranges_apart(arrays, 7))
+    return set_error(SF_ERR_ARG, "sf_token_logprobs: an array that the call writes overlaps another");
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);

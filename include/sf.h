@@ -562,7 +562,8 @@ SF_API sf_status sf_chunk_attention(const sf_paged_cache* cache, const sf_rows* 
  * them, into pages of its own. sf_page_plan knows nothing of shares: requests
  * that hold shared pages may grow by it, but are cut and ended by sf_page_free.
  * All arrays int32, updated in place unless said otherwise; entries of tables
- * that are no page (outside 0..n_pages - 1) are passed over, not counted.
+ * that are no page (outside 0..n_pages - 1) are passed over, not counted. Arrays
+ * that a call writes may lie over no other of its arrays (refused).
  */
 
 /*
@@ -649,7 +650,8 @@ SF_API sf_status sf_page_copy(const sf_paged_cache* cache, int32_t layers, int64
  * probability is -infinity and the entropy 0. A row that holds a NaN or
  * +infinity gives NaN for log probabilities and entropy. Rows whose token lies
  * outside 0..vocab - 1 are padding: nothing is written for them. vocab 1..2^31 -
- * 65; logits aligned to their type, with any row stride from 0 to 2^38.
+ * 65; logits aligned to their type, with any row stride from 0 to 2^38. Outputs
+ * may lie over no other array (refused).
  */
 SF_API sf_status sf_token_logprobs(const void* d_logits, int32_t dtype, int64_t row_stride, int32_t n, int32_t vocab,
                                    const int32_t* d_tokens, int32_t top, float* d_logprob, float* d_entropy,

@@ -339,6 +339,21 @@ def test_offsets_past_32_bits(pkg):
         check(c, res, lse)
 
 
+@pytest.mark.parametrize("dq,dc", TYPES)
+def test_workspace_of_any_contents_and_batches_of_other_sizes(pkg, dq, dc):
+    """One workspace, full of ones, for calls of different sizes one after the other."""
+    cs = [attn_case(44 + i, lens, rows, 6, 2, 128, 64, dq, dc)
+          for i, (lens, rows) in enumerate([([900, 40, 2100], [300, 40, 700]), ([130], [130]), ([5000, 17], [60, 17])])]
+    ws = pkg.chunk_attention_workspace(cs[0]["q"], cs[0]["k"], i32(cs[0]["tables"]), 700)
+    ws.fill_(255)
+    got = [(c, wide, *call(pkg, c, wide, workspace=ws)) for _ in range(2) for c in cs for wide in (False, True)]
+    for i, (c, wide, out, lse) in enumerate(got):
+        check(c, out, lse)
+        ws.fill_(255 if i % 2 else 127)
+        again = call(pkg, c, wide, workspace=ws)
+        assert torch.equal(again[0], out) and torch.equal(again[1], lse)
+
+
 def test_prior_calls_are_seen(pkg):
     """Append and chunk back to back: the attention waits for the cache."""
     c = attn_case(31, [1000], [600], 28, 4, 128, 64, pad=0)

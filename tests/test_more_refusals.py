@@ -101,6 +101,36 @@ def test_copy_refusals(lib, kw):
     assert copy(lib, **kw) == L.SF_ERR_ARG and b"sf_page_copy" in lib.sf_last_error()
 
 
+def apart(names):
+    """An address of its own for each array, 256 KB apart."""
+    return {name: PTR + (i << 18) for i, name in enumerate(names)}
+
+
+FREE = ("requests", "keep", "tables", "held", "shares", "stack", "n_free", "status")
+FORK = ("src", "dst", "lens", "tables", "held", "shares", "stack", "n_free", "source", "target", "slots", "status")
+COMPACT = ("tables", "held", "shares", "tables_out", "shares_out", "stack", "n_free", "source", "target", "count")
+
+
+@pytest.mark.parametrize("f,names,written,allowed", [
+    (free, FREE, {"held", "shares", "stack", "n_free", "status"}, ()),
+    (fork, FORK, {"tables", "held", "shares", "n_free", "source", "target", "slots", "status"}, ()),
+    (compact, COMPACT, {"tables_out", "shares_out", "stack", "n_free", "source", "target", "count"},
+     ({"tables", "tables_out"}, {"shares", "shares_out"}))])
+def test_written_arrays_over_others_are_refused(lib, f, names, written, allowed):
+    ints = dict(requests=3, keep=3, status=3, src=3, dst=3, source=3, target=3, slots=3, tables=32, tables_out=32, held=4,
+                lens=4, shares=50, shares_out=50, stack=50, n_free=1, count=1)
+    if f is compact:
+        ints.update(source=25, target=25)
+    for x in names:
+        for y in names:
+            if x == y or not {x, y} & written:
+                continue
+            for shift in (0, 4 * ints[y] - 4) if {x, y} not in allowed else (4,):   # (up to its last element)
+                kw = apart(names)
+                kw[x] = kw[y] + shift
+                assert f(lib, **kw) == L.SF_ERR_ARG and b"overlaps" in lib.sf_last_error(), (x, y, shift)
+
+
 def score(lib, logits=PTR, dtype=L.SF_DT_F32, row=100, n=3, vocab=100, tokens=PTR, top=5):
     return lib.sf_token_logprobs(logits, dtype, row, n, vocab, tokens, top, PTR, PTR, PTR, PTR, PTR, None)
 
@@ -113,6 +143,20 @@ def score(lib, logits=PTR, dtype=L.SF_DT_F32, row=100, n=3, vocab=100, tokens=PT
     (dict(row=2 ** 39), L.SF_ERR_ARG), (dict(dtype=3), L.SF_ERR_UNSUPPORTED), (dict(dtype=-1), L.SF_ERR_UNSUPPORTED)])
 def test_logprob_refusals(lib, kw, status):
     assert score(lib, **kw) == status and b"sf_token_logprobs" in lib.sf_last_error()
+
+
+def test_outputs_over_other_arrays_are_refused(lib):
+    """3 rows of 100 fp32 logits, 100 apart; five of top."""
+    bytes = [1200, 12, 12, 12, 12, 60, 60]                 # logits, tokens, outputs
+    for x in range(2, 7):
+        for y in range(7):
+            if x == y:
+                continue
+            for shift in (0, bytes[y] - 4):
+                at = [PTR + (i << 18) for i in range(7)]
+                at[x] = at[y] + shift
+                assert lib.sf_token_logprobs(at[0], L.SF_DT_F32, 100, 3, 100, at[1], 5, *at[2:], None) == L.SF_ERR_ARG
+                assert b"overlaps" in lib.sf_last_error(), (x, y, shift)
 
 
 def test_nothing_to_do_is_ok(lib):
