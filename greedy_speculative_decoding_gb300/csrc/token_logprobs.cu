@@ -39,7 +39,7 @@ namespace sf {
 namespace {
 
 constexpr int kMaxTop = 32;
-constexpr int kMaxCluster = 8;           // (of 4: one row 8.9 us for 6.8)
+constexpr int kMaxCluster = 8;          // (of 4: one row 8.9 us for 6.8; of 16: 5.8 for 6.3, but with five 9.5 for 9.4, 16 rows 12.4 for 10.8)
 constexpr int kBuffer = 1024;           // elements that reach the bound; more (rows made for it) are handled apart
 constexpr int kAhead = 4;               // vectors that a thread works on together
 constexpr int kStages = 2;              // as often as many on their way
