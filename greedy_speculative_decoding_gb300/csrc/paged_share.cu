@@ -5,8 +5,8 @@
 // Each is one cluster of CTAs, or one small CTA. What must be known of every
 // request of the list (its entries' place among all entries, whether an earlier
 // one names the same request) every CTA finds for itself in shared memory; the
-// entries are then dealt out, a stretch to each CTA and eight in a row to each
-// thread, so that their loads are on their way together. Counts change by atomic
+// entries are then dealt out, a stretch to each CTA and two to eight in a row to
+// each thread, so that their loads are on their way together. Counts change by atomic
 // additions of whole numbers, whose order does not matter, and where order
 // matters (which of the releases of one page puts it onto the stack) the first
 // in the list wins. What bounds all three is the chain of barriers and of loads
@@ -15,6 +15,7 @@
 #include <atomic>
 #include <climits>
 #include <initializer_list>
+#include <type_traits>
 
 #include "paged.h"
 
@@ -23,7 +24,6 @@ namespace {
 
 constexpr int kThreads = 1024, kCluster = 8;   // of many entries; few: one CTA of kFewThreads
 constexpr int kFewThreads = 256;
-constexpr int kRun = 8;              // entries of a thread, one after the other
 constexpr int kMaxPages = 1 << 20;   // of a compaction (its bit map lies in shared memory)
 
 // Exclusive sum of x over the CTA's threads and its total.
@@ -75,6 +75,21 @@ __device__ __forceinline__ void first_of(const int* list, int n, int B, int* s_f
   __syncthreads();
 }
 
+// Calls f with the entries that a thread takes one after the other. In a cluster
+// four, or eight where that leaves one round of the threads: more a thread are
+// more loads under way together, but fewer threads at work (a release and a fork
+// of 18997 entries: 2, which is two rounds, 27.7 us, 4 21.9, 8 28.8). One CTA: two,
+// as there is little to do and the code has to be fetched.
+template <bool FEW, typename F>
+__device__ __forceinline__ void with_run(int n, int threads, F f) {
+  if constexpr (FEW) {
+    f(std::integral_constant<int, 2>());
+  } else {
+    if (n <= 4 * threads) f(std::integral_constant<int, 4>());
+    else f(std::integral_constant<int, 8>());
+  }
+}
+
 struct FreeArgs {
   const int *requests, *keep;
   int n;
@@ -87,7 +102,8 @@ struct FreeArgs {
   int B, W, P, cap, shift;
 };
 
-__global__ void __launch_bounds__(kThreads) k_page_free(const FreeArgs a) {
+template <bool FEW>   // one CTA of kFewThreads
+__global__ void __launch_bounds__(FEW ? kFewThreads : kThreads, 1) k_page_free(const FreeArgs a) {
   extern __shared__ int share_smem[];
   int* s_first = share_smem;        // [B] the first of the list that names a request
   int* s_at = s_first + a.B;        // [n + 1] entries released before
@@ -129,90 +145,94 @@ __global__ void __launch_bounds__(kThreads) k_page_free(const FreeArgs a) {
   }
   if (tid == 0) s_at[a.n] = total;
   cluster_sync();   // held, n_free and shares have been read
-  // A stretch of the releases for each CTA, in rounds of kRun for each thread:
-  // their pages, or -1 (one round, nearly always: they are looked up once).
-  const int k0 = (int)((long long)total * rank / ctas), k1 = (int)((long long)total * (rank + 1) / ctas);
-  const int round = NT * kRun, rounds = (k1 - k0 + round - 1) / round;
-  int page[kRun];
-  auto look_up = [&](int rd) {
-    const int first = k0 + rd * round + tid * kRun;
-    int i = first < k1 ? place_of(s_at, a.n - 1, first) : 0;
+  int all = 0;   // pages that go onto the stack
+  with_run<FEW>(total, ctas * NT, [&](auto run) {
+    constexpr int kRun = decltype(run)::value;
+    // A stretch of the releases for each CTA, in rounds of kRun for each thread:
+    // their pages, or -1 (one round, nearly always: they are looked up once).
+    const int k0 = (int)((long long)total * rank / ctas), k1 = (int)((long long)total * (rank + 1) / ctas);
+    const int round = NT * kRun, rounds = (k1 - k0 + round - 1) / round;
+    int page[kRun];
+    auto look_up = [&](int rd) {
+      const int first = k0 + rd * round + tid * kRun;
+      int i = first < k1 ? place_of(s_at, a.n - 1, first) : 0;
 #pragma unroll
-    for (int e = 0; e < kRun; ++e) {
-      const int k = first + e;
-      page[e] = -1;
-      if (k < k1) {
-        while (k >= s_at[i + 1]) ++i;
-        const int p = a.tables[(size_t)s_row[i] * a.W + s_from[i] + (k - s_at[i])];
-        page[e] = p >= 0 && p < a.P ? p : -1;
+      for (int e = 0; e < kRun; ++e) {
+        const int k = first + e;
+        page[e] = -1;
+        if (k < k1) {
+          while (k >= s_at[i + 1]) ++i;
+          const int p = a.tables[(size_t)s_row[i] * a.W + s_from[i] + (k - s_at[i])];
+          page[e] = p >= 0 && p < a.P ? p : -1;
+        }
       }
+    };
+    if (rounds == 1) look_up(0);
+    // Count the releases. A page that has as many as holders is left at -1.
+    for (int rd = 0; rd < rounds; ++rd) {
+      if (rounds > 1) look_up(rd);
+#pragma unroll
+      for (int e = 0; e < kRun; ++e)
+        if (page[e] >= 0) atomicSub(&a.shares[page[e]], 1);
     }
-  };
-  if (rounds == 1) look_up(0);
-  // Count the releases. A page that has as many as holders is left at -1.
-  for (int rd = 0; rd < rounds; ++rd) {
-    if (rounds > 1) look_up(rd);
+    cluster_sync();
+    // Its first release claims it (claims lie below all counts: total < 2^30).
+    for (int rd = 0; rd < rounds; ++rd) {
+      if (rounds > 1) look_up(rd);
+      const int first = k0 + rd * round + tid * kRun;
+      int count[kRun];
 #pragma unroll
-    for (int e = 0; e < kRun; ++e)
-      if (page[e] >= 0) atomicSub(&a.shares[page[e]], 1);
-  }
-  cluster_sync();
-  // Its first release claims it (claims lie below all counts: total < 2^30).
-  for (int rd = 0; rd < rounds; ++rd) {
-    if (rounds > 1) look_up(rd);
-    const int first = k0 + rd * round + tid * kRun;
-    int count[kRun];
+      for (int e = 0; e < kRun; ++e) count[e] = page[e] >= 0 ? __ldcg(&a.shares[page[e]]) : 0;
 #pragma unroll
-    for (int e = 0; e < kRun; ++e) count[e] = page[e] >= 0 ? __ldcg(&a.shares[page[e]]) : 0;
+      for (int e = 0; e < kRun; ++e)
+        if (count[e] < 0) atomicMin(&a.shares[page[e]], INT_MIN + first + e);
+    }
+    cluster_sync();
+    // Claimed pages go onto the stack in the list's order: first how many they
+    // are in each CTA's stretch, then where they go.
+    auto claimed = [&](int rd) {   // bit e: release e of the thread's has its page
+      const int first = k0 + rd * round + tid * kRun;
+      int count[kRun], bits = 0;
 #pragma unroll
-    for (int e = 0; e < kRun; ++e)
-      if (count[e] < 0) atomicMin(&a.shares[page[e]], INT_MIN + first + e);
-  }
-  cluster_sync();
-  // Claimed pages go onto the stack in the list's order: first how many they
-  // are in each CTA's stretch, then where they go.
-  auto claimed = [&](int rd) {   // bit e: release e of the thread's has its page
-    const int first = k0 + rd * round + tid * kRun;
-    int count[kRun], bits = 0;
+      for (int e = 0; e < kRun; ++e) count[e] = page[e] >= 0 ? __ldcg(&a.shares[page[e]]) : 0;
 #pragma unroll
-    for (int e = 0; e < kRun; ++e) count[e] = page[e] >= 0 ? __ldcg(&a.shares[page[e]]) : 0;
-#pragma unroll
-    for (int e = 0; e < kRun; ++e) bits |= (page[e] >= 0 && count[e] == INT_MIN + first + e) << e;
-    return bits;
-  };
-  int mine = 0, bits = 0;
-  for (int rd = 0; rd < rounds; ++rd) {
-    if (rounds > 1) look_up(rd);
-    bits = claimed(rd);
-    mine += __popc(bits);
-  }
-  int of_cta;
-  scan_cta(mine, of_cta, warp_sums);
-  if (tid == 0) s_mine = of_cta;
-  cluster_sync();
-  int at = n_free, all = 0;
-  for (int c = 0; c < ctas; ++c) {
-    int x;
-    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(x) : "r"(dsmem_addr(smem_u32(&s_mine), c)) : "memory");
-    at += c < rank ? x : 0;
-    all += x;
-  }
-  for (int rd = 0; rd < rounds; ++rd) {
-    if (rounds > 1) {
-      look_up(rd);
+      for (int e = 0; e < kRun; ++e) bits |= (page[e] >= 0 && count[e] == INT_MIN + first + e) << e;
+      return bits;
+    };
+    int mine = 0, bits = 0;
+    for (int rd = 0; rd < rounds; ++rd) {
+      if (rounds > 1) look_up(rd);
       bits = claimed(rd);
+      mine += __popc(bits);
     }
-    int t;
-    int pos = at + scan_cta(__popc(bits), t, warp_sums);
-    at += t;
-#pragma unroll
-    for (int e = 0; e < kRun; ++e)
-      if (bits >> e & 1) {
-        if (pos < a.cap) a.free[pos] = page[e];
-        a.shares[page[e]] = 0;
-        ++pos;
+    int of_cta;
+    scan_cta(mine, of_cta, warp_sums);
+    if (tid == 0) s_mine = of_cta;
+    cluster_sync();
+    int at = n_free;
+    for (int c = 0; c < ctas; ++c) {
+      int x;
+      asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(x) : "r"(dsmem_addr(smem_u32(&s_mine), c)) : "memory");
+      at += c < rank ? x : 0;
+      all += x;
+    }
+    for (int rd = 0; rd < rounds; ++rd) {
+      if (rounds > 1) {
+        look_up(rd);
+        bits = claimed(rd);
       }
-  }
+      int t;
+      int pos = at + scan_cta(__popc(bits), t, warp_sums);
+      at += t;
+#pragma unroll
+      for (int e = 0; e < kRun; ++e)
+        if (bits >> e & 1) {
+          if (pos < a.cap) a.free[pos] = page[e];
+          a.shares[page[e]] = 0;
+          ++pos;
+        }
+    }
+  });
   if (rank == 0) {
     for (int i = tid; i < a.n; i += NT) {
       const int r = s_row[i];
@@ -236,7 +256,8 @@ struct ForkArgs {
   int B, W, P, cap, shift;
 };
 
-__global__ void __launch_bounds__(kThreads) k_page_fork(const ForkArgs a) {
+template <bool FEW>   // one CTA of kFewThreads
+__global__ void __launch_bounds__(FEW ? kFewThreads : kThreads, 1) k_page_fork(const ForkArgs a) {
   extern __shared__ int share_smem[];
   int* s_first = share_smem;        // [B]
   int* s_at = s_first + a.B;        // [n + 1] shared entries before
@@ -291,29 +312,32 @@ __global__ void __launch_bounds__(kThreads) k_page_fork(const ForkArgs a) {
   }
   if (tid == 0) s_at[a.n] = total;
   cluster_sync();   // held and n_free have been read
-  for (int first = (rank * NT + tid) * kRun; first < total; first += ctas * NT * kRun) {
-    int page[kRun];
-    const int i0 = place_of(s_at, a.n - 1, first);
-    int i = i0;
+  with_run<FEW>(total, ctas * NT, [&](auto run) {
+    constexpr int kRun = decltype(run)::value;
+    for (int first = (rank * NT + tid) * kRun; first < total; first += ctas * NT * kRun) {
+      int page[kRun];
+      const int i0 = place_of(s_at, a.n - 1, first);
+      int i = i0;
 #pragma unroll
-    for (int e = 0; e < kRun; ++e) {
-      const int k = first + e;
-      if (k < total) {
-        while (k >= s_at[i + 1]) ++i;
-        page[e] = a.tables[(size_t)s_src[i] * a.W + (k - s_at[i])];
+      for (int e = 0; e < kRun; ++e) {
+        const int k = first + e;
+        if (k < total) {
+          while (k >= s_at[i + 1]) ++i;
+          page[e] = a.tables[(size_t)s_src[i] * a.W + (k - s_at[i])];
+        }
+      }
+      i = i0;
+#pragma unroll
+      for (int e = 0; e < kRun; ++e) {
+        const int k = first + e;
+        if (k < total) {
+          while (k >= s_at[i + 1]) ++i;
+          a.tables[(size_t)s_dst[i] * a.W + (k - s_at[i])] = page[e];
+          if (page[e] >= 0 && page[e] < a.P) atomicAdd(&a.shares[page[e]], 1);
+        }
       }
     }
-    i = i0;
-#pragma unroll
-    for (int e = 0; e < kRun; ++e) {
-      const int k = first + e;
-      if (k < total) {
-        while (k >= s_at[i + 1]) ++i;
-        a.tables[(size_t)s_dst[i] * a.W + (k - s_at[i])] = page[e];
-        if (page[e] >= 0 && page[e] < a.P) atomicAdd(&a.shares[page[e]], 1);
-      }
-    }
-  }
+  });
   if (rank == 0) {
     for (int i = tid; i < a.n; i += NT)
       if (s_src[i] >= 0) a.held[s_dst[i]] = ceil_pages(a.lens[s_src[i]], a.shift);
@@ -444,12 +468,13 @@ __global__ void __launch_bounds__(kThreads) k_page_compact(const CompactArgs a) 
 }
 
 // Launches a cluster of CTAs, or one small CTA for at most kFew entries and
-// requests (us, one CTA and a cluster: a release that finds nothing 4.6 and 6.2, a
-// compaction of 97 pages 5.3 and 6.1; a release and a fork of 256 requests with
-// 18997 entries 131 and 29, a compaction of 50191 pages 470 and 30).
-constexpr long kFew = 4096;
+// requests, as the tables could hold them (us, one CTA and a cluster: a release
+// that finds nothing 4.4 and 6.2, a compaction of 97 pages 5.3 and 6.1; a release
+// and a fork in tables of 336 entries 12.2 and 15.3, 672 12.1 and 14.9, 1408 23.9
+// and 16.4).
+constexpr long kFew = 1024;
 template <typename Args>
-cudaError_t launch_share(void (*fn)(Args), const Args& a, long entries, size_t smem, std::atomic<uint64_t>& ready,
+cudaError_t launch_share(void (*fn)(Args), const Args& a, bool few, size_t smem, std::atomic<uint64_t>& ready,
                          cudaStream_t st) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -462,11 +487,11 @@ cudaError_t launch_share(void (*fn)(Args), const Args& a, long entries, size_t s
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = entries <= kFew ? 1 : kCluster;
+  attr[1].val.clusterDim.x = few ? 1 : kCluster;
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(entries <= kFew ? 1 : kCluster);
-  cfg.blockDim = dim3(entries <= kFew ? kFewThreads : kThreads);
+  cfg.gridDim = dim3(few ? 1 : kCluster);
+  cfg.blockDim = dim3(few ? kFewThreads : kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cfg.attrs = attr;
@@ -522,10 +547,12 @@ extern "C" sf_status sf_page_free(const int32_t* d_requests, const int32_t* d_ke
                                    {d_held, batch, true}, {d_shares, n_pages, true}, {d_free, capacity, true},
                                    {d_n_free, 1, true}, {d_status, n, true}});
   if (s != SF_OK) return s;
-  static std::atomic<uint64_t> ready{0};
+  static std::atomic<uint64_t> ready[2];
+  const bool few = (long)n * table_width + batch <= kFew;
   const FreeArgs a{d_requests, d_keep, n, d_tables, d_held, d_shares, d_free, d_n_free, d_status, batch, table_width,
                    n_pages, capacity, log2_of(page)};
-  const cudaError_t e = launch_share(k_page_free, a, (long)n * table_width + batch, ((size_t)batch + 3 * n + 1) * sizeof(int), ready,
+  const cudaError_t e = launch_share(few ? k_page_free<true> : k_page_free<false>, a, few,
+                                     ((size_t)batch + 3 * n + 1) * sizeof(int), ready[few],
                                      static_cast<cudaStream_t>(cuda_stream));
   if (e != cudaSuccess) return set_error(SF_ERR_CUDA, "sf_page_free: %s", cudaGetErrorString(e));
   return SF_OK;
@@ -548,10 +575,12 @@ extern "C" sf_status sf_page_fork(const int32_t* d_src, const int32_t* d_dst, in
                                    {d_shares, n_pages, true}, {d_free, capacity, false}, {d_n_free, 1, true},
                                    {d_source, n, true}, {d_target, n, true}, {d_slots, n, true}, {d_status, n, true}});
   if (s != SF_OK) return s;
-  static std::atomic<uint64_t> ready{0};
+  static std::atomic<uint64_t> ready[2];
+  const bool few = (long)n * table_width + batch <= kFew;
   const ForkArgs a{d_src, d_dst, d_lens, n, d_tables, d_held, d_shares, d_free, d_n_free, d_source, d_target, d_slots,
                    d_status, batch, table_width, n_pages, capacity, log2_of(page)};
-  const cudaError_t e = launch_share(k_page_fork, a, (long)n * table_width + batch, ((size_t)batch + 3 * n + 1) * sizeof(int), ready,
+  const cudaError_t e = launch_share(few ? k_page_fork<true> : k_page_fork<false>, a, few,
+                                     ((size_t)batch + 3 * n + 1) * sizeof(int), ready[few],
                                      static_cast<cudaStream_t>(cuda_stream));
   if (e != cudaSuccess) return set_error(SF_ERR_CUDA, "sf_page_fork: %s", cudaGetErrorString(e));
   return SF_OK;
@@ -581,7 +610,7 @@ extern "C" sf_status sf_page_compact(const int32_t* d_tables, int32_t batch, int
   const CompactArgs a{d_tables, d_held, d_shares, d_tables_out, d_shares_out, d_free, d_n_free, d_source, d_target,
                       d_count, batch, table_width, n_pages, moves};
   const size_t blocks = ((size_t)n_pages + 255) / 256;
-  const cudaError_t e = launch_share(k_page_compact, a, (long)batch * table_width + n_pages, (9 * blocks + 1 + batch + 1) * sizeof(int), ready,
+  const cudaError_t e = launch_share(k_page_compact, a, (long)batch * table_width + n_pages <= kFew, (9 * blocks + 1 + batch + 1) * sizeof(int), ready,
                                      static_cast<cudaStream_t>(cuda_stream));
   if (e != cudaSuccess) return set_error(SF_ERR_CUDA, "sf_page_compact: %s", cudaGetErrorString(e));
   return SF_OK;
