@@ -137,6 +137,10 @@ static cudaError_t enqueue(Args& a, const sf_paged_cache& c, int q_dtype, float 
   a.mt = z.mt;
   a.mt_max = std::min(a.max_rows * a.group, a.mt);
   a.ntq_max = z.ntq;
+  // (400 fp32 rows of 6000 tokens, 28 / 4 heads of 128: error 1.07e-6 with 4, 1.74e-6
+  // with 8, 3.0e-6 with 16, torch in fp32 1.24e-6; 1000 rows of 4000, 40 / 8 heads, 290,
+  // 274 and 270 us, 313 with 2. paged_attention keeps 16, as its calls are short.)
+  a.fold = chunk ? 4 : 16;
   a.by_item = z.items <= kMaxDesc;
   const Layout lay = layout(a.nq, a.nkv, c.head_dim, a.max_rows);
   unsigned char* ws = static_cast<unsigned char*>(workspace);

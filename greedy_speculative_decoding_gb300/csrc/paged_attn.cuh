@@ -55,6 +55,7 @@ struct Args {
   int ntq_max;             // items of a (request, KV head) at most
   int piece;               // units that an item's beginning counts for
   int rounds;              // of a chunk's units, at most
+  int fold;                // fp32 queries, tiles of 128: units after which O moves to the sums (a power of two)
   int by_warp;             // few requests: every warp finds the CTA's units by itself
   int wide;                // few items: a CTA joins one query, else four
   int by_item;             // descriptors by item (else by the CTA that starts it)

@@ -62,8 +62,8 @@ struct TcShape {
   static constexpr int kCtas = HD == 64 && !F32 ? 2 : 1, kCols = 512 / kCtas;
   // Units after which O moves to the sums. Of 16-bit queries the sums are the
   // piece's place in the workspace (over 2^20 slots in one CTA outputs were 0.5%
-  // too small without).
-  static constexpr int kFold = F32 ? 16 : 256;
+  // too small without). With fp32 queries the call says after how many (Args::fold).
+  static constexpr int kFold = 256;
   static constexpr int kSums = F32 ? MT * HD * 4 : 0;
   static constexpr int kStages = !F32 ? 6 : HD == 64 ? 10 : 4;
   static constexpr int kSmem = 1024 + kStages * kStage + kSums;
@@ -208,7 +208,7 @@ __global__ void __launch_bounds__(TcShape<HD, TC, F32>::kThreads, TcShape<HD, TC
         await(&p_full[n & 1], (n >> 1) & 1);
         if (!good) break;
         tc_fence_after();
-        const uint32_t keep = u % S::kFold ? 1u : (uint32_t)__shfl_sync(0xffffffffu, s_keep[n & 1], 0);
+        const uint32_t keep = (F32 ? u & (a.fold - 1) : u % S::kFold) ? 1u : (uint32_t)__shfl_sync(0xffffffffu, s_keep[n & 1], 0);
         const uint64_t d = dv + (uint64_t)(n % S::kStages * (S::kStage >> 4));
         const uint32_t t = utmem + S::kS + S::kSCols * (n & 1);
         if (elect_one()) {
@@ -395,7 +395,7 @@ __global__ void __launch_bounds__(TcShape<HD, TC, F32>::kThreads, TcShape<HD, TC
           l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
         }
         // ---- O starts anew with the piece and after moving to the sums
-        const bool fresh = (t - w.t0) % S::kFold == 0;
+        const bool fresh = (F32 ? (t - w.t0) & (a.fold - 1) : (t - w.t0) % S::kFold) == 0;
         if constexpr (F32) {
           if (fresh && t > w.t0) {
             o_wait(n - 1);
