@@ -584,8 +584,10 @@ __global__ void __launch_bounds__(Shape<HD, WM, WK, F32>::kThreads, Shape<HD, WM
       const int s = n % S::kStages;
       const uint32_t ks = smem_u32(ring) + s * S::kStage, vs = ks + S::kHalf * S::kBox;
       const int base = t * kTile + wk * SW;         // this warp's first slot
-      // ---- scores
-      float x[NS][4];
+      // ---- scores (fp32 queries: the small terms have a sum of their own, as the
+      // tensor cores cut off what they add to a large one: 19 rows over up to 4144
+      // slots, 128 dimensions, output off by 5.3e-7, 1.2e-6 without; as fast)
+      float x[NS][4], small[F32 ? NS : 1][4] = {};
 #pragma unroll
       for (int i = 0; i < NS; ++i) x[i][0] = x[i][1] = x[i][2] = x[i][3] = 0.f;
 #pragma unroll
@@ -607,10 +609,16 @@ __global__ void __launch_bounds__(Shape<HD, WM, WK, F32>::kThreads, Shape<HD, WM
           ldsm_x4(kb, ((ks + k_off) ^ ((2 * k & 7) << 4)) + (k >> 2) * S::kBox + i * 2048);
 #pragma unroll
           for (int e = NQ - 1; e >= 0; --e) {       // the small terms first
-            Num<TC>::mma(x[2 * i], qk[e], kb[0], kb[1]);
-            Num<TC>::mma(x[2 * i + 1], qk[e], kb[2], kb[3]);
+            Num<TC>::mma(e > 0 ? small[2 * i] : x[2 * i], qk[e], kb[0], kb[1]);
+            Num<TC>::mma(e > 0 ? small[2 * i + 1] : x[2 * i + 1], qk[e], kb[2], kb[3]);
           }
         }
+      }
+      if constexpr (F32) {
+#pragma unroll
+        for (int i = 0; i < NS; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[i][e] += small[i][e];
       }
       // ---- what a row does not see is -infinity (set, not added: what such
       // slots hold, NaN included, does not matter). vis[e]: the slots of the
