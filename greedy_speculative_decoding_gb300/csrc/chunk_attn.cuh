@@ -36,7 +36,7 @@
 //
 // Measured: 2048 rows over 16384 tokens, 40 / 8 heads of 128, 365 us (1770
 // TFLOP/s), of 64 300; a whole prompt of 8192, 28 / 4 heads of 128, 299 (1607);
-// nine prompts of 33..4099 tokens 314. Tried, at 128 and 64, for what stood then:
+// nine prompts of 33..4099 tokens 316. Tried, at 128 and 64, for what stood then:
 // the maximum of half a unit at a time 458 for 405 and 463 for 320; P apart from
 // S, 388 for 317 at 64; a third warpgroup that loads and stores 466 for 392;
 // scalar multiplications in place of pairs 416 for 405 and 346 for 319; one
@@ -275,8 +275,13 @@ struct Piece {
   int whole;               // all of the item's units
   int v;                   // the share
 };
-// The ring of tiles lets the producer be at most six units ahead, so as many pieces.
-constexpr int kPieces = 16, kChecks = 8;
+// Places for pieces. The ring of tiles lets the producer be at most six units, so
+// six pieces, ahead of the MMA warp, the warps that look at values and the first
+// tile; but not of the second tile's warps, which it does not hold back over pieces
+// that have no queries for them. So the softmax warps say when they are done with a
+// place (kPieceWarps of them), and the producer waits for that before it writes the
+// place anew.
+constexpr int kPieces = 16, kPieceWarps = 8, kChecks = 8;
 
 // The join's descriptor of an item that begins in share v (one thread).
 __device__ __forceinline__ void describe(const Args& a, const ChunkWalk& w, int v, const Shares& shares, bool whole) {
@@ -372,7 +377,7 @@ __global__ void __launch_bounds__(ChunkShape<HD, TC>::kThreads, 1) k_chunk_attn(
   __shared__ Shares s_shares;
   // full: a tile of the ring has landed; empty: it may be loaded anew; checked: a unit's values may be used.
   __shared__ __align__(8) uint64_t full[NS], empty[NS], checked[kChecks], q_full[2], s_full[2], p_full[2][2], o_done[2], drain;
-  __shared__ __align__(8) uint64_t piece_full[kPieces];
+  __shared__ __align__(8) uint64_t piece_full[kPieces], piece_empty[kPieces];
   __shared__ Piece s_piece[kPieces];
   __shared__ int s_odd[kPieces];   // the first slot with a value that is no finite number, among those looked at
   __shared__ uint32_t s_tmem;
@@ -392,13 +397,15 @@ __global__ void __launch_bounds__(ChunkShape<HD, TC>::kThreads, 1) k_chunk_attn(
       mbar_init(&o_done[x], 1);
     }
     mbar_init(&drain, 1);
-    for (int i = 0; i < kPieces; ++i) mbar_init(&piece_full[i], 1);
+    for (int i = 0; i < kPieces; ++i) {
+      mbar_init(&piece_full[i], 1);
+      mbar_init(&piece_empty[i], kPieceWarps);
+    }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   } else if (warp == 8 && lane < 2) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(lane ? &a.vm : &a.km)) : "memory");
   }
-  if (tid < kPieces) s_odd[tid] = INT32_MAX;
-  if (tid == kPieces) s_fail = 0;
+  if (tid == 0) s_fail = 0;
   if (warp == 9) {
     tmem_alloc(&s_tmem, 512);
     tmem_relinquish();
@@ -411,7 +418,8 @@ __global__ void __launch_bounds__(ChunkShape<HD, TC>::kThreads, 1) k_chunk_attn(
   pdl_launch_next();
   chunk_walk<HD, TC>(a, sh_loc, s_shares);
   bool ok = true;
-  // Piece i of the CTA, for the other warps; no units at the end.
+  // Piece i of the CTA, for the other warps; no units at the end. (A warp that has
+  // given up sees the end.)
   auto piece_at = [&](int i) {
     await(ok, &piece_full[i % kPieces], i / kPieces & 1);
     ok = __all_sync(0xffffffffu, ok);
@@ -442,8 +450,15 @@ __global__ void __launch_bounds__(ChunkShape<HD, TC>::kThreads, 1) k_chunk_attn(
           continue;
         }
         const int v = blockIdx.x + round * gridDim.x;
+        // Its place (also to tell of an end because a wait ran out, unless this one does).
+        const bool place = __all_sync(0xffffffffu, mbar_wait(&piece_empty[piece % kPieces], piece / kPieces & 1 ^ 1, kWaitPolls));
+        if (!place) {
+          ok = false;
+          break;
+        }
         if (lane == 0) {
           const bool whole = more && w.t0 == 0 && w.t1 == w.nt;
+          s_odd[piece % kPieces] = INT32_MAX;
           s_piece[piece % kPieces] =
               more ? Piece{w.r.s0, w.r.rows, w.r.len, w.r.p0, w.item_h, w.item_q, w.t0, w.t1, whole, v} : Piece{};
           mbar_arrive(&piece_full[piece % kPieces]);
@@ -588,7 +603,6 @@ __global__ void __launch_bounds__(ChunkShape<HD, TC>::kThreads, 1) k_chunk_attn(
       for (int piece = 0;; ++piece) {
         const Piece w = piece_at(piece);
         if (w.t1 == 0) break;
-        if (me == 0) s_odd[(piece + 8) % kPieces] = INT32_MAX;   // (nobody is that many pieces behind)
         // From slot `seen` on some row of the item does not see a slot.
         const int seen = w.p0 + w.q * 256 / a.group + 1;
         for (int t = w.t0; t < w.t1; ++t, ++n) {
@@ -676,6 +690,11 @@ __global__ void __launch_bounds__(ChunkShape<HD, TC>::kThreads, 1) k_chunk_attn(
       __syncwarp();
       if (lane == 0) mbar_arrive(&q_full[x]);
     };
+    // The warp is done with piece i's place, its first odd slot among it.
+    auto release = [&](int i) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&piece_empty[i % kPieces]);
+    };
     // The next piece with queries for this tile, its queries on their way.
     int i = 0;
     auto next_piece = [&] {
@@ -686,6 +705,7 @@ __global__ void __launch_bounds__(ChunkShape<HD, TC>::kThreads, 1) k_chunk_attn(
           load_queries(p);
           return p;
         }
+        release(i);
         ++i;
       }
     };
@@ -814,21 +834,23 @@ __global__ void __launch_bounds__(ChunkShape<HD, TC>::kThreads, 1) k_chunk_attn(
         }
         unit(t);
       }
-      // ---- the next piece's queries (the scores have been read, so these have too)
-      const int odd_at = i++ % kPieces;
-      w = next_piece();
-
-      // ---- the end of the piece
+      // ---- O is there, and all that is to be known of the piece; only then is the
+      // next one looked for, over any number of pieces that other tiles have alone.
+      // (Its queries go where this one's were, whose scores have been read. Loaded
+      // before the wait, with the search behind it: 322 us for nine prompts, 315 so.)
       await(ok, &o_done[x], my_pieces & 1);
       tc_fence_after();
       ++my_pieces;
+      const int odd = s_odd[i % kPieces];
+      release(i++);
+      w = next_piece();
       float f = 0.f;                                          // of what lies in the part
       if (folded && live) {
         const float2 ml = *part_ml;
         f = ml.x == -INFINITY ? 0.f : exp2_approx((ml.x - m) * a.scale2);
         l = fmaf(ml.y, f, l);
       }
-      if (s_odd[odd_at] < lim) l = __int_as_float(0x7fc00000);   // the row sees a value that is no number: NaN
+      if (odd < lim) l = __int_as_float(0x7fc00000);   // the row sees a value that is no number: NaN
       if (m != -INFINITY) m = fmaf(m, a.scale2, (float)-S::kUp);
       if (warp_live) {
         const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
