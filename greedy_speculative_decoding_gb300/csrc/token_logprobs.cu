@@ -429,7 +429,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) k_token_logprobs(co
       for (int j = tid; j < n * per; j += kThreads) {
         const int p = j / per, r = j - p * per, g = groups[p], w = v0 + (r >> 2) * kThreads + 4 * g + (r & 3);
         if (w < v1) {
-          const V y = {__ldg(xv + w)};
+          const V y = {xv[w]};   // (not through the read-only path: the kernel may start before the logits' writer has ended)
 #pragma unroll
           for (int e = 0; e < V::N; ++e) f(y.get(e), head + w * V::N + e, g);
         }
