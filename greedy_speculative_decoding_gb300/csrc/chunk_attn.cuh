@@ -36,7 +36,7 @@
 //
 // Measured: 2048 rows over 16384 tokens, 40 / 8 heads of 128, 365 us (1770
 // TFLOP/s), of 64 300; a whole prompt of 8192, 28 / 4 heads of 128, 299 (1607);
-// nine prompts of 33..4099 tokens 316. Tried, at 128 and 64, for what stood then:
+// nine prompts of 33..4099 tokens 297. Tried, at 128 and 64, for what stood then:
 // the maximum of half a unit at a time 458 for 405 and 463 for 320; P apart from
 // S, 388 for 317 at 64; a third warpgroup that loads and stores 466 for 392;
 // scalar multiplications in place of pairs 416 for 405 and 346 for 319; one
@@ -359,10 +359,13 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
 // As wait, without a call (setmaxnreg's register counts allow none), for a
 // converged warp; once a wait has run out (ok false) no further one is begun.
 // The lanes do not vote on it: that would cost 100 cycles a wait. Whoever gave up
-// goes on without waiting, to the end of the piece at least; the CTA's rows
-// become NaN in the end.
-__device__ __forceinline__ void await(bool& ok, uint64_t* bar, uint32_t parity) {
-  if (ok) ok = mbar_wait(bar, parity, kWaitPolls);
+// goes on without waiting, to the end of the piece at least, but frees no tile any
+// more (a copy into one that is on its way already may not be begun); the CTA's
+// rows become NaN in the end. (The bound is an argument of the call, for a test
+// that makes waits run out. As a constant: nine prompts 313 us, 297 so; 64 chunks of
+// 200 rows at 64 dimensions 239 and 227.)
+__device__ __forceinline__ void await(bool& ok, uint64_t* bar, uint32_t parity, uint32_t polls) {
+  if (ok) ok = mbar_wait(bar, parity, polls);
   __syncwarp();
 }
 
@@ -421,7 +424,7 @@ __global__ void __launch_bounds__(ChunkShape<HD, TC>::kThreads, 1) k_chunk_attn(
   // Piece i of the CTA, for the other warps; no units at the end. (A warp that has
   // given up sees the end.)
   auto piece_at = [&](int i) {
-    await(ok, &piece_full[i % kPieces], i / kPieces & 1);
+    await(ok, &piece_full[i % kPieces], i / kPieces & 1, a.polls);
     ok = __all_sync(0xffffffffu, ok);
     Piece p = s_piece[i % kPieces];
     if (!ok) p.t1 = p.t0 = 0, s_fail = 1;
@@ -451,7 +454,7 @@ __global__ void __launch_bounds__(ChunkShape<HD, TC>::kThreads, 1) k_chunk_attn(
         }
         const int v = blockIdx.x + round * gridDim.x;
         // Its place (also to tell of an end because a wait ran out, unless this one does).
-        const bool place = __all_sync(0xffffffffu, mbar_wait(&piece_empty[piece % kPieces], piece / kPieces & 1 ^ 1, kWaitPolls));
+        const bool place = __all_sync(0xffffffffu, mbar_wait(&piece_empty[piece % kPieces], piece / kPieces & 1 ^ 1, a.polls));
         if (!place) {
           ok = false;
           break;
@@ -489,7 +492,7 @@ __global__ void __launch_bounds__(ChunkShape<HD, TC>::kThreads, 1) k_chunk_attn(
           const int off = (t * SL) & ((1 << a.shift) - 1);
 #pragma unroll
           for (int v = 0; v < 2; ++v) {               // keys, then values
-            await(ok, &empty[s], phase);
+            await(ok, &empty[s], phase, a.polls);
             if (!__all_sync(0xffffffffu, ok)) {
               ok = false;
               break;
@@ -520,10 +523,10 @@ __global__ void __launch_bounds__(ChunkShape<HD, TC>::kThreads, 1) k_chunk_attn(
         const uint64_t dq = sw128_desc(smem_u32(qbuf)), dk = sw128_desc(smem_u32(ring));
         const uint64_t dv = sw128_desc_mn(smem_u32(ring), S::kBox);
         auto wait_for = [&](uint64_t* bar, uint32_t parity) {
-          if (ok && !mbar_wait(bar, parity, 1)) ok = mbar_wait(bar, parity, kWaitPolls);
+          if (ok && !mbar_wait(bar, parity, 1)) ok = mbar_wait(bar, parity, a.polls);
           tc_fence_after();
         };
-        // S of tile x with the keys in stage s; the last tile frees the stage.
+        // S of tile x with the keys in stage s; the last tile frees the stage (unless a wait has run out).
         auto scores = [&](int x, int s, bool last) {
           const uint64_t q = dq + (uint64_t)(x * (S::kTileBytes >> 4)), d = dk + (uint64_t)(s * (S::kTileBytes >> 4));
 #pragma unroll
@@ -532,7 +535,7 @@ __global__ void __launch_bounds__(ChunkShape<HD, TC>::kThreads, 1) k_chunk_attn(
             umma_bf16(tmem + S::kS + SL * x, q + o, d + o, id_s, k > 0);
           }
           umma_commit(&s_full[x]);
-          if (last) umma_commit(&empty[s]);
+          if (last && ok) umma_commit(&empty[s]);
         };
         // O of tile x += P V for half h of the unit's slots, the values in stage s.
         auto output = [&](int x, int s, int h, uint32_t keep) {
@@ -577,7 +580,7 @@ __global__ void __launch_bounds__(ChunkShape<HD, TC>::kThreads, 1) k_chunk_attn(
               wait_for(&p_full[x][1], done[x]);
               done[x] ^= 1;
               output(x, sv, 1, 1u);
-              if (last) umma_commit(&empty[sv]);
+              if (last && ok) umma_commit(&empty[sv]);
               if (more) {
                 if (x == 0) wait_for(&full[s], phase);
                 scores(x, s, last);
@@ -606,7 +609,7 @@ __global__ void __launch_bounds__(ChunkShape<HD, TC>::kThreads, 1) k_chunk_attn(
         // From slot `seen` on some row of the item does not see a slot.
         const int seen = w.p0 + w.q * 256 / a.group + 1;
         for (int t = w.t0; t < w.t1; ++t, ++n) {
-          await(ok, &full[s], phase);
+          await(ok, &full[s], phase, a.polls);
           const int s0 = min(max(seen - t * SL, 0), SL), s1 = min(max(w.len - t * SL, 0), SL);
           if (s0 < SL) {
             unsigned char* vs = ring + s * S::kTileBytes;
@@ -647,7 +650,7 @@ __global__ void __launch_bounds__(ChunkShape<HD, TC>::kThreads, 1) k_chunk_attn(
             }
           }
           __syncwarp();
-          if (lane == 0) mbar_arrive(&checked[n % kChecks]);
+          if (lane == 0 && ok) mbar_arrive(&checked[n % kChecks]);
           s += 2;
           if (s >= NS) s -= NS, phase ^= 1;
         }
@@ -663,7 +666,7 @@ __global__ void __launch_bounds__(ChunkShape<HD, TC>::kThreads, 1) k_chunk_attn(
     unsigned char* const qs = qbuf + x * S::kTileBytes;
     int n = 0, my_pieces = 0;                                 // units and pieces of this tile
     auto s_wait = [&] {
-      await(ok, &s_full[x], n & 1);
+      await(ok, &s_full[x], n & 1, a.polls);
       tc_fence_after();
     };
     // The piece's queries into shared memory (rows past the end: zeros).
@@ -838,7 +841,7 @@ __global__ void __launch_bounds__(ChunkShape<HD, TC>::kThreads, 1) k_chunk_attn(
       // next one looked for, over any number of pieces that other tiles have alone.
       // (Its queries go where this one's were, whose scores have been read. Loaded
       // before the wait, with the search behind it: 322 us for nine prompts, 315 so.)
-      await(ok, &o_done[x], my_pieces & 1);
+      await(ok, &o_done[x], my_pieces & 1, a.polls);
       tc_fence_after();
       ++my_pieces;
       const int odd = s_odd[i % kPieces];

@@ -3,6 +3,7 @@
 #include <algorithm>
 #include <cfloat>
 #include <cmath>
+#include <cstdlib>
 
 #include "paged_attn_launch.cuh"
 
@@ -157,6 +158,15 @@ static cudaError_t enqueue(Args& a, const sf_paged_cache& c, int q_dtype, float 
 // units of 128 slots, one CTA an SM (half as many, of twice the queries), and in
 // the workspace room for kRounds times as many.
 constexpr int kChunkQueries = 256, kChunkUnit = 128;
+// SF_TEST_WAIT_POLLS: fewer polls, so that some waits run out (error-path test).
+static uint32_t chunk_polls() {
+  static const uint32_t polls = [] {
+    const char* const v = std::getenv("SF_TEST_WAIT_POLLS");
+    const long n = v ? std::atol(v) : 0;
+    return n > 0 && n < (long)kWaitPolls ? (uint32_t)n : kWaitPolls;
+  }();
+  return polls;
+}
 static cudaError_t enqueue_chunk(Args& a, const sf_paged_cache& c, int q_dtype, float scale, void* workspace, int sms,
                                  cudaStream_t st) {
   const cudaError_t e = describe_cache(a, c, q_dtype, scale, kChunkUnit);
@@ -173,6 +183,7 @@ static cudaError_t enqueue_chunk(Args& a, const sf_paged_cache& c, int q_dtype, 
   a.part = reinterpret_cast<float*>(ws + lay.part);
   // Rounds, where the tables can hold more than L2 (the kernel looks at the lengths).
   a.rounds = (long)a.B * a.W * c.page * a.nkv * c.head_dim * 4 > 64l << 20 ? kRounds : 1;
+  a.polls = chunk_polls();
   const long max_units = items * (((long)a.W * c.page + kChunkUnit - 1) / kChunkUnit);
   sms = std::min(sms, kMaxCtas / 2);
   return c.head_dim == 128 ? launch_chunk_hd128(a, q_dtype, sms, max_units, st)

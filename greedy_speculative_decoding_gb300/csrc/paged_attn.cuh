@@ -36,7 +36,7 @@ namespace pa {
 
 constexpr int kTile = 64;                 // slots of a unit
 constexpr int kMaxPiece = 8;              // units that an item's beginning counts for, at most
-constexpr uint32_t kWaitPolls = 750000;   // bound of every wait: one second at 1.33 us a poll (measured)
+constexpr uint32_t kWaitPolls = 750000;   // bound of every wait: one to three seconds, at 1.33 to 4 us a poll (measured)
 
 struct Args {
   CUtensorMap km, vm;      // cache as {head_dim, slot or head, head or slot, page}
@@ -65,6 +65,7 @@ struct Args {
   bf16* frag;              // fp32 queries: the output in a projection's operand order instead of rows (act_store)
   int frag_umma;
   int* err;                // status word, or null
+  uint32_t polls;          // bound of a chunk's waits (kWaitPolls, unless a test makes some run out)
 };
 
 constexpr int kRounds = 3;   // that a chunk's units may be dealt out in
@@ -108,7 +109,7 @@ struct Deal {
   }
 };
 
-// Wait on an mbarrier phase; false after a second without it (the copies and
+// Wait on an mbarrier phase; false after seconds without it (the copies and
 // products waited for take microseconds). Counted in polls: a kernel that is
 // switched out while it waits, whatever the clock says, has not waited.
 static __device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity) {

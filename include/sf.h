@@ -515,7 +515,7 @@ SF_API sf_status sf_kv_append(const sf_paged_cache* cache, int32_t n, const sf_r
  * where the formula gives an infinity or a weight of 0.
  * workspace: sf_paged_attention_workspace_bytes(...) bytes of device scratch,
  * 256-byte aligned, any contents; calls that may overlap on the GPU need one
- * each. Waits inside the kernels are bounded (a second; what they wait for takes
+ * each. Waits inside the kernels are bounded (seconds; what they wait for takes
  * microseconds): one that runs out leaves NaN in the rows concerned.
  * The queries' tiles follow from what the tables can hold (batch, table_width,
  * page), as the lengths lie on the device. In tables much wider than the lengths
