@@ -204,7 +204,7 @@ static cudaError_t enqueue_chunk(Args& a, const sf_paged_cache& c, int q_dtype, 
 // At up to 128 queries the chunk kernel's second tile has nothing to do.
 static bool little_chunk(const sf_paged_cache& c, int n_heads, int max_rows, int batch, int table_width) {
   const long queries = (long)max_rows * (n_heads / c.n_kv_heads);
-  const long total = batch * c.n_kv_heads * ((queries + 127) / 128) * (((long)table_width * c.page + kTile - 1) / kTile);
+  const long total = (long)batch * c.n_kv_heads * ((queries + 127) / 128) * (((long)table_width * c.page + kTile - 1) / kTile);
   return queries <= 128 || total < 256 || (queries <= 768 && total <= 1536);
 }
 // The kernel counts a request's units as (group * slots) / 128 and its items in 32 bits.
