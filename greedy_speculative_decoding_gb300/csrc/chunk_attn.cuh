@@ -72,7 +72,7 @@ struct ChunkShape {
   // first scores and last output, which nothing runs beside). Nine whole prompts
   // at the 7B shape: 2 356 us, 3 327, 4 319, 5 341.
   static constexpr int kPiece = 4;
-  // Units of 128 slots whose keys and values stay in L2 (64 MB of 129; at 96 MB 24576 tokens take 588 us; chunk_walk).
+  // Units of 128 slots whose keys and values stay in L2 (64 MB of 129; at 96 MB 24576 tokens take 584 us; chunk_walk).
   static constexpr long kRound = (64l << 20) / (kSlots * HD * 4);
 };
 
@@ -183,10 +183,15 @@ struct Shares {
 // where their keys and values are more than L2 holds, items bring them from memory
 // again. So then the units are dealt out in up to three rounds, one after the
 // other over all CTAs (share v = CTA + round * CTAs), if items are enough that a
-// round still shares keys and values and the shares stay long. 2048 rows, 40 / 8
-// heads of 128, us in one round and so: 16384 tokens (67 MB) 363 and 365 (two),
-// 24576 588 and 575, 32768 811 and 763 (without a pause, at the power cap, 927 to
-// 969 and 850 to 875), 65536 1695 and 1592 (three).
+// round still shares keys and values (eight items a head) and the shares stay long
+// (64 units). 40 / 8 heads of 128, us in one round and in rounds: 17000 tokens (66
+// MB), 40 items a head (2048 rows) 390 and 391; 24576 584 and 569, 16 items 259 and
+// 245; 32768 811 and 758 (without a pause, at the power cap, 927 to 969 and 850 to
+// 875 once), 12 items 271 and 250; 65536, 40 items 1690 and 1583 (three), 8 374 and
+// 344. Not taken: 24576, 8 items 136 and 141, 2 57 and 80; 32768, 8 items 188 and
+// 178, 4 105 and 114; 65536, 6 items 289 and 272, 4 196 and 205. At 64 dimensions,
+// where the exponentials bound it, calls ask for one round (32 / 16 heads, 32768
+// tokens, 40 items 1120 and 1130, 24 704 and 719, 2 80 and 90).
 template <int HD, typename TC>
 __device__ __forceinline__ void chunk_walk(const Args& a, long* sh, Shares& shares) {
   using S = ChunkShape<HD, TC>;

@@ -156,8 +156,9 @@ static cudaError_t enqueue(Args& a, const sf_paged_cache& c, int q_dtype, float 
 
 // The same with the kernel for chunks (16-bit queries): items of 256 queries,
 // units of 128 slots, one CTA an SM (half as many, of twice the queries), and in
-// the workspace room for kRounds times as many.
+// the workspace room for chunk_rounds times as many (measured at chunk_walk).
 constexpr int kChunkQueries = 256, kChunkUnit = 128;
+static int chunk_rounds(int head_dim) { return head_dim == 128 ? kRounds : 1; }
 // SF_TEST_WAIT_POLLS: fewer polls, so that some waits run out (error-path test).
 static uint32_t chunk_polls() {
   static const uint32_t polls = [] {
@@ -176,13 +177,13 @@ static cudaError_t enqueue_chunk(Args& a, const sf_paged_cache& c, int q_dtype, 
   a.mt_max = (int)std::min<long>(queries, kChunkQueries);
   a.ntq_max = (int)((queries + kChunkQueries - 1) / kChunkQueries);
   const long items = (long)a.B * a.nkv * a.ntq_max;
-  const Layout lay = layout(a.nq, a.nkv, c.head_dim, a.max_rows, kRounds);
+  const Layout lay = layout(a.nq, a.nkv, c.head_dim, a.max_rows, chunk_rounds(c.head_dim));
   unsigned char* ws = static_cast<unsigned char*>(workspace);
   a.desc = reinterpret_cast<int4*>(ws);
   a.part_ml = reinterpret_cast<float2*>(ws + lay.ml);
   a.part = reinterpret_cast<float*>(ws + lay.part);
   // Rounds, where the tables can hold more than L2 (the kernel looks at the lengths).
-  a.rounds = (long)a.B * a.W * c.page * a.nkv * c.head_dim * 4 > 64l << 20 ? kRounds : 1;
+  a.rounds = (long)a.B * a.W * c.page * a.nkv * c.head_dim * 4 > 64l << 20 ? chunk_rounds(c.head_dim) : 1;
   a.polls = chunk_polls();
   const long max_units = items * (((long)a.W * c.page + kChunkUnit - 1) / kChunkUnit);
   sms = std::min(sms, kMaxCtas / 2);
@@ -343,7 +344,7 @@ extern "C" size_t sf_chunk_attention_workspace_bytes(int32_t n_heads, int32_t n_
   if (n_heads < 1 || n_kv_heads < 1 || n_heads % n_kv_heads || n_heads > 65535 || (head_dim != 64 && head_dim != 128) ||
       max_rows < 1 || max_rows > kMaxChunk)
     return 0;
-  return pa::layout(n_heads, n_kv_heads, head_dim, max_rows, pa::kRounds).total;
+  return pa::layout(n_heads, n_kv_heads, head_dim, max_rows, pa::chunk_rounds(head_dim)).total;
 }
 
 extern "C" sf_status sf_chunk_attention(const sf_paged_cache* cache, const sf_rows* q, const sf_rows* out, int32_t n,
