@@ -572,13 +572,23 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) k_token_logprobs(co
 
 constexpr int kCtaThreads = 256;
 
-// CTAs of a row for n rows, `slots` CTAs at a time: the least waves times a
-// CTA's share of the row and what it takes beside that (0.15 of a long row).
-int ctas_of(long n, int vocab, long slots) {
+// CTAs of a row for n rows of less than a wave. By what was measured, in us: a CTA
+// alone takes 0.1 (16 bits: 0.05) for a thousand elements, half as much again with
+// alternatives; a cluster 1.2 and 0.007 for every CTA in all, of which a third stays
+// where memory, at 7 TB/s, is what bounds the call. us with 1 / 2 / 4 / 8 CTAs a row,
+// [] the choice, fp32: 152064 elements, 1 row 16.9 / 11.3 / 8.2 / [6.4], 72 17.7 / 11.9 /
+// [10.8] / 11.8, with twenty first 35.7 / 22.6 / 18.0 / [19.0], 152 17.9 / [15.9] / 20.5 /
+// 23.3; 32768, 1 row 6.2 / 5.6 / 5.0 / [4.8], 72 [6.5] / 6.0 / 6.3 / 7.5; 8192, 72 [4.2] /
+// 4.7 / 5.7 / 7.5; bf16: 152064, 1 row 12.6 / 9.3 / 7.2 / [6.3], 72 13.4 / 9.9 / [9.4] /
+// 11.1; 65536, 72 [7.9] / 6.8 / 7.2 / 8.2 (the furthest from the best of 132 measured).
+int ctas_of(long n, int vocab, int dtype, bool top) {
+  const bool f32 = dtype == SF_DT_F32;
+  const double alone = vocab * (f32 ? 1e-4 : 5e-5) * (top ? 1.5 : 1.0), memory = (double)n * vocab * (f32 ? 4 : 2) / 7e6;
   int best = 1;
   double least = 1e30;
-  for (int c = 1; c <= kMaxCluster && (c == 1 || vocab / c >= 4096); c *= 2) {
-    const double cost = (double)((n * c + slots - 1) / slots) * (1.0 / c + 0.15);
+  for (int c = 1; c <= kMaxCluster; c *= 2) {
+    const double more = c > 1 ? 0.007 * (double)n * c : 0.0;
+    const double cost = std::max(alone / c + (c > 1 ? 1.2 : 0.0) + more, memory + 0.3 * more);
     if (cost < least) least = cost, best = c;
   }
   return best;
@@ -639,7 +649,7 @@ extern "C" sf_status sf_token_logprobs(const void* d_logits, int32_t dtype, int6
   // Whole waves of rows, a CTA each, then the rest spread over the GPU.
   const long slots = (long)sms * (1024 / kCtaThreads), rest = n > slots ? n % slots : n;
   const cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
-  const int ctas = rest ? ctas_of(rest, vocab, slots) : 1;
+  const int ctas = rest ? ctas_of(rest, vocab, dtype, top > 0) : 1;
   if (rest < n && ctas > 1) {
     a.chain = 1;
     e = launch_rows(a, dtype, 0, n - rest, 1, st);
