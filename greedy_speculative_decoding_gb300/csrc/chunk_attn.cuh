@@ -34,9 +34,9 @@
 // Tensor memory holds both tiles' O and S (P over S), 512 columns at head
 // dimension 128.
 //
-// Measured: 2048 rows over 16384 tokens, 40 / 8 heads of 128, 365 us (1770
-// TFLOP/s), of 64 300; a whole prompt of 8192, 28 / 4 heads of 128, 299 (1607);
-// nine prompts of 33..4099 tokens 297. Tried, at 128 and 64, for what stood then:
+// Measured: 2048 rows over 16384 tokens, 40 / 8 heads of 128, 362 us (1780
+// TFLOP/s), of 64 299; a whole prompt of 8192, 28 / 4 heads of 128, 296 (1625);
+// nine prompts of 33..4099 tokens 296. Tried, at 128 and 64, for what stood then:
 // the maximum of half a unit at a time 458 for 405 and 463 for 320; P apart from
 // S, 388 for 317 at 64; a third warpgroup that loads and stores 466 for 392;
 // scalar multiplications in place of pairs 416 for 405 and 346 for 319; one

@@ -23,8 +23,8 @@
 // arithmetic (us: loaded into registers behind it, 1021 rows of 152064 bf16
 // logits 74, now 65; 400 fp32 rows 47.5, now 40; once four on their way 73 and 49,
 // three or four times two 71 and 42). 1021 rows of bf16 run at 4.8 TB/s, 400 of
-// fp32 at 6.0; 72 fp32 rows take 13 and with 20 alternatives 20, one row 6.5 and
-// with five 9.6: few rows are a chain of loads, reductions, the second look and
+// fp32 at 6.0; 72 fp32 rows take 10.8 and with 20 alternatives 19, one row 6.5 and
+// with five 9.7: few rows are a chain of loads, reductions, the second look and
 // the cluster's barriers; many are bound by memory in fp32, and in 16 bits by the
 // six instructions of an element and by the last wave's empty places. CTAs of 256
 // threads, four on an SM, so that some stream while others choose (with loads
@@ -55,8 +55,8 @@ struct ScoreArgs {
   // every CTA of the first has waited for what comes before both, so that is
   // done, and it touches nothing that the first one writes; before its own end it
   // waits for the first one's, as what follows looks at the second alone. (620
-  // rows of 152064 bf16 logits 52 us; with the wait in front of its reads 62, both
-  // in one launch of clusters 67.)
+  // rows of 152064 bf16 logits 38 us; with the wait in front of its reads 43, in one
+  // launch of a CTA a row 43, of clusters 76.)
   int chain;
   float *logprob, *entropy;
   int *rank, *top_ids;
