@@ -934,14 +934,17 @@ __global__ void __launch_bounds__(ChunkShape<HD, TC>::kThreads, 1) k_chunk_attn(
 
 // The join of the items that several CTAs share: the parts lie with the CTAs
 // first .. first + count - 1, and every CTA that one begins in has a descriptor.
-// A warp takes four queries of an item (a lane HD / 32 dimensions), so that all
-// of an item's CTAs are there at once: 6 us after nine whole prompts at the 7B
-// shape, 21 with a warp and a launched CTA for every item's every query.
-constexpr int kChunkJoinThreads = 256, kChunkJoinQueries = 4 * kChunkJoinThreads / 32;
+// A warp takes two queries of an item (a lane HD / 32 dimensions), four parts on
+// their way, so that nearly all of an item's CTAs are there at once: 6 us after nine
+// whole prompts at the 7B shape, 21 with a warp and a launched CTA for every item's
+// every query. Few items have many parts each: 30 rows of 16384 tokens, 28 / 4
+// heads of 128, the call 35 us, with four queries a warp and two parts 54, with one and eight
+// 32 (but nine prompts 300 for 296).
+constexpr int kChunkJoinThreads = 256, kChunkJoinQueries = 2 * kChunkJoinThreads / 32;
 template <int HD, typename TC>
 __global__ void __launch_bounds__(kChunkJoinThreads) k_chunk_join(const __grid_constant__ Args a) {
   constexpr int V = HD / 32;
-  const int lane = threadIdx.x & 31, x0 = blockIdx.y * kChunkJoinQueries + (threadIdx.x >> 5) * 4;
+  const int lane = threadIdx.x & 31, x0 = blockIdx.y * kChunkJoinQueries + (threadIdx.x >> 5) * 2;
   pdl_launch_next();
   pdl_wait();   // (before any return: what follows the join relies on the main kernel's end as well)
   const int4 d = a.desc[blockIdx.x];
@@ -949,20 +952,20 @@ __global__ void __launch_bounds__(kChunkJoinThreads) k_chunk_join(const __grid_c
   const Request r = request<256>(a, d.z);
   const int kvh = d.w / r.ntq, qt = d.w - kvh * r.ntq, Mq = r.rows * a.group;
   if (qt * 256 + x0 >= Mq) return;
-  float m[4], l[4], o[4][V];
+  float m[2], l[2], o[2][V];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < 2; ++i) {
     m[i] = -INFINITY, l[i] = 0.f;
 #pragma unroll
     for (int e = 0; e < V; ++e) o[i][e] = 0.f;
   }
-#pragma unroll 2
+#pragma unroll 4
   for (int k = 0; k < d.y; ++k) {
     const long slot = (2l * (d.x + k) + (k == 0 ? 1 : 0)) * a.mt_max + x0;
-    float2 ml[4];
-    float v[4][V];
+    float2 ml[2];
+    float v[2][V];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2; ++i) {
       ml[i] = make_float2(-INFINITY, 0.f);
 #pragma unroll
       for (int e = 0; e < V; ++e) v[i][e] = 0.f;
@@ -979,7 +982,7 @@ __global__ void __launch_bounds__(kChunkJoinThreads) k_chunk_join(const __grid_c
       }
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2; ++i) {
       const float mm = fmaxf(m[i], ml[i].x);
       const float f0 = m[i] == -INFINITY ? 0.f : exp2_approx(m[i] - mm), f1 = ml[i].x == -INFINITY ? 0.f : exp2_approx(ml[i].x - mm);
       // (a part that saw nothing has sum 0, one whose row sees a value that is no number NaN)
@@ -990,7 +993,7 @@ __global__ void __launch_bounds__(kChunkJoinThreads) k_chunk_join(const __grid_c
     }
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < 2; ++i) {
     const int q = qt * 256 + x0 + i;
     if (q >= Mq) return;
     const int j = q / a.group, hh = kvh * a.group + q - j * a.group;
