@@ -192,21 +192,26 @@ static cudaError_t enqueue_chunk(Args& a, const sf_paged_cache& c, int q_dtype, 
 }
 // Whether a chunk of 16-bit queries is so little work that paged_attention's
 // kernels finish first: they start sooner and share it out more finely, but read
-// the cache more often and compute what causality masks. `total` counts tiles of
-// 128 queries by 64 slots, in requests that fill their tables. Measured, us of
-// the chunk kernel / of those, bf16, requests x rows of tokens:
-//   head_dim 64, 14 / 2 heads: 1 x 97 of 97 11.5 / 9.4; 1 x 256 of 512 14.9 / 14.6;
-//     1 x 64 of 4096 14.4 / 12.7; 1 x 512 of 512 16.9 / 22.5; 8 x 64 of 2048 20.8 / 26.8
-//   128, 28 / 4: 1 x 97 of 97 13.7 / 11.6; 4 x 100 of 300 21.5 / 18.5; 1 x 64 of 4096
-//     19.6 / 18.0; 1 x 256 of 512 22.1 / 21.1; 1 x 512 of 512 24.8 / 25.6; 8 x 64 of
-//     2048 35.0 / 38.6; 2 x 512 of 2048 51.4 / 68.8
-//   128, 40 / 8: 1 x 64 of 4096 21.2 / 19.2; 1 x 256 of 512 24.4 / 20.5; 1 x 150 of
-//     150 17.0 / 22.0; 16 x 200 of 200 74.8 / 103.6
+// the cache more often and compute what causality masks; and with few items
+// behind a long context the chunk kernel's come in many parts to be joined. `total`
+// counts tiles of 128 queries by 64 slots, in requests that fill their tables.
+// Measured, us of the chunk kernel / of those, bf16, requests x rows of tokens, []
+// the choice:
+//   head_dim 64, 14 / 2 heads: 1 x 97 of 97 11.5 / [9.5]; 1 x 256 of 512 15.5 / [14.7];
+//     1 x 64 of 4096 26.1 / [12.9], of 32768 35.0 / [25.6]; 1 x 128 of 4096 22.4 /
+//     [17.6]; 1 x 512 of 512 [17.0] / 22.3; 8 x 64 of 2048 [21.6] / 26.8; 32 x 64 of 256
+//     [17.7] / 29.2
+//   128, 28 / 4: 1 x 97 of 97 13.1 / [11.2]; 4 x 100 of 300 20.9 / [18.4]; 1 x 64 of 4096
+//     25.6 / [17.9], of 8192 28.2 / [22.2], of 16384 [31.6] / 29.3; 1 x 30 of 16384 35.1 /
+//     [20.9]; 1 x 256 of 512 [20.1] / 20.8; 2 x 512 of 2048 [38.7] / 68.3
+//   128, 40 / 8: 1 x 64 of 4096 24.2 / [18.9], of 6144 [26.4] / 22.3 (1.18, the furthest from
+//     the better of 107); 1 x 256 of 512 [20.4] / 20.4; 16 x 200 of 200 [41.9] / 103.6
 // At up to 128 queries the chunk kernel's second tile has nothing to do.
 static bool little_chunk(const sf_paged_cache& c, int n_heads, int max_rows, int batch, int table_width) {
-  const long queries = (long)max_rows * (n_heads / c.n_kv_heads);
-  const long total = (long)batch * c.n_kv_heads * ((queries + 127) / 128) * (((long)table_width * c.page + kTile - 1) / kTile);
-  return queries <= 128 || total < 256 || (queries <= 768 && total <= 1536);
+  const long queries = (long)max_rows * (n_heads / c.n_kv_heads), heads = (long)batch * c.n_kv_heads;
+  const long total = heads * ((queries + 127) / 128) * (((long)table_width * c.page + kTile - 1) / kTile);
+  const long items = heads * ((queries + kChunkQueries - 1) / kChunkQueries);
+  return queries <= 128 || total < 256 || (queries <= 1024 && total <= 4096 && total * items <= 30000);
 }
 // The kernel counts a request's units as (group * slots) / 128 and its items in 32 bits.
 static bool chunk_fits(const sf_paged_cache& c, int n_heads, int max_rows, int table_width) {
